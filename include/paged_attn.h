@@ -305,6 +305,130 @@ pa_status pa_paged_attention_decode_noalloc(const pa_shape* shape, const void* q
                                             void* out, uint32_t* device_flag_out,
                                             void* cuda_stream);
 
+/* ---- A cache held in 4 bits ------------------------------------------------
+ *
+ * A 4-bit pool holds the same [num_pages, H_kv, page_size] rows as the bf16
+ * and fp32 pools, each row's 128 values as 64 bytes of codes and 8 scales
+ * (72 bytes, 28% of a bf16 row):
+ *   codes  [num_pages, H_kv, page_size, 64] bytes, 16-byte aligned: e2m1, dim
+ *          2i in the low half of byte i, dim 2i + 1 in the high half;
+ *   scales [num_pages, H_kv, page_size, 8] bytes, 8-byte aligned: e4m3, one
+ *          per 16 consecutive dims, sign bit 0.
+ * The value of a dim is code * scale.  pa_append_kv_q4 writes
+ *   scale = min(max(RNE_e4m3(max |x| over the 16 dims / 6), 2^-9), 448),
+ *   code  = RNE_e2m1(x / scale), magnitudes above 6 stored as 6,
+ * exactly (no code or scale depends on how a division is rounded), so values
+ * beyond +-2688 saturate; a NaN makes its 16 dims NaN.  Block tables, context
+ * lengths, unused slots and shared pages are as for the other pools.  In the
+ * pa_shape of these calls dtype is that of the query, output or new rows. */
+typedef struct {
+    void* key_codes;
+    void* key_scales;
+    void* value_codes;
+    void* value_scales;
+} pa_q4_pool;
+
+/* pa_append_kv into a 4-bit pool: the new tokens' K/V rows k_new, v_new [B,
+ * H_kv, L, D] (bf16 or fp32, 16-byte aligned) rounded to 4 bits into their
+ * pages.  Positions, flags and the workspace (>= 256 bytes, zeroed once) as
+ * for pa_append_kv.  Returns PA_ERR_INVALID_ARG for null or misaligned
+ * pointers, PA_ERR_WORKSPACE, PA_ERR_UNSUPPORTED or PA_ERR_CUDA. */
+pa_status pa_append_kv_q4(const pa_shape* shape, const void* k_new, const void* v_new,
+                          const pa_q4_pool* pool, const int32_t* block_table,
+                          const int32_t* context_lens, void* workspace, size_t workspace_bytes,
+                          void* cuda_stream);
+
+/* Reads n positions of every (b, kv_head) back, dense and dequantised (exact
+ * in bf16 and fp32): k_dense, v_dense [B, H_kv, n, D] of shape->dtype.  Row i
+ * is position i, or, with tail != 0, position context_lens[b] - n + i (tail
+ * with n = L reads what pa_append_kv_q4 just stored); rows outside [0,
+ * context_lens[b]) are zero.  A context length outside [0, capacity] sets
+ * PA_FLAG_BAD_CONTEXT and reads as 0, a bad page id sets PA_FLAG_BAD_PAGE and
+ * its rows are zero. */
+pa_status pa_gather_kv_q4(const pa_shape* shape, const pa_q4_pool* pool,
+                          const int32_t* block_table, const int32_t* context_lens, int n, int tail,
+                          void* k_dense, void* v_dense, void* workspace, size_t workspace_bytes,
+                          void* cuda_stream);
+
+/* pa_paged_attention over a 4-bit pool, any L, bf16 or fp32 query and output:
+ * the attention of the stored values (nothing else is rounded to 4 bits).
+ * Keys behind a bad page id are left out (PA_FLAG_BAD_PAGE).
+ *
+ * Key weights (key_weights_out not null): what every key received,
+ *   key_weights_out[b, kv_head, s] = key_weights[b, kv_head, s]
+ *       + sum over the kv head's query heads and the L positions of the
+ *         softmax probability of key s     (s < context_lens[b], else 0),
+ * fp32 [B, H_kv, weights_S], weights_S >= max_pages_per_seq * page_size; a
+ * null key_weights counts as zeros, and key_weights may be key_weights_out
+ * itself (accumulated in place).  The sum's order is fixed: equal calls give
+ * equal bits.  key_weights without key_weights_out is PA_ERR_INVALID_ARG.
+ *
+ * workspace: pa_q4_workspace_bytes(shape, key_weights_out != NULL), 256-byte
+ * aligned, zeroed once by the caller; calls that may overlap need their own.
+ * Returns as pa_paged_attention_sched. */
+pa_status pa_paged_attention_q4(const pa_shape* shape, const void* query, const pa_q4_pool* pool,
+                                const int32_t* block_table, const int32_t* context_lens,
+                                float scale, int causal, const float* key_weights,
+                                float* key_weights_out, long long weights_S, void* out,
+                                void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* Bytes of workspace of pa_paged_attention_q4, with or without key weights;
+ * 0 for an invalid shape or without a device. */
+size_t pa_q4_workspace_bytes(const pa_shape* shape, int key_weights);
+
+/* ---- Key weights and eviction ----------------------------------------------
+ *
+ * pa_paged_attention over bf16 pages that also accumulates what every key
+ * received (key_weights_out required; see pa_paged_attention_q4).  fp32 pools
+ * are PA_ERR_UNSUPPORTED.  workspace: pa_weights_workspace_bytes(shape). */
+pa_status pa_paged_attention_weights(const pa_shape* shape, const void* query,
+                                     const void* key_pages, const void* value_pages,
+                                     const int32_t* block_table, const int32_t* context_lens,
+                                     float scale, int causal, const float* key_weights,
+                                     float* key_weights_out, long long weights_S, void* out,
+                                     void* workspace, size_t workspace_bytes, void* cuda_stream);
+size_t pa_weights_workspace_bytes(const pa_shape* shape);
+
+/* Trims every sequence to at most `keep` keys per kv head: of sequence b with
+ * S = context_lens[b] > keep, kv head h keeps its `recent` last positions and,
+ * of the others, the keep - recent of the largest key_weights (equal weights:
+ * the lower position; NaN counts as larger than any number); S <= keep keeps
+ * all.  The kept rows go, in order, to positions 0, 1, ... of dst_block_table
+ * [B, dst_max_pages_per_seq] (capacity at least keep), pages of the same pool
+ * that nothing else uses: the pages of block_table are only read, so shared
+ * ones stay as they are, and the caller frees them after the call.  Also
+ * written:
+ *   context_lens_out [B]: min(S, keep);
+ *   key_weights_out [B, H_kv, weights_out_S >= keep]: the kept keys' weights,
+ *     then zeros;
+ *   kept [B, H_kv, keep]: the kept positions, ascending, then -1.
+ * A kv head's keys keep their order, so causal attention goes on with the new
+ * table and lengths; positions are no longer those of the text (keys that
+ * encode their position carry it already).
+ *
+ * Shape fields used: B, H_kv, num_pages, page_size, max_pages_per_seq, dtype
+ * (of the pool; both pools' element types here).  key_weights [B, H_kv,
+ * weights_S], weights_S >= capacity.  context_lens_out, key_weights_out and
+ * dst_block_table must not be the inputs themselves (PA_ERR_INVALID_ARG).
+ * Device flags: PA_FLAG_BAD_CONTEXT for a context length outside [0,
+ * capacity] (treated as 0), PA_FLAG_BAD_PAGE for a row whose page id in either
+ * table is out of range (not copied).  workspace: >= 256 bytes, zeroed once. */
+pa_status pa_evict_kv(const pa_shape* shape, void* key_pages, void* value_pages,
+                      const int32_t* block_table, const int32_t* context_lens,
+                      const float* key_weights, long long weights_S, int keep, int recent,
+                      const int32_t* dst_block_table, int dst_max_pages_per_seq,
+                      int32_t* context_lens_out, float* key_weights_out, long long weights_out_S,
+                      int32_t* kept, void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* pa_evict_kv of a 4-bit pool. */
+pa_status pa_evict_kv_q4(const pa_shape* shape, const pa_q4_pool* pool,
+                         const int32_t* block_table, const int32_t* context_lens,
+                         const float* key_weights, long long weights_S, int keep, int recent,
+                         const int32_t* dst_block_table, int dst_max_pages_per_seq,
+                         int32_t* context_lens_out, float* key_weights_out,
+                         long long weights_out_S, int32_t* kept, void* workspace,
+                         size_t workspace_bytes, void* cuda_stream);
+
 const char* pa_status_str(pa_status status);
 
 #ifdef __cplusplus

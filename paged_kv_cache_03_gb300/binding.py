@@ -13,9 +13,11 @@ workspace with torch and calls ``pa_paged_attention_sched``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
+from typing import NamedTuple
 
 from . import build as _build
 
@@ -54,6 +56,11 @@ class pa_shape(ctypes.Structure):
                 ("L", ctypes.c_int), ("D", ctypes.c_int), ("num_pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("max_pages_per_seq", ctypes.c_int),
                 ("dtype", ctypes.c_int)]
+
+
+class pa_q4_pool(ctypes.Structure):
+    _fields_ = [("key_codes", ctypes.c_void_p), ("key_scales", ctypes.c_void_p),
+                ("value_codes", ctypes.c_void_p), ("value_scales", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -113,6 +120,27 @@ def load(auto_build: bool = True):
         lib.pa_selftest_wait_timeout.restype = ctypes.c_int
         lib.pa_append_kv.argtypes = [sp, vp, vp, vp, vp, i32p, i32p, vp, sz, vp]
         lib.pa_append_kv.restype = ctypes.c_int
+        qp, f32, ci, ll = (ctypes.POINTER(pa_q4_pool), ctypes.c_float, ctypes.c_int,
+                           ctypes.c_longlong)
+        lib.pa_append_kv_q4.argtypes = [sp, vp, vp, qp, i32p, i32p, vp, sz, vp]
+        lib.pa_append_kv_q4.restype = ci
+        lib.pa_gather_kv_q4.argtypes = [sp, qp, i32p, i32p, ci, ci, vp, vp, vp, sz, vp]
+        lib.pa_gather_kv_q4.restype = ci
+        lib.pa_paged_attention_q4.argtypes = [sp, vp, qp, i32p, i32p, f32, ci, vp, vp, ll, vp, vp,
+                                              sz, vp]
+        lib.pa_paged_attention_q4.restype = ci
+        lib.pa_q4_workspace_bytes.argtypes = [sp, ci]
+        lib.pa_q4_workspace_bytes.restype = sz
+        lib.pa_paged_attention_weights.argtypes = [sp, vp, vp, vp, i32p, i32p, f32, ci, vp, vp, ll,
+                                                   vp, vp, sz, vp]
+        lib.pa_paged_attention_weights.restype = ci
+        lib.pa_weights_workspace_bytes.argtypes = [sp]
+        lib.pa_weights_workspace_bytes.restype = sz
+        evict = [i32p, i32p, vp, ll, ci, ci, i32p, ci, i32p, vp, ll, i32p, vp, sz, vp]
+        lib.pa_evict_kv.argtypes = [sp, vp, vp] + evict
+        lib.pa_evict_kv.restype = ci
+        lib.pa_evict_kv_q4.argtypes = [sp, qp] + evict
+        lib.pa_evict_kv_q4.restype = ci
         lib.pa_status_str.argtypes = [ctypes.c_int]
         lib.pa_status_str.restype = ctypes.c_char_p
         _lib = lib
@@ -400,3 +428,404 @@ def paged_attention_varlen(query, key_pages, value_pages, block_table, context_l
     if st != PA_OK:
         raise PagedAttentionError(st, "pa_paged_attention_varlen")
     return out
+
+
+# ---- 4-bit pages, key weights and eviction -----------------------------------
+def pa_append_kv_q4(shape, k_new, v_new, pool, block_table, context_lens, workspace,
+                    workspace_bytes, stream=None) -> int:
+    return load().pa_append_kv_q4(
+        ctypes.byref(shape), _ptr(k_new), _ptr(v_new), _q4(pool), _ptr(block_table),
+        _ptr(context_lens), _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def pa_gather_kv_q4(shape, pool, block_table, context_lens, n, tail, k_dense, v_dense, workspace,
+                    workspace_bytes, stream=None) -> int:
+    return load().pa_gather_kv_q4(
+        ctypes.byref(shape), _q4(pool), _ptr(block_table), _ptr(context_lens), int(n),
+        int(bool(tail)), _ptr(k_dense), _ptr(v_dense), _ptr(workspace), int(workspace_bytes),
+        _stream(stream))
+
+
+def pa_q4_workspace_bytes(shape, key_weights=False) -> int:
+    return int(load().pa_q4_workspace_bytes(ctypes.byref(shape), int(bool(key_weights))))
+
+
+def pa_weights_workspace_bytes(shape) -> int:
+    return int(load().pa_weights_workspace_bytes(ctypes.byref(shape)))
+
+
+def pa_paged_attention_q4(shape, query, pool, block_table, context_lens, scale, causal,
+                          key_weights, key_weights_out, weights_S, out, workspace,
+                          workspace_bytes, stream=None) -> int:
+    return load().pa_paged_attention_q4(
+        ctypes.byref(shape), _ptr(query), _q4(pool), _ptr(block_table), _ptr(context_lens),
+        float(scale), int(bool(causal)), _ptr(key_weights), _ptr(key_weights_out),
+        int(weights_S), _ptr(out), _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def pa_paged_attention_weights(shape, query, key_pages, value_pages, block_table, context_lens,
+                               scale, causal, key_weights, key_weights_out, weights_S, out,
+                               workspace, workspace_bytes, stream=None) -> int:
+    return load().pa_paged_attention_weights(
+        ctypes.byref(shape), _ptr(query), _ptr(key_pages), _ptr(value_pages), _ptr(block_table),
+        _ptr(context_lens), float(scale), int(bool(causal)), _ptr(key_weights),
+        _ptr(key_weights_out), int(weights_S), _ptr(out), _ptr(workspace), int(workspace_bytes),
+        _stream(stream))
+
+
+def pa_evict_kv(shape, key_pages, value_pages, block_table, context_lens, key_weights, weights_S,
+                keep, recent, dst_block_table, dst_max_pages_per_seq, context_lens_out,
+                key_weights_out, weights_out_S, kept, workspace, workspace_bytes,
+                stream=None) -> int:
+    return load().pa_evict_kv(
+        ctypes.byref(shape), _ptr(key_pages), _ptr(value_pages), _ptr(block_table),
+        _ptr(context_lens), _ptr(key_weights), int(weights_S), int(keep), int(recent),
+        _ptr(dst_block_table), int(dst_max_pages_per_seq), _ptr(context_lens_out),
+        _ptr(key_weights_out), int(weights_out_S), _ptr(kept), _ptr(workspace),
+        int(workspace_bytes), _stream(stream))
+
+
+def pa_evict_kv_q4(shape, pool, block_table, context_lens, key_weights, weights_S, keep, recent,
+                   dst_block_table, dst_max_pages_per_seq, context_lens_out, key_weights_out,
+                   weights_out_S, kept, workspace, workspace_bytes, stream=None) -> int:
+    return load().pa_evict_kv_q4(
+        ctypes.byref(shape), _q4(pool), _ptr(block_table), _ptr(context_lens),
+        _ptr(key_weights), int(weights_S), int(keep), int(recent), _ptr(dst_block_table),
+        int(dst_max_pages_per_seq), _ptr(context_lens_out), _ptr(key_weights_out),
+        int(weights_out_S), _ptr(kept), _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+class Q4Pool:
+    """A page pool held in 4 bits (layout in include/paged_attn.h): uint8
+    codes [num_pages, H_kv, page_size, 64] and scales [..., 8] of keys and
+    values, checked once here.  `dims` is (num_pages, H_kv, page_size)."""
+    __slots__ = ("key_codes", "key_scales", "value_codes", "value_scales", "dims", "device",
+                 "c_pool")
+
+    def __init__(self, key_codes, key_scales, value_codes, value_scales):
+        import torch
+        if key_codes.dim() != 4:
+            raise ValueError("key_codes must be uint8 [num_pages, H_kv, page_size, 64]")
+        self.dims = tuple(key_codes.shape[:3])
+        self.device = key_codes.device
+        tensors = (("key_codes", key_codes, 64), ("key_scales", key_scales, 8),
+                   ("value_codes", value_codes, 64), ("value_scales", value_scales, 8))
+        for name, t, w in tensors:
+            if t.dtype != torch.uint8 or tuple(t.shape) != (*self.dims, w):
+                raise ValueError(f"{name} must be uint8 [num_pages, H_kv, page_size, {w}]")
+            if not t.is_cuda or t.device != self.device or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous CUDA tensor on {self.device}")
+            setattr(self, name, t)
+        self.c_pool = pa_q4_pool(*[t.data_ptr() for t in self])
+
+    def __iter__(self):
+        return iter((self.key_codes, self.key_scales, self.value_codes, self.value_scales))
+
+
+class Evicted(NamedTuple):
+    """What an eviction leaves: the new lengths [B], the kept keys' weights
+    [B, H_kv, n] and their old positions [B, H_kv, keep] (-1 past the end)."""
+    context_lens: object
+    key_weights: object
+    kept: object
+
+
+def _q4(pool):
+    """A Q4Pool, four addresses or tensors, or None, for the C calls."""
+    if isinstance(pool, Q4Pool):
+        return ctypes.byref(pool.c_pool)
+    return None if pool is None else ctypes.byref(pa_q4_pool(*[_ptr(t) for t in pool]))
+
+
+def new_q4_pool(num_pages, H_kv, page_size, device=None) -> Q4Pool:
+    """A 4-bit pool of zeros (head dim 128)."""
+    import torch
+
+    def new(n):
+        return torch.zeros((num_pages, H_kv, page_size, n), dtype=torch.uint8,
+                           device=device or "cuda")
+    return Q4Pool(new(64), new(8), new(64), new(8))
+
+
+def new_cache_workspace(device=None):
+    """Zeroed workspace of append_kv_q4, gather_kv_q4 and evict_kv*."""
+    import torch
+    return torch.zeros(256, dtype=torch.uint8, device=device or "cuda")
+
+
+def _dtype_id(t):
+    import torch
+    if t == torch.bfloat16:
+        return PA_BF16
+    if t == torch.float32:
+        return PA_F32
+    raise ValueError(f"unsupported dtype {t}")
+
+
+def _on_device(device, **tensors):
+    """Every named tensor (None allowed) is contiguous on the CUDA device."""
+    for name, t in tensors.items():
+        if t is not None and not (t.is_cuda and t.device == device and t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
+
+
+def _table(block_table, context_lens, B):
+    import torch
+    if block_table.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block tables and context lengths must be int32")
+    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_table must be [B, max_pages_per_seq] and context_lens [B]")
+
+
+def _pages_dims(key_pages, value_pages):
+    """(num_pages, H_kv, page_size) of a checked bf16 or fp32 pool."""
+    if key_pages.dim() != 4 or key_pages.shape != value_pages.shape or \
+            key_pages.dtype != value_pages.dtype:
+        raise ValueError("key and value pages must be alike, [num_pages, H_kv, page_size, D]")
+    _on_device(key_pages.device, key_pages=key_pages, value_pages=value_pages)
+    return key_pages.shape[:3]
+
+
+def _call(name, device, fn):
+    """Runs fn(stream) with `device` current, on its current stream."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        st = fn(_stream(None))
+    else:
+        with torch.cuda.device(device):
+            st = fn(_stream(None))
+    if st != PA_OK:
+        raise PagedAttentionError(st, name)
+
+
+def _streamed(fn):
+    """Runs the call with its `stream` argument (a torch stream or a raw
+    handle) current, so that what it allocates, zeroes and returns belongs to
+    that stream too."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+@_streamed
+def append_kv_q4(k_new, v_new, pool, block_table, context_lens, *, workspace=None):
+    """Rounds k_new/v_new [B, H_kv, L, 128] (bf16 or fp32) -- the last L
+    positions of each context -- to 4 bits into their pages (in place)."""
+    P, H_kv, ps = pool.dims
+    if k_new.dim() != 4 or k_new.shape[1] != H_kv or k_new.shape[3] != 128 or \
+            v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+        raise ValueError("k_new/v_new must be alike, [B, H_kv, L, 128] matching the pool")
+    B_, _, L, D = k_new.shape
+    _table(block_table, context_lens, B_)
+    device = pool.device
+    k_new, v_new = k_new.contiguous(), v_new.contiguous()
+    if workspace is None:
+        workspace = new_cache_workspace(device)
+    _on_device(device, k_new=k_new, v_new=v_new, block_table=block_table,
+               context_lens=context_lens, workspace=workspace)
+    shape = make_shape(B_, H_kv, H_kv, L, D, P, ps, block_table.shape[1], _dtype_id(k_new.dtype))
+    _call("pa_append_kv_q4", device, lambda s: pa_append_kv_q4(
+        shape, k_new, v_new, pool, block_table, context_lens, workspace, workspace.numel(), s))
+    return workspace
+
+
+@_streamed
+def gather_kv_q4(pool, block_table, context_lens, n, *, tail=False, dtype=None, workspace=None):
+    """Dense dequantised (keys, values), each [B, H_kv, n, 128] of `dtype`
+    (bf16 by default, or fp32; both exact): positions 0 .. n - 1, or with
+    `tail` the last n of each context; zeros outside a context."""
+    import torch
+    dtype = dtype or torch.bfloat16
+    P, H_kv, ps = pool.dims
+    B_ = block_table.shape[0]
+    _table(block_table, context_lens, B_)
+    device = pool.device
+    if workspace is None:
+        workspace = new_cache_workspace(device)
+    _on_device(device, block_table=block_table, context_lens=context_lens, workspace=workspace)
+    shape = make_shape(B_, H_kv, H_kv, 1, 128, P, ps, block_table.shape[1], _dtype_id(dtype))
+    k = torch.empty((B_, H_kv, n, 128), dtype=dtype, device=device)
+    v = torch.empty_like(k)
+    _call("pa_gather_kv_q4", device, lambda s: pa_gather_kv_q4(
+        shape, pool, block_table, context_lens, n, tail, k, v, workspace, workspace.numel(), s))
+    return k, v
+
+
+def _weights_shape(name, w, B_, H_kv, capacity):
+    import torch
+    if w.dtype != torch.float32 or w.dim() != 3 or tuple(w.shape[:2]) != (B_, H_kv) or \
+            w.shape[2] < capacity:
+        raise ValueError(f"{name} must be fp32 [B, H_kv, S] with S >= {capacity}")
+
+
+def _q4_shape(query, pool, block_table):
+    P, H_kv, ps = pool.dims
+    if query.dim() != 4 or query.shape[3] != 128:
+        raise ValueError("query must be [B, H_q, L, 128]")
+    B_, H_q, L, D = query.shape
+    return make_shape(B_, H_q, H_kv, L, D, P, ps, block_table.shape[1], _dtype_id(query.dtype))
+
+
+def _zeroed(n, device, name):
+    import torch
+    if n == 0:
+        raise PagedAttentionError(PA_ERR_INVALID_ARG, name)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def new_q4_workspace(query, pool, block_table, key_weights=True):
+    """Zeroed workspace of paged_attention_q4 for tensors of these shapes."""
+    import torch
+    with torch.cuda.device(query.device):
+        n = pa_q4_workspace_bytes(_q4_shape(query, pool, block_table), key_weights)
+    return _zeroed(n, query.device, "pa_q4_workspace_bytes")
+
+
+def new_weights_workspace(query, key_pages, block_table):
+    """Zeroed workspace of paged_attention_weights for tensors of these shapes."""
+    import torch
+    with torch.cuda.device(query.device):
+        n = pa_weights_workspace_bytes(shape_of(query, key_pages, block_table))
+    return _zeroed(n, query.device, "pa_weights_workspace_bytes")
+
+
+def _attend(name, fn, shape, query, block_table, context_lens, page_size, key_weights,
+            key_weights_out, out, workspace):
+    import torch
+    if shape.page_size != int(page_size):
+        raise ValueError("page_size disagrees with the pool's")
+    _table(block_table, context_lens, shape.B)
+    if out is None:
+        out = torch.empty_like(query)
+    elif out.shape != query.shape or out.dtype != query.dtype:
+        raise ValueError("out must be like query")
+    w_S = 0
+    if key_weights_out is not None:
+        _weights_shape("key_weights_out", key_weights_out, shape.B, shape.H_kv,
+                       shape.max_pages_per_seq * shape.page_size)
+        w_S = key_weights_out.shape[2]
+        if key_weights is not None and (key_weights.shape != key_weights_out.shape or
+                                        key_weights.dtype != key_weights_out.dtype):
+            raise ValueError("key_weights must be like key_weights_out")
+    elif key_weights is not None:
+        raise ValueError("key_weights without key_weights_out")
+    _on_device(query.device, query=query, block_table=block_table, context_lens=context_lens,
+               key_weights=key_weights, key_weights_out=key_weights_out, out=out,
+               workspace=workspace)
+    _call(name, query.device, lambda s: fn(w_S, out, s))
+    return out
+
+
+@_streamed
+def paged_attention_q4(query, pool, block_table, context_lens, page_size, scale=None, causal=True,
+                       *, key_weights=None, key_weights_out=None, out=None, workspace=None):
+    """paged_attention over a 4-bit pool (query bf16 or fp32).  With
+    key_weights_out (fp32 [B, H_kv, S], S >= the table's capacity) the call
+    also writes key_weights (zeros if None; may be key_weights_out itself)
+    plus the probability each key received."""
+    shape = _q4_shape(query, pool, block_table)
+    if scale is None:
+        scale = 1.0 / math.sqrt(query.shape[-1])
+    if pool.device != query.device:
+        raise ValueError(f"pool must be on {query.device}")
+    if workspace is None:
+        workspace = new_q4_workspace(query, pool, block_table, key_weights_out is not None)
+    return _attend(
+        "pa_paged_attention_q4",
+        lambda w_S, o, s: pa_paged_attention_q4(
+            shape, query, pool, block_table, context_lens, scale, causal, key_weights,
+            key_weights_out, w_S, o, workspace, workspace.numel(), s),
+        shape, query, block_table, context_lens, page_size, key_weights, key_weights_out, out,
+        workspace)
+
+
+@_streamed
+def paged_attention_weights(query, key_pages, value_pages, block_table, context_lens, page_size,
+                            scale=None, causal=True, *, key_weights=None, key_weights_out=None,
+                            out=None, workspace=None):
+    """paged_attention over bf16 pages that also writes key_weights_out (fp32
+    [B, H_kv, S], S >= the table's capacity): key_weights (zeros if None; may
+    be key_weights_out itself) plus the probability each key received."""
+    _pages_dims(key_pages, value_pages)
+    shape = shape_of(query, key_pages, block_table)
+    if scale is None:
+        scale = 1.0 / math.sqrt(query.shape[-1])
+    if key_pages.device != query.device:
+        raise ValueError(f"pages must be on {query.device}")
+    if key_weights_out is None:
+        raise ValueError("key_weights_out is what this call is for: use paged_attention")
+    if workspace is None:
+        workspace = new_weights_workspace(query, key_pages, block_table)
+    return _attend(
+        "pa_paged_attention_weights",
+        lambda w_S, o, s: pa_paged_attention_weights(
+            shape, query, key_pages, value_pages, block_table, context_lens, scale, causal,
+            key_weights, key_weights_out, w_S, o, workspace, workspace.numel(), s),
+        shape, query, block_table, context_lens, page_size, key_weights, key_weights_out, out,
+        workspace)
+
+
+def _evict(name, fn, dims, dtype_id, device, block_table, context_lens, key_weights, keep,
+           dst_block_table, workspace):
+    import torch
+    P, H_kv, ps = dims
+    B_ = block_table.shape[0]
+    _table(block_table, context_lens, B_)
+    _table(dst_block_table, context_lens, B_)
+    _weights_shape("key_weights", key_weights, B_, H_kv, block_table.shape[1] * ps)
+    if workspace is None:
+        workspace = new_cache_workspace(device)
+    _on_device(device, block_table=block_table, context_lens=context_lens,
+               key_weights=key_weights, dst_block_table=dst_block_table, workspace=workspace)
+    if not 1 <= keep <= dst_block_table.shape[1] * ps:
+        raise ValueError("keep must be at least 1 and fit dst_block_table")
+    shape = make_shape(B_, H_kv, H_kv, 1, 128, P, ps, block_table.shape[1], dtype_id)
+    ints = torch.empty(B_ + B_ * H_kv * keep, dtype=torch.int32, device=device)
+    new = Evicted(ints[:B_],
+                  torch.empty((B_, H_kv, keep), dtype=torch.float32, device=device),
+                  ints[B_:].view(B_, H_kv, keep))
+    _call(name, device, lambda s: fn(shape, new, workspace, s))
+    return new
+
+
+@_streamed
+def evict_kv(key_pages, value_pages, block_table, context_lens, key_weights, keep, recent,
+             dst_block_table, *, workspace=None) -> Evicted:
+    """Trims every (sequence, kv head) to its `recent` last keys and the
+    heaviest others, `keep` in all, copied in order to the pages of
+    dst_block_table [B, n] (other pages of the same pool).  Returns the new
+    lengths, the kept keys' weights [B, H_kv, keep] and their old positions."""
+    dims = _pages_dims(key_pages, value_pages)
+    if key_pages.shape[3] != 128:
+        raise ValueError("head dim must be 128")
+    return _evict(
+        "pa_evict_kv",
+        lambda sh, new, ws, s: pa_evict_kv(
+            sh, key_pages, value_pages, block_table, context_lens, key_weights,
+            key_weights.shape[2], keep, recent, dst_block_table, dst_block_table.shape[1],
+            new.context_lens, new.key_weights, new.key_weights.shape[2], new.kept, ws,
+            ws.numel(), s),
+        dims, _dtype_id(key_pages.dtype), key_pages.device, block_table, context_lens,
+        key_weights, keep, dst_block_table, workspace)
+
+
+@_streamed
+def evict_kv_q4(pool, block_table, context_lens, key_weights, keep, recent, dst_block_table, *,
+                workspace=None) -> Evicted:
+    """evict_kv of a 4-bit pool."""
+    dims = pool.dims
+    return _evict(
+        "pa_evict_kv_q4",
+        lambda sh, new, ws, s: pa_evict_kv_q4(
+            sh, pool, block_table, context_lens, key_weights, key_weights.shape[2], keep,
+            recent, dst_block_table, dst_block_table.shape[1], new.context_lens,
+            new.key_weights, new.key_weights.shape[2], new.kept, ws, ws.numel(), s),
+        dims, PA_BF16, pool.device, block_table, context_lens, key_weights, keep,
+        dst_block_table, workspace)

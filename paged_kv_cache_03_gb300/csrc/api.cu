@@ -7,6 +7,7 @@
 #include <mutex>
 #include <vector>
 
+#include "cache.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -43,8 +44,6 @@ pa_status current_device_info(DeviceInfo* out) {
     return PA_OK;
 }
 
-namespace {
-
 pa_status check_shape(const pa_shape* s) {
     if (!s) return PA_ERR_INVALID_ARG;
     if (s->B < 1 || s->H_q < 1 || s->H_kv < 1 || s->L < 1 || s->D < 1 || s->num_pages < 1 ||
@@ -61,6 +60,8 @@ pa_status check_shape(const pa_shape* s) {
     if (static_cast<long long>(s->H_q) * s->L >= (1ll << 30)) return PA_ERR_UNSUPPORTED;
     return PA_OK;
 }
+
+namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

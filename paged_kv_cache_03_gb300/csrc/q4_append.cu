@@ -1,0 +1,253 @@
+// q4_append.cu -- new K/V rows rounded to 4 bits into their pages, and the
+// dense read-back of such pages.
+//
+// A group of 16 dims gets the scale s = RNE_e4m3(max|x| / 6), kept in [2^-9,
+// 448], and the codes RNE_e2m1(x / s), which saturate at +-6.  Both divisions
+// are fp32: a quotient that rounds to a border between two codes (at most 3
+// significant bits) or two scales (5 bits) is exactly on it, because x and
+// border * s are both fp32 numbers, and two different ones lie more than half
+// an ulp of the quotient apart; so every code is the one of the real quotient.
+// A NaN in a group makes its scale NaN.
+//
+// The new tokens of sequence b are its last L positions, through the block
+// table as in append.cu; sequences or pages that break the contract set the
+// same flags and are skipped.
+#include "cache.h"
+#include "ptx.cuh"
+#include "q4.cuh"
+
+namespace pa {
+namespace {
+
+struct Q4AppendParams {
+    const void* k_new;
+    const void* v_new;
+    pa_q4_pool pool;
+    const int32_t* bt;
+    const int32_t* ctx;
+    uint32_t* flag;
+    long long units;  // rows * 2 (K, V) * 8 groups
+    int H_kv, L, ps, max_npg, num_pages;
+    long long max_S;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// e4m3 byte of x >= 0, round to nearest even, saturating at 448 (NaN: 0x7f).
+__device__ __forceinline__ uint32_t float_to_e4m3(float x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+    return r & 0xffu;
+}
+
+// e2m1 codes of (lo, hi): low and high half of a byte.
+__device__ __forceinline__ uint32_t float_to_e2m1x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n\t"
+        "mov.b32 %0, {c, 0, 0, 0};\n\t}"
+        : "=r"(r)
+        : "f"(lo), "f"(hi));
+    return r;
+}
+
+// One thread per group of 16 dims.
+template <typename T>
+__global__ void __launch_bounds__(256) q4_append_kernel(const Q4AppendParams p) {
+    for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < p.units;
+         u += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const int grp = static_cast<int>(u & 7);
+        const int isv = static_cast<int>((u >> 3) & 1);
+        const long long row = u >> 4;
+        const long long bk = row / p.L;
+        const int t = static_cast<int>(row - bk * p.L);
+        const int b = static_cast<int>(bk / p.H_kv);
+        const int kvh = static_cast<int>(bk - static_cast<long long>(b) * p.H_kv);
+        const int S = __ldg(p.ctx + b);
+        if (S < p.L || static_cast<long long>(S) > p.max_S) {
+            if (kvh == 0 && t == 0 && (u & 15) == 0) atomicOr(p.flag, PA_FLAG_BAD_CONTEXT);
+            continue;
+        }
+        const int s = S - p.L + t;
+        const int lp = s / p.ps, slot = s - lp * p.ps;
+        const int pp = __ldg(p.bt + static_cast<long long>(b) * p.max_npg + lp);
+        if (pp < 0 || pp >= p.num_pages) {
+            if ((u & 15) == 0) atomicOr(p.flag, PA_FLAG_BAD_PAGE);
+            continue;
+        }
+        const T* const src = static_cast<const T*>(isv ? p.v_new : p.k_new) + row * kHeadDim + grp * 16;
+        float x[16];
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = bf16x2_to_float2(ww[j]);
+                    x[8 * i + 2 * j] = f.x;
+                    x[8 * i + 2 * j + 1] = f.y;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 f = __ldcs(reinterpret_cast<const float4*>(src) + i);
+                x[4 * i] = f.x;
+                x[4 * i + 1] = f.y;
+                x[4 * i + 2] = f.z;
+                x[4 * i + 3] = f.w;
+            }
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
+        const uint32_t sb = float_to_e4m3(max_nan(__fdiv_rn(amax, 6.f), 0.001953125f));
+        const float sc = f16x2_to_float2(e4m3x2_to_f16x2(sb)).x;
+        uint32_t code[2] = {0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            code[i >> 2] |= float_to_e2m1x2(__fdiv_rn(x[2 * i], sc), __fdiv_rn(x[2 * i + 1], sc))
+                            << (8 * (i & 3));
+        const long long dst = (static_cast<long long>(pp) * p.H_kv + kvh) * p.ps + slot;
+        uint8_t* const codes = static_cast<uint8_t*>(isv ? p.pool.value_codes : p.pool.key_codes);
+        uint8_t* const scales = static_cast<uint8_t*>(isv ? p.pool.value_scales : p.pool.key_scales);
+        *reinterpret_cast<uint2*>(codes + dst * kQ4CodeBytes + grp * 8) = make_uint2(code[0], code[1]);
+        scales[dst * kQ4Groups + grp] = static_cast<uint8_t>(sb);
+    }
+}
+
+struct Q4GatherParams {
+    pa_q4_pool pool;
+    const int32_t* bt;
+    const int32_t* ctx;
+    void* k;
+    void* v;
+    uint32_t* flag;
+    long long units;  // B * H_kv * n rows * 2 (K, V) * 8 groups
+    int H_kv, n, tail, ps, max_npg, num_pages;
+    long long max_S;
+};
+
+// One thread per group of 16 dims: 8 code bytes and a scale in, 16 values out.
+template <typename T>
+__global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherParams p) {
+    for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < p.units;
+         u += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const int grp = static_cast<int>(u & 7);
+        const int isv = static_cast<int>((u >> 3) & 1);
+        const long long row = u >> 4;
+        const long long bk = row / p.n;
+        const int i = static_cast<int>(row - bk * p.n);
+        const int b = static_cast<int>(bk / p.H_kv);
+        const int kvh = static_cast<int>(bk - static_cast<long long>(b) * p.H_kv);
+        int S = __ldg(p.ctx + b);
+        if (S < 0 || static_cast<long long>(S) > p.max_S) {
+            if (kvh == 0 && i == 0 && (u & 15) == 0) atomicOr(p.flag, PA_FLAG_BAD_CONTEXT);
+            S = 0;
+        }
+        const long long s = p.tail ? static_cast<long long>(S) - p.n + i : i;
+        uint2 code = make_uint2(0u, 0u);
+        uint32_t sb = 0u;
+        if (s >= 0 && s < S) {
+            const int lp = static_cast<int>(s) / p.ps, slot = static_cast<int>(s) - lp * p.ps;
+            const int pp = __ldg(p.bt + static_cast<long long>(b) * p.max_npg + lp);
+            if (pp >= 0 && pp < p.num_pages) {
+                const long long src = (static_cast<long long>(pp) * p.H_kv + kvh) * p.ps + slot;
+                const void* const c = isv ? p.pool.value_codes : p.pool.key_codes;
+                const void* const sc = isv ? p.pool.value_scales : p.pool.key_scales;
+                code = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c) +
+                                                       src * kQ4CodeBytes + grp * 8);
+                sb = static_cast<const uint8_t*>(sc)[src * kQ4Groups + grp];
+            } else if ((u & 15) == 0) {
+                atomicOr(p.flag, PA_FLAG_BAD_PAGE);
+            }
+        }
+        const uint32_t s2 = e4m3x2_to_f16x2(sb | (sb << 8));
+        uint32_t h[8];
+        e2m1x8_to_f16x2(code.x, *reinterpret_cast<uint32_t(*)[4]>(h));
+        e2m1x8_to_f16x2(code.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+        T* const dst = static_cast<T*>(isv ? p.v : p.k) + row * kHeadDim + grp * 16;
+        float2 f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = f16x2_to_float2(hmul2(h[j], s2));
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                reinterpret_cast<uint4*>(dst)[j] =
+                    make_uint4(pack_bf16x2(f[4 * j].x, f[4 * j].y), pack_bf16x2(f[4 * j + 1].x, f[4 * j + 1].y),
+                               pack_bf16x2(f[4 * j + 2].x, f[4 * j + 2].y), pack_bf16x2(f[4 * j + 3].x, f[4 * j + 3].y));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                reinterpret_cast<float4*>(dst)[j] = make_float4(f[2 * j].x, f[2 * j].y, f[2 * j + 1].x, f[2 * j + 1].y);
+        }
+    }
+}
+
+// Blocks of 256 threads that cover `units` once, at most 8 per SM.
+unsigned grid_for(long long units, int sm_count) {
+    const long long blocks = (units + 255) / 256, cap = 8ll * (sm_count > 0 ? sm_count : 1);
+    return static_cast<unsigned>(blocks < cap ? blocks : cap);
+}
+
+}  // namespace
+
+pa_status q4_append_launch(const pa_shape& sh, const void* k_new, const void* v_new,
+                           const pa_q4_pool& pool, const int32_t* bt, const int32_t* ctx,
+                           uint32_t* flag, int sm_count, cudaStream_t stream) {
+    Q4AppendParams p;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.pool = pool;
+    p.bt = bt;
+    p.ctx = ctx;
+    p.flag = flag;
+    p.units = static_cast<long long>(sh.B) * sh.H_kv * sh.L * 2 * kQ4Groups;
+    p.H_kv = sh.H_kv;
+    p.L = sh.L;
+    p.ps = sh.page_size;
+    p.max_npg = sh.max_pages_per_seq;
+    p.num_pages = sh.num_pages;
+    p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
+    const unsigned grid = grid_for(p.units, sm_count);
+    if (sh.dtype == PA_BF16)
+        q4_append_kernel<uint16_t><<<grid, 256, 0, stream>>>(p);
+    else
+        q4_append_kernel<float><<<grid, 256, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status q4_gather_launch(const pa_shape& sh, const pa_q4_pool& pool, const int32_t* bt,
+                           const int32_t* ctx, int n, int tail, void* k_dense, void* v_dense,
+                           uint32_t* flag, cudaStream_t stream) {
+    DeviceInfo dev;
+    const pa_status st = current_device_info(&dev);
+    if (st != PA_OK) return st;
+    Q4GatherParams p;
+    p.pool = pool;
+    p.bt = bt;
+    p.ctx = ctx;
+    p.k = k_dense;
+    p.v = v_dense;
+    p.flag = flag;
+    p.units = static_cast<long long>(sh.B) * sh.H_kv * n * 2 * kQ4Groups;
+    p.H_kv = sh.H_kv;
+    p.n = n;
+    p.tail = tail;
+    p.ps = sh.page_size;
+    p.max_npg = sh.max_pages_per_seq;
+    p.num_pages = sh.num_pages;
+    p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
+    const unsigned grid = grid_for(p.units, dev.sm_count);
+    if (sh.dtype == PA_BF16)
+        q4_gather_kernel<uint16_t><<<grid, 256, 0, stream>>>(p);
+    else
+        q4_gather_kernel<float><<<grid, 256, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace pa
