@@ -352,7 +352,7 @@ pa_status pa_gather_kv_q4(const pa_shape* shape, const pa_q4_pool* pool,
 
 /* pa_paged_attention over a 4-bit pool, any L, bf16 or fp32 query and output:
  * the attention of the stored values (nothing else is rounded to 4 bits).
- * Keys behind a bad page id are left out (PA_FLAG_BAD_PAGE).
+ * Keys behind a bad page id read as zeros (PA_FLAG_BAD_PAGE).
  *
  * Key weights (key_weights_out not null): what every key received,
  *   key_weights_out[b, kv_head, s] = key_weights[b, kv_head, s]

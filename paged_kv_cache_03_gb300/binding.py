@@ -590,10 +590,10 @@ def _call(name, device, fn):
     """Runs fn(stream) with `device` current, on its current stream."""
     import torch
     if torch.cuda.current_device() == device.index:
-        st = fn(_stream(None))
+        st = fn(torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with torch.cuda.device(device):
-            st = fn(_stream(None))
+            st = fn(torch._C._cuda_getCurrentRawStream(device.index))
     if st != PA_OK:
         raise PagedAttentionError(st, name)
 
@@ -680,11 +680,14 @@ def _zeroed(n, device, name):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def new_q4_workspace(query, pool, block_table, key_weights=True):
-    """Zeroed workspace of paged_attention_q4 for tensors of these shapes."""
+def new_q4_workspace(query, pool, block_table, key_weights=None):
+    """Zeroed workspace of paged_attention_q4 for tensors of these shapes,
+    with key weights, without, or (None) for either."""
     import torch
+    shape = _q4_shape(query, pool, block_table)
+    kinds = (False, True) if key_weights is None else (key_weights,)
     with torch.cuda.device(query.device):
-        n = pa_q4_workspace_bytes(_q4_shape(query, pool, block_table), key_weights)
+        n = max(pa_q4_workspace_bytes(shape, k) for k in kinds)
     return _zeroed(n, query.device, "pa_q4_workspace_bytes")
 
 

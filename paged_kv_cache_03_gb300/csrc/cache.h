@@ -19,10 +19,13 @@ pa_status q4_append_launch(const pa_shape& sh, const void* k_new, const void* v_
                            uint32_t* flag, int sm_count, cudaStream_t stream);
 
 // Dense rows [B, H_kv, n, D] (sh.dtype) of positions first + i, first = 0 or,
-// with tail, context_lens[b] - n; zeros outside [0, context_lens[b]).
+// with tail, context_lens[b] - n; outside [0, context_lens[b]) zeros, or with
+// fill = 0 whatever was there.  id (or null) receives 0 .. B - 1, the block
+// table under which the dense rows are a pool of B pages of n slots, and
+// id + nid the lengths, 0 for one outside [0, capacity].
 pa_status q4_gather_launch(const pa_shape& sh, const pa_q4_pool& pool, const int32_t* bt,
-                           const int32_t* ctx, int n, int tail, void* k_dense, void* v_dense,
-                           uint32_t* flag, cudaStream_t stream);
+                           const int32_t* ctx, int n, int tail, int fill, int32_t* id, int nid,
+                           void* k_dense, void* v_dense, uint32_t* flag, cudaStream_t stream);
 
 // One attention call over 4-bit pages, or over bf16 pages with key weights.
 struct WalkCall {

@@ -134,7 +134,7 @@ pa_status pa_gather_kv_q4(const pa_shape* shape, const pa_q4_pool* pool, const i
     DeviceInfo dev;
     st = device_ok(&dev);
     if (st != PA_OK) return st;
-    return q4_gather_launch(*shape, *pool, block_table, context_lens, n, tail ? 1 : 0, k_dense, v_dense,
+    return q4_gather_launch(*shape, *pool, block_table, context_lens, n, tail ? 1 : 0, 1, nullptr, 0, k_dense, v_dense,
                             static_cast<uint32_t*>(workspace), static_cast<cudaStream_t>(cuda_stream));
 }
 

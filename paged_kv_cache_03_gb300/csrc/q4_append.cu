@@ -12,6 +12,8 @@
 // The new tokens of sequence b are its last L positions, through the block
 // table as in append.cu; sequences or pages that break the contract set the
 // same flags and are skipped.
+#include <climits>
+
 #include "cache.h"
 #include "ptx.cuh"
 #include "q4.cuh"
@@ -127,63 +129,91 @@ struct Q4GatherParams {
     void* k;
     void* v;
     uint32_t* flag;
-    long long units;  // B * H_kv * n rows * 2 (K, V) * 8 groups
-    int H_kv, n, tail, ps, max_npg, num_pages;
+    int H_kv, n, tail, ps, max_npg, num_pages, ntile;
+    int fill;     // rows outside [0, context_lens[b]): 1 zeros, 0 not written
+    int32_t* id;  // if not null: id[b] = b, id[nid + b] = the length (0 for a bad one)
+    int nid;
     long long max_S;
 };
 
-// One thread per group of 16 dims: 8 code bytes and a scale in, 16 values out.
+constexpr int kGatherRows = 64;
+
+// A block takes 64 dense rows of one (sequence, kv head), keys and values: 8
+// lanes a row, each 8 code bytes and a scale in, 16 values out.  Bound by the
+// rows it writes (256 bytes in bf16 for 72 read).
 template <typename T>
 __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherParams p) {
-    for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < p.units;
-         u += static_cast<long long>(gridDim.x) * blockDim.x) {
-        const int grp = static_cast<int>(u & 7);
-        const int isv = static_cast<int>((u >> 3) & 1);
-        const long long row = u >> 4;
-        const long long bk = row / p.n;
-        const int i = static_cast<int>(row - bk * p.n);
-        const int b = static_cast<int>(bk / p.H_kv);
-        const int kvh = static_cast<int>(bk - static_cast<long long>(b) * p.H_kv);
-        int S = __ldg(p.ctx + b);
-        if (S < 0 || static_cast<long long>(S) > p.max_S) {
-            if (kvh == 0 && i == 0 && (u & 15) == 0) atomicOr(p.flag, PA_FLAG_BAD_CONTEXT);
-            S = 0;
-        }
+    const int tile = static_cast<int>(blockIdx.x) % p.ntile, bk = static_cast<int>(blockIdx.x) / p.ntile;
+    const int b = bk / p.H_kv, kvh = bk - b * p.H_kv;
+    const int grp = threadIdx.x & 7;
+    int S = __ldg(p.ctx + b);
+    if (S < 0 || static_cast<long long>(S) > p.max_S) {
+        if (kvh == 0 && tile == 0 && threadIdx.x == 0) atomicOr(p.flag, PA_FLAG_BAD_CONTEXT);
+        S = 0;
+    }
+    if (p.id && kvh == 0 && tile == 0 && threadIdx.x == 0) {
+        p.id[b] = b;
+        p.id[p.nid + b] = S;
+    }
+    if (!p.fill && tile * kGatherRows >= S) return;
+    uint2 code[2][2];
+    uint32_t sb[2][2];
+    bool write[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = tile * kGatherRows + 32 * e + static_cast<int>(threadIdx.x >> 3);
         const long long s = p.tail ? static_cast<long long>(S) - p.n + i : i;
-        uint2 code = make_uint2(0u, 0u);
-        uint32_t sb = 0u;
-        if (s >= 0 && s < S) {
+        const bool in = s >= 0 && s < S;
+        write[e] = i < p.n && (in || p.fill);
+        code[e][0] = code[e][1] = make_uint2(0u, 0u);
+        sb[e][0] = sb[e][1] = 0u;
+        if (i < p.n && in) {
             const int lp = static_cast<int>(s) / p.ps, slot = static_cast<int>(s) - lp * p.ps;
             const int pp = __ldg(p.bt + static_cast<long long>(b) * p.max_npg + lp);
             if (pp >= 0 && pp < p.num_pages) {
                 const long long src = (static_cast<long long>(pp) * p.H_kv + kvh) * p.ps + slot;
-                const void* const c = isv ? p.pool.value_codes : p.pool.key_codes;
-                const void* const sc = isv ? p.pool.value_scales : p.pool.key_scales;
-                code = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c) +
-                                                       src * kQ4CodeBytes + grp * 8);
-                sb = static_cast<const uint8_t*>(sc)[src * kQ4Groups + grp];
-            } else if ((u & 15) == 0) {
+                const uint8_t* const kc = static_cast<const uint8_t*>(p.pool.key_codes);
+                const uint8_t* const vc = static_cast<const uint8_t*>(p.pool.value_codes);
+                code[e][0] = *reinterpret_cast<const uint2*>(kc + src * kQ4CodeBytes + grp * 8);
+                code[e][1] = *reinterpret_cast<const uint2*>(vc + src * kQ4CodeBytes + grp * 8);
+                sb[e][0] = static_cast<const uint8_t*>(p.pool.key_scales)[src * kQ4Groups + grp];
+                sb[e][1] = static_cast<const uint8_t*>(p.pool.value_scales)[src * kQ4Groups + grp];
+            } else if (grp == 0) {
                 atomicOr(p.flag, PA_FLAG_BAD_PAGE);
             }
         }
-        const uint32_t s2 = e4m3x2_to_f16x2(sb | (sb << 8));
-        uint32_t h[8];
-        e2m1x8_to_f16x2(code.x, *reinterpret_cast<uint32_t(*)[4]>(h));
-        e2m1x8_to_f16x2(code.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
-        T* const dst = static_cast<T*>(isv ? p.v : p.k) + row * kHeadDim + grp * 16;
-        float2 f[8];
+    }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f16x2_to_float2(hmul2(h[j], s2));
-        if constexpr (sizeof(T) == 2) {
+    for (int e = 0; e < 2; ++e) {
+        if (!write[e]) continue;
+        const long long row = static_cast<long long>(bk) * p.n + tile * kGatherRows + 32 * e + (threadIdx.x >> 3);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                reinterpret_cast<uint4*>(dst)[j] =
-                    make_uint4(pack_bf16x2(f[4 * j].x, f[4 * j].y), pack_bf16x2(f[4 * j + 1].x, f[4 * j + 1].y),
-                               pack_bf16x2(f[4 * j + 2].x, f[4 * j + 2].y), pack_bf16x2(f[4 * j + 3].x, f[4 * j + 3].y));
-        } else {
+        for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t s2 = e4m3x2_to_f16x2(sb[e][kv] | (sb[e][kv] << 8));
+            uint32_t h[8];
+            e2m1x8_to_f16x2(code[e][kv].x, *reinterpret_cast<uint32_t(*)[4]>(h));
+            e2m1x8_to_f16x2(code[e][kv].y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+            T* const dst = static_cast<T*>(kv ? p.v : p.k) + row * kHeadDim + grp * 16;
+            float2 f[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                reinterpret_cast<float4*>(dst)[j] = make_float4(f[2 * j].x, f[2 * j].y, f[2 * j + 1].x, f[2 * j + 1].y);
+            for (int j = 0; j < 8; ++j) f[j] = f16x2_to_float2(hmul2(h[j], s2));
+            if constexpr (sizeof(T) == 2) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(f[j].x, f[j].y);
+                // 32 bytes a lane where the caller's buffer allows them
+                if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+                    st_global_v8(dst, w);
+                } else {
+                    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    reinterpret_cast<float4*>(dst)[j] =
+                        make_float4(f[2 * j].x, f[2 * j].y, f[2 * j + 1].x, f[2 * j + 1].y);
+            }
         }
     }
 }
@@ -222,11 +252,8 @@ pa_status q4_append_launch(const pa_shape& sh, const void* k_new, const void* v_
 }
 
 pa_status q4_gather_launch(const pa_shape& sh, const pa_q4_pool& pool, const int32_t* bt,
-                           const int32_t* ctx, int n, int tail, void* k_dense, void* v_dense,
-                           uint32_t* flag, cudaStream_t stream) {
-    DeviceInfo dev;
-    const pa_status st = current_device_info(&dev);
-    if (st != PA_OK) return st;
+                           const int32_t* ctx, int n, int tail, int fill, int32_t* id, int nid,
+                           void* k_dense, void* v_dense, uint32_t* flag, cudaStream_t stream) {
     Q4GatherParams p;
     p.pool = pool;
     p.bt = bt;
@@ -234,19 +261,23 @@ pa_status q4_gather_launch(const pa_shape& sh, const pa_q4_pool& pool, const int
     p.k = k_dense;
     p.v = v_dense;
     p.flag = flag;
-    p.units = static_cast<long long>(sh.B) * sh.H_kv * n * 2 * kQ4Groups;
     p.H_kv = sh.H_kv;
     p.n = n;
     p.tail = tail;
+    p.fill = fill;
+    p.id = id;
+    p.nid = nid;
     p.ps = sh.page_size;
     p.max_npg = sh.max_pages_per_seq;
     p.num_pages = sh.num_pages;
+    p.ntile = (n + kGatherRows - 1) / kGatherRows;
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
-    const unsigned grid = grid_for(p.units, dev.sm_count);
+    const long long blocks = static_cast<long long>(sh.B) * sh.H_kv * p.ntile;
+    if (blocks > INT_MAX || n > INT_MAX - kGatherRows) return PA_ERR_UNSUPPORTED;
     if (sh.dtype == PA_BF16)
-        q4_gather_kernel<uint16_t><<<grid, 256, 0, stream>>>(p);
+        q4_gather_kernel<uint16_t><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
     else
-        q4_gather_kernel<float><<<grid, 256, 0, stream>>>(p);
+        q4_gather_kernel<float><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -7,7 +7,7 @@
 //
 // Layout.  A CTA of four warps takes up to 8 * NT rows of one (sequence, kv
 // head) over one chunk of its keys; each warp takes every fourth step of 32
-// keys with its own running max, sum and O, and the warps merge at the end.
+// keys (16 over bf16 pages) with its own running max, sum and O, and the warps merge at the end.
 // Chunks of one row are merged by walk_combine_kernel.
 //
 // Keys are the M side of both products: S^T = K Q^T and O^T += V^T P^T with
@@ -28,6 +28,7 @@
 // Weights: walk_weights_kernel repeats K Q^T for 16 keys a warp over all rows
 // with the row's final log-sum-exp and adds the rows' probabilities in a fixed
 // order (no atomics: a call's results repeat bit for bit).
+#include <cfloat>
 #include <climits>
 
 #include "cache.h"
@@ -39,7 +40,6 @@ namespace {
 
 constexpr int kD = kHeadDim;
 constexpr int kWarps = 4;
-constexpr int kStep = 32;  // keys per warp step
 constexpr float kLazyRescaleLog2 = 8.0f;
 constexpr int kMerge = kD + 4;  // floats per (warp, row) in the merge buffer
 
@@ -71,81 +71,157 @@ __device__ __forceinline__ int seq_len(const WalkParams& p, int b, bool report) 
     return bad ? 0 : S;
 }
 
-// Pool row of key `key` of sequence b (key inside the context), -1 for a bad page.
-__device__ __forceinline__ int key_row(const WalkParams& p, int b, int kvh, int key) {
-    const int lp = key / p.ps, slot = key - lp * p.ps;
+// Page of logical page lp of sequence b, -1 past `end` (its number of pages)
+// and for a bad id (flagged).
+__device__ __forceinline__ int page_of(const WalkParams& p, int b, int lp, int end) {
+    if (lp >= end) return -1;
     const int pp = __ldg(p.bt + static_cast<long long>(b) * p.max_npg + lp);
     if (pp < 0 || pp >= p.num_pages) {
         atomicOr(p.flag, PA_FLAG_BAD_PAGE);
         return -1;
     }
-    return (pp * p.H_kv + kvh) * p.ps + slot;
+    return pp;
 }
+
+// Pool rows of the 16 U keys of a warp's step (U = 1 or 2); -1: no row (the key
+// reads as zeros).  Pages of a multiple of 16 slots: 16 keys share a page, so one row
+// number serves them (A16).  Otherwise each lane looks its key up.
+template <bool A16, int U>
+struct StepRows {
+    int r[A16 ? U : 1];
+    // row of key i (0 .. 15) of half u
+    __device__ __forceinline__ int row(int u, int i) const {
+        if constexpr (A16)
+            return r[u] + i;
+        else
+            return __shfl_sync(0xffffffffu, r[0], 16 * u + i);
+    }
+    __device__ __forceinline__ bool any(int u) const { return A16 ? r[u] >= 0 : true; }
+};
+
+// Walks a warp's steps, `stride` keys apart, without dividing.
+template <bool A16, int U>
+struct StepWalker {
+    int lp, slot, dlp, dslot;  // of the step's first key (A16) or this lane's key
+    __device__ __forceinline__ void start(const WalkParams& p, int key, int stride) {
+        lp = key / p.ps;
+        slot = key - lp * p.ps;
+        dlp = stride / p.ps;
+        dslot = stride - dlp * p.ps;
+    }
+    __device__ __forceinline__ void next(const WalkParams& p) {
+        lp += dlp;
+        slot += dslot;
+        if (slot >= p.ps) {
+            slot -= p.ps;
+            ++lp;
+        }
+    }
+    // pages of the step (npg: pages of the sequence)
+    __device__ __forceinline__ void pages(const WalkParams& p, int b, int npg, int (&pg)[2]) const {
+        pg[0] = page_of(p, b, lp, npg);
+        if constexpr (A16 && U == 2) pg[1] = slot + 16 < p.ps ? pg[0] : page_of(p, b, lp + 1, npg);
+    }
+    __device__ __forceinline__ StepRows<A16, U> rows(const WalkParams& p, int kvh, const int (&pg)[2]) const {
+        StepRows<A16, U> w;
+        w.r[0] = pg[0] < 0 ? -1 : (pg[0] * p.H_kv + kvh) * p.ps + slot;
+        if constexpr (A16 && U == 2) {
+            const int s1 = slot + 16 < p.ps ? slot + 16 : 0;
+            w.r[1] = pg[1] < 0 ? -1 : (pg[1] * p.H_kv + kvh) * p.ps + s1;
+        }
+        return w;
+    }
+};
 
 // ---- 16 keys of 4-bit pages as A fragments --------------------------------
 struct Q4Keys {
     static constexpr bool kF16 = true;
+    static constexpr int kU = 2;  // 16-key halves per warp step
     // first of the two dims of B fragment register `half` in k-step j, lane t
     __device__ static int qdim(int j, int half, int t) { return 32 * t + 4 * j + 2 * half; }
-    uint32_t w[2][4], sc[2][2];
-    // rows: pool rows of keys g and g + 8 (or -1)
-    __device__ __forceinline__ void load(const WalkParams& p, int r0, int r1, int t) {
+    uint32_t w[2][4], s[2];
+    template <bool A16, int U>
+    __device__ __forceinline__ void load(const WalkParams& p, const StepRows<A16, U>& rows, int u, int g, int t) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const long long r = e ? r1 : r0;
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            uint32_t s = 0u;
-            if (r >= 0) {
-                u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.kc) + r * kQ4CodeBytes) + t);
-                s = __ldg(reinterpret_cast<const unsigned short*>(static_cast<const uint8_t*>(p.ks) + r * kQ4Groups) + t);
+            const long long r = rows.row(u, g + 8 * e);
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            s[e] = 0u;
+            if (A16 ? rows.any(u) : r >= 0) {
+                x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.kc) + r * kQ4CodeBytes) + t);
+                s[e] = __ldg(reinterpret_cast<const unsigned short*>(static_cast<const uint8_t*>(p.ks) + r * kQ4Groups) + t);
             }
-            w[e][0] = u.x;
-            w[e][1] = u.y;
-            w[e][2] = u.z;
-            w[e][3] = u.w;
-            const uint32_t s2 = e4m3x2_to_f16x2(s);  // scales of dims 32t.., 32t + 16..
-            sc[e][0] = __byte_perm(s2, s2, 0x1010);
-            sc[e][1] = __byte_perm(s2, s2, 0x3232);
+            w[e][0] = x.x;
+            w[e][1] = x.y;
+            w[e][2] = x.z;
+            w[e][3] = x.w;
         }
     }
+    // the scales of dims 32t .., 32t + 16 .. of both keys, ready for frags()
+    struct Scales {
+        uint32_t v[2][2];
+    };
+    __device__ __forceinline__ Scales scales() const {
+        Scales r;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t s2 = e4m3x2_to_f16x2(s[e]);
+            r.v[e][0] = __byte_perm(s2, s2, 0x1010);
+            r.v[e][1] = __byte_perm(s2, s2, 0x3232);
+        }
+        return r;
+    }
     // A fragments of k-steps 2i and 2i + 1 (code word i of each key)
-    __device__ __forceinline__ void frags(int i, uint32_t (&a)[2][4]) const {
+    __device__ __forceinline__ void frags(const Scales& sc, int i, uint32_t (&a)[2][4]) const {
         uint32_t v0[4], v1[4];
         e2m1x8_to_f16x2(w[0][i], v0);
         e2m1x8_to_f16x2(w[1][i], v1);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            a[j][0] = hmul2(v0[2 * j], sc[0][i >> 1]);
-            a[j][1] = hmul2(v1[2 * j], sc[1][i >> 1]);
-            a[j][2] = hmul2(v0[2 * j + 1], sc[0][i >> 1]);
-            a[j][3] = hmul2(v1[2 * j + 1], sc[1][i >> 1]);
+            a[j][0] = hmul2(v0[2 * j], sc.v[0][i >> 1]);
+            a[j][1] = hmul2(v1[2 * j], sc.v[1][i >> 1]);
+            a[j][2] = hmul2(v0[2 * j + 1], sc.v[0][i >> 1]);
+            a[j][3] = hmul2(v1[2 * j + 1], sc.v[1][i >> 1]);
         }
     }
 };
 
 struct Q4Values {
-    uint32_t w[4][2], sc[2];
-    // r[i]: pool rows of keys 2t, 2t + 1, 2t + 8, 2t + 9 (or -1)
-    __device__ __forceinline__ void load(const WalkParams& p, const int (&r)[4], int g) {
-        uint32_t s[4];
+    uint32_t w[4][2], s[4];
+    // keys 2t, 2t + 1, 2t + 8, 2t + 9
+    template <bool A16, int U>
+    __device__ __forceinline__ void load(const WalkParams& p, const StepRows<A16, U>& rows, int u, int g, int t) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            uint2 u = make_uint2(0u, 0u);
+            const long long r = rows.row(u, 2 * t + (e & 1) + 8 * (e >> 1));
+            uint2 x = make_uint2(0u, 0u);
             s[e] = 0u;
-            if (r[e] >= 0) {
-                const long long rr = r[e];
-                u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.vc) + rr * kQ4CodeBytes) + g);
-                s[e] = __ldg(static_cast<const uint8_t*>(p.vs) + rr * kQ4Groups + g);
+            if (A16 ? rows.any(u) : r >= 0) {
+                x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.vc) + r * kQ4CodeBytes) + g);
+                s[e] = __ldg(static_cast<const uint8_t*>(p.vs) + r * kQ4Groups + g);
             }
-            w[e][0] = u.x;
-            w[e][1] = u.y;
+            w[e][0] = x.x;
+            w[e][1] = x.y;
         }
-        sc[0] = e4m3x2_to_f16x2(s[0] | (s[1] << 8));
-        sc[1] = e4m3x2_to_f16x2(s[2] | (s[3] << 8));
+    }
+    // keys of the half from number n on read as zeros
+    __device__ __forceinline__ void cut(int n, int t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (2 * t + (e & 1) + 8 * (e >> 1) >= n) w[e][0] = w[e][1] = s[e] = 0u;
+    }
+    struct Scales {
+        uint32_t v[2];
+    };
+    __device__ __forceinline__ Scales scales() const {
+        Scales r;
+        r.v[0] = e4m3x2_to_f16x2(s[0] | (s[1] << 8));
+        r.v[1] = e4m3x2_to_f16x2(s[2] | (s[3] << 8));
+        return r;
     }
     // A fragments of m-tiles 4i .. 4i + 3 (code word i of each key); m-tile
     // row g is dim 16g + 2m, row g + 8 dim 16g + 2m + 1
-    __device__ __forceinline__ void frags(int i, uint32_t (&a)[4][4]) const {
+    __device__ __forceinline__ void frags(const Scales& sc, int i, uint32_t (&a)[4][4]) const {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // keys 2t, 2t + 1; then 2t + 8, 2t + 9
             const uint32_t x = w[2 * h][i], y = w[2 * h + 1][i];
@@ -157,8 +233,8 @@ struct Q4Values {
             e2m1x8_to_f16x2(hi, vh);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                a[m][2 * h] = hmul2(vl[m], sc[h]);
-                a[m][2 * h + 1] = hmul2(vh[m], sc[h]);
+                a[m][2 * h] = hmul2(vl[m], sc.v[h]);
+                a[m][2 * h + 1] = hmul2(vh[m], sc.v[h]);
             }
         }
     }
@@ -167,23 +243,28 @@ struct Q4Values {
 // ---- 16 keys of bf16 pages as A fragments ---------------------------------
 struct BfKeys {
     static constexpr bool kF16 = false;
+    static constexpr int kU = 1;  // (a step of 32 keys would not fit the registers)
     __device__ static int qdim(int j, int half, int t) {
         return 32 * (j >> 1) + 8 * t + 4 * (j & 1) + 2 * half;
     }
     uint4 w[2][4];
-    __device__ __forceinline__ void load(const WalkParams& p, int r0, int r1, int t) {
+    template <bool A16, int U>
+    __device__ __forceinline__ void load(const WalkParams& p, const StepRows<A16, U>& rows, int u, int g, int t) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const long long r = e ? r1 : r0;
+            const long long r = rows.row(u, g + 8 * e);
+            const bool ok = A16 ? rows.any(u) : r >= 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 w[e][i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r >= 0)
+                if (ok)
                     w[e][i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.kc) + r * (2 * kD)) + 4 * i + t);
             }
         }
     }
-    __device__ __forceinline__ void frags(int i, uint32_t (&a)[2][4]) const {
+    struct Scales {};
+    __device__ __forceinline__ Scales scales() const { return Scales(); }
+    __device__ __forceinline__ void frags(const Scales&, int i, uint32_t (&a)[2][4]) const {
         a[0][0] = w[0][i].x;
         a[0][1] = w[1][i].x;
         a[0][2] = w[0][i].y;
@@ -197,26 +278,37 @@ struct BfKeys {
 
 struct BfValues {
     uint32_t w[4][8];
-    __device__ __forceinline__ void load(const WalkParams& p, const int (&r)[4], int g) {
+    template <bool A16, int U>
+    __device__ __forceinline__ void load(const WalkParams& p, const StepRows<A16, U>& rows, int u, int g, int t) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-            if (r[e] >= 0) {
-                const long long rr = r[e];
-                const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.vc) + rr * (2 * kD)) + 2 * g;
-                u[0] = __ldg(src);
-                u[1] = __ldg(src + 1);
+            const long long r = rows.row(u, 2 * t + (e & 1) + 8 * (e >> 1));
+            uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+            if (A16 ? rows.any(u) : r >= 0) {
+                const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.vc) + r * (2 * kD)) + 2 * g;
+                x[0] = __ldg(src);
+                x[1] = __ldg(src + 1);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                w[e][4 * i] = u[i].x;
-                w[e][4 * i + 1] = u[i].y;
-                w[e][4 * i + 2] = u[i].z;
-                w[e][4 * i + 3] = u[i].w;
+                w[e][4 * i] = x[i].x;
+                w[e][4 * i + 1] = x[i].y;
+                w[e][4 * i + 2] = x[i].z;
+                w[e][4 * i + 3] = x[i].w;
             }
         }
     }
-    __device__ __forceinline__ void frags(int i, uint32_t (&a)[4][4]) const {
+    __device__ __forceinline__ void cut(int n, int t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (2 * t + (e & 1) + 8 * (e >> 1) >= n) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[e][i] = 0u;
+            }
+    }
+    struct Scales {};
+    __device__ __forceinline__ Scales scales() const { return Scales(); }
+    __device__ __forceinline__ void frags(const Scales&, int i, uint32_t (&a)[4][4]) const {
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -297,10 +389,11 @@ struct QueryFrags {
 };
 
 // ---------------------------------------------------------------------------
-template <class Keys, class Values, int NT, bool F32>
+template <class Keys, class Values, int NT, bool F32, bool A16>
 __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
     constexpr bool F16 = Keys::kF16;
     constexpr int ROWS = 8 * NT;
+    constexpr int U = Keys::kU, kStep = 16 * U;
     extern __shared__ float merge[];  // [warp][row][kMerge]: o, m, applied sum, sum
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -343,8 +436,9 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
         const int rr = 8 * n + g;
         const float down = q[n].load(p.q, row0 + rr, rr < nrows, t);
         // lane 4g' + t' holds row g': rows 2t and 2t + 1 are lanes 8t and 8t + 4
-        qs[n][0] = __shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2;
-        qs[n][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2;
+        // (never 0: a hidden key's -inf times it has to stay -inf)
+        qs[n][0] = fmaxf(__shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2, FLT_MIN);
+        qs[n][1] = fmaxf(__shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2, FLT_MIN);
     }
 
     float m[NT][2], l[NT][2], la[NT][2];
@@ -357,37 +451,50 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
         for (int i = 0; i < 8; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
     }
 
-    for (int base = k0 + warp * kStep; base < k1; base += kWarps * kStep) {
-        const int myrow = base + lane < k1 ? key_row(p, b, kvh, base + lane) : -1;
-        const uint32_t live = __ballot_sync(0xffffffffu, myrow >= 0);
-        Keys kk[2];
-        Values vv[2];
+    // The values of a step are requested when it begins and the keys of the next
+    // one with them, so a step's S = K Q^T hides both.
+    const int npg = (S + p.ps - 1) / p.ps;
+    StepWalker<A16, U> wk;
+    const int first = k0 + warp * kStep;
+    wk.start(p, A16 ? first : first + lane, kWarps * kStep);
+    StepRows<A16, U> rows = {};
+    int pg[2] = {-1, -1};
+    Keys kk[U];
+    if (first < k1) {
+        wk.pages(p, b, npg, pg);
+        rows = wk.rows(p, kvh, pg);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int ra = __shfl_sync(0xffffffffu, myrow, 16 * u + g);
-            const int rb = __shfl_sync(0xffffffffu, myrow, 16 * u + g + 8);
-            kk[u].load(p, ra, rb, t);
+        for (int u = 0; u < U; ++u) kk[u].load(p, rows, u, g, t);
+        wk.next(p);
+        if (first + kWarps * kStep < k1) wk.pages(p, b, npg, pg);
+    }
+    for (int base = first; base < k1; base += kWarps * kStep) {
+        Values vv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) vv[u].load(p, rows, u, g, t);
+        Keys kn[U];
+        if (base + kWarps * kStep < k1) {
+            rows = wk.rows(p, kvh, pg);
+#pragma unroll
+            for (int u = 0; u < U; ++u) kn[u].load(p, rows, u, g, t);
+            wk.next(p);
+            if (base + 2 * kWarps * kStep < k1) wk.pages(p, b, npg, pg);
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            int r[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                r[e] = __shfl_sync(0xffffffffu, myrow, 16 * u + 2 * t + (e & 1) + 8 * (e >> 1));
-            vv[u].load(p, r, g);
-        }
-        // S^T: 32 keys x 8 NT rows
-        float s[NT][2][4];
+        // S^T: 16 U keys x 8 NT rows
+        float s[NT][U][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) s[n][u][0] = s[n][u][1] = s[n][u][2] = s[n][u][3] = 0.f;
+            for (int u = 0; u < U; ++u) s[n][u][0] = s[n][u][1] = s[n][u][2] = s[n][u][3] = 0.f;
+        typename Keys::Scales ksc[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) ksc[u] = kk[u].scales();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < U; ++u) {
                 uint32_t a[2][4];
-                kk[u].frags(i, a);
+                kk[u].frags(ksc[u], i, a);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -396,30 +503,29 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
                         if constexpr (F32) mma<F16>(s[n][u], a[j], q[n].lo[2 * i + j][0], q[n].lo[2 * i + j][1]);
                     }
             }
-        const bool masked = live != 0xffffffffu || base + kStep - 1 > lim_min;
-        uint32_t pb[NT][2][2], pl[NT][2][2];  // P^T fragments, and their low parts
+        if (base + kStep - 1 > lim_min) {  // a row does not see every key (uniform over the warp)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (base + 16 * u + g + 8 * (e >> 1) > lim[n][e & 1]) s[n][u][e] = neg_inf();
+        }
+        uint32_t pb[NT][U][2], pl[NT][U][2];  // P^T fragments, and their low parts
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float mt[2] = {neg_inf(), neg_inf()};
+            float mt[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int e = 0; e < 2; ++e)
+                mt[e] = fmaxf(fmaxf(s[n][0][e], s[n][0][2 + e]), fmaxf(s[n][U - 1][e], s[n][U - 1][2 + e])) * qs[n][e];
+            if (__any_sync(0xffffffffu, mt[0] > m[n][0] + kLazyRescaleLog2 || mt[1] > m[n][1] + kLazyRescaleLog2)) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = s[n][u][e] * qs[n][e & 1];
-                    if (masked) {
-                        const int k = 16 * u + g + 8 * (e >> 1);
-                        if (!((live >> k) & 1u) || base + k > lim[n][e & 1]) x = neg_inf();
-                    }
-                    s[n][u][e] = x;
-                    mt[e & 1] = fmaxf(mt[e & 1], x);
+                for (int d = 4; d < 32; d <<= 1) {
+                    mt[0] = fmaxf(mt[0], __shfl_xor_sync(0xffffffffu, mt[0], d));
+                    mt[1] = fmaxf(mt[1], __shfl_xor_sync(0xffffffffu, mt[1], d));
                 }
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                mt[0] = fmaxf(mt[0], __shfl_xor_sync(0xffffffffu, mt[0], d));
-                mt[1] = fmaxf(mt[1], __shfl_xor_sync(0xffffffffu, mt[1], d));
-            }
-            const bool g0 = mt[0] > m[n][0] + kLazyRescaleLog2, g1 = mt[1] > m[n][1] + kLazyRescaleLog2;
-            if (__any_sync(0xffffffffu, g0 || g1)) {
+                const bool g0 = mt[0] > m[n][0] + kLazyRescaleLog2, g1 = mt[1] > m[n][1] + kLazyRescaleLog2;
                 const float a0 = g0 ? fast_exp2(m[n][0] - mt[0]) : 1.f;  // 2^-inf = 0 at the start
                 const float a1 = g1 ? fast_exp2(m[n][1] - mt[1]) : 1.f;
                 if (g0) m[n][0] = mt[0];
@@ -438,10 +544,11 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
             }
             const float mu[2] = {m[n][0] == neg_inf() ? 0.f : m[n][0], m[n][1] == neg_inf() ? 0.f : m[n][1]};
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {  // keys g, then g + 8
-                    const float p0 = fast_exp2(s[n][u][2 * h] - mu[0]), p1 = fast_exp2(s[n][u][2 * h + 1] - mu[1]);
+                    const float p0 = fast_exp2(fmaf(s[n][u][2 * h], qs[n][0], -mu[0]));
+                    const float p1 = fast_exp2(fmaf(s[n][u][2 * h + 1], qs[n][1], -mu[1]));
                     l[n][0] += p0;
                     l[n][1] += p1;
                     if constexpr (F16) {
@@ -460,13 +567,18 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
                     }
                 }
         }
+        if (base + kStep > S) {  // slots past the context may hold anything
+#pragma unroll
+            for (int u = 0; u < U; ++u) vv[u].cut(S - base - 16 * u, t);
+        }
         // O^T += V^T P^T
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < U; ++u) {
+            const typename Values::Scales vsc = vv[u].scales();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t a[4][4];
-                vv[u].frags(i, a);
+                vv[u].frags(vsc, i, a);
 #pragma unroll
                 for (int mm = 0; mm < 4; ++mm)
 #pragma unroll
@@ -475,6 +587,9 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
                         if constexpr (F32) mma<F16>(o[n][4 * i + mm], a[mm], pl[n][u][0], pl[n][u][1]);
                     }
             }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) kk[u] = kn[u];
     }
 
     // ---- merge the four warps ---------------------------------------------
@@ -587,11 +702,14 @@ __global__ void __launch_bounds__(kWarps * 32) walk_weights_kernel(const WalkPar
     float acc[2] = {0.f, 0.f};  // keys g and g + 8, this lane's rows
     if (base < S) {
         const int k0 = static_cast<int>(base);
-        const int myrow = lane < 16 && k0 + lane < S ? key_row(p, b, kvh, k0 + lane) : -1;
-        const uint32_t live = __ballot_sync(0xffffffffu, myrow >= 0);
+        StepWalker<false, 1> wk;
+        wk.start(p, k0 + lane, 0);
+        int pg[2];
+        wk.pages(p, b, k0 + lane < S && lane < 16 ? INT_MAX : 0, pg);
+        const StepRows<false, 1> rows = wk.rows(p, kvh, pg);
         Keys kk;
-        const int ra = __shfl_sync(0xffffffffu, myrow, g), rb = __shfl_sync(0xffffffffu, myrow, g + 8);
-        kk.load(p, ra, rb, t);
+        kk.load(p, rows, 0, g, t);
+        const typename Keys::Scales ksc = kk.scales();
         const long long row0 = (static_cast<long long>(b) * p.H_kv + kvh) * p.R;
         for (int r0 = 0; r0 < p.R; r0 += 8) {
             QueryFrags<Keys, F32> q;
@@ -600,7 +718,7 @@ __global__ void __launch_bounds__(kWarps * 32) walk_weights_kernel(const WalkPar
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t a[2][4];
-                kk.frags(i, a);
+                kk.frags(ksc, i, a);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     mma<Keys::kF16>(s, a[j], q.hi[2 * i + j][0], q.hi[2 * i + j][1]);
@@ -609,7 +727,7 @@ __global__ void __launch_bounds__(kWarps * 32) walk_weights_kernel(const WalkPar
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float qs = __shfl_sync(0xffffffffu, down, 8 * t + 4 * e) * p.scale_log2;
+                const float qs = fmaxf(__shfl_sync(0xffffffffu, down, 8 * t + 4 * e) * p.scale_log2, FLT_MIN);
                 const int r = r0 + 2 * t + e;
                 if (r >= p.R) continue;
                 const int lim = p.causal ? r % p.L + S - p.L : S - 1;
@@ -617,7 +735,7 @@ __global__ void __launch_bounds__(kWarps * 32) walk_weights_kernel(const WalkPar
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int k = g + 8 * h;
-                    if (((live >> k) & 1u) && k0 + k <= lim) acc[h] += fast_exp2(s[2 * h + e] * qs - lse);
+                    if (k0 + k <= lim) acc[h] += fast_exp2(s[2 * h + e] * qs - lse);
                 }
             }
         }
@@ -659,7 +777,7 @@ WalkPlan plan(const pa_shape& sh, bool weights, int sm_count) {
     const long long most = (cap + 255) / 256;
     nkc = nkc < most ? nkc : most;
     long long C = (cap + nkc - 1) / nkc;
-    C = (C + kWarps * kStep - 1) / (kWarps * kStep) * (kWarps * kStep);
+    C = (C + kWarps * 32 - 1) / (kWarps * 32) * (kWarps * 32);  // whole steps of every warp
     w.C = static_cast<int>(C);
     w.nkc = static_cast<int>((cap + C - 1) / C);
     const size_t rows = static_cast<size_t>(sh.B) * sh.H_kv * w.R;
@@ -674,15 +792,15 @@ WalkPlan plan(const pa_shape& sh, bool weights, int sm_count) {
     return w;
 }
 
-template <class Keys, class Values, int NT, bool F32>
-pa_status launch(const WalkParams& p, cudaStream_t stream) {
+template <class Keys, class Values, int NT, bool F32, bool A16>
+pa_status launch_as(const WalkParams& p, cudaStream_t stream) {
     constexpr size_t smem = sizeof(float) * kWarps * 8 * NT * kMerge;
     static_assert(smem <= 48 * 1024, "merge buffer within the default limit");
     const long long items = static_cast<long long>(p.B) * p.H_kv * p.nrc * p.nkc;
     const long long rows = static_cast<long long>(p.B) * p.H_kv * p.R;
     const long long ntile = (p.w_S + 16 * kWarps - 1) / (16 * kWarps);
     if (items > INT_MAX || rows > 4ll * INT_MAX || ntile * p.B * p.H_kv > INT_MAX) return PA_ERR_UNSUPPORTED;
-    walk_kernel<Keys, Values, NT, F32><<<static_cast<unsigned>(items), kWarps * 32, smem, stream>>>(p);
+    walk_kernel<Keys, Values, NT, F32, A16><<<static_cast<unsigned>(items), kWarps * 32, smem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     if (p.nkc > 1) {
         cudaLaunchConfig_t cfg = {};
@@ -704,14 +822,106 @@ pa_status launch(const WalkParams& p, cudaStream_t stream) {
     return PA_OK;
 }
 
+template <class Keys, class Values, int NT, bool F32>
+pa_status launch(const WalkParams& p, cudaStream_t stream) {
+    return p.ps % 16 == 0 ? launch_as<Keys, Values, NT, F32, true>(p, stream)
+                          : launch_as<Keys, Values, NT, F32, false>(p, stream);
+}
+
+// ---- many rows over 4-bit pages: dense bf16 copies and the tensor-core tiles --
+// (exact: a 4-bit value is a bf16 number).  Sequences go in groups whose
+// copies fit kDenseBytes.
+// Rows per kv head from which the tiles take a call.  Measured (walk, tiles, us;
+// G = 4, H_kv = 8): B = 8 over 1000 .. 8000 keys 61, 96 at 32 rows, 91, 96 at 64,
+// 123, 97 at 96; B = 1 over 16000 keys 41, 41 at 16, 57, 41 at 32; B = 64 over 500
+// .. 2000 keys 111, 166 at 32, 169, 166 at 64.
+constexpr int kTileRows = 48;
+constexpr size_t kDenseBytes = size_t(1) << 30;
+
+struct TilePlan {
+    pa_shape sh;  // one group, over the dense copies
+    size_t id_off, k_off, v_off, total;  // id: block table, then lengths
+};
+
+bool tiles_take(const pa_shape& sh, bool q4, bool weights, int sm_count, TilePlan* t) {
+    if (!q4 || weights || sh.dtype != PA_BF16) return false;
+    if (static_cast<long long>(sh.H_q / sh.H_kv) * sh.L < kTileRows) return false;
+    const long long cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
+    const long long slots = (cap + 127) / 128 * 128;
+    const size_t per_seq = static_cast<size_t>(slots) * sh.H_kv * kD * 2 * 2;
+    if (slots * sh.H_kv >= (1ll << 31)) return false;
+    long long nb = static_cast<long long>(kDenseBytes / per_seq);
+    nb = nb < 1 ? 1 : nb < sh.B ? nb : sh.B;
+    t->sh = sh;
+    t->sh.B = static_cast<int>(nb);
+    t->sh.num_pages = t->sh.B;
+    t->sh.page_size = static_cast<int>(slots);
+    t->sh.max_pages_per_seq = 1;
+    if (!prefill_supported(t->sh)) return false;
+    size_t off = tile_partials_offset(t->sh, sm_count) + tile_partial_bytes(t->sh, sm_count);
+    pa_shape last = t->sh;  // the last group may split its keys more
+    last.B = sh.B % last.B > 0 ? sh.B % last.B : last.B;
+    const size_t off_last = tile_partials_offset(last, sm_count) + tile_partial_bytes(last, sm_count);
+    t->id_off = off = align_up(off > off_last ? off : off_last, 256);
+    off = align_up(off + 8 * static_cast<size_t>(nb), 256);
+    t->k_off = off;
+    off += nb * per_seq / 2;
+    t->v_off = off;
+    t->total = off + nb * per_seq / 2;
+    return true;
+}
+
+pa_status tiles_launch(const WalkCall& c, const TilePlan& t) {
+    const pa_shape& sh = c.sh;
+    uint8_t* const ws = static_cast<uint8_t*>(c.ws);
+    const pa_q4_pool pool = {const_cast<void*>(c.kc), const_cast<void*>(c.ks), const_cast<void*>(c.vc),
+                             const_cast<void*>(c.vs)};
+    const size_t per_seq = static_cast<size_t>(sh.H_q) * sh.L * kD * 2;  // query and output bytes
+    for (int b0 = 0; b0 < sh.B; b0 += t.sh.B) {
+        const int nb = t.sh.B < sh.B - b0 ? t.sh.B : sh.B - b0;
+        pa_shape src = sh;
+        src.B = nb;
+        pa_status st = q4_gather_launch(src, pool, c.bt + static_cast<long long>(b0) * sh.max_pages_per_seq,
+                                        c.ctx + b0, t.sh.page_size, 0, 0,
+                                        reinterpret_cast<int32_t*>(ws + t.id_off), t.sh.B, ws + t.k_off, ws + t.v_off,
+                                        reinterpret_cast<uint32_t*>(ws), c.stream);
+        if (st != PA_OK) return st;
+        Call d;
+        d.sh = t.sh;
+        d.sh.B = nb;
+        d.q = static_cast<const uint8_t*>(c.q) + b0 * per_seq;
+        d.kp = ws + t.k_off;
+        d.vp = ws + t.v_off;
+        d.bt = reinterpret_cast<const int32_t*>(ws + t.id_off);
+        d.ctx = d.bt + t.sh.B;
+        d.scale = c.scale;
+        d.causal = c.causal;
+        d.out = static_cast<uint8_t*>(c.out) + b0 * per_seq;
+        d.ws = c.ws;
+        d.ws_bytes = t.id_off;
+        d.stream = c.stream;
+        d.dev = c.dev;
+        st = prefill_launch(d);
+        if (st != PA_OK) return st;
+    }
+    return PA_OK;
+}
+
 }  // namespace
 
-size_t walk_workspace_bytes(const pa_shape& sh, bool /*q4*/, bool weights, int sm_count) {
+size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_count) {
+    TilePlan t;
+    if (tiles_take(sh, q4, weights, sm_count, &t)) return t.total;
     return plan(sh, weights, sm_count).total;
 }
 
 pa_status walk_launch(const WalkCall& c) {
     const pa_shape& sh = c.sh;
+    TilePlan t;
+    if (tiles_take(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count, &t)) {
+        if (c.ws_bytes < t.total) return PA_ERR_WORKSPACE;
+        return tiles_launch(c, t);
+    }
     const WalkPlan w = plan(sh, c.w_out != nullptr, c.dev.sm_count);
     if (c.ws_bytes < w.total) return PA_ERR_WORKSPACE;
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);

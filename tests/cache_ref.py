@@ -139,10 +139,11 @@ def attend(inp: Inputs, skip=()):
       an instruction adds 17 terms, each cut by at most 2^-23 T: with the
       scaling and the exponential's own 2^-21 at most 2^-15 T + 2^-20
       relative in every p;
-    * p as an operand: 2^-11 for f16 (4-bit pages), 2^-22 for its two parts
-      (fp32), 2^-8 for bf16, and as much again where the row sum adds the
-      rounded weights; parts below f16's range lose up to 2^-25 of the row's
-      largest p each;
+    * p as an operand: 2^-11 for f16 (4-bit pages, few rows), 2^-22 for its two
+      parts (fp32), 2^-8 for bf16 (bf16 pages; 4-bit pages and more than 8 rows
+      per kv head, which may go through bf16 copies of the pages), and as much
+      again where the row sum adds the rounded weights; parts below f16's range
+      lose up to 2^-25 of the row's largest p each;
     * sums of S terms in fp32: 2^-24 S at worst, S below 2^12 here.
     """
     c = inp.c
@@ -151,7 +152,8 @@ def attend(inp: Inputs, skip=()):
     w = np.zeros(inp.w.shape)
     w_tol = np.zeros(inp.w.shape)
     eps = 2.0 ** -8 if c.dtype == "bf16" else 2.0 ** -24
-    pop = 2 * 2.0 ** -8 if c.pool == "bf16" else 2.0 ** -11 if c.dtype == "bf16" else 2.0 ** -22
+    many = c.pool == "bf16" or c.G * c.L > 8
+    pop = 2.0 ** -22 if c.dtype == "f32" else 2 * 2.0 ** -8 if many else 2.0 ** -11
     for b, S in enumerate(inp.ctx):
         if b in skip:
             continue
@@ -187,3 +189,8 @@ def evict(w, ctx, keep, recent):
             order = np.lexsort((np.arange(S - last), -x, ~nan))
             kept[b, h, :n] = np.sort(np.append(order[:n - last], np.arange(S - last, S)))
     return kept, np.minimum(ctx, keep).astype(np.int32)
+
+
+def worst(got, want, tol):
+    """The largest error in units of its tolerance."""
+    return float(np.max(np.abs(got - want) / np.maximum(tol, 1e-300)))

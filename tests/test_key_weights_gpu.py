@@ -57,16 +57,15 @@ def test_weights(c):
     in_w[:, :, :inp.cap][torch.from_numpy(~live).cuda().expand(c.B, c.H_kv, -1)] = float("nan")
     out = run(inp, d, in_w, out_w, ws)
     assert B.pa_check_device_flag(ws)[1] == 0
-    assert np.all(np.abs(_np(out) - want) <= tol)
+    assert ref.worst(_np(out), want, tol) <= 1
     got = _np(out_w)
     assert not got[:, :, inp.cap:].any()
     w = np.where(live, added + inp.w, 0.0)
-    err = np.abs(got[:, :, :inp.cap] - w)
-    assert np.all(err <= w_tol + 2.0 ** -24 * w), np.max(err / (w_tol + 2.0 ** -24 * w + 1e-30))
+    assert ref.worst(got[:, :, :inp.cap], w, w_tol + 2.0 ** -24 * w) <= 1
     # without what was there: each (sequence, kv head) hands out its rows' weight
     none_w = torch.empty_like(d["w"])
     run(inp, d, None, none_w, ws)
-    assert np.all(np.abs(_np(none_w) - added) <= w_tol)
+    assert ref.worst(_np(none_w), added, w_tol) <= 1
     assert np.allclose(_np(none_w).sum(-1), c.G * c.L, rtol=1e-4)
     # in place, twice
     acc = d["w"].clone()
@@ -74,7 +73,7 @@ def test_weights(c):
     assert torch.equal(acc, out_w[:, :, :inp.cap])
     run(inp, d, acc, acc, ws)
     w2 = np.where(live, 2 * added + inp.w, 0.0)
-    assert np.all(np.abs(_np(acc) - w2) <= 2 * w_tol + 2.0 ** -23 * w2)
+    assert ref.worst(_np(acc), w2, 2 * w_tol + 2.0 ** -23 * w2) <= 1
 
 
 @pytest.mark.parametrize("pool", ["bf16", "q4"])
@@ -90,17 +89,19 @@ def test_bad_lengths_and_pages(pool, L):
     out = run(inp, d, d["w"], w, ws, ctx)
     assert B.pa_check_device_flag(ws)[1] == B.PA_FLAG_BAD_CONTEXT
     want, added, tol, w_tol = ref.attend(inp, skip=(0, 2))
-    assert np.all(np.abs(_np(out) - want) <= tol)
+    assert ref.worst(_np(out), want, tol) <= 1
     assert not w[0].any() and not w[2].any()
     full = (added + inp.w)[[1, 3]]
     live = np.arange(inp.cap)[None, None] < inp.ctx[[1, 3]][:, None, None]
-    assert np.all(np.abs(_np(w)[[1, 3]] - full * live) <= w_tol[[1, 3]] + 2.0 ** -24 * full)
+    assert ref.worst(_np(w)[[1, 3]], full * live, w_tol[[1, 3]] + 2.0 ** -24 * full) <= 1
     ws.zero_()
     d["table"][1, 2] = inp.P + 3  # keys 32 .. 47 of sequence 1
     run(inp, d, None, w, ws)
     assert B.pa_check_device_flag(ws)[1] == B.PA_FLAG_BAD_PAGE
-    assert not w[1, :, 32:48].any()
-    assert np.allclose(_np(w)[1].sum(-1), c.G * c.L, rtol=1e-4)
+    for x in inp.dense:
+        x[inp.table[1, 2]] = 0  # they read as zeros
+    _, added, _, w_tol = ref.attend(inp)
+    assert ref.worst(_np(w), added, w_tol) <= 1
 
 
 def test_peaked_rows():
@@ -114,6 +115,6 @@ def test_peaked_rows():
         w = d["w"].clone()
         out = run(inp, d, None, w)
         want, added, tol, w_tol = ref.attend(inp)
-        assert np.all(np.abs(_np(out) - want) <= tol)
+        assert ref.worst(_np(out), want, tol) <= 1
         # probabilities below fp32's normal range flush to zero
-        assert np.all(np.abs(_np(w) - added) <= w_tol + 2.0 ** -125)
+        assert ref.worst(_np(w), added, w_tol + 2.0 ** -125) <= 1

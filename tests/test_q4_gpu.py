@@ -57,7 +57,8 @@ def test_append_and_read_back(dtype, Bn, H, L, ps, ctx):
             for t in range(L):
                 s = ctx[b] - L + t
                 pg, slot = inp.table[b, s // ps], s % ps
-                want[2 * i][pg, :, slot], want[2 * i + 1][pg, :, slot] = codes[b, :, t], scales[b, :, t]
+                want[2 * i][pg, :, slot] = codes[b, :, t]
+                want[2 * i + 1][pg, :, slot] = scales[b, :, t]
     kn, vn = (torch.from_numpy(x).to(dt).cuda() for x in new)
     ws = B.append_kv_q4(kn, vn, d["pool"], d["table"], d["ctx"])
     for got, w in zip(d["pool"], want):
@@ -121,6 +122,8 @@ CASES = [
     Case(2, 4, 2, 17, 16, [17, 400]),
     Case(2, 2, 2, 65, 128, [65, 513]),
     Case(1, 4, 2, 200, 64, [333]),
+    Case(3, 4, 2, 65, 16, [65, 129, 700], spare=9),
+    Case(2, 5, 2, 70, 12, [71, 300]),
     Case(2, 4, 2, 1, 16, [2500, 7], causal=False),
     Case(2, 2, 2, 40, 8, [20, 300], causal=False),
     Case(1, 2, 1, 1, 16, [4000], spare=200),
@@ -137,7 +140,7 @@ def test_attention(c):
                                workspace=ws)
     want, _, tol, _ = ref.attend(inp)
     assert _flag(ws) == 0
-    assert np.all(np.abs(_np(out) - want) <= tol), np.max(np.abs(_np(out) - want) / tol)
+    assert ref.worst(_np(out), want, tol) <= 1
     assert out.dtype == d["q"].dtype
     again = B.paged_attention_q4(d["q"], d["pool"], d["table"], d["ctx"], c.ps, inp.scale,
                                  c.causal, workspace=ws)
@@ -156,7 +159,7 @@ def test_queries_far_from_one(mult):
     d = inp.device()
     out = B.paged_attention_q4(d["q"], d["pool"], d["table"], d["ctx"], c.ps, inp.scale)
     want, _, tol, _ = ref.attend(inp)
-    assert np.all(np.abs(_np(out) - want) <= tol)
+    assert ref.worst(_np(out), want, tol) <= 1
     assert torch.isfinite(out).all()
 
 
@@ -164,30 +167,29 @@ def test_queries_far_from_one(mult):
 @pytest.mark.parametrize("L", [1, 33])
 def test_bad_sequences_and_pages(dtype, L):
     """A sequence whose length breaks the contract gets zero rows, a key
-    behind a bad page is left out; the others are as alone."""
+    behind a bad page reads as zeros; the others are as alone."""
     import torch
     c = Case(4, 2, 2, L, 16, [40, 100, 64, 50], dtype=dtype)
     inp = ref.Inputs(c)
     d = inp.device()
     ws = B.new_q4_workspace(d["q"], d["pool"], d["table"])
-    ctx = torch.tensor([0, 100, 10 ** 6, 50], dtype=torch.int32, device="cuda")
-    out = B.paged_attention_q4(d["q"], d["pool"], d["table"], ctx, c.ps, inp.scale, workspace=ws)
-    want, _, tol, _ = ref.attend(inp, skip=(0, 2))
-    assert _flag(ws) == B.PA_FLAG_BAD_CONTEXT
-    assert np.all(np.abs(_np(out) - want) <= tol)
+    for bad in (10 ** 6, inp.cap + 1, -3):
+        ws.zero_()
+        ctx = torch.tensor([0, 100, bad, 50], dtype=torch.int32, device="cuda")
+        out = B.paged_attention_q4(d["q"], d["pool"], d["table"], ctx, c.ps, inp.scale,
+                                   workspace=ws)
+        want, _, tol, _ = ref.attend(inp, skip=(0, 2))
+        assert _flag(ws) == B.PA_FLAG_BAD_CONTEXT
+        assert ref.worst(_np(out), want, tol) <= 1
     ws.zero_()
     table = d["table"].clone()
     table[1, 0] = -1
     out = B.paged_attention_q4(d["q"], d["pool"], table, d["ctx"], c.ps, inp.scale, workspace=ws)
     assert _flag(ws) == B.PA_FLAG_BAD_PAGE
-    # sequence 1 without its first 16 keys
-    cut = ref.Inputs(Case(**{**c.__dict__}))
-    cut.table = inp.table.copy()
-    cut.table[1, :-1] = inp.table[1, 1:]
-    cut.ctx = inp.ctx.copy()
-    cut.ctx[1] = 84
-    want, _, tol, _ = ref.attend(cut)
-    assert np.all(np.abs(_np(out) - want) <= tol)
+    for x in inp.dense:  # a page of zeros for the first 16 keys of sequence 1
+        x[inp.table[1, 0]] = 0
+    want, _, tol, _ = ref.attend(inp)
+    assert ref.worst(_np(out), want, tol) <= 1
 
 
 def test_table_of_unread_junk_and_shared_pages():
@@ -238,13 +240,14 @@ def test_whole_flow():
     import torch
     Bn, H, G, ps, keep, recent = 2, 2, 4, 16, 48, 9
     rng = np.random.default_rng(5)
+
+    def normal(*shape):
+        return torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).bfloat16().cuda()
     pool = B.new_q4_pool(40, H, ps)
     lens = [70, 100]
     table = torch.arange(14, dtype=torch.int32, device="cuda").view(2, 7)
     ctx = torch.tensor([100, 100], dtype=torch.int32, device="cuda")
-    x = [torch.from_numpy(rng.standard_normal((Bn, H, 100, 128)).astype(np.float32)).bfloat16().cuda()
-         for _ in range(2)]
-    ws = B.append_kv_q4(*x, pool, table, ctx)
+    ws = B.append_kv_q4(normal(Bn, H, 100, 128), normal(Bn, H, 100, 128), pool, table, ctx)
     ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
 
     def check(q, out, table, ctx, w_out, w_in):
@@ -254,11 +257,11 @@ def test_whole_flow():
         inp.dense = [ref.dequantise(*raw[:2]), ref.dequantise(*raw[2:])]
         inp.w = np.zeros(tuple(w_out.shape))
         want, w, tol, w_tol = ref.attend(inp)
-        assert np.all(np.abs(_np(out) - want) <= tol)
-        err = np.abs(_np(w_out) - (w + _np(w_in) * (np.arange(w.shape[2]) < inp.ctx[:, None, None])))
-        assert np.all(err <= w_tol + 2.0 ** -23 * _np(w_out))
+        assert ref.worst(_np(out), want, tol) <= 1
+        w += _np(w_in) * (np.arange(w.shape[2]) < inp.ctx[:, None, None])
+        assert ref.worst(_np(w_out), w, w_tol + 2.0 ** -23 * w) <= 1
 
-    q = torch.from_numpy(rng.standard_normal((Bn, H * G, 8, 128)).astype(np.float32)).bfloat16().cuda()
+    q = normal(Bn, H * G, 8, 128)
     w = torch.zeros(Bn, H, 112, device="cuda")
     out = B.paged_attention_q4(q, pool, table, ctx, ps, key_weights_out=w)
     check(q, out, table, ctx, w, torch.zeros_like(w))
@@ -272,10 +275,9 @@ def test_whole_flow():
     w[:, :, :keep] = new.key_weights
     for step in range(3):
         ctx = ctx + 1
-        n = [torch.from_numpy(rng.standard_normal((Bn, H, 1, 128)).astype(np.float32)).bfloat16().cuda()
-             for _ in range(2)]
-        B.append_kv_q4(*n, pool, table, ctx, workspace=ws)
-        q = torch.from_numpy(rng.standard_normal((Bn, H * G, 1, 128)).astype(np.float32)).bfloat16().cuda()
+        B.append_kv_q4(normal(Bn, H, 1, 128), normal(Bn, H, 1, 128), pool, table, ctx,
+                       workspace=ws)
+        q = normal(Bn, H * G, 1, 128)
         before = w.clone()
         out = B.paged_attention_q4(q, pool, table, ctx, ps, key_weights=w, key_weights_out=w)
         check(q, out, table, ctx, w, before)
