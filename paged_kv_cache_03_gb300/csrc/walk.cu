@@ -52,6 +52,8 @@ struct WalkParams {
     float4* part_ml;  // [(b, kvh, row)][chunk]: max, sum of the applied weights, sum
     float* part_o;    // [(b, kvh, row)][chunk][D]
     float* lse;       // [(b, kvh, row)] log2 of the sum of 2^score, or null
+    float* score;     // [(b, kvh)][key < cap][row] scores in log2 units, or null
+    long long cap;    // keys of a (b, kvh) in score
     const float* w_in;
     float* w_out;
     long long w_S;
@@ -389,7 +391,7 @@ struct QueryFrags {
 };
 
 // ---------------------------------------------------------------------------
-template <class Keys, class Values, int NT, bool F32, bool A16>
+template <class Keys, class Values, int NT, bool F32, bool A16, bool W>
 __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
     constexpr bool F16 = Keys::kF16;
     constexpr int ROWS = 8 * NT;
@@ -511,6 +513,25 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (base + 16 * u + g + 8 * (e >> 1) > lim[n][e & 1]) s[n][u][e] = neg_inf();
+        }
+        if constexpr (W) {  // (keys past the chunk's last one stay inside the table)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = base + 16 * u + g + 8 * h, rr = 8 * n + 2 * t;
+                        if (key >= p.cap) continue;
+                        float* const to = p.score + ((static_cast<long long>(b) * p.H_kv + kvh) * p.cap + key) * p.R + rr;
+                        const float x0 = s[n][u][2 * h] * qs[n][0], x1 = s[n][u][2 * h + 1] * qs[n][1];
+                        if (rr + 1 < nrows && p.R % 2 == 0) {
+                            *reinterpret_cast<float2*>(to) = make_float2(x0, x1);
+                        } else {
+                            if (rr < nrows) to[0] = x0;
+                            if (rr + 1 < nrows) to[1] = x1;
+                        }
+                    }
         }
         uint32_t pb[NT][U][2], pl[NT][U][2];  // P^T fragments, and their low parts
 #pragma unroll
@@ -687,71 +708,441 @@ __global__ void __launch_bounds__(128) walk_combine_kernel(const WalkParams p) {
     if (lane == 0 && p.lse) p.lse[row] = lt > 0.f ? M + log2f(lt) : __int_as_float(0x7f800000);
 }
 
-// w_out[b, kvh, k] = w_in[b, kvh, k] + the rows' probabilities of key k, 0 past
-// the context.  A warp holds 16 keys as A fragments and runs over the rows.
-template <class Keys, bool F32>
-__global__ void __launch_bounds__(kWarps * 32) walk_weights_kernel(const WalkParams p, int ntile) {
+// ---- many rows: tiles of 64 keys shared by 64 rows --------------------------
+//
+// With more rows than a warp holds, dequantising per warp would cost more than
+// the products.  Here a CTA's four warps take 16 rows each (M = rows) and the
+// 64-key K and V tiles go through shared memory once, as f16 (4-bit pages) or
+// as they are (bf16): S = Q K^T with K by ldmatrix, O += P V with V by
+// ldmatrix.trans.  Two buffers: the next tile is requested when a tile begins
+// and, 4-bit, written dequantised when it ends.  A 256-byte row holds its even
+// 16-byte chunks first, then the odd ones, both permuted by the row's low bits:
+// the writers (32 bytes a lane) and ldmatrix meet no bank conflict.
+constexpr int kTK = 64;
+constexpr int kTileBytes = kTK * kD * 2;
+
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+    return static_cast<uint32_t>(row * 256 + (c & 1) * 128 + (((c >> 1) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
+template <bool Q4>
+struct TileLoader;
+
+template <>
+struct TileLoader<true> {  // thread: dims 16 grp .. of keys (tid >> 3) + 16 i
+    uint2 c[4][2];
+    uint32_t s[4][2];
+    __device__ __forceinline__ void request(const WalkParams& p, int b, int kvh, int base, int S, uint32_t, uint32_t) {
+        const int grp = threadIdx.x & 7;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = base + static_cast<int>(threadIdx.x >> 3) + 16 * i;
+            const int lp = key / p.ps;
+            const int pg = key < S ? page_of(p, b, lp, INT_MAX) : -1;
+            c[i][0] = c[i][1] = make_uint2(0u, 0u);
+            s[i][0] = s[i][1] = 0u;
+            if (pg >= 0) {
+                const long long r = static_cast<long long>(pg * p.H_kv + kvh) * p.ps + (key - lp * p.ps);
+                c[i][0] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.kc) + r * kQ4CodeBytes) + grp);
+                c[i][1] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.vc) + r * kQ4CodeBytes) + grp);
+                s[i][0] = __ldg(static_cast<const uint8_t*>(p.ks) + r * kQ4Groups + grp);
+                s[i][1] = __ldg(static_cast<const uint8_t*>(p.vs) + r * kQ4Groups + grp);
+            }
+        }
+    }
+    __device__ __forceinline__ void finish(uint32_t kbuf, uint32_t vbuf) {
+        const int grp = threadIdx.x & 7;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = static_cast<int>(threadIdx.x >> 3) + 16 * i;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t s2 = e4m3x2_to_f16x2(s[i][kv] | (s[i][kv] << 8));
+                uint32_t h[8];
+                e2m1x8_to_f16x2(c[i][kv].x, *reinterpret_cast<uint32_t(*)[4]>(h));
+                e2m1x8_to_f16x2(c[i][kv].y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[j] = hmul2(h[j], s2);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((kv ? vbuf : kbuf) + chunk_at(row, 2 * grp + j)),
+                                 "r"(h[4 * j]), "r"(h[4 * j + 1]), "r"(h[4 * j + 2]), "r"(h[4 * j + 3])
+                                 : "memory");
+            }
+        }
+    }
+};
+
+template <>
+struct TileLoader<false> {  // thread: chunk tid & 15 of keys (tid >> 4) + 8 i
+    __device__ __forceinline__ void request(const WalkParams& p, int b, int kvh, int base, int S, uint32_t kbuf,
+                                            uint32_t vbuf) {
+        const int c = threadIdx.x & 15;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = static_cast<int>(threadIdx.x >> 4) + 8 * i, key = base + row;
+            const int lp = key / p.ps;
+            const int pg = key < S ? page_of(p, b, lp, INT_MAX) : -1;
+            const long long r = pg >= 0 ? static_cast<long long>(pg * p.H_kv + kvh) * p.ps + (key - lp * p.ps) : 0;
+            cp_async16(kbuf + chunk_at(row, c), static_cast<const uint8_t*>(p.kc) + r * (2 * kD) + 16 * c, pg >= 0);
+            cp_async16(vbuf + chunk_at(row, c), static_cast<const uint8_t*>(p.vc) + r * (2 * kD) + 16 * c, pg >= 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void finish(uint32_t, uint32_t) { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+};
+
+// Dim pairs of Q's A fragments: the natural order (K's tile is in it).
+template <bool Q4>
+struct NaturalDims {
+    static constexpr bool kF16 = Q4;
+    __device__ static int qdim(int j, int half, int t) { return 16 * j + 8 * half + 2 * t; }
+};
+
+template <bool Q4, bool F32>
+__global__ void __launch_bounds__(kWarps * 32) block_kernel(const WalkParams p) {
+    constexpr int ROWS = 16 * kWarps;
+    extern __shared__ __align__(1024) uint8_t smem[];  // K, V, K, V tiles
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     int item = static_cast<int>(blockIdx.x);
-    const int tile = item % ntile;
-    item /= ntile;
+    const int kc = item % p.nkc;
+    item /= p.nkc;
+    const int rc = p.nrc - 1 - item % p.nrc;  // the longest rows first
+    item /= p.nrc;
     const int kvh = item % p.H_kv, b = item / p.H_kv;
-    const long long base = (static_cast<long long>(tile) * kWarps + warp) * 16;
+    const int S = seq_len(p, b, kc == 0 && rc == 0 && kvh == 0 && threadIdx.x == 0);
+    const int r0 = rc * ROWS, nrows = min(ROWS, p.R - r0);
+    const long long row0 = (static_cast<long long>(b) * p.H_kv + kvh) * p.R + r0;
+    // the last key each of this lane's rows (g, g + 8 of the warp's 16) sees, and
+    // the extremes over the warp and the CTA
+    int lim[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int rr = 16 * warp + g + 8 * e;
+        lim[e] = rr < nrows ? (p.causal ? (r0 + rr) % p.L + S - p.L : S - 1) : -1;
+    }
+    int cta_max = S - 1;
+    if (p.causal) {  // rows r0 .. r0 + nrows - 1: positions r % L
+        const int l0 = r0 % p.L;
+        cta_max = (l0 + nrows - 1 >= p.L ? p.L - 1 : l0 + nrows - 1) + S - p.L;
+    }
+    int lim_min = min(lim[0] < 0 ? INT_MAX : lim[0], lim[1] < 0 ? INT_MAX : lim[1]), lim_max = max(lim[0], lim[1]);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
+        lim_max = max(lim_max, __shfl_xor_sync(0xffffffffu, lim_max, o));
+    }
+    const int k0 = kc * p.C, k1 = S > 0 ? min(cta_max + 1, k0 + p.C) : 0;
+
+    // A fragments of the warp's 16 rows: two sets of 8 rows, as B fragments are
+    QueryFrags<NaturalDims<Q4>, F32> q[2];
+    float qs[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int rr = 16 * warp + g + 8 * e;
+        qs[e] = fmaxf(q[e].load(p.q, row0 + rr, rr < nrows, t) * p.scale_log2, FLT_MIN);
+    }
+    float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f}, la[2] = {0.f, 0.f};
+    float o[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    const uint32_t buf = smem_u32(smem);
+    TileLoader<Q4> ld;
+    if (k0 < k1) {
+        ld.request(p, b, kvh, k0, S, buf, buf + kTileBytes);
+        ld.finish(buf, buf + kTileBytes);
+    }
+    int cur = 0;
+    for (int base = k0; base < k1; base += kTK, cur ^= 1) {
+        __syncthreads();  // the tile is whole; the other buffer is no longer read
+        const uint32_t kb = buf + cur * 2 * kTileBytes, vb = kb + kTileBytes;
+        const uint32_t kn = buf + (cur ^ 1) * 2 * kTileBytes, vn = kn + kTileBytes;
+        const bool more = base + kTK < k1;
+        if (more) ld.request(p, b, kvh, base + kTK, S, kn, vn);
+        if (base <= lim_max) {  // (uniform over the warp)
+            float s[8][4];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // 16 dims
+                const uint32_t a[4] = {q[0].hi[j][0], q[1].hi[j][0], q[0].hi[j][1], q[1].hi[j][1]};
+                uint32_t al[4];
+                if constexpr (F32) {
+                    al[0] = q[0].lo[j][0];
+                    al[1] = q[1].lo[j][0];
+                    al[2] = q[0].lo[j][1];
+                    al[3] = q[1].lo[j][1];
+                }
+#pragma unroll
+                for (int n = 0; n < 8; n += 2) {  // 16 keys
+                    uint32_t x[4];
+                    ldmatrix_x4(x, kb + chunk_at(8 * n + (lane & 7) + 8 * (lane >> 4), 2 * j + ((lane >> 3) & 1)));
+                    mma<Q4>(s[n], a, x[0], x[1]);
+                    mma<Q4>(s[n + 1], a, x[2], x[3]);
+                    if constexpr (F32) {
+                        mma<Q4>(s[n], al, x[0], x[1]);
+                        mma<Q4>(s[n + 1], al, x[2], x[3]);
+                    }
+                }
+            }
+            if (base + kTK - 1 > lim_min) {
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (base + 8 * n + 2 * t + (e & 1) > lim[e >> 1]) s[n][e] = neg_inf();
+            }
+            float mt[2] = {neg_inf(), neg_inf()};
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                mt[0] = fmax3(mt[0], s[n][0], s[n][1]);
+                mt[1] = fmax3(mt[1], s[n][2], s[n][3]);
+            }
+            mt[0] *= qs[0];
+            mt[1] *= qs[1];
+            if (__any_sync(0xffffffffu, mt[0] > m[0] + kLazyRescaleLog2 || mt[1] > m[1] + kLazyRescaleLog2)) {
+                float al[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], 1));
+                    mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], 2));
+                    const bool grow = mt[e] > m[e] + kLazyRescaleLog2;
+                    al[e] = grow ? fast_exp2(m[e] - mt[e]) : 1.f;  // 2^-inf = 0 at the start
+                    if (grow) m[e] = mt[e];
+                    l[e] *= al[e];
+                    la[e] *= al[e];
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    o[i][0] *= al[0];
+                    o[i][1] *= al[0];
+                    o[i][2] *= al[1];
+                    o[i][3] *= al[1];
+                }
+            }
+            const float mu[2] = {m[0] == neg_inf() ? 0.f : m[0], m[1] == neg_inf() ? 0.f : m[1]};
+#pragma unroll
+            for (int n = 0; n < 8; n += 2) {  // 16 keys: P's A fragment, then O += P V
+                uint32_t a[4], al[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)  // keys 8 (n + h) .., rows g and g + 8
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float p0 = fast_exp2(fmaf(s[n + h][2 * e], qs[e], -mu[e]));
+                        const float p1 = fast_exp2(fmaf(s[n + h][2 * e + 1], qs[e], -mu[e]));
+                        l[e] += p0 + p1;
+                        if constexpr (Q4) {
+                            const uint32_t x = pack_f16x2(p0, p1);
+                            a[2 * h + e] = x;
+                            if constexpr (F32) {
+                                const float2 f = f16x2_to_float2(x);
+                                al[2 * h + e] = pack_f16x2(p0 - f.x, p1 - f.y);
+                            }
+                        } else {
+                            const uint32_t x = pack_bf16x2(p0, p1);
+                            const float2 f = bf16x2_to_float2(x);
+                            la[e] += f.x + f.y;
+                            a[2 * h + e] = x;
+                        }
+                    }
+#pragma unroll
+                for (int d = 0; d < 16; d += 2) {  // 16 dims
+                    uint32_t x[4];
+                    ldmatrix_x4_trans(x, vb + chunk_at(8 * n + (lane & 15), d + (lane >> 4)));
+                    mma<Q4>(o[d], a, x[0], x[1]);
+                    mma<Q4>(o[d + 1], a, x[2], x[3]);
+                    if constexpr (F32) {
+                        mma<Q4>(o[d], al, x[0], x[1]);
+                        mma<Q4>(o[d + 1], al, x[2], x[3]);
+                    }
+                }
+            }
+        }
+        if (more) ld.finish(kn, vn);
+    }
+    // rows g and g + 8: dims 8 d + 2t, + 1
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+            la[e] += __shfl_xor_sync(0xffffffffu, la[e], d);
+        }
+        const int rr = 16 * warp + g + 8 * e;
+        if (rr >= nrows) continue;
+        const float at = Q4 ? l[e] : la[e];
+        const long long row = row0 + rr;
+        if (p.nkc == 1) {
+            const float inv = at > 0.f ? 1.f / at : 0.f;
+#pragma unroll
+            for (int d = 0; d < 16; ++d) {
+                const float x = o[d][2 * e] * inv, y = o[d][2 * e + 1] * inv;
+                if constexpr (F32)
+                    *reinterpret_cast<float2*>(static_cast<float*>(p.out) + row * kD + 8 * d + 2 * t) = make_float2(x, y);
+                else
+                    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * kD + 8 * d + 2 * t) = pack_bf16x2(x, y);
+            }
+            if (t == 0 && p.lse) p.lse[row] = l[e] > 0.f ? m[e] + log2f(l[e]) : __int_as_float(0x7f800000);
+        } else {
+            if (t == 0) p.part_ml[row * p.nkc + kc] = make_float4(l[e] > 0.f ? m[e] : neg_inf(), at, l[e], 0.f);
+            if (l[e] > 0.f) {
+#pragma unroll
+                for (int d = 0; d < 16; ++d)
+                    *reinterpret_cast<float2*>(p.part_o + (row * p.nkc + kc) * kD + 8 * d + 2 * t) =
+                        make_float2(o[d][2 * e], o[d][2 * e + 1]);
+            }
+        }
+    }
+}
+
+// w_out[b, kvh, k] = w_in[b, kvh, k] + the rows' probabilities of key k, 0 past
+// the context, from the scores that walk_kernel left.  One thread per key; the
+// R scores of a key lie together, so a warp reads them as whole lines.
+__global__ void __launch_bounds__(256) walk_sum_kernel(const WalkParams p, int ntile) {
+    pdl_wait_primary();
+    const int tile = static_cast<int>(blockIdx.x) % ntile;
+    const long long bk = static_cast<int>(blockIdx.x) / ntile;
+    const long long k = static_cast<long long>(tile) * 256 + threadIdx.x;
+    if (k >= p.w_S) return;
+    const int S = seq_len(p, static_cast<int>(bk / p.H_kv), false);
+    float acc = 0.f;
+    if (k < S) {
+        const float* const x = p.score + (bk * p.cap + k) * p.R;
+        const float* const lse = p.lse + bk * p.R;
+        if (p.R % 4 == 0) {
+            for (int r = 0; r < p.R; r += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(x + r);
+                acc += fast_exp2(v.x - lse[r]);
+                acc += fast_exp2(v.y - lse[r + 1]);
+                acc += fast_exp2(v.z - lse[r + 2]);
+                acc += fast_exp2(v.w - lse[r + 3]);
+            }
+        } else {
+            for (int r = 0; r < p.R; ++r) acc += fast_exp2(x[r] - lse[r]);
+        }
+        if (p.w_in) acc += p.w_in[bk * p.w_S + k];
+    }
+    p.w_out[bk * p.w_S + k] = acc;
+}
+
+// The same from the query and the keys, for many rows: a CTA takes 128 keys of
+// one (sequence, kv head), each warp 32 of them as A fragments in registers, and
+// runs over the rows in chunks of 64 whose B fragments the warps lay out in
+// shared memory once per chunk (16 bytes a lane and k-step pair).  Bound by the
+// warp-level MMA rate (8 cycles per m16n8k16 and SM sub-partition).
+constexpr int kChunkTiles = 8;  // n-tiles of 8 rows per shared-memory chunk
+
+template <class Keys, bool F32>
+__global__ void __launch_bounds__(kWarps * 32) walk_weights_kernel(const WalkParams p, int ntile) {
+    constexpr int PARTS = F32 ? 2 : 1;
+    __shared__ uint4 qsm[PARTS][kChunkTiles][4][32];
+    __shared__ float qs_s[kChunkTiles * 8], lse_s[kChunkTiles * 8];
+    __shared__ int lim_s[kChunkTiles * 8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int tile = static_cast<int>(blockIdx.x) % ntile, bk = static_cast<int>(blockIdx.x) / ntile;
+    const int b = bk / p.H_kv, kvh = bk - b * p.H_kv;
+    const long long cta0 = static_cast<long long>(tile) * (32 * kWarps);
     const int S = seq_len(p, b, false);
-    float acc[2] = {0.f, 0.f};  // keys g and g + 8, this lane's rows
-    if (base < S) {
-        const int k0 = static_cast<int>(base);
-        StepWalker<false, 1> wk;
-        wk.start(p, k0 + lane, 0);
-        int pg[2];
-        wk.pages(p, b, k0 + lane < S && lane < 16 ? INT_MAX : 0, pg);
-        const StepRows<false, 1> rows = wk.rows(p, kvh, pg);
-        Keys kk;
-        kk.load(p, rows, 0, g, t);
-        const typename Keys::Scales ksc = kk.scales();
-        const long long row0 = (static_cast<long long>(b) * p.H_kv + kvh) * p.R;
-        for (int r0 = 0; r0 < p.R; r0 += 8) {
-            QueryFrags<Keys, F32> q;
-            const float down = q.load(p.q, row0 + r0 + g, r0 + g < p.R, t);
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
+    float acc[2][2] = {};  // keys g and g + 8 of both halves, this lane's rows
+    if (cta0 < S) {        // (uniform over the CTA)
+        const int k0 = static_cast<int>(cta0) + 32 * warp;
+        uint32_t a[2][8][4];
+        {
+            StepWalker<false, 2> wk;
+            wk.start(p, k0 + lane, 0);
+            int pg[2];
+            wk.pages(p, b, k0 + lane < S ? INT_MAX : 0, pg);
+            const StepRows<false, 2> rows = wk.rows(p, kvh, pg);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t a[2][4];
-                kk.frags(ksc, i, a);
+            for (int u = 0; u < 2; ++u) {
+                Keys kk;
+                kk.load(p, rows, u, g, t);
+                const typename Keys::Scales ksc = kk.scales();
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    mma<Keys::kF16>(s, a[j], q.hi[2 * i + j][0], q.hi[2 * i + j][1]);
-                    if constexpr (F32) mma<Keys::kF16>(s, a[j], q.lo[2 * i + j][0], q.lo[2 * i + j][1]);
+                for (int i = 0; i < 4; ++i) kk.frags(ksc, i, *reinterpret_cast<uint32_t(*)[2][4]>(a[u][2 * i]));
+            }
+        }
+        const long long row0 = static_cast<long long>(bk) * p.R;
+        for (int r0 = 0; r0 < p.R; r0 += 8 * kChunkTiles) {
+            const int nt = min(kChunkTiles, (p.R - r0 + 7) / 8);
+            __syncthreads();
+            for (int n = warp; n < nt; n += kWarps) {
+                const int r = r0 + 8 * n + g;
+                QueryFrags<Keys, F32> q;
+                const float down = q.load(p.q, row0 + r, r < p.R, t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    qsm[0][n][i][lane] = make_uint4(q.hi[2 * i][0], q.hi[2 * i][1], q.hi[2 * i + 1][0], q.hi[2 * i + 1][1]);
+                    if constexpr (F32)
+                        qsm[1][n][i][lane] = make_uint4(q.lo[2 * i][0], q.lo[2 * i][1], q.lo[2 * i + 1][0], q.lo[2 * i + 1][1]);
+                }
+                if (t == 0) {
+                    qs_s[8 * n + g] = fmaxf(down * p.scale_log2, FLT_MIN);
+                    // (a row past the last one weighs 2^-inf = 0)
+                    lse_s[8 * n + g] = r < p.R ? p.lse[row0 + r] : __int_as_float(0x7f800000);
+                    lim_s[8 * n + g] = p.causal ? r % p.L + S - p.L : S - 1;
                 }
             }
+            __syncthreads();
+            for (int n = 0; n < nt; ++n) {
+                const float2 qs = *reinterpret_cast<const float2*>(qs_s + 8 * n + 2 * t);
+                const float2 nl = *reinterpret_cast<const float2*>(lse_s + 8 * n + 2 * t);
+                const int2 lim = *reinterpret_cast<const int2*>(lim_s + 8 * n + 2 * t);
+                if (!__any_sync(0xffffffffu, max(lim.x, lim.y) >= k0)) continue;
+                float s[2][4] = {};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float qs = fmaxf(__shfl_sync(0xffffffffu, down, 8 * t + 4 * e) * p.scale_log2, FLT_MIN);
-                const int r = r0 + 2 * t + e;
-                if (r >= p.R) continue;
-                const int lim = p.causal ? r % p.L + S - p.L : S - 1;
-                const float lse = p.lse[row0 + r];
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 x = qsm[0][n][i][lane];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int k = g + 8 * h;
-                    if (k0 + k <= lim) acc[h] += fast_exp2(s[2 * h + e] * qs - lse);
+                    for (int u = 0; u < 2; ++u) {
+                        mma<Keys::kF16>(s[u], a[u][2 * i], x.x, x.y);
+                        mma<Keys::kF16>(s[u], a[u][2 * i + 1], x.z, x.w);
+                    }
+                    if constexpr (F32) {
+                        const uint4 y = qsm[PARTS - 1][n][i][lane];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            mma<Keys::kF16>(s[u], a[u][2 * i], y.x, y.y);
+                            mma<Keys::kF16>(s[u], a[u][2 * i + 1], y.z, y.w);
+                        }
+                    }
                 }
+                if (__any_sync(0xffffffffu, k0 + 31 > min(lim.x, lim.y))) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (k0 + 16 * u + g + 8 * (e >> 1) > (e & 1 ? lim.y : lim.x)) s[u][e] = neg_inf();
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        acc[u][h] += fast_exp2(fmaf(s[u][2 * h], qs.x, -nl.x)) + fast_exp2(fmaf(s[u][2 * h + 1], qs.y, -nl.y));
             }
         }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        acc[h] += __shfl_xor_sync(0xffffffffu, acc[h], 1);
-        acc[h] += __shfl_xor_sync(0xffffffffu, acc[h], 2);
-    }
-    if (t < 2) {
-        const long long k = base + g + 8 * t;
-        if (k < p.w_S) {
-            const long long at = (static_cast<long long>(b) * p.H_kv + kvh) * p.w_S + k;
-            const float old = p.w_in && k < S ? p.w_in[at] : 0.f;
-            p.w_out[at] = k < S ? old + (t ? acc[1] : acc[0]) : 0.f;
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            acc[u][h] += __shfl_xor_sync(0xffffffffu, acc[u][h], 1);
+            acc[u][h] += __shfl_xor_sync(0xffffffffu, acc[u][h], 2);
         }
+    // lane t of the quad writes half t >> 1, key g + 8 (t & 1)
+    const float mine = t & 2 ? (t & 1 ? acc[1][1] : acc[1][0]) : (t & 1 ? acc[0][1] : acc[0][0]);
+    const long long k = cta0 + 32 * warp + 16 * (t >> 1) + g + 8 * (t & 1);
+    if (k < p.w_S) {
+        const long long at = static_cast<long long>(bk) * p.w_S + k;
+        const float old = p.w_in && k < S ? p.w_in[at] : 0.f;
+        p.w_out[at] = k < S ? old + mine : 0.f;
     }
 }
 
@@ -759,21 +1150,28 @@ __global__ void __launch_bounds__(kWarps * 32) walk_weights_kernel(const WalkPar
 // host side
 // ---------------------------------------------------------------------------
 struct WalkPlan {
-    int R, nt, nrc, nkc, C;
-    size_t ml_off, o_off, lse_off, total;
+    int R, nt, nrc, nkc, C;  // nt: n-tiles of 8 rows of walk_kernel, 0: block_kernel
+    bool scores;             // key weights from stored scores
+    size_t ml_off, o_off, lse_off, score_off, total;
 };
 
-// Rows per CTA: 8, or 16 where a (sequence, kv head) has more than 8 (not for
-// fp32 queries, whose fragments take twice the registers).  Key chunks: enough
-// for about eight CTAs per SM, of at least 256 keys.
+constexpr int kBlockRows = 32;  // rows per kv head from which block_kernel takes a call
+constexpr int kScoreRows = 8;   // rows per kv head up to which scores are stored
+
+// walk_kernel: 8 rows per CTA, or 16 where a (sequence, kv head) has more than
+// 8 (not for fp32 queries, whose fragments take twice the registers);
+// block_kernel: 64.  Key chunks: enough for about eight CTAs per SM (block: four), of
+// at least 256 keys.
 WalkPlan plan(const pa_shape& sh, bool weights, int sm_count) {
     WalkPlan w;
     w.R = sh.H_q / sh.H_kv * sh.L;
-    w.nt = w.R > 8 && sh.dtype == PA_BF16 ? 2 : 1;
-    w.nrc = (w.R + 8 * w.nt - 1) / (8 * w.nt);
+    w.nt = w.R >= kBlockRows ? 0 : w.R > 8 && sh.dtype == PA_BF16 ? 2 : 1;
+    const int rows_cta = w.nt ? 8 * w.nt : 16 * kWarps;
+    w.nrc = (w.R + rows_cta - 1) / rows_cta;
+    w.scores = weights && w.R <= kScoreRows;
     const long long cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     const long long items = static_cast<long long>(sh.B) * sh.H_kv * w.nrc;
-    long long nkc = (8ll * sm_count + items - 1) / items;
+    long long nkc = ((w.nt ? 8ll : 4ll) * sm_count + items - 1) / items;
     const long long most = (cap + 255) / 256;
     nkc = nkc < most ? nkc : most;
     long long C = (cap + nkc - 1) / nkc;
@@ -788,44 +1186,91 @@ WalkPlan plan(const pa_shape& sh, bool weights, int sm_count) {
     if (w.nkc > 1) off = align_up(off + rows * w.nkc * kD * 4, 256);
     w.lse_off = off;
     if (weights) off = align_up(off + rows * 4, 256);
+    w.score_off = off;
+    if (w.scores) off = align_up(off + rows * cap * 4, 256);
     w.total = off;
     return w;
 }
 
-template <class Keys, class Values, int NT, bool F32, bool A16>
-pa_status launch_as(const WalkParams& p, cudaStream_t stream) {
+// Launches `kernel`, whose start may overlap the end of the kernel before it.
+template <class... P, class... A>
+bool launch_dependent(void (*kernel)(P...), long long grid, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+// The attention, its merge over key chunks, then the key weights.
+template <class Keys, class Values, int NT, bool F32, bool A16, bool W>
+pa_status launch_walk(const WalkParams& p, long long items, cudaStream_t stream) {
     constexpr size_t smem = sizeof(float) * kWarps * 8 * NT * kMerge;
     static_assert(smem <= 48 * 1024, "merge buffer within the default limit");
-    const long long items = static_cast<long long>(p.B) * p.H_kv * p.nrc * p.nkc;
-    const long long rows = static_cast<long long>(p.B) * p.H_kv * p.R;
-    const long long ntile = (p.w_S + 16 * kWarps - 1) / (16 * kWarps);
-    if (items > INT_MAX || rows > 4ll * INT_MAX || ntile * p.B * p.H_kv > INT_MAX) return PA_ERR_UNSUPPORTED;
-    walk_kernel<Keys, Values, NT, F32, A16><<<static_cast<unsigned>(items), kWarps * 32, smem, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
-    if (p.nkc > 1) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
-        cfg.blockDim = dim3(128);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, walk_combine_kernel<F32>, p) != cudaSuccess) return PA_ERR_CUDA;
-    }
-    if (p.w_out) {
-        walk_weights_kernel<Keys, F32><<<static_cast<unsigned>(ntile * p.B * p.H_kv), kWarps * 32, 0, stream>>>(
-            p, static_cast<int>(ntile));
-        if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
-    }
-    return PA_OK;
+    walk_kernel<Keys, Values, NT, F32, A16, W><<<static_cast<unsigned>(items), kWarps * 32, smem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <class Keys, class Values, int NT, bool F32>
-pa_status launch(const WalkParams& p, cudaStream_t stream) {
-    return p.ps % 16 == 0 ? launch_as<Keys, Values, NT, F32, true>(p, stream)
-                          : launch_as<Keys, Values, NT, F32, false>(p, stream);
+pa_status launch_walk_for(const WalkParams& p, long long items, cudaStream_t stream) {
+    const bool a16 = p.ps % 16 == 0;
+    if constexpr (NT == 1) {
+        if (p.score) return a16 ? launch_walk<Keys, Values, NT, F32, true, true>(p, items, stream)
+                                : launch_walk<Keys, Values, NT, F32, false, true>(p, items, stream);
+    }
+    return a16 ? launch_walk<Keys, Values, NT, F32, true, false>(p, items, stream)
+               : launch_walk<Keys, Values, NT, F32, false, false>(p, items, stream);
+}
+
+template <bool Q4, bool F32>
+pa_status launch_block(const WalkParams& p, long long items, int device, cudaStream_t stream) {
+    static int attr_done[64] = {0};
+    if (!attr_done[device]) {
+        if (cudaFuncSetAttribute(block_kernel<Q4, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 4 * kTileBytes) != cudaSuccess)
+            return PA_ERR_CUDA;
+        attr_done[device] = 1;
+    }
+    block_kernel<Q4, F32><<<static_cast<unsigned>(items), kWarps * 32, 4 * kTileBytes, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, int device, cudaStream_t stream) {
+    const long long bk = static_cast<long long>(p.B) * p.H_kv;
+    const long long items = bk * p.nrc * p.nkc, rows = bk * p.R;
+    const long long per = w.scores ? 256 : 32 * kWarps, ntile = (p.w_S + per - 1) / per;
+    if (items > INT_MAX || rows > 4ll * INT_MAX || ntile * bk > INT_MAX) return PA_ERR_UNSUPPORTED;
+    pa_status st;
+    if (w.nt == 0)
+        st = !q4 ? launch_block<false, false>(p, items, device, stream)
+                 : f32 ? launch_block<true, true>(p, items, device, stream)
+                       : launch_block<true, false>(p, items, device, stream);
+    else if (!q4)
+        st = w.nt == 2 ? launch_walk_for<BfKeys, BfValues, 2, false>(p, items, stream)
+                       : launch_walk_for<BfKeys, BfValues, 1, false>(p, items, stream);
+    else if (f32)
+        st = launch_walk_for<Q4Keys, Q4Values, 1, true>(p, items, stream);
+    else
+        st = w.nt == 2 ? launch_walk_for<Q4Keys, Q4Values, 2, false>(p, items, stream)
+                       : launch_walk_for<Q4Keys, Q4Values, 1, false>(p, items, stream);
+    if (st != PA_OK) return st;
+    if (p.nkc > 1 && !launch_dependent(f32 ? walk_combine_kernel<true> : walk_combine_kernel<false>, (rows + 3) / 4, 128, stream, p))
+        return PA_ERR_CUDA;
+    if (!p.w_out) return PA_OK;
+    if (w.scores) return launch_dependent(walk_sum_kernel, ntile * bk, 256, stream, p, static_cast<int>(ntile)) ? PA_OK : PA_ERR_CUDA;
+    const unsigned grid = static_cast<unsigned>(ntile * bk);
+    if (!q4)
+        walk_weights_kernel<BfKeys, false><<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(ntile));
+    else if (f32)
+        walk_weights_kernel<Q4Keys, true><<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(ntile));
+    else
+        walk_weights_kernel<Q4Keys, false><<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(ntile));
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 // ---- many rows over 4-bit pages: dense bf16 copies and the tensor-core tiles --
@@ -954,13 +1399,9 @@ pa_status walk_launch(const WalkCall& c) {
     p.C = w.C;
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     p.scale_log2 = c.scale * 1.4426950408889634f;
-    if (!c.ks) {
-        if (w.nt == 2) return launch<BfKeys, BfValues, 2, false>(p, c.stream);
-        return launch<BfKeys, BfValues, 1, false>(p, c.stream);
-    }
-    if (sh.dtype == PA_F32) return launch<Q4Keys, Q4Values, 1, true>(p, c.stream);
-    if (w.nt == 2) return launch<Q4Keys, Q4Values, 2, false>(p, c.stream);
-    return launch<Q4Keys, Q4Values, 1, false>(p, c.stream);
+    p.score = w.scores ? reinterpret_cast<float*>(ws + w.score_off) : nullptr;
+    p.cap = p.max_S;
+    return launch(p, w, c.ks != nullptr, sh.dtype == PA_F32, c.dev.device, c.stream);
 }
 
 }  // namespace pa
