@@ -312,7 +312,7 @@ pa_status pa_paged_attention_decode_noalloc(const pa_shape* shape, const void* q
  * (72 bytes, 28% of a bf16 row):
  *   codes  [num_pages, H_kv, page_size, 64] bytes, 16-byte aligned: e2m1, dim
  *          2i in the low half of byte i, dim 2i + 1 in the high half;
- *   scales [num_pages, H_kv, page_size, 8] bytes, 8-byte aligned: e4m3, one
+ *   scales [num_pages, H_kv, page_size, 8] bytes, 16-byte aligned: e4m3, one
  *          per 16 consecutive dims, sign bit 0.
  * The value of a dim is code * scale.  pa_append_kv_q4 writes
  *   scale = min(max(RNE_e4m3(max |x| over the 16 dims / 6), 2^-9), 448),

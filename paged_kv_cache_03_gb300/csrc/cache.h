@@ -16,7 +16,7 @@ constexpr int kQ4Groups = kHeadDim / 16;
 
 pa_status q4_append_launch(const pa_shape& sh, const void* k_new, const void* v_new,
                            const pa_q4_pool& pool, const int32_t* bt, const int32_t* ctx,
-                           uint32_t* flag, int sm_count, cudaStream_t stream);
+                           uint32_t* flag, cudaStream_t stream);
 
 // Dense rows [B, H_kv, n, D] (sh.dtype) of positions first + i, first = 0 or,
 // with tail, context_lens[b] - n; outside [0, context_lens[b]) zeros, or with
@@ -49,12 +49,11 @@ struct WalkCall {
 size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_count);
 pa_status walk_launch(const WalkCall& c);
 
-// Eviction: the copied rows are `row_bytes` long in each of `nbuf` buffers.
+// Eviction from the buffers K and V (rows of sh.dtype) or, where buf[2] is not
+// null, K codes, V codes, K scales, V scales.
 struct EvictCall {
     pa_shape sh;
     void* buf[4];
-    int row_bytes[4];
-    int nbuf;
     const int32_t* bt;
     const int32_t* ctx;
     const float* w;

@@ -11,9 +11,8 @@ namespace {
 
 bool on(const void* p, uintptr_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// Codes 16-byte, scales 8-byte aligned.
 bool pool_ok(const pa_q4_pool* p) {
-    return p && on(p->key_codes, 16) && on(p->value_codes, 16) && on(p->key_scales, 8) && on(p->value_scales, 8);
+    return p && on(p->key_codes, 16) && on(p->value_codes, 16) && on(p->key_scales, 16) && on(p->value_scales, 16);
 }
 
 long long capacity(const pa_shape& s) { return static_cast<long long>(s.max_pages_per_seq) * s.page_size; }
@@ -119,8 +118,7 @@ pa_status pa_append_kv_q4(const pa_shape* shape, const void* k_new, const void* 
     st = device_ok(&dev);
     if (st != PA_OK) return st;
     return q4_append_launch(*shape, k_new, v_new, *pool, block_table, context_lens,
-                            static_cast<uint32_t*>(workspace), dev.sm_count,
-                            static_cast<cudaStream_t>(cuda_stream));
+                            static_cast<uint32_t*>(workspace), static_cast<cudaStream_t>(cuda_stream));
 }
 
 pa_status pa_gather_kv_q4(const pa_shape* shape, const pa_q4_pool* pool, const int32_t* block_table,
@@ -174,8 +172,6 @@ pa_status pa_evict_kv(const pa_shape* shape, void* key_pages, void* value_pages,
     EvictCall c = {};
     c.buf[0] = key_pages;
     c.buf[1] = value_pages;
-    c.row_bytes[0] = c.row_bytes[1] = kHeadDim * (shape->dtype == PA_BF16 ? 2 : 4);
-    c.nbuf = 2;
     return evict(shape, c, block_table, context_lens, key_weights, weights_S, keep, recent, dst_block_table,
                  dst_max_pages_per_seq, context_lens_out, key_weights_out, weights_out_S, kept, workspace,
                  workspace_bytes, cuda_stream);
@@ -194,9 +190,6 @@ pa_status pa_evict_kv_q4(const pa_shape* shape, const pa_q4_pool* pool, const in
     c.buf[1] = pool->value_codes;
     c.buf[2] = pool->key_scales;
     c.buf[3] = pool->value_scales;
-    c.row_bytes[0] = c.row_bytes[1] = kQ4CodeBytes;
-    c.row_bytes[2] = c.row_bytes[3] = kQ4Groups;
-    c.nbuf = 4;
     return evict(shape, c, block_table, context_lens, key_weights, weights_S, keep, recent, dst_block_table,
                  dst_max_pages_per_seq, context_lens_out, key_weights_out, weights_out_S, kept, workspace,
                  workspace_bytes, cuda_stream);

@@ -4,9 +4,12 @@
 // to the pages of another block table.
 //
 // evict_select_kernel, one CTA per (sequence, kv head): a radix select over
-// the weights' bits finds the smallest kept weight and how many keys of
-// exactly that weight stay; a block scan in position order then writes the
-// kept positions and their weights.  evict_copy_kernel moves the rows.
+// the weights' bits (11, 11 and 10 of them) finds the smallest kept weight and
+// how many keys of exactly that weight stay; then each warp takes a run of
+// positions, and ballots and one scan over the warps give every kept position
+// its place.  The keys stay in shared memory between the passes where the
+// table's capacity fits.  evict_copy_kernel moves the rows: bound by HBM (each
+// kept row read and written once).
 #include <climits>
 
 #include "cache.h"
@@ -14,7 +17,9 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kCached = 49152;  // keys held in shared memory (192 KB)
 
 struct EvictParams {
     const int32_t* bt;
@@ -38,10 +43,22 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+// Inclusive scan over a warp.
+__device__ __forceinline__ int warp_incl(int v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+
+template <bool kCache>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p) {
-    __shared__ int hist[256];
-    __shared__ int warp_sum[kThreads / 32];
+    __shared__ int hist[kBins];
+    __shared__ int warp_a[kWarps], warp_b[kWarps];
     __shared__ int sel[2];
+    extern __shared__ uint32_t cache[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = static_cast<int>(blockIdx.x) / p.H_kv, kvh = static_cast<int>(blockIdx.x) % p.H_kv;
     int S = __ldg(p.ctx + b);
@@ -54,120 +71,177 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     float* const w_out = p.w_out + static_cast<long long>(blockIdx.x) * p.w_out_S;
     const int n = min(S, p.keep);
     if (tid == 0 && kvh == 0) p.ctx_out[b] = n;
-
-    const bool all = S <= p.keep;
-    const int cand = all ? 0 : S - p.recent;  // positions that compete
-    uint32_t T = 0u;                          // the smallest kept key
-    int left = all ? 0 : p.keep - p.recent;   // keys still to find at or below the prefix
-    if (!all && left > 0) {
-#pragma unroll 1
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0;
-            __syncthreads();
-            for (int base = 0; base < cand; base += kThreads) {
-                const int i = base + tid;
-                const uint32_t key = i < cand ? order_key(w[i]) : 0u;
-                const bool in = i < cand && (shift == 24 || (key >> (shift + 8)) == (T >> (shift + 8)));
-                const uint32_t bin = in ? (key >> shift) & 255u : 256u;
-                const uint32_t same = __match_any_sync(0xffffffffu, bin);
-                if (in && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
-            }
-            __syncthreads();
-            if (tid == 0) {
-                int c = 0, v = 255;
-                while (v > 0 && c + hist[v] < left) c += hist[v--];
-                sel[0] = v;
-                sel[1] = c;
-            }
-            __syncthreads();
-            T |= static_cast<uint32_t>(sel[0]) << shift;
-            left -= sel[1];
-            __syncthreads();
-        }
-    }
-    // `left` keys equal to T stay, those of the lowest positions
-    int gt_before = 0, eq_before = 0;  // over earlier positions
-    for (int base = 0; base < S; base += kThreads) {
-        const int i = base + tid;
-        const float wi = i < S ? w[i] : 0.f;
-        const uint32_t key = order_key(wi);
-        const bool fixed = i < S && (all || i >= cand);
-        const bool gt = fixed || (i < cand && p.keep > p.recent && key > T);
-        const bool eq = !fixed && i < cand && p.keep > p.recent && key == T;
-        // counts of both kinds up to and including this thread, packed
-        int x = (gt ? 1 : 0) | (eq ? 1 << 16 : 0);
-        const int own = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) warp_sum[warp] = x;
-        __syncthreads();
-        int before = x - own, total = 0;
-#pragma unroll
-        for (int v = 0; v < kThreads / 32; ++v) {
-            const int y = warp_sum[v];
-            if (v < warp) before += y;
-            total += y;
-        }
-        __syncthreads();
-        const int eqb = eq_before + (before >> 16), gtb = gt_before + (before & 0xffff);
-        if (gt || (eq && eqb < left)) {
-            const int dst = gtb + min(eqb, left);
-            kept[dst] = i;
-            w_out[dst] = wi;
-        }
-        gt_before += total & 0xffff;
-        eq_before += total >> 16;
-    }
     for (int i = n + tid; i < p.keep; i += kThreads) kept[i] = -1;
     for (long long i = n + tid; i < p.w_out_S; i += kThreads) w_out[i] = 0.f;
+    if (S <= p.keep) {  // all stay
+        for (int i = tid; i < S; i += kThreads) {
+            kept[i] = i;
+            w_out[i] = w[i];
+        }
+        return;
+    }
+
+    const int cand = S - p.recent;  // positions that compete
+    int left = p.keep - p.recent;   // of them, how many stay at or below the prefix
+    uint32_t T = 0u;                // the smallest kept key
+    auto key_at = [&](int i) { return kCache ? cache[i] : order_key(__ldg(w + i)); };
+    for (int i = tid; i < p.recent; i += kThreads) {  // the last positions
+        kept[left + i] = cand + i;
+        w_out[left + i] = w[cand + i];
+    }
+    if (left == 0) return;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t mask = pass == 2 ? 1023u : 2047u;
+        hist[tid] = hist[tid + kThreads] = 0;
+        __syncthreads();
+        const int above = pass == 1 ? 21 : 10;  // bits of T already known
+#pragma unroll 4
+        for (int i = tid; i < cand; i += kThreads) {
+            uint32_t key;
+            if (kCache && pass == 0) {
+                key = order_key(__ldg(w + i));
+                cache[i] = key;
+            } else {
+                key = key_at(i);
+            }
+            if (pass == 0 || (key >> above) == (T >> above)) atomicAdd(&hist[(key >> shift) & mask], 1);
+        }
+        __syncthreads();
+        // the bin that holds the left-th largest: thread tid has bins 2 tid' and
+        // 2 tid' + 1 from the top
+        const int top = kBins - 1 - 2 * tid;
+        const int c0 = hist[top], c1 = hist[top - 1];
+        const int incl = warp_incl(c0 + c1, lane);
+        if (lane == 31) warp_a[warp] = incl;
+        __syncthreads();
+        int before = incl - c0 - c1;
+        for (int v = 0; v < warp; ++v) before += warp_a[v];
+        if (before < left && left <= before + c0 + c1) {
+            const bool first = left <= before + c0;
+            sel[0] = first ? top : top - 1;
+            sel[1] = first ? before : before + c0;
+        }
+        __syncthreads();
+        T |= static_cast<uint32_t>(sel[0]) << shift;
+        left -= sel[1];  // (the next pass's first barrier comes before sel is written again)
+    }
+
+    // Warp v takes positions [v * run, (v + 1) * run): how many are above T, how
+    // many equal; then where each kept one goes.  `left` of the equal ones stay,
+    // those of the lowest positions.
+    const int run = ((cand + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int i0 = warp * run, i1 = min(cand, i0 + run);
+    int gt = 0, eq = 0;
+    for (int i = i0 + lane; i < i0 + run && __any_sync(0xffffffffu, i < i1); i += 32) {
+        const uint32_t key = i < i1 ? key_at(i) : 0u;
+        gt += __popc(__ballot_sync(0xffffffffu, i < i1 && key > T));
+        eq += __popc(__ballot_sync(0xffffffffu, i < i1 && key == T));
+    }
+    if (lane == 0) {
+        warp_a[warp] = gt;
+        warp_b[warp] = eq;
+    }
+    __syncthreads();
+    gt = eq = 0;
+    for (int v = 0; v < warp; ++v) {
+        gt += warp_a[v];
+        eq += warp_b[v];
+    }
+    const uint32_t lower = (1u << lane) - 1;
+    for (int i = i0 + lane; i < i0 + run && __any_sync(0xffffffffu, i < i1); i += 32) {
+        const uint32_t key = i < i1 ? key_at(i) : 0u;
+        const uint32_t g = __ballot_sync(0xffffffffu, i < i1 && key > T);
+        const uint32_t e = __ballot_sync(0xffffffffu, i < i1 && key == T);
+        const int eqb = eq + __popc(e & lower);
+        if (((g >> lane) & 1u) || (((e >> lane) & 1u) && eqb < left)) {
+            const int dst = gt + __popc(g & lower) + min(eqb, left);
+            kept[dst] = i;
+            w_out[dst] = w[i];
+        }
+        gt += __popc(g);
+        eq += __popc(e);
+    }
 }
 
 struct CopyParams {
     uint8_t* buf[4];
-    int row_bytes[4];
-    int nbuf;
     const int32_t* bt;
     const int32_t* dst_bt;
     const int32_t* kept;
     uint32_t* flag;
-    long long rows;  // B * H_kv * keep
-    int H_kv, keep, ps, max_npg, dst_max_npg, num_pages;
+    int H_kv, keep, ps, max_npg, dst_max_npg, num_pages, ntile;
 };
 
-// One warp per kept row.
+// A block moves ROWS kept rows of one (sequence, kv head): first their source
+// and destination rows, then 16 bytes a thread and copy, four in flight.  RB:
+// bytes of a K or V row; SB: bytes of its scales (4-bit pages), else 0.
+template <int ROWS, int RB, int SB>
 __global__ void __launch_bounds__(256) evict_copy_kernel(const CopyParams p) {
-    const int lane = threadIdx.x & 31;
-    for (long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < p.rows;
-         row += static_cast<long long>(gridDim.x) * 8) {
-        const int s = p.kept[row];
-        if (s < 0) continue;
-        const long long bk = row / p.keep;
-        const int j = static_cast<int>(row - bk * p.keep);
-        const int b = static_cast<int>(bk / p.H_kv);
-        const int kvh = static_cast<int>(bk - static_cast<long long>(b) * p.H_kv);
-        const int from = __ldg(p.bt + static_cast<long long>(b) * p.max_npg + s / p.ps);
-        const int to = __ldg(p.dst_bt + static_cast<long long>(b) * p.dst_max_npg + j / p.ps);
-        if (from < 0 || from >= p.num_pages || to < 0 || to >= p.num_pages) {
-            if (lane == 0) atomicOr(p.flag, PA_FLAG_BAD_PAGE);
-            continue;
+    __shared__ int src_s[ROWS], dst_s[ROWS];
+    const int tile = static_cast<int>(blockIdx.x) % p.ntile, bk = static_cast<int>(blockIdx.x) / p.ntile;
+    const int b = bk / p.H_kv, kvh = bk - b * p.H_kv;
+    const int j0 = tile * ROWS;
+    for (int i = threadIdx.x; i < ROWS; i += 256) {
+        const int j = j0 + i;
+        const int s = j < p.keep ? __ldg(p.kept + static_cast<long long>(bk) * p.keep + j) : -1;
+        int src = -1, dst = -1;
+        if (s >= 0) {
+            const int from = __ldg(p.bt + static_cast<long long>(b) * p.max_npg + s / p.ps);
+            const int to = __ldg(p.dst_bt + static_cast<long long>(b) * p.dst_max_npg + j / p.ps);
+            if (from >= 0 && from < p.num_pages && to >= 0 && to < p.num_pages) {
+                src = (from * p.H_kv + kvh) * p.ps + s % p.ps;
+                dst = (to * p.H_kv + kvh) * p.ps + j % p.ps;
+            } else {
+                atomicOr(p.flag, PA_FLAG_BAD_PAGE);
+            }
         }
-        const long long src = (static_cast<long long>(from) * p.H_kv + kvh) * p.ps + s % p.ps;
-        const long long dst = (static_cast<long long>(to) * p.H_kv + kvh) * p.ps + j % p.ps;
-        for (int k = 0; k < p.nbuf; ++k)
-            for (int o = 8 * lane; o < p.row_bytes[k]; o += 256)
-                *reinterpret_cast<uint2*>(p.buf[k] + dst * p.row_bytes[k] + o) =
-                    *reinterpret_cast<const uint2*>(p.buf[k] + src * p.row_bytes[k] + o);
+        src_s[i] = src;
+        dst_s[i] = dst;
     }
+    __syncthreads();
+    constexpr int LPR = RB / 16, PER = ROWS * LPR / 256;  // copies per thread and buffer
+    static_assert(ROWS * LPR % 256 == 0, "whole passes");
+    uint4 v[2][PER];
+    const int c = threadIdx.x % LPR;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int src = src_s[(threadIdx.x + 256 * i) / LPR];
+            if (src >= 0)
+                v[k][i] = __ldcs(reinterpret_cast<const uint4*>(p.buf[k] + static_cast<long long>(src) * RB) + c);
+        }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int dst = dst_s[(threadIdx.x + 256 * i) / LPR];
+            if (dst >= 0) reinterpret_cast<uint4*>(p.buf[k] + static_cast<long long>(dst) * RB)[c] = v[k][i];
+        }
+    if constexpr (SB > 0) {
+        static_assert(SB == 8 && ROWS == 128, "one 8-byte copy per thread: K scales, then V scales");
+        const int i = threadIdx.x & 127, src = src_s[i];
+        uint8_t* const buf = threadIdx.x < 128 ? p.buf[2] : p.buf[3];
+        if (src >= 0)
+            *reinterpret_cast<uint2*>(buf + static_cast<long long>(dst_s[i]) * SB) =
+                *reinterpret_cast<const uint2*>(buf + static_cast<long long>(src) * SB);
+    }
+}
+
+template <int ROWS, int RB, int SB>
+pa_status launch_copy(CopyParams& q, long long bk, cudaStream_t stream) {
+    q.ntile = (q.keep + ROWS - 1) / ROWS;
+    if (bk * q.ntile > INT_MAX) return PA_ERR_UNSUPPORTED;
+    evict_copy_kernel<ROWS, RB, SB><<<static_cast<unsigned>(bk * q.ntile), 256, 0, stream>>>(q);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
 
 pa_status evict_launch(const EvictCall& c) {
     const pa_shape& sh = c.sh;
-    if (static_cast<long long>(sh.B) * sh.H_kv > INT_MAX) return PA_ERR_UNSUPPORTED;
     EvictParams p;
     p.bt = c.bt;
     p.ctx = c.ctx;
@@ -182,28 +256,36 @@ pa_status evict_launch(const EvictCall& c) {
     p.flag = c.flag;
     p.H_kv = sh.H_kv;
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
-    evict_select_kernel<<<static_cast<unsigned>(sh.B * sh.H_kv), kThreads, 0, c.stream>>>(p);
+    const long long bk = static_cast<long long>(sh.B) * sh.H_kv;
+    if (bk * ((c.keep + 15ll) / 16) > INT_MAX) return PA_ERR_UNSUPPORTED;
+    if (p.max_S <= kCached) {
+        static int attr_done[64] = {0};
+        if (!attr_done[c.dev.device]) {
+            if (cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kCached * 4) != cudaSuccess)
+                return PA_ERR_CUDA;
+            attr_done[c.dev.device] = 1;
+        }
+        evict_select_kernel<true><<<static_cast<unsigned>(bk), kThreads, static_cast<size_t>(p.max_S) * 4, c.stream>>>(p);
+    } else {
+        evict_select_kernel<false><<<static_cast<unsigned>(bk), kThreads, 0, c.stream>>>(p);
+    }
     if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     CopyParams q;
-    for (int k = 0; k < 4; ++k) {
-        q.buf[k] = static_cast<uint8_t*>(c.buf[k]);
-        q.row_bytes[k] = c.row_bytes[k];
-    }
-    q.nbuf = c.nbuf;
+    for (int k = 0; k < 4; ++k) q.buf[k] = static_cast<uint8_t*>(c.buf[k]);
     q.bt = c.bt;
     q.dst_bt = c.dst_bt;
     q.kept = c.kept;
     q.flag = c.flag;
-    q.rows = static_cast<long long>(sh.B) * sh.H_kv * c.keep;
     q.H_kv = sh.H_kv;
     q.keep = c.keep;
     q.ps = sh.page_size;
     q.max_npg = sh.max_pages_per_seq;
     q.dst_max_npg = c.dst_max_pages;
     q.num_pages = sh.num_pages;
-    const long long blocks = (q.rows + 7) / 8, cap = 8ll * c.dev.sm_count;
-    evict_copy_kernel<<<static_cast<unsigned>(blocks < cap ? blocks : cap), 256, 0, c.stream>>>(q);
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    if (c.buf[2]) return launch_copy<128, kQ4CodeBytes, kQ4Groups>(q, bk, c.stream);
+    return sh.dtype == PA_BF16 ? launch_copy<32, 2 * kHeadDim, 0>(q, bk, c.stream)
+                               : launch_copy<16, 4 * kHeadDim, 0>(q, bk, c.stream);
 }
 
 }  // namespace pa

@@ -28,7 +28,7 @@ struct Q4AppendParams {
     const int32_t* bt;
     const int32_t* ctx;
     uint32_t* flag;
-    long long units;  // rows * 2 (K, V) * 8 groups
+    int rows;  // B * H_kv * L new rows (host-checked: 8 threads a row fit an int)
     int H_kv, L, ps, max_npg, num_pages;
     long long max_S;
 };
@@ -56,68 +56,92 @@ __device__ __forceinline__ uint32_t float_to_e2m1x2(float lo, float hi) {
     return r;
 }
 
-// One thread per group of 16 dims.
+// 16 consecutive values of a row.
+template <typename T>
+__device__ __forceinline__ void load16(const T* src, float (&x)[16]) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = bf16x2_to_float2(ww[j]);
+                x[8 * i + 2 * j] = f.x;
+                x[8 * i + 2 * j + 1] = f.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 f = __ldcs(reinterpret_cast<const float4*>(src) + i);
+            x[4 * i] = f.x;
+            x[4 * i + 1] = f.y;
+            x[4 * i + 2] = f.z;
+            x[4 * i + 3] = f.w;
+        }
+    }
+}
+
+// The scale byte and the codes of 16 values.  x / s is rounded correctly by
+// Markstein's correction: with r the correctly rounded 1 / s and q0 = x r, the
+// remainder x - q0 s is exact in one FMA and q0 + r (x - q0 s) rounds to the
+// quotient.  |x| is cut to 8 s first (its code stays 6), so nothing overflows.
+__device__ __forceinline__ uint2 encode16(const float (&x)[16], uint32_t& sb) {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
+    sb = float_to_e4m3(max_nan(__fdiv_rn(amax, 6.f), 0.001953125f));
+    const float sc = f16x2_to_float2(e4m3x2_to_f16x2(sb)).x;
+    const float r = __frcp_rn(sc), cut = 8.f * sc;
+    uint32_t code[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float y[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float c = fminf(fmaxf(x[2 * i + e], -cut), cut);
+            const float q0 = c * r;
+            y[e] = copysignf(fmaf(fmaf(-q0, sc, c), r, q0), c);  // (-0 stays -0)
+        }
+        code[i >> 2] |= float_to_e2m1x2(y[0], y[1]) << (8 * (i & 3));
+    }
+    return make_uint2(code[0], code[1]);
+}
+
+// Eight threads a row, 16 dims each, its key and its value.  Bound by the rows
+// read: 512 bytes in (bf16) for 144 out.
 template <typename T>
 __global__ void __launch_bounds__(256) q4_append_kernel(const Q4AppendParams p) {
-    for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < p.units;
-         u += static_cast<long long>(gridDim.x) * blockDim.x) {
-        const int grp = static_cast<int>(u & 7);
-        const int isv = static_cast<int>((u >> 3) & 1);
-        const long long row = u >> 4;
-        const long long bk = row / p.L;
-        const int t = static_cast<int>(row - bk * p.L);
-        const int b = static_cast<int>(bk / p.H_kv);
-        const int kvh = static_cast<int>(bk - static_cast<long long>(b) * p.H_kv);
-        const int S = __ldg(p.ctx + b);
-        if (S < p.L || static_cast<long long>(S) > p.max_S) {
-            if (kvh == 0 && t == 0 && (u & 15) == 0) atomicOr(p.flag, PA_FLAG_BAD_CONTEXT);
-            continue;
-        }
-        const int s = S - p.L + t;
-        const int lp = s / p.ps, slot = s - lp * p.ps;
-        const int pp = __ldg(p.bt + static_cast<long long>(b) * p.max_npg + lp);
-        if (pp < 0 || pp >= p.num_pages) {
-            if ((u & 15) == 0) atomicOr(p.flag, PA_FLAG_BAD_PAGE);
-            continue;
-        }
-        const T* const src = static_cast<const T*>(isv ? p.v_new : p.k_new) + row * kHeadDim + grp * 16;
-        float x[16];
-        if constexpr (sizeof(T) == 2) {
+    const int u = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x);
+    const int row = u >> 3, grp = u & 7;
+    if (row >= p.rows) return;
+    const int bk = row / p.L, t = row - bk * p.L;
+    const int b = bk / p.H_kv, kvh = bk - b * p.H_kv;
+    const int S = __ldg(p.ctx + b);
+    if (S < p.L || static_cast<long long>(S) > p.max_S) {
+        if (kvh == 0 && t == 0 && grp == 0) atomicOr(p.flag, PA_FLAG_BAD_CONTEXT);
+        return;
+    }
+    const int s = S - p.L + t;
+    const int lp = s / p.ps, slot = s - lp * p.ps;
+    const int pp = __ldg(p.bt + static_cast<long long>(b) * p.max_npg + lp);
+    const long long src = static_cast<long long>(row) * kHeadDim + grp * 16;
+    float x[2][16];
+    load16(static_cast<const T*>(p.k_new) + src, x[0]);
+    load16(static_cast<const T*>(p.v_new) + src, x[1]);
+    if (pp < 0 || pp >= p.num_pages) {
+        if (grp == 0) atomicOr(p.flag, PA_FLAG_BAD_PAGE);
+        return;
+    }
+    const long long dst = (static_cast<long long>(pp) * p.H_kv + kvh) * p.ps + slot;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src) + i);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = bf16x2_to_float2(ww[j]);
-                    x[8 * i + 2 * j] = f.x;
-                    x[8 * i + 2 * j + 1] = f.y;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 f = __ldcs(reinterpret_cast<const float4*>(src) + i);
-                x[4 * i] = f.x;
-                x[4 * i + 1] = f.y;
-                x[4 * i + 2] = f.z;
-                x[4 * i + 3] = f.w;
-            }
-        }
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
-        const uint32_t sb = float_to_e4m3(max_nan(__fdiv_rn(amax, 6.f), 0.001953125f));
-        const float sc = f16x2_to_float2(e4m3x2_to_f16x2(sb)).x;
-        uint32_t code[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            code[i >> 2] |= float_to_e2m1x2(__fdiv_rn(x[2 * i], sc), __fdiv_rn(x[2 * i + 1], sc))
-                            << (8 * (i & 3));
-        const long long dst = (static_cast<long long>(pp) * p.H_kv + kvh) * p.ps + slot;
-        uint8_t* const codes = static_cast<uint8_t*>(isv ? p.pool.value_codes : p.pool.key_codes);
-        uint8_t* const scales = static_cast<uint8_t*>(isv ? p.pool.value_scales : p.pool.key_scales);
-        *reinterpret_cast<uint2*>(codes + dst * kQ4CodeBytes + grp * 8) = make_uint2(code[0], code[1]);
+    for (int kv = 0; kv < 2; ++kv) {
+        uint32_t sb;
+        const uint2 code = encode16(x[kv], sb);
+        uint8_t* const codes = static_cast<uint8_t*>(kv ? p.pool.value_codes : p.pool.key_codes);
+        uint8_t* const scales = static_cast<uint8_t*>(kv ? p.pool.value_scales : p.pool.key_scales);
+        *reinterpret_cast<uint2*>(codes + dst * kQ4CodeBytes + grp * 8) = code;
         scales[dst * kQ4Groups + grp] = static_cast<uint8_t>(sb);
     }
 }
@@ -218,17 +242,11 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherParams p) 
     }
 }
 
-// Blocks of 256 threads that cover `units` once, at most 8 per SM.
-unsigned grid_for(long long units, int sm_count) {
-    const long long blocks = (units + 255) / 256, cap = 8ll * (sm_count > 0 ? sm_count : 1);
-    return static_cast<unsigned>(blocks < cap ? blocks : cap);
-}
-
 }  // namespace
 
 pa_status q4_append_launch(const pa_shape& sh, const void* k_new, const void* v_new,
                            const pa_q4_pool& pool, const int32_t* bt, const int32_t* ctx,
-                           uint32_t* flag, int sm_count, cudaStream_t stream) {
+                           uint32_t* flag, cudaStream_t stream) {
     Q4AppendParams p;
     p.k_new = k_new;
     p.v_new = v_new;
@@ -236,14 +254,16 @@ pa_status q4_append_launch(const pa_shape& sh, const void* k_new, const void* v_
     p.bt = bt;
     p.ctx = ctx;
     p.flag = flag;
-    p.units = static_cast<long long>(sh.B) * sh.H_kv * sh.L * 2 * kQ4Groups;
+    const long long rows = static_cast<long long>(sh.B) * sh.H_kv * sh.L;
+    if (rows * 8 > INT_MAX - 256) return PA_ERR_UNSUPPORTED;
+    p.rows = static_cast<int>(rows);
     p.H_kv = sh.H_kv;
     p.L = sh.L;
     p.ps = sh.page_size;
     p.max_npg = sh.max_pages_per_seq;
     p.num_pages = sh.num_pages;
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
-    const unsigned grid = grid_for(p.units, sm_count);
+    const unsigned grid = static_cast<unsigned>((rows * 8 + 255) / 256);
     if (sh.dtype == PA_BF16)
         q4_append_kernel<uint16_t><<<grid, 256, 0, stream>>>(p);
     else

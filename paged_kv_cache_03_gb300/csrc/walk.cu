@@ -135,6 +135,101 @@ struct StepWalker {
     }
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
+// ---- a warp's step of keys and values in shared memory ----------------------
+// Filled by asynchronous copies, whole lines a warp; the values' rows are placed
+// so that the fragment loads below meet no bank conflict.
+template <bool Q4>
+struct Stage;
+
+template <>
+struct Stage<true> {  // 32 keys: K codes, V codes, K scales, V scales
+    static constexpr int kV = 2048, kKS = 4096, kVS = 4352, kBytes = 4608;
+    // byte of 16-byte chunk c of value i (0 .. 15) of half u
+    __device__ static uint32_t v_at(int u, int i, int c) {
+        const int slot = (i >> 1) | ((i & 1) << 3);
+        return kV + (16 * u + slot) * 64 + ((c ^ (slot & 2)) << 4);
+    }
+    template <bool A16>
+    __device__ static void fill(const WalkParams& p, const StepRows<A16, 2>& rows, uint32_t st, int lane) {
+        const uint8_t* const kc = static_cast<const uint8_t*>(p.kc);
+        const uint8_t* const vc = static_cast<const uint8_t*>(p.vc);
+        const uint8_t* const ks = static_cast<const uint8_t*>(p.ks);
+        const uint8_t* const vs = static_cast<const uint8_t*>(p.vs);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int u = j >> 1, i = (lane >> 2) + 8 * (j & 1), c = lane & 3;
+            const int row = rows.row(u, i);
+            const bool ok = A16 ? rows.any(u) : row >= 0;
+            const long long off = ok ? static_cast<long long>(row) * kQ4CodeBytes + 16 * c : 0;
+            cp_async16(st + 16 * (lane + 32 * j), kc + off, ok);
+            cp_async16(st + v_at(u, i, c), vc + off, ok);
+        }
+        if constexpr (A16) {  // two keys a chunk: lanes 0 - 15 K, 16 - 31 V
+            const int i = lane & 15, r = i < 8 ? rows.r[0] : rows.r[1];
+            const long long off = r >= 0 ? static_cast<long long>(r + 2 * (i & 7)) * kQ4Groups : 0;
+            cp_async16(st + kKS + 16 * lane, (lane < 16 ? ks : vs) + off, r >= 0);
+        } else {
+            const int r = rows.r[0];
+            const long long off = r >= 0 ? static_cast<long long>(r) * kQ4Groups : 0;
+            cp_async8(st + kKS + 8 * lane, ks + off, r >= 0);
+            cp_async8(st + kVS + 8 * lane, vs + off, r >= 0);
+        }
+    }
+};
+
+template <>
+struct Stage<false> {  // 16 keys: K rows, V rows
+    static constexpr int kV = 4096, kBytes = 8192;
+    __device__ static uint32_t k_at(int i, int c) { return i * 256 + ((c ^ ((i & 1) << 2)) << 4); }
+    __device__ static uint32_t v_at(int i, int c) {
+        return kV + i * 256 + ((c ^ (((i >> 1) & 1) | ((i >> 2 & 1) << 2))) << 4);
+    }
+    template <bool A16>
+    __device__ static void fill(const WalkParams& p, const StepRows<A16, 1>& rows, uint32_t st, int lane) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = (lane >> 4) + 2 * j, c = lane & 15;
+            const int row = rows.row(0, i);
+            const bool ok = A16 ? rows.any(0) : row >= 0;
+            const long long off = ok ? static_cast<long long>(row) * (2 * kD) + 16 * c : 0;
+            cp_async16(st + k_at(i, c), static_cast<const uint8_t*>(p.kc) + off, ok);
+            cp_async16(st + v_at(i, c), static_cast<const uint8_t*>(p.vc) + off, ok);
+        }
+    }
+};
+
 // ---- 16 keys of 4-bit pages as A fragments --------------------------------
 struct Q4Keys {
     static constexpr bool kF16 = true;
@@ -157,6 +252,17 @@ struct Q4Keys {
             w[e][1] = x.y;
             w[e][2] = x.z;
             w[e][3] = x.w;
+        }
+    }
+    __device__ __forceinline__ void load(uint32_t st, int u, int g, int t) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint4 x = lds128(st + (16 * u + g + 8 * e) * 64 + t * 16);
+            w[e][0] = x.x;
+            w[e][1] = x.y;
+            w[e][2] = x.z;
+            w[e][3] = x.w;
+            s[e] = lds16(st + Stage<true>::kKS + (16 * u + g + 8 * e) * 8 + 2 * t);
         }
     }
     // the scales of dims 32t .., 32t + 16 .. of both keys, ready for frags()
@@ -191,19 +297,14 @@ struct Q4Keys {
 struct Q4Values {
     uint32_t w[4][2], s[4];
     // keys 2t, 2t + 1, 2t + 8, 2t + 9
-    template <bool A16, int U>
-    __device__ __forceinline__ void load(const WalkParams& p, const StepRows<A16, U>& rows, int u, int g, int t) {
+    __device__ __forceinline__ void load(uint32_t st, int u, int g, int t) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const long long r = rows.row(u, 2 * t + (e & 1) + 8 * (e >> 1));
-            uint2 x = make_uint2(0u, 0u);
-            s[e] = 0u;
-            if (A16 ? rows.any(u) : r >= 0) {
-                x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.vc) + r * kQ4CodeBytes) + g);
-                s[e] = __ldg(static_cast<const uint8_t*>(p.vs) + r * kQ4Groups + g);
-            }
+            const int i = 2 * t + (e & 1) + 8 * (e >> 1);
+            const uint2 x = lds64(st + Stage<true>::v_at(u, i, g >> 1) + 8 * (g & 1));
             w[e][0] = x.x;
             w[e][1] = x.y;
+            s[e] = lds8(st + Stage<true>::kVS + (16 * u + i) * 8 + g);
         }
     }
     // keys of the half from number n on read as zeros
@@ -264,6 +365,12 @@ struct BfKeys {
             }
         }
     }
+    __device__ __forceinline__ void load(uint32_t st, int, int g, int t) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[e][i] = lds128(st + Stage<false>::k_at(g + 8 * e, 4 * i + t));
+    }
     struct Scales {};
     __device__ __forceinline__ Scales scales() const { return Scales(); }
     __device__ __forceinline__ void frags(const Scales&, int i, uint32_t (&a)[2][4]) const {
@@ -280,25 +387,17 @@ struct BfKeys {
 
 struct BfValues {
     uint32_t w[4][8];
-    template <bool A16, int U>
-    __device__ __forceinline__ void load(const WalkParams& p, const StepRows<A16, U>& rows, int u, int g, int t) {
+    __device__ __forceinline__ void load(uint32_t st, int, int g, int t) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const long long r = rows.row(u, 2 * t + (e & 1) + 8 * (e >> 1));
-            uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-            if (A16 ? rows.any(u) : r >= 0) {
-                const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.vc) + r * (2 * kD)) + 2 * g;
-                x[0] = __ldg(src);
-                x[1] = __ldg(src + 1);
-            }
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                w[e][4 * i] = x[i].x;
-                w[e][4 * i + 1] = x[i].y;
-                w[e][4 * i + 2] = x[i].z;
-                w[e][4 * i + 3] = x[i].w;
+                const uint4 x = lds128(st + Stage<false>::v_at(2 * t + (e & 1) + 8 * (e >> 1), 2 * g + i));
+                w[e][4 * i] = x.x;
+                w[e][4 * i + 1] = x.y;
+                w[e][4 * i + 2] = x.z;
+                w[e][4 * i + 3] = x.w;
             }
-        }
     }
     __device__ __forceinline__ void cut(int n, int t) {
 #pragma unroll
@@ -396,7 +495,8 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
     constexpr bool F16 = Keys::kF16;
     constexpr int ROWS = 8 * NT;
     constexpr int U = Keys::kU, kStep = 16 * U;
-    extern __shared__ float merge[];  // [warp][row][kMerge]: o, m, applied sum, sum
+    extern __shared__ __align__(1024) uint8_t smem[];         // the warps' stages, then
+    float* const merge = reinterpret_cast<float*>(smem);  // [warp][row][kMerge]: o, m, applied sum, sum
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     int item = static_cast<int>(blockIdx.x);
@@ -453,35 +553,37 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
         for (int i = 0; i < 8; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
     }
 
-    // The values of a step are requested when it begins and the keys of the next
-    // one with them, so a step's S = K Q^T hides both.
+    // Each warp has two stages of its own: the next step is requested when a
+    // step begins.
+    using St = Stage<F16>;
+    const uint32_t ring = smem_u32(smem) + warp * 2 * St::kBytes;
     const int npg = (S + p.ps - 1) / p.ps;
     StepWalker<A16, U> wk;
     const int first = k0 + warp * kStep;
     wk.start(p, A16 ? first : first + lane, kWarps * kStep);
-    StepRows<A16, U> rows = {};
     int pg[2] = {-1, -1};
-    Keys kk[U];
     if (first < k1) {
         wk.pages(p, b, npg, pg);
-        rows = wk.rows(p, kvh, pg);
-#pragma unroll
-        for (int u = 0; u < U; ++u) kk[u].load(p, rows, u, g, t);
+        St::fill(p, wk.rows(p, kvh, pg), ring, lane);
         wk.next(p);
         if (first + kWarps * kStep < k1) wk.pages(p, b, npg, pg);
     }
+    cp_async_commit();
+    uint32_t st = ring;
     for (int base = first; base < k1; base += kWarps * kStep) {
-        Values vv[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) vv[u].load(p, rows, u, g, t);
-        Keys kn[U];
+        __syncwarp();  // the other stage has been read
+        const uint32_t st_next = st == ring ? ring + St::kBytes : ring;
         if (base + kWarps * kStep < k1) {
-            rows = wk.rows(p, kvh, pg);
-#pragma unroll
-            for (int u = 0; u < U; ++u) kn[u].load(p, rows, u, g, t);
+            St::fill(p, wk.rows(p, kvh, pg), st_next, lane);
             wk.next(p);
             if (base + 2 * kWarps * kStep < k1) wk.pages(p, b, npg, pg);
         }
+        cp_async_commit();
+        cp_async_wait<1>();
+        __syncwarp();
+        Keys kk[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) kk[u].load(st, u, g, t);
         // S^T: 16 U keys x 8 NT rows
         float s[NT][U][4];
 #pragma unroll
@@ -588,6 +690,9 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
                     }
                 }
         }
+        Values vv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) vv[u].load(st, u, g, t);
         if (base + kStep > S) {  // slots past the context may hold anything
 #pragma unroll
             for (int u = 0; u < U; ++u) vv[u].cut(S - base - 16 * u, t);
@@ -609,9 +714,10 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
                     }
             }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) kk[u] = kn[u];
+        st = st_next;
     }
+    cp_async_wait<0>();
+    __syncthreads();  // the stages become the merge buffer
 
     // ---- merge the four warps ---------------------------------------------
     float* const mw = merge + warp * ROWS * kMerge;
@@ -725,10 +831,6 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
     return static_cast<uint32_t>(row * 256 + (c & 1) * 128 + (((c >> 1) ^ (row & 7)) << 4));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-
 template <bool Q4>
 struct TileLoader;
 
@@ -791,9 +893,9 @@ struct TileLoader<false> {  // thread: chunk tid & 15 of keys (tid >> 4) + 8 i
             cp_async16(kbuf + chunk_at(row, c), static_cast<const uint8_t*>(p.kc) + r * (2 * kD) + 16 * c, pg >= 0);
             cp_async16(vbuf + chunk_at(row, c), static_cast<const uint8_t*>(p.vc) + r * (2 * kD) + 16 * c, pg >= 0);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        cp_async_commit();
     }
-    __device__ __forceinline__ void finish(uint32_t, uint32_t) { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+    __device__ __forceinline__ void finish(uint32_t, uint32_t) { cp_async_wait<0>(); }
 };
 
 // Dim pairs of Q's A fragments: the natural order (K's tile is in it).
@@ -1209,22 +1311,31 @@ bool launch_dependent(void (*kernel)(P...), long long grid, int threads, cudaStr
 
 // The attention, its merge over key chunks, then the key weights.
 template <class Keys, class Values, int NT, bool F32, bool A16, bool W>
-pa_status launch_walk(const WalkParams& p, long long items, cudaStream_t stream) {
-    constexpr size_t smem = sizeof(float) * kWarps * 8 * NT * kMerge;
-    static_assert(smem <= 48 * 1024, "merge buffer within the default limit");
+pa_status launch_walk(const WalkParams& p, long long items, [[maybe_unused]] int device, cudaStream_t stream) {
+    constexpr size_t ring = kWarps * 2 * Stage<Keys::kF16>::kBytes, merge = sizeof(float) * kWarps * 8 * NT * kMerge;
+    constexpr size_t smem = ring > merge ? ring : merge;
+    if constexpr (smem > 48 * 1024) {
+        static int attr_done[64] = {0};
+        if (!attr_done[device]) {
+            if (cudaFuncSetAttribute(walk_kernel<Keys, Values, NT, F32, A16, W>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+                return PA_ERR_CUDA;
+            attr_done[device] = 1;
+        }
+    }
     walk_kernel<Keys, Values, NT, F32, A16, W><<<static_cast<unsigned>(items), kWarps * 32, smem, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <class Keys, class Values, int NT, bool F32>
-pa_status launch_walk_for(const WalkParams& p, long long items, cudaStream_t stream) {
+pa_status launch_walk_for(const WalkParams& p, long long items, int device, cudaStream_t stream) {
     const bool a16 = p.ps % 16 == 0;
     if constexpr (NT == 1) {
-        if (p.score) return a16 ? launch_walk<Keys, Values, NT, F32, true, true>(p, items, stream)
-                                : launch_walk<Keys, Values, NT, F32, false, true>(p, items, stream);
+        if (p.score) return a16 ? launch_walk<Keys, Values, NT, F32, true, true>(p, items, device, stream)
+                                : launch_walk<Keys, Values, NT, F32, false, true>(p, items, device, stream);
     }
-    return a16 ? launch_walk<Keys, Values, NT, F32, true, false>(p, items, stream)
-               : launch_walk<Keys, Values, NT, F32, false, false>(p, items, stream);
+    return a16 ? launch_walk<Keys, Values, NT, F32, true, false>(p, items, device, stream)
+               : launch_walk<Keys, Values, NT, F32, false, false>(p, items, device, stream);
 }
 
 template <bool Q4, bool F32>
@@ -1251,13 +1362,13 @@ pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, int 
                  : f32 ? launch_block<true, true>(p, items, device, stream)
                        : launch_block<true, false>(p, items, device, stream);
     else if (!q4)
-        st = w.nt == 2 ? launch_walk_for<BfKeys, BfValues, 2, false>(p, items, stream)
-                       : launch_walk_for<BfKeys, BfValues, 1, false>(p, items, stream);
+        st = w.nt == 2 ? launch_walk_for<BfKeys, BfValues, 2, false>(p, items, device, stream)
+                       : launch_walk_for<BfKeys, BfValues, 1, false>(p, items, device, stream);
     else if (f32)
-        st = launch_walk_for<Q4Keys, Q4Values, 1, true>(p, items, stream);
+        st = launch_walk_for<Q4Keys, Q4Values, 1, true>(p, items, device, stream);
     else
-        st = w.nt == 2 ? launch_walk_for<Q4Keys, Q4Values, 2, false>(p, items, stream)
-                       : launch_walk_for<Q4Keys, Q4Values, 1, false>(p, items, stream);
+        st = w.nt == 2 ? launch_walk_for<Q4Keys, Q4Values, 2, false>(p, items, device, stream)
+                       : launch_walk_for<Q4Keys, Q4Values, 1, false>(p, items, device, stream);
     if (st != PA_OK) return st;
     if (p.nkc > 1 && !launch_dependent(f32 ? walk_combine_kernel<true> : walk_combine_kernel<false>, (rows + 3) / 4, 128, stream, p))
         return PA_ERR_CUDA;

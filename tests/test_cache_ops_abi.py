@@ -35,7 +35,7 @@ def test_q4_attention_refusals():
     assert attend(out=FAKE + 8) == bad and attend(p=None) == bad
     assert attend(p=pool(key_codes=FAKE + 8)) == bad
     assert attend(p=pool(value_codes=None)) == bad
-    assert attend(p=pool(key_scales=FAKE + 4)) == bad
+    assert attend(p=pool(key_scales=FAKE + 8)) == bad
     assert attend(scale=float("nan")) == bad and attend(scale=-1.0) == bad
     assert attend(sh=shape(H_q=5)) == bad
     assert attend(sh=shape(D=64)) == B.PA_ERR_UNSUPPORTED
