@@ -553,27 +553,39 @@ def new_cache_workspace(device=None):
     return torch.zeros(256, dtype=torch.uint8, device=device or "cuda")
 
 
-def _dtype_id(t):
+# The calls below are made per layer and token: what they check is checked with
+# few and cheap tensor queries, and torch is looked up once.
+_torch = None
+
+
+def _load_torch():
+    global _torch
     import torch
-    if t == torch.bfloat16:
+    _torch = torch
+    return torch
+
+
+def _dtype_id(t):
+    torch = _torch or _load_torch()
+    if t is torch.bfloat16:
         return PA_BF16
-    if t == torch.float32:
+    if t is torch.float32:
         return PA_F32
     raise ValueError(f"unsupported dtype {t}")
 
 
-def _on_device(device, **tensors):
-    """Every named tensor (None allowed) is contiguous on the CUDA device."""
-    for name, t in tensors.items():
-        if t is not None and not (t.is_cuda and t.device == device and t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
+def _on_device(index, *named):
+    """Every (name, tensor) is contiguous on CUDA device `index`."""
+    for name, t in named:
+        if t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor on cuda:{index}")
 
 
 def _table(block_table, context_lens, B):
-    import torch
-    if block_table.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    int32 = (_torch or _load_torch()).int32
+    if block_table.dtype is not int32 or context_lens.dtype is not int32:
         raise ValueError("block tables and context lengths must be int32")
-    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(context_lens.shape) != (B,):
+    if block_table.dim() != 2 or block_table.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_table must be [B, max_pages_per_seq] and context_lens [B]")
 
 
@@ -582,18 +594,28 @@ def _pages_dims(key_pages, value_pages):
     if key_pages.dim() != 4 or key_pages.shape != value_pages.shape or \
             key_pages.dtype != value_pages.dtype:
         raise ValueError("key and value pages must be alike, [num_pages, H_kv, page_size, D]")
-    _on_device(key_pages.device, key_pages=key_pages, value_pages=value_pages)
+    index = key_pages.get_device()
+    if index < 0:
+        raise ValueError("key_pages must be on a CUDA device")
+    _on_device(index, ("key_pages", key_pages), ("value_pages", value_pages))
     return key_pages.shape[:3]
 
 
-def _call(name, device, fn):
-    """Runs fn(stream) with `device` current, on its current stream."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        st = fn(torch._C._cuda_getCurrentRawStream(device.index))
+def _weights_shape(name, w, B_, H_kv, capacity):
+    torch = _torch or _load_torch()
+    if w.dtype is not torch.float32 or w.dim() != 3 or w.shape[:2] != (B_, H_kv) or \
+            w.shape[2] < capacity:
+        raise ValueError(f"{name} must be fp32 [B, H_kv, S] with S >= {capacity}")
+
+
+def _launch(name, index, fn, *args):
+    """fn(*args, stream) with device `index` current, on its current stream."""
+    torch = _torch or _load_torch()
+    if torch.cuda.current_device() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(torch._C._cuda_getCurrentRawStream(device.index))
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != PA_OK:
         raise PagedAttentionError(st, name)
 
@@ -624,15 +646,17 @@ def append_kv_q4(k_new, v_new, pool, block_table, context_lens, *, workspace=Non
         raise ValueError("k_new/v_new must be alike, [B, H_kv, L, 128] matching the pool")
     B_, _, L, D = k_new.shape
     _table(block_table, context_lens, B_)
-    device = pool.device
     k_new, v_new = k_new.contiguous(), v_new.contiguous()
     if workspace is None:
-        workspace = new_cache_workspace(device)
-    _on_device(device, k_new=k_new, v_new=v_new, block_table=block_table,
-               context_lens=context_lens, workspace=workspace)
-    shape = make_shape(B_, H_kv, H_kv, L, D, P, ps, block_table.shape[1], _dtype_id(k_new.dtype))
-    _call("pa_append_kv_q4", device, lambda s: pa_append_kv_q4(
-        shape, k_new, v_new, pool, block_table, context_lens, workspace, workspace.numel(), s))
+        workspace = new_cache_workspace(pool.device)
+    index = pool.device.index
+    _on_device(index, ("k_new", k_new), ("v_new", v_new), ("block_table", block_table),
+               ("context_lens", context_lens), ("workspace", workspace))
+    shape = pa_shape(B_, H_kv, H_kv, L, D, P, ps, block_table.shape[1], _dtype_id(k_new.dtype))
+    _launch("pa_append_kv_q4", index, load().pa_append_kv_q4, ctypes.byref(shape),
+            k_new.data_ptr(), v_new.data_ptr(), ctypes.byref(pool.c_pool),
+            block_table.data_ptr(), context_lens.data_ptr(), workspace.data_ptr(),
+            workspace.numel())
     return workspace
 
 
@@ -641,28 +665,23 @@ def gather_kv_q4(pool, block_table, context_lens, n, *, tail=False, dtype=None, 
     """Dense dequantised (keys, values), each [B, H_kv, n, 128] of `dtype`
     (bf16 by default, or fp32; both exact): positions 0 .. n - 1, or with
     `tail` the last n of each context; zeros outside a context."""
-    import torch
+    torch = _torch or _load_torch()
     dtype = dtype or torch.bfloat16
     P, H_kv, ps = pool.dims
     B_ = block_table.shape[0]
     _table(block_table, context_lens, B_)
-    device = pool.device
     if workspace is None:
-        workspace = new_cache_workspace(device)
-    _on_device(device, block_table=block_table, context_lens=context_lens, workspace=workspace)
-    shape = make_shape(B_, H_kv, H_kv, 1, 128, P, ps, block_table.shape[1], _dtype_id(dtype))
-    k = torch.empty((B_, H_kv, n, 128), dtype=dtype, device=device)
+        workspace = new_cache_workspace(pool.device)
+    index = pool.device.index
+    _on_device(index, ("block_table", block_table), ("context_lens", context_lens),
+               ("workspace", workspace))
+    shape = pa_shape(B_, H_kv, H_kv, 1, 128, P, ps, block_table.shape[1], _dtype_id(dtype))
+    k = torch.empty((B_, H_kv, n, 128), dtype=dtype, device=pool.device)
     v = torch.empty_like(k)
-    _call("pa_gather_kv_q4", device, lambda s: pa_gather_kv_q4(
-        shape, pool, block_table, context_lens, n, tail, k, v, workspace, workspace.numel(), s))
+    _launch("pa_gather_kv_q4", index, load().pa_gather_kv_q4, ctypes.byref(shape),
+            ctypes.byref(pool.c_pool), block_table.data_ptr(), context_lens.data_ptr(), n,
+            bool(tail), k.data_ptr(), v.data_ptr(), workspace.data_ptr(), workspace.numel())
     return k, v
-
-
-def _weights_shape(name, w, B_, H_kv, capacity):
-    import torch
-    if w.dtype != torch.float32 or w.dim() != 3 or tuple(w.shape[:2]) != (B_, H_kv) or \
-            w.shape[2] < capacity:
-        raise ValueError(f"{name} must be fp32 [B, H_kv, S] with S >= {capacity}")
 
 
 def _q4_shape(query, pool, block_table):
@@ -670,7 +689,7 @@ def _q4_shape(query, pool, block_table):
     if query.dim() != 4 or query.shape[3] != 128:
         raise ValueError("query must be [B, H_q, L, 128]")
     B_, H_q, L, D = query.shape
-    return make_shape(B_, H_q, H_kv, L, D, P, ps, block_table.shape[1], _dtype_id(query.dtype))
+    return pa_shape(B_, H_q, H_kv, L, D, P, ps, block_table.shape[1], _dtype_id(query.dtype))
 
 
 def _zeroed(n, device, name):
@@ -699,30 +718,37 @@ def new_weights_workspace(query, key_pages, block_table):
     return _zeroed(n, query.device, "pa_weights_workspace_bytes")
 
 
-def _attend(name, fn, shape, query, block_table, context_lens, page_size, key_weights,
-            key_weights_out, out, workspace):
-    import torch
-    if shape.page_size != int(page_size):
+def _attend(name, fn, pools, shape, query, block_table, context_lens, page_size, scale, causal,
+            key_weights, key_weights_out, out, workspace):
+    if shape.page_size != page_size:
         raise ValueError("page_size disagrees with the pool's")
     _table(block_table, context_lens, shape.B)
+    index = query.get_device()
     if out is None:
-        out = torch.empty_like(query)
+        out = (_torch or _load_torch()).empty_like(query)
     elif out.shape != query.shape or out.dtype != query.dtype:
         raise ValueError("out must be like query")
-    w_S = 0
+    w_S = w_in = w_out = 0
     if key_weights_out is not None:
         _weights_shape("key_weights_out", key_weights_out, shape.B, shape.H_kv,
                        shape.max_pages_per_seq * shape.page_size)
-        w_S = key_weights_out.shape[2]
-        if key_weights is not None and (key_weights.shape != key_weights_out.shape or
-                                        key_weights.dtype != key_weights_out.dtype):
-            raise ValueError("key_weights must be like key_weights_out")
+        _on_device(index, ("key_weights_out", key_weights_out))
+        w_S, w_out = key_weights_out.shape[2], key_weights_out.data_ptr()
+        if key_weights is not None:
+            if key_weights.shape != key_weights_out.shape or \
+                    key_weights.dtype != key_weights_out.dtype:
+                raise ValueError("key_weights must be like key_weights_out")
+            _on_device(index, ("key_weights", key_weights))
+            w_in = key_weights.data_ptr()
     elif key_weights is not None:
         raise ValueError("key_weights without key_weights_out")
-    _on_device(query.device, query=query, block_table=block_table, context_lens=context_lens,
-               key_weights=key_weights, key_weights_out=key_weights_out, out=out,
-               workspace=workspace)
-    _call(name, query.device, lambda s: fn(w_S, out, s))
+    _on_device(index, ("query", query), ("block_table", block_table),
+               ("context_lens", context_lens), ("out", out), ("workspace", workspace))
+    if scale is None:
+        scale = 1.0 / math.sqrt(shape.D)
+    _launch(name, index, fn, ctypes.byref(shape), query.data_ptr(), *pools,
+            block_table.data_ptr(), context_lens.data_ptr(), scale, bool(causal), w_in, w_out,
+            w_S, out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -734,19 +760,13 @@ def paged_attention_q4(query, pool, block_table, context_lens, page_size, scale=
     also writes key_weights (zeros if None; may be key_weights_out itself)
     plus the probability each key received."""
     shape = _q4_shape(query, pool, block_table)
-    if scale is None:
-        scale = 1.0 / math.sqrt(query.shape[-1])
-    if pool.device != query.device:
-        raise ValueError(f"pool must be on {query.device}")
+    if query.get_device() != pool.device.index:
+        raise ValueError(f"query must be on {pool.device}")
     if workspace is None:
         workspace = new_q4_workspace(query, pool, block_table, key_weights_out is not None)
-    return _attend(
-        "pa_paged_attention_q4",
-        lambda w_S, o, s: pa_paged_attention_q4(
-            shape, query, pool, block_table, context_lens, scale, causal, key_weights,
-            key_weights_out, w_S, o, workspace, workspace.numel(), s),
-        shape, query, block_table, context_lens, page_size, key_weights, key_weights_out, out,
-        workspace)
+    return _attend("pa_paged_attention_q4", load().pa_paged_attention_q4,
+                   (ctypes.byref(pool.c_pool),), shape, query, block_table, context_lens,
+                   page_size, scale, causal, key_weights, key_weights_out, out, workspace)
 
 
 @_streamed
@@ -756,28 +776,28 @@ def paged_attention_weights(query, key_pages, value_pages, block_table, context_
     """paged_attention over bf16 pages that also writes key_weights_out (fp32
     [B, H_kv, S], S >= the table's capacity): key_weights (zeros if None; may
     be key_weights_out itself) plus the probability each key received."""
-    _pages_dims(key_pages, value_pages)
-    shape = shape_of(query, key_pages, block_table)
-    if scale is None:
-        scale = 1.0 / math.sqrt(query.shape[-1])
-    if key_pages.device != query.device:
-        raise ValueError(f"pages must be on {query.device}")
+    P, H_kv, ps = _pages_dims(key_pages, value_pages)
+    if query.dim() != 4 or query.dtype != key_pages.dtype or query.shape[3] != key_pages.shape[3]:
+        raise ValueError("query must be [B, H_q, L, D] of the pages' dtype and head dim")
+    B_, H_q, L, D = query.shape
+    shape = pa_shape(B_, H_q, H_kv, L, D, P, ps, block_table.shape[1], _dtype_id(query.dtype))
+    if shape.dtype != PA_BF16:
+        raise PagedAttentionError(PA_ERR_UNSUPPORTED, "pa_paged_attention_weights")
+    if query.get_device() != key_pages.get_device():
+        raise ValueError(f"query must be on {key_pages.device}")
     if key_weights_out is None:
         raise ValueError("key_weights_out is what this call is for: use paged_attention")
     if workspace is None:
         workspace = new_weights_workspace(query, key_pages, block_table)
-    return _attend(
-        "pa_paged_attention_weights",
-        lambda w_S, o, s: pa_paged_attention_weights(
-            shape, query, key_pages, value_pages, block_table, context_lens, scale, causal,
-            key_weights, key_weights_out, w_S, o, workspace, workspace.numel(), s),
-        shape, query, block_table, context_lens, page_size, key_weights, key_weights_out, out,
-        workspace)
+    return _attend("pa_paged_attention_weights", load().pa_paged_attention_weights,
+                   (key_pages.data_ptr(), value_pages.data_ptr()), shape, query, block_table,
+                   context_lens, page_size, scale, causal, key_weights, key_weights_out, out,
+                   workspace)
 
 
-def _evict(name, fn, dims, dtype_id, device, block_table, context_lens, key_weights, keep,
-           dst_block_table, workspace):
-    import torch
+def _evict(name, fn, pools, dims, dtype_id, device, block_table, context_lens, key_weights, keep,
+           recent, dst_block_table, workspace):
+    torch = _torch or _load_torch()
     P, H_kv, ps = dims
     B_ = block_table.shape[0]
     _table(block_table, context_lens, B_)
@@ -785,17 +805,21 @@ def _evict(name, fn, dims, dtype_id, device, block_table, context_lens, key_weig
     _weights_shape("key_weights", key_weights, B_, H_kv, block_table.shape[1] * ps)
     if workspace is None:
         workspace = new_cache_workspace(device)
-    _on_device(device, block_table=block_table, context_lens=context_lens,
-               key_weights=key_weights, dst_block_table=dst_block_table, workspace=workspace)
+    index = device.index
+    _on_device(index, ("block_table", block_table), ("context_lens", context_lens),
+               ("key_weights", key_weights), ("dst_block_table", dst_block_table),
+               ("workspace", workspace))
     if not 1 <= keep <= dst_block_table.shape[1] * ps:
         raise ValueError("keep must be at least 1 and fit dst_block_table")
-    shape = make_shape(B_, H_kv, H_kv, 1, 128, P, ps, block_table.shape[1], dtype_id)
-    ints = torch.empty(B_ + B_ * H_kv * keep, dtype=torch.int32, device=device)
-    new = Evicted(ints[:B_],
-                  torch.empty((B_, H_kv, keep), dtype=torch.float32, device=device),
-                  ints[B_:].view(B_, H_kv, keep))
-    _call(name, device, lambda s: fn(shape, new, workspace, s))
-    return new
+    shape = pa_shape(B_, H_kv, H_kv, 1, 128, P, ps, block_table.shape[1], dtype_id)
+    lens = torch.empty(B_, dtype=torch.int32, device=device)
+    weights = torch.empty((B_, H_kv, keep), dtype=torch.float32, device=device)
+    kept = torch.empty((B_, H_kv, keep), dtype=torch.int32, device=device)
+    _launch(name, index, fn, ctypes.byref(shape), *pools, block_table.data_ptr(),
+            context_lens.data_ptr(), key_weights.data_ptr(), key_weights.shape[2], keep, recent,
+            dst_block_table.data_ptr(), dst_block_table.shape[1], lens.data_ptr(),
+            weights.data_ptr(), keep, kept.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return Evicted(lens, weights, kept)
 
 
 @_streamed
@@ -808,27 +832,16 @@ def evict_kv(key_pages, value_pages, block_table, context_lens, key_weights, kee
     dims = _pages_dims(key_pages, value_pages)
     if key_pages.shape[3] != 128:
         raise ValueError("head dim must be 128")
-    return _evict(
-        "pa_evict_kv",
-        lambda sh, new, ws, s: pa_evict_kv(
-            sh, key_pages, value_pages, block_table, context_lens, key_weights,
-            key_weights.shape[2], keep, recent, dst_block_table, dst_block_table.shape[1],
-            new.context_lens, new.key_weights, new.key_weights.shape[2], new.kept, ws,
-            ws.numel(), s),
-        dims, _dtype_id(key_pages.dtype), key_pages.device, block_table, context_lens,
-        key_weights, keep, dst_block_table, workspace)
+    return _evict("pa_evict_kv", load().pa_evict_kv,
+                  (key_pages.data_ptr(), value_pages.data_ptr()), dims,
+                  _dtype_id(key_pages.dtype), key_pages.device, block_table, context_lens,
+                  key_weights, keep, recent, dst_block_table, workspace)
 
 
 @_streamed
 def evict_kv_q4(pool, block_table, context_lens, key_weights, keep, recent, dst_block_table, *,
                 workspace=None) -> Evicted:
     """evict_kv of a 4-bit pool."""
-    dims = pool.dims
-    return _evict(
-        "pa_evict_kv_q4",
-        lambda sh, new, ws, s: pa_evict_kv_q4(
-            sh, pool, block_table, context_lens, key_weights, key_weights.shape[2], keep,
-            recent, dst_block_table, dst_block_table.shape[1], new.context_lens,
-            new.key_weights, new.key_weights.shape[2], new.kept, ws, ws.numel(), s),
-        dims, PA_BF16, pool.device, block_table, context_lens, key_weights, keep,
-        dst_block_table, workspace)
+    return _evict("pa_evict_kv_q4", load().pa_evict_kv_q4, (ctypes.byref(pool.c_pool),),
+                  pool.dims, PA_BF16, pool.device, block_table, context_lens, key_weights, keep,
+                  recent, dst_block_table, workspace)

@@ -5,10 +5,13 @@
 //   s[r][k] = scale * q_r . K_k  (k <= position's frontier),
 //   out_r = sum_k softmax(s_r)[k] V_k,   w_out[k] = w_in[k] + sum_r softmax(s_r)[k].
 //
-// Layout.  A CTA of four warps takes up to 8 * NT rows of one (sequence, kv
-// head) over one chunk of its keys; each warp takes every fourth step of 32
-// keys (16 over bf16 pages) with its own running max, sum and O, and the warps merge at the end.
-// Chunks of one row are merged by walk_combine_kernel.
+// Layout.  A segment is up to 8 * NT rows of one (sequence, kv head).  The keys
+// of all segments, in units of 128, are cut into equal shares, one per resident
+// CTA (four warps); in each segment of its share a warp takes every fourth step
+// of 32 keys (16 over bf16 pages) with its own running max, sum and O, and the
+// warps merge at the end.  Segments that cross shares leave partial states, which
+// walk_combine_kernel merges.  Equal shares keep ragged batches balanced and pay
+// the start of a pipeline once per CTA.
 //
 // Keys are the M side of both products: S^T = K Q^T and O^T += V^T P^T with
 // mma m16n8k16 (16 keys, 8 rows), so 8 rows fill an instruction and a
@@ -49,8 +52,10 @@ struct WalkParams {
     const int32_t* bt;
     const int32_t* ctx;
     void* out;
-    float4* part_ml;  // [(b, kvh, row)][chunk]: max, sum of the applied weights, sum
-    float* part_o;    // [(b, kvh, row)][chunk][D]
+    // partial states: max, sum of the applied weights, sum; O.  walk_kernel: two
+    // slots per CTA of its rows; block_kernel: [(b, kvh, row)][chunk]
+    float4* part_ml;
+    float* part_o;
     float* lse;       // [(b, kvh, row)] log2 of the sum of 2^score, or null
     float* score;     // [(b, kvh)][key < cap][row] scores in log2 units, or null
     long long cap;    // keys of a (b, kvh) in score
@@ -58,7 +63,11 @@ struct WalkParams {
     float* w_out;
     long long w_S;
     uint32_t* flag;
-    int B, H_kv, L, R, num_pages, ps, max_npg, causal, nrc, nkc, C;
+    int B, H_kv, L, R, num_pages, ps, max_npg, causal, nrc;
+    int nkc, C;   // block_kernel: key chunks of a row, keys per chunk
+    int whole;    // walk_kernel: 1 one CTA per segment, 0 equal shares of all keys
+    int min_per;  // least units of a share
+    int* prefix;  // [B] first unit of a sequence, [B] all units, [B + 1] units per share
     long long max_S;
     float scale_log2;
 };
@@ -490,8 +499,90 @@ struct QueryFrags {
 };
 
 // ---------------------------------------------------------------------------
+// Units of 128 keys (a step of every warp, or two) are what the shares count.
+constexpr int kUnit = 128;
+
+__device__ __forceinline__ int warp_sum(int v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// This CTA's equal share of the keys of all segments (sequence, kv head, row
+// chunk): share = all units, units per share, the sequence that holds the
+// share's first unit and that sequence's first unit.  CTA 0 also leaves the
+// sequences' first units in p.prefix for the merge.
+__device__ __forceinline__ void find_share(const WalkParams& p, int* share) {
+    __shared__ int sums[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int segs = p.H_kv * p.nrc;
+    auto units = [&](int b) { return b < p.B ? (seq_len(p, b, false) + kUnit - 1) / kUnit * segs : 0; };
+    const int mine = units(threadIdx.x);
+    int v = mine;
+    for (int b = threadIdx.x + kWarps * 32; b < p.B; b += kWarps * 32) v += units(b);
+    v = warp_sum(v);
+    if (lane == 0) sums[warp] = v;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += sums[w];
+    const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), p.min_per);
+    if (threadIdx.x == 0) {
+        share[0] = total;
+        share[1] = per;
+        if (blockIdx.x == 0) {
+            p.prefix[p.B] = total;
+            p.prefix[p.B + 1] = per;
+        }
+    }
+    const int u = static_cast<int>(blockIdx.x) * per;
+    int carry = 0;
+    for (int base = 0; base < p.B; base += kWarps * 32) {
+        const int b = base + static_cast<int>(threadIdx.x);
+        const int x = base == 0 ? mine : units(b);
+        int incl = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        __syncthreads();  // sums is free
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        int before = carry + incl - x;
+        for (int w = 0; w < warp; ++w) before += sums[w];
+        if (b < p.B) {
+            if (blockIdx.x == 0) p.prefix[b] = before;
+            if (before <= u && u < before + x) {
+                share[2] = b;
+                share[3] = before;
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) carry += sums[w];
+    }
+    __syncthreads();
+}
+
+// The merged row (four dims a lane) and its log-sum-exp.
+template <bool F32>
+__device__ __forceinline__ void store_row(const WalkParams& p, long long row, int lane, float4 acc, float at, float lt,
+                                          float M) {
+    const float inv = at > 0.f ? 1.f / at : 0.f;
+    if constexpr (F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kD + 4 * lane) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kD + 4 * lane) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0 && p.lse) p.lse[row] = lt > 0.f ? M + log2f(lt) : __int_as_float(0x7f800000);
+}
+
+// CTAs of walk_kernel resident per SM.
+constexpr int resident_ctas(int nt, bool q4, bool f32) { return nt == 2 ? 2 : f32 || !q4 ? 3 : 4; }
+
 template <class Keys, class Values, int NT, bool F32, bool A16, bool W>
-__global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
+__global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32)) walk_kernel(const WalkParams p) {
     constexpr bool F16 = Keys::kF16;
     constexpr int ROWS = 8 * NT;
     constexpr int U = Keys::kU, kStep = 16 * U;
@@ -499,13 +590,36 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
     float* const merge = reinterpret_cast<float*>(smem);  // [warp][row][kMerge]: o, m, applied sum, sum
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    int item = static_cast<int>(blockIdx.x);
-    const int kc = item % p.nkc;
-    item /= p.nkc;
-    const int rc = item % p.nrc;
-    item /= p.nrc;
-    const int kvh = item % p.H_kv, b = item / p.H_kv;
-    const int S = seq_len(p, b, kc == 0 && rc == 0 && kvh == 0 && threadIdx.x == 0);
+    __shared__ int share[4];  // total units, units per share, first sequence, its first unit
+    int b, kvh, rc, S, g0, u = 0, u1 = 1, pref = 0;
+    if (p.whole) {
+        int item = static_cast<int>(blockIdx.x);
+        rc = item % p.nrc;
+        item /= p.nrc;
+        kvh = item % p.H_kv;
+        b = item / p.H_kv;
+        S = seq_len(p, b, rc == 0 && kvh == 0 && threadIdx.x == 0);
+        g0 = 0;
+    } else {
+        find_share(p, share);
+        const int per = share[1];
+        u = static_cast<int>(blockIdx.x) * per;
+        u1 = min(u + per, share[0]);
+        if (u >= u1) return;
+        b = share[2];
+        pref = share[3];
+        S = seq_len(p, b, false);
+    }
+    for (;;) {  // segments of this CTA's share
+    int n_units = 0, ng = 0;
+    if (!p.whole) {
+        ng = (S + kUnit - 1) / kUnit;
+        const int sib = (u - pref) / ng;  // (b has units: ng > 0)
+        g0 = (u - pref) - sib * ng;
+        kvh = sib / p.nrc;
+        rc = sib - kvh * p.nrc;
+        n_units = min(ng - g0, u1 - u);
+    }
     const int r0 = rc * ROWS, nrows = min(ROWS, p.R - r0);
     const long long row0 = (static_cast<long long>(b) * p.H_kv + kvh) * p.R + r0;
 
@@ -528,8 +642,8 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
         lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
         lim_max = max(lim_max, __shfl_xor_sync(0xffffffffu, lim_max, o));
     }
-    const int k0 = kc * p.C;
-    const int k1 = S > 0 ? min(lim_max + 1, k0 + p.C) : 0;
+    const int k0 = g0 * kUnit;
+    const int k1 = p.whole ? (S > 0 ? lim_max + 1 : 0) : min(lim_max + 1, (g0 + n_units) * kUnit);
 
     QueryFrags<Keys, F32> q[NT];
     float qs[NT][2];  // score scale of rows 2t, 2t + 1 in log2 units
@@ -744,6 +858,7 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
         }
     __syncthreads();
     const int d = threadIdx.x;  // one dim per thread
+    const bool full = p.whole || n_units == ng;
     for (int rr = 0; rr < nrows; ++rr) {
         float M = neg_inf();
 #pragma unroll
@@ -759,8 +874,8 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
                 lt += a * mr[kD + 2];
             }
         }
-        const long long row = row0 + rr;
-        if (p.nkc == 1) {
+        if (full) {
+            const long long row = row0 + rr;
             const float v = at > 0.f ? acc / at : 0.f;
             if constexpr (F32)
                 static_cast<float*>(p.out)[row * kD + d] = v;
@@ -768,16 +883,111 @@ __global__ void __launch_bounds__(kWarps * 32) walk_kernel(const WalkParams p) {
                 static_cast<uint16_t*>(p.out)[row * kD + d] = float_to_bf16_bits(v);
             if (d == 0 && p.lse) p.lse[row] = lt > 0.f ? M + log2f(lt) : __int_as_float(0x7f800000);
         } else {
-            if (d == 0) p.part_ml[row * p.nkc + kc] = make_float4(M, at, lt, 0.f);
-            if (M != neg_inf()) p.part_o[(row * p.nkc + kc) * kD + d] = acc;
+            // a share's segment that began in an earlier one, or its last one
+            const long long row = static_cast<long long>(2 * blockIdx.x + (g0 > 0 ? 0 : 1)) * ROWS + rr;
+            if (d == 0) p.part_ml[row] = make_float4(M, at, lt, 0.f);
+            if (M != neg_inf()) p.part_o[row * kD + d] = acc;
         }
     }
+    if (p.whole) return;
+    u += n_units;
+    if (u >= u1) return;
+    if (u == pref + ng * p.H_kv * p.nrc) {  // on to the next sequence with keys
+        pref = u;
+        do S = seq_len(p, ++b, false);
+        while (S == 0);
+    }
+    __syncthreads();  // the merge buffer becomes the stages again
+    }
+}
+
+// Merges the pieces of a segment that several shares hold: one CTA per row, its
+// warps take every fourth piece, four dims a lane.  Rows of sequences that
+// break the contract are written as zeros.
+template <bool F32>
+__global__ void __launch_bounds__(kWarps * 32) walk_combine_kernel(const WalkParams p, int rows_cta) {
+    __shared__ float4 mls[kWarps];
+    __shared__ float4 os[kWarps][32];
+    pdl_wait_primary();
+    const int per_seg = min(rows_cta, p.R);
+    const int seg = static_cast<int>(blockIdx.x) / per_seg, rr = static_cast<int>(blockIdx.x) - seg * per_seg;
+    const int bk = seg / p.nrc, rc = seg - bk * p.nrc;
+    const int b = bk / p.H_kv, kvh = bk - b * p.H_kv;
+    if (rc * rows_cta + rr >= p.R) return;
+    const long long row = static_cast<long long>(bk) * p.R + rc * rows_cta + rr;
+    const int S = seq_len(p, b, kvh == 0 && rc == 0 && rr == 0 && threadIdx.x == 0);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int ng = (S + kUnit - 1) / kUnit, per = p.prefix[p.B + 1];
+    const int first = p.prefix[b] + (kvh * p.nrc + rc) * ng;
+    const int c0 = first / per, c1 = ng > 0 ? (first + ng - 1) / per : c0 - 1;
+    if (c0 == c1) return;  // one share wrote it
+    // slot of piece i: the first share's last segment, then the others' first
+    auto slot = [&](int i) { return static_cast<long long>(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * rows_cta + rr; };
+    const int np = c1 - c0 + 1;
+    float M = neg_inf(), at = 0.f, lt = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int base = 0; base < np; base += 32 * kWarps) {  // lane i: piece base + 4 i + warp
+        const int mine = base + kWarps * lane + warp;
+        const float4 v = mine < np ? p.part_ml[slot(mine)] : make_float4(neg_inf(), 0.f, 0.f, 0.f);
+        float mt = v.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+        if (mt == neg_inf()) continue;
+        if (mt > M) {
+            const float a = fast_exp2(M - mt);  // 2^-inf = 0 at the start
+            acc.x *= a;
+            acc.y *= a;
+            acc.z *= a;
+            acc.w *= a;
+            at *= a;
+            lt *= a;
+            M = mt;
+        }
+        const float mine_a = fast_exp2(v.x - M);  // 0 for a piece without keys
+        const int n = min(32, (np - base - warp + kWarps - 1) / kWarps);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float a = __shfl_sync(0xffffffffu, mine_a, i);
+            const float y = __shfl_sync(0xffffffffu, v.y, i), z = __shfl_sync(0xffffffffu, v.z, i);
+            if (a == 0.f) continue;  // (its O was not written)
+            const float4 x = *reinterpret_cast<const float4*>(p.part_o + slot(base + kWarps * i + warp) * kD + 4 * lane);
+            at += a * y;
+            lt += a * z;
+            acc.x += a * x.x;
+            acc.y += a * x.y;
+            acc.z += a * x.z;
+            acc.w += a * x.w;
+        }
+    }
+    if (lane == 0) mls[warp] = make_float4(M, at, lt, 0.f);
+    os[warp][lane] = acc;
+    __syncthreads();
+    if (warp > 0) return;
+    float Mx = neg_inf();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) Mx = fmaxf(Mx, mls[w].x);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    at = lt = 0.f;
+    if (Mx != neg_inf()) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float a = fast_exp2(mls[w].x - Mx);
+            const float4 x = os[w][lane];
+            at += a * mls[w].y;
+            lt += a * mls[w].z;
+            acc.x += a * x.x;
+            acc.y += a * x.y;
+            acc.z += a * x.z;
+            acc.w += a * x.w;
+        }
+    }
+    store_row<F32>(p, row, lane, acc, at, lt, Mx);
 }
 
 // Merges the key chunks of a row: one warp per row, four dims per lane.  A
 // row without keys is written as zeros.
 template <bool F32>
-__global__ void __launch_bounds__(128) walk_combine_kernel(const WalkParams p) {
+__global__ void __launch_bounds__(128) block_combine_kernel(const WalkParams p) {
     pdl_wait_primary();
     const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (row >= static_cast<long long>(p.B) * p.H_kv * p.R) return;
@@ -804,14 +1014,7 @@ __global__ void __launch_bounds__(128) walk_combine_kernel(const WalkParams p) {
             acc.w += a * x.w;
         }
     }
-    const float inv = at > 0.f ? 1.f / at : 0.f;
-    if constexpr (F32)
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kD + 4 * lane) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kD + 4 * lane) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (lane == 0 && p.lse) p.lse[row] = lt > 0.f ? M + log2f(lt) : __int_as_float(0x7f800000);
+    store_row<F32>(p, row, lane, acc, at, lt, M);
 }
 
 // ---- many rows: tiles of 64 keys shared by 64 rows --------------------------
@@ -1253,39 +1456,58 @@ __global__ void __launch_bounds__(kWarps * 32) walk_weights_kernel(const WalkPar
 // ---------------------------------------------------------------------------
 struct WalkPlan {
     int R, nt, nrc, nkc, C;  // nt: n-tiles of 8 rows of walk_kernel, 0: block_kernel
+    bool whole;              // walk_kernel: a CTA per segment
     bool scores;             // key weights from stored scores
-    size_t ml_off, o_off, lse_off, score_off, total;
+    long long items;         // CTAs
+    size_t prefix_off, ml_off, o_off, lse_off, score_off, total;
 };
 
-constexpr int kBlockRows = 32;  // rows per kv head from which block_kernel takes a call
-constexpr int kScoreRows = 8;   // rows per kv head up to which scores are stored
+constexpr int kBlockRows = 32;   // rows per kv head from which block_kernel takes a call
+constexpr int kScoreRows = 8;    // rows per kv head up to which scores are stored
+constexpr int kWholeKeys = 512;  // table capacity up to which a CTA takes a whole segment
+constexpr int kMinPer = 2;       // least units of a share
 
 // walk_kernel: 8 rows per CTA, or 16 where a (sequence, kv head) has more than
-// 8 (not for fp32 queries, whose fragments take twice the registers);
-// block_kernel: 64.  Key chunks: enough for about eight CTAs per SM (block: four), of
-// at least 256 keys.
-WalkPlan plan(const pa_shape& sh, bool weights, int sm_count) {
+// 8 (not for fp32 queries, whose fragments take twice the registers); as many
+// CTAs as are resident together (4 per SM, 2 with 16 rows or fp32), each an equal
+// share of all keys, or, over short tables, one per segment and no merge.
+// block_kernel: 64 rows, key chunks for about four CTAs per SM, of at least 256 keys.
+WalkPlan plan(const pa_shape& sh, bool q4, bool weights, int sm_count) {
     WalkPlan w;
     w.R = sh.H_q / sh.H_kv * sh.L;
-    w.nt = w.R >= kBlockRows ? 0 : w.R > 8 && sh.dtype == PA_BF16 ? 2 : 1;
+    const bool f32 = sh.dtype == PA_F32;
+    w.nt = w.R >= kBlockRows ? 0 : w.R > 8 && !f32 ? 2 : 1;
     const int rows_cta = w.nt ? 8 * w.nt : 16 * kWarps;
     w.nrc = (w.R + rows_cta - 1) / rows_cta;
     w.scores = weights && w.R <= kScoreRows;
     const long long cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
-    const long long items = static_cast<long long>(sh.B) * sh.H_kv * w.nrc;
-    long long nkc = ((w.nt ? 8ll : 4ll) * sm_count + items - 1) / items;
-    const long long most = (cap + 255) / 256;
-    nkc = nkc < most ? nkc : most;
-    long long C = (cap + nkc - 1) / nkc;
-    C = (C + kWarps * 32 - 1) / (kWarps * 32) * (kWarps * 32);  // whole steps of every warp
-    w.C = static_cast<int>(C);
-    w.nkc = static_cast<int>((cap + C - 1) / C);
+    const long long segs = static_cast<long long>(sh.B) * sh.H_kv * w.nrc;
     const size_t rows = static_cast<size_t>(sh.B) * sh.H_kv * w.R;
+    w.whole = w.nt && cap <= kWholeKeys;
+    w.nkc = 1;
+    w.C = 0;
+    size_t slots = 0;  // rows of partial states
+    if (w.nt) {
+        w.items = w.whole ? segs : static_cast<long long>(sm_count) * resident_ctas(w.nt, q4, f32);
+        if (!w.whole) slots = static_cast<size_t>(w.items) * 2 * rows_cta;
+    } else {
+        long long nkc = (4ll * sm_count + segs - 1) / segs;
+        const long long most = (cap + 255) / 256;
+        nkc = nkc < most ? nkc : most;
+        long long C = (cap + nkc - 1) / nkc;
+        C = (C + kTK - 1) / kTK * kTK;
+        w.C = static_cast<int>(C);
+        w.nkc = static_cast<int>((cap + C - 1) / C);
+        w.items = segs * w.nkc;
+        if (w.nkc > 1) slots = rows * w.nkc;
+    }
     size_t off = kFlagBytes;
+    w.prefix_off = off;
+    if (w.nt && !w.whole) off = align_up(off + (static_cast<size_t>(sh.B) + 2) * 4, 256);
     w.ml_off = off;
-    if (w.nkc > 1) off = align_up(off + rows * w.nkc * 16, 256);
+    off = align_up(off + slots * 16, 256);
     w.o_off = off;
-    if (w.nkc > 1) off = align_up(off + rows * w.nkc * kD * 4, 256);
+    off = align_up(off + slots * kD * 4, 256);
     w.lse_off = off;
     if (weights) off = align_up(off + rows * 4, 256);
     w.score_off = off;
@@ -1353,9 +1575,11 @@ pa_status launch_block(const WalkParams& p, long long items, int device, cudaStr
 
 pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, int device, cudaStream_t stream) {
     const long long bk = static_cast<long long>(p.B) * p.H_kv;
-    const long long items = bk * p.nrc * p.nkc, rows = bk * p.R;
+    const long long items = w.items, rows = bk * p.R;
     const long long per = w.scores ? 256 : 32 * kWarps, ntile = (p.w_S + per - 1) / per;
-    if (items > INT_MAX || rows > 4ll * INT_MAX || ntile * bk > INT_MAX) return PA_ERR_UNSUPPORTED;
+    if (items > INT_MAX || rows > INT_MAX || ntile * bk > INT_MAX) return PA_ERR_UNSUPPORTED;
+    // the shares count units in an int
+    if (w.nt && !w.whole && bk * p.nrc * (p.max_S / kUnit + 1) > INT_MAX / 2) return PA_ERR_UNSUPPORTED;
     pa_status st;
     if (w.nt == 0)
         st = !q4 ? launch_block<false, false>(p, items, device, stream)
@@ -1370,8 +1594,14 @@ pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, int 
         st = w.nt == 2 ? launch_walk_for<Q4Keys, Q4Values, 2, false>(p, items, device, stream)
                        : launch_walk_for<Q4Keys, Q4Values, 1, false>(p, items, device, stream);
     if (st != PA_OK) return st;
-    if (p.nkc > 1 && !launch_dependent(f32 ? walk_combine_kernel<true> : walk_combine_kernel<false>, (rows + 3) / 4, 128, stream, p))
+    if (p.nkc > 1 && !launch_dependent(f32 ? block_combine_kernel<true> : block_combine_kernel<false>, (rows + 3) / 4, 128, stream, p))
         return PA_ERR_CUDA;
+    if (w.nt && !w.whole) {
+        const int rows_cta = 8 * w.nt;
+        const long long grid = bk * p.nrc * (rows_cta < p.R ? rows_cta : p.R);
+        if (!launch_dependent(f32 ? walk_combine_kernel<true> : walk_combine_kernel<false>, grid, kWarps * 32, stream, p, rows_cta))
+            return PA_ERR_CUDA;
+    }
     if (!p.w_out) return PA_OK;
     if (w.scores) return launch_dependent(walk_sum_kernel, ntile * bk, 256, stream, p, static_cast<int>(ntile)) ? PA_OK : PA_ERR_CUDA;
     const unsigned grid = static_cast<unsigned>(ntile * bk);
@@ -1468,7 +1698,7 @@ pa_status tiles_launch(const WalkCall& c, const TilePlan& t) {
 size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_count) {
     TilePlan t;
     if (tiles_take(sh, q4, weights, sm_count, &t)) return t.total;
-    return plan(sh, weights, sm_count).total;
+    return plan(sh, q4, weights, sm_count).total;
 }
 
 pa_status walk_launch(const WalkCall& c) {
@@ -1478,7 +1708,7 @@ pa_status walk_launch(const WalkCall& c) {
         if (c.ws_bytes < t.total) return PA_ERR_WORKSPACE;
         return tiles_launch(c, t);
     }
-    const WalkPlan w = plan(sh, c.w_out != nullptr, c.dev.sm_count);
+    const WalkPlan w = plan(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count);
     if (c.ws_bytes < w.total) return PA_ERR_WORKSPACE;
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
     WalkParams p;
@@ -1508,6 +1738,9 @@ pa_status walk_launch(const WalkCall& c) {
     p.nrc = w.nrc;
     p.nkc = w.nkc;
     p.C = w.C;
+    p.whole = w.whole ? 1 : 0;
+    p.min_per = kMinPer;
+    p.prefix = reinterpret_cast<int*>(ws + w.prefix_off);
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     p.scale_log2 = c.scale * 1.4426950408889634f;
     p.score = w.scores ? reinterpret_cast<float*>(ws + w.score_off) : nullptr;
