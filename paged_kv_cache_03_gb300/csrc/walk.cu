@@ -82,16 +82,18 @@ __device__ __forceinline__ int seq_len(const WalkParams& p, int b, bool report) 
     return bad ? 0 : S;
 }
 
-// Page of logical page lp of sequence b, -1 past `end` (its number of pages)
-// and for a bad id (flagged).
-__device__ __forceinline__ int page_of(const WalkParams& p, int b, int lp, int end) {
-    if (lp >= end) return -1;
-    const int pp = __ldg(p.bt + static_cast<long long>(b) * p.max_npg + lp);
-    if (pp < 0 || pp >= p.num_pages) {
-        atomicOr(p.flag, PA_FLAG_BAD_PAGE);
-        return -1;
-    }
-    return pp;
+// A page id, requested before it is needed: kNoPage past a sequence's pages.
+constexpr int kNoPage = INT_MIN;
+
+// Pool row of slot `slot` of page `pg`, -1 for no page or a bad id; bad ids are
+// gathered in `bad` (no branch here) and flagged once at a kernel's end.
+__device__ __forceinline__ int row_in(const WalkParams& p, int kvh, int pg, int slot, bool& bad) {
+    const bool ok = static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages);
+    bad |= !ok && pg != kNoPage;
+    return ok ? (pg * p.H_kv + kvh) * p.ps + slot : -1;
+}
+__device__ __forceinline__ void report_pages(const WalkParams& p, bool bad) {
+    if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) atomicOr(p.flag, PA_FLAG_BAD_PAGE);
 }
 
 // Pool rows of the 16 U keys of a warp's step (U = 1 or 2); -1: no row (the key
@@ -114,6 +116,7 @@ struct StepRows {
 template <bool A16, int U>
 struct StepWalker {
     int lp, slot, dlp, dslot;  // of the step's first key (A16) or this lane's key
+    bool bad = false;          // a bad page id was met
     __device__ __forceinline__ void start(const WalkParams& p, int key, int stride) {
         lp = key / p.ps;
         slot = key - lp * p.ps;
@@ -128,18 +131,18 @@ struct StepWalker {
             ++lp;
         }
     }
-    // pages of the step (npg: pages of the sequence)
-    __device__ __forceinline__ void pages(const WalkParams& p, int b, int npg, int (&pg)[2]) const {
-        pg[0] = page_of(p, b, lp, npg);
-        if constexpr (A16 && U == 2) pg[1] = slot + 16 < p.ps ? pg[0] : page_of(p, b, lp + 1, npg);
+    // Requests the step's page ids (npg: pages of the sequence, 0 for a step that
+    // is not taken); rows() checks them a step later, so that nothing waits for the
+    // load here.
+    __device__ __forceinline__ void pages(const int32_t* row, const WalkParams& p, int npg, int (&pg)[2]) const {
+        pg[0] = lp < npg ? __ldg(row + lp) : kNoPage;
+        if constexpr (A16 && U == 2) pg[1] = slot + 16 >= p.ps && lp + 1 < npg ? __ldg(row + lp + 1) : kNoPage;
     }
-    __device__ __forceinline__ StepRows<A16, U> rows(const WalkParams& p, int kvh, const int (&pg)[2]) const {
+    __device__ __forceinline__ StepRows<A16, U> rows(const WalkParams& p, int kvh, const int (&pg)[2]) {
         StepRows<A16, U> w;
-        w.r[0] = pg[0] < 0 ? -1 : (pg[0] * p.H_kv + kvh) * p.ps + slot;
-        if constexpr (A16 && U == 2) {
-            const int s1 = slot + 16 < p.ps ? slot + 16 : 0;
-            w.r[1] = pg[1] < 0 ? -1 : (pg[1] * p.H_kv + kvh) * p.ps + s1;
-        }
+        w.r[0] = row_in(p, kvh, pg[0], slot, bad);
+        if constexpr (A16 && U == 2)
+            w.r[1] = slot + 16 < p.ps ? (w.r[0] < 0 ? -1 : w.r[0] + 16) : row_in(p, kvh, pg[1], 0, bad);
         return w;
     }
 };
@@ -196,14 +199,31 @@ struct Stage<true> {  // 32 keys: K codes, V codes, K scales, V scales
         const uint8_t* const vc = static_cast<const uint8_t*>(p.vc);
         const uint8_t* const ks = static_cast<const uint8_t*>(p.ks);
         const uint8_t* const vs = static_cast<const uint8_t*>(p.vs);
+        if constexpr (A16) {  // 16 rows lie together: 64 chunks, two copies a lane
+            // v_at(u, i, c) of chunk lane + 32 j is v0 + 1024 u + 256 j
+            const uint32_t v0 = st + v_at(0, lane >> 2, lane & 3);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int u = j >> 1, i = (lane >> 2) + 8 * (j & 1), c = lane & 3;
-            const int row = rows.row(u, i);
-            const bool ok = A16 ? rows.any(u) : row >= 0;
-            const long long off = ok ? static_cast<long long>(row) * kQ4CodeBytes + 16 * c : 0;
-            cp_async16(st + 16 * (lane + 32 * j), kc + off, ok);
-            cp_async16(st + v_at(u, i, c), vc + off, ok);
+            for (int u = 0; u < 2; ++u) {
+                const bool ok = rows.any(u);
+                const long long off = ok ? static_cast<long long>(rows.r[u]) * kQ4CodeBytes + 16 * lane : 0;
+                const uint8_t* const k = kc + off;
+                const uint8_t* const v = vc + off;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    cp_async16(st + 16 * lane + 1024 * u + 512 * j, k + 512 * j, ok);
+                    cp_async16(v0 + 1024 * u + 256 * j, v + 512 * j, ok);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int u = j >> 1, i = (lane >> 2) + 8 * (j & 1), c = lane & 3;
+                const int row = rows.row(u, i);
+                const bool ok = row >= 0;
+                const long long off = ok ? static_cast<long long>(row) * kQ4CodeBytes + 16 * c : 0;
+                cp_async16(st + 16 * (lane + 32 * j), kc + off, ok);
+                cp_async16(st + v_at(u, i, c), vc + off, ok);
+            }
         }
         if constexpr (A16) {  // two keys a chunk: lanes 0 - 15 K, 16 - 31 V
             const int i = lane & 15, r = i < 8 ? rows.r[0] : rows.r[1];
@@ -431,11 +451,18 @@ struct BfValues {
 };
 
 template <bool F16>
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        mma_16816_f16_first(d, a, b0, b1);
+    else
+        mma_16816_bf16_first(d, a, b0, b1);
+}
+template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (F16)
         mma_16816_f16(d, a, b0, b1);
     else
-        mma_16816(d, a, b0, b1);
+        mma_16816_bf16(d, a, b0, b1);
 }
 
 // The B fragments of 8 query rows.  Lane 4g + t holds row g; hi and, for fp32
@@ -445,34 +472,32 @@ struct QueryFrags {
     uint32_t hi[8][2];
     uint32_t lo[F32 ? 8 : 1][2];
 
-    // Loads row `row` of the (b, kvh) block (zeros when !ok); returns the
-    // factor that takes a product with the stored fragments to the real one.
-    __device__ __forceinline__ float load(const void* q, long long row, bool ok, int t) {
+    // Requests row `row` (zeros when !ok); finish() turns it into fragments and
+    // returns the factor that takes a product with them to the real one.
+    __device__ __forceinline__ void request(const void* q, long long row, bool ok, int t) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const long long at = row * kD + Keys::qdim(k >> 1, k & 1, t);
+            if constexpr (F32) {
+                float2 f = make_float2(0.f, 0.f);
+                if (ok) f = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(q) + at));
+                hi[k >> 1][k & 1] = __float_as_uint(f.x);
+                lo[k >> 1][k & 1] = __float_as_uint(f.y);
+            } else {
+                hi[k >> 1][k & 1] = 0u;
+                if (ok) hi[k >> 1][k & 1] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(q) + at));
+            }
+        }
+    }
+    __device__ __forceinline__ float finish() {
+        if constexpr (!F32 && !Keys::kF16) return 1.f;
         float2 f[16];
-        if constexpr (F32) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                f[k] = make_float2(0.f, 0.f);
-                if (ok)
-                    f[k] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(q) + row * kD +
-                                                                 Keys::qdim(k >> 1, k & 1, t)));
-            }
-        } else {
-            uint32_t u[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                u[k] = 0u;
-                if (ok)
-                    u[k] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(q) + row * kD +
-                                                                   Keys::qdim(k >> 1, k & 1, t)));
-            }
-            if constexpr (!Keys::kF16) {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) hi[k >> 1][k & 1] = u[k];
-                return 1.f;
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) f[k] = bf16x2_to_float2(u[k]);
+        for (int k = 0; k < 16; ++k) {
+            if constexpr (F32)
+                f[k] = make_float2(__uint_as_float(hi[k >> 1][k & 1]), __uint_as_float(lo[k >> 1][k & 1]));
+            else
+                f[k] = bf16x2_to_float2(hi[k >> 1][k & 1]);
         }
         // into f16's range: the row's largest value into [2^14, 2^15)
         float mx = 0.f;
@@ -495,6 +520,10 @@ struct QueryFrags {
             }
         }
         return down;
+    }
+    __device__ __forceinline__ float load(const void* q, long long row, bool ok, int t) {
+        request(q, row, ok, t);
+        return finish();
     }
 };
 
@@ -564,6 +593,46 @@ __device__ __forceinline__ void find_share(const WalkParams& p, int* share) {
     __syncthreads();
 }
 
+// A piece of a segment: units g0 .. g0 + n - 1 of its ng.
+struct Segment {
+    int b, S, pref;  // sequence, its length and first unit
+    int kvh, rc, ng, g0, n;
+    // The piece at unit `pos` of sequence b (which has it), up to unit `end`.
+    __device__ __forceinline__ void at(const WalkParams& p, int pos, int end) {
+        ng = (S + kUnit - 1) / kUnit;
+        const int sib = (pos - pref) / ng;
+        g0 = (pos - pref) - sib * ng;
+        kvh = sib / p.nrc;
+        rc = sib - kvh * p.nrc;
+        n = min(ng - g0, end - pos);
+    }
+    // On to unit `pos`, the one after this piece.
+    __device__ __forceinline__ void advance(const WalkParams& p, int pos, int end) {
+        if (pos == pref + ng * p.H_kv * p.nrc) {  // the next sequence with keys
+            pref = pos;
+            do S = seq_len(p, ++b, false);
+            while (S == 0);
+        }
+        at(p, pos, end);
+    }
+    __device__ __forceinline__ long long row0(const WalkParams& p, int rows) const {
+        return (static_cast<long long>(b) * p.H_kv + kvh) * p.R + rc * rows;
+    }
+    // k1: the keys of the piece that some row sees end before it; lo: the last key
+    // that every row sees.
+    template <int ROWS>
+    __device__ __forceinline__ void bounds(const WalkParams& p, int& k1, int& lo) const {
+        int hi = S - 1;
+        lo = hi;
+        if (p.causal) {  // rows r0 .. r0 + nrows - 1 are positions r % L
+            const int l0 = rc * ROWS % p.L, last = l0 + min(ROWS, p.R - rc * ROWS) - 1;
+            hi = (last < p.L ? last : p.L - 1) + S - p.L;
+            lo = (last < p.L ? l0 : 0) + S - p.L;
+        }
+        k1 = S > 0 ? min(hi + 1, (g0 + n) * kUnit) : 0;
+    }
+};
+
 // The merged row (four dims a lane) and its log-sum-exp.
 template <bool F32>
 __device__ __forceinline__ void store_row(const WalkParams& p, long long row, int lane, float4 acc, float at, float lt,
@@ -580,77 +649,92 @@ __device__ __forceinline__ void store_row(const WalkParams& p, long long row, in
 
 // CTAs of walk_kernel resident per SM.
 constexpr int resident_ctas(int nt, bool q4, bool f32) { return nt == 2 ? 2 : f32 || !q4 ? 3 : 4; }
+constexpr size_t walk_smem(bool q4, int rows) {
+    return kWarps * 2 * (q4 ? Stage<true>::kBytes : Stage<false>::kBytes) + sizeof(float) * kWarps * rows * kMerge;
+}
 
 template <class Keys, class Values, int NT, bool F32, bool A16, bool W>
 __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32)) walk_kernel(const WalkParams p) {
     constexpr bool F16 = Keys::kF16;
     constexpr int ROWS = 8 * NT;
     constexpr int U = Keys::kU, kStep = 16 * U;
-    extern __shared__ __align__(1024) uint8_t smem[];         // the warps' stages, then
-    float* const merge = reinterpret_cast<float*>(smem);  // [warp][row][kMerge]: o, m, applied sum, sum
+    using St = Stage<F16>;
+    extern __shared__ __align__(1024) uint8_t smem[];  // the warps' stages, then the merge buffer:
+    const int mrows = min(ROWS, p.R);                  // [warp][row][kMerge]: o, max, applied sum, sum
+    float* const merge = reinterpret_cast<float*>(smem + kWarps * 2 * St::kBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     __shared__ int share[4];  // total units, units per share, first sequence, its first unit
-    int b, kvh, rc, S, g0, u = 0, u1 = 1, pref = 0;
+    pdl_launch_dependents();
+    Segment sg;
+    int pos = 0, end = 0;  // units of this CTA's share
     if (p.whole) {
         int item = static_cast<int>(blockIdx.x);
-        rc = item % p.nrc;
+        sg.rc = item % p.nrc;
         item /= p.nrc;
-        kvh = item % p.H_kv;
-        b = item / p.H_kv;
-        S = seq_len(p, b, rc == 0 && kvh == 0 && threadIdx.x == 0);
-        g0 = 0;
+        sg.kvh = item % p.H_kv;
+        sg.b = item / p.H_kv;
+        sg.S = seq_len(p, sg.b, sg.rc == 0 && sg.kvh == 0 && threadIdx.x == 0);
+        sg.pref = sg.g0 = 0;
+        sg.ng = sg.n = (sg.S + kUnit - 1) / kUnit;
     } else {
         find_share(p, share);
-        const int per = share[1];
-        u = static_cast<int>(blockIdx.x) * per;
-        u1 = min(u + per, share[0]);
-        if (u >= u1) return;
-        b = share[2];
-        pref = share[3];
-        S = seq_len(p, b, false);
+        pos = static_cast<int>(blockIdx.x) * share[1];
+        end = min(pos + share[1], share[0]);
+        if (pos >= end) return;
+        sg.b = share[2];
+        sg.pref = share[3];
+        sg.S = seq_len(p, sg.b, false);
+        sg.at(p, pos, end);
     }
-    for (;;) {  // segments of this CTA's share
-    int n_units = 0, ng = 0;
-    if (!p.whole) {
-        ng = (S + kUnit - 1) / kUnit;
-        const int sib = (u - pref) / ng;  // (b has units: ng > 0)
-        g0 = (u - pref) - sib * ng;
-        kvh = sib / p.nrc;
-        rc = sib - kvh * p.nrc;
-        n_units = min(ng - g0, u1 - u);
-    }
-    const int r0 = rc * ROWS, nrows = min(ROWS, p.R - r0);
-    const long long row0 = (static_cast<long long>(b) * p.H_kv + kvh) * p.R + r0;
+    const uint32_t ring = smem_u32(smem) + warp * 2 * St::kBytes;
+    uint32_t st = ring;
+    StepWalker<A16, U> wk;
+    int pg[2] = {-1, -1};
+    QueryFrags<Keys, F32> q[NT];
+    // Requests the first stage, the page ids after it and the query rows of `sg`.
+    auto open_keys = [&]() {
+        int k1, lo;
+        sg.bounds<ROWS>(p, k1, lo);
+        const int first = sg.g0 * kUnit + warp * kStep;
+        wk.start(p, A16 ? first : first + lane, kWarps * kStep);
+        const int npg = (sg.S + p.ps - 1) / p.ps;
+        const int32_t* const table = p.bt + static_cast<long long>(sg.b) * p.max_npg;
+        wk.pages(table, p, first < k1 ? npg : 0, pg);
+        St::fill(p, wk.rows(p, sg.kvh, pg), st, lane);
+        wk.next(p);
+        wk.pages(table, p, first + kWarps * kStep < k1 ? npg : 0, pg);
+        cp_async_commit();
+    };
+    auto open_query = [&]() {
+        const long long row0 = sg.row0(p, ROWS);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) q[n].request(p.q, row0 + 8 * n + g, sg.rc * ROWS + 8 * n + g < p.R, t);
+    };
+    open_query();
+    open_keys();
 
+    for (;;) {  // segments of the share
+    const int S = sg.S, b = sg.b, kvh = sg.kvh;
+    const int r0 = sg.rc * ROWS, nrows = min(ROWS, p.R - r0);
+    const long long row0 = sg.row0(p, ROWS);
+    const int npg = (S + p.ps - 1) / p.ps;
+    const int32_t* const table = p.bt + static_cast<long long>(b) * p.max_npg;
+    int k1, lim_min;  // last key any row sees + 1 (within the share), last key every row sees
+    sg.bounds<ROWS>(p, k1, lim_min);
     // the last key each of this lane's rows (2t, 2t + 1 of every n-tile) sees
-    int lim[NT][2], lim_min = INT_MAX, lim_max = -1;
+    int lim[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int rr = 8 * n + 2 * t + e;
-            lim[n][e] = -1;
-            if (rr < nrows) lim[n][e] = p.causal ? (r0 + rr) % p.L + S - p.L : S - 1;
-            if (rr < nrows) {
-                lim_min = min(lim_min, lim[n][e]);
-                lim_max = max(lim_max, lim[n][e]);
-            }
+            lim[n][e] = rr < nrows ? (p.causal ? (r0 + rr) % p.L + S - p.L : S - 1) : -1;
         }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
-        lim_max = max(lim_max, __shfl_xor_sync(0xffffffffu, lim_max, o));
-    }
-    const int k0 = g0 * kUnit;
-    const int k1 = p.whole ? (S > 0 ? lim_max + 1 : 0) : min(lim_max + 1, (g0 + n_units) * kUnit);
-
-    QueryFrags<Keys, F32> q[NT];
     float qs[NT][2];  // score scale of rows 2t, 2t + 1 in log2 units
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int rr = 8 * n + g;
-        const float down = q[n].load(p.q, row0 + rr, rr < nrows, t);
+        const float down = q[n].finish();
         // lane 4g' + t' holds row g': rows 2t and 2t + 1 are lanes 8t and 8t + 4
         // (never 0: a hidden key's -inf times it has to stay -inf)
         qs[n][0] = fmaxf(__shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2, FLT_MIN);
@@ -668,30 +752,13 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
     }
 
     // Each warp has two stages of its own: the next step is requested when a
-    // step begins.
-    using St = Stage<F16>;
-    const uint32_t ring = smem_u32(smem) + warp * 2 * St::kBytes;
-    const int npg = (S + p.ps - 1) / p.ps;
-    StepWalker<A16, U> wk;
-    const int first = k0 + warp * kStep;
-    wk.start(p, A16 ? first : first + lane, kWarps * kStep);
-    int pg[2] = {-1, -1};
-    if (first < k1) {
-        wk.pages(p, b, npg, pg);
-        St::fill(p, wk.rows(p, kvh, pg), ring, lane);
-        wk.next(p);
-        if (first + kWarps * kStep < k1) wk.pages(p, b, npg, pg);
-    }
-    cp_async_commit();
-    uint32_t st = ring;
-    for (int base = first; base < k1; base += kWarps * kStep) {
+    // step begins, the next segment's first one when a segment's last step ends.
+    for (int base = sg.g0 * kUnit + warp * kStep; base < k1; base += kWarps * kStep) {
         __syncwarp();  // the other stage has been read
         const uint32_t st_next = st == ring ? ring + St::kBytes : ring;
-        if (base + kWarps * kStep < k1) {
-            St::fill(p, wk.rows(p, kvh, pg), st_next, lane);
-            wk.next(p);
-            if (base + 2 * kWarps * kStep < k1) wk.pages(p, b, npg, pg);
-        }
+        St::fill(p, wk.rows(p, kvh, pg), st_next, lane);  // (zeros past the last step: no branch)
+        wk.next(p);
+        wk.pages(table, p, base + 2 * kWarps * kStep < k1 ? npg : 0, pg);
         cp_async_commit();
         cp_async_wait<1>();
         __syncwarp();
@@ -700,10 +767,6 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
         for (int u = 0; u < U; ++u) kk[u].load(st, u, g, t);
         // S^T: 16 U keys x 8 NT rows
         float s[NT][U][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int u = 0; u < U; ++u) s[n][u][0] = s[n][u][1] = s[n][u][2] = s[n][u][3] = 0.f;
         typename Keys::Scales ksc[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) ksc[u] = kk[u].scales();
@@ -717,7 +780,10 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma<F16>(s[n][u], a[j], q[n].hi[2 * i + j][0], q[n].hi[2 * i + j][1]);
+                        if (i == 0 && j == 0)
+                            mma_first<F16>(s[n][u], a[j], q[n].hi[0][0], q[n].hi[0][1]);
+                        else
+                            mma<F16>(s[n][u], a[j], q[n].hi[2 * i + j][0], q[n].hi[2 * i + j][1]);
                         if constexpr (F32) mma<F16>(s[n][u], a[j], q[n].lo[2 * i + j][0], q[n].lo[2 * i + j][1]);
                     }
             }
@@ -755,7 +821,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
             float mt[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                mt[e] = fmaxf(fmaxf(s[n][0][e], s[n][0][2 + e]), fmaxf(s[n][U - 1][e], s[n][U - 1][2 + e])) * qs[n][e];
+                mt[e] = fmax3(fmaxf(s[n][0][e], s[n][0][2 + e]), s[n][U - 1][e], s[n][U - 1][2 + e]) * qs[n][e];
             if (__any_sync(0xffffffffu, mt[0] > m[n][0] + kLazyRescaleLog2 || mt[1] > m[n][1] + kLazyRescaleLog2)) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) {
@@ -830,11 +896,18 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
         }
         st = st_next;
     }
-    cp_async_wait<0>();
-    __syncthreads();  // the stages become the merge buffer
+    const Segment done = sg;
+    pos += sg.n;
+    const bool more = pos < end;
+    if (more) {
+        sg.advance(p, pos, end);
+        cp_async_wait<0>();  // the last step's empty fill of the same stage
+        __syncwarp();
+        open_keys();
+    }
 
     // ---- merge the four warps ---------------------------------------------
-    float* const mw = merge + warp * ROWS * kMerge;
+    float* const mw = merge + warp * mrows * kMerge;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -845,6 +918,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
                 lt += __shfl_xor_sync(0xffffffffu, lt, d);
                 at += __shfl_xor_sync(0xffffffffu, at, d);
             }
+            if (8 * n + 2 * t + e >= mrows) continue;
             float* const mr = mw + (8 * n + 2 * t + e) * kMerge;
             if (g == 0) {
                 mr[kD] = m[n][e];
@@ -856,49 +930,47 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
                 *reinterpret_cast<float4*>(mr + 16 * g + 4 * i) =
                     make_float4(o[n][2 * i][e], o[n][2 * i][2 + e], o[n][2 * i + 1][e], o[n][2 * i + 1][2 + e]);
         }
+    if (more) open_query();
     __syncthreads();
-    const int d = threadIdx.x;  // one dim per thread
-    const bool full = p.whole || n_units == ng;
-    for (int rr = 0; rr < nrows; ++rr) {
-        float M = neg_inf();
+    const bool full = done.n == done.ng;
+    for (int rr = warp; rr < nrows; rr += kWarps) {  // a warp per row, four dims a lane
+        const float* const mr = merge + rr * kMerge;
+        float mv[kWarps], M = neg_inf();
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, merge[(w * ROWS + rr) * kMerge + kD]);
-        float acc = 0.f, at = 0.f, lt = 0.f;
+        for (int w = 0; w < kWarps; ++w) {
+            mv[w] = mr[w * mrows * kMerge + kD];
+            M = fmaxf(M, mv[w]);
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float at = 0.f, lt = 0.f;
         if (M != neg_inf()) {
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float* const mr = merge + (w * ROWS + rr) * kMerge;
-                const float a = fast_exp2(mr[kD] - M);
-                acc += a * mr[d];
-                at += a * mr[kD + 1];
-                lt += a * mr[kD + 2];
+                const float* const mw_ = mr + w * mrows * kMerge;
+                const float a = fast_exp2(mv[w] - M);
+                const float4 x = *reinterpret_cast<const float4*>(mw_ + 4 * lane);
+                acc.x += a * x.x;
+                acc.y += a * x.y;
+                acc.z += a * x.z;
+                acc.w += a * x.w;
+                at += a * mw_[kD + 1];
+                lt += a * mw_[kD + 2];
             }
         }
         if (full) {
-            const long long row = row0 + rr;
-            const float v = at > 0.f ? acc / at : 0.f;
-            if constexpr (F32)
-                static_cast<float*>(p.out)[row * kD + d] = v;
-            else
-                static_cast<uint16_t*>(p.out)[row * kD + d] = float_to_bf16_bits(v);
-            if (d == 0 && p.lse) p.lse[row] = lt > 0.f ? M + log2f(lt) : __int_as_float(0x7f800000);
+            store_row<F32>(p, row0 + rr, lane, acc, at, lt, M);
         } else {
             // a share's segment that began in an earlier one, or its last one
-            const long long row = static_cast<long long>(2 * blockIdx.x + (g0 > 0 ? 0 : 1)) * ROWS + rr;
-            if (d == 0) p.part_ml[row] = make_float4(M, at, lt, 0.f);
-            if (M != neg_inf()) p.part_o[row * kD + d] = acc;
+            const long long row = static_cast<long long>(2 * blockIdx.x + (done.g0 > 0 ? 0 : 1)) * ROWS + rr;
+            if (lane == 0) p.part_ml[row] = make_float4(M, at, lt, 0.f);
+            if (M != neg_inf()) *reinterpret_cast<float4*>(p.part_o + row * kD + 4 * lane) = acc;
         }
     }
-    if (p.whole) return;
-    u += n_units;
-    if (u >= u1) return;
-    if (u == pref + ng * p.H_kv * p.nrc) {  // on to the next sequence with keys
-        pref = u;
-        do S = seq_len(p, ++b, false);
-        while (S == 0);
+    if (!more) break;
+    __syncthreads();  // the merge buffer is free
     }
-    __syncthreads();  // the merge buffer becomes the stages again
-    }
+    cp_async_wait<0>();
+    report_pages(p, wk.bad);
 }
 
 // Merges the pieces of a segment that several shares hold: one CTA per row, its
@@ -908,6 +980,7 @@ template <bool F32>
 __global__ void __launch_bounds__(kWarps * 32) walk_combine_kernel(const WalkParams p, int rows_cta) {
     __shared__ float4 mls[kWarps];
     __shared__ float4 os[kWarps][32];
+    pdl_launch_dependents();
     pdl_wait_primary();
     const int per_seg = min(rows_cta, p.R);
     const int seg = static_cast<int>(blockIdx.x) / per_seg, rr = static_cast<int>(blockIdx.x) - seg * per_seg;
@@ -1039,6 +1112,7 @@ struct TileLoader;
 
 template <>
 struct TileLoader<true> {  // thread: dims 16 grp .. of keys (tid >> 3) + 16 i
+    bool bad = false;
     uint2 c[4][2];
     uint32_t s[4][2];
     __device__ __forceinline__ void request(const WalkParams& p, int b, int kvh, int base, int S, uint32_t, uint32_t) {
@@ -1047,11 +1121,11 @@ struct TileLoader<true> {  // thread: dims 16 grp .. of keys (tid >> 3) + 16 i
         for (int i = 0; i < 4; ++i) {
             const int key = base + static_cast<int>(threadIdx.x >> 3) + 16 * i;
             const int lp = key / p.ps;
-            const int pg = key < S ? page_of(p, b, lp, INT_MAX) : -1;
+            const int pg = key < S ? __ldg(p.bt + static_cast<long long>(b) * p.max_npg + lp) : kNoPage;
+            const long long r = row_in(p, kvh, pg, key - lp * p.ps, bad);
             c[i][0] = c[i][1] = make_uint2(0u, 0u);
             s[i][0] = s[i][1] = 0u;
-            if (pg >= 0) {
-                const long long r = static_cast<long long>(pg * p.H_kv + kvh) * p.ps + (key - lp * p.ps);
+            if (r >= 0) {
                 c[i][0] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.kc) + r * kQ4CodeBytes) + grp);
                 c[i][1] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.vc) + r * kQ4CodeBytes) + grp);
                 s[i][0] = __ldg(static_cast<const uint8_t*>(p.ks) + r * kQ4Groups + grp);
@@ -1084,6 +1158,7 @@ struct TileLoader<true> {  // thread: dims 16 grp .. of keys (tid >> 3) + 16 i
 
 template <>
 struct TileLoader<false> {  // thread: chunk tid & 15 of keys (tid >> 4) + 8 i
+    bool bad = false;
     __device__ __forceinline__ void request(const WalkParams& p, int b, int kvh, int base, int S, uint32_t kbuf,
                                             uint32_t vbuf) {
         const int c = threadIdx.x & 15;
@@ -1091,10 +1166,11 @@ struct TileLoader<false> {  // thread: chunk tid & 15 of keys (tid >> 4) + 8 i
         for (int i = 0; i < 8; ++i) {
             const int row = static_cast<int>(threadIdx.x >> 4) + 8 * i, key = base + row;
             const int lp = key / p.ps;
-            const int pg = key < S ? page_of(p, b, lp, INT_MAX) : -1;
-            const long long r = pg >= 0 ? static_cast<long long>(pg * p.H_kv + kvh) * p.ps + (key - lp * p.ps) : 0;
-            cp_async16(kbuf + chunk_at(row, c), static_cast<const uint8_t*>(p.kc) + r * (2 * kD) + 16 * c, pg >= 0);
-            cp_async16(vbuf + chunk_at(row, c), static_cast<const uint8_t*>(p.vc) + r * (2 * kD) + 16 * c, pg >= 0);
+            const int pg = key < S ? __ldg(p.bt + static_cast<long long>(b) * p.max_npg + lp) : kNoPage;
+            const int r = row_in(p, kvh, pg, key - lp * p.ps, bad);
+            const long long off = r >= 0 ? static_cast<long long>(r) * (2 * kD) + 16 * c : 0;
+            cp_async16(kbuf + chunk_at(row, c), static_cast<const uint8_t*>(p.kc) + off, r >= 0);
+            cp_async16(vbuf + chunk_at(row, c), static_cast<const uint8_t*>(p.vc) + off, r >= 0);
         }
         cp_async_commit();
     }
@@ -1271,6 +1347,7 @@ __global__ void __launch_bounds__(kWarps * 32) block_kernel(const WalkParams p) 
         }
         if (more) ld.finish(kn, vn);
     }
+    report_pages(p, ld.bad);
     // rows g and g + 8: dims 8 d + 2t, + 1
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -1363,7 +1440,7 @@ __global__ void __launch_bounds__(kWarps * 32) walk_weights_kernel(const WalkPar
             StepWalker<false, 2> wk;
             wk.start(p, k0 + lane, 0);
             int pg[2];
-            wk.pages(p, b, k0 + lane < S ? INT_MAX : 0, pg);
+            wk.pages(p.bt + static_cast<long long>(b) * p.max_npg, p, k0 + lane < S ? INT_MAX : 0, pg);
             const StepRows<false, 2> rows = wk.rows(p, kvh, pg);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -1488,7 +1565,9 @@ WalkPlan plan(const pa_shape& sh, bool q4, bool weights, int sm_count) {
     w.C = 0;
     size_t slots = 0;  // rows of partial states
     if (w.nt) {
-        w.items = w.whole ? segs : static_cast<long long>(sm_count) * resident_ctas(w.nt, q4, f32);
+        int resident = resident_ctas(w.nt, q4, f32);
+        if (!q4 && w.nt == 1 && w.R > 4) resident = 2;  // (shared memory: 16 KB stages per warp)
+        w.items = w.whole ? segs : static_cast<long long>(sm_count) * resident;
         if (!w.whole) slots = static_cast<size_t>(w.items) * 2 * rows_cta;
     } else {
         long long nkc = (4ll * sm_count + segs - 1) / segs;
@@ -1533,17 +1612,14 @@ bool launch_dependent(void (*kernel)(P...), long long grid, int threads, cudaStr
 
 // The attention, its merge over key chunks, then the key weights.
 template <class Keys, class Values, int NT, bool F32, bool A16, bool W>
-pa_status launch_walk(const WalkParams& p, long long items, [[maybe_unused]] int device, cudaStream_t stream) {
-    constexpr size_t ring = kWarps * 2 * Stage<Keys::kF16>::kBytes, merge = sizeof(float) * kWarps * 8 * NT * kMerge;
-    constexpr size_t smem = ring > merge ? ring : merge;
-    if constexpr (smem > 48 * 1024) {
-        static int attr_done[64] = {0};
-        if (!attr_done[device]) {
-            if (cudaFuncSetAttribute(walk_kernel<Keys, Values, NT, F32, A16, W>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-                return PA_ERR_CUDA;
-            attr_done[device] = 1;
-        }
+pa_status launch_walk(const WalkParams& p, long long items, int device, cudaStream_t stream) {
+    const size_t smem = walk_smem(Keys::kF16, p.R < 8 * NT ? p.R : 8 * NT);
+    static int attr_done[64] = {0};
+    if (!attr_done[device]) {
+        if (cudaFuncSetAttribute(walk_kernel<Keys, Values, NT, F32, A16, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 walk_smem(Keys::kF16, 8 * NT)) != cudaSuccess)
+            return PA_ERR_CUDA;
+        attr_done[device] = 1;
     }
     walk_kernel<Keys, Values, NT, F32, A16, W><<<static_cast<unsigned>(items), kWarps * 32, smem, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
