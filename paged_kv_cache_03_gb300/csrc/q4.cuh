@@ -94,4 +94,14 @@ __device__ __forceinline__ void mma_16816_bf16_first(float (&d)[4], const uint32
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// The power of two that takes a row with largest magnitude mx into f16's range
+// (mx into [2^14, 2^15)), and its inverse.  Rows with an inf or NaN stay as they
+// are; the exponent is cut so that both factors are normal numbers.
+__device__ __forceinline__ void f16_scale(float mx, float& up, float& down) {
+    const int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;  // -127: zero or subnormal
+    const int k = e >= 128 ? 0 : min(14 - e, 126);
+    up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+    down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+}
+
 }  // namespace pa

@@ -505,10 +505,8 @@ struct QueryFrags {
         for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;  // -127: zero or subnormal
-        const int k2 = e >= 128 ? 0 : min(14 - e, 126);                   // inf or NaN: as they are
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23);
+        float up, down;
+        f16_scale(mx, up, down);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             const float x = f[k].x * up, y = f[k].y * up;
@@ -1649,6 +1647,20 @@ pa_status launch_block(const WalkParams& p, long long items, int device, cudaStr
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// The key weights from the rows' log-sum-exp.
+pa_status launch_weights(const WalkParams& p, bool q4, bool f32, cudaStream_t stream) {
+    const long long bk = static_cast<long long>(p.B) * p.H_kv, ntile = (p.w_S + 32 * kWarps - 1) / (32 * kWarps);
+    if (ntile * bk > INT_MAX) return PA_ERR_UNSUPPORTED;
+    const unsigned grid = static_cast<unsigned>(ntile * bk);
+    if (!q4)
+        walk_weights_kernel<BfKeys, false><<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(ntile));
+    else if (f32)
+        walk_weights_kernel<Q4Keys, true><<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(ntile));
+    else
+        walk_weights_kernel<Q4Keys, false><<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(ntile));
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, int device, cudaStream_t stream) {
     const long long bk = static_cast<long long>(p.B) * p.H_kv;
     const long long items = w.items, rows = bk * p.R;
@@ -1680,35 +1692,36 @@ pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, int 
     }
     if (!p.w_out) return PA_OK;
     if (w.scores) return launch_dependent(walk_sum_kernel, ntile * bk, 256, stream, p, static_cast<int>(ntile)) ? PA_OK : PA_ERR_CUDA;
-    const unsigned grid = static_cast<unsigned>(ntile * bk);
-    if (!q4)
-        walk_weights_kernel<BfKeys, false><<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(ntile));
-    else if (f32)
-        walk_weights_kernel<Q4Keys, true><<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(ntile));
-    else
-        walk_weights_kernel<Q4Keys, false><<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(ntile));
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launch_weights(p, q4, f32, stream);
 }
 
-// ---- many rows over 4-bit pages: dense bf16 copies and the tensor-core tiles --
-// (exact: a 4-bit value is a bf16 number).  Sequences go in groups whose
-// copies fit kDenseBytes.
-// Rows per kv head from which the tiles take a call.  Measured (walk, tiles, us;
-// G = 4, H_kv = 8): B = 8 over 1000 .. 8000 keys 61, 96 at 32 rows, 91, 96 at 64,
-// 123, 97 at 96; B = 1 over 16000 keys 41, 41 at 16, 57, 41 at 32; B = 64 over 500
-// .. 2000 keys 111, 166 at 32, 169, 166 at 64.
+// Rows per kv head from which bf16 queries over 4-bit pages go to the tensor-core
+// tiles of q4_tiles.cu.
 constexpr int kTileRows = 48;
+
+bool tiles_take(const pa_shape& sh, bool q4, int sm_count) {
+    return q4 && sh.dtype == PA_BF16 && static_cast<long long>(sh.H_q / sh.H_kv) * sh.L >= kTileRows &&
+           q4_tiles_supported(sh, sm_count);
+}
+
+// ---- whole prompts over 4-bit pages: bf16 copies and the bf16 tile kernel -------
+// (exact: a 4-bit value is a bf16 number).  Where a kv head has half as many rows as
+// keys or more, the copies cost less than what q4_tiles.cu spends per segment
+// (G = 4, H_kv = 8, us, tiles against copies: 4 x 2048 rows over 600 keys 46, 38; 4 x
+// 8192 over 2048 198, 145; 8 x 2080 over 1000 .. 8000 352, 382; 8 x 1040 209, 247; 1 x
+// 8192 over 16000 436, 444).  Sequences go in groups whose copies fit kDenseBytes.
 constexpr size_t kDenseBytes = size_t(1) << 30;
 
-struct TilePlan {
+struct DensePlan {
     pa_shape sh;  // one group, over the dense copies
     size_t id_off, k_off, v_off, total;  // id: block table, then lengths
 };
 
-bool tiles_take(const pa_shape& sh, bool q4, bool weights, int sm_count, TilePlan* t) {
+bool dense_take(const pa_shape& sh, bool q4, bool weights, int sm_count, DensePlan* t) {
     if (!q4 || weights || sh.dtype != PA_BF16) return false;
-    if (static_cast<long long>(sh.H_q / sh.H_kv) * sh.L < kTileRows) return false;
     const long long cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
+    const long long R = static_cast<long long>(sh.H_q / sh.H_kv) * sh.L;
+    if (R < kTileRows || 2 * R < cap) return false;
     const long long slots = (cap + 127) / 128 * 128;
     const size_t per_seq = static_cast<size_t>(slots) * sh.H_kv * kD * 2 * 2;
     if (slots * sh.H_kv >= (1ll << 31)) return false;
@@ -1733,7 +1746,7 @@ bool tiles_take(const pa_shape& sh, bool q4, bool weights, int sm_count, TilePla
     return true;
 }
 
-pa_status tiles_launch(const WalkCall& c, const TilePlan& t) {
+pa_status dense_launch(const WalkCall& c, const DensePlan& t) {
     const pa_shape& sh = c.sh;
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
     const pa_q4_pool pool = {const_cast<void*>(c.kc), const_cast<void*>(c.ks), const_cast<void*>(c.vc),
@@ -1772,20 +1785,20 @@ pa_status tiles_launch(const WalkCall& c, const TilePlan& t) {
 }  // namespace
 
 size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_count) {
-    TilePlan t;
-    if (tiles_take(sh, q4, weights, sm_count, &t)) return t.total;
+    DensePlan d;
+    if (dense_take(sh, q4, weights, sm_count, &d)) return d.total;
+    if (tiles_take(sh, q4, sm_count)) {
+        const size_t n = align_up(q4_tiles_workspace_bytes(sh, sm_count), 256);
+        return n + (weights ? static_cast<size_t>(sh.B) * sh.H_q * sh.L * 4 : 0);
+    }
     return plan(sh, q4, weights, sm_count).total;
 }
 
 pa_status walk_launch(const WalkCall& c) {
     const pa_shape& sh = c.sh;
-    TilePlan t;
-    if (tiles_take(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count, &t)) {
-        if (c.ws_bytes < t.total) return PA_ERR_WORKSPACE;
-        return tiles_launch(c, t);
-    }
+    const bool tiles = tiles_take(sh, c.ks != nullptr, c.dev.sm_count);
     const WalkPlan w = plan(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count);
-    if (c.ws_bytes < w.total) return PA_ERR_WORKSPACE;
+    if (c.ws_bytes < walk_workspace_bytes(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count)) return PA_ERR_WORKSPACE;
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
     WalkParams p;
     p.q = c.q;
@@ -1821,6 +1834,14 @@ pa_status walk_launch(const WalkCall& c) {
     p.scale_log2 = c.scale * 1.4426950408889634f;
     p.score = w.scores ? reinterpret_cast<float*>(ws + w.score_off) : nullptr;
     p.cap = p.max_S;
+    DensePlan d;
+    if (dense_take(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count, &d)) return dense_launch(c, d);
+    if (tiles) {
+        if (c.w_out)
+            p.lse = reinterpret_cast<float*>(ws + align_up(q4_tiles_workspace_bytes(sh, c.dev.sm_count), 256));
+        const pa_status st = q4_tiles_launch(c, p.lse);
+        return st != PA_OK || !c.w_out ? st : launch_weights(p, true, false, c.stream);
+    }
     return launch(p, w, c.ks != nullptr, sh.dtype == PA_F32, c.dev.device, c.stream);
 }
 

@@ -129,6 +129,22 @@ CASES = [
     Case(1, 2, 1, 1, 16, [4000], spare=200),
 ]
 CASES += [Case(**{**c.__dict__, "dtype": "f32"}) for c in CASES]
+# many rows per kv head: whole and short last tiles, group sizes that do not
+# divide a tile, contexts that cross every SM's share, many short sequences
+CASES += [
+    Case(1, 1, 1, 300, 16, [300]),
+    Case(2, 7, 1, 130, 16, [130, 513]),
+    Case(1, 48, 1, 3, 64, [260]),
+    Case(1, 128, 1, 1, 16, [390]),
+    Case(1, 100, 1, 5, 16, [129]),
+    Case(1, 4, 2, 16, 128, [3900], spare=4),
+    Case(2, 4, 1, 97, 16, [2000, 97]),
+    Case(1, 8, 1, 33, 8, [3000]),
+    Case(40, 4, 2, 65, 16, [65 + 7 * i for i in range(40)]),
+    Case(2, 4, 1, 66, 16, [66, 200]),
+    Case(2, 4, 2, 129, 24, [100, 40], causal=False),
+    Case(2, 3, 1, 43, 1, [43, 140]),
+]
 
 
 @pytest.mark.parametrize("c", CASES, ids=str)
