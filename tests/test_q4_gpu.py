@@ -137,6 +137,7 @@ CASES += [
     Case(1, 48, 1, 3, 64, [260]),
     Case(1, 128, 1, 1, 16, [390]),
     Case(1, 100, 1, 5, 16, [129]),
+    Case(1, 130, 1, 1, 16, [100]),
     Case(1, 4, 2, 16, 128, [3900], spare=4),
     Case(2, 4, 1, 97, 16, [2000, 97]),
     Case(1, 8, 1, 33, 8, [3000]),
