@@ -56,23 +56,23 @@ WalkPlan plan(const pa_shape& sh, bool q4, bool weights, int sm_count) {
     w.lse_off = off;
     if (weights) off = align_up(off + rows * 4, 256);
     w.score_off = off;
-    if (weights) off = align_up(off + (w.scores ? rows * cap * 4 : weights_scratch_bytes(sh)), 256);
+    if (weights) off = align_up(off + (w.scores ? rows * cap * 4 : weights_scratch_bytes(sh, sm_count)), 256);
     w.total = off;
     return w;
 }
 
 // The attention, its merge over shares, then the key weights.
-pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, int device, void* scratch,
+pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, const DeviceInfo& dev, void* scratch,
                  cudaStream_t stream) {
     const long long bk = static_cast<long long>(p.B) * p.H_kv;
     if (w.items > INT_MAX || bk * p.R > INT_MAX) return PA_ERR_UNSUPPORTED;
     // the shares count costs in an int
     if (!w.whole && bk * p.nrc * (p.max_S / kUnit + 1 + kSegCost) > INT_MAX / 2) return PA_ERR_UNSUPPORTED;
-    const WalkLaunch l = {w.nt, q4, f32, w.items, device, stream};
+    const WalkLaunch l = {w.nt, q4, f32, w.items, dev.device, stream};
     pa_status st = w.nt ? walk_attend(p, l) : block_attend(p, l);
     if (st == PA_OK && !w.whole) st = merge_shares(p, w.rows_cta, static_cast<int>(w.items), f32, stream);
     if (st != PA_OK || !p.w_out) return st;
-    return w.scores ? weights_from_scores(p, stream) : weights_from_keys(p, q4, f32, scratch, stream);
+    return w.scores ? weights_from_scores(p, stream) : weights_from_keys(p, q4, f32, scratch, dev.sm_count, stream);
 }
 
 // Rows per kv head from which bf16 queries over 4-bit pages go to the tensor-core
@@ -176,7 +176,7 @@ size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_co
     if (dense_take(sh, q4, weights, sm_count, &d)) return d.total;
     if (tiles_take(sh, q4, sm_count)) {
         const size_t n = align_up(q4_tiles_workspace_bytes(sh, sm_count), 256);
-        return weights ? tiles_scratch(sh, sm_count) + weights_scratch_bytes(sh) : n;
+        return weights ? tiles_scratch(sh, sm_count) + weights_scratch_bytes(sh, sm_count) : n;
     }
     return plan(sh, q4, weights, sm_count).total;
 }
@@ -226,9 +226,9 @@ pa_status walk_launch(const WalkCall& c) {
         if (c.w_out)
             p.lse = reinterpret_cast<float*>(ws + align_up(q4_tiles_workspace_bytes(sh, c.dev.sm_count), 256));
         const pa_status st = q4_tiles_launch(c, p.lse);
-        return st != PA_OK || !c.w_out ? st : weights_from_keys(p, true, false, scratch, c.stream);
+        return st != PA_OK || !c.w_out ? st : weights_from_keys(p, true, false, scratch, c.dev.sm_count, c.stream);
     }
-    return launch(p, w, c.ks != nullptr, sh.dtype == PA_F32, c.dev.device, ws + w.score_off, c.stream);
+    return launch(p, w, c.ks != nullptr, sh.dtype == PA_F32, c.dev, ws + w.score_off, c.stream);
 }
 
 }  // namespace pa

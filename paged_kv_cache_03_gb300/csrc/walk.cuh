@@ -688,8 +688,8 @@ pa_status merge_shares(const WalkParams& p, int rows_cta, int shares, bool f32, 
 // weights.cu: key weights from stored scores, or from the query, the keys and
 // the rows' log-sum-exp (scratch: weights_scratch_bytes, 16-byte aligned).
 pa_status weights_from_scores(const WalkParams& p, cudaStream_t stream);
-size_t weights_scratch_bytes(const pa_shape& sh);
-pa_status weights_from_keys(const WalkParams& p, bool q4, bool f32, void* scratch, cudaStream_t stream);
+size_t weights_scratch_bytes(const pa_shape& sh, int sm_count);
+pa_status weights_from_keys(const WalkParams& p, bool q4, bool f32, void* scratch, int sm_count, cudaStream_t stream);
 
 }  // namespace walk
 }  // namespace pa
