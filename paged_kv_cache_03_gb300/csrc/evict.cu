@@ -13,11 +13,11 @@
 #include <climits>
 
 #include "cache.h"
+#include "ptx.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kCached = 49152;  // keys held in shared memory (192 KB)
 
@@ -53,13 +53,20 @@ __device__ __forceinline__ int warp_incl(int v, int lane) {
     return v;
 }
 
-template <bool kCache>
+// The sum of v[0 .. n), n < 32, by a whole warp.
+__device__ __forceinline__ int warp_sum_before(const int* v, int n, int lane) {
+    return __reduce_add_sync(0xffffffffu, lane < n ? v[lane] : 0);
+}
+
+template <int kThreads, bool kCache>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p) {
+    constexpr int kWarps = kThreads / 32, kMine = kBins / kThreads;  // kMine: bins per thread
     __shared__ int hist[kBins];
     __shared__ int warp_a[kWarps], warp_b[kWarps];
     __shared__ int sel[2];
     extern __shared__ uint32_t cache[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
     const int b = static_cast<int>(blockIdx.x) / p.H_kv, kvh = static_cast<int>(blockIdx.x) % p.H_kv;
     int S = __ldg(p.ctx + b);
     if (S < 0 || static_cast<long long>(S) > p.max_S) {
@@ -94,7 +101,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t mask = pass == 2 ? 1023u : 2047u;
-        hist[tid] = hist[tid + kThreads] = 0;
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) hist[tid + k * kThreads] = 0;
         __syncthreads();
         const int above = pass == 1 ? 21 : 10;  // bits of T already known
 #pragma unroll 4
@@ -109,19 +117,24 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
             if (pass == 0 || (key >> above) == (T >> above)) atomicAdd(&hist[(key >> shift) & mask], 1);
         }
         __syncthreads();
-        // the bin that holds the left-th largest: thread tid has bins 2 tid' and
-        // 2 tid' + 1 from the top
-        const int top = kBins - 1 - 2 * tid;
-        const int c0 = hist[top], c1 = hist[top - 1];
-        const int incl = warp_incl(c0 + c1, lane);
+        // the bin that holds the left-th largest: thread tid has kMine bins, from the top
+        const int top = kBins - 1 - kMine * tid;
+        int c[kMine], own = 0;
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) own += c[k] = hist[top - k];
+        const int incl = warp_incl(own, lane);
         if (lane == 31) warp_a[warp] = incl;
         __syncthreads();
-        int before = incl - c0 - c1;
-        for (int v = 0; v < warp; ++v) before += warp_a[v];
-        if (before < left && left <= before + c0 + c1) {
-            const bool first = left <= before + c0;
-            sel[0] = first ? top : top - 1;
-            sel[1] = first ? before : before + c0;
+        int before = incl - own + warp_sum_before(warp_a, warp, lane);
+        if (before < left && left <= before + own) {
+#pragma unroll
+            for (int k = 0; k < kMine; ++k) {
+                if (before < left && left <= before + c[k]) {
+                    sel[0] = top - k;
+                    sel[1] = before;
+                }
+                before += c[k];
+            }
         }
         __syncthreads();
         T |= static_cast<uint32_t>(sel[0]) << shift;
@@ -134,7 +147,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     const int run = ((cand + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int i0 = warp * run, i1 = min(cand, i0 + run);
     int gt = 0, eq = 0;
-    for (int i = i0 + lane; i < i0 + run && __any_sync(0xffffffffu, i < i1); i += 32) {
+#pragma unroll 4
+    for (int i = i0 + lane; i - lane < i1; i += 32) {
         const uint32_t key = i < i1 ? key_at(i) : 0u;
         gt += __popc(__ballot_sync(0xffffffffu, i < i1 && key > T));
         eq += __popc(__ballot_sync(0xffffffffu, i < i1 && key == T));
@@ -144,21 +158,20 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
         warp_b[warp] = eq;
     }
     __syncthreads();
-    gt = eq = 0;
-    for (int v = 0; v < warp; ++v) {
-        gt += warp_a[v];
-        eq += warp_b[v];
-    }
+    gt = warp_sum_before(warp_a, warp, lane);
+    eq = warp_sum_before(warp_b, warp, lane);
     const uint32_t lower = (1u << lane) - 1;
-    for (int i = i0 + lane; i < i0 + run && __any_sync(0xffffffffu, i < i1); i += 32) {
+#pragma unroll 4
+    for (int i = i0 + lane; i - lane < i1; i += 32) {
         const uint32_t key = i < i1 ? key_at(i) : 0u;
+        const float wi = i < i1 ? __ldg(w + i) : 0.f;
         const uint32_t g = __ballot_sync(0xffffffffu, i < i1 && key > T);
         const uint32_t e = __ballot_sync(0xffffffffu, i < i1 && key == T);
         const int eqb = eq + __popc(e & lower);
         if (((g >> lane) & 1u) || (((e >> lane) & 1u) && eqb < left)) {
             const int dst = gt + __popc(g & lower) + min(eqb, left);
             kept[dst] = i;
-            w_out[dst] = w[i];
+            w_out[dst] = wi;
         }
         gt += __popc(g);
         eq += __popc(e);
@@ -183,6 +196,7 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const CopyParams p) {
     const int tile = static_cast<int>(blockIdx.x) % p.ntile, bk = static_cast<int>(blockIdx.x) / p.ntile;
     const int b = bk / p.H_kv, kvh = bk - b * p.H_kv;
     const int j0 = tile * ROWS;
+    pdl_wait_primary();
     for (int i = threadIdx.x; i < ROWS; i += 256) {
         const int j = j0 + i;
         const int s = j < p.keep ? __ldg(p.kept + static_cast<long long>(bk) * p.keep + j) : -1;
@@ -234,7 +248,24 @@ template <int ROWS, int RB, int SB>
 pa_status launch_copy(CopyParams& q, long long bk, cudaStream_t stream) {
     q.ntile = (q.keep + ROWS - 1) / ROWS;
     if (bk * q.ntile > INT_MAX) return PA_ERR_UNSUPPORTED;
-    evict_copy_kernel<ROWS, RB, SB><<<static_cast<unsigned>(bk * q.ntile), 256, 0, stream>>>(q);
+    return launch_dependent(evict_copy_kernel<ROWS, RB, SB>, dim3(static_cast<unsigned>(bk * q.ntile)), 256, stream, q)
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+template <int kThreads, bool kCache>
+pa_status launch_select(const EvictParams& p, long long heads, const EvictCall& c) {
+    const size_t smem = kCache ? static_cast<size_t>(p.max_S) * 4 : 0;
+    if (kCache) {
+        static int attr_done[64] = {0};
+        if (!attr_done[c.dev.device]) {
+            if (cudaFuncSetAttribute(evict_select_kernel<kThreads, kCache>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kCached * 4) != cudaSuccess)
+                return PA_ERR_CUDA;
+            attr_done[c.dev.device] = 1;
+        }
+    }
+    evict_select_kernel<kThreads, kCache><<<static_cast<unsigned>(heads), kThreads, smem, c.stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -258,19 +289,17 @@ pa_status evict_launch(const EvictCall& c) {
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     const long long bk = static_cast<long long>(sh.B) * sh.H_kv;
     if (bk * ((c.keep + 15ll) / 16) > INT_MAX) return PA_ERR_UNSUPPORTED;
-    if (p.max_S <= kCached) {
-        static int attr_done[64] = {0};
-        if (!attr_done[c.dev.device]) {
-            if (cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kCached * 4) != cudaSuccess)
-                return PA_ERR_CUDA;
-            attr_done[c.dev.device] = 1;
-        }
-        evict_select_kernel<true><<<static_cast<unsigned>(bk), kThreads, static_cast<size_t>(p.max_S) * 4, c.stream>>>(p);
-    } else {
-        evict_select_kernel<false><<<static_cast<unsigned>(bk), kThreads, 0, c.stream>>>(p);
-    }
-    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+    // 1024 threads, or 512 where the heads are more than are resident with 1024 (1024,
+    // 512, us for select and copy and read-back: 512 heads of 4096 keys 77, 73, of
+    // about 1000 62, 59; 64 heads of 4096 24, 26; 16 of 32768 54, 73).
+    pa_status st;
+    if (p.max_S > kCached)
+        st = launch_select<1024, false>(p, bk, c);
+    else if (bk > 2ll * c.dev.sm_count)
+        st = launch_select<512, true>(p, bk, c);
+    else
+        st = launch_select<1024, true>(p, bk, c);
+    if (st != PA_OK) return st;
     CopyParams q;
     for (int k = 0; k < 4; ++k) q.buf[k] = static_cast<uint8_t*>(c.buf[k]);
     q.bt = c.bt;

@@ -654,21 +654,6 @@ __device__ __forceinline__ void store_row(const WalkParams& p, long long row, in
     if (lane == 0 && p.lse) p.lse[row] = lt > 0.f ? M + log2f(lt) : __int_as_float(0x7f800000);
 }
 
-// Launches `kernel`, whose start may overlap the end of the kernel before it.
-template <class... P, class... A>
-inline bool launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
-}
-
 // walk.cu: up to 8 nt rows per CTA (nt = 1, 2; bf16 pages or codes)
 struct WalkLaunch {
     int nt;
