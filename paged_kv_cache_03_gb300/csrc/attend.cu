@@ -72,7 +72,7 @@ pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, cons
     pa_status st = w.nt ? walk_attend(p, l) : block_attend(p, l);
     if (st == PA_OK && !w.whole) st = merge_shares(p, w.rows_cta, static_cast<int>(w.items), f32, stream);
     if (st != PA_OK || !p.w_out) return st;
-    return w.scores ? weights_from_scores(p, stream) : weights_from_keys(p, q4, f32, scratch, dev.sm_count, stream);
+    return w.scores ? weights_from_scores(p, stream) : weights_from_keys(p, q4, f32, scratch, dev, stream);
 }
 
 // Rows per kv head from which bf16 queries over 4-bit pages go to the tensor-core
@@ -226,7 +226,7 @@ pa_status walk_launch(const WalkCall& c) {
         if (c.w_out)
             p.lse = reinterpret_cast<float*>(ws + align_up(q4_tiles_workspace_bytes(sh, c.dev.sm_count), 256));
         const pa_status st = q4_tiles_launch(c, p.lse);
-        return st != PA_OK || !c.w_out ? st : weights_from_keys(p, true, false, scratch, c.dev.sm_count, c.stream);
+        return st != PA_OK || !c.w_out ? st : weights_from_keys(p, true, false, scratch, c.dev, c.stream);
     }
     return launch(p, w, c.ks != nullptr, sh.dtype == PA_F32, c.dev, ws + w.score_off, c.stream);
 }

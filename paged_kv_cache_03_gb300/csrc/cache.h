@@ -79,10 +79,11 @@ pa_status evict_launch(const EvictCall& c);
 
 // Launches `kernel`, whose start may overlap the end of the kernel before it.
 template <class... P, class... A>
-inline bool launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+inline bool launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -248,7 +248,7 @@ template <int ROWS, int RB, int SB>
 pa_status launch_copy(CopyParams& q, long long bk, cudaStream_t stream) {
     q.ntile = (q.keep + ROWS - 1) / ROWS;
     if (bk * q.ntile > INT_MAX) return PA_ERR_UNSUPPORTED;
-    return launch_dependent(evict_copy_kernel<ROWS, RB, SB>, dim3(static_cast<unsigned>(bk * q.ntile)), 256, stream, q)
+    return launch_dependent(evict_copy_kernel<ROWS, RB, SB>, dim3(static_cast<unsigned>(bk * q.ntile)), 256, 0, stream, q)
                ? PA_OK
                : PA_ERR_CUDA;
 }

@@ -33,7 +33,7 @@
 
 #include "cache.h"
 #include "ptx.cuh"
-#include "q4.cuh"
+#include "q4_stage.cuh"
 #include "tc.cuh"
 
 namespace pa {
@@ -47,7 +47,7 @@ constexpr float kLazyRescaleLog2 = 8.0f;
 // What a segment's query load, first softmax and epilogue cost, in key tiles: the
 // shares count it, or CTAs with many short segments would finish last.
 constexpr int kSegCost = 3;
-constexpr int kHalf = BM * 128;      // 128 rows x 64 f16 (one swizzled column block)
+constexpr int kHalf = kStageHalf;    // 128 rows x 64 f16 (one swizzled column block)
 constexpr int kTile = 2 * kHalf;
 constexpr int kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffBar = 6 * kTile;
 enum Bar {
@@ -195,66 +195,6 @@ template <int N>
 __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-
-// 16-byte chunk c (of 8) of row r in a 64-dim half, 128-byte swizzle.
-__device__ __forceinline__ uint32_t sw128(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
-
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
-// 16 bytes and a 16-bit word, or zeros.  Volatile: the requests stay where they
-// are issued, a tile before their use, whatever the register pressure.
-__device__ __forceinline__ void ldg_or_zero(const void* a, const void* b, bool ok, uint4& x, uint32_t& y) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b16 h;\n\tsetp.ne.b32 p, %7, 0;\n\t"
-        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\tmov.b16 h, 0;\n\t"
-        "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%5];\n\t@p ld.global.nc.b16 h, [%6];\n\t"
-        "cvt.u32.u16 %4, h;\n\t}"
-        : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w), "=&r"(y)
-        : "l"(a), "l"(b), "r"(static_cast<int>(ok)));
-}
-
-// A producer thread's part of one operand's tile: 32 dims (16 code bytes and two
-// scales) of four rows.  Lane bits: 0 and 3 the 32-dim quarter (bit 3 its 64-dim
-// half), 1, 2 and 4 the row; row i of warp w is 32 i + 8 w + the lane's.  So eight
-// neighbouring lanes store to eight different chunk positions (no bank conflict),
-// and a warp reads whole code rows.
-struct RawTile {
-    uint4 c[4];
-    uint32_t s[4];
-    __device__ static int row_of(int lane) { return ((lane >> 1) & 3) | ((lane >> 4) << 2); }
-    __device__ static int quarter(int lane) { return (lane & 1) | ((lane >> 2) & 2); }
-    // rows: lane 8 i + r holds the pool row of row 32 i + 8 w + r, -1: zeros
-    __device__ __forceinline__ void request(const uint8_t* codes, const uint8_t* scales, int rows, int lane) {
-        const int q = quarter(lane), rl = row_of(lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = __shfl_sync(0xffffffffu, rows, 8 * i + rl);
-            ldg_or_zero(codes + static_cast<long long>(row) * kQ4CodeBytes + 16 * q,
-                        scales + static_cast<long long>(row) * kQ4Groups + 2 * q, row >= 0, c[i], s[i]);
-        }
-    }
-    __device__ __forceinline__ void store(uint32_t tile, int warp, int lane) const {
-        const int q = quarter(lane), rl = row_of(lane);
-        const uint32_t base = tile + (q >> 1) * kHalf + (8 * warp + rl) * 128;
-        const uint32_t x0 = ((4 * (q & 1)) ^ rl) << 4;  // chunk 4 (q & 1) + j sits at x0 ^ (j << 4)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-            const uint32_t s2 = e4m3x2_to_f16x2(s[i]);
-            const uint32_t sc[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t v[4];
-                e2m1x8_to_f16x2(w[j], v);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = hmul2(v[k], sc[j >> 1]);
-                sts128(base + (x0 ^ (j << 4)) + i * 4096, v[0], v[1], v[2], v[3]);
-            }
-        }
-    }
-};
 
 __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -418,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p
                     ok = false;
                     break;
                 }
-                rk.store(base + kOffK + s * kTile, warp, lane);
+                rk.store<false>(base + kOffK + s * kTile, warp, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kKFull + s));
@@ -431,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p
                     break;
                 }
                 if (aborted(abort_flag)) break;
-                rv.store(base + kOffV + s * kTile, warp, lane);
+                rv.store<false>(base + kOffV + s * kTile, warp, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kVFull + s));

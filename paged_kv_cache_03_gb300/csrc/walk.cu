@@ -476,7 +476,7 @@ pa_status merge_shares(const WalkParams& p, int rows_cta, int shares, bool f32, 
     const dim3 grid(static_cast<unsigned>(shares), static_cast<unsigned>((rows + n - 1) / n));
     auto* const kernel = n == 1 ? (f32 ? merge_kernel<true, 1, 4> : merge_kernel<false, 1, 4>)
                                 : (f32 ? merge_kernel<true, 4, 1> : merge_kernel<false, 4, 1>);
-    return launch_dependent(kernel, grid, kWarps * 32, stream, p, rows_cta) ? PA_OK : PA_ERR_CUDA;
+    return launch_dependent(kernel, grid, kWarps * 32, 0, stream, p, rows_cta) ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace walk

@@ -120,6 +120,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool o
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -674,7 +677,20 @@ pa_status merge_shares(const WalkParams& p, int rows_cta, int shares, bool f32, 
 // the rows' log-sum-exp (scratch: weights_scratch_bytes, 16-byte aligned).
 pa_status weights_from_scores(const WalkParams& p, cudaStream_t stream);
 size_t weights_scratch_bytes(const pa_shape& sh, int sm_count);
-pa_status weights_from_keys(const WalkParams& p, bool q4, bool f32, void* scratch, int sm_count, cudaStream_t stream);
+pa_status weights_from_keys(const WalkParams& p, bool q4, bool f32, void* scratch, const DeviceInfo& dev,
+                            cudaStream_t stream);
+// The query rows of a (sequence, kv head) cut into n runs, each CTA taking one; n > 1:
+// their sums in part, [run][(b, kvh)][key < max_S].
+struct RowSplits {
+    float* part;
+    int n;
+    __device__ __forceinline__ float* at(const WalkParams& p, int run, int bk) const {
+        return part + (static_cast<long long>(run) * p.B * p.H_kv + bk) * p.max_S;
+    }
+};
+// weights_tiles.cu: the same for bf16 queries on tcgen05 (n up to ceil(R / 64))
+pa_status weights_on_tiles(const WalkParams& p, bool q4, const RowSplits& sp, const DeviceInfo& dev,
+                           cudaStream_t stream);
 
 }  // namespace walk
 }  // namespace pa
