@@ -76,19 +76,19 @@ pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, cons
 }
 
 // Rows per kv head from which bf16 queries over 4-bit pages go to the tensor-core
-// tiles of q4_tiles.cu.  Measured (walk, block, tiles, us; G = 4, H_kv = 8): B = 8 over
+// tiles of tiles.cu.  Measured (walk, block, tiles, us; G = 4, H_kv = 8): B = 8 over
 // 1000 .. 8000 keys 54, 50, 55 at 48 rows, 65, 53, 55 at 64, 89, 87, 55 at 96; B = 1 over
 // 16000 keys 52, 49, 46 at 128; B = 64 over 500 .. 2000 keys 152, 109, 114 at 64.
 constexpr int kTileRows = 64;
 
-bool tiles_take(const pa_shape& sh, bool q4, int sm_count) {
-    return q4 && sh.dtype == PA_BF16 && static_cast<long long>(sh.H_q / sh.H_kv) * sh.L >= kTileRows &&
-           q4_tiles_supported(sh, sm_count);
+bool tiles_take(const pa_shape& sh, int sm_count) {
+    return sh.dtype == PA_BF16 && static_cast<long long>(sh.H_q / sh.H_kv) * sh.L >= kTileRows &&
+           tiles_supported(sh, sm_count);
 }
 
 // ---- whole prompts over 4-bit pages: bf16 copies and the bf16 tile kernel -------
 // (exact: a 4-bit value is a bf16 number).  Where a kv head has half as many rows as
-// keys or more, the copies cost less than what q4_tiles.cu spends per segment
+// keys or more, the copies cost less than what tiles.cu spends per segment
 // (G = 4, H_kv = 8, us, tiles against copies: 4 x 2048 rows over 600 keys 46, 38; 4 x
 // 8192 over 2048 198, 145; 8 x 2080 over 1000 .. 8000 352, 382; 8 x 1040 209, 247; 1 x
 // 8192 over 16000 436, 444).  Sequences go in groups whose copies fit kDenseBytes.
@@ -168,14 +168,14 @@ pa_status dense_launch(const WalkCall& c, const DensePlan& t) {
 
 // Where the packed query lies: after the tiles' own part and the log-sum-exps.
 static size_t tiles_scratch(const pa_shape& sh, int sm_count) {
-    return align_up(align_up(q4_tiles_workspace_bytes(sh, sm_count), 256) + static_cast<size_t>(sh.B) * sh.H_q * sh.L * 4, 256);
+    return align_up(align_up(tiles_workspace_bytes(sh, sm_count), 256) + static_cast<size_t>(sh.B) * sh.H_q * sh.L * 4, 256);
 }
 
 size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_count) {
     DensePlan d;
     if (dense_take(sh, q4, weights, sm_count, &d)) return d.total;
-    if (tiles_take(sh, q4, sm_count)) {
-        const size_t n = align_up(q4_tiles_workspace_bytes(sh, sm_count), 256);
+    if (tiles_take(sh, sm_count)) {
+        const size_t n = align_up(tiles_workspace_bytes(sh, sm_count), 256);
         return weights ? tiles_scratch(sh, sm_count) + weights_scratch_bytes(sh, sm_count) : n;
     }
     return plan(sh, q4, weights, sm_count).total;
@@ -183,7 +183,7 @@ size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_co
 
 pa_status walk_launch(const WalkCall& c) {
     const pa_shape& sh = c.sh;
-    const bool tiles = tiles_take(sh, c.ks != nullptr, c.dev.sm_count);
+    const bool tiles = tiles_take(sh, c.dev.sm_count);
     const WalkPlan w = plan(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count);
     if (c.ws_bytes < walk_workspace_bytes(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count)) return PA_ERR_WORKSPACE;
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
@@ -224,9 +224,9 @@ pa_status walk_launch(const WalkCall& c) {
     if (tiles) {
         void* const scratch = ws + tiles_scratch(sh, c.dev.sm_count);
         if (c.w_out)
-            p.lse = reinterpret_cast<float*>(ws + align_up(q4_tiles_workspace_bytes(sh, c.dev.sm_count), 256));
-        const pa_status st = q4_tiles_launch(c, p.lse);
-        return st != PA_OK || !c.w_out ? st : weights_from_keys(p, true, false, scratch, c.dev, c.stream);
+            p.lse = reinterpret_cast<float*>(ws + align_up(tiles_workspace_bytes(sh, c.dev.sm_count), 256));
+        const pa_status st = tiles_launch(c, p.lse);
+        return st != PA_OK || !c.w_out ? st : weights_from_keys(p, c.ks != nullptr, false, scratch, c.dev, c.stream);
     }
     return launch(p, w, c.ks != nullptr, sh.dtype == PA_F32, c.dev, ws + w.score_off, c.stream);
 }

@@ -1,4 +1,4 @@
-// block.cu -- attention of many rows where the tensor-core tiles of q4_tiles.cu do not
+// block.cu -- attention of many rows where the tensor-core tiles of tiles.cu do not
 // apply: fp32 queries over 4-bit pages, bf16 pages with key weights.  The formulas and
 // roundings are those of walk.cu.
 //

@@ -50,10 +50,10 @@ size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_co
 pa_status walk_launch(const WalkCall& c);
 
 // bf16 queries with many rows per kv head over 4-bit pages, on tcgen05 tiles
-// (q4_tiles.cu); lse: [B, H_q, L], or null.
-bool q4_tiles_supported(const pa_shape& sh, int sm_count);
-size_t q4_tiles_workspace_bytes(const pa_shape& sh, int sm_count);
-pa_status q4_tiles_launch(const WalkCall& c, float* lse);
+// (tiles.cu); lse: [B, H_q, L], or null.
+bool tiles_supported(const pa_shape& sh, int sm_count);
+size_t tiles_workspace_bytes(const pa_shape& sh, int sm_count);
+pa_status tiles_launch(const WalkCall& c, float* lse);
 
 // Eviction from the buffers K and V (rows of sh.dtype) or, where buf[2] is not
 // null, K codes, V codes, K scales, V scales.

@@ -94,6 +94,21 @@ __device__ __forceinline__ void mma_16816_bf16_first(float (&d)[4], const uint32
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+template <bool F16>
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        mma_16816_f16_first(d, a, b0, b1);
+    else
+        mma_16816_bf16_first(d, a, b0, b1);
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        mma_16816_f16(d, a, b0, b1);
+    else
+        mma_16816_bf16(d, a, b0, b1);
+}
+
 // The power of two that takes a row with largest magnitude mx into f16's range
 // (mx into [2^14, 2^15)), and its inverse.  Rows with an inf or NaN stay as they
 // are; the exponent is cut so that both factors are normal numbers.

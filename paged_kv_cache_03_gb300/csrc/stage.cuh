@@ -1,5 +1,6 @@
-// q4_stage.cuh -- tiles of 128 4-bit rows, dequantised into shared memory in the
-// 128-byte swizzle that tcgen05.mma reads.
+// stage.cuh -- asynchronous copies, and tiles of 128 rows in shared memory in the
+// 128-byte swizzle that tcgen05.mma reads: 4-bit rows dequantised on the way, bf16
+// rows as they are.
 #pragma once
 #include "cache.h"
 #include "ptx.cuh"
@@ -8,6 +9,21 @@
 namespace pa {
 
 constexpr int kStageHalf = 128 * 128;  // bytes of 128 rows x 64 dims, one swizzled column block
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // 16-byte chunk c (of 8) of row r in a 64-dim half, 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
@@ -75,5 +91,17 @@ struct RawTile {
         }
     }
 };
+
+// The same part of a bf16 tile, 32 rows a warp: two rows at a time, 16 lanes a row.
+// The caller commits the copies.
+__device__ __forceinline__ void copy_tile(uint32_t tile, const uint8_t* pool, int rows, int warp, int lane) {
+    const int c = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int x = 2 * i + (lane >> 4), row = __shfl_sync(0xffffffffu, rows, x);
+        cp_async16(tile + (c >> 3) * kStageHalf + sw128(32 * (x >> 3) + 8 * warp + (x & 7), c & 7),
+                   pool + (row < 0 ? 0 : static_cast<long long>(row) * (2 * kHeadDim)) + 16 * c, row >= 0);
+    }
+}
 
 }  // namespace pa

@@ -12,7 +12,7 @@
 //     (sequence, kv head), and its units are the 128-key tiles that its rows see.
 //     The units of all segments are cut into equal shares, one per CTA, so ragged
 //     contexts leave no SM idle; a segment that crosses shares leaves fp32 partial
-//     states that q4_tile_merge_kernel joins.
+//     states that tile_merge_kernel joins.
 //   * Warps 0-3 read codes and scales (a tile ahead, in registers), dequantise and
 //     store K and V tiles into two-slot rings in shared memory in the 128-byte
 //     swizzle the MMA reads: about 420 instructions a warp and tile, hidden behind
@@ -33,7 +33,7 @@
 
 #include "cache.h"
 #include "ptx.cuh"
-#include "q4_stage.cuh"
+#include "stage.cuh"
 #include "tc.cuh"
 
 namespace pa {
@@ -183,8 +183,13 @@ __device__ __forceinline__ void give_up(const TileParams& p, volatile int* f) {
     atomicOr(p.flag, PA_FLAG_TIMEOUT);
 }
 
-constexpr uint32_t idesc_f16(int a_mn, int b_mn) {
-    return tc::idesc_bf16(BM, BN, a_mn, b_mn) & ~((1u << 7) | (1u << 10));  // A, B f16
+constexpr uint32_t idesc(bool f16, int a_mn, int b_mn) {
+    return tc::idesc_bf16(BM, BN, a_mn, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
+}
+// Two weights or query values for the products: f16 next to 4-bit rows, bf16 next to bf16 rows.
+template <bool Q4>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return Q4 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
 template <int N>
@@ -196,7 +201,8 @@ __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p) {
+template <bool Q4>
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ int share[4];  // all units, units per share, first sequence, its first unit
     __shared__ int sums[kThreads / 32];
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p
         };
         bool ok = take(0);
         int k = 0, g = 0;  // piece, tiles so far
-        if (ok && slot(0)->n > 0) {
+        if constexpr (Q4) if (ok && slot(0)->n > 0) {
             RawTile rk, rv;
             int j = slot(0)->j0, last = j + slot(0)->n - 1;
             lookup(slot(0)->b, slot(0)->S, slot(0)->kvh, j);
@@ -379,14 +385,69 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p
                 if (more) rv.request(p.vc, p.vs, rows, lane);
             }
         }
+        if constexpr (!Q4) {
+            // K of tile g is requested before V of tile g - 1 is announced, and V of tile
+            // g before K of tile g: each has most of a tile's time to arrive.
+            auto announce = [&](int b) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(b));
+            };
+            int j = 0, last = 0, rows = -1;
+            bool more = ok && slot(0)->n > 0;
+            if (more) {
+                j = slot(0)->j0;
+                last = j + slot(0)->n - 1;
+                lookup(slot(0)->b, slot(0)->S, slot(0)->kvh, j);
+                rows = rows_of();
+            }
+            while (more) {
+                if (j < last) {
+                    ++j;
+                } else {
+                    release(k);
+                    ++k;
+                    ok = take(k);
+                    if (!ok) break;
+                    more = slot(k)->n > 0;
+                    j = slot(k)->j0;
+                    last = j + slot(k)->n - 1;
+                }
+                if (more) lookup(slot(k)->b, slot(k)->S, slot(k)->kvh, j);
+                const int s = g & 1;
+                if (g >= 2 && !warp_wait(bar(kKEmpty + s), ((g >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (aborted(abort_flag)) break;
+                copy_tile(base + kOffK + s * kTile, p.kc, rows, warp, lane);
+                cp_async_commit();
+                if (g > 0) {
+                    cp_async_wait<1>();
+                    announce(kVFull + (s ^ 1));
+                }
+                if (g >= 2 && !warp_wait(bar(kVEmpty + s), ((g >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                copy_tile(base + kOffV + s * kTile, p.vc, rows, warp, lane);
+                cp_async_commit();
+                cp_async_wait<1>();
+                announce(kKFull + s);
+                ++g;
+                if (more) rows = rows_of();
+            }
+            cp_async_wait<0>();
+            if (g > 0) announce(kVFull + ((g - 1) & 1));
+        }
         if (!ok && lane == 0) give_up(p, abort_flag);
         if (__any_sync(0xffffffffu, bad_page) && lane == 0) atomicOr(p.flag, PA_FLAG_BAD_PAGE);
     } else if (warp < 8) {
         reg_dec<104>();
         if (warp == 4 && lane == 0) {
             // =========================== MMA issuer ===============================
-            constexpr uint32_t idS = idesc_f16(0, 0);  // Q, K both K-major
-            constexpr uint32_t idO = idesc_f16(0, 1);  // P K-major, V MN-major
+            constexpr uint32_t idS = idesc(Q4, 0, 0);  // Q, K both K-major
+            constexpr uint32_t idO = idesc(Q4, 0, 1);  // P K-major, V MN-major
             const uint64_t dQ[2] = {tc::smem_desc_sw128(base + kOffQ, 16, 1024),
                                     tc::smem_desc_sw128(base + kOffQ + kTile, 16, 1024)};
             const uint64_t dK0 = tc::smem_desc_sw128(base + kOffK, 16, 1024);
@@ -505,10 +566,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     float up, down;
                     f16_scale(mx, up, down);
+                    if constexpr (Q4) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 f = bf16x2_to_float2(qf[k >> 1][k & 1]);
-                        qf[k >> 1][k & 1] = pack_f16x2(f.x * up, f.y * up);
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 f = bf16x2_to_float2(qf[k >> 1][k & 1]);
+                            qf[k >> 1][k & 1] = pack_f16x2(f.x * up, f.y * up);
+                        }
+                    } else {
+                        down = 1.f;
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -544,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p
                             if (ks < 7) load(ks + 1);
 #pragma unroll
                             for (int grp = 0; grp < 4; ++grp) {
-                                if (ks == 0) mma_16816_f16_first(x[grp], a[0][grp], qf[0][0], qf[0][1]);
-                                else mma_16816_f16(x[grp], a[ks & 1][grp], qf[ks][0], qf[ks][1]);
+                                if (ks == 0) mma_first<Q4>(x[grp], a[0][grp], qf[0][0], qf[0][1]);
+                                else mma<Q4>(x[grp], a[ks & 1][grp], qf[ks][0], qf[ks][1]);
                             }
                         }
                     }
@@ -596,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p
                                 const float p0 = fast_exp2(x[grp][2 * h] - mu0), p1 = fast_exp2(x[grp][2 * h + 1] - mu1);
                                 l_r[0] += p0;
                                 l_r[1] += p1;
-                                pb[grp][h] = movmatrix_trans(pack_f16x2(p0, p1));
+                                pb[grp][h] = movmatrix_trans(pack2<Q4>(p0, p1));
                             }
                         // step n: dims 64 (n & 1) .. of group n >> 1
                         const int r = 64 * wr + (lane & 7) + (lane >> 4) * 8;
@@ -613,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p
                             if (n < 7) load(n + 1);
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                mma_16816_f16(o[4 * (n & 1) + i], a[n & 1][i], pb[n >> 1][0], pb[n >> 1][1]);
+                                mma<Q4>(o[4 * (n & 1) + i], a[n & 1][i], pb[n >> 1][0], pb[n >> 1][1]);
                         }
                     }
                     __syncwarp();
@@ -711,34 +776,38 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        // Each thread's row in place to f16, the largest value in [2^14, 2^15).  The
+        // Each thread's row in place to f16, the largest value in [2^14, 2^15) (bf16 pages:
+        // as it is).  The
         // tile of a pair that has nothing to do in a piece must not run ahead: piece k
         // is announced once the products of piece k - 1 are through.
         auto convert = [&](int k) {
             if (k > 0 && !warp_wait(bar(kQEmpty), (k - 1) & 1)) return false;
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncwarp();
-            uint4 v[16];
-            float mx = 0.f;
+            float down = 1.f;
+            if constexpr (Q4) {
+                uint4 v[16];
+                float mx = 0.f;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
-                             : "r"(qrow + (c >> 3) * kHalf + sw128(r, c & 7)));
-                const float2 f[4] = {bf16x2_to_float2(v[c].x), bf16x2_to_float2(v[c].y), bf16x2_to_float2(v[c].z),
-                                     bf16x2_to_float2(v[c].w)};
+                for (int c = 0; c < 16; ++c) {
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
+                                 : "r"(qrow + (c >> 3) * kHalf + sw128(r, c & 7)));
+                    const float2 f[4] = {bf16x2_to_float2(v[c].x), bf16x2_to_float2(v[c].y), bf16x2_to_float2(v[c].z),
+                                         bf16x2_to_float2(v[c].w)};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx = fmax3(mx, fabsf(f[e].x), fabsf(f[e].y));
-            }
-            float up, down;
-            f16_scale(mx, up, down);
+                    for (int e = 0; e < 4; ++e) mx = fmax3(mx, fabsf(f[e].x), fabsf(f[e].y));
+                }
+                float up;
+                f16_scale(mx, up, down);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const float2 f[4] = {bf16x2_to_float2(v[c].x), bf16x2_to_float2(v[c].y), bf16x2_to_float2(v[c].z),
-                                     bf16x2_to_float2(v[c].w)};
-                sts128(qrow + (c >> 3) * kHalf + sw128(r, c & 7), pack_f16x2(f[0].x * up, f[0].y * up),
-                       pack_f16x2(f[1].x * up, f[1].y * up), pack_f16x2(f[2].x * up, f[2].y * up),
-                       pack_f16x2(f[3].x * up, f[3].y * up));
+                for (int c = 0; c < 16; ++c) {
+                    const float2 f[4] = {bf16x2_to_float2(v[c].x), bf16x2_to_float2(v[c].y), bf16x2_to_float2(v[c].z),
+                                         bf16x2_to_float2(v[c].w)};
+                    sts128(qrow + (c >> 3) * kHalf + sw128(r, c & 7), pack_f16x2(f[0].x * up, f[0].y * up),
+                           pack_f16x2(f[1].x * up, f[1].y * up), pack_f16x2(f[2].x * up, f[2].y * up),
+                           pack_f16x2(f[3].x * up, f[3].y * up));
+                }
             }
             qs = fmaxf(down * p.scale_log2, FLT_MIN);
             fence_proxy_async_smem();
@@ -808,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const TileParams p
                     const float2 y = __ffma2_rn(make_float2(x[cc][e], x[cc][e + 1]), c2, nm2);
                     const float2 ex = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                     ts = __fadd2_rn(ts, ex);
-                    pw[k] = pack_f16x2(ex.x, ex.y);
+                    pw[k] = pack2<Q4>(ex.x, ex.y);
                 }
                 lsum.x = lsum.x * alpha + ts.x;
                 lsum.y = lsum.y * alpha + ts.y;
@@ -939,7 +1008,7 @@ constexpr int kMergeRows = 16;  // rows per merge CTA, four a warp
 // Merges the partial states of the segments that cross shares: CTA (c, y) rows
 // 16 y .. of the segment that starts in share c; and, for c past the shares, the
 // remainder rows of a (sequence, kv head).
-__global__ void __launch_bounds__(128) q4_tile_merge_kernel(const TileParams p, int shares) {
+__global__ void __launch_bounds__(128) tile_merge_kernel(const TileParams p, int shares) {
     pdl_launch_dependents();
     pdl_wait_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1038,9 +1107,21 @@ TilePlan plan(const pa_shape& sh, int sm_count) {
     return t;
 }
 
+template <bool Q4>
+pa_status launch_tiles(const TileParams& p, const WalkCall& c) {
+    static int attr_done[64] = {0};
+    if (!attr_done[c.dev.device]) {
+        if (cudaFuncSetAttribute(tile_kernel<Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+            return PA_ERR_CUDA;
+        attr_done[c.dev.device] = 1;
+    }
+    tile_kernel<Q4><<<static_cast<unsigned>(c.dev.sm_count), kThreads, kSmemBytes, c.stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 }  // namespace
 
-bool q4_tiles_supported(const pa_shape& sh, int sm_count) {
+bool tiles_supported(const pa_shape& sh, int sm_count) {
     const long long G = sh.H_q / sh.H_kv;
     if (sh.dtype != PA_BF16 || G > BM || sm_count < 1) return false;
     const long long cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
@@ -1050,9 +1131,9 @@ bool q4_tiles_supported(const pa_shape& sh, int sm_count) {
            static_cast<long long>(sh.H_q) * sh.L * sh.B < (1ll << 31);
 }
 
-size_t q4_tiles_workspace_bytes(const pa_shape& sh, int sm_count) { return plan(sh, sm_count).total; }
+size_t tiles_workspace_bytes(const pa_shape& sh, int sm_count) { return plan(sh, sm_count).total; }
 
-pa_status q4_tiles_launch(const WalkCall& c, float* lse) {
+pa_status tiles_launch(const WalkCall& c, float* lse) {
     const pa_shape& sh = c.sh;
     if (c.dev.smem_optin < kSmemBytes) return PA_ERR_UNSUPPORTED;
     const TilePlan t = plan(sh, c.dev.sm_count);
@@ -1093,26 +1174,12 @@ pa_status q4_tiles_launch(const WalkCall& c, float* lse) {
     p.scale_log2 = c.scale * 1.4426950408889634f;
     p.min_per = kMinPer;
     p.out32 = reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
-    static int attr_done[64] = {0};
-    if (!attr_done[c.dev.device]) {
-        if (cudaFuncSetAttribute(q4_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
-            return PA_ERR_CUDA;
-        attr_done[c.dev.device] = 1;
-    }
-    q4_tile_kernel<<<static_cast<unsigned>(c.dev.sm_count), kThreads, kSmemBytes, c.stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+    const pa_status st = c.ks ? launch_tiles<true>(p, c) : launch_tiles<false>(p, c);
+    if (st != PA_OK) return st;
     const int shares = c.dev.sm_count;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(shares + (t.nrem ? sh.B * sh.H_kv : 0)),
-                       static_cast<unsigned>((t.nM > 1 ? 2 : 1) * BM / kMergeRows));
-    cfg.blockDim = dim3(128);
-    cfg.stream = c.stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, q4_tile_merge_kernel, p, shares) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(shares + (t.nrem ? sh.B * sh.H_kv : 0)),
+                    static_cast<unsigned>((t.nM > 1 ? 2 : 1) * BM / kMergeRows));
+    return launch_dependent(tile_merge_kernel, grid, 128, 0, c.stream, p, shares) ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace pa

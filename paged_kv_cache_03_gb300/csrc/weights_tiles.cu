@@ -12,7 +12,7 @@
 // spent most of its time on its start (8 x 4 heads x 32 rows over 1000 .. 8000 keys, 8 kv
 // heads: 59 us with a CTA per item, 45 so).  Bound by instruction latency: 12 warps an
 // SM, each key's row costing a multiply-add, a MUFU exponential and an add.
-#include "q4_stage.cuh"
+#include "stage.cuh"
 #include "tc.cuh"
 #include "walk.cuh"
 
@@ -41,7 +41,6 @@ __global__ void __launch_bounds__(kThreads, 3) weights_tile_kernel(const WalkPar
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) float lse_s[3][kRows];
     __shared__ __align__(16) int last_s[3][kRows];  // the last key a row sees
-    __shared__ int rows_s[kKeys];
     __shared__ __align__(8) uint64_t done_s[3];  // the products of even and odd tiles, of all at a time-out
     __shared__ uint32_t tmem_s;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -65,22 +64,21 @@ __global__ void __launch_bounds__(kThreads, 3) weights_tile_kernel(const WalkPar
         it.id = id;
         return it;
     };
-    // 4-bit pages: lane 8 i + r looks up key 32 i + 8 warp + r, as RawTile wants
+    // lane 8 i + r looks up key 32 i + 8 warp + r
     int page = kNoPage, in_page = 0;
     bool bad = false;
     auto lookup = [&](const Item& it) {
-        const int k = it.k0 + (Q4 ? 32 * (lane >> 3) + 8 * warp + (lane & 7) : tid);
+        const int k = it.k0 + 32 * (lane >> 3) + 8 * warp + (lane & 7);
         const int lp = k / p.ps;
         in_page = k - lp * p.ps;
         page = k < it.S ? __ldg(p.bt + static_cast<long long>(it.b) * p.max_npg + lp) : kNoPage;
     };
     RawTile raw;
+    int rows;  // pool rows of the next item's keys
+    const uint8_t* const keys = static_cast<const uint8_t*>(p.kc);
     auto request = [&](const Item& it) {
-        const int row = row_in(p, it.bk - it.b * p.H_kv, page, in_page, bad);
-        if constexpr (Q4)
-            raw.request(static_cast<const uint8_t*>(p.kc), static_cast<const uint8_t*>(p.ks), row, lane);
-        else
-            rows_s[tid] = row;
+        rows = row_in(p, it.bk - it.b * p.H_kv, page, in_page, bad);
+        if constexpr (Q4) raw.request(keys, static_cast<const uint8_t*>(p.ks), rows, lane);
     };
 
     pdl_wait_primary();  // (what follows writes the weights)
@@ -157,14 +155,7 @@ __global__ void __launch_bounds__(kThreads, 3) weights_tile_kernel(const WalkPar
         };
         // ---- the keys; the next item's page ids -------------------------------------
         if constexpr (!Q4) {
-            __syncthreads();  // rows_s
-#pragma unroll
-            for (int j = 0; j < kKeys / 8; ++j) {
-                const int k = r0 + 8 * j, row = rows_s[k];
-                cp_async16(base + (c >> 3) * kStageHalf + sw128(k, c & 7),
-                           static_cast<const uint8_t*>(p.kc) + (row < 0 ? 0 : static_cast<long long>(row) * (2 * kD)) + 16 * c,
-                           row >= 0);
-            }
+            copy_tile(base, keys, rows, warp, lane);
             cp_async_commit();
         }
         RowTile now = from({n0, n0 > 0 ? n0 * kRows % p.L : 0}), next = from(behind(now));
