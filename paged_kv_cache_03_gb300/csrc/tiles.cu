@@ -1003,49 +1003,46 @@ struct RowState {
     }
 };
 
-constexpr int kMergeRows = 16;  // rows per merge CTA, four a warp
+constexpr int kMergeRows = 4;  // rows per merge CTA, one a warp
 
-// Merges the partial states of the segments that cross shares: CTA (c, y) rows
-// 16 y .. of the segment that starts in share c; and, for c past the shares, the
-// remainder rows of a (sequence, kv head).
-__global__ void __launch_bounds__(128) tile_merge_kernel(const TileParams p, int shares) {
+// Merges the partial states of the segments that cross shares: CTA y + ny c takes rows
+// 4 y .. of the segment that starts in share c, four partial states a warp in flight;
+// then two CTAs for the remainder rows of each (sequence, kv head).
+__global__ void __launch_bounds__(128) tile_merge_kernel(const TileParams p, int shares, int ny) {
     pdl_launch_dependents();
     pdl_wait_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int N = kMergeRows / 4;
-    RowState st[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) st[i].init();
-    const int rr0 = kMergeRows * static_cast<int>(blockIdx.y) + N * warp;
-    if (static_cast<int>(blockIdx.x) < shares) {
-        const int c = blockIdx.x;
+    RowState st;
+    st.init();
+    const int rest = static_cast<int>(blockIdx.x) - shares * ny;
+    if (rest < 0) {
+        const int c = static_cast<int>(blockIdx.x) / ny, rr = kMergeRows * (static_cast<int>(blockIdx.x) - c * ny) + warp;
         const int4 sp = p.split[c];
         if (sp.x < 0) return;
-        const int t = rr0 >> 7, r0 = rr0 & 127, m = 2 * sp.z + t;
-        if (m >= p.nM) return;
-        for (int k = c; k <= sp.w; ++k) {
-            const long long slot = ((2ll * k + (k == c ? 1 : 0)) * 2 + t) * BM + r0;
-            float2 v[N];
-            float4 x[N];
+        const int t = rr >> 7, r = rr & 127, m = 2 * sp.z + t;
+        const int g = r / p.Lt, pos = m * p.Lt + (r - g * p.Lt);
+        if (m >= p.nM || g >= p.G || pos >= tile_end(p, m)) return;
+        constexpr int U = 4;
+        for (int k = c; k <= sp.w; k += U) {
+            float2 v[U];
+            float4 x[U];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                v[i] = p.part_ml[slot + i];
-                x[i] = *reinterpret_cast<const float4*>(p.part_o + (slot + i) * kD + 4 * lane);
+            for (int u = 0; u < U; ++u) {
+                v[u].x = neg_inf();
+                if (k + u > sp.w) continue;
+                const long long slot = ((2ll * (k + u) + (k + u == c ? 1 : 0)) * 2 + t) * BM + r;
+                v[u] = p.part_ml[slot];
+                x[u] = *reinterpret_cast<const float4*>(p.part_o + slot * kD + 4 * lane);
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) st[i].add(v[i], x[i]);
+            for (int u = 0; u < U; ++u) st.add(v[u], x[u]);
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int g = (r0 + i) / p.Lt, pos = m * p.Lt + (r0 + i - g * p.Lt);
-            if (g < p.G && pos < tile_end(p, m))
-                store_row(p, (static_cast<long long>(sp.x) * p.H_q + sp.y * p.G + g) * p.L + pos, lane, st[i].acc,
-                          st[i].l, st[i].M);
-        }
+        store_row(p, (static_cast<long long>(sp.x) * p.H_q + sp.y * p.G + g) * p.L + pos, lane, st.acc, st.l, st.M);
         return;
     }
-    if (blockIdx.y > 0 || N * warp >= p.nrem) return;
-    const int bk = static_cast<int>(blockIdx.x) - shares, b = bk / p.H_kv, kvh = bk - b * p.H_kv;
+    const int bk = rest >> 1, rr = kMergeRows * (rest & 1) + warp;
+    if (rr >= p.nrem) return;
+    const int b = bk / p.H_kv, kvh = bk - b * p.H_kv;
     bool bad;
     const int S = seq_len(p, b, bad);
     if (bad) return;  // (its rows are zeros already)
@@ -1053,19 +1050,12 @@ __global__ void __launch_bounds__(128) tile_merge_kernel(const TileParams p, int
     const int last = p.prefix[b] + (kvh + 1) * hu - 1, first = last - ng + 1;  // its tiles' positions
     for (int k = first / per; k <= last / per; ++k)
         for (int w = 0; w < 2; ++w) {
-            const long long slot = ((static_cast<long long>(bk) + k) * 2 + w) * 8 + N * warp;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                st[i].add(p.rem_ml[slot + i], *reinterpret_cast<const float4*>(p.rem_o + (slot + i) * kD + 4 * lane));
+            const long long slot = ((static_cast<long long>(bk) + k) * 2 + w) * 8 + rr;
+            st.add(p.rem_ml[slot], *reinterpret_cast<const float4*>(p.rem_o + slot * kD + 4 * lane));
         }
-    const int Lrem = p.L - p.rem_l0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int rr = N * warp + i, g = rr / Lrem;
-        if (rr < p.nrem)
-            store_row(p, (static_cast<long long>(b) * p.H_q + kvh * p.G + g) * p.L + p.rem_l0 + rr - g * Lrem, lane,
-                      st[i].acc, st[i].l, st[i].M);
-    }
+    const int Lrem = p.L - p.rem_l0, g = rr / Lrem;
+    store_row(p, (static_cast<long long>(b) * p.H_q + kvh * p.G + g) * p.L + p.rem_l0 + rr - g * Lrem, lane, st.acc, st.l,
+              st.M);
 }
 
 constexpr int kMinPer = 4;  // least cost of a share
@@ -1177,9 +1167,9 @@ pa_status tiles_launch(const WalkCall& c, float* lse) {
     const pa_status st = c.ks ? launch_tiles<true>(p, c) : launch_tiles<false>(p, c);
     if (st != PA_OK) return st;
     const int shares = c.dev.sm_count;
-    const dim3 grid(static_cast<unsigned>(shares + (t.nrem ? sh.B * sh.H_kv : 0)),
-                    static_cast<unsigned>((t.nM > 1 ? 2 : 1) * BM / kMergeRows));
-    return launch_dependent(tile_merge_kernel, grid, 128, 0, c.stream, p, shares) ? PA_OK : PA_ERR_CUDA;
+    const int ny = (t.nM > 1 ? 2 : 1) * BM / kMergeRows;
+    const dim3 grid(static_cast<unsigned>(shares * ny + (t.nrem ? 2 * sh.B * sh.H_kv : 0)));
+    return launch_dependent(tile_merge_kernel, grid, 128, 0, c.stream, p, shares, ny) ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace pa

@@ -28,7 +28,7 @@ constexpr uint32_t kCols = 2 * kRows;
 
 // 128 keys of a (sequence, kv head) and a run of its rows.
 struct Item {
-    int id;  // (run * B * H_kv + bk) * ntile + tile
+    int id;  // (run * ntile + tile) * B * H_kv + bk: a CTA meets short and long sequences in turn
     int S, b, bk, run, k0;
 };
 // Query rows 64 n .. of a (sequence, kv head), the first at position l of its head.
@@ -52,10 +52,10 @@ __global__ void __launch_bounds__(kThreads, 3) weights_tile_kernel(const WalkPar
     auto find = [&](int id) {
         Item it = {};
         for (; id < items; id += static_cast<int>(gridDim.x)) {
-            const int u = id / ntile;
-            it.k0 = (id - u * ntile) * kKeys;
-            it.run = u / heads;
-            it.bk = u - it.run * heads;
+            const int u = id / heads;
+            it.bk = id - u * heads;
+            it.run = u / ntile;
+            it.k0 = (u - it.run * ntile) * kKeys;
             it.b = it.bk / p.H_kv;
             it.S = seq_len(p, it.b, false);
             if (it.k0 < it.S) break;
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kThreads, 3) weights_tile_kernel(const WalkPar
     tc::fence_after_sync();
     const uint32_t tmem = tmem_s;
     const int c = tid & 15, r0 = tid >> 4;  // this thread's 16-byte chunk, and its first row of eight
+    const float scale = fmaxf(p.scale_log2, FLT_MIN);  // (times -inf, a key not seen: -inf)
     const int nt = (p.R + kRows - 1) / kRows, step = kRows % p.L;
     auto product = [&](int i) {
         constexpr uint32_t idesc = tc::idesc_bf16(kKeys, kRows, 0, 0);  // both K-major
@@ -202,21 +203,24 @@ __global__ void __launch_bounds__(kThreads, 3) weights_tile_kernel(const WalkPar
                 float s[32];
                 tc::ld32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + (i & 1) * kRows + 32 * h, s);
                 tc::wait_ld();
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const int4 x = *reinterpret_cast<const int4*>(last + 32 * h + e);
+                        const int k = it.k0 + tid;
+                        if (k > x.x) s[e] = neg_inf();
+                        if (k > x.y) s[e + 1] = neg_inf();
+                        if (k > x.z) s[e + 2] = neg_inf();
+                        if (k > x.w) s[e + 3] = neg_inf();
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                     const float4 m = *reinterpret_cast<const float4*>(lse + 32 * h + e);
-                    float w[4] = {fast_exp2(fmaf(s[e], p.scale_log2, -m.x)), fast_exp2(fmaf(s[e + 1], p.scale_log2, -m.y)),
-                                  fast_exp2(fmaf(s[e + 2], p.scale_log2, -m.z)), fast_exp2(fmaf(s[e + 3], p.scale_log2, -m.w))};
-                    if (masked) {
-                        const int4 x = *reinterpret_cast<const int4*>(last + 32 * h + e);
-                        const int k = it.k0 + tid;
-                        if (k > x.x) w[0] = 0.f;
-                        if (k > x.y) w[1] = 0.f;
-                        if (k > x.z) w[2] = 0.f;
-                        if (k > x.w) w[3] = 0.f;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[k] += w[k];
+                    acc[0] += fast_exp2(fmaf(s[e], scale, -m.x));
+                    acc[1] += fast_exp2(fmaf(s[e + 1], scale, -m.y));
+                    acc[2] += fast_exp2(fmaf(s[e + 2], scale, -m.z));
+                    acc[3] += fast_exp2(fmaf(s[e + 3], scale, -m.w));
                 }
             }
             now = next;
