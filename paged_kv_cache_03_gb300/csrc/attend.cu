@@ -185,6 +185,7 @@ pa_status walk_launch(const WalkCall& c) {
     const pa_shape& sh = c.sh;
     const bool tiles = tiles_take(sh, c.dev.sm_count);
     const WalkPlan w = plan(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count);
+    if (c.w_out && !weights_supported(sh, c.w_S, c.dev.sm_count)) return PA_ERR_UNSUPPORTED;
     if (c.ws_bytes < walk_workspace_bytes(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count)) return PA_ERR_WORKSPACE;
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
     WalkParams p;

@@ -201,10 +201,12 @@ __global__ void __launch_bounds__(256) add_splits_kernel(const WalkParams p, con
     }
 }
 
+constexpr int kKeysCta = 32 * kWarps;  // keys of a CTA that recomputes
+
 // How the rows are cut: about two CTAs per SM, of at least 64 rows.  (Counted in the
 // table's keys, so that neither the workspace nor the sums depend on w_S.)
 int row_runs(long long bk, long long cap, int R, int sm_count) {
-    const long long ctas = bk * ((cap + 32 * kWarps - 1) / (32 * kWarps)), most = (R + 63) / 64;
+    const long long ctas = bk * ((cap + kKeysCta - 1) / kKeysCta), most = (R + 63) / 64;
     const long long want = (2ll * sm_count + ctas - 1) / (ctas > 0 ? ctas : 1);
     return static_cast<int>(want < most ? want : most);
 }
@@ -214,10 +216,9 @@ size_t runs_bytes(long long bk, long long cap, int R, int sm_count) {
 }
 // fp32 queries (over 4-bit pages).
 pa_status weights_of_f32(const WalkParams& p, const RowSplits& sp, void* scratch, cudaStream_t stream) {
-    const long long bk = static_cast<long long>(p.B) * p.H_kv, ntile = (p.w_S + 32 * kWarps - 1) / (32 * kWarps);
+    const long long bk = static_cast<long long>(p.B) * p.H_kv, ntile = (p.w_S + kKeysCta - 1) / kKeysCta;
     Packed k;
     k.nt = (p.R + 7) / 8;
-    if (ntile * bk > INT_MAX || bk * k.nt > INT_MAX) return PA_ERR_UNSUPPORTED;
     k.frags = static_cast<uint4*>(scratch);
     k.rows = reinterpret_cast<PackedRow*>(k.frags + bk * k.nt * 256);
     k.last = reinterpret_cast<int*>(k.rows + bk * k.nt * 8);
@@ -232,11 +233,18 @@ pa_status weights_of_f32(const WalkParams& p, const RowSplits& sp, void* scratch
 
 pa_status weights_from_scores(const WalkParams& p, cudaStream_t stream) {
     const long long bk = static_cast<long long>(p.B) * p.H_kv, ntile = (p.w_S + 255) / 256;
-    if (ntile * bk > INT_MAX) return PA_ERR_UNSUPPORTED;
     return launch_dependent(walk_sum_kernel, dim3(static_cast<unsigned>(ntile * bk)), 256, 0, stream, p,
                             static_cast<int>(ntile))
                ? PA_OK
                : PA_ERR_CUDA;
+}
+
+bool weights_supported(const pa_shape& sh, long long w_S, int sm_count) {
+    const long long bk = static_cast<long long>(sh.B) * sh.H_kv, cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
+    const long long R = static_cast<long long>(sh.H_q / sh.H_kv) * sh.L;
+    // items and blocks are counted in ints
+    const long long most = INT_MAX / 2 / bk / row_runs(bk, cap, static_cast<int>(R), sm_count);
+    return w_S <= INT_MAX / 2 && w_S / kKeysCta < most && bk * ((R + 7) / 8) <= INT_MAX;
 }
 
 size_t weights_scratch_bytes(const pa_shape& sh, int sm_count) {

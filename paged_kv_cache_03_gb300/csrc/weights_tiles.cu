@@ -256,8 +256,8 @@ pa_status launch_tiles(const WalkParams& p, const RowSplits& sp, int device, int
         attr_done[device] = 1;
     }
     const long long ntile = (p.w_S + kKeys - 1) / kKeys, all = ntile * p.B * p.H_kv * sp.n, most = 3ll * sm_count;
-    if (p.w_S > INT_MAX / 2 || all > INT_MAX - most) return PA_ERR_UNSUPPORTED;
-    return launch_dependent(weights_tile_kernel<Q4>, dim3(static_cast<unsigned>(all < most ? all : most)), kThreads, kSmem, stream, p, static_cast<int>(ntile), sp)
+    const dim3 grid(static_cast<unsigned>(all < most ? all : most));
+    return launch_dependent(weights_tile_kernel<Q4>, grid, kThreads, kSmem, stream, p, static_cast<int>(ntile), sp)
                ? PA_OK
                : PA_ERR_CUDA;
 }
