@@ -75,14 +75,20 @@ pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, cons
     return w.scores ? weights_from_scores(p, stream) : weights_from_keys(p, q4, f32, scratch, dev, stream);
 }
 
-// Rows per kv head from which bf16 queries over 4-bit pages go to the tensor-core
-// tiles of tiles.cu.  Measured (walk, block, tiles, us; G = 4, H_kv = 8): B = 8 over
-// 1000 .. 8000 keys 54, 50, 55 at 48 rows, 65, 53, 55 at 64, 89, 87, 55 at 96; B = 1 over
-// 16000 keys 52, 49, 46 at 128; B = 64 over 500 .. 2000 keys 152, 109, 114 at 64.
-constexpr int kTileRows = 64;
+// Rows per kv head from which bf16 queries go to the tensor-core tiles of tiles.cu.
+// 4-bit pages, measured (walk, block, tiles, us; G = 4, H_kv = 8): B = 8 over 1000 ..
+// 8000 keys 54, 50, 55 at 48 rows, 65, 53, 55 at 64, 89, 87, 55 at 96; B = 1 over 16000
+// keys 52, 49, 46 at 128; B = 64 over 500 .. 2000 keys 152, 109, 114 at 64.  bf16 pages
+// with key weights (walk, tiles, us at 24 rows): B = 8 over 1000 .. 8000 keys 83, 83, at 40
+// 101 (block), 85; B = 64 over 500 .. 2000 179, 146; B = 1 over 16000 42, 56; B = 2 over 500
+// 18, 32: the tiles from fewer rows where the keys are many.
+constexpr int kTileRows = 64, kTileRowsBf16 = 24;
+constexpr long long kTileKeysBf16 = 1 << 18;  // of all (sequence, kv head)
 
-bool tiles_take(const pa_shape& sh, int sm_count) {
-    return sh.dtype == PA_BF16 && static_cast<long long>(sh.H_q / sh.H_kv) * sh.L >= kTileRows &&
+bool tiles_take(const pa_shape& sh, bool q4, int sm_count) {
+    const long long R = static_cast<long long>(sh.H_q / sh.H_kv) * sh.L;
+    const long long keys = static_cast<long long>(sh.B) * sh.H_kv * sh.max_pages_per_seq * sh.page_size;
+    return sh.dtype == PA_BF16 && (R >= kTileRows || (!q4 && R >= kTileRowsBf16 && keys >= kTileKeysBf16)) &&
            tiles_supported(sh, sm_count);
 }
 
@@ -174,7 +180,7 @@ static size_t tiles_scratch(const pa_shape& sh, int sm_count) {
 size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_count) {
     DensePlan d;
     if (dense_take(sh, q4, weights, sm_count, &d)) return d.total;
-    if (tiles_take(sh, sm_count)) {
+    if (tiles_take(sh, q4, sm_count)) {
         const size_t n = align_up(tiles_workspace_bytes(sh, sm_count), 256);
         return weights ? tiles_scratch(sh, sm_count) + weights_scratch_bytes(sh, sm_count) : n;
     }
@@ -183,7 +189,7 @@ size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_co
 
 pa_status walk_launch(const WalkCall& c) {
     const pa_shape& sh = c.sh;
-    const bool tiles = tiles_take(sh, c.dev.sm_count);
+    const bool tiles = tiles_take(sh, c.ks != nullptr, c.dev.sm_count);
     const WalkPlan w = plan(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count);
     if (c.w_out && !weights_supported(sh, c.w_S, c.dev.sm_count)) return PA_ERR_UNSUPPORTED;
     if (c.ws_bytes < walk_workspace_bytes(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count)) return PA_ERR_WORKSPACE;

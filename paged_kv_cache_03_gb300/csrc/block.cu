@@ -242,40 +242,57 @@ __global__ void __launch_bounds__(kWarps * 32) block_kernel(const WalkParams p) 
                 }
             }
             const float mu[2] = {m[0] == neg_inf() ? 0.f : m[0], m[1] == neg_inf() ? 0.f : m[1]};
+            // P's A fragments of 16 keys each, then O += P V (fp32: a tile's products on their
+            // own, then a rounded add, as the MMA cuts what it adds to)
+            uint32_t a[4][4], al[F32 ? 4 : 1][4];
 #pragma unroll
-            for (int n = 0; n < 8; n += 2) {  // 16 keys: P's A fragment, then O += P V
-                uint32_t a[4], al[4];
+            for (int n = 0; n < 8; ++n)  // keys 8 n .., rows g and g + 8
 #pragma unroll
-                for (int h = 0; h < 2; ++h)  // keys 8 (n + h) .., rows g and g + 8
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float p0 = fast_exp2(fmaf(s[n + h][2 * e], qs[e], -mu[e]));
-                        const float p1 = fast_exp2(fmaf(s[n + h][2 * e + 1], qs[e], -mu[e]));
-                        l[e] += p0 + p1;
-                        if constexpr (Q4) {
-                            const uint32_t x = pack_f16x2(p0, p1);
-                            a[2 * h + e] = x;
-                            if constexpr (F32) {
-                                const float2 f = f16x2_to_float2(x);
-                                al[2 * h + e] = pack_f16x2(p0 - f.x, p1 - f.y);
-                            }
-                        } else {
-                            const uint32_t x = pack_bf16x2(p0, p1);
-                            const float2 f = bf16x2_to_float2(x);
-                            la[e] += f.x + f.y;
-                            a[2 * h + e] = x;
+                for (int e = 0; e < 2; ++e) {
+                    const float p0 = fast_exp2(fmaf(s[n][2 * e], qs[e], -mu[e]));
+                    const float p1 = fast_exp2(fmaf(s[n][2 * e + 1], qs[e], -mu[e]));
+                    const int at = 2 * (n & 1) + e;
+                    l[e] += p0 + p1;
+                    if constexpr (Q4) {
+                        const uint32_t x = pack_f16x2(p0, p1);
+                        a[n >> 1][at] = x;
+                        if constexpr (F32) {
+                            const float2 f = f16x2_to_float2(x);
+                            al[n >> 1][at] = pack_f16x2(p0 - f.x, p1 - f.y);
                         }
+                    } else {
+                        const uint32_t x = pack_bf16x2(p0, p1);
+                        const float2 f = bf16x2_to_float2(x);
+                        la[e] += f.x + f.y;
+                        a[n >> 1][at] = x;
                     }
+                }
 #pragma unroll
-                for (int d = 0; d < 16; d += 2) {  // 16 dims
+            for (int d = 0; d < 16; d += 2) {  // 16 dims
+                float y[2][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // 16 keys
                     uint32_t x[4];
-                    ldmatrix_x4_trans(x, vb + chunk_at(8 * n + (lane & 15), d + (lane >> 4)));
-                    mma<Q4>(o[d], a, x[0], x[1]);
-                    mma<Q4>(o[d + 1], a, x[2], x[3]);
+                    ldmatrix_x4_trans(x, vb + chunk_at(16 * k + (lane & 15), d + (lane >> 4)));
                     if constexpr (F32) {
-                        mma<Q4>(o[d], al, x[0], x[1]);
-                        mma<Q4>(o[d + 1], al, x[2], x[3]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (k == 0)
+                                mma_first<Q4>(y[h], al[k], x[2 * h], x[2 * h + 1]);
+                            else
+                                mma<Q4>(y[h], al[k], x[2 * h], x[2 * h + 1]);
+                            mma<Q4>(y[h], a[k], x[2 * h], x[2 * h + 1]);
+                        }
+                    } else {
+                        mma<Q4>(o[d], a[k], x[0], x[1]);
+                        mma<Q4>(o[d + 1], a[k], x[2], x[3]);
                     }
+                }
+                if constexpr (F32) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[d + h][e] += y[h][e];
                 }
             }
         }

@@ -269,7 +269,9 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
 #pragma unroll
             for (int u = 0; u < U; ++u) vv[u].cut(S - base - 16 * u, t);
         }
-        // O^T += V^T P^T
+        // O^T += V^T P^T (fp32: each step's products on their own, then a rounded add.  The
+        // MMA cuts what it adds to: over thousands of keys that would show, 5e-6 of the
+        // result over 3000 against 5e-7.)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const typename Values::Scales vsc = vv[u].scales();
@@ -281,8 +283,16 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
                 for (int mm = 0; mm < 4; ++mm)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma<F16>(o[n][4 * i + mm], a[mm], pb[n][u][0], pb[n][u][1]);
-                        if constexpr (F32) mma<F16>(o[n][4 * i + mm], a[mm], pl[n][u][0], pl[n][u][1]);
+                        float(&acc)[4] = o[n][4 * i + mm];
+                        if constexpr (F32) {
+                            float x[4];
+                            mma_first<F16>(x, a[mm], pl[n][u][0], pl[n][u][1]);
+                            mma<F16>(x, a[mm], pb[n][u][0], pb[n][u][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[e] += x[e];
+                        } else {
+                            mma<F16>(acc, a[mm], pb[n][u][0], pb[n][u][1]);
+                        }
                     }
             }
         }
