@@ -172,7 +172,7 @@ pa_status dense_launch(const WalkCall& c, const DensePlan& t) {
 
 }  // namespace
 
-// Where the packed query lies: after the tiles' own part and the log-sum-exps.
+// Where the weights' scratch lies: after the tiles' own part and the log-sum-exps.
 static size_t tiles_scratch(const pa_shape& sh, int sm_count) {
     return align_up(align_up(tiles_workspace_bytes(sh, sm_count), 256) + static_cast<size_t>(sh.B) * sh.H_q * sh.L * 4, 256);
 }

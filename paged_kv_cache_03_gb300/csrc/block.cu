@@ -10,6 +10,10 @@
 // and, 4-bit, written dequantised when it ends.  A 256-byte row holds its even
 // 16-byte chunks first, then the odd ones, both permuted by the row's low bits:
 // the writers (32 bytes a lane) and ldmatrix meet no bank conflict.
+//
+// Bound by the warp-level products, twice as many for fp32's two parts: 64 fp32 rows
+// over 8 sequences of 1000 .. 8000 4-bit keys, 8 kv heads, 82 us; 204 over 2 of 6400 ..
+// 13000, 4 kv heads, with weights 114 us.
 #include "walk.cuh"
 
 namespace pa {

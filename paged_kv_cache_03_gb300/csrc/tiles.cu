@@ -1,10 +1,12 @@
-// q4_tiles.cu -- many query rows over 4-bit pages on tcgen05 tensor cores.
+// tiles.cu -- many query rows over 4-bit pages, or over bf16 pages with key weights, on
+// tcgen05 tensor cores.
 //
 // The attention of walk.cu for bf16 queries with many rows per kv head: S = Q K^T
 // and O += P V with 128 x 128 tiles, K and V dequantised to f16 on chip (a 4-bit
 // value is exact in f16), Q scaled by a power of two per row into f16's range
 // (exact), P rounded to f16 (2^-12), max, sums and O in fp32.  Row sums add the
-// unrounded weights, so the log-sum-exp that the key weights need is exact.
+// unrounded weights, so the log-sum-exp that the key weights need is exact.  Over bf16
+// pages Q, K, V and P are bf16 (P rounded to 2^-9).
 //
 // Layout on GB300: one CTA per SM, four warpgroups.
 //   * The 128 rows of a query tile are Lt = 128 / G consecutive positions of the
@@ -15,8 +17,8 @@
 //     states that tile_merge_kernel joins.
 //   * Warps 0-3 read codes and scales (a tile ahead, in registers), dequantise and
 //     store K and V tiles into two-slot rings in shared memory in the 128-byte
-//     swizzle the MMA reads: about 420 instructions a warp and tile, hidden behind
-//     the tile's products.  No dequantised byte ever leaves the SM.
+//     swizzle the MMA reads, hidden behind the tile's products; bf16 rows come by
+//     16-byte asynchronous copies.  No dequantised byte ever leaves the SM.
 //   * Warp 4 issues tcgen05.mma in the order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1):
 //     one tile's softmax overlaps the other's products.
 //   * Warps 8-11 (tile A) and 12-15 (tile B) have one query row per thread: they
@@ -27,6 +29,11 @@
 //     take those rows over every staged K/V tile with warp-level MMA.
 //   * All waits are bounded; on a timeout the CTA records PA_FLAG_TIMEOUT, frees
 //     its TMEM and exits.
+//
+// Bound by the exponentials and the dependent steps of a tile pair (products, softmax,
+// products), and with one tile pair per kv head by the dequantisation.  Measured with the
+// merge (G = 4, H_kv = 8): 8 sequences of 1000 .. 8000 4-bit keys 65 us at 64 positions, 77 at
+// 65 (a last tile of 4 rows), 55 at 16.
 #include <algorithm>
 #include <cfloat>
 #include <climits>

@@ -28,9 +28,14 @@
 // Max, sums and O are fp32.  The running max moves only when it grows by more
 // than 2^8, so O is rarely rescaled.
 //
-// Weights: walk_weights_kernel repeats K Q^T for 16 keys a warp over all rows
-// with the row's final log-sum-exp and adds the rows' probabilities in a fixed
-// order (no atomics: a call's results repeat bit for bit).
+// Weights: with few rows the scores are left for weights.cu, which adds the rows'
+// probabilities in a fixed order (no atomics: a call's results repeat bit for bit).
+//
+// Measured (G = 4, H_kv = 8, one query position, L2 flushed): 16 sequences of 32768
+// 4-bit keys 118 us, 5.1 TB/s of rows read; 64 of 128 .. 4096 45 us, 3.5 TB/s: bound by
+// the conversions of codes to f16, which issue at half rate, and with short contexts by
+// the start and the merge of each segment; 64 of 128 .. 4096 bf16 keys with weights 107 us,
+// 5.3 TB/s.
 #include "walk.cuh"
 
 namespace pa {

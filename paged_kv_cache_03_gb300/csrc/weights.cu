@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kWarps * 32) pack_query_kernel(const WalkParam
 // runs over the packed query rows (16 bytes a lane and k-step pair, shared by its
 // warps through L1), the next 8 rows requested before these are multiplied.  Bound
 // by the warp-level MMA rate (8 cycles per m16n8k16 and SM sub-partition).  Few keys
-// and many rows: the rows are cut into runs, whose sums add_splits_kernel adds.
+// and many rows: the rows are cut into runs, whose sums add_splits_kernel adds (with bf16
+// rows then: 7 heads x 196 rows over 196 keys 90 us without runs, 39 with).
 __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WalkParams p, int ntile, const Packed pk,
                                                               const RowSplits sp) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

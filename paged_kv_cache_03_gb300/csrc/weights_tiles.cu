@@ -10,8 +10,9 @@
 // a tile run while the tile before it is summed.  Three CTAs on an SM take the items in
 // turn, the next item's 4-bit rows in registers before this one's sums: a CTA per item
 // spent most of its time on its start (8 x 4 heads x 32 rows over 1000 .. 8000 keys, 8 kv
-// heads: 59 us with a CTA per item, 45 so).  Bound by instruction latency: 12 warps an
-// SM, each key's row costing a multiply-add, a MUFU exponential and an add.
+// heads: 59 us with a CTA per item, 36 so).  Items cycle over the heads first: over the
+// tiles first, a CTA met the same part of every sequence (50 us).  Bound by instruction
+// latency: 12 warps an SM, a key and row costing a multiply-add, an exponential and an add.
 #include "stage.cuh"
 #include "tc.cuh"
 #include "walk.cuh"
