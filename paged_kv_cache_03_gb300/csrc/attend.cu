@@ -75,20 +75,20 @@ pa_status launch(const WalkParams& p, const WalkPlan& w, bool q4, bool f32, cons
     return w.scores ? weights_from_scores(p, stream) : weights_from_keys(p, q4, f32, scratch, dev, stream);
 }
 
-// Rows per kv head from which bf16 queries go to the tensor-core tiles of tiles.cu.
-// 4-bit pages, measured (walk, block, tiles, us; G = 4, H_kv = 8): B = 8 over 1000 ..
-// 8000 keys 54, 50, 55 at 48 rows, 65, 53, 55 at 64, 89, 87, 55 at 96; B = 1 over 16000
-// keys 52, 49, 46 at 128; B = 64 over 500 .. 2000 keys 152, 109, 114 at 64.  bf16 pages
-// with key weights (walk, tiles, us at 24 rows): B = 8 over 1000 .. 8000 keys 83, 83, at 40
-// 101 (block), 85; B = 64 over 500 .. 2000 179, 146; B = 1 over 16000 42, 56; B = 2 over 500
-// 18, 32: the tiles from fewer rows where the keys are many.
-constexpr int kTileRows = 64, kTileRowsBf16 = 24;
-constexpr long long kTileKeysBf16 = 1 << 18;  // of all (sequence, kv head)
+// Rows per kv head from which bf16 queries go to the tensor-core tiles of tiles.cu: fewer
+// where the keys of all (sequence, kv head) are many.  Measured (walk or block, tiles, us;
+// G = 4, H_kv = 8).  4-bit pages, 40 rows: 64 sequences of 500 .. 2000 keys 115, 98; 8 of
+// 1000 .. 8000 55, 49; one of 16000 33, 33; 2 of 900 16, 25; 32 rows: 86, 98; 43, 49; 27, 33.
+// At 56 rows 2 of 900 22, 25.  bf16 pages with key weights, 20 rows: 171, 138; 79, 79; one of
+// 16000 42, 46, at 40 50, 48; 2 of 500 18, 30.
+constexpr int kTileRows = 64, kTileRowsMany = 40, kTileRowsManyBf16 = 20;
+constexpr long long kManyKeys = 1 << 17, kManyKeysBf16 = 1 << 18;
 
 bool tiles_take(const pa_shape& sh, bool q4, int sm_count) {
     const long long R = static_cast<long long>(sh.H_q / sh.H_kv) * sh.L;
     const long long keys = static_cast<long long>(sh.B) * sh.H_kv * sh.max_pages_per_seq * sh.page_size;
-    return sh.dtype == PA_BF16 && (R >= kTileRows || (!q4 && R >= kTileRowsBf16 && keys >= kTileKeysBf16)) &&
+    const bool many = keys >= (q4 ? kManyKeys : kManyKeysBf16);
+    return sh.dtype == PA_BF16 && R >= (!many ? kTileRows : q4 ? kTileRowsMany : kTileRowsManyBf16) &&
            tiles_supported(sh, sm_count);
 }
 

@@ -8,6 +8,7 @@
 
 namespace pa {
 
+constexpr int kRawStage = 32 * (kQ4CodeBytes + kQ4Groups);  // bytes of 32 4-bit rows
 constexpr int kStageHalf = 128 * 128;  // bytes of 128 rows x 64 dims, one swizzled column block
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
@@ -62,6 +63,31 @@ struct RawTile {
             const int row = __shfl_sync(0xffffffffu, rows, 8 * i + rl);
             ldg_or_zero(codes + static_cast<long long>(row) * kQ4CodeBytes + 16 * q,
                         scales + static_cast<long long>(row) * kQ4Groups + 2 * q, row >= 0, c[i], s[i]);
+        }
+    }
+    // The same by way of a warp's kRawStage bytes of shared memory (copy; the caller
+    // commits, waits and synchronises the warp; read).
+    __device__ __forceinline__ static void copy(uint32_t stage, const uint8_t* codes, const uint8_t* scales, int rows,
+                                                int lane) {
+        const int q = quarter(lane), rl = row_of(lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = __shfl_sync(0xffffffffu, rows, 8 * i + rl);
+            cp_async16(stage + 512 * i + 16 * lane,
+                       codes + (row < 0 ? 0 : static_cast<long long>(row) * kQ4CodeBytes) + 16 * q, row >= 0);
+        }
+        cp_async8(stage + 2048 + 8 * lane, scales + (rows < 0 ? 0 : static_cast<long long>(rows) * kQ4Groups), rows >= 0);
+    }
+    __device__ __forceinline__ void read(uint32_t stage, int lane) {
+        const uint32_t at = stage + 2048 + 8 * row_of(lane) + 2 * quarter(lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(c[i].x), "=r"(c[i].y), "=r"(c[i].z), "=r"(c[i].w)
+                         : "r"(stage + 512 * i + 16 * lane));
+            uint16_t h;
+            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(at + 64 * i));
+            s[i] = h;
         }
     }
     template <bool BF16>

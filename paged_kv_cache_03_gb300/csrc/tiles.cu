@@ -30,10 +30,13 @@
 //   * All waits are bounded; on a timeout the CTA records PA_FLAG_TIMEOUT, frees
 //     its TMEM and exits.
 //
-// Bound by the exponentials and the dependent steps of a tile pair (products, softmax,
-// products), and with one tile pair per kv head by the dequantisation.  Measured with the
-// merge (G = 4, H_kv = 8): 8 sequences of 1000 .. 8000 4-bit keys 65 us at 64 positions, 77 at
-// 65 (a last tile of 4 rows), 55 at 16.
+// Two query tiles are bound by the products as they are issued (about 3600 cycles of a
+// key tile's 4200, both operands of Q K^T from shared memory).  One query tile (ONE) would
+// wait for its own chain of product, softmax and product: so both softmax warpgroups take
+// it, each every other key tile, which leaves the dequantisation as the bound.  Measured
+// with the merge (G = 4, H_kv = 8): 8 sequences of 1000 .. 8000 4-bit keys 51 us at 16 or 32
+// positions (63 with one warpgroup), 74 at 64, 88 at 65 (a last tile of 4 rows); 64 of
+// 500 .. 2000 100, 143, 184.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -71,12 +74,21 @@ enum Bar {
     kMmaDone = 18,
     kItemFull = 19,   // + slot: a piece is published
     kItemEmpty = 23,  // + slot: every role is done with it
-    kNumBars = 28     // (even: what follows stays 16-byte aligned)
+    kXFull = 27,      // + parity of a piece (ONE): B's max and sum
+    kNumBars = 30     // (even: what follows stays 16-byte aligned)
 };
 constexpr int kOffItems = kOffBar + kNumBars * 8;  // four slots
 constexpr int kOffTmemSlot = kOffItems + 4 * 64;
 constexpr int kOffAbort = kOffTmemSlot + 8;
-constexpr int kSmemBytes = kOffAbort + 8 + 1024;  // slack to align the base
+constexpr int kOffX = kOffAbort + 8;         // ONE: [2][128] max and sum of B's rows
+constexpr int kOffRaw = kOffX + 2 * BM * 8;  // ONE: [warp][K, V] 4-bit rows on their way
+// With slack to align the base.  Two tiles' loads go through L1, and with more than 196 KB
+// of shared memory an SM keeps 28 KB of it instead of 60: 64 sequences of 500 .. 2000 keys,
+// 256 rows, 149 us instead of 141.
+constexpr int smem_bytes(bool q4, bool one) {
+    return (!one ? kOffX : q4 ? kOffRaw + 4 * 2 * kRawStage : kOffRaw) + 1024;
+}
+static_assert(kOffRaw % 16 == 0, "16-byte copies");
 
 struct TileParams {
     const uint16_t* q;
@@ -165,8 +177,11 @@ struct Piece {
         }
         cut(p, seg, end);
     }
-    // Key tiles of this piece that query tile t takes: the first of them.
+    // Key tiles of this piece that query tile t takes: the first of them (one query tile
+    // for both: A the even ones, B the odd ones).
+    template <bool ONE>
     __device__ __forceinline__ int tiles(const TileParams& p, int t) const {
+        if constexpr (ONE) return (n + 1 - t) >> 1;
         const int m = 2 * mp + t;
         if (m >= p.nM) return 0;
         return max(0, min(j0 + n, key_tiles(p, S, tile_end(p, m) - 1)) - j0);
@@ -178,6 +193,7 @@ struct Piece {
 struct Item {
     int b, S, kvh, mp, ng, j0, n;  // n = 0: no more
     int tiles[2];
+    int before_b;  // key tiles of B in earlier pieces
 };
 static_assert(sizeof(Item) <= 64, "item slot");
 
@@ -208,7 +224,9 @@ __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <bool Q4>
+// ONE: all rows of a (sequence, kv head) fit one query tile, which both softmax
+// warpgroups take, each every other key tile; A joins the two states at a piece's end.
+template <bool Q4, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ int share[4];  // all units, units per share, first sequence, its first unit
@@ -302,6 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
             mbar_init(bar(kOFree + s), 4);
         }
         mbar_init(bar(kMmaDone), 1);
+        mbar_init(bar(kXFull), 4);
+        mbar_init(bar(kXFull + 1), 4);
         for (int s = 0; s < 4; ++s) {
             mbar_init(bar(kItemFull + s), 1);
             // producers, the MMA thread, softmax warps, warps 5 and 6
@@ -345,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
         };
         bool ok = take(0);
         int k = 0, g = 0;  // piece, tiles so far
-        if constexpr (Q4) if (ok && slot(0)->n > 0) {
+        if constexpr (Q4 && !ONE) if (ok && slot(0)->n > 0) {
             RawTile rk, rv;
             int j = slot(0)->j0, last = j + slot(0)->n - 1;
             lookup(slot(0)->b, slot(0)->S, slot(0)->kvh, j);
@@ -391,6 +411,70 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                 ++g;
                 if (more) rv.request(p.vc, p.vs, rows, lane);
             }
+        }
+        // One query tile: a key tile's time is short, and the loads above, which ptxas waits
+        // for where they are issued, would set it.  The rows are copied to this warp's staging
+        // a tile ahead: K of tile g + 1 when K of tile g is stored, V likewise, one group of
+        // copies each.  (64 rows over 8 sequences of 1000 .. 8000 keys: loads 61 us, copies
+        // 59, copies and both warpgroups on the tile 52.  Two tiles of 260 rows: 88, 90.)
+        if constexpr (Q4 && ONE) if (ok && slot(0)->n > 0) {
+            const uint32_t raw_k = base + kOffRaw + warp * 2 * kRawStage, raw_v = raw_k + kRawStage;
+            RawTile raw;
+            int j = slot(0)->j0, last = j + slot(0)->n - 1;
+            lookup(slot(0)->b, slot(0)->S, slot(0)->kvh, j);
+            int rows = rows_of();
+            RawTile::copy(raw_k, p.kc, p.ks, rows, lane);
+            cp_async_commit();
+            RawTile::copy(raw_v, p.vc, p.vs, rows, lane);
+            cp_async_commit();
+            for (bool more = true; more;) {  // tile j of piece k is on its way
+                // the tile after it: its page ids are requested now
+                if (j < last) {
+                    ++j;
+                } else {
+                    release(k);
+                    ++k;
+                    ok = take(k);
+                    if (!ok) break;
+                    more = slot(k)->n > 0;
+                    j = slot(k)->j0;
+                    last = j + slot(k)->n - 1;
+                }
+                if (more) lookup(slot(k)->b, slot(k)->S, slot(k)->kvh, j);
+                const int s = g & 1;
+                cp_async_wait<1>();
+                __syncwarp();
+                raw.read(raw_k, lane);
+                if (g >= 2 && !warp_wait(bar(kKEmpty + s), ((g >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                raw.store<false>(base + kOffK + s * kTile, warp, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kKFull + s));
+                if (more) {
+                    rows = rows_of();
+                    RawTile::copy(raw_k, p.kc, p.ks, rows, lane);
+                }
+                cp_async_commit();
+                cp_async_wait<1>();
+                __syncwarp();
+                raw.read(raw_v, lane);
+                if (g >= 2 && !warp_wait(bar(kVEmpty + s), ((g >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (aborted(abort_flag)) break;
+                raw.store<false>(base + kOffV + s * kTile, warp, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kVFull + s));
+                ++g;
+                if (more) RawTile::copy(raw_v, p.vc, p.vs, rows, lane);
+                cp_async_commit();
+            }
+            cp_async_wait<0>();
         }
         if constexpr (!Q4) {
             // K of tile g is requested before V of tile g - 1 is announced, and V of tile
@@ -491,6 +575,40 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                 ok = mbar_wait(bar(kQFull), k & 1) && mbar_wait(bar(kKFull + (gk & 1)), (gk >> 1) & 1);
                 if (!ok || *abort_flag) break;
                 tc::fence_after_sync();
+                if constexpr (ONE) {  // key tile j belongs to t = j & 1
+                    qk(0, gk);
+                    tc::commit(bar(kKEmpty + (gk & 1)));
+                    if (nk > 1) {
+                        ok = mbar_wait(bar(kKFull + ((gk + 1) & 1)), ((gk + 1) >> 1) & 1);
+                        if (!ok || *abort_flag) break;
+                        tc::fence_after_sync();
+                        qk(1, gk + 1);
+                        tc::commit(bar(kKEmpty + ((gk + 1) & 1)));
+                    }
+                    if (nk <= 2) tc::commit(bar(kQEmpty));
+                    for (int j = 0; j < nk; ++j, ++gk) {
+                        const int t = j & 1, pc = t ? pc1++ : pc0++, oe = t ? oe1 : oe0;
+                        ok = mbar_wait(bar(kVFull + (gk & 1)), (gk >> 1) & 1) && mbar_wait(bar(kPFull + t), pc & 1);
+                        // the previous piece's epilogue has read O
+                        if (ok && j < 2 && oe > 0) ok = mbar_wait(bar(kOFree + t), (oe - 1) & 1);
+                        if (!ok || *abort_flag) break;
+                        tc::fence_after_sync();
+                        pv(t, j < 2, gk);
+                        tc::commit(bar(kVEmpty + (gk & 1)));
+                        if (j + 2 < nk) {
+                            ok = mbar_wait(bar(kKFull + (gk & 1)), ((gk + 2) >> 1) & 1);
+                            if (!ok || *abort_flag) break;
+                            tc::fence_after_sync();
+                            qk(t, gk + 2);
+                            tc::commit(bar(kKEmpty + (gk & 1)));
+                            if (j + 3 == nk) tc::commit(bar(kQEmpty));  // the piece's last Q.K^T
+                        }
+                    }
+                    if (!ok || *abort_flag) break;
+                    ++oe0;
+                    if (n1 > 0) ++oe1;
+                    continue;
+                }
                 if (n0 > 0) qk(0, gk);
                 if (n1 > 0) qk(1, gk);
                 tc::commit(bar(kKEmpty + (gk & 1)));
@@ -725,6 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                 if (it.n == 0) it.advance(p, end);  // the share's first segment ends before its first tile here
             }
             int4 crossing = make_int4(-1, 0, 0, 0);
+            int before_b = 0;
             for (int k = 0;; ++k) {
                 if (k >= 4 && !warp_wait(bar(kItemEmpty + (k & 3)), ((k >> 2) - 1) & 1)) {
                     if (lane == 0) give_up(p, abort_flag);
@@ -740,7 +859,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                     o->ng = it.ng;
                     o->j0 = it.j0;
                     o->n = n;
-                    for (int t = 0; t < 2; ++t) o->tiles[t] = n > 0 ? it.tiles(p, t) : 0;
+                    for (int t = 0; t < 2; ++t) o->tiles[t] = n > 0 ? it.template tiles<ONE>(p, t) : 0;
+                    o->before_b = before_b;
+                    before_b += o->tiles[1];
                     if (n > 0 && it.j0 == 0 && n < it.ng)  // it ends in a later share
                         crossing = make_int4(it.b, it.kvh, it.mp, (it.seg + kSegCost + it.ng - 1) / share[1]);
                     mbar_arrive(bar(kItemFull + (k & 3)));
@@ -766,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
         // buffer: the warp's 32 rows two at a time, 16 lanes a row.  The tile's last
         // S of the piece before must be done (no one else reads the buffer).
         auto fetch = [&](int k) {
-            const int m = 2 * slot(k)->mp + t, l_end = m < p.nM ? tile_end(p, m) : 0;
+            const int m = 2 * slot(k)->mp + (ONE ? 0 : t), l_end = m < p.nM ? tile_end(p, m) : 0;
             const uint16_t* const head = p.q + (static_cast<long long>(slot(k)->b) * p.H_q + slot(k)->kvh * p.G) * p.L * kD;
             const int c = lane & 15;
             int rr = q4 * 32 + (lane >> 4), gr = rr / p.Lt, dr = rr - gr * p.Lt;
@@ -828,10 +949,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
             ok = convert(0);
         }
         for (int k = 0; ok && slot(k)->n > 0; ++k) {
-            const int nk = slot(k)->tiles[t], tile0 = slot(k)->j0 * BN;
+            const int nk = slot(k)->tiles[t];
+            int key0 = (slot(k)->j0 + (ONE ? t : 0)) * BN;
             int lim = slot(k)->S - 1, lim_min = lim;  // the last key this row sees, the tile's first
             if (p.causal) {
-                const int l0 = (2 * slot(k)->mp + t) * p.Lt + slot(k)->S - p.L;
+                const int l0 = (2 * slot(k)->mp + (ONE ? 0 : t)) * p.Lt + slot(k)->S - p.L;
                 lim = l0 + dl;
                 lim_min = l0;
             }
@@ -852,7 +974,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                     fetch(k + 1);
                     fetched = true;
                 }
-                const int key0 = tile0 + j * BN;
                 if (key0 + BN - 1 > lim_min) {
                     const int cmax = lim - key0;
 #pragma unroll
@@ -861,6 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                         for (int e = 0; e < 32; ++e)
                             if (cc * 32 + e > cmax) x[cc][e] = neg_inf();
                 }
+                key0 += ONE ? 2 * BN : BN;
                 float mq[4];
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) {
@@ -922,12 +1044,39 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                 if (!ok) break;
             }
             const volatile Item* const done = slot(k);
+            float l1 = lsum.x + lsum.y;
+            if (ONE && t == 1) {  // A joins this half with its own
+                float2* const x = reinterpret_cast<float2*>(sbase + kOffX) + (k & 1) * BM + r;
+                *x = make_float2(l1 > 0.f ? mrow : neg_inf(), l1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kXFull + (k & 1)));
+                sc += nk;
+                release(k);
+                continue;
+            }
             const int m = 2 * done->mp + t, l = m * p.Lt + dl;
             const bool valid = m < p.nM && g < p.G && l < tile_end(p, m);
-            const float l1 = lsum.x + lsum.y;
             const bool full = done->n == done->ng;
             const long long row = (static_cast<long long>(done->b) * p.H_q + done->kvh * p.G + g) * p.L + l;
             const long long part = ((2ll * blockIdx.x + (done->j0 > 0 ? 0 : 1)) * 2 + t) * BM + r;
+            const int nb = ONE ? done->tiles[1] : 0;  // key tiles of the other half
+            float own = 1.f, other = 0.f;
+            if constexpr (ONE) {
+                ok = warp_wait(bar(kXFull + (k & 1)), (k >> 1) & 1);
+                if (!ok) break;
+                const float2 x = reinterpret_cast<const float2*>(sbase + kOffX)[(k & 1) * BM + r];
+                if (nb > 0 && x.x != neg_inf()) {
+                    const float M = fmaxf(mrow, x.x);
+                    own = fast_exp2(mrow - M);
+                    other = fast_exp2(x.x - M);
+                    l1 = l1 * own + x.y * other;
+                    mrow = M;
+                }
+                if (nb > 0) {
+                    ok = warp_wait(bar(kODone + 1), (done->before_b + nb - 1) & 1);
+                    if (!ok) break;
+                }
+            }
             if (!full) p.part_ml[part] = make_float2(l1 > 0.f ? mrow : neg_inf(), l1);
             if (nk > 0) {
                 ok = warp_wait(bar(kODone + t), (sc + nk - 1) & 1);
@@ -940,6 +1089,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                     __syncwarp();
                     tc::ld32(trow + 256u + 128u * t + cc * 32, o);
                     tc::wait_ld();
+                    if (nb > 0) {  // (uniform)
+                        float o2[32];
+                        tc::ld32(trow + 256u + 128u + cc * 32, o2);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = o[e] * own + o2[e] * other;
+                    }
                     if (!valid) continue;
                     if (full) {
                         uint32_t w[16];
@@ -964,7 +1120,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                 // O of this tile is read: the next piece's first P.V may overwrite it
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kOFree + t));
+                if (lane == 0) {
+                    mbar_arrive(bar(kOFree + t));
+                    if (nb > 0) mbar_arrive(bar(kOFree + 1));
+                }
             }
             if (full && valid && p.lse) p.lse[row] = l1 > 0.f ? mrow + log2f(l1) : __int_as_float(0x7f800000);
             sc += nk;
@@ -1104,15 +1263,16 @@ TilePlan plan(const pa_shape& sh, int sm_count) {
     return t;
 }
 
-template <bool Q4>
+template <bool Q4, bool ONE>
 pa_status launch_tiles(const TileParams& p, const WalkCall& c) {
     static int attr_done[64] = {0};
     if (!attr_done[c.dev.device]) {
-        if (cudaFuncSetAttribute(tile_kernel<Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+        if (cudaFuncSetAttribute(tile_kernel<Q4, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 smem_bytes(Q4, ONE)) != cudaSuccess)
             return PA_ERR_CUDA;
         attr_done[c.dev.device] = 1;
     }
-    tile_kernel<Q4><<<static_cast<unsigned>(c.dev.sm_count), kThreads, kSmemBytes, c.stream>>>(p);
+    tile_kernel<Q4, ONE><<<static_cast<unsigned>(c.dev.sm_count), kThreads, smem_bytes(Q4, ONE), c.stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -1132,7 +1292,7 @@ size_t tiles_workspace_bytes(const pa_shape& sh, int sm_count) { return plan(sh,
 
 pa_status tiles_launch(const WalkCall& c, float* lse) {
     const pa_shape& sh = c.sh;
-    if (c.dev.smem_optin < kSmemBytes) return PA_ERR_UNSUPPORTED;
+    if (c.dev.smem_optin < smem_bytes(true, true)) return PA_ERR_UNSUPPORTED;
     const TilePlan t = plan(sh, c.dev.sm_count);
     if (c.ws_bytes < t.total) return PA_ERR_WORKSPACE;
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
@@ -1171,7 +1331,8 @@ pa_status tiles_launch(const WalkCall& c, float* lse) {
     p.scale_log2 = c.scale * 1.4426950408889634f;
     p.min_per = kMinPer;
     p.out32 = reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
-    const pa_status st = c.ks ? launch_tiles<true>(p, c) : launch_tiles<false>(p, c);
+    const pa_status st = t.nM > 1 ? (c.ks ? launch_tiles<true, false>(p, c) : launch_tiles<false, false>(p, c))
+                                  : (c.ks ? launch_tiles<true, true>(p, c) : launch_tiles<false, true>(p, c));
     if (st != PA_OK) return st;
     const int shares = c.dev.sm_count;
     const int ny = (t.nM > 1 ? 2 : 1) * BM / kMergeRows;

@@ -69,8 +69,14 @@ PATHS = [
     Case(600, 8, 1, 8, 16, spread(600, 8, 90), spare=6),
     Case(600, 8, 1, 8, 16, spread(600, 8, 90), pool="bf16", spare=6),
     Case(520, 4, 1, 33, 16, spread(520, 33, 80), spare=15),
+    # few rows, tables wide enough to count as many keys
+    Case(2, 4, 2, 10, 16, [900, 90], spare=2100),
+    Case(2, 4, 2, 5, 16, [900, 90], pool="bf16", spare=4200),
+    # one query tile: a sequence's pieces of one, two and more key tiles
+    Case(90, 8, 2, 16, 16, spread(90, 16, 700)),
+    Case(90, 4, 2, 25, 16, spread(90, 25, 700), pool="bf16"),
 ], ids=str)
-def test_many_sequences(c):
+def test_many_sequences_and_wide_tables(c):
     inp = ref.Inputs(c)
     d = inp.device()
     ws = workspace(c, d)
