@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                 if (more) rv.request(p.vc, p.vs, rows, lane);
             }
         }
-        // One query tile: a key tile's time is short, and the loads above, which ptxas waits
-        // for where they are issued, would set it.  The rows are copied to this warp's staging
+        // One query tile: a key tile's time is short, and the loads above, whose wait comes
+        // right after their issue (1500 cycles a tile), would set it.  The rows are copied to this warp's staging
         // a tile ahead: K of tile g + 1 when K of tile g is stored, V likewise, one group of
         // copies each.  (64 rows over 8 sequences of 1000 .. 8000 keys: loads 61 us, copies
         // 59, copies and both warpgroups on the tile 52.  Two tiles of 260 rows: 88, 90.)
@@ -1169,12 +1169,14 @@ struct RowState {
     }
 };
 
-constexpr int kMergeRows = 4;  // rows per merge CTA, one a warp
+// Rows per merge CTA, one a warp (8, 4 rows, us for the call: 2 sequences of 900 keys, 256
+// rows 33, 37; one of 16000 45, 47).
+constexpr int kMergeRows = 8;
 
 // Merges the partial states of the segments that cross shares: CTA y + ny c takes rows
-// 4 y .. of the segment that starts in share c, four partial states a warp in flight;
-// then two CTAs for the remainder rows of each (sequence, kv head).
-__global__ void __launch_bounds__(128) tile_merge_kernel(const TileParams p, int shares, int ny) {
+// 8 y .. of the segment that starts in share c, four partial states a warp in flight;
+// then a CTA for the remainder rows of each (sequence, kv head).
+__global__ void __launch_bounds__(256) tile_merge_kernel(const TileParams p, int shares, int ny) {
     pdl_launch_dependents();
     pdl_wait_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1206,7 +1208,7 @@ __global__ void __launch_bounds__(128) tile_merge_kernel(const TileParams p, int
         store_row(p, (static_cast<long long>(sp.x) * p.H_q + sp.y * p.G + g) * p.L + pos, lane, st.acc, st.l, st.M);
         return;
     }
-    const int bk = rest >> 1, rr = kMergeRows * (rest & 1) + warp;
+    const int bk = rest, rr = warp;
     if (rr >= p.nrem) return;
     const int b = bk / p.H_kv, kvh = bk - b * p.H_kv;
     bool bad;
@@ -1336,8 +1338,8 @@ pa_status tiles_launch(const WalkCall& c, float* lse) {
     if (st != PA_OK) return st;
     const int shares = c.dev.sm_count;
     const int ny = (t.nM > 1 ? 2 : 1) * BM / kMergeRows;
-    const dim3 grid(static_cast<unsigned>(shares * ny + (t.nrem ? 2 * sh.B * sh.H_kv : 0)));
-    return launch_dependent(tile_merge_kernel, grid, 128, 0, c.stream, p, shares, ny) ? PA_OK : PA_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(shares * ny + (t.nrem ? sh.B * sh.H_kv : 0)));
+    return launch_dependent(tile_merge_kernel, grid, 256, 0, c.stream, p, shares, ny) ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace pa
