@@ -611,8 +611,9 @@ def _weights_shape(name, w, B_, H_kv, capacity):
 def _launch(name, index, fn, *args):
     """fn(*args, stream) with device `index` current, on its current stream."""
     torch = _torch or _load_torch()
-    if torch.cuda.current_device() == index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    raw = torch._C  # (the tensors are there, so CUDA is initialised)
+    if raw._cuda_getDevice() == index:
+        st = fn(*args, raw._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
             st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
@@ -653,7 +654,7 @@ def append_kv_q4(k_new, v_new, pool, block_table, context_lens, *, workspace=Non
     _on_device(index, ("k_new", k_new), ("v_new", v_new), ("block_table", block_table),
                ("context_lens", context_lens), ("workspace", workspace))
     shape = pa_shape(B_, H_kv, H_kv, L, D, P, ps, block_table.shape[1], _dtype_id(k_new.dtype))
-    _launch("pa_append_kv_q4", index, load().pa_append_kv_q4, ctypes.byref(shape),
+    _launch("pa_append_kv_q4", index, (_lib or load()).pa_append_kv_q4, ctypes.byref(shape),
             k_new.data_ptr(), v_new.data_ptr(), ctypes.byref(pool.c_pool),
             block_table.data_ptr(), context_lens.data_ptr(), workspace.data_ptr(),
             workspace.numel())
@@ -678,7 +679,7 @@ def gather_kv_q4(pool, block_table, context_lens, n, *, tail=False, dtype=None, 
     shape = pa_shape(B_, H_kv, H_kv, 1, 128, P, ps, block_table.shape[1], _dtype_id(dtype))
     k = torch.empty((B_, H_kv, n, 128), dtype=dtype, device=pool.device)
     v = torch.empty_like(k)
-    _launch("pa_gather_kv_q4", index, load().pa_gather_kv_q4, ctypes.byref(shape),
+    _launch("pa_gather_kv_q4", index, (_lib or load()).pa_gather_kv_q4, ctypes.byref(shape),
             ctypes.byref(pool.c_pool), block_table.data_ptr(), context_lens.data_ptr(), n,
             bool(tail), k.data_ptr(), v.data_ptr(), workspace.data_ptr(), workspace.numel())
     return k, v
@@ -764,7 +765,7 @@ def paged_attention_q4(query, pool, block_table, context_lens, page_size, scale=
         raise ValueError(f"query must be on {pool.device}")
     if workspace is None:
         workspace = new_q4_workspace(query, pool, block_table, key_weights_out is not None)
-    return _attend("pa_paged_attention_q4", load().pa_paged_attention_q4,
+    return _attend("pa_paged_attention_q4", (_lib or load()).pa_paged_attention_q4,
                    (ctypes.byref(pool.c_pool),), shape, query, block_table, context_lens,
                    page_size, scale, causal, key_weights, key_weights_out, out, workspace)
 
@@ -789,7 +790,7 @@ def paged_attention_weights(query, key_pages, value_pages, block_table, context_
         raise ValueError("key_weights_out is what this call is for: use paged_attention")
     if workspace is None:
         workspace = new_weights_workspace(query, key_pages, block_table)
-    return _attend("pa_paged_attention_weights", load().pa_paged_attention_weights,
+    return _attend("pa_paged_attention_weights", (_lib or load()).pa_paged_attention_weights,
                    (key_pages.data_ptr(), value_pages.data_ptr()), shape, query, block_table,
                    context_lens, page_size, scale, causal, key_weights, key_weights_out, out,
                    workspace)
@@ -832,7 +833,7 @@ def evict_kv(key_pages, value_pages, block_table, context_lens, key_weights, kee
     dims = _pages_dims(key_pages, value_pages)
     if key_pages.shape[3] != 128:
         raise ValueError("head dim must be 128")
-    return _evict("pa_evict_kv", load().pa_evict_kv,
+    return _evict("pa_evict_kv", (_lib or load()).pa_evict_kv,
                   (key_pages.data_ptr(), value_pages.data_ptr()), dims,
                   _dtype_id(key_pages.dtype), key_pages.device, block_table, context_lens,
                   key_weights, keep, recent, dst_block_table, workspace)
@@ -842,6 +843,6 @@ def evict_kv(key_pages, value_pages, block_table, context_lens, key_weights, kee
 def evict_kv_q4(pool, block_table, context_lens, key_weights, keep, recent, dst_block_table, *,
                 workspace=None) -> Evicted:
     """evict_kv of a 4-bit pool."""
-    return _evict("pa_evict_kv_q4", load().pa_evict_kv_q4, (ctypes.byref(pool.c_pool),),
+    return _evict("pa_evict_kv_q4", (_lib or load()).pa_evict_kv_q4, (ctypes.byref(pool.c_pool),),
                   pool.dims, PA_BF16, pool.device, block_table, context_lens, key_weights, keep,
                   recent, dst_block_table, workspace)
