@@ -6,34 +6,54 @@ namespace pa {
 namespace walk {
 namespace {
 
+constexpr int kSumKeys = 4;  // keys of a thread of walk_sum_kernel
+
 // w_out[b, kvh, k] = w_in[b, kvh, k] + the rows' probabilities of key k, 0 past
-// the context, from the scores that walk_kernel left.  One thread per key; the
-// R scores of a key lie together, so a warp reads them as whole lines.
+// the context, from the scores that walk_kernel left.  Four keys per thread, 256
+// apart, their loads together (64 sequences of 128 .. 4096 4-bit keys, 4 rows, the call:
+// 65 us with one key a thread, 60 with four); the R scores of a key lie together, so a
+// warp reads them as whole lines.  Bound by the scores read and the weights' lines.
 __global__ void __launch_bounds__(256) walk_sum_kernel(const WalkParams p, int ntile) {
-    pdl_wait_primary();
     const int tile = static_cast<int>(blockIdx.x) % ntile;
     const long long bk = static_cast<int>(blockIdx.x) / ntile;
-    const long long k = static_cast<long long>(tile) * 256 + threadIdx.x;
-    if (k >= p.w_S) return;
+    const long long k0 = static_cast<long long>(tile) * (256 * kSumKeys) + threadIdx.x;
+    pdl_wait_primary();
     const int S = seq_len(p, static_cast<int>(bk / p.H_kv), false);
-    float acc = 0.f;
-    if (k < S) {
-        const float* const x = p.score + (bk * p.cap + k) * p.R;
-        const float* const lse = p.lse + bk * p.R;
-        if (p.R % 4 == 0) {
-            for (int r = 0; r < p.R; r += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(x + r);
-                acc += fast_exp2(v.x - lse[r]);
-                acc += fast_exp2(v.y - lse[r + 1]);
-                acc += fast_exp2(v.z - lse[r + 2]);
-                acc += fast_exp2(v.w - lse[r + 3]);
+    const float* const x = p.score + bk * p.cap * p.R;
+    const float* const lse = p.lse + bk * p.R;
+    float acc[kSumKeys] = {}, old[kSumKeys] = {};
+#pragma unroll
+    for (int j = 0; j < kSumKeys; ++j)
+        if (p.w_in && k0 + 256 * j < S) old[j] = p.w_in[bk * p.w_S + k0 + 256 * j];
+    if (p.R % 4 == 0) {
+        for (int r = 0; r < p.R; r += 4) {
+            float4 v[kSumKeys];
+#pragma unroll
+            for (int j = 0; j < kSumKeys; ++j)
+                if (k0 + 256 * j < S) v[j] = *reinterpret_cast<const float4*>(x + (k0 + 256 * j) * p.R + r);
+            const float l[4] = {lse[r], lse[r + 1], lse[r + 2], lse[r + 3]};
+#pragma unroll
+            for (int j = 0; j < kSumKeys; ++j) {
+                if (k0 + 256 * j >= S) continue;
+                acc[j] += fast_exp2(v[j].x - l[0]);
+                acc[j] += fast_exp2(v[j].y - l[1]);
+                acc[j] += fast_exp2(v[j].z - l[2]);
+                acc[j] += fast_exp2(v[j].w - l[3]);
             }
-        } else {
-            for (int r = 0; r < p.R; ++r) acc += fast_exp2(x[r] - lse[r]);
         }
-        if (p.w_in) acc += p.w_in[bk * p.w_S + k];
+    } else {
+        for (int r = 0; r < p.R; ++r) {
+            const float l = lse[r];
+#pragma unroll
+            for (int j = 0; j < kSumKeys; ++j)
+                if (k0 + 256 * j < S) acc[j] += fast_exp2(x[(k0 + 256 * j) * p.R + r] - l);
+        }
     }
-    p.w_out[bk * p.w_S + k] = acc;
+#pragma unroll
+    for (int j = 0; j < kSumKeys; ++j) {
+        const long long k = k0 + 256 * j;
+        if (k < p.w_S) p.w_out[bk * p.w_S + k] = k < S ? acc[j] + old[j] : 0.f;
+    }
 }
 
 // The packed query: the rows of every (sequence, kv head) as B fragments, [part]
@@ -233,7 +253,7 @@ pa_status weights_of_f32(const WalkParams& p, const RowSplits& sp, void* scratch
 }  // namespace
 
 pa_status weights_from_scores(const WalkParams& p, cudaStream_t stream) {
-    const long long bk = static_cast<long long>(p.B) * p.H_kv, ntile = (p.w_S + 255) / 256;
+    const long long bk = static_cast<long long>(p.B) * p.H_kv, ntile = (p.w_S + 256 * kSumKeys - 1) / (256 * kSumKeys);
     return launch_dependent(walk_sum_kernel, dim3(static_cast<unsigned>(ntile * bk)), 256, 0, stream, p,
                             static_cast<int>(ntile))
                ? PA_OK
