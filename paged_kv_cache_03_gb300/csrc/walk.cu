@@ -34,8 +34,8 @@
 // Measured (G = 4, H_kv = 8, one query position, L2 flushed): 16 sequences of 32768
 // 4-bit keys 118 us, 5.1 TB/s of rows read; 64 of 128 .. 4096 45 us, 3.5 TB/s: bound by
 // the conversions of codes to f16, which issue at half rate, and with short contexts by
-// the start and the merge of each segment; 64 of 128 .. 4096 bf16 keys with weights 107 us,
-// 5.3 TB/s.
+// the start and the merge of each segment; 64 of 128 .. 4096 bf16 keys with weights 104 us,
+// 5.4 TB/s.
 #include "walk.cuh"
 
 namespace pa {
