@@ -74,7 +74,7 @@ enum Bar {
     kMmaDone = 18,
     kItemFull = 19,   // + slot: a piece is published
     kItemEmpty = 23,  // + slot: every role is done with it
-    kXFull = 27,      // + parity of a piece (ONE): B's max and sum
+    kXFull = 27,      // + slot (ONE): B's max and sum
     kNumBars = 30     // (even: what follows stays 16-byte aligned)
 };
 constexpr int kOffItems = kOffBar + kNumBars * 8;  // four slots
@@ -881,6 +881,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
         const uint32_t qrow = base + kOffQ + t * kTile;
         const int g = r / p.Lt, dl = r - g * p.Lt;
         int sc = 0;  // S fills and P.V products of this tile in earlier pieces
+        // ONE: B's states that A has taken, two slots in turn.  Only a piece in which B has
+        // key tiles hands one over: B then waited for an S of this piece, hence (kQFull) for
+        // every warp of A to be through with the piece before the last one, so a slot is free
+        // again when its turn comes.  A piece of one key tile would let B run ahead of A.
+        int xc = 0;
         float qs = 1.f;
         bool ok = true;
         // The query rows of piece k, as they are, on their way into this tile's
@@ -1046,10 +1051,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
             const volatile Item* const done = slot(k);
             float l1 = lsum.x + lsum.y;
             if (ONE && t == 1) {  // A joins this half with its own
-                float2* const x = reinterpret_cast<float2*>(sbase + kOffX) + (k & 1) * BM + r;
-                *x = make_float2(l1 > 0.f ? mrow : neg_inf(), l1);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kXFull + (k & 1)));
+                if (nk > 0) {
+                    float2* const x = reinterpret_cast<float2*>(sbase + kOffX) + (xc & 1) * BM + r;
+                    *x = make_float2(l1 > 0.f ? mrow : neg_inf(), l1);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kXFull + (xc & 1)));
+                    ++xc;
+                }
                 sc += nk;
                 release(k);
                 continue;
@@ -1061,21 +1069,20 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
             const long long part = ((2ll * blockIdx.x + (done->j0 > 0 ? 0 : 1)) * 2 + t) * BM + r;
             const int nb = ONE ? done->tiles[1] : 0;  // key tiles of the other half
             float own = 1.f, other = 0.f;
-            if constexpr (ONE) {
-                ok = warp_wait(bar(kXFull + (k & 1)), (k >> 1) & 1);
+            if (nb > 0) {
+                ok = warp_wait(bar(kXFull + (xc & 1)), (xc >> 1) & 1);
                 if (!ok) break;
-                const float2 x = reinterpret_cast<const float2*>(sbase + kOffX)[(k & 1) * BM + r];
-                if (nb > 0 && x.x != neg_inf()) {
+                const float2 x = reinterpret_cast<const float2*>(sbase + kOffX)[(xc & 1) * BM + r];
+                ++xc;
+                if (x.x != neg_inf()) {
                     const float M = fmaxf(mrow, x.x);
                     own = fast_exp2(mrow - M);
                     other = fast_exp2(x.x - M);
                     l1 = l1 * own + x.y * other;
                     mrow = M;
                 }
-                if (nb > 0) {
-                    ok = warp_wait(bar(kODone + 1), (done->before_b + nb - 1) & 1);
-                    if (!ok) break;
-                }
+                ok = warp_wait(bar(kODone + 1), (done->before_b + nb - 1) & 1);
+                if (!ok) break;
             }
             if (!full) p.part_ml[part] = make_float2(l1 > 0.f ? mrow : neg_inf(), l1);
             if (nk > 0) {
