@@ -227,6 +227,10 @@ __global__ void __launch_bounds__(kThreads, 3) weights_tile_kernel(const WalkPar
             now = next;
             next = after;
         }
+        // A wait that ran out ends the call for the whole CTA, before anything is added to the
+        // weights: the warps would part at the next item's barriers otherwise.
+        ok = !__syncthreads_or(!ok);
+        if (!ok) break;
         const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         if (sp.n > 1) {
             if (mine) sp.at(p, it.run, it.bk)[it.k0 + tid] = sum;
@@ -235,6 +239,10 @@ __global__ void __launch_bounds__(kThreads, 3) weights_tile_kernel(const WalkPar
         }
         it = then;
     }
+    // (runs that are joined later: what was not summed adds nothing)
+    if (!ok && sp.n > 1)
+        for (it = find(it.id); it.id < items; it = find(it.id + static_cast<int>(gridDim.x)))
+            if (it.k0 + tid < it.S) sp.at(p, it.run, it.bk)[it.k0 + tid] = 0.f;
     // nothing of ours may still be running when TMEM is freed
     cp_async_wait<0>();
     if (!ok && tid == 0) {
