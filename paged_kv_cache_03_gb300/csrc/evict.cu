@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const CopyParams p) {
     pdl_wait_primary();
     for (int i = threadIdx.x; i < ROWS; i += 256) {
         const int j = j0 + i;
-        const int s = j < p.keep ? __ldg(p.kept + static_cast<long long>(bk) * p.keep + j) : -1;
+        // (written by the kernel before: a plain load, which stays behind the wait)
+        const int s = j < p.keep ? p.kept[static_cast<long long>(bk) * p.keep + j] : -1;
         int src = -1, dst = -1;
         if (s >= 0) {
             const int from = __ldg(p.bt + static_cast<long long>(b) * p.max_npg + s / p.ps);

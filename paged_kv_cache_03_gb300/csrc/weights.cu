@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WalkParams p
     const long long first = (static_cast<long long>(tile) * kWarps + warp) * 32;
     pdl_launch_dependents();
     pdl_wait_primary();
+    // (the packed query is the kernel before's: plain loads, which stay behind the wait)
     const int S = seq_len(p, b, false);
     float acc[2][2] = {};  // keys g and g + 8 of both halves, this lane's rows
     if (first < S) {       // (uniform over the warp)
@@ -135,9 +136,9 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WalkParams p
         const int2* const last = reinterpret_cast<const int2*>(pk.last + mine * 8 + 2 * t);
         uint4 next[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) next[i] = __ldg(q0 + n0 * 128 + 32 * i);
-        float4 row_next = __ldg(rows + n0 * 4);
-        int2 lim_next = __ldg(last + n0 * 4);
+        for (int i = 0; i < 4; ++i) next[i] = q0[n0 * 128 + 32 * i];
+        float4 row_next = rows[n0 * 4];
+        int2 lim_next = last[n0 * 4];
         for (int n = n0; n < n1; ++n) {
             uint4 x[4];
 #pragma unroll
@@ -146,9 +147,9 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WalkParams p
             const int2 lim = lim_next;
             if (n + 1 < n1) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) next[i] = __ldg(q0 + (n + 1) * 128 + 32 * i);
-                row_next = __ldg(rows + (n + 1) * 4);
-                lim_next = __ldg(last + (n + 1) * 4);
+                for (int i = 0; i < 4; ++i) next[i] = q0[(n + 1) * 128 + 32 * i];
+                row_next = rows[(n + 1) * 4];
+                lim_next = last[(n + 1) * 4];
             }
             if (!__any_sync(0xffffffffu, max(lim.x, lim.y) >= k0)) continue;
             float s[2][4];
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WalkParams p
                 }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint4 y = __ldg(q0 + (tiles + n) * 128 + 32 * i);
+                const uint4 y = q0[(tiles + n) * 128 + 32 * i];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     mma<true>(s[u], a[u][2 * i], y.x, y.y);

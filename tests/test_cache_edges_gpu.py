@@ -30,3 +30,53 @@ def test_short_pieces_of_one_query_tile(c):
         again = attend(inp, d, ws)
         assert torch.equal(again[0], out) and torch.equal(again[1], w)
     assert B.pa_check_device_flag(ws)[1] == 0
+
+
+def test_evictions_back_to_back():
+    """Evictions without a wait between them, their outputs in the same memory:
+    each copies the rows that its own selection chose."""
+    import torch
+    c = Case(8, 1, 4, 1, 16, spread(8, 200, 900), pool="bf16")
+    keep, n = 128, 24
+    inp = ref.Inputs(c, extra_pages=8 * 8)
+    d = inp.device()
+    dst = torch.from_numpy(inp.free[:64].reshape(8, 8).astype(np.int32)).cuda()
+    ws = B.new_cache_workspace()
+    rng = np.random.default_rng(11)
+    ws_in = [torch.from_numpy(rng.random(inp.w.shape).astype(np.float32)).cuda() for _ in range(n)]
+    torch.cuda.synchronize()
+    got = []
+    for w in ws_in:
+        new = B.evict_kv(*d["pool"], d["table"], d["ctx"], w, keep, 16, dst, workspace=ws)
+        got.append((new.kept.clone(), [t[dst.long()].clone() for t in d["pool"]]))
+        del new
+    b, h = np.arange(8)[:, None, None], np.arange(4)[None, :, None]
+    at = np.arange(keep)
+    for w, (kept, rows) in zip(ws_in, got):
+        want, _ = ref.evict(w.cpu().numpy(), c.ctx, keep, 16)
+        assert np.array_equal(kept.cpu().numpy(), want)
+        for t, x in zip(d["pool"], rows):
+            src = t[inp.table[b, want // 16], h, want % 16]
+            assert torch.equal(x[b, at // 16, h, at % 16].view(torch.uint8), src.view(torch.uint8))
+
+
+def test_fp32_weights_back_to_back():
+    """fp32 queries one after the other through one workspace, without a wait:
+    the weights are those of each query, not of the one before."""
+    import torch
+    c = Case(3, 4, 2, 12, 16, [300, 90, 500], dtype="f32")
+    inp = ref.Inputs(c)
+    d = inp.device()
+    ws = workspace(c, d)
+    rng = np.random.default_rng(4)
+    qs = [rng.standard_normal(inp.q.shape).astype(np.float32) * 1.5 for _ in range(6)]
+    dev = [torch.from_numpy(q).cuda() for q in qs]
+    torch.cuda.synchronize()
+    got = []
+    for q in dev + dev:
+        d["q"] = q
+        got.append(attend(inp, d, ws))
+    for q, first, again in zip(qs, got, got[6:]):
+        inp.q = q
+        check(inp, *first)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
