@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kWarps * 32) block_kernel(const WalkParams p) 
             // P's A fragments of 16 keys each, then O += P V (fp32: a tile's products on their
             // own, then a rounded add, as the MMA cuts what it adds to)
             uint32_t a[4][4], al[F32 ? 4 : 1][4];
+            float ls[2], las[2];  // of this tile: a sum of many small weights keeps them
 #pragma unroll
             for (int n = 0; n < 8; ++n)  // keys 8 n .., rows g and g + 8
 #pragma unroll
@@ -256,24 +257,29 @@ __global__ void __launch_bounds__(kWarps * 32) block_kernel(const WalkParams p) 
                     const float p0 = fast_exp2(fmaf(s[n][2 * e], qs[e], -mu[e]));
                     const float p1 = fast_exp2(fmaf(s[n][2 * e + 1], qs[e], -mu[e]));
                     const int at = 2 * (n & 1) + e;
-                    l[e] += p0 + p1;
+                    ls[e] = n == 0 ? p0 + p1 : ls[e] + (p0 + p1);
                     if constexpr (Q4) {
                         const uint32_t x = pack_f16x2(p0, p1);
                         a[n >> 1][at] = x;
                         if constexpr (F32) {
                             const float2 f = f16x2_to_float2(x);
-                            al[n >> 1][at] = pack_f16x2(p0 - f.x, p1 - f.y);
+                            al[n >> 1][at] = pack_f16x2((p0 - f.x) * kLowScale, (p1 - f.y) * kLowScale);
                         }
                     } else {
                         const uint32_t x = pack_bf16x2(p0, p1);
                         const float2 f = bf16x2_to_float2(x);
-                        la[e] += f.x + f.y;
+                        las[e] = n == 0 ? f.x + f.y : las[e] + (f.x + f.y);
                         a[n >> 1][at] = x;
                     }
                 }
 #pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[e] += ls[e];
+                if constexpr (!Q4) la[e] += las[e];
+            }
+#pragma unroll
             for (int d = 0; d < 16; d += 2) {  // 16 dims
-                float y[2][4];
+                float y[2][4], z[2][4];  // V hi, V lo
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {  // 16 keys
                     uint32_t x[4];
@@ -281,11 +287,13 @@ __global__ void __launch_bounds__(kWarps * 32) block_kernel(const WalkParams p) 
                     if constexpr (F32) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            if (k == 0)
-                                mma_first<Q4>(y[h], al[k], x[2 * h], x[2 * h + 1]);
-                            else
-                                mma<Q4>(y[h], al[k], x[2 * h], x[2 * h + 1]);
-                            mma<Q4>(y[h], a[k], x[2 * h], x[2 * h + 1]);
+                            if (k == 0) {
+                                mma_first<Q4>(z[h], al[k], x[2 * h], x[2 * h + 1]);
+                                mma_first<Q4>(y[h], a[k], x[2 * h], x[2 * h + 1]);
+                            } else {
+                                mma<Q4>(z[h], al[k], x[2 * h], x[2 * h + 1]);
+                                mma<Q4>(y[h], a[k], x[2 * h], x[2 * h + 1]);
+                            }
                         }
                     } else {
                         mma<Q4>(o[d], a[k], x[0], x[1]);
@@ -296,7 +304,7 @@ __global__ void __launch_bounds__(kWarps * 32) block_kernel(const WalkParams p) 
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[d + h][e] += y[h][e];
+                        for (int e = 0; e < 4; ++e) o[d + h][e] += fmaf(z[h][e], kLowStep, y[h][e]);
                 }
             }
         }

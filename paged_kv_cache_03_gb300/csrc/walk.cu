@@ -23,8 +23,10 @@
 // share one scale each.  A 4-bit value is exact in f16, so the products see
 // exactly the stored values; the query rows are scaled by a power of two into
 // f16's range (bf16 keeps all bits; fp32 is split into two f16 parts) and P is
-// rounded to f16 (2^-12 relative; split in two for fp32).  Over bf16 pages the
-// operands are bf16, and the row sum that divides O adds the rounded weights.
+// rounded to f16 (2^-11 relative, and keys below 2^-25 of the row's largest weight are lost:
+// less than half a bf16 step while a warp has fewer than 2^17 of them; split in two for
+// fp32, 2^-22, with no such limit: kLowScale).  Over bf16 pages the operands are bf16, and
+// the row sum that divides O adds the rounded weights.
 // Max, sums and O are fp32.  The running max moves only when it grows by more
 // than 2^8, so O is rarely rescaled.
 //
@@ -242,6 +244,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
                     o[n][i][3] *= a1;
                 }
             }
+            float ls[2], las[2];  // of this step: a sum of many small weights keeps them
             const float mu[2] = {m[n][0] == neg_inf() ? 0.f : m[n][0], m[n][1] == neg_inf() ? 0.f : m[n][1]};
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -249,23 +252,29 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
                 for (int h = 0; h < 2; ++h) {  // keys g, then g + 8
                     const float p0 = fast_exp2(fmaf(s[n][u][2 * h], qs[n][0], -mu[0]));
                     const float p1 = fast_exp2(fmaf(s[n][u][2 * h + 1], qs[n][1], -mu[1]));
-                    l[n][0] += p0;
-                    l[n][1] += p1;
+                    const bool first = u == 0 && h == 0;
+                    ls[0] = first ? p0 : ls[0] + p0;
+                    ls[1] = first ? p1 : ls[1] + p1;
                     if constexpr (F16) {
                         const uint32_t x = pack_f16x2(p0, p1);
                         pb[n][u][h] = movmatrix_trans(x);
                         if constexpr (F32) {
                             const float2 f = f16x2_to_float2(x);
-                            pl[n][u][h] = movmatrix_trans(pack_f16x2(p0 - f.x, p1 - f.y));
+                            pl[n][u][h] = movmatrix_trans(pack_f16x2((p0 - f.x) * kLowScale, (p1 - f.y) * kLowScale));
                         }
                     } else {
                         const uint32_t x = pack_bf16x2(p0, p1);
                         const float2 f = bf16x2_to_float2(x);
-                        la[n][0] += f.x;
-                        la[n][1] += f.y;
+                        las[0] = first ? f.x : las[0] + f.x;
+                        las[1] = first ? f.y : las[1] + f.y;
                         pb[n][u][h] = movmatrix_trans(x);
                     }
                 }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[n][e] += ls[e];
+                if constexpr (!F16) la[n][e] += las[e];
+            }
         }
         Values vv[U];
 #pragma unroll
@@ -292,6 +301,8 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
                         if constexpr (F32) {
                             float x[4];
                             mma_first<F16>(x, a[mm], pl[n][u][0], pl[n][u][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[e] *= kLowStep;
                             mma<F16>(x, a[mm], pb[n][u][0], pb[n][u][1]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) acc[e] += x[e];

@@ -14,6 +14,11 @@ namespace walk {
 constexpr int kD = kHeadDim;
 constexpr int kWarps = 4;
 constexpr float kLazyRescaleLog2 = 8.0f;
+// fp32 queries: a weight is hi + kLowStep * lo, both f16, and V^T lo is scaled before V^T hi
+// is added to it.  lo has f16's whole range for itself, steps of 2^-35 where the row's
+// largest weight is at least 1: with both parts in one range, keys below 2^-25 of the
+// largest counted in the row's sum and were missing in O (32768 of them 2^-25.5 each: 3.5e-4 of the result).
+constexpr float kLowScale = 2048.f, kLowStep = 1.f / kLowScale;
 constexpr int kMerge = kD + 4;  // floats per (warp, row) in the merge buffer
 
 struct WalkParams {

@@ -80,3 +80,43 @@ def test_fp32_weights_back_to_back():
         inp.q = q
         check(inp, *first)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def one_heavy_key(Bn, G, L, n, dtype, gap):
+    """Bn sequences over the same n keys of one kv head, all values 1: key n // 3
+    scores `gap` log2 units, the others 0.  Every output is exactly 1."""
+    import torch
+    ps = 128
+    P = n // ps
+    codes = torch.zeros(P, 1, ps, 64, dtype=torch.uint8, device="cuda")
+    scales = torch.full((P, 1, ps, 8), 0x38, dtype=torch.uint8, device="cuda")  # 1.0
+    codes[(n // 3) // ps, 0, (n // 3) % ps] = 0x22                              # 1.0, twice
+    values = torch.full_like(codes, 0x22)
+    pool = B.Q4Pool(codes, scales, values, scales.clone())
+    table = torch.arange(P, dtype=torch.int32, device="cuda").repeat(Bn, 1)
+    ctx = torch.full((Bn,), n, dtype=torch.int32, device="cuda")
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q = torch.ones(Bn, G, L, 128, device="cuda").to(dt)
+    scale = float(np.float32(gap * np.log(2) / 128))
+    out = B.paged_attention_q4(q, pool, table, ctx, ps, scale, False)
+    return float((out.double() - 1).abs().max())
+
+
+# log2 units below the heaviest key: f16 has steps of 2^-24 at its lower end
+@pytest.mark.parametrize("gap", [22.3, 25.5, 30.0])
+@pytest.mark.parametrize("Bn,L,n", [(640, 1, 32768), (320, 16, 32768), (2, 1, 4096)],
+                         ids=["walk", "block", "short"])
+def test_many_light_keys_fp32(Bn, L, n, gap):
+    """Counted: the two parts of a weight 2^-22; a row sum and an O that take n / 64 sums of
+    a step, each add off by 2^-24; a step's products, 68 terms cut by 2^-23; joining lanes,
+    warps and shares, 64 adds.  (Weights below f16's steps, if they were lost, would be a
+    quarter of 32768 * 2^-25.5 in the heaviest key's warp: 1.7e-4.)"""
+    tol = 2.0 ** -22 + (2 * n / 64 + 64) * 2.0 ** -24 + 68 * 2.0 ** -23
+    assert one_heavy_key(Bn, 4, L, n, "f32", gap) <= tol
+
+
+@pytest.mark.parametrize("L", [1, 16, 65])
+def test_many_light_keys_bf16(L):
+    """bf16 queries: 2^15 keys that weigh 2^-25.5 are 2^-10.5 of the row; lost or not, the
+    output is within half a step of 1."""
+    assert one_heavy_key(160, 4, L, 32768, "bf16", 25.5) <= 2.0 ** -8
