@@ -353,6 +353,10 @@ pa_status pa_gather_kv_q4(const pa_shape* shape, const pa_q4_pool* pool,
 /* pa_paged_attention over a 4-bit pool, any L, bf16 or fp32 query and output:
  * the attention of the stored values (nothing else is rounded to 4 bits).
  * Keys behind a bad page id read as zeros (PA_FLAG_BAD_PAGE).
+ * A query row with a NaN, or one that sees a key with a NaN, comes out as NaN
+ * whatever the shapes, and so do the weights of the keys that it sees; other
+ * rows and weights are as without it.  (A value row is different: a NaN or Inf
+ * in it may reach every row of its kv head, as said above.)
  *
  * Key weights (key_weights_out not null): what every key received,
  *   key_weights_out[b, kv_head, s] = key_weights[b, kv_head, s]

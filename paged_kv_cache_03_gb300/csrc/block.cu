@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kWarps * 32) block_kernel(const WalkParams p) 
         const float at = Q4 ? l[e] : la[e];
         if (full) {
             const long long row = row0 + rr;
-            const float inv = at > 0.f ? 1.f / at : 0.f;
+            const float inv = at == 0.f ? 0.f : 1.f / at;
 #pragma unroll
             for (int d = 0; d < 16; ++d) {
                 const float x = o[d][2 * e] * inv, y = o[d][2 * e + 1] * inv;
@@ -334,11 +334,11 @@ __global__ void __launch_bounds__(kWarps * 32) block_kernel(const WalkParams p) 
                 else
                     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * kD + 8 * d + 2 * t) = pack_bf16x2(x, y);
             }
-            if (t == 0 && p.lse) p.lse[row] = l[e] > 0.f ? m[e] + log2f(l[e]) : __int_as_float(0x7f800000);
+            if (t == 0 && p.lse) p.lse[row] = l[e] == 0.f ? __int_as_float(0x7f800000) : m[e] + log2f(l[e]);
         } else {
             const long long row = sg.slot() * ROWS + rr;
-            if (t == 0) p.part_ml[row] = make_float4(l[e] > 0.f ? m[e] : neg_inf(), at, l[e], 0.f);
-            if (l[e] > 0.f) {
+            if (t == 0) p.part_ml[row] = make_float4(m[e], at, l[e], 0.f);
+            if (l[e] != 0.f) {
 #pragma unroll
                 for (int d = 0; d < 16; ++d)
                     *reinterpret_cast<float2*>(p.part_o + row * kD + 8 * d + 2 * t) =

@@ -839,7 +839,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // a split pair: this chunk's (m, l) of every row, o of rows with keys
             constexpr bool split = kSplit;
             const long long prow = kSplit ? orow_idx * p.nsplit + it.c : 0;
-            if (split && row_valid) p.part_ml[prow] = make_float2(nkt > 0 ? mrow : neg_inf(), lsum);
+            // (a sum of NaN is joined: its maximum may still be -inf, which means no key)
+            if (split && row_valid)
+                p.part_ml[prow] = make_float2(lsum != lsum ? 0.f : nkt > 0 ? mrow : neg_inf(), lsum);
             if (nkt > 0) {
                 if (!warp_wait(bar(kODone + t), (pv_own + nkt - 1) & 1)) {
                     ok = false;
@@ -1160,7 +1162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (rr >= p.nrem) continue;
                         const long long pr =
                             (static_cast<long long>(it.b * p.H_kv + it.kvh) * p.nrem + rr) * nslot + slot;
-                        if (g == 0) p.rem_ml[pr] = make_float2(l_r[e] > 0.f ? m_r[e] : neg_inf(), l_r[e]);
+                        if (g == 0)
+                            p.rem_ml[pr] = make_float2(l_r[e] > 0.f ? m_r[e] : l_r[e] != l_r[e] ? 0.f : neg_inf(), l_r[e]);
                         float* const po = p.rem_o + pr * kD;
 #pragma unroll
                         for (int mt = 0; mt < 8; ++mt) {

@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int rr = 2 * t4 + e;
-                        if (g == 0) p.rem_ml[slot * 8 + rr] = make_float2(l_r[e] > 0.f ? m_r[e] : neg_inf(), l_r[e]);
+                        if (g == 0) p.rem_ml[slot * 8 + rr] = make_float2(m_r[e], l_r[e]);
                         float* const po = p.rem_o + (slot * 8 + rr) * kD;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -1053,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
             if (ONE && t == 1) {  // A joins this half with its own
                 if (nk > 0) {
                     float2* const x = reinterpret_cast<float2*>(sbase + kOffX) + (xc & 1) * BM + r;
-                    *x = make_float2(l1 > 0.f ? mrow : neg_inf(), l1);
+                    *x = make_float2(mrow, l1);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kXFull + (xc & 1)));
                     ++xc;
@@ -1074,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                 if (!ok) break;
                 const float2 x = reinterpret_cast<const float2*>(sbase + kOffX)[(xc & 1) * BM + r];
                 ++xc;
-                if (x.x != neg_inf()) {
+                if (x.y != 0.f) {
                     const float M = fmaxf(mrow, x.x);
                     own = fast_exp2(mrow - M);
                     other = fast_exp2(x.x - M);
@@ -1084,12 +1084,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                 ok = warp_wait(bar(kODone + 1), (done->before_b + nb - 1) & 1);
                 if (!ok) break;
             }
-            if (!full) p.part_ml[part] = make_float2(l1 > 0.f ? mrow : neg_inf(), l1);
+            if (!full) p.part_ml[part] = make_float2(mrow, l1);
             if (nk > 0) {
                 ok = warp_wait(bar(kODone + t), (sc + nk - 1) & 1);
                 if (!ok) break;
                 tc::fence_after_sync();
-                const float inv = l1 > 0.f ? 1.f / l1 : 0.f;
+                const float inv = l1 == 0.f ? 0.f : 1.f / l1;
 #pragma unroll 1
                 for (int cc = 0; cc < 4; ++cc) {
                     float o[32];
@@ -1117,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                             for (int e = 0; e < 4; ++e)
                                 reinterpret_cast<uint4*>(dst)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                         }
-                    } else if (l1 > 0.f) {
+                    } else if (l1 != 0.f) {
                         float* const dst = p.part_o + part * kD + cc * 32;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -1132,7 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
                     if (nb > 0) mbar_arrive(bar(kOFree + 1));
                 }
             }
-            if (full && valid && p.lse) p.lse[row] = l1 > 0.f ? mrow + log2f(l1) : __int_as_float(0x7f800000);
+            if (full && valid && p.lse) p.lse[row] = l1 == 0.f ? __int_as_float(0x7f800000) : mrow + log2f(l1);
             sc += nk;
             release(k);
         }
@@ -1149,10 +1149,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams p) {
 }
 
 __device__ __forceinline__ void store_row(const TileParams& p, long long row, int lane, float4 acc, float l, float M) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // (0: a row without keys; NaN stays)
     *reinterpret_cast<uint2*>(p.out + row * kD + 4 * lane) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (lane == 0 && p.lse) p.lse[row] = l > 0.f ? M + log2f(l) : __int_as_float(0x7f800000);
+    if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? __int_as_float(0x7f800000) : M + log2f(l);
 }
 
 // A merged state of one row, four dims a lane.
@@ -1165,7 +1165,7 @@ struct RowState {
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __device__ __forceinline__ void add(const float2 v, const float4 x) {
-        if (v.x == neg_inf()) return;  // no key (x was not written)
+        if (v.y == 0.f) return;  // no key (x was not written)
         const float m = fmaxf(M, v.x), a = fast_exp2(M - m), b = fast_exp2(v.x - m);
         M = m;
         l = l * a + v.y * b;
@@ -1203,7 +1203,7 @@ __global__ void __launch_bounds__(256) tile_merge_kernel(const TileParams p, int
             float4 x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                v[u].x = neg_inf();
+                v[u] = make_float2(neg_inf(), 0.f);
                 if (k + u > sp.w) continue;
                 const long long slot = ((2ll * (k + u) + (k + u == c ? 1 : 0)) * 2 + t) * BM + r;
                 v[u] = p.part_ml[slot];

@@ -364,26 +364,25 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, Keys::kF16, F32
         }
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float at = 0.f, lt = 0.f;
-        if (M != neg_inf()) {
+        const float Mu = M == neg_inf() ? 0.f : M;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float* const mw_ = mr + w * mrows * kMerge;
-                const float a = fast_exp2(mv[w] - M);
-                const float4 x = *reinterpret_cast<const float4*>(mw_ + 4 * lane);
-                acc.x += a * x.x;
-                acc.y += a * x.y;
-                acc.z += a * x.z;
-                acc.w += a * x.w;
-                at += a * mw_[kD + 1];
-                lt += a * mw_[kD + 2];
-            }
+        for (int w = 0; w < kWarps; ++w) {
+            const float* const mw_ = mr + w * mrows * kMerge;
+            const float a = fast_exp2(mv[w] - Mu);  // a warp without keys: 0 times zeros
+            const float4 x = *reinterpret_cast<const float4*>(mw_ + 4 * lane);
+            acc.x += a * x.x;
+            acc.y += a * x.y;
+            acc.z += a * x.z;
+            acc.w += a * x.w;
+            at += a * mw_[kD + 1];
+            lt += a * mw_[kD + 2];
         }
         if (full) {
             store_row<F32>(p, row0 + rr, lane, acc, at, lt, M);
         } else {
             const long long row = done.slot() * ROWS + rr;
             if (lane == 0) p.part_ml[row] = make_float4(M, at, lt, 0.f);
-            if (M != neg_inf()) *reinterpret_cast<float4*>(p.part_o + row * kD + 4 * lane) = acc;
+            if (lt != 0.f) *reinterpret_cast<float4*>(p.part_o + row * kD + 4 * lane) = acc;
         }
     }
     if (!more) break;
@@ -413,7 +412,7 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const WalkParams p, 
         acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     auto add = [](float4& s, float4& o, const float4 v, const float4 x) {
-        if (v.x == neg_inf()) return;  // no key (and x was not written)
+        if (v.z == 0.f) return;  // no key (and x was not written)
         const float m = fmaxf(s.x, v.x), a = fast_exp2(s.x - m), b = fast_exp2(v.x - m);
         s = make_float4(m, s.y * a + v.y * b, s.z * a + v.z * b, 0.f);
         o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);

@@ -17,7 +17,8 @@ constexpr float kLazyRescaleLog2 = 8.0f;
 // fp32 queries: a weight is hi + kLowStep * lo, both f16, and V^T lo is scaled before V^T hi
 // is added to it.  lo has f16's whole range for itself, steps of 2^-35 where the row's
 // largest weight is at least 1: with both parts in one range, keys below 2^-25 of the
-// largest counted in the row's sum and were missing in O (32768 of them 2^-25.5 each: 3.5e-4 of the result).
+// largest counted in the row's sum and were missing in O (32768 of them 2^-25.5 each:
+// 3.5e-4 of the result).
 constexpr float kLowScale = 2048.f, kLowStep = 1.f / kLowScale;
 constexpr int kMerge = kD + 4;  // floats per (warp, row) in the merge buffer
 
@@ -619,18 +620,19 @@ struct Segment {
     }
 };
 
-// The merged row (four dims a lane) and its log-sum-exp.
+// The merged row (four dims a lane) and its log-sum-exp.  A sum of 0 is a row without keys;
+// one of NaN (a score was NaN; the maximum need not have moved) makes the row NaN.
 template <bool F32>
 __device__ __forceinline__ void store_row(const WalkParams& p, long long row, int lane, float4 acc, float at, float lt,
                                           float M) {
-    const float inv = at > 0.f ? 1.f / at : 0.f;
+    const float inv = at == 0.f ? 0.f : 1.f / at;
     if constexpr (F32)
         *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kD + 4 * lane) =
             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     else
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kD + 4 * lane) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (lane == 0 && p.lse) p.lse[row] = lt > 0.f ? M + log2f(lt) : __int_as_float(0x7f800000);
+    if (lane == 0 && p.lse) p.lse[row] = lt == 0.f ? __int_as_float(0x7f800000) : M + log2f(lt);
 }
 
 // walk.cu: up to 8 nt rows per CTA (nt = 1, 2; bf16 pages or codes)

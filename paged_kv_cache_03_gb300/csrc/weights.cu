@@ -8,6 +8,15 @@ namespace {
 
 constexpr int kSumKeys = 4;  // keys of a thread of walk_sum_kernel
 
+// A row's weight of a key from the score in log2 units, 0 for one it does not see (-inf; the
+// row's log-sum-exp may be NaN).
+__device__ __forceinline__ float weight_of(float score, float lse) {
+    return score == neg_inf() ? 0.f : fast_exp2(score - lse);
+}
+__device__ __forceinline__ float weight_of(float product, float scale, float minus_lse) {
+    return product == neg_inf() ? 0.f : fast_exp2(fmaf(product, scale, minus_lse));
+}
+
 // w_out[b, kvh, k] = w_in[b, kvh, k] + the rows' probabilities of key k, 0 past
 // the context, from the scores that walk_kernel left.  Four keys per thread, 256
 // apart, their loads together (64 sequences of 128 .. 4096 4-bit keys, 4 rows, the call:
@@ -35,10 +44,10 @@ __global__ void __launch_bounds__(256) walk_sum_kernel(const WalkParams p, int n
 #pragma unroll
             for (int j = 0; j < kSumKeys; ++j) {
                 if (k0 + 256 * j >= S) continue;
-                acc[j] += fast_exp2(v[j].x - l[0]);
-                acc[j] += fast_exp2(v[j].y - l[1]);
-                acc[j] += fast_exp2(v[j].z - l[2]);
-                acc[j] += fast_exp2(v[j].w - l[3]);
+                acc[j] += weight_of(v[j].x, l[0]);
+                acc[j] += weight_of(v[j].y, l[1]);
+                acc[j] += weight_of(v[j].z, l[2]);
+                acc[j] += weight_of(v[j].w, l[3]);
             }
         }
     } else {
@@ -46,7 +55,7 @@ __global__ void __launch_bounds__(256) walk_sum_kernel(const WalkParams p, int n
             const float l = lse[r];
 #pragma unroll
             for (int j = 0; j < kSumKeys; ++j)
-                if (k0 + 256 * j < S) acc[j] += fast_exp2(x[(k0 + 256 * j) * p.R + r] - l);
+                if (k0 + 256 * j < S) acc[j] += weight_of(x[(k0 + 256 * j) * p.R + r], l);
         }
     }
 #pragma unroll
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WalkParams p
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    acc[u][h] += fast_exp2(fmaf(s[u][2 * h], row.x, row.y)) + fast_exp2(fmaf(s[u][2 * h + 1], row.z, row.w));
+                    acc[u][h] += weight_of(s[u][2 * h], row.x, row.y) + weight_of(s[u][2 * h + 1], row.z, row.w);
         }
     }
 #pragma unroll

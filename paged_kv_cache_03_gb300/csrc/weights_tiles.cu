@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 3) weights_tile_kernel(const WalkPar
     tc::fence_after_sync();
     const uint32_t tmem = tmem_s;
     const int c = tid & 15, r0 = tid >> 4;  // this thread's 16-byte chunk, and its first row of eight
-    const float scale = fmaxf(p.scale_log2, FLT_MIN);  // (times -inf, a key not seen: -inf)
+    const float scale = fmaxf(p.scale_log2, FLT_MIN);
     const int nt = (p.R + kRows - 1) / kRows, step = kRows % p.L;
     auto product = [&](int i) {
         constexpr uint32_t idesc = tc::idesc_bf16(kKeys, kRows, 0, 0);  // both K-major
@@ -204,24 +204,27 @@ __global__ void __launch_bounds__(kThreads, 3) weights_tile_kernel(const WalkPar
                 float s[32];
                 tc::ld32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + (i & 1) * kRows + 32 * h, s);
                 tc::wait_ld();
-                if (masked) {
+                const int k = it.k0 + tid;
+                auto add = [&](int j, float x, float m) { acc[j] += fast_exp2(fmaf(x, scale, -m)); };
+                if (masked) {  // (a row that does not see the key adds nothing, whatever its sum is)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const int4 x = *reinterpret_cast<const int4*>(last + 32 * h + e);
-                        const int k = it.k0 + tid;
-                        if (k > x.x) s[e] = neg_inf();
-                        if (k > x.y) s[e + 1] = neg_inf();
-                        if (k > x.z) s[e + 2] = neg_inf();
-                        if (k > x.w) s[e + 3] = neg_inf();
+                        const float4 m = *reinterpret_cast<const float4*>(lse + 32 * h + e);
+                        if (k <= x.x) add(0, s[e], m.x);
+                        if (k <= x.y) add(1, s[e + 1], m.y);
+                        if (k <= x.z) add(2, s[e + 2], m.z);
+                        if (k <= x.w) add(3, s[e + 3], m.w);
                     }
-                }
+                } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(lse + 32 * h + e);
-                    acc[0] += fast_exp2(fmaf(s[e], scale, -m.x));
-                    acc[1] += fast_exp2(fmaf(s[e + 1], scale, -m.y));
-                    acc[2] += fast_exp2(fmaf(s[e + 2], scale, -m.z));
-                    acc[3] += fast_exp2(fmaf(s[e + 3], scale, -m.w));
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(lse + 32 * h + e);
+                        add(0, s[e], m.x);
+                        add(1, s[e + 1], m.y);
+                        add(2, s[e + 2], m.z);
+                        add(3, s[e + 3], m.w);
+                    }
                 }
             }
             now = next;

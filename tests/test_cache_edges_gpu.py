@@ -6,7 +6,7 @@ import pytest
 import cache_ref as ref
 from cache_ref import Case
 from paged_kv_cache_03_gb300 import binding as B
-from test_cache_paths_gpu import attend, check, spread, workspace
+from test_cache_paths_gpu import PATHS, attend, check, spread, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,55 @@ def test_many_light_keys_bf16(L):
     """bf16 queries: 2^15 keys that weigh 2^-25.5 are 2^-10.5 of the row; lost or not, the
     output is within half a step of 1."""
     assert one_heavy_key(160, 4, L, 32768, "bf16", 25.5) <= 2.0 ** -8
+
+
+# every path, its states whole and cut over shares, key chunks and remainder rows
+NAN_CASES = [(c, True) for c in PATHS] + [(c, False) for c in PATHS if c.pool == "q4"] + [
+    (Case(1, 4, 1, 1, 16, [3900]), True),
+    (Case(1, 4, 1, 3, 16, [3900], pool="bf16"), True),
+    (Case(1, 4, 1, 13, 16, [3900], dtype="f32"), True),
+    (Case(1, 4, 1, 32, 16, [3900]), True),
+    (Case(1, 4, 1, 65, 16, [3900], pool="bf16"), True),
+    (Case(1, 2, 1, 200, 16, [310]), False),              # whole prompts, keys cut in chunks
+    (Case(1, 4, 1, 130, 16, [600]), False),              # ... and a last tile of few rows
+    (Case(2, 2, 2, 40, 8, [300, 120], causal=False), True),
+]
+
+
+@pytest.mark.parametrize("c,weights", NAN_CASES, ids=str)
+@pytest.mark.parametrize("where", ["query", "key"])
+def test_nan_rows(where, c, weights):
+    """A row whose query, or a key it sees, holds a NaN is NaN on every path, and so are the
+    weights of the keys it sees; nothing else changes."""
+    import torch
+    if where == "key" and not c.causal:
+        return  # every row sees every key
+    inp = ref.Inputs(c)
+    d = inp.device()
+    ws = workspace(c, d)
+    out, w = attend(inp, d, ws, weights)
+    S, L = c.ctx[0], c.L
+    pos = np.arange(L) + (S - L if c.causal else S)  # the last key that a row of sequence 0 sees
+    rows = np.zeros((c.B, c.H_kv, c.G, L), bool)
+    if where == "query":
+        rows[0, c.H_kv - 1, c.G // 2, 0] = rows[0, 0, 0, L // 2] = rows[0, 0, c.G - 1, L - 1] = True
+        d["q"] = d["q"].clone()
+        d["q"].view(c.B, c.H_kv, c.G, L, 128)[torch.from_numpy(rows).cuda()] = float("nan")
+    else:
+        k = S - 1 - L // 2
+        rows[0, 0] = pos >= k
+        page, slot = inp.table[0, k // c.ps], k % c.ps
+        if c.pool == "q4":
+            d["pool"].key_scales[page, 0, slot] = 0x7f
+        else:
+            d["pool"][0][page, 0, slot] = float("nan")
+    got, got_w = attend(inp, d, ws, weights)
+    assert B.pa_check_device_flag(ws)[1] == 0
+    bad = torch.from_numpy(rows.reshape(c.B, c.H_kv * c.G, L)).cuda()
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], out[~bad])
+    if weights:
+        far = np.where(rows, pos, -1).max((2, 3))  # the last key that a NaN row sees
+        bad = np.arange(inp.cap) <= far[:, :, None]
+        bad &= np.arange(inp.cap) < inp.ctx[:, None, None]
+        bad = torch.from_numpy(bad).cuda()
+        assert torch.isnan(got_w[bad]).all() and torch.equal(got_w[~bad], w[~bad])
