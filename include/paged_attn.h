@@ -368,8 +368,8 @@ pa_status pa_gather_kv_q4(const pa_shape* shape, const pa_q4_pool* pool,
  * equal bits.  key_weights without key_weights_out is PA_ERR_INVALID_ARG.
  *
  * workspace: pa_q4_workspace_bytes(shape, key_weights_out != NULL), 256-byte
- * aligned, zeroed once by the caller; calls that may overlap need their own.
- * Returns as pa_paged_attention_sched. */
+ * aligned, its first 256 bytes zeroed once by the caller; calls that may
+ * overlap need their own.  Returns as pa_paged_attention_sched. */
 pa_status pa_paged_attention_q4(const pa_shape* shape, const void* query, const pa_q4_pool* pool,
                                 const int32_t* block_table, const int32_t* context_lens,
                                 float scale, int causal, const float* key_weights,
@@ -377,14 +377,20 @@ pa_status pa_paged_attention_q4(const pa_shape* shape, const void* query, const 
                                 void* workspace, size_t workspace_bytes, void* cuda_stream);
 
 /* Bytes of workspace of pa_paged_attention_q4, with or without key weights;
- * 0 for an invalid shape or without a device. */
+ * 0 for an invalid shape or without a device.  Enough for this shape and for
+ * every one with at most its B, L and max_pages_per_seq (all else equal), so
+ * one sized for the largest chunk serves decode steps too.  It grows with the
+ * query rows; with key weights and up to 8 rows per kv head by 4 bytes for
+ * every row and slot of the tables, up to 512 MiB; for many rows without key
+ * weights by bf16 copies of the sequences, up to 1 GiB (or one sequence). */
 size_t pa_q4_workspace_bytes(const pa_shape* shape, int key_weights);
 
 /* ---- Key weights and eviction ----------------------------------------------
  *
  * pa_paged_attention over bf16 pages that also accumulates what every key
  * received (key_weights_out required; see pa_paged_attention_q4).  fp32 pools
- * are PA_ERR_UNSUPPORTED.  workspace: pa_weights_workspace_bytes(shape). */
+ * are PA_ERR_UNSUPPORTED.  workspace: pa_weights_workspace_bytes(shape), as
+ * for pa_paged_attention_q4. */
 pa_status pa_paged_attention_weights(const pa_shape* shape, const void* query,
                                      const void* key_pages, const void* value_pages,
                                      const int32_t* block_table, const int32_t* context_lens,

@@ -693,30 +693,35 @@ def _q4_shape(query, pool, block_table):
     return pa_shape(B_, H_q, H_kv, L, D, P, ps, block_table.shape[1], _dtype_id(query.dtype))
 
 
-def _zeroed(n, device, name):
+def _workspace(n, device, name):
+    """n bytes, the flag and the counters in front zeroed (all that needs it)."""
     import torch
     if n == 0:
         raise PagedAttentionError(PA_ERR_INVALID_ARG, name)
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
 
 
 def new_q4_workspace(query, pool, block_table, key_weights=None):
-    """Zeroed workspace of paged_attention_q4 for tensors of these shapes,
-    with key weights, without, or (None) for either."""
+    """Workspace of paged_attention_q4 for tensors of these shapes and for any
+    with at most their B, L and table width, with key weights, without, or
+    (None) for either."""
     import torch
     shape = _q4_shape(query, pool, block_table)
     kinds = (False, True) if key_weights is None else (key_weights,)
     with torch.cuda.device(query.device):
         n = max(pa_q4_workspace_bytes(shape, k) for k in kinds)
-    return _zeroed(n, query.device, "pa_q4_workspace_bytes")
+    return _workspace(n, query.device, "pa_q4_workspace_bytes")
 
 
 def new_weights_workspace(query, key_pages, block_table):
-    """Zeroed workspace of paged_attention_weights for tensors of these shapes."""
+    """Workspace of paged_attention_weights for tensors of these shapes and for
+    any with at most their B, L and table width."""
     import torch
     with torch.cuda.device(query.device):
         n = pa_weights_workspace_bytes(shape_of(query, key_pages, block_table))
-    return _zeroed(n, query.device, "pa_weights_workspace_bytes")
+    return _workspace(n, query.device, "pa_weights_workspace_bytes")
 
 
 def _attend(name, fn, pools, shape, query, block_table, context_lens, page_size, scale, causal,

@@ -1,5 +1,7 @@
 // attend.cu -- the cache attention's host side: which kernel takes a call, the
 // workspace, the launches.
+#include <algorithm>
+
 #include "walk.cuh"
 
 namespace pa {
@@ -20,7 +22,13 @@ struct WalkPlan {
 // B = 8 over 1000 .. 8000 keys 61, 69 at 32 rows, 84, 71 at 48; B = 64 over 500 .. 2000
 // keys 130, 143 at 32, 186, 147 at 48; B = 1 over 16000 keys 49, 49 at 64).
 constexpr int kBlockRows = 48;
-constexpr int kScoreRows = 8;    // rows per kv head up to which scores are stored
+// Key weights: rows per kv head up to which scores are stored, and the most bytes of them
+// (4 for every slot of the table and row: a wide table would take more than the cache);
+// otherwise the weights are recomputed from the keys (stored, recomputed, us, 64 sequences
+// of 128 .. 4096 keys, 4 rows, 8 kv heads: 4-bit pages 60, 122, and 93, 194 in tables of
+// 32768 slots, 268 MB of scores; bf16 pages 120, 169, and 153, 243).
+constexpr int kScoreRows = 8;
+constexpr size_t kScoreBytes = size_t(1) << 29;
 // Table capacity up to which a CTA takes a whole segment, without a merge (shares,
 // whole, us, G = 4, H_kv = 8): 64 sequences of 1000 keys 30, 23, one of 1000 18, 16,
 // one of 2000 18, 18, one of 4000 18, 34.
@@ -38,10 +46,10 @@ WalkPlan plan(const pa_shape& sh, bool q4, bool weights, int sm_count) {
     w.nt = w.R >= kBlockRows ? 0 : w.R > 8 && !f32 ? 2 : 1;
     w.rows_cta = w.nt ? 8 * w.nt : kBlockCtaRows;
     w.nrc = (w.R + w.rows_cta - 1) / w.rows_cta;
-    w.scores = weights && w.R <= kScoreRows;
     const long long cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     const long long segs = static_cast<long long>(sh.B) * sh.H_kv * w.nrc;
     const size_t rows = static_cast<size_t>(sh.B) * sh.H_kv * w.R;
+    w.scores = weights && w.R <= kScoreRows && rows * cap * 4 <= kScoreBytes;
     w.whole = w.nt && cap <= kWholeKeys;
     const int resident = w.nt ? walk_resident(w.nt, q4, f32, w.R) : 2;
     w.items = w.whole ? segs : static_cast<long long>(sm_count) * resident;
@@ -177,7 +185,8 @@ static size_t tiles_scratch(const pa_shape& sh, int sm_count) {
     return align_up(align_up(tiles_workspace_bytes(sh, sm_count), 256) + static_cast<size_t>(sh.B) * sh.H_q * sh.L * 4, 256);
 }
 
-size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_count) {
+// What this very shape needs.
+static size_t needed_bytes(const pa_shape& sh, bool q4, bool weights, int sm_count) {
     DensePlan d;
     if (dense_take(sh, q4, weights, sm_count, &d)) return d.total;
     if (tiles_take(sh, q4, sm_count)) {
@@ -187,12 +196,43 @@ size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_co
     return plan(sh, q4, weights, sm_count).total;
 }
 
+// The most that a call of at most this B, L and max_pages_per_seq needs.  Which kernel takes
+// a call is not monotone in them (a decode step stores scores, a chunk does not), so each
+// part is counted for every kernel that some smaller call may take, at its largest.
+size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_count) {
+    const size_t cap = static_cast<size_t>(sh.max_pages_per_seq) * sh.page_size, sms = static_cast<size_t>(sm_count);
+    const size_t G = sh.H_q / sh.H_kv, R = G * sh.L, bk = static_cast<size_t>(sh.B) * sh.H_kv, rows = bk * R;
+    const bool f32 = sh.dtype == PA_F32;
+    constexpr size_t kState = 16 + kD * 4;  // of a row: max and sums, O
+    const size_t lse = weights ? rows * 4 : 0, scratch = weights ? weights_scratch_most(sh, sm_count) : 0;
+    // walk_kernel with 8 or 16 rows a CTA, block_kernel with 64
+    auto shares = [&](size_t ctas, size_t rows_cta) { return ctas * (16 + 2 * rows_cta * kState); };
+    size_t few = 0;
+    if (cap > kWholeKeys) few = shares(sms * walk_resident(1, q4, f32, 1), 8);
+    if (cap > kWholeKeys && R > 8 && !f32) few = std::max(few, shares(sms * walk_resident(2, q4, f32, 16), 16));
+    if (R >= kBlockRows) few = std::max(few, shares(sms * 2, kBlockCtaRows));
+    size_t scores = 0;
+    if (weights && G <= kScoreRows)
+        scores = std::min(bk * G * std::min<size_t>(sh.L, kScoreRows / G) * cap * 4, kScoreBytes);
+    size_t most = few + lse + std::max(scores, scratch);
+    if (!f32 && R >= (q4 ? kTileRowsMany : kTileRowsManyBf16))
+        most = std::max(most, tiles_workspace_most(sh, sm_count) + lse + scratch);
+    if (q4 && !weights && !f32 && R >= kTileRows) {  // bf16 copies of up to 2 R keys
+        const size_t per_seq = (std::min(cap, 2 * R) + 127) / 128 * 128 * sh.H_kv * kD * 2 * 2;
+        const size_t copies = std::max(per_seq, std::min(per_seq * sh.B, kDenseBytes));
+        const size_t states = std::max(rows, 256 * sms + 128 * bk) + 256 * bk;  // key chunks, a short last tile
+        most = std::max(most, tile_partials_offset(sh, sm_count) + states * kState + 8 * static_cast<size_t>(sh.B) + copies);
+    }
+    most = align_up(kFlagBytes + most + 16 * 256, 256);  // (each part starts on 256 bytes)
+    return std::max(most, needed_bytes(sh, q4, weights, sm_count));
+}
+
 pa_status walk_launch(const WalkCall& c) {
     const pa_shape& sh = c.sh;
     const bool tiles = tiles_take(sh, c.ks != nullptr, c.dev.sm_count);
     const WalkPlan w = plan(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count);
     if (c.w_out && !weights_supported(sh, c.w_S, c.dev.sm_count)) return PA_ERR_UNSUPPORTED;
-    if (c.ws_bytes < walk_workspace_bytes(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count)) return PA_ERR_WORKSPACE;
+    if (c.ws_bytes < needed_bytes(sh, c.ks != nullptr, c.w_out != nullptr, c.dev.sm_count)) return PA_ERR_WORKSPACE;
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
     WalkParams p;
     p.q = c.q;

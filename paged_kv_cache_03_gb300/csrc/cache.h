@@ -46,6 +46,7 @@ struct WalkCall {
     cudaStream_t stream;
     DeviceInfo dev;
 };
+// Enough for this shape and any with at most its B, L and max_pages_per_seq.
 size_t walk_workspace_bytes(const pa_shape& sh, bool q4, bool weights, int sm_count);
 pa_status walk_launch(const WalkCall& c);
 
@@ -53,6 +54,7 @@ pa_status walk_launch(const WalkCall& c);
 // (tiles.cu); lse: [B, H_q, L], or null.
 bool tiles_supported(const pa_shape& sh, int sm_count);
 size_t tiles_workspace_bytes(const pa_shape& sh, int sm_count);
+size_t tiles_workspace_most(const pa_shape& sh, int sm_count);  // ... of any smaller call
 pa_status tiles_launch(const WalkCall& c, float* lse);
 
 // Eviction from the buffers K and V (rows of sh.dtype) or, where buf[2] is not

@@ -1298,6 +1298,10 @@ bool tiles_supported(const pa_shape& sh, int sm_count) {
 }
 
 size_t tiles_workspace_bytes(const pa_shape& sh, int sm_count) { return plan(sh, sm_count).total; }
+size_t tiles_workspace_most(const pa_shape& sh, int sm_count) {
+    const size_t slots = 4ull * sm_count * BM, rem_slots = (static_cast<size_t>(sh.B) * sh.H_kv + sm_count) * 2 * 8;
+    return kFlagBytes + 4 * (static_cast<size_t>(sh.B) + 1) + 16ull * sm_count + (slots + rem_slots) * (8 + kD * 4) + 6 * 256;
+}
 
 pa_status tiles_launch(const WalkCall& c, float* lse) {
     const pa_shape& sh = c.sh;

@@ -656,6 +656,7 @@ pa_status merge_shares(const WalkParams& p, int rows_cta, int shares, bool f32, 
 pa_status weights_from_scores(const WalkParams& p, cudaStream_t stream);
 bool weights_supported(const pa_shape& sh, long long w_S, int sm_count);
 size_t weights_scratch_bytes(const pa_shape& sh, int sm_count);
+size_t weights_scratch_most(const pa_shape& sh, int sm_count);  // ... of any smaller call
 pa_status weights_from_keys(const WalkParams& p, bool q4, bool f32, void* scratch, const DeviceInfo& dev,
                             cudaStream_t stream);
 // The query rows of a (sequence, kv head) cut into n runs, each CTA taking one; n > 1:

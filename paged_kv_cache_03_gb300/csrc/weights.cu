@@ -278,13 +278,23 @@ bool weights_supported(const pa_shape& sh, long long w_S, int sm_count) {
     return w_S <= INT_MAX / 2 && w_S / kKeysCta < most && bk * ((R + 7) / 8) <= INT_MAX;
 }
 
+// The packed query of fp32 calls.
+static size_t packed_bytes(const pa_shape& sh) {
+    const size_t tile = 2 * 128 * 16 + 8 * (sizeof(PackedRow) + sizeof(int));
+    const long long R = static_cast<long long>(sh.H_q / sh.H_kv) * sh.L;
+    return sh.dtype == PA_F32 ? static_cast<size_t>(sh.B) * sh.H_kv * ((R + 7) / 8) * tile : 0;
+}
+
 size_t weights_scratch_bytes(const pa_shape& sh, int sm_count) {
     const long long bk = static_cast<long long>(sh.B) * sh.H_kv;
     const long long R = static_cast<long long>(sh.H_q / sh.H_kv) * sh.L;
     const long long cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
-    const size_t tile = 2 * 128 * 16 + 8 * (sizeof(PackedRow) + sizeof(int));  // of the packed query
-    return runs_bytes(bk, cap, static_cast<int>(R), sm_count) +
-           (sh.dtype == PA_F32 ? static_cast<size_t>(bk) * ((R + 7) / 8) * tile : 0);
+    return runs_bytes(bk, cap, static_cast<int>(R), sm_count) + packed_bytes(sh);
+}
+
+size_t weights_scratch_most(const pa_shape& sh, int sm_count) {
+    // runs: two CTAs an SM and the CTAs of one run, themselves less than that, 128 keys each
+    return 4ull * sm_count * kKeysCta * 4 + 16 + packed_bytes(sh);
 }
 
 pa_status weights_from_keys(const WalkParams& p, bool q4, bool f32, void* scratch, const DeviceInfo& dev,

@@ -172,3 +172,56 @@ def test_nan_rows(where, c, weights):
         bad &= np.arange(inp.cap) < inp.ctx[:, None, None]
         bad = torch.from_numpy(bad).cuda()
         assert torch.isnan(got_w[bad]).all() and torch.equal(got_w[~bad], w[~bad])
+
+
+@pytest.mark.parametrize("pool,dtype", [("q4", "bf16"), ("q4", "f32"), ("bf16", "bf16")])
+def test_one_workspace_for_every_smaller_call(pool, dtype):
+    """Sized for the largest batch, chunk and table, a workspace serves the decode steps,
+    short chunks, small batches and narrow tables."""
+    def case(Bn, L, spare):
+        return Case(Bn, 4, 2, L, 16, spread(Bn, L, 300), pool=pool, dtype=dtype, spare=spare)
+    big = case(16, 65, 1000)
+    ws = workspace(big, ref.Inputs(big).device())
+    for c in (big, case(16, 1, 1000), case(3, 2, 1000), case(16, 8, 60), case(1, 16, 3), case(2, 33, 0),
+              case(16, 1, 0)):
+        inp = ref.Inputs(c)
+        d = inp.device()
+        for weights in ((True, False) if pool == "q4" else (True,)):
+            out, w = attend(inp, d, ws, weights)
+            check(inp, out, w)
+    assert B.pa_check_device_flag(ws)[1] == 0
+
+
+def test_workspace_sizes_are_monotone():
+    """pa_*_workspace_bytes of any shape with at most the B, L and table of another."""
+    rng = np.random.default_rng(8)
+    for _ in range(300):
+        G, H = int(rng.choice([1, 2, 4, 7, 8, 16, 48, 130])), int(rng.choice([1, 2, 8]))
+        dtype, ps = int(rng.choice([B.PA_BF16, B.PA_F32])), int(rng.choice([1, 12, 16, 128]))
+        top = [int(np.exp(rng.uniform(0, np.log(m)))) for m in (500, 5000, 100000 // ps)]
+
+        def sizes(Bn, L, n):
+            sh = B.make_shape(Bn, G * H, H, L, 128, 1000, ps, n, dtype)
+            got = [B.pa_q4_workspace_bytes(sh, False), B.pa_q4_workspace_bytes(sh, True)]
+            return got + ([B.pa_weights_workspace_bytes(sh)] if dtype == B.PA_BF16 else [])
+        most = sizes(*top)
+        assert min(most) > 0
+        for _ in range(20):
+            less = [int(rng.integers(1, m + 1)) if rng.random() < 0.7 else m for m in top]
+            assert all(a <= b for a, b in zip(sizes(*less), most))
+
+
+@pytest.mark.parametrize("pool,dtype", [("q4", "bf16"), ("q4", "f32"), ("bf16", "bf16")])
+def test_weights_of_few_rows_over_very_wide_tables(pool, dtype):
+    """A table of 2 million slots a sequence: the scores are not stored (4 bytes a row and
+    slot would pass 512 MiB), the weights are the same."""
+    c = Case(4, 8, 2, 1, 128, [300, 1, 129, 1000], pool=pool, dtype=dtype, spare=16400)
+    inp = ref.Inputs(c)
+    d = inp.device()
+    ws = workspace(c, d)
+    assert 4 * 2 * 8 * inp.cap * 4 > 2 ** 29 >= ws.numel() - 2 ** 26
+    out, w = attend(inp, d, ws)
+    check(inp, out, w)
+    again = attend(inp, d, ws)
+    assert (again[0] == out).all() and (again[1] == w).all()
+    assert B.pa_check_device_flag(ws)[1] == 0
