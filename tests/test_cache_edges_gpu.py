@@ -225,3 +225,64 @@ def test_weights_of_few_rows_over_very_wide_tables(pool, dtype):
     again = attend(inp, d, ws)
     assert (again[0] == out).all() and (again[1] == w).all()
     assert B.pa_check_device_flag(ws)[1] == 0
+
+
+def test_whole_prompts_in_groups():
+    """Whole prompts whose bf16 copies do not fit together (tables of 65536 slots and 8 kv
+    heads: 268 MB a sequence, 1 GiB in all): six sequences go as four and two.  Every
+    sequence is as in a call of its group alone, and against 64 bits; a bad length and a bad
+    page in the second group stay where they are."""
+    import torch
+    H, G, L, ps, n = 8, 16, 2048, 128, 512
+    ctx = [2048, 2500, 4100, 3001, 2222, 2600]
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    npg = [-(-s // ps) for s in ctx]
+    P = sum(npg) + 3
+    perm = torch.randperm(P, generator=gen, device="cuda").int()
+    table = torch.full((6, n), -9, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, k in enumerate(npg):
+        table[b, :k] = perm[at:at + k]
+        at += k
+    pool = B.new_q4_pool(P, H, ps)
+    for t in (pool.key_codes, pool.value_codes):
+        t.copy_(torch.randint(0, 256, t.shape, generator=gen, device="cuda"))
+    for t in (pool.key_scales, pool.value_scales):  # 0.25 .. 0.94
+        t.copy_(torch.randint(0x28, 0x38, t.shape, generator=gen, device="cuda"))
+    q = torch.randn(6, H * G, L, 128, generator=gen, device="cuda").bfloat16()
+    lens = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+    ws = B.new_q4_workspace(q, pool, table, False)
+    assert ws.numel() > 4 * n * ps * H * 512
+
+    def call(b0, b1, table=table, lens=lens):
+        return B.paged_attention_q4(q[b0:b1], pool, table[b0:b1], lens[b0:b1], ps, workspace=ws)
+    out = call(0, 6)
+    assert torch.equal(call(0, 4), out[:4]) and torch.equal(call(4, 6), out[4:])
+    assert B.pa_check_device_flag(ws)[1] == 0
+
+    def against_64_bits(out, table, seqs):
+        K, V = B.gather_kv_q4(pool, table, lens, max(ctx), dtype=torch.float32)
+        for b in seqs:
+            for h, l in ((0, 0), (G + 3, 1000), (H * G - 1, L - 1)):
+                S = ctx[b] - L + l + 1
+                k, v = K[b, h // G, :S].double(), V[b, h // G, :S].double()
+                x = q[b, h, l].double()
+                p = torch.softmax(k @ x * float(np.float32(128 ** -0.5)), 0)
+                T = float((k.abs() @ x.abs()).max()) * 128 ** -0.5
+                want = p @ v
+                # roundings as in cache_ref.attend: scores, P in bf16 and in its sum, the output
+                tol = (T * 2.0 ** -15 + 2.0 ** -12 + 2.0 ** -7) * (p @ v.abs()) + 2.0 ** -8 * want.abs() + \
+                    2.0 ** -25 * p.max() * v.abs().sum(0)
+                assert ((out[b, h, l].double() - want).abs() <= tol).all(), (b, h, l)
+    against_64_bits(out, table, range(6))
+    bad = lens.clone()
+    bad[5] = n * ps + 1
+    got = call(0, 6, lens=bad)
+    assert B.pa_check_device_flag(ws, clear=True)[1] == B.PA_FLAG_BAD_CONTEXT
+    assert torch.equal(got[:5], out[:5]) and not got[5].any()
+    hole = table.clone()
+    hole[4, 3] = P + 7
+    got = call(0, 6, table=hole)
+    assert B.pa_check_device_flag(ws, clear=True)[1] == B.PA_FLAG_BAD_PAGE
+    assert torch.equal(got[:4], out[:4]) and torch.equal(got[5], out[5])
+    against_64_bits(got, hole, [4])
