@@ -524,7 +524,8 @@ class Q4Pool:
 
 class Evicted(NamedTuple):
     """What an eviction leaves: the new lengths [B], the kept keys' weights
-    [B, H_kv, n] and their old positions [B, H_kv, keep] (-1 past the end)."""
+    [B, H_kv, keep] (or the caller's key_weights_out) and their old positions
+    [B, H_kv, keep] (-1 past the end)."""
     context_lens: object
     key_weights: object
     kept: object
@@ -802,7 +803,7 @@ def paged_attention_weights(query, key_pages, value_pages, block_table, context_
 
 
 def _evict(name, fn, pools, dims, dtype_id, device, block_table, context_lens, key_weights, keep,
-           recent, dst_block_table, workspace):
+           recent, dst_block_table, key_weights_out, workspace):
     torch = _torch or _load_torch()
     P, H_kv, ps = dims
     B_ = block_table.shape[0]
@@ -819,35 +820,43 @@ def _evict(name, fn, pools, dims, dtype_id, device, block_table, context_lens, k
         raise ValueError("keep must be at least 1 and fit dst_block_table")
     shape = pa_shape(B_, H_kv, H_kv, 1, 128, P, ps, block_table.shape[1], dtype_id)
     lens = torch.empty(B_, dtype=torch.int32, device=device)
-    weights = torch.empty((B_, H_kv, keep), dtype=torch.float32, device=device)
+    weights = key_weights_out
+    if weights is None:
+        weights = torch.empty((B_, H_kv, keep), dtype=torch.float32, device=device)
+    else:
+        _weights_shape("key_weights_out", weights, B_, H_kv, keep)
+        _on_device(index, ("key_weights_out", weights))
     kept = torch.empty((B_, H_kv, keep), dtype=torch.int32, device=device)
     _launch(name, index, fn, ctypes.byref(shape), *pools, block_table.data_ptr(),
             context_lens.data_ptr(), key_weights.data_ptr(), key_weights.shape[2], keep, recent,
             dst_block_table.data_ptr(), dst_block_table.shape[1], lens.data_ptr(),
-            weights.data_ptr(), keep, kept.data_ptr(), workspace.data_ptr(), workspace.numel())
+            weights.data_ptr(), weights.shape[2], kept.data_ptr(), workspace.data_ptr(), workspace.numel())
     return Evicted(lens, weights, kept)
 
 
 @_streamed
 def evict_kv(key_pages, value_pages, block_table, context_lens, key_weights, keep, recent,
-             dst_block_table, *, workspace=None) -> Evicted:
+             dst_block_table, *, key_weights_out=None, workspace=None) -> Evicted:
     """Trims every (sequence, kv head) to its `recent` last keys and the
     heaviest others, `keep` in all, copied in order to the pages of
     dst_block_table [B, n] (other pages of the same pool).  Returns the new
-    lengths, the kept keys' weights [B, H_kv, keep] and their old positions."""
+    lengths, the kept keys' weights [B, H_kv, keep] and their old positions.
+    key_weights_out (fp32 [B, H_kv, S], S >= keep, not key_weights) receives
+    the weights, then zeros: with S the new table's capacity it goes straight
+    into the next attention call."""
     dims = _pages_dims(key_pages, value_pages)
     if key_pages.shape[3] != 128:
         raise ValueError("head dim must be 128")
     return _evict("pa_evict_kv", (_lib or load()).pa_evict_kv,
                   (key_pages.data_ptr(), value_pages.data_ptr()), dims,
                   _dtype_id(key_pages.dtype), key_pages.device, block_table, context_lens,
-                  key_weights, keep, recent, dst_block_table, workspace)
+                  key_weights, keep, recent, dst_block_table, key_weights_out, workspace)
 
 
 @_streamed
 def evict_kv_q4(pool, block_table, context_lens, key_weights, keep, recent, dst_block_table, *,
-                workspace=None) -> Evicted:
+                key_weights_out=None, workspace=None) -> Evicted:
     """evict_kv of a 4-bit pool."""
     return _evict("pa_evict_kv_q4", (_lib or load()).pa_evict_kv_q4, (ctypes.byref(pool.c_pool),),
                   pool.dims, PA_BF16, pool.device, block_table, context_lens, key_weights, keep,
-                  recent, dst_block_table, workspace)
+                  recent, dst_block_table, key_weights_out, workspace)

@@ -286,3 +286,35 @@ def test_whole_prompts_in_groups():
     assert B.pa_check_device_flag(ws, clear=True)[1] == B.PA_FLAG_BAD_PAGE
     assert torch.equal(got[:4], out[:4]) and torch.equal(got[5], out[5])
     against_64_bits(got, hole, [4])
+
+
+@pytest.mark.parametrize("pool", ["q4", "bf16"])
+def test_evicted_weights_go_on_without_a_copy(pool):
+    """key_weights_out of an eviction is the key_weights of the next attention call."""
+    import torch
+    c = Case(3, 4, 2, 1, 16, [300, 40, 500], pool=pool)
+    inp = ref.Inputs(c, extra_pages=3 * 5)
+    d = inp.device()
+    dst = torch.from_numpy(inp.free[:15].reshape(3, 5).astype(np.int32)).cuda()
+    evict = B.evict_kv_q4 if pool == "q4" else B.evict_kv
+    pages = (d["pool"],) if pool == "q4" else d["pool"]
+    args = (*pages, d["table"], d["ctx"], d["w"], 60, 7, dst)
+    plain = evict(*args)
+    w2 = torch.full((3, 2, 80), float("nan"), device="cuda")
+    new = evict(*args, key_weights_out=w2)
+    assert new.key_weights is w2 and torch.equal(w2[:, :, :60], plain.key_weights)
+    assert not w2[:, :, 60:].any() and torch.equal(new.kept, plain.kept)
+    assert plain.key_weights.shape == (3, 2, 60)
+    # the attention that follows, with w2 in place and with a copy
+    copy = torch.nn.functional.pad(plain.key_weights, (0, 20))
+    d["table"], d["ctx"] = dst, new.context_lens
+    call = B.paged_attention_q4 if pool == "q4" else B.paged_attention_weights
+    outs = [call(d["q"], *pages, dst, new.context_lens, 16, key_weights=w, key_weights_out=w)
+            for w in (w2, copy)]
+    assert torch.equal(*outs) and torch.equal(w2, copy)
+    for bad in (w2[:, :, :59].contiguous(), w2.double(), w2[:2].contiguous(), w2.cpu(),
+                w2.transpose(0, 1).contiguous().transpose(0, 1)):
+        with pytest.raises(ValueError):
+            evict(*args, key_weights_out=bad)
+    with pytest.raises(B.PagedAttentionError):  # not in place
+        evict(*args, key_weights_out=d["w"])
