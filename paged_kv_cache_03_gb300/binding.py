@@ -624,15 +624,21 @@ def _launch(name, index, fn, *args):
 
 def _streamed(fn):
     """Runs the call with its `stream` argument (a torch stream or a raw
-    handle) current, so that what it allocates, zeroes and returns belongs to
-    that stream too."""
+    handle, of the tensors' device) current, so that what it allocates, zeroes
+    and returns belongs to that stream too."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
         import torch
+        device = next((x.device for x in (*args, *kw.values()) if hasattr(x, "device")), None)
+        if device is None or device.type != "cuda":
+            return fn(*args, **kw)  # (which refuses it)
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
+                torch.cuda.default_stream(device)
+        elif stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         with torch.cuda.stream(stream):
             return fn(*args, **kw)
     return call

@@ -318,3 +318,20 @@ def test_evicted_weights_go_on_without_a_copy(pool):
             evict(*args, key_weights_out=bad)
     with pytest.raises(B.PagedAttentionError):  # not in place
         evict(*args, key_weights_out=d["w"])
+
+
+def test_streams_as_raw_handles():
+    """A raw handle, 0 (the default stream) and a stream object, from another current stream."""
+    import torch
+    c = Case(2, 4, 2, 1, 16, [300, 1900])
+    inp = ref.Inputs(c)
+    d = inp.device()
+    ws = workspace(c, d)
+    want = attend(inp, d, ws)
+    torch.cuda.synchronize()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        for stream in (side, side.cuda_stream, 0):
+            got = attend(inp, d, ws, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
