@@ -824,6 +824,8 @@ def _evict(name, fn, pools, dims, dtype_id, device, block_table, context_lens, k
                ("workspace", workspace))
     if not 1 <= keep <= dst_block_table.shape[1] * ps:
         raise ValueError("keep must be at least 1 and fit dst_block_table")
+    if not 0 <= recent <= keep:
+        raise ValueError("recent must be at least 0 and at most keep")
     shape = pa_shape(B_, H_kv, H_kv, 1, 128, P, ps, block_table.shape[1], dtype_id)
     lens = torch.empty(B_, dtype=torch.int32, device=device)
     weights = key_weights_out

@@ -56,3 +56,14 @@ def test_streams_of_another_device_are_refused(calls):
     stream.device = x.device
     assert call(x, stream=stream) is x and calls == [stream]
     assert call(x) is x and len(calls) == 1
+
+
+@pytest.mark.parametrize("recent", [-1, 21, 2 ** 32])
+def test_recent_out_of_range(recent, monkeypatch):
+    """(2 ** 32 would reach a C int as 0.)"""
+    import torch
+    monkeypatch.setattr(B, "_on_device", lambda *a: None)
+    table, ctx = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="recent"):
+        B._evict("x", None, (), (4, 1, 16), B.PA_BF16, on("cuda:0").device, table, ctx,
+                 torch.zeros(1, 1, 32), 20, recent, table, None, torch.zeros(256, dtype=torch.uint8))
