@@ -476,10 +476,7 @@ pa_status launch_walk_for(const WalkParams& p, long long items, int device, cuda
                : launch_walk<Keys, Values, NT, F32, false, false>(p, items, device, stream);
 }
 
-
 }  // namespace
-
-size_t walk_shared_bytes(bool q4, int rows) { return walk_smem(q4, rows); }
 
 int walk_resident(int nt, bool q4, bool f32, int rows) {
     // (bf16 pages: 16 KB of stages a warp leave room for three CTAs of 4 merge rows)

@@ -437,34 +437,37 @@ struct QueryFrags {
         }
     }
     __device__ __forceinline__ float finish() {
-        if constexpr (!F32 && !Keys::kF16) return 1.f;
-        float2 f[16];
+        if constexpr (F32 || Keys::kF16) {
+            float2 f[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            if constexpr (F32)
-                f[k] = make_float2(__uint_as_float(hi[k >> 1][k & 1]), __uint_as_float(lo[k >> 1][k & 1]));
-            else
-                f[k] = bf16x2_to_float2(hi[k >> 1][k & 1]);
-        }
-        // into f16's range: the row's largest value into [2^14, 2^15)
-        float mx = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        float up, down;
-        f16_scale(mx, up, down);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float x = f[k].x * up, y = f[k].y * up;
-            const uint32_t h = pack_f16x2(x, y);
-            hi[k >> 1][k & 1] = h;
-            if constexpr (F32) {
-                const float2 b = f16x2_to_float2(h);
-                lo[k >> 1][k & 1] = pack_f16x2(x - b.x, y - b.y);
+            for (int k = 0; k < 16; ++k) {
+                if constexpr (F32)
+                    f[k] = make_float2(__uint_as_float(hi[k >> 1][k & 1]), __uint_as_float(lo[k >> 1][k & 1]));
+                else
+                    f[k] = bf16x2_to_float2(hi[k >> 1][k & 1]);
             }
+            // into f16's range: the row's largest value into [2^14, 2^15)
+            float mx = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            float up, down;
+            f16_scale(mx, up, down);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float x = f[k].x * up, y = f[k].y * up;
+                const uint32_t h = pack_f16x2(x, y);
+                hi[k >> 1][k & 1] = h;
+                if constexpr (F32) {
+                    const float2 b = f16x2_to_float2(h);
+                    lo[k >> 1][k & 1] = pack_f16x2(x - b.x, y - b.y);
+                }
+            }
+            return down;
+        } else {
+            return 1.f;
         }
-        return down;
     }
     __device__ __forceinline__ float load(const void* q, long long row, bool ok, int t) {
         request(q, row, ok, t);
@@ -644,7 +647,6 @@ struct WalkLaunch {
     cudaStream_t stream;
 };
 pa_status walk_attend(const WalkParams& p, const WalkLaunch& w);
-size_t walk_shared_bytes(bool q4, int rows);
 int walk_resident(int nt, bool q4, bool f32, int rows);  // CTAs per SM
 // block.cu: 64 rows per CTA, 2 CTAs per SM
 constexpr int kBlockCtaRows = 64;
