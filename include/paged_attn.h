@@ -318,9 +318,19 @@ pa_status pa_paged_attention_decode_noalloc(const pa_shape* shape, const void* q
  *   scale = min(max(RNE_e4m3(max |x| over the 16 dims / 6), 2^-9), 448),
  *   code  = RNE_e2m1(x / scale), magnitudes above 6 stored as 6,
  * exactly (no code or scale depends on how a division is rounded), so values
- * beyond +-2688 saturate; a NaN makes its 16 dims NaN.  Block tables, context
- * lengths, unused slots and shared pages are as for the other pools.  In the
- * pa_shape of these calls dtype is that of the query, output or new rows. */
+ * beyond +-2688 saturate; a NaN makes its 16 dims NaN.
+ *
+ * Magnitudes: with a the largest of 16 dims, |stored - x| <= 0.18 a from a =
+ * 0.094 (6 * 2^-6) to 2688.  Below, scales are e4m3 subnormals, 2^-9 apart,
+ * and the bound is a / 6 + 0.006, no longer small beside a; from a = 2^-11
+ * down all 16 are stored as 0.  There is no scale per tensor, so rows of
+ * smaller numbers are for the caller to scale: keys times 2^k with `scale`
+ * times 2^-k, values times 2^k with the output times 2^-k (powers of two lose
+ * nothing).
+ *
+ * Block tables, context lengths, unused slots and shared pages are as for the
+ * other pools.  In the pa_shape of these calls dtype is that of the query,
+ * output or new rows. */
 typedef struct {
     void* key_codes;
     void* key_scales;

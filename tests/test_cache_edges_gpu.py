@@ -335,3 +335,32 @@ def test_streams_as_raw_handles():
             got = attend(inp, d, ws, stream=stream)
             torch.cuda.synchronize()
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_small_rows_scaled_by_a_power_of_two():
+    """Values of a few thousandths are below the scales' range; stored times 2^10, with the key's
+    factor taken out of `scale` and the value's out of the output, the attention is that of
+    rows 0.18 of a group's largest value off at most."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda")
+    k, v = normal(1, 2, 200, 128) * 2.0 ** -9, normal(1, 2, 200, 128) * 2.0 ** -9
+    q = (normal(1, 8, 1, 128) * 2.0 ** 9).bfloat16()
+    table = torch.arange(13, dtype=torch.int32, device="cuda").view(1, 13)
+    ctx = torch.tensor([200], dtype=torch.int32, device="cuda")
+    scale = 128 ** -0.5
+    pool = B.new_q4_pool(13, 2, 16)
+    B.append_kv_q4(k * 1024, v * 1024, pool, table, ctx)
+    K, V = (t.double() / 1024 for t in B.gather_kv_q4(pool, table, ctx, 200, dtype=torch.float32))
+    for stored, x in ((K, k), (V, v)):
+        a = x.view(1, 2, 200, 8, 16).abs().amax(-1, keepdim=True)
+        assert ((stored - x).view(1, 2, 200, 8, 16).abs() <= 0.18 * a).all()
+    out = B.paged_attention_q4(q, pool, table, ctx, 16, scale / 1024).double() / 1024
+    s = q.double().view(1, 2, 4, 128) @ K.transpose(2, 3) * scale
+    p = torch.softmax(s, -1)
+    T = (q.double().abs().view(1, 2, 4, 128) @ K.abs().transpose(2, 3) * scale).amax(-1, keepdim=True)
+    tol = (T * 2.0 ** -15 + 2.0 ** -11 + 2.0 ** -12) * (p @ V.abs()) + 2.0 ** -8 * (p @ V).abs() + \
+        2.0 ** -25 * p.amax(-1, keepdim=True) * V.abs().sum(2, keepdim=True)
+    assert ((out.view(1, 2, 4, 128) - p @ V).abs() <= tol).all()
