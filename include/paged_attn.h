@@ -363,6 +363,11 @@ pa_status pa_gather_kv_q4(const pa_shape* shape, const pa_q4_pool* pool,
 /* pa_paged_attention over a 4-bit pool, any L, bf16 or fp32 query and output:
  * the attention of the stored values (nothing else is rounded to 4 bits).
  * Keys behind a bad page id read as zeros (PA_FLAG_BAD_PAGE).
+ * Rounded on the way: each probability, for bf16 queries to f16 (keys below
+ * 2^-25 of a row's heaviest may be lost) or, where the query rows of a kv head
+ * are half the table's slots or more and no key weights are asked for, to bf16
+ * as pa_paged_attention does; for fp32 queries to 22 bits.  Maxima, sums and
+ * the output before its own rounding are fp32.
  * A query row with a NaN, or one that sees a key with a NaN, comes out as NaN
  * whatever the shapes, and so do the weights of the keys that it sees; other
  * rows and weights are as without it.  (A value row is different: a NaN or Inf

@@ -20,7 +20,8 @@ struct WalkPlan {
 
 // Rows per kv head from which block_kernel takes a call (walk, block, us, fp32 queries:
 // B = 8 over 1000 .. 8000 keys 61, 69 at 32 rows, 84, 71 at 48; B = 64 over 500 .. 2000
-// keys 130, 143 at 32, 186, 147 at 48; B = 1 over 16000 keys 49, 49 at 64).
+// keys 130, 143 at 32, 186, 147 at 48; B = 1 over 16000 keys 49, 49 at 64; both since 2 us
+// more, for the low parts' own range).
 constexpr int kBlockRows = 48;
 // Key weights: rows per kv head up to which scores are stored, and the most bytes of them
 // (4 for every slot of the table and row: a wide table would take more than the cache);
@@ -101,7 +102,9 @@ bool tiles_take(const pa_shape& sh, bool q4, int sm_count) {
 }
 
 // ---- whole prompts over 4-bit pages: bf16 copies and the bf16 tile kernel -------
-// (exact: a 4-bit value is a bf16 number).  Where a kv head has half as many rows as
+// (K and V exact: a 4-bit value is a bf16 number; P rounded to bf16 as over bf16 pages,
+// where the other kernels round it to f16: whole prompts 0.0020 from 64 bits, relative,
+// against 0.0017, of which 0.0016 is the bf16 output).  Where a kv head has half as many rows as
 // keys or more, the copies cost less than what tiles.cu spends per segment
 // (G = 4, H_kv = 8, us, tiles against copies: 4 x 2048 rows over 600 keys 46, 38; 4 x
 // 8192 over 2048 198, 145; 8 x 2080 over 1000 .. 8000 352, 382; 8 x 1040 209, 247; 1 x

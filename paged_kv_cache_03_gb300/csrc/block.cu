@@ -12,8 +12,8 @@
 // the writers (32 bytes a lane) and ldmatrix meet no bank conflict.
 //
 // Bound by the warp-level products, twice as many for fp32's two parts: 64 fp32 rows
-// over 8 sequences of 1000 .. 8000 4-bit keys, 8 kv heads, 82 us; 204 over 2 of 6400 ..
-// 13000, 4 kv heads, with weights 114 us.
+// over 8 sequences of 1000 .. 8000 4-bit keys, 8 kv heads, 84 us; 204 over 2 of 6400 ..
+// 13000, 4 kv heads, with weights 114 to 124 us by the lengths drawn.
 #include "walk.cuh"
 
 namespace pa {

@@ -109,9 +109,10 @@ __device__ __forceinline__ uint2 encode16(const float (&x)[16], uint32_t& sb) {
     return make_uint2(code[0], code[1]);
 }
 
-// Eight threads a row, 16 dims each, its key and its value.  Bound by the rows
-// read: 512 bytes in (bf16) for 144 out; 4 x 8 heads x 2048 rows 15 us, 2.8 TB/s, the
-// conversions and divisions of a row beside its loads.
+// Eight threads a row, 16 dims each, its key and its value: 512 bytes in (bf16) for 144
+// out.  4 x 8 heads x 2048 rows 15.8 us, 3.0 TB/s.  Bound by latency: 8.3 M warp instructions
+// are about 7 us of issue, and a thread loads its row, then encodes it, with no other row
+// on its way.
 template <typename T>
 __global__ void __launch_bounds__(256) q4_append_kernel(const Q4AppendParams p) {
     const int u = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x);

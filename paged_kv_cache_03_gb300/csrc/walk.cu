@@ -34,10 +34,11 @@
 // probabilities in a fixed order (no atomics: a call's results repeat bit for bit).
 //
 // Measured (G = 4, H_kv = 8, one query position, L2 flushed): 16 sequences of 32768
-// 4-bit keys 118 us, 5.1 TB/s of rows read; 64 of 128 .. 4096 45 us, 3.5 TB/s: bound by
-// the conversions of codes to f16, which issue at half rate, and with short contexts by
-// the start and the merge of each segment; 64 of 128 .. 4096 bf16 keys with weights 104 us,
-// 5.4 TB/s.
+// 4-bit keys 118 us, 5.1 TB/s of rows read; 64 of 128 .. 4096 45 us, 3.5 TB/s.  No pipe is
+// full there (issue 61% of active cycles, ALU 46%): 3.5 warps a scheduler wait for chains of
+// a code's conversion, product and exponential; with short contexts 15% is the launch's
+// start and end, and a merge follows.  64 of 128 .. 4096 bf16 keys with weights 106 us,
+// 5.3 TB/s.
 #include "walk.cuh"
 
 namespace pa {
