@@ -403,9 +403,10 @@ size_t pa_q4_workspace_bytes(const pa_shape* shape, int key_weights);
 /* ---- Key weights and eviction ----------------------------------------------
  *
  * pa_paged_attention over bf16 pages that also accumulates what every key
- * received (key_weights_out required; see pa_paged_attention_q4).  fp32 pools
- * are PA_ERR_UNSUPPORTED.  workspace: pa_weights_workspace_bytes(shape), as
- * for pa_paged_attention_q4. */
+ * received (key_weights_out required; see pa_paged_attention_q4).  The output's
+ * probabilities are rounded to bf16 as there, those of the weights are not.
+ * fp32 pools are PA_ERR_UNSUPPORTED.  workspace:
+ * pa_weights_workspace_bytes(shape), as for pa_paged_attention_q4. */
 pa_status pa_paged_attention_weights(const pa_shape* shape, const void* query,
                                      const void* key_pages, const void* value_pages,
                                      const int32_t* block_table, const int32_t* context_lens,
