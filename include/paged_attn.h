@@ -380,7 +380,8 @@ pa_status pa_gather_kv_q4(const pa_shape* shape, const pa_q4_pool* pool,
  * fp32 [B, H_kv, weights_S], weights_S >= max_pages_per_seq * page_size; a
  * null key_weights counts as zeros, and key_weights may be key_weights_out
  * itself (accumulated in place).  The sum's order is fixed: equal calls give
- * equal bits.  key_weights without key_weights_out is PA_ERR_INVALID_ARG.
+ * equal bits.  key_weights without key_weights_out is PA_ERR_INVALID_ARG, 2^27
+ * query rows per kv head or more with them are PA_ERR_UNSUPPORTED.
  *
  * workspace: pa_q4_workspace_bytes(shape, key_weights_out != NULL), 256-byte
  * aligned, its first 256 bytes zeroed once by the caller; calls that may

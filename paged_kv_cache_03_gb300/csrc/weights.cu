@@ -273,7 +273,8 @@ pa_status weights_from_scores(const WalkParams& p, cudaStream_t stream) {
 bool weights_supported(const pa_shape& sh, long long w_S, int sm_count) {
     const long long bk = static_cast<long long>(sh.B) * sh.H_kv, cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     const long long R = static_cast<long long>(sh.H_q / sh.H_kv) * sh.L;
-    // items and blocks are counted in ints
+    // items and blocks are counted in ints, and so are a kv head's query tiles times 128
+    if (R >= (1ll << 27)) return false;
     const long long most = INT_MAX / 2 / bk / row_runs(bk, cap, static_cast<int>(R), sm_count);
     return w_S <= INT_MAX / 2 && w_S / kKeysCta < most && bk * ((R + 7) / 8) <= INT_MAX;
 }

@@ -364,3 +364,14 @@ def test_small_rows_scaled_by_a_power_of_two():
     tol = (T * 2.0 ** -15 + 2.0 ** -11 + 2.0 ** -12) * (p @ V.abs()) + 2.0 ** -8 * (p @ V).abs() + \
         2.0 ** -25 * p.amax(-1, keepdim=True) * V.abs().sum(2, keepdim=True)
     assert ((out.view(1, 2, 4, 128) - p @ V).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("G,L,status", [(1, 2 ** 27, B.PA_ERR_UNSUPPORTED), (8, 2 ** 24, B.PA_ERR_UNSUPPORTED),
+                                        (1, 2 ** 27 - 1, B.PA_ERR_WORKSPACE)])
+def test_too_many_rows_for_the_weights(G, L, status):
+    """Refused on the host.  (No workspace: nothing could be launched in any case.)"""
+    fake = 1 << 20
+    sh = B.make_shape(1, G, 1, L, 128, 16, 16, 8, B.PA_F32)
+    st = B.pa_paged_attention_q4(sh, fake, (fake,) * 4, fake, fake, 0.1, 0, None, fake, 128, fake,
+                                 fake, 0, 0)
+    assert st == status
