@@ -88,6 +88,8 @@ typedef enum {
 #define PA_FLAG_BAD_CONTEXT 0x2u /* context_lens[b] < 1, > max_pages_per_seq*page_size,
                                     or < L under causal: that sequence's rows are 0 */
 #define PA_FLAG_TIMEOUT 0x4u     /* an on-chip pipeline wait gave up (bounded spin) */
+#define PA_FLAG_BAD_TREE 0x8u    /* a draft's parent or an accepted path breaks the contract */
+#define PA_FLAG_NO_PAGES 0x10u   /* too few free pages: a sequence did not grow */
 
 typedef struct {
     int B, H_q, H_kv, L, D, num_pages, page_size, max_pages_per_seq;
@@ -455,6 +457,154 @@ pa_status pa_evict_kv_q4(const pa_shape* shape, const pa_q4_pool* pool,
                          int32_t* context_lens_out, float* key_weights_out,
                          long long weights_out_S, int32_t* kept, void* workspace,
                          size_t workspace_bytes, void* cuda_stream);
+
+/* ---- Trees of drafted tokens ------------------------------------------------
+ *
+ * Speculative decoding appends L drafted tokens to every sequence (pa_append_kv,
+ * or pa_append_kv_q4: they are the last L of its context_lens[b] positions),
+ * attends them in one call, and keeps those that the model agrees with.  The
+ * drafts form trees: parents [B, L] int32, parents[b, i] < i the draft that draft i
+ * follows, -1 for the last position before the drafts, -2 for a slot without a
+ * draft (a sequence with fewer than L; what follows such a slot is none either).
+ * Several drafts may have no parent.  L is at most 1024 (PA_ERR_UNSUPPORTED).
+ *
+ * pa_tree_mask writes what every draft sees of the drafts, its ancestors and
+ * itself, once per step for all layers:
+ *   mask [B, L, W], W = (L + 31) / 32 words: bit n % 32 of word n / 32 of
+ *     mask[b, i] is 1 where draft i sees draft n; all 0 for a slot without a draft;
+ *   depths [B, L] int32: how many ancestors a draft has (its position is
+ *     context_lens[b] - L + depth), -1 for a slot without a draft.
+ * A parent that is neither -2, -1 nor below its child counts as -2 and sets
+ * PA_FLAG_BAD_TREE.  workspace: >= 256 bytes, zeroed once. */
+pa_status pa_tree_mask(int B, int L, const int32_t* parents, uint32_t* mask, int32_t* depths,
+                       void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* pa_paged_attention for the shape->L drafts of every sequence: draft i sees all
+ * context_lens[b] - L positions before the drafts and the drafts n whose bit is
+ * set in tree_mask[b, i] (laid out as by pa_tree_mask, 4-byte aligned; any set of
+ * drafts, in any order of the slots).  A slot whose own words are all 0 holds no
+ * draft: its output is 0, no draft sees it whatever its bits say, and its key and
+ * value rows may hold anything.  bf16 or fp32 pages of the query's type, any page
+ * size and group size.
+ * Rounded on the way: with bf16 queries each probability to bf16 (2^-8), the sums
+ * that divide the output adding the rounded ones; nothing else.  Maxima, sums and
+ * the output before its own rounding are fp32.  NaN as in pa_paged_attention_q4.
+ * A sequence with context_lens[b] < L or above the table's capacity sets
+ * PA_FLAG_BAD_CONTEXT and gets zero rows; keys behind a bad page id read as zeros
+ * (PA_FLAG_BAD_PAGE).
+ * workspace: pa_tree_workspace_bytes(shape), 256-byte aligned, its first 256 bytes
+ * zeroed once; calls that may overlap need their own.  Enough for this shape and
+ * for every one with at most its B, L and max_pages_per_seq (all else equal); 0
+ * for an invalid shape or without a device.  Returns as pa_paged_attention_sched. */
+pa_status pa_paged_attention_tree(const pa_shape* shape, const void* query, const void* key_pages,
+                                  const void* value_pages, const int32_t* block_table,
+                                  const int32_t* context_lens, const uint32_t* tree_mask,
+                                  float scale, void* out, void* workspace, size_t workspace_bytes,
+                                  void* cuda_stream);
+size_t pa_tree_workspace_bytes(const pa_shape* shape);
+
+/* pa_paged_attention_tree over a 4-bit pool, bf16 or fp32 query and output. */
+pa_status pa_paged_attention_tree_q4(const pa_shape* shape, const void* query,
+                                     const pa_q4_pool* pool, const int32_t* block_table,
+                                     const int32_t* context_lens, const uint32_t* tree_mask,
+                                     float scale, void* out, void* workspace,
+                                     size_t workspace_bytes, void* cuda_stream);
+
+/* Keeps the accepted drafts: of sequence b the n = path_lens[b] drafts path[b, 0] <
+ * path[b, 1] < ... < path[b, n - 1] (path [B, path_n] int32, entries past n are not
+ * read).  Their key and value rows move, in place and in this order, to the
+ * positions right behind those before the drafts, context_lens[b] - L + j, and
+ *   context_lens_out[b] = context_lens[b] - L + n  (not context_lens itself).
+ * The rows behind the last kept one stay as they were.  The pages that hold the
+ * drafts must be the sequence's own (pa_resize_pages sees to it).  One call per
+ * layer: all calls read the same context_lens.
+ * Shape fields used: B, H_kv, L, num_pages, page_size, max_pages_per_seq, dtype (of
+ * the pool).  A path that does not ascend within [0, L), or is longer than L or
+ * path_n, sets PA_FLAG_BAD_TREE: nothing moves and context_lens_out[b] =
+ * context_lens[b] - L.  A context length outside [L, capacity] sets
+ * PA_FLAG_BAD_CONTEXT and is handed on.  A row whose old or new page id is out of
+ * range does not move (PA_FLAG_BAD_PAGE).  workspace: >= 256 bytes, zeroed once. */
+pa_status pa_compact_kv(const pa_shape* shape, void* key_pages, void* value_pages,
+                        const int32_t* block_table, const int32_t* context_lens,
+                        const int32_t* path, int path_n, const int32_t* path_lens,
+                        int32_t* context_lens_out, void* workspace, size_t workspace_bytes,
+                        void* cuda_stream);
+
+/* pa_compact_kv of a 4-bit pool: codes and scales move as they are. */
+pa_status pa_compact_kv_q4(const pa_shape* shape, const pa_q4_pool* pool,
+                           const int32_t* block_table, const int32_t* context_lens,
+                           const int32_t* path, int path_n, const int32_t* path_lens,
+                           int32_t* context_lens_out, void* workspace, size_t workspace_bytes,
+                           void* cuda_stream);
+
+/* ---- Pages shared between sequences ----------------------------------------
+ *
+ * Block table, lengths and a count of holders per page live on the device:
+ * page_refs [num_pages] int32 is the number of table rows that name a page within
+ * their lengths, 0 for a free page (a caller that keeps pages to itself gives them
+ * any other count).  A row of length 0 holds nothing.  The three calls below change
+ * them in place; each is asynchronous, so a step's calls follow one another on one
+ * stream without the host knowing a length.  What they decide depends on the
+ * numbers of rows and pages alone: equal calls give equal tables.
+ * Shape fields used: B (rows of the table), num_pages, page_size,
+ * max_pages_per_seq; the others must be valid.
+ *
+ * pa_fork_pages: row targets[i] becomes a fork of row sources[i], for i < n (int32
+ * device arrays): it names the source's first pages, as many as its first lens[i]
+ * positions have (lens null: all of them), whose counts go up by one, -1 behind
+ * them, and context_lens[targets[i]] = that length.  No row of K or V is copied:
+ * a shared page is read by all, and pa_resize_pages gives a sequence that is about
+ * to write into one a page of its own.  Sources are taken as they were before the
+ * call.  PA_FLAG_BAD_CONTEXT, and that fork is not made, for a row outside [0, B),
+ * a target that is not empty (length 0), that is also a source of the same fork or
+ * of another of this call, or that an earlier fork of this call has, and a length
+ * outside [0, context_lens[sources[i]]].  A page id out of range is copied but not
+ * counted (PA_FLAG_BAD_PAGE).  n = 0 is PA_OK.  workspace: >= 256 bytes, zeroed
+ * once. */
+pa_status pa_fork_pages(const pa_shape* shape, int32_t* block_table, int32_t* context_lens,
+                        int32_t* page_refs, const int32_t* sources, const int32_t* targets,
+                        const int32_t* lens, int n, void* workspace, size_t workspace_bytes,
+                        void* cuda_stream);
+
+/* pa_resize_pages: every sequence with new_lens[b] >= 0 gets that length (new_lens
+ * [B], not context_lens itself); a negative one leaves it alone.
+ *   Shorter (0: freed): the counts of the pages past the new end go down by one and
+ *   their entries become -1.
+ *   Longer: pages for the new positions, the lowest free ones, rows in ascending
+ *   order (pages that other sequences give up in the same call included).  Where the
+ *   last page is partly filled and others hold it, it is replaced by a free page,
+ *   its count goes down by one, and copies[b] (int32 [B, 3]) = (old page, new page,
+ *   rows) says what pa_copy_pages has to copy before anything is written and before
+ *   the next resize; (-1, -1, 0) where nothing has to be.  Where all holders of a
+ *   page grow in this call, the last row of them keeps it.
+ * The new positions' rows hold whatever the pages held.
+ * PA_FLAG_NO_PAGES: there were too few free pages, and from the first sequence on
+ * that found too few none that needs a page grew (their lengths are as before).
+ * PA_FLAG_BAD_CONTEXT: a length, old or new, above the capacity or an old one below
+ * 0 (left alone).  PA_FLAG_BAD_PAGE: an entry out of range, or a page that nobody
+ * held, was not given back.
+ * workspace: pa_pages_workspace_bytes(shape), 256-byte aligned, its first 256 bytes
+ * zeroed once; calls that may overlap need their own. */
+pa_status pa_resize_pages(const pa_shape* shape, int32_t* block_table, int32_t* context_lens,
+                          int32_t* page_refs, const int32_t* new_lens, int32_t* copies,
+                          void* workspace, size_t workspace_bytes, void* cuda_stream);
+size_t pa_pages_workspace_bytes(const pa_shape* shape);
+
+/* The copies [n, 3] of pa_resize_pages carried out in one layer's pool: of every
+ * kv head the first `rows` rows of the old page go to the new one, the rows behind
+ * them stay as they were.  Entries with a new page of -1 or without rows are
+ * skipped, as is a page copied to itself; an id outside [0, num_pages) or more than
+ * page_size rows set PA_FLAG_BAD_PAGE and copy nothing.  No page may be the new one
+ * of two entries, or the new one of one and the old one of another.  Shape fields
+ * used: H_kv, num_pages, page_size, dtype (of the pool).  workspace: >= 256 bytes,
+ * zeroed once. */
+pa_status pa_copy_pages(const pa_shape* shape, void* key_pages, void* value_pages,
+                        const int32_t* copies, int n, void* workspace, size_t workspace_bytes,
+                        void* cuda_stream);
+
+/* pa_copy_pages of a 4-bit pool. */
+pa_status pa_copy_pages_q4(const pa_shape* shape, const pa_q4_pool* pool, const int32_t* copies,
+                           int n, void* workspace, size_t workspace_bytes, void* cuda_stream);
 
 const char* pa_status_str(pa_status status);
 

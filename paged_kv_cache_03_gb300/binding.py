@@ -39,6 +39,10 @@ PA_SCHED_PREFILL = 2
 PA_FLAG_BAD_PAGE = 0x1
 PA_FLAG_BAD_CONTEXT = 0x2
 PA_FLAG_TIMEOUT = 0x4
+PA_FLAG_BAD_TREE = 0x8
+PA_FLAG_NO_PAGES = 0x10
+
+TREE_MAX = 1024  # drafted slots of a sequence at most
 
 _lock = threading.Lock()
 _lib = None
@@ -141,6 +145,29 @@ def load(auto_build: bool = True):
         lib.pa_evict_kv.restype = ci
         lib.pa_evict_kv_q4.argtypes = [sp, qp] + evict
         lib.pa_evict_kv_q4.restype = ci
+        end = [vp, sz, vp]  # workspace, its bytes, stream
+        lib.pa_tree_mask.argtypes = [ci, ci, i32p, vp, i32p] + end
+        lib.pa_tree_mask.restype = ci
+        lib.pa_tree_workspace_bytes.argtypes = [sp]
+        lib.pa_tree_workspace_bytes.restype = sz
+        lib.pa_paged_attention_tree.argtypes = [sp, vp, vp, vp, i32p, i32p, vp, f32, vp] + end
+        lib.pa_paged_attention_tree.restype = ci
+        lib.pa_paged_attention_tree_q4.argtypes = [sp, vp, qp, i32p, i32p, vp, f32, vp] + end
+        lib.pa_paged_attention_tree_q4.restype = ci
+        lib.pa_compact_kv.argtypes = [sp, vp, vp, i32p, i32p, i32p, ci, i32p, i32p] + end
+        lib.pa_compact_kv.restype = ci
+        lib.pa_compact_kv_q4.argtypes = [sp, qp, i32p, i32p, i32p, ci, i32p, i32p] + end
+        lib.pa_compact_kv_q4.restype = ci
+        lib.pa_pages_workspace_bytes.argtypes = [sp]
+        lib.pa_pages_workspace_bytes.restype = sz
+        lib.pa_fork_pages.argtypes = [sp, i32p, i32p, i32p, i32p, i32p, i32p, ci] + end
+        lib.pa_fork_pages.restype = ci
+        lib.pa_resize_pages.argtypes = [sp, i32p, i32p, i32p, i32p, i32p] + end
+        lib.pa_resize_pages.restype = ci
+        lib.pa_copy_pages.argtypes = [sp, vp, vp, i32p, ci] + end
+        lib.pa_copy_pages.restype = ci
+        lib.pa_copy_pages_q4.argtypes = [sp, qp, i32p, ci] + end
+        lib.pa_copy_pages_q4.restype = ci
         lib.pa_status_str.argtypes = [ctypes.c_int]
         lib.pa_status_str.restype = ctypes.c_char_p
         _lib = lib
@@ -868,3 +895,335 @@ def evict_kv_q4(pool, block_table, context_lens, key_weights, keep, recent, dst_
     return _evict("pa_evict_kv_q4", (_lib or load()).pa_evict_kv_q4, (ctypes.byref(pool.c_pool),),
                   pool.dims, PA_BF16, pool.device, block_table, context_lens, key_weights, keep,
                   recent, dst_block_table, key_weights_out, workspace)
+
+
+# ---- trees of drafted tokens --------------------------------------------------
+def pa_tree_mask(B_, L, parents, mask, depths, workspace, workspace_bytes, stream=None) -> int:
+    return load().pa_tree_mask(int(B_), int(L), _ptr(parents), _ptr(mask), _ptr(depths),
+                               _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def pa_tree_workspace_bytes(shape) -> int:
+    return int(load().pa_tree_workspace_bytes(ctypes.byref(shape)))
+
+
+def pa_paged_attention_tree(shape, query, key_pages, value_pages, block_table, context_lens,
+                            tree_mask, scale, out, workspace, workspace_bytes, stream=None) -> int:
+    return load().pa_paged_attention_tree(
+        ctypes.byref(shape), _ptr(query), _ptr(key_pages), _ptr(value_pages), _ptr(block_table),
+        _ptr(context_lens), _ptr(tree_mask), float(scale), _ptr(out), _ptr(workspace),
+        int(workspace_bytes), _stream(stream))
+
+
+def pa_paged_attention_tree_q4(shape, query, pool, block_table, context_lens, tree_mask, scale,
+                               out, workspace, workspace_bytes, stream=None) -> int:
+    return load().pa_paged_attention_tree_q4(
+        ctypes.byref(shape), _ptr(query), _q4(pool), _ptr(block_table), _ptr(context_lens),
+        _ptr(tree_mask), float(scale), _ptr(out), _ptr(workspace), int(workspace_bytes),
+        _stream(stream))
+
+
+def pa_compact_kv(shape, key_pages, value_pages, block_table, context_lens, path, path_n,
+                  path_lens, context_lens_out, workspace, workspace_bytes, stream=None) -> int:
+    return load().pa_compact_kv(
+        ctypes.byref(shape), _ptr(key_pages), _ptr(value_pages), _ptr(block_table),
+        _ptr(context_lens), _ptr(path), int(path_n), _ptr(path_lens), _ptr(context_lens_out),
+        _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def pa_compact_kv_q4(shape, pool, block_table, context_lens, path, path_n, path_lens,
+                     context_lens_out, workspace, workspace_bytes, stream=None) -> int:
+    return load().pa_compact_kv_q4(
+        ctypes.byref(shape), _q4(pool), _ptr(block_table), _ptr(context_lens), _ptr(path),
+        int(path_n), _ptr(path_lens), _ptr(context_lens_out), _ptr(workspace),
+        int(workspace_bytes), _stream(stream))
+
+
+def pa_pages_workspace_bytes(shape) -> int:
+    return int(load().pa_pages_workspace_bytes(ctypes.byref(shape)))
+
+
+def pa_fork_pages(shape, block_table, context_lens, page_refs, sources, targets, lens, n,
+                  workspace, workspace_bytes, stream=None) -> int:
+    return load().pa_fork_pages(
+        ctypes.byref(shape), _ptr(block_table), _ptr(context_lens), _ptr(page_refs),
+        _ptr(sources), _ptr(targets), _ptr(lens), int(n), _ptr(workspace), int(workspace_bytes),
+        _stream(stream))
+
+
+def pa_resize_pages(shape, block_table, context_lens, page_refs, new_lens, copies, workspace,
+                    workspace_bytes, stream=None) -> int:
+    return load().pa_resize_pages(
+        ctypes.byref(shape), _ptr(block_table), _ptr(context_lens), _ptr(page_refs),
+        _ptr(new_lens), _ptr(copies), _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def pa_copy_pages(shape, key_pages, value_pages, copies, n, workspace, workspace_bytes,
+                  stream=None) -> int:
+    return load().pa_copy_pages(
+        ctypes.byref(shape), _ptr(key_pages), _ptr(value_pages), _ptr(copies), int(n),
+        _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def pa_copy_pages_q4(shape, pool, copies, n, workspace, workspace_bytes, stream=None) -> int:
+    return load().pa_copy_pages_q4(
+        ctypes.byref(shape), _q4(pool), _ptr(copies), int(n), _ptr(workspace),
+        int(workspace_bytes), _stream(stream))
+
+
+def _int32(name, t, shape):
+    if t.dtype is not (_torch or _load_torch()).int32 or t.shape != shape:
+        raise ValueError(f"{name} must be int32 {list(shape)}")
+
+
+@_streamed
+def tree_mask(parents, *, workspace=None):
+    """(mask, depths) of drafted trees: parents int32 [B, L], parents[b, i] < i
+    the draft that draft i follows, -1 for the last position before the
+    drafts, -2 for a slot without a draft.  mask int32 [B, L, (L + 31) // 32]
+    holds, as bits, the drafts that draft i sees (its ancestors and itself);
+    depths int32 [B, L] counts its ancestors (-1: no draft).  L <= 1024."""
+    torch = _torch or _load_torch()
+    if parents.dim() != 2 or parents.dtype is not torch.int32:
+        raise ValueError("parents must be int32 [B, L]")
+    index = parents.get_device()
+    if index < 0:
+        raise ValueError("parents must be on a CUDA device")
+    if workspace is None:
+        workspace = new_cache_workspace(parents.device)
+    _on_device(index, ("parents", parents), ("workspace", workspace))
+    B_, L = parents.shape
+    mask = torch.empty((B_, L, (L + 31) // 32), dtype=torch.int32, device=parents.device)
+    depths = torch.empty_like(parents)
+    _launch("pa_tree_mask", index, (_lib or load()).pa_tree_mask, B_, L, parents.data_ptr(),
+            mask.data_ptr(), depths.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return mask, depths
+
+
+def new_tree_workspace(query, pool, block_table):
+    """Workspace of paged_attention_tree (pool: the key pages) or
+    paged_attention_tree_q4 (pool: the Q4Pool) for tensors of these shapes and
+    for any with at most their B, L and table width."""
+    import torch
+    shape = _q4_shape(query, pool, block_table) if isinstance(pool, Q4Pool) else \
+        shape_of(query, pool, block_table)
+    with torch.cuda.device(query.device):
+        n = pa_tree_workspace_bytes(shape)
+    return _workspace(n, query.device, "pa_tree_workspace_bytes")
+
+
+def _attend_tree(name, fn, pools, shape, query, block_table, context_lens, tree_mask, page_size,
+                 scale, out, workspace):
+    if shape.page_size != page_size:
+        raise ValueError("page_size disagrees with the pool's")
+    _table(block_table, context_lens, shape.B)
+    _int32("tree_mask", tree_mask, (shape.B, shape.L, (shape.L + 31) // 32))
+    index = query.get_device()
+    if out is None:
+        out = (_torch or _load_torch()).empty_like(query)
+    elif out.shape != query.shape or out.dtype != query.dtype:
+        raise ValueError("out must be like query")
+    _on_device(index, ("query", query), ("block_table", block_table),
+               ("context_lens", context_lens), ("tree_mask", tree_mask), ("out", out),
+               ("workspace", workspace))
+    if scale is None:
+        scale = 1.0 / math.sqrt(shape.D)
+    _launch(name, index, fn, ctypes.byref(shape), query.data_ptr(), *pools,
+            block_table.data_ptr(), context_lens.data_ptr(), tree_mask.data_ptr(), scale,
+            out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+@_streamed
+def paged_attention_tree(query, key_pages, value_pages, block_table, context_lens, tree_mask,
+                         page_size, scale=None, *, out=None, workspace=None):
+    """Attention of L drafted tokens per sequence (query [B, H_q, L, 128], the
+    last L of context_lens, stored by append_kv): each sees every position
+    before the drafts and the drafts of its row of tree_mask (int32 [B, L,
+    (L + 31) // 32], from ``tree_mask`` or any other).  A slot whose row is 0
+    holds no draft: its output is 0 and nobody sees it."""
+    P, H_kv, ps = _pages_dims(key_pages, value_pages)
+    if query.dim() != 4 or query.dtype != key_pages.dtype or query.shape[3] != key_pages.shape[3]:
+        raise ValueError("query must be [B, H_q, L, D] of the pages' dtype and head dim")
+    B_, H_q, L, D = query.shape
+    shape = pa_shape(B_, H_q, H_kv, L, D, P, ps, block_table.shape[1], _dtype_id(query.dtype))
+    if query.get_device() != key_pages.get_device():
+        raise ValueError(f"query must be on {key_pages.device}")
+    if workspace is None:
+        workspace = new_tree_workspace(query, key_pages, block_table)
+    return _attend_tree("pa_paged_attention_tree", (_lib or load()).pa_paged_attention_tree,
+                        (key_pages.data_ptr(), value_pages.data_ptr()), shape, query, block_table,
+                        context_lens, tree_mask, page_size, scale, out, workspace)
+
+
+@_streamed
+def paged_attention_tree_q4(query, pool, block_table, context_lens, tree_mask, page_size,
+                            scale=None, *, out=None, workspace=None):
+    """paged_attention_tree over a 4-bit pool (query bf16 or fp32)."""
+    shape = _q4_shape(query, pool, block_table)
+    if query.get_device() != pool.device.index:
+        raise ValueError(f"query must be on {pool.device}")
+    if workspace is None:
+        workspace = new_tree_workspace(query, pool, block_table)
+    return _attend_tree("pa_paged_attention_tree_q4", (_lib or load()).pa_paged_attention_tree_q4,
+                        (ctypes.byref(pool.c_pool),), shape, query, block_table, context_lens,
+                        tree_mask, page_size, scale, out, workspace)
+
+
+def _compact(name, fn, pools, dims, dtype_id, device, block_table, context_lens, path, path_lens,
+             L, workspace):
+    torch = _torch or _load_torch()
+    P, H_kv, ps = dims
+    B_ = block_table.shape[0]
+    _table(block_table, context_lens, B_)
+    if path.dim() != 2 or path.shape[1] < 1:
+        raise ValueError("path must be int32 [B, n]")
+    _int32("path", path, (B_, path.shape[1]))
+    _int32("path_lens", path_lens, (B_,))
+    if workspace is None:
+        workspace = new_cache_workspace(device)
+    index = device.index
+    _on_device(index, ("block_table", block_table), ("context_lens", context_lens),
+               ("path", path), ("path_lens", path_lens), ("workspace", workspace))
+    shape = pa_shape(B_, H_kv, H_kv, L, 128, P, ps, block_table.shape[1], dtype_id)
+    lens = torch.empty_like(context_lens)
+    _launch(name, index, fn, ctypes.byref(shape), *pools, block_table.data_ptr(),
+            context_lens.data_ptr(), path.data_ptr(), path.shape[1], path_lens.data_ptr(),
+            lens.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return lens
+
+
+@_streamed
+def compact_kv(key_pages, value_pages, block_table, context_lens, path, path_lens, L, *,
+               workspace=None):
+    """Keeps, of the L drafts behind each context, path[b, :path_lens[b]]
+    (ascending; int32 [B, n] and [B]): their rows move in place right behind
+    the positions before the drafts.  Returns the new lengths [B]."""
+    dims = _pages_dims(key_pages, value_pages)
+    if key_pages.shape[3] != 128:
+        raise ValueError("head dim must be 128")
+    return _compact("pa_compact_kv", (_lib or load()).pa_compact_kv,
+                    (key_pages.data_ptr(), value_pages.data_ptr()), dims,
+                    _dtype_id(key_pages.dtype), key_pages.device, block_table, context_lens, path,
+                    path_lens, L, workspace)
+
+
+@_streamed
+def compact_kv_q4(pool, block_table, context_lens, path, path_lens, L, *, workspace=None):
+    """compact_kv of a 4-bit pool."""
+    return _compact("pa_compact_kv_q4", (_lib or load()).pa_compact_kv_q4,
+                    (ctypes.byref(pool.c_pool),), pool.dims, PA_BF16, pool.device, block_table,
+                    context_lens, path, path_lens, L, workspace)
+
+
+# ---- pages shared between sequences ---------------------------------------------
+def _pages_shape(block_table, page_refs, page_size):
+    return pa_shape(block_table.shape[0], 1, 1, 1, 128, page_refs.shape[0], page_size,
+                    block_table.shape[1], PA_BF16)
+
+
+def _page_state(block_table, context_lens, page_refs):
+    """The CUDA device index of a checked table, lengths and page counts."""
+    _table(block_table, context_lens, block_table.shape[0])
+    _int32("page_refs", page_refs, (page_refs.shape[0],))
+    index = block_table.get_device()
+    if index < 0:
+        raise ValueError("block_table must be on a CUDA device")
+    _on_device(index, ("block_table", block_table), ("context_lens", context_lens),
+               ("page_refs", page_refs))
+    return index
+
+
+def new_pages_workspace(block_table, page_refs):
+    """Workspace of resize_pages (and fork_pages, copy_pages) for tables of at
+    most these rows and pools of at most these pages."""
+    n = pa_pages_workspace_bytes(_pages_shape(block_table, page_refs, 1))
+    return _workspace(n, block_table.device, "pa_pages_workspace_bytes")
+
+
+@_streamed
+def fork_pages(block_table, context_lens, page_refs, sources, targets, page_size, lens=None, *,
+               workspace=None):
+    """Row targets[i] of block_table becomes a fork of row sources[i] (int32
+    [n]): the pages of its first lens[i] positions (None: all) are named twice
+    and counted in page_refs (int32 [num_pages], 0: free); nothing is copied.
+    Targets must be empty (length 0).  Table, lengths and counts change in
+    place."""
+    index = _page_state(block_table, context_lens, page_refs)
+    _int32("sources", sources, (sources.shape[0],))
+    _int32("targets", targets, (sources.shape[0],))
+    at = 0
+    if lens is not None:
+        _int32("lens", lens, (sources.shape[0],))
+        _on_device(index, ("lens", lens))
+        at = lens.data_ptr()
+    if workspace is None:
+        workspace = new_cache_workspace(block_table.device)
+    _on_device(index, ("sources", sources), ("targets", targets), ("workspace", workspace))
+    shape = _pages_shape(block_table, page_refs, page_size)
+    _launch("pa_fork_pages", index, (_lib or load()).pa_fork_pages, ctypes.byref(shape),
+            block_table.data_ptr(), context_lens.data_ptr(), page_refs.data_ptr(),
+            sources.data_ptr(), targets.data_ptr(), at, sources.shape[0], workspace.data_ptr(),
+            workspace.numel())
+    return workspace
+
+
+@_streamed
+def resize_pages(block_table, context_lens, page_refs, new_lens, page_size, *, copies=None,
+                 workspace=None):
+    """Gives every sequence the length new_lens[b] (int32 [B]; negative: left
+    alone, 0: freed), in place: pages past a new end go back, longer sequences
+    get the lowest free pages and, where others hold their partly filled last
+    page, one of their own for it.  Returns copies int32 [B, 3]: (old page, new
+    page, rows) for copy_pages, which every layer's pool needs before it is
+    written to, or (-1, -1, 0)."""
+    torch = _torch or _load_torch()
+    index = _page_state(block_table, context_lens, page_refs)
+    B_ = block_table.shape[0]
+    _int32("new_lens", new_lens, (B_,))
+    if copies is None:
+        copies = torch.empty((B_, 3), dtype=torch.int32, device=block_table.device)
+    else:
+        _int32("copies", copies, (B_, 3))
+    if workspace is None:
+        workspace = new_pages_workspace(block_table, page_refs)
+    _on_device(index, ("new_lens", new_lens), ("copies", copies), ("workspace", workspace))
+    shape = _pages_shape(block_table, page_refs, page_size)
+    _launch("pa_resize_pages", index, (_lib or load()).pa_resize_pages, ctypes.byref(shape),
+            block_table.data_ptr(), context_lens.data_ptr(), page_refs.data_ptr(),
+            new_lens.data_ptr(), copies.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return copies
+
+
+def _copy_pages(name, fn, pools, dims, dtype_id, device, copies, workspace):
+    P, H_kv, ps = dims
+    if copies.dim() != 2:
+        raise ValueError("copies must be int32 [n, 3]")
+    _int32("copies", copies, (copies.shape[0], 3))
+    if workspace is None:
+        workspace = new_cache_workspace(device)
+    _on_device(device.index, ("copies", copies), ("workspace", workspace))
+    shape = pa_shape(1, H_kv, H_kv, 1, 128, P, ps, 1, dtype_id)
+    _launch(name, device.index, fn, ctypes.byref(shape), *pools, copies.data_ptr(),
+            copies.shape[0], workspace.data_ptr(), workspace.numel())
+    return workspace
+
+
+@_streamed
+def copy_pages(key_pages, value_pages, copies, *, workspace=None):
+    """Carries out the copies (int32 [n, 3]: old page, new page, rows) of
+    resize_pages in one layer's pages, in place."""
+    dims = _pages_dims(key_pages, value_pages)
+    if key_pages.shape[3] != 128:
+        raise ValueError("head dim must be 128")
+    return _copy_pages("pa_copy_pages", (_lib or load()).pa_copy_pages,
+                       (key_pages.data_ptr(), value_pages.data_ptr()), dims,
+                       _dtype_id(key_pages.dtype), key_pages.device, copies, workspace)
+
+
+@_streamed
+def copy_pages_q4(pool, copies, *, workspace=None):
+    """copy_pages of a 4-bit pool."""
+    return _copy_pages("pa_copy_pages_q4", (_lib or load()).pa_copy_pages_q4,
+                       (ctypes.byref(pool.c_pool),), pool.dims, PA_BF16, pool.device, copies,
+                       workspace)
