@@ -481,8 +481,8 @@ pa_status pa_tree_mask(int B, int L, const int32_t* parents, uint32_t* mask, int
 
 /* pa_paged_attention for the shape->L drafts of every sequence: draft i sees all
  * context_lens[b] - L positions before the drafts and the drafts n whose bit is
- * set in tree_mask[b, i] (laid out as by pa_tree_mask, 4-byte aligned; any set of
- * drafts, in any order of the slots).  A slot whose own words are all 0 holds no
+ * set in tree_mask[b, i] (laid out as by pa_tree_mask, 4-byte aligned, bits behind L
+ * 0; any set of drafts, in any order of the slots).  A slot whose own words are all 0 holds no
  * draft: its output is 0, no draft sees it whatever its bits say, and its key and
  * value rows may hold anything.  bf16 or fp32 pages of the query's type, any page
  * size and group size.
@@ -503,7 +503,9 @@ pa_status pa_paged_attention_tree(const pa_shape* shape, const void* query, cons
                                   void* cuda_stream);
 size_t pa_tree_workspace_bytes(const pa_shape* shape);
 
-/* pa_paged_attention_tree over a 4-bit pool, bf16 or fp32 query and output. */
+/* pa_paged_attention_tree over a 4-bit pool, bf16 or fp32 query and output.  Rounded
+ * on the way: with bf16 queries each probability to f16 (2^-11; up to 2^-25 of a row's
+ * heaviest key may be lost of every other); nothing else. */
 pa_status pa_paged_attention_tree_q4(const pa_shape* shape, const void* query,
                                      const pa_q4_pool* pool, const int32_t* block_table,
                                      const int32_t* context_lens, const uint32_t* tree_mask,

@@ -12,8 +12,6 @@
 // during the scores.  Bound by the FMA pipe and shared memory (TR = 8: 16 FMAs for each
 // 16-byte load of a key).
 #include <algorithm>
-#include <climits>
-
 #include "tree.h"
 #include "ptx.cuh"
 #include "q4.cuh"
@@ -393,14 +391,9 @@ pa_status launch_tr(const RowsParams& p, const RowsPlan& t, const TreeCall& c) {
 
 }  // namespace
 
-bool tree_supported(const pa_shape& sh) {
-    const long long rows = static_cast<long long>(sh.B) * sh.H_q * sh.L;
-    return sh.L <= kTreeMax && rows < INT_MAX;  // (a CTA per 8 rows or fewer)
-}
+size_t tree_rows_workspace_bytes(const pa_shape& sh, int sm_count) { return plan(sh, sm_count).total; }
 
-size_t tree_workspace_bytes(const pa_shape& sh, int sm_count) { return plan(sh, sm_count).total; }
-
-pa_status tree_launch(const TreeCall& c) {
+pa_status tree_rows_launch(const TreeCall& c) {
     const pa_shape& sh = c.sh;
     const RowsPlan t = plan(sh, c.dev.sm_count);
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);

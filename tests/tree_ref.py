@@ -145,17 +145,21 @@ def attend(inp: Inputs, skip=()):
       additions each off by at most 2^-23 T (the tensor cores cut) make 2^-16 T;
       with the scaling and the exponential's own 2^-21 at most 2^-15 T + 2^-20
       relative in every p (T of the row's largest score, both in p and the sum);
-    * p of bf16 queries is rounded to bf16: 2^-8, and as much again where the row
-      sum adds the rounded ones;
+    * p of bf16 queries is rounded to bf16 over bf16 pages: 2^-8, and as much again
+      as the row sum adds the rounded ones; over 4-bit pages to f16: 2^-11 from
+      2^-14 on, below that its steps are 2^-24, so up to 2^-25 is lost of a p whose
+      row's largest is 1 or more (the maximum that p is taken against is one that
+      some key of the row has reached);
     * sums of S terms in fp32: 2^-24 S at worst;
     * a p below 2^-126 of the row's largest is 0 in fp32 (the smallest normal
-      number): at most 2^-126 of every value is lost.
+      number): at most 2^-126 of every value is lost (times the row's largest p).
     """
     c = inp.c
     out = np.zeros(inp.q.shape)
     tol = np.full(inp.q.shape, 1e-300)
     eps = 2.0 ** -8 if c.dtype == "bf16" else 2.0 ** -24
-    pop = 2 * 2.0 ** -8 if c.dtype == "bf16" else 0.0
+    pop = 0.0 if c.dtype == "f32" else 2.0 ** -11 if c.pool == "q4" else 2 * 2.0 ** -8
+    lost = 2.0 ** -25 if c.dtype == "bf16" and c.pool == "q4" else 2.0 ** -126
     for b, S in enumerate(inp.ctx):
         if b in skip:
             continue
@@ -179,7 +183,7 @@ def attend(inp: Inputs, skip=()):
             o = p @ v
             out[b, h, there] = o
             tol[b, h, there] = (rel + pop) * (p @ np.abs(v)) + eps * np.abs(o) + \
-                2.0 ** -126 * np.abs(v).sum(0)
+                lost * p.max(-1, keepdims=True) * np.abs(v).sum(0)
     return out, tol
 
 
