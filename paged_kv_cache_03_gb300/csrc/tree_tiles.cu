@@ -5,26 +5,28 @@
 // consecutive rows of the query, cut into tiles of 128.  All of them see every position
 // before the drafts, so a key tile of 128 needs no mask unless it holds drafts or lies at
 // the end ("tail"); there a row's 128 bits come out of its words of the tree's mask.
-//   S = Q K^T,  P = 2^(scale S - m),  O += P V,  with the running maximum m and sum l
-// per row; O / l at the end.  bf16 pages: P rounded to bf16, l adds the rounded ones.
-// 4-bit pages: K and V dequantised to f16 on chip (exact), Q scaled by a power of two
-// into f16's range (exact), P rounded to f16 (2^-11).
+//   S = Q K^T,  P = 2^(scale S - m),  O += P V,  with a maximum m and the sum l per row;
+//   O / l at the end.
+// bf16 pages: P rounded to bf16, l adds the rounded ones.  4-bit pages: K and V dequantised
+// to f16 on chip (exact), Q scaled by a power of two into f16's range (exact), P rounded to
+// f16 (2^-11).
 //
-// Layout on GB300: one CTA per SM, four warpgroups.
-//   * A segment is a pair of query tiles (or a lone one) of one (sequence, kv head) over
-//     all its key tiles.  The key tiles of all segments are cut into equal shares, one per
-//     CTA, so ragged contexts leave no SM idle; a segment that crosses shares leaves fp32
-//     partial states that tree_merge_kernel joins.
-//   * A job is one key tile for one query tile; job i uses S, P and O of slot t = i & 1.
-//     A pair takes jobs (A, key tile 0), (B, 0), (A, 1), ...; a lone tile takes its key
-//     tiles in turn in both slots, each with its own m, l and O, which A joins at the end.
-//     So both softmax warpgroups work in either case, one on each slot, and the MMA warp
-//     issues P V of job i, then Q K^T of job i + 2.
-//   * Warps 0-3 bring K and V into two-slot rings in the 128-byte swizzle that the MMA
-//     reads: one lane per page box by TMA (bf16, pages of a multiple of 8 slots), 16-byte
+// Layout on GB300: one CTA per SM.
+//   * A segment is one query tile of one (sequence, kv head) over all its key tiles, or, over
+//     bf16 pages by TMA, C query tiles on the C CTAs of a cluster: each CTA loads 1 / C of
+//     every key tile and multicasts it to all, so K and V cross from HBM once for C tiles.
+//   * The key tiles of all segments are cut into equal shares, one per CTA (cluster), so
+//     ragged contexts leave no SM idle; a segment that crosses shares leaves fp32 partial
+//     states that tree_merge_kernel joins.
+//   * The key tiles of a piece go in turn to two slots t = 0, 1, each with its own S and P
+//     (P over S), O, m and l in Tensor Memory and one softmax warpgroup, one row per thread;
+//     both join them at the piece's end.  The MMA warp issues P V of tile i, then
+//     Q K^T of tile i + 2, so one slot's softmax overlaps the other's products.
+//   * The producer warps bring K and V into rings in the 128-byte swizzle that the MMA reads:
+//     one lane per page box by TMA (bf16, pages of a multiple of 8 slots), 16-byte
 //     asynchronous copies (other page sizes), or 4-bit rows dequantised on the way.
-//   * Warp 7 publishes the pieces of segments in a ring of four slots, with the bits of
-//     the slots that hold drafts, and loads the query tiles by TMA.
+//   * One warp publishes the pieces of segments in a ring, with the bits of the slots that
+//     hold drafts, and another loads the query tiles by TMA.
 //   * Value rows that nobody sees (behind the context, slots without a draft) may hold
 //     NaN, and 0 * NaN is NaN: copies leave zeros there, and behind TMA warp 1 zeroes them
 //     before the tile is announced.
@@ -33,10 +35,12 @@
 #include <algorithm>
 #include <cfloat>
 #include <climits>
+#include <mutex>
 
-#include "ptx.cuh"
+#include <cudaTypedefs.h>
+
+#include "cluster.cuh"
 #include "stage.cuh"
-#include "tc.cuh"
 #include "tree.h"
 
 namespace pa {
@@ -44,45 +48,74 @@ namespace {
 
 constexpr int kD = kHeadDim;
 constexpr int BM = 128, BN = 128;  // query rows and keys of a tile
-constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;  // S of slot t at 128 t, O at 256 + 128 t
-constexpr float kLazyRescaleLog2 = 8.0f;
 // What a segment's query load, first softmax and epilogue cost, in key tiles: the
 // shares count it, or CTAs with many short segments would finish last.
 constexpr int kSegCost = 3;
 constexpr int kMinPer = 8;  // least cost of a share
-constexpr int kHalf = kStageHalf;  // 128 rows x 64 values (one swizzled column block)
-constexpr int kTile = 2 * kHalf;
-constexpr int kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffBar = 6 * kTile;
+constexpr int kTile = BN * kD * 2;
 enum Bar {
-    kQFull = 0,     // + buffer: the query tiles are there (4 bit: as they are)
+    kQFull = 0,     // + buffer: the query tile is there (4 bit: as it is)
     kQReady = 2,    // + buffer: ... in f16 (4 bit)
-    kQEmpty = 4,    // every Q K^T of a piece is done
-    kKFull = 5,     // + slot
-    kKEmpty = 7,    // + slot
-    kVFull = 9,     // + slot
-    kVEmpty = 11,   // + slot
-    kVTail = 13,    // + slot: a tail tile's values are there, not yet cleaned
-    kSFull = 15,    // + t
-    kPFull = 17,    // + t
-    kODone = 19,    // + t
-    kOFree = 21,    // + t: the epilogue has read O
-    kXFull = 23,    // + slot: B's max and sum (lone tile)
-    kItemFull = 25,   // + slot
-    kItemEmpty = 29,  // + slot
-    kMmaDone = 33,
-    kNumBars = 34
+    kQEmpty = 4,    // + buffer: every Q K^T of its piece is done
+    kKFull = 6,     // + slot
+    kKEmpty = 9,    // + slot: in every CTA of the cluster
+    kVFull = 12,    // + slot
+    kVEmpty = 15,   // + slot
+    kVTail = 18,    // + slot: a tail tile's values are there, not yet cleaned
+    kSFull = 21,    // + t
+    kPFull = 23,    // + t
+    kODone = 25,    // + t
+    kOFree = 27,    // + t: the epilogue has read O
+    kXFull = 29,    // both slots' maxima and sums are there
+    kXFree = 30,    // ... and read
+    kMmaDone = 31,
+    kItemFull = 32    // + place, then kItemEmpty + place
 };
-constexpr int kItemBytes = 256;
-constexpr int kOffItems = kOffBar + kNumBars * 8;
-constexpr int kOffTmemSlot = kOffItems + 4 * kItemBytes;
-constexpr int kOffAbort = kOffTmemSlot + 8;
-constexpr int kOffX = kOffAbort + 8;             // [2][128] max and sum of B's rows
-constexpr int kOffQScale = kOffX + 2 * BM * 8;   // 4 bit: [2][128] the inverse of a row's scale
-constexpr int kOffRaw = kOffQScale + 2 * BM * 4; // 4 bit: [warp][K, V] rows on their way
-static_assert(kOffItems % 16 == 0 && kOffRaw % 16 == 0, "16-byte copies");
 enum Source { kTma, kCopy, kQ4 };
-constexpr int smem_bytes(Source s) { return (s == kQ4 ? kOffRaw + 4 * 2 * kRawStage : kOffQScale) + 1024; }
+// Warps: K/V producers (4 bit: four for K, four for V), then four of MMA and pieces, then
+// eight of softmax.
+constexpr int producers(Source s) { return s == kQ4 ? 8 : 4; }
+constexpr int threads(Source s) { return 32 * (producers(s) + 4 + 8); }
+// K and V tiles in the rings.  Three: with C = 2 a tile's time is below the latency of HBM.
+// 4-bit rows wait as they are, kRawStages tiles of them, and need the space for that.
+constexpr int slots(Source s) { return s == kQ4 ? 2 : 3; }
+constexpr int kRawStages = 3;
+// Published pieces: enough for producers that are that many tiles ahead, were each tile a
+// piece.
+constexpr int items(Source s) { return s == kQ4 ? 8 : 4; }
+
+// Shared memory from a 1024-byte boundary (the attribute of smem_raw) on.  Q: one tile, or
+// two of at most 64 rows that the pieces take in turn.
+struct Smem {
+    int k, v, raw, bar, items, tmem, abort, x, q_scale, total;
+};
+constexpr int kItemBytes = 168;
+constexpr Smem smem(Source s) {
+    Smem m{};
+    int at = kTile;
+    m.k = at;
+    at += slots(s) * kTile;
+    m.v = at;
+    at += slots(s) * kTile;
+    m.raw = at;  // [producer warp][stage]
+    if (s == kQ4) at += 8 * kRawStages * kRawStage;
+    m.bar = at;
+    at += (kItemFull + 2 * items(s)) * 8;
+    m.items = at;
+    at += items(s) * kItemBytes;
+    m.tmem = at;
+    m.abort = at + 8;
+    at += 16;
+    m.x = at;  // [2][128] maximum and sum; before that the share and the scan's sums
+    at += 2 * BM * 8;
+    m.q_scale = at;  // 4 bit: [2][128] the inverse of a row's scale
+    if (s == kQ4) at += 2 * BM * 4;
+    m.total = at;
+    return m;
+}
+static_assert(smem(kTma).total <= 232448 && smem(kQ4).total <= 232448, "227 KB");
+static_assert(smem(kQ4).raw % 16 == 0 && smem(kTma).bar % 8 == 0 && smem(kTma).x % 8 == 0, "alignment");
 
 struct TileParams {
     const uint8_t *kc, *ks, *vc, *vs;  // codes or bf16 rows, scales
@@ -91,11 +124,12 @@ struct TileParams {
     const uint32_t* mask;
     uint16_t* out;
     uint32_t* flag;
-    float2* part_ml;  // [2 per CTA][tile][128]: max, sum
-    float* part_o;    // [2 per CTA][tile][128][D]
-    int4* split;      // per CTA: the segment that starts in its share and ends in a later one
-    int B, H_kv, R, L, W, nM, nPairs, num_pages, ps, max_npg;
-    int pool_rows, box, q_box;  // rows of the pool, of a K/V box, of a query box
+    float2* part_ml;  // [2 per CTA][128]: max, sum
+    float* part_o;    // [2 per CTA][128][D]
+    int4* split;      // per share: the segment that starts in it and ends in a later one
+    int B, H_kv, R, L, W, nG, num_pages, ps, max_npg;  // nG: groups of C query tiles
+    int pool_rows, box;          // rows of the pool, of a K/V box
+    int q_box, q_half, q_bufs;   // rows of a query box, bytes of 64 dims of them, buffers
     long long max_S;
     float scale_log2;
     int out32;  // the output is 32-byte aligned
@@ -110,18 +144,30 @@ __device__ __forceinline__ int seq_len(const TileParams& p, int b) {
 }
 __device__ __forceinline__ int key_tiles(int S) { return (S + BN - 1) / BN; }
 __device__ __forceinline__ int seq_cost(const TileParams& p, int S) {
-    return S == 0 ? 0 : p.H_kv * p.nPairs * (kSegCost + key_tiles(S));
+    return S == 0 ? 0 : p.H_kv * p.nG * (kSegCost + key_tiles(S));
 }
 
-// A published piece: key tiles j0 .. j0 + n - 1 of its ng, for nt query tiles.  Slot k & 3
-// holds piece k from kItemFull to kItemEmpty.
+// A published piece: key tiles j0 .. j0 + n - 1 of its ng.  Place k % items holds piece k
+// from kItemFull to kItemEmpty.
 struct Item {
-    int b, S, kvh, mp, ng, j0, n, nt;  // n = 0: no more
-    int jobs[2];    // jobs of slot t
-    int before[2];  // ... in earlier pieces
+    int b, S, kvh, mp, ng, j0, n;  // n = 0: no more
+    int before[2];      // tiles of slot t in earlier pieces
     uint32_t live[32];  // slots that hold a draft (pieces with tail tiles)
 };
-static_assert(sizeof(Item) <= kItemBytes, "item slot");
+static_assert(sizeof(Item) <= kItemBytes && kItemBytes % 8 == 0, "item slot");
+
+// A place in a ring of N and how often it has come round.
+template <int N>
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0u;
+    __device__ __forceinline__ void next() {
+        if (++s == N) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -145,57 +191,65 @@ __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// MULTI: more than one query tile per (sequence, kv head).  Without it the two query
-// buffers take the pieces in turn.
-template <Source SRC, bool MULTI>
-__global__ void __launch_bounds__(kThreads, 1)
+template <Source SRC, int C>
+__global__ void __launch_bounds__(threads(SRC), 1)
     tree_tile_kernel(const TileParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
+    static_assert(C == 1 || SRC == kTma, "only TMA multicasts");
     constexpr bool Q4 = SRC == kQ4;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ int share[4];  // all units, units per share, first sequence, its first unit
-    __shared__ int sums[kThreads / 32];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t* const sbase = smem_raw + (base - raw);
-    const uint32_t bar0 = base + kOffBar;
-    auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
-    volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + kOffAbort);
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sbase + kOffTmemSlot);
+    constexpr int kThreads = threads(SRC), kProd = producers(SRC), N = slots(SRC), I = items(SRC);
+    constexpr int kItemEmpty = kItemFull + I;
+    constexpr Smem M = smem(SRC);
+    // Tiles behind TMA: [8 rows][64-dim half][row][128 bytes], as boxes of rows come; else
+    // [half][128 rows][128 bytes].
+    constexpr uint32_t kHalf = SRC == kTma ? 1024u : kStageHalf, kGroup = SRC == kTma ? 2048u : 1024u;
+    constexpr uint16_t kAll = (1u << C) - 1u;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = smem_u32(smem_raw);
+    auto bar = [&](int i) { return base + M.bar + 8u * static_cast<uint32_t>(i); };
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem_raw + M.abort);
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + M.tmem);
+    // all units, units per share, first sequence, its first unit; [4 ..): sums of a scan
+    int* const share = reinterpret_cast<int*>(smem_raw + M.x);
+    int* const sums = share + 4;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = C == 1 ? 0 : static_cast<int>(cluster_rank());
+    const int my_share = static_cast<int>(blockIdx.x) / C, shares = static_cast<int>(gridDim.x) / C;
     pdl_launch_dependents();
 
     // ---- set-up ----------------------------------------------------------------
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar(kQFull + s), 1);
-            mbar_init(bar(kQReady + s), MULTI ? 8 : 4);
-            mbar_init(bar(kKFull + s), SRC == kTma ? 1 : 4);
-            mbar_init(bar(kKEmpty + s), 1);
-            mbar_init(bar(kVFull + s), SRC == kTma ? 1 : 4);
-            mbar_init(bar(kVEmpty + s), 1);
-            mbar_init(bar(kVTail + s), 1);
+            mbar_init(bar(kQReady + s), 4);
+            mbar_init(bar(kQEmpty + s), 1);
             mbar_init(bar(kSFull + s), 1);
             mbar_init(bar(kPFull + s), 4);
             mbar_init(bar(kODone + s), 1);
-            mbar_init(bar(kOFree + s), 4);
-            mbar_init(bar(kXFull + s), 4);
+            mbar_init(bar(kOFree + s), 8);
+            mbar_init(bar(kXFull + s), 8);  // (and kXFree)
         }
-        mbar_init(bar(kQEmpty), 1);
+        for (int s = 0; s < N; ++s) {
+            mbar_init(bar(kKFull + s), SRC == kTma ? 1 : 4);
+            mbar_init(bar(kKEmpty + s), C);
+            mbar_init(bar(kVFull + s), SRC == kTma ? 1 : 4);
+            mbar_init(bar(kVEmpty + s), C);
+            mbar_init(bar(kVTail + s), 1);
+        }
         mbar_init(bar(kMmaDone), 1);
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < I; ++s) {
             mbar_init(bar(kItemFull + s), 1);
-            // K/V warps, the MMA thread, softmax warps
-            mbar_init(bar(kItemEmpty + s), (SRC == kTma ? 2 : 4) + 1 + 8);
+            // K/V warps, the MMA thread, the query warp, softmax warps
+            mbar_init(bar(kItemEmpty + s), (SRC == kTma ? 2 : kProd) + 2 + 8);
         }
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 4) {
-        tc::tmem_alloc(base + kOffTmemSlot, kTmemCols);
+    if (warp == kProd) {
+        tc::tmem_alloc(base + M.tmem, kTmemCols);
         tc::tmem_relinquish();
     }
-    // ---- this CTA's share --------------------------------------------------------
+    // ---- this share ----------------------------------------------------------------
     {
         int mine = 0, v = 0;
         for (int b = tid; b < p.B; b += kThreads) {
@@ -208,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         int total = 0;
         for (int w = 0; w < kThreads / 32; ++w) total += sums[w];
-        const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinPer);
-        const int u = static_cast<int>(blockIdx.x) * per;
+        const int per = max((total + shares - 1) / shares, kMinPer);
+        const int u = my_share * per;
         if (tid == 0) {
             share[0] = total;
             share[1] = per;
@@ -247,28 +301,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc::fence_before_sync();
     __syncthreads();
+    if constexpr (C > 1) cluster_sync();  // no peer's copy or commit before the barriers stand
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    auto slot = [&](int k) { return reinterpret_cast<volatile Item*>(sbase + kOffItems + kItemBytes * (k & 3)); };
-    auto take = [&](int k) { return warp_wait(bar(kItemFull + (k & 3)), (k >> 2) & 1); };  // a whole warp
+    const int total = share[0], per = share[1], first_b = share[2], first_unit = share[3];
+    __syncthreads();  // (the states lie there)
+    auto slot = [&](int k) { return reinterpret_cast<volatile Item*>(smem_raw + M.items + kItemBytes * (k % I)); };
+    auto take = [&](int k) { return warp_wait(bar(kItemFull + k % I), (k / I) & 1); };  // a whole warp
     auto release = [&](int k) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kItemEmpty + (k & 3)));
+        if (lane == 0) mbar_arrive(bar(kItemEmpty + k % I));
     };
     // key tiles of a piece from this one on hold drafts or the context's end
     auto first_tail = [&](int S) { return (S - p.L) / BN; };
+    // query buffer of a piece, and how often it has come round
+    auto q_buf = [&](int k) { return p.q_bufs == 2 ? k & 1 : 0; };
+    auto q_use = [&](int k) { return p.q_bufs == 2 ? k >> 1 : k; };
 
-    if (warp < 4) {
+    if (warp < kProd) {
         // ========================= K/V producers ==================================
         reg_dec<72>();
         bool ok = true;
         if constexpr (SRC == kTma) {
             if (warp == 0) {
-                const uint64_t policy = p.nPairs == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
+                const uint64_t policy = p.nG == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
                 const int nbox = BN / p.box;
                 bool bad_page = false;
-                int g = 0;  // tiles so far
-                for (int k = 0;; ++k) {
+                Ring<N> g;
+                int tiles = 0;
+                for (int k = 0; ok; ++k) {
                     ok = take(k);
                     if (!ok) break;
                     const int n = slot(k)->n, j0 = slot(k)->j0, b = slot(k)->b, S = slot(k)->S, kvh = slot(k)->kvh;
@@ -276,74 +337,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (n == 0) break;
                     const int32_t* const table = p.bt + static_cast<long long>(b) * p.max_npg;
                     const int tail = first_tail(S);
-                    // lane i brings box i of a tile; its page id is requested a tile ahead
+                    // lane i brings box i of a tile (every C-th from its rank on); its page id
+                    // is requested a tile ahead
                     auto page_of = [&](int j) {
                         const int key = j * BN + lane * p.box;
                         return lane < nbox && key < S ? __ldg(table + key / p.ps) : 0;
                     };
                     int page = page_of(j0);
-                    for (int j = j0; j < j0 + n; ++j, ++g) {
-                        const int s = g & 1, key = j * BN + lane * p.box;
-                        const bool mine = lane < nbox && key < S;
+                    for (int j = j0; j < j0 + n; ++j, g.next(), ++tiles) {
+                        const int key = j * BN + lane * p.box;
+                        const bool there = lane < nbox && key < S, mine = there && lane % C == rank;
                         const bool good = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
-                        bad_page |= mine && !good;
-                        // (a row behind the pool reads as zeros)
-                        const int row = good ? (page * p.H_kv + kvh) * p.ps + key % p.ps : p.pool_rows;
+                        bad_page |= there && !good;
+                        // (groups of 8 rows; those behind the pool read as zeros)
+                        const int row = (good ? (page * p.H_kv + kvh) * p.ps + key % p.ps : p.pool_rows) >> 3;
                         const uint32_t bytes = static_cast<uint32_t>(min(nbox, (S - j * BN + p.box - 1) / p.box)) * p.box * 256u;
                         if (j + 1 < j0 + n) page = page_of(j + 1);
-                        if (g >= 2 && !warp_wait(bar(kKEmpty + s), ((g >> 1) - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        if (aborted(abort_flag)) break;
-                        if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + s), bytes);
-                        __syncwarp();
-                        if (mine) {
-                            const uint32_t dst = base + kOffK + s * kTile + lane * p.box * 128;
-                            tc::tma_load_2d(dst, &kmap, 0, row, bar(kKFull + s), policy);
-                            tc::tma_load_2d(dst + kHalf, &kmap, 64, row, bar(kKFull + s), policy);
-                        }
-                        if (g >= 2 && !warp_wait(bar(kVEmpty + s), ((g >> 1) - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        if (aborted(abort_flag)) break;
-                        const uint32_t vbar = bar((j >= tail ? kVTail : kVFull) + s);
-                        if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
-                        __syncwarp();
-                        if (mine) {
-                            const uint32_t dst = base + kOffV + s * kTile + lane * p.box * 128;
-                            tc::tma_load_2d(dst, &vmap, 0, row, vbar, policy);
-                            tc::tma_load_2d(dst + kHalf, &vmap, 64, row, vbar, policy);
-                        }
+                        auto load = [&](int empty, int full, uint32_t ring, const CUtensorMap* map) {
+                            if (!warp_wait(bar(empty + g.s), g.phase ^ 1u) || aborted(abort_flag)) return false;
+                            if (lane == 0) mbar_arrive_expect_tx(bar(full + g.s), bytes);
+                            __syncwarp();
+                            if (mine) {
+                                const uint32_t dst = base + ring + g.s * kTile + lane * p.box * 256;
+                                if constexpr (C == 1)
+                                    tc::tma_load_4d(dst, map, 0, 0, 0, row, bar(full + g.s), policy);
+                                else
+                                    tc::tma_load_4d_multicast(dst, map, 0, 0, 0, row, bar(full + g.s), kAll, policy);
+                            }
+                            return true;
+                        };
+                        ok = load(kKEmpty, kKFull, M.k, &kmap) && load(kVEmpty, j >= tail ? kVTail : kVFull, M.v, &vmap);
+                        if (!ok) break;
                     }
-                    if (!ok || aborted(abort_flag)) break;
                 }
-                // no copy may land after the CTA's shared memory is gone: the last tiles'
-                for (int s = 0; s < 2; ++s)
-                    if (g > s) {
-                        const int u = (g - 1 - s) & 1, x = (g - 1 - s) >> 1;  // tile g - 1 - s, use x of its slot
-                        if (!warp_wait(bar(kKFull + u), x & 1) || !warp_wait(bar(kVFull + u), x & 1)) ok = false;
+                // Without an error every copy has been waited for by the MMA thread.  With one,
+                // give those in flight time to land before the shared memory goes.
+                if (!ok)
+                    for (int s = 0; s < N; ++s) {
+                        mbar_wait_for(bar(kKFull + s), g.phase ^ (s >= g.s), 50000000ull);
+                        mbar_wait_for(bar(kVFull + s), g.phase ^ (s >= g.s), 50000000ull);
                     }
                 if (__any_sync(0xffffffffu, bad_page) && lane == 0) atomicOr(p.flag, PA_FLAG_BAD_PAGE);
             } else if (warp == 1) {
                 // value rows of tail tiles that nobody sees
-                int g = 0, tails[2] = {0, 0};
-                for (int k = 0;; ++k) {
+                Ring<N> g;
+                uint32_t phases = 0u;  // of the slots' tail barriers
+                for (int k = 0; ok; ++k) {
                     ok = take(k);
                     if (!ok) break;
                     const int n = slot(k)->n, j0 = slot(k)->j0, S = slot(k)->S, first = S - p.L, tail = first_tail(S);
-                    for (int j = max(j0, tail); j < j0 + n && ok; ++j) {
-                        const int s = (g + j - j0) & 1;
-                        ok = warp_wait(bar(kVTail + s), (s ? tails[1] : tails[0]) & 1);
+                    for (int j = j0; j < j0 + n; ++j, g.next()) {
+                        if (j < tail) continue;
+                        ok = warp_wait(bar(kVTail + g.s), phases >> g.s & 1u);
                         if (!ok) break;
-                        if (s) ++tails[1];
-                        else ++tails[0];
+                        phases ^= 1u << g.s;
 #pragma unroll 1
                         for (int r = lane; r < BN; r += 32) {
                             const int x = j * BN + r - first;  // draft
                             if (x < 0 || (x < p.L && (slot(k)->live[x >> 5] >> (x & 31) & 1u))) continue;
-                            const uint32_t at = base + kOffV + s * kTile + r * 128;
+                            const uint32_t at = base + M.v + g.s * kTile + (r >> 3) * kGroup + (r & 7) * 128;
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 sts128(at + 16 * c, 0u, 0u, 0u, 0u);
@@ -352,21 +404,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(kVFull + s));
+                        if (lane == 0) mbar_arrive(bar(kVFull + g.s));
                     }
-                    g += n;
                     release(k);
                     if (!ok || n == 0 || aborted(abort_flag)) break;
                 }
             }
         } else {
-            // pool rows of the next tile, lane 8 i + r: key 32 i + 8 warp + r; -1 where
+            // pool rows of the next tile, lane 8 i + r: key 32 i + 8 (warp & 3) + r; -1 where
             // nobody sees the key
             int page = 0, in_page = -1, row_base = 0;
             bool bad_page = false;
             auto lookup = [&](int k, int j) {
                 const volatile Item* const it = slot(k);
-                const int key = j * BN + 32 * (lane >> 3) + 8 * warp + (lane & 7), lp = key / p.ps;
+                const int key = j * BN + 32 * (lane >> 3) + 8 * (warp & 3) + (lane & 7), lp = key / p.ps;
                 const int S = it->S, x = key - (S - p.L);
                 const bool seen = key < S && (x < 0 || (it->live[x >> 5] >> (x & 31) & 1u));
                 in_page = seen ? key - lp * p.ps : -1;
@@ -383,14 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(x));
             };
-            int k = 0, g = 0, j = 0, last = 0, rows = -1;
+            int k = 0, j = 0, last = -1;
             ok = take(0);
             bool more = ok && slot(0)->n > 0;
             if (more) {
                 j = slot(0)->j0;
                 last = j + slot(0)->n - 1;
                 lookup(0, j);
-                rows = rows_of();
             }
             // the tile after tile j of piece k: its page ids are requested now
             auto next = [&]() {
@@ -400,186 +450,203 @@ __global__ void __launch_bounds__(kThreads, 1)
                     release(k);
                     ++k;
                     ok = take(k);
-                    if (!ok) return;
+                    if (!ok) {
+                        more = false;
+                        return;
+                    }
                     more = slot(k)->n > 0;
                     j = slot(k)->j0;
                     last = j + slot(k)->n - 1;
                 }
                 if (more) lookup(k, j);
             };
+            Ring<N> g;
             if constexpr (Q4) {
-                // A tile's 4-bit rows are copied to the warp's staging a tile ahead, K when K
-                // of the tile before is stored, V likewise, one group of copies each.
-                const uint32_t raw_k = base + kOffRaw + warp * 2 * kRawStage, raw_v = raw_k + kRawStage;
+                // Warps 0-3 dequantise K, 4-7 V.  A tile's 4-bit rows are copied to the warp's
+                // staging kRawStages tiles ahead.
+                const bool is_v = warp >= 4;
+                const uint32_t stages = base + M.raw + warp * kRawStages * kRawStage, ring = base + (is_v ? M.v : M.k);
+                const uint8_t *const codes = is_v ? p.vc : p.kc, *const scales = is_v ? p.vs : p.ks;
+                const int full = is_v ? kVFull : kKFull, empty = is_v ? kVEmpty : kKEmpty;
                 RawTile t;
-                if (more) {
-                    RawTile::copy(raw_k, p.kc, p.ks, rows, lane);
-                    cp_async_commit();
-                    RawTile::copy(raw_v, p.vc, p.vs, rows, lane);
-                    cp_async_commit();
-                }
-                while (more) {
-                    next();
-                    if (!ok) break;
-                    const int s = g & 1;
-                    cp_async_wait<1>();
-                    __syncwarp();
-                    t.read(raw_k, lane);
-                    if (g >= 2 && !warp_wait(bar(kKEmpty + s), ((g >> 1) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    t.store<false>(base + kOffK + s * kTile, warp, lane);
-                    announce(kKFull + s);
+                Ring<kRawStages> r;
+                int ahead = 0;  // tiles on their way
+                auto request = [&](int stage) {  // ... the next one (an empty group past the last)
                     if (more) {
-                        rows = rows_of();
-                        RawTile::copy(raw_k, p.kc, p.ks, rows, lane);
+                        const int rows = rows_of();
+                        RawTile::copy(stages + stage * kRawStage, codes, scales, rows, lane);
+                        ++ahead;
+                        next();
                     }
                     cp_async_commit();
-                    cp_async_wait<1>();
+                };
+                for (int i = 0; i < kRawStages; ++i) request(i);
+                while (ok && ahead > 0) {
+                    cp_async_wait<kRawStages - 1>();
                     __syncwarp();
-                    t.read(raw_v, lane);
-                    if (g >= 2 && !warp_wait(bar(kVEmpty + s), ((g >> 1) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (aborted(abort_flag)) break;
-                    t.store<false>(base + kOffV + s * kTile, warp, lane);
-                    announce(kVFull + s);
-                    ++g;
-                    if (more) RawTile::copy(raw_v, p.vc, p.vs, rows, lane);
-                    cp_async_commit();
+                    t.read(stages + r.s * kRawStage, lane);
+                    --ahead;
+                    ok = warp_wait(bar(empty + g.s), g.phase ^ 1u);
+                    if (!ok || aborted(abort_flag)) break;
+                    t.store<false>(ring + g.s * kTile, warp & 3, lane);
+                    announce(full + g.s);
+                    g.next();
+                    // (after that: the piece it may have to wait for can need this tile)
+                    request(r.s);
+                    r.next();
                 }
                 cp_async_wait<0>();
             } else {
-                // K of tile g is requested before V of tile g - 1 is announced, and V of tile
-                // g before K of tile g: each has most of a tile's time to arrive.
+                // K and V of a tile are one group of copies; a tile is announced when the next
+                // one is requested.
+                Ring<N> a;
+                int pending = 0;
+                auto finish = [&]() {
+                    announce(kKFull + a.s);
+                    announce(kVFull + a.s);
+                    a.next();
+                    --pending;
+                };
                 while (more) {
+                    const int rows = rows_of();
                     next();
                     if (!ok) break;
-                    const int s = g & 1;
-                    if (g >= 2 && !warp_wait(bar(kKEmpty + s), ((g >> 1) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (aborted(abort_flag)) break;
-                    copy_tile(base + kOffK + s * kTile, p.kc, rows, warp, lane);
+                    ok = warp_wait(bar(kKEmpty + g.s), g.phase ^ 1u);
+                    if (!ok || aborted(abort_flag)) break;
+                    copy_tile(base + M.k + g.s * kTile, p.kc, rows, warp, lane);
+                    ok = warp_wait(bar(kVEmpty + g.s), g.phase ^ 1u);
+                    if (!ok || aborted(abort_flag)) break;
+                    copy_tile(base + M.v + g.s * kTile, p.vc, rows, warp, lane);
                     cp_async_commit();
-                    if (g > 0) {
-                        cp_async_wait<1>();
-                        announce(kVFull + (s ^ 1));
+                    g.next();
+                    if (++pending == N - 1) {
+                        cp_async_wait<N - 2>();
+                        finish();
                     }
-                    if (g >= 2 && !warp_wait(bar(kVEmpty + s), ((g >> 1) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    copy_tile(base + kOffV + s * kTile, p.vc, rows, warp, lane);
-                    cp_async_commit();
-                    cp_async_wait<1>();
-                    announce(kKFull + s);
-                    ++g;
-                    if (more) rows = rows_of();
                 }
                 cp_async_wait<0>();
-                if (g > 0) announce(kVFull + ((g - 1) & 1));
+                while (ok && pending > 0) finish();
             }
             if (__any_sync(0xffffffffu, bad_page) && lane == 0) atomicOr(p.flag, PA_FLAG_BAD_PAGE);
         }
         if (!ok && lane == 0) give_up(p, abort_flag);
-    } else if (warp < 8) {
-        reg_dec<104>();
-        if (warp == 4 && lane == 0) {
+    } else if (warp < kProd + 4) {
+        reg_dec<Q4 ? 72 : 104>();
+        if (warp == kProd) {
             // =========================== MMA issuer ===============================
+            // The whole warp runs the loop and one elected lane issues.
             constexpr uint32_t idS = idesc(Q4, 0, 0);  // Q, K both K-major
             constexpr uint32_t idO = idesc(Q4, 0, 1);  // P K-major, V MN-major
-            const uint64_t dQ0 = tc::smem_desc_sw128(base + kOffQ, 16, 1024);
-            const uint64_t dK0 = tc::smem_desc_sw128(base + kOffK, 16, 1024);
-            const uint64_t dV0 = tc::smem_desc_sw128(base + kOffV, kHalf, 1024);
-            auto qk = [&](int t, int buf, int gk) {
-                const uint64_t dq = tc::desc_advance(dQ0, buf * kTile), dk = tc::desc_advance(dK0, (gk & 1) * kTile);
-                const uint32_t d = tmem + 128u * t;
-                tc::mma_bf16_c<0>(d, dq, dk, idS);
-#pragma unroll
-                for (int kk = 1; kk < kD / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                    tc::mma_bf16_c<1>(d, tc::desc_advance(dq, off), tc::desc_advance(dk, off), idS);
-                }
-                tc::commit(bar(kSFull + t));
-            };
-            auto pv = [&](int t, bool first, int gk) {
-                const uint64_t dv = tc::desc_advance(dV0, (gk & 1) * kTile);
-                const uint32_t d = tmem + 256u + 128u * t, a = tmem + 128u * t;
-                if (first) tc::mma_bf16_ts_c<0>(d, a, dv, idO);
-                else tc::mma_bf16_ts_c<1>(d, a, dv, idO);
-#pragma unroll
-                for (int kk = 1; kk < BN / 16; ++kk)
-                    tc::mma_bf16_ts_c<1>(d, a + kk * 8, tc::desc_advance(dv, kk * 16 * 128), idO);
-                tc::commit(bar(kODone + t));
-            };
-            int gk = 0, pc0 = 0, pc1 = 0, oe0 = 0, oe1 = 0;
+            const uint64_t dQ0 = tc::smem_desc_sw128(base, 16, 1024);
+            const uint64_t dK0 = tc::smem_desc_sw128(base + M.k, 16, kGroup);
+            const uint64_t dV0 = tc::smem_desc_sw128(base + M.v, kHalf, kGroup);
+            const bool leader = elect_one();
+            Ring<N> kr, vr;
+            int pc0 = 0, pc1 = 0, oe0 = 0, oe1 = 0;
             bool ok = true;
             for (int k = 0; ok; ++k) {
-                ok = mbar_wait(bar(kItemFull + (k & 3)), (k >> 2) & 1);
+                ok = take(k);
                 if (!ok) break;
-                const int nk = slot(k)->n;
-                const bool lone = !MULTI || slot(k)->nt == 1;
-                mbar_arrive(bar(kItemEmpty + (k & 3)));
-                if (nk == 0) break;
-                const int jobs = lone ? nk : 2 * nk;
-                // job i: key tile, query buffer, and whether it is its key tile's last
-                auto tile = [&](int i) { return gk + (lone ? i : i >> 1); };
-                auto buf = [&](int i) { return MULTI ? (lone ? 0 : i & 1) : k & 1; };
-                auto closes = [&](int i) { return lone || (i & 1); };
-                auto issue_qk = [&](int i) {
-                    const int x = tile(i);
-                    if (!mbar_wait(bar(kKFull + (x & 1)), (x >> 1) & 1)) return false;
+                const int n = slot(k)->n;
+                release(k);
+                if (n == 0) break;
+                const int buf = q_buf(k);
+                const uint64_t dq0 = tc::desc_advance(dQ0, buf * (kTile / 2)), dq1 = tc::desc_advance(dq0, p.q_half);
+                auto qk = [&](int i) {  // Q K^T of the piece's tile i
+                    if (!warp_wait(bar(kKFull + kr.s), kr.phase)) return false;
                     tc::fence_after_sync();
-                    qk(i & 1, buf(i), x);
-                    if (closes(i)) tc::commit(bar(kKEmpty + (x & 1)));
-                    if (i == jobs - 1) tc::commit(bar(kQEmpty));
+                    const uint64_t dk = tc::desc_advance(dK0, kr.s * kTile);
+                    const uint32_t d = tmem + 128u * (i & 1);
+                    if (leader) {
+                        tc::mma_bf16_c<0>(d, dq0, dk, idS);
+#pragma unroll
+                        for (int kk = 1; kk < kD / 16; ++kk)
+                            tc::mma_bf16_c<1>(d, tc::desc_advance(kk < 4 ? dq0 : dq1, (kk & 3) * 32),
+                                              tc::desc_advance(dk, (kk >> 2) * kHalf + (kk & 3) * 32), idS);
+                        tc::commit(bar(kSFull + (i & 1)));
+                        if constexpr (C == 1) tc::commit(bar(kKEmpty + kr.s));
+                        else tc::commit_multicast(bar(kKEmpty + kr.s), kAll);
+                        if (i == n - 1) tc::commit(bar(kQEmpty + buf));
+                    }
+                    __syncwarp();
+                    kr.next();
                     return true;
                 };
-                const int qb = MULTI ? 0 : k & 1;
-                ok = mbar_wait(bar((Q4 ? kQReady : kQFull) + qb), (MULTI ? k : k >> 1) & 1);
-                if (!ok || *abort_flag) break;
-                tc::fence_after_sync();
-                ok = issue_qk(0) && (jobs < 2 || issue_qk(1));
-                for (int i = 0; ok && i < jobs; ++i) {
-                    const int t = i & 1, x = tile(i), pc = t ? pc1++ : pc0++, oe = t ? oe1 : oe0;
-                    ok = mbar_wait(bar(kVFull + (x & 1)), (x >> 1) & 1) && mbar_wait(bar(kPFull + t), pc & 1);
+                ok = warp_wait(bar((Q4 ? kQReady : kQFull) + buf), q_use(k) & 1);
+                if (!ok) break;
+                ok = qk(0) && (n < 2 || qk(1));
+                for (int i = 0; ok && i < n; ++i) {
+                    const int t = i & 1, pc = t ? pc1++ : pc0++, oe = t ? oe1 : oe0;
+                    ok = warp_wait(bar(kVFull + vr.s), vr.phase) && warp_wait(bar(kPFull + t), pc & 1);
                     // the previous piece's epilogue has read O
-                    if (ok && i < 2 && oe > 0) ok = mbar_wait(bar(kOFree + t), (oe - 1) & 1);
-                    if (!ok || *abort_flag) break;
+                    if (ok && i < 2 && oe > 0) ok = warp_wait(bar(kOFree + t), (oe - 1) & 1);
+                    if (!ok) break;
                     tc::fence_after_sync();
-                    pv(t, i < 2, x);
-                    if (closes(i)) tc::commit(bar(kVEmpty + (x & 1)));
-                    if (i + 2 < jobs) ok = issue_qk(i + 2);
+                    const uint64_t dv = tc::desc_advance(dV0, vr.s * kTile);
+                    const uint32_t d = tmem + 256u + 128u * t, a = tmem + 128u * t;
+                    if (leader) {
+                        tc::mma_bf16_ts(d, a, dv, idO, i >= 2);
+#pragma unroll
+                        for (int kk = 1; kk < BN / 16; ++kk)
+                            tc::mma_bf16_ts_c<1>(d, a + kk * 8, tc::desc_advance(dv, kk * 2 * kGroup), idO);
+                        tc::commit(bar(kODone + t));
+                        if constexpr (C == 1) tc::commit(bar(kVEmpty + vr.s));
+                        else tc::commit_multicast(bar(kVEmpty + vr.s), kAll);
+                    }
+                    __syncwarp();
+                    vr.next();
+                    if (i + 2 < n) ok = qk(i + 2);
                 }
-                if (!ok || *abort_flag) break;
-                gk += nk;
+                if (!ok) break;
                 ++oe0;
-                if (jobs > 1) ++oe1;
+                if (n > 1) ++oe1;
             }
-            if (!ok) give_up(p, abort_flag);
+            if (!ok && lane == 0) give_up(p, abort_flag);
             // nothing of ours may still be running when TMEM is freed
-            tc::commit(bar(kMmaDone));
-            if (!mbar_wait(bar(kMmaDone), 0)) give_up(p, abort_flag);
-        } else if (warp == 7) {
-            // ==================== pieces and query tiles =============================
+            if (leader) tc::commit(bar(kMmaDone));
+            __syncwarp();
+            if (!warp_wait(bar(kMmaDone), 0) && lane == 0) give_up(p, abort_flag);
+        } else if (warp == kProd + 2) {
+            // ========================= query tiles ===================================
             const uint64_t policy = l2_policy_evict_first();
-            const int start = static_cast<int>(blockIdx.x) * share[1], end = min(start + share[1], share[0]);
+            bool ok = true;
+            for (int k = 0;; ++k) {
+                ok = take(k);
+                if (!ok || slot(k)->n == 0) break;
+                // when the products of the last piece in the buffer are done
+                const int buf = q_buf(k), use = q_use(k), m = slot(k)->mp * C + rank;
+                const int row = (slot(k)->b * p.H_kv + slot(k)->kvh) * p.R + m * BM;
+                release(k);
+                ok = use == 0 || warp_wait(bar(kQEmpty + buf), (use - 1) & 1);
+                if (!ok || aborted(abort_flag)) break;
+                if (lane == 0) {
+                    if (m * BM < p.R) {
+                        const uint32_t dst = base + buf * (kTile / 2);
+                        mbar_arrive_expect_tx(bar(kQFull + buf), static_cast<uint32_t>(p.q_box) * 256u);
+                        tc::tma_load_2d(dst, &qmap, 0, row, bar(kQFull + buf), policy);
+                        tc::tma_load_2d(dst + p.q_half, &qmap, 64, row, bar(kQFull + buf), policy);
+                    } else {  // no rows for this CTA: its products are not looked at
+                        mbar_arrive(bar(kQFull + buf));
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok && lane == 0) give_up(p, abort_flag);
+        } else if (warp == kProd + 3) {
+            // ============================ pieces =====================================
+            const int start = my_share * per, end = min(start + per, total);
             int b = 0, S = 0, kvh = 0, mp = 0, ng = 0, seg = end;  // seg: first position of the segment
             if (start < end) {
-                b = share[2];
+                b = first_b;
                 S = seq_len(p, b);
                 ng = key_tiles(S);
-                const int i = (start - share[3]) / (kSegCost + ng);
-                kvh = i / p.nPairs;
-                mp = i - kvh * p.nPairs;
-                seg = share[3] + i * (kSegCost + ng);
+                const int i = (start - first_unit) / (kSegCost + ng);
+                kvh = i / p.nG;
+                mp = i - kvh * p.nG;
+                seg = first_unit + i * (kSegCost + ng);
             }
             int4 crossing = make_int4(-1, 0, 0, 0);
-            int before0 = 0, before1 = 0, loads = 0;
+            int before0 = 0, before1 = 0;
             bool ok = true;
             for (int k = 0;; ++k) {
                 // this share's key tiles of the segment (none: the share ends before them)
@@ -588,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     j0 = max(0, start - seg - kSegCost);
                     n = max(0, min(ng, end - seg - kSegCost) - j0);
                 }
-                if (k >= 4 && !warp_wait(bar(kItemEmpty + (k & 3)), ((k >> 2) - 1) & 1)) {
+                if (k >= I && !warp_wait(bar(kItemEmpty + k % I), (k / I - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -610,14 +677,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 8
                             for (int i = 0; i < 32; ++i) {
                                 const int row = 32 * w + i;
-                                const uint32_t word = row < p.L && lane < p.W ? __ldg(m + static_cast<long long>(row) * p.W + lane) : 0u;
+                                const uint32_t word =
+                                    row < p.L && lane < p.W ? __ldg(m + static_cast<long long>(row) * p.W + lane) : 0u;
                                 bits |= (__any_sync(0xffffffffu, word != 0u) ? 1u : 0u) << i;
                             }
                             if (lane == 0) o->live[w] = bits;
                         }
                     }
                 }
-                const int nt = !MULTI || 2 * mp + 1 >= p.nM ? 1 : 2;
                 if (lane == 0) {
                     o->b = b;
                     o->S = S;
@@ -626,41 +693,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o->ng = ng;
                     o->j0 = j0;
                     o->n = n;
-                    o->nt = nt;
-                    const int n0 = nt == 1 ? (n + 1) / 2 : n, n1 = nt == 1 ? n / 2 : n;
-                    o->jobs[0] = n0;
-                    o->jobs[1] = n1;
                     o->before[0] = before0;
                     o->before[1] = before1;
-                    before0 += n0;
-                    before1 += n1;
+                    before0 += (n + 1) / 2;
+                    before1 += n / 2;
                     if (n > 0 && j0 == 0 && n < ng)  // it ends in a later share
-                        crossing = make_int4(b, kvh, mp, (seg + kSegCost + ng - 1) / share[1]);
-                    mbar_arrive(bar(kItemFull + (k & 3)));
+                        crossing = make_int4(b, kvh, mp, (seg + kSegCost + ng - 1) / per);
+                    mbar_arrive(bar(kItemFull + k % I));
                 }
                 __syncwarp();
                 if (n == 0 || aborted(abort_flag)) break;
-                // its query tiles, when the products of the last piece in the buffer are done
-                const int ahead = MULTI ? 1 : 2, qb = MULTI ? 0 : k & 1;
-                if (k >= ahead && !warp_wait(bar(kQEmpty), (k - ahead) & 1)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    const int row = (b * p.H_kv + kvh) * p.R + 2 * mp * BM;
-                    mbar_arrive_expect_tx(bar(kQFull + qb), static_cast<uint32_t>(nt * p.q_box) * 256u);
-                    for (int t = 0; t < nt; ++t) {
-                        const uint32_t dst = base + kOffQ + (qb + t) * kTile;
-                        tc::tma_load_2d(dst, &qmap, 0, row + t * BM, bar(kQFull + qb), policy);
-                        tc::tma_load_2d(dst + kHalf, &qmap, 64, row + t * BM, bar(kQFull + qb), policy);
-                    }
-                }
-                ++loads;
-                __syncwarp();
                 // on to the next segment
                 seg += kSegCost + ng;
                 if (seg >= end) continue;
-                if (++mp == p.nPairs) {
+                if (++mp == p.nG) {
                     mp = 0;
                     if (++kvh == p.H_kv) {
                         kvh = 0;
@@ -670,43 +716,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (lane == 0) p.split[blockIdx.x] = crossing;
-            // no copy may land after the CTA's shared memory is gone
-            for (int x = MULTI ? 1 : 2; x >= 1; --x)
-                if (loads >= x) {
-                    const int k = loads - x, qb = MULTI ? 0 : k & 1;
-                    if (!warp_wait(bar(kQFull + qb), (MULTI ? k : k >> 1) & 1)) ok = false;
-                }
+            if (lane == 0 && rank == 0) p.split[my_share] = crossing;
             if (!ok && lane == 0) give_up(p, abort_flag);
         }
         __syncwarp();
     } else {
         // ============================== softmax =======================================
-        reg_inc<168>();
-        const int t = (warp - 8) >> 2, q4 = warp & 3, r = q4 * 32 + lane;  // slot, lane quarter, row
+        reg_inc<Q4 ? 128 : 168>();
+        const int t = (warp - kProd - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;  // slot, lane quarter, row
         const uint32_t trow = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-        int xc = 0;  // B's states handed over, two slots in turn
+        // How far (log2) a row's scores may rise above its maximum before O is rescaled:
+        // bf16 weights and fp32 sums have the exponents for it, f16 ends at 2^16.
+        constexpr float kSlack = Q4 ? 8.f : 64.f;
+        int xc = 0;  // pieces whose states were joined
         bool ok = true;
         for (int k = 0;; ++k) {
             ok = take(k);
             if (!ok || slot(k)->n == 0) break;
-            const int nk = slot(k)->jobs[t], sc = slot(k)->before[t], S = slot(k)->S, first = S - p.L;
-            const bool lone = !MULTI || slot(k)->nt == 1;
-            const int m = 2 * slot(k)->mp + (lone ? 0 : t);  // query tile
-            const int rows = p.R - m * BM;                    // of which a tile has at most BM
+            const int n = slot(k)->n, nk = (n + 1 - t) >> 1;  // this slot's tiles
+            const int sc = slot(k)->before[t], S = slot(k)->S, first = S - p.L;
+            const int m = slot(k)->mp * C + rank;  // query tile
+            const int rows = p.R - m * BM;         // of which a tile has at most BM
             const bool busy = q4 * 32 < rows, valid = r < rows;
             const int l = (m * BM + r) % p.L;  // draft
             const uint32_t* const mask = p.mask + (static_cast<long long>(slot(k)->b) * p.L + l) * p.W;
             float c = fmaxf(p.scale_log2, FLT_MIN);  // (scale 0: -inf stays -inf)
             if constexpr (Q4) {
-                // A's rows (a lone tile) or each tile's own, in place to f16, the largest
-                // value in [2^14, 2^15)
-                const int buf = MULTI ? (lone ? 0 : t) : k & 1, qb = MULTI ? 0 : k & 1;
-                float* const down = reinterpret_cast<float*>(sbase + kOffQScale) + buf * BM + r;
-                if (!lone || t == 0) {
-                    ok = warp_wait(bar(kQFull + qb), (MULTI ? k : k >> 1) & 1);
+                // A takes the rows in place to f16, the largest value in [2^14, 2^15)
+                const int buf = q_buf(k);
+                float* const down = reinterpret_cast<float*>(smem_raw + M.q_scale) + buf * BM + r;
+                if (t == 0) {
+                    ok = warp_wait(bar(kQFull + buf), q_use(k) & 1);
                     if (!ok) break;
-                    const uint32_t qrow = base + kOffQ + buf * kTile;
+                    const uint32_t qrow = base + buf * (kTile / 2);
                     if (busy) {
                         uint4 v[16];
                         float mx = 0.f;
@@ -714,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < 16; ++c) {
                             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                          : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
-                                         : "r"(qrow + (c >> 3) * kHalf + sw128(r, c & 7)));
+                                         : "r"(qrow + (c >> 3) * p.q_half + sw128(r, c & 7)));
                             const float2 f[4] = {bf16x2_to_float2(v[c].x), bf16x2_to_float2(v[c].y),
                                                  bf16x2_to_float2(v[c].z), bf16x2_to_float2(v[c].w)};
 #pragma unroll
@@ -726,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < 16; ++c) {
                             const float2 f[4] = {bf16x2_to_float2(v[c].x), bf16x2_to_float2(v[c].y),
                                                  bf16x2_to_float2(v[c].z), bf16x2_to_float2(v[c].w)};
-                            sts128(qrow + (c >> 3) * kHalf + sw128(r, c & 7), pack_f16x2(f[0].x * up, f[0].y * up),
+                            sts128(qrow + (c >> 3) * p.q_half + sw128(r, c & 7), pack_f16x2(f[0].x * up, f[0].y * up),
                                    pack_f16x2(f[1].x * up, f[1].y * up), pack_f16x2(f[2].x * up, f[2].y * up),
                                    pack_f16x2(f[3].x * up, f[3].y * up));
                         }
@@ -734,23 +776,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(kQReady + qb));
-                        if (MULTI && lone) mbar_arrive(bar(kQReady + qb));  // for B's warp, which has none
-                    }
-                }
-                // (B, without a job in a piece, must not wait: the pieces can run ahead of it)
-                if (nk > 0) {
-                    ok = warp_wait(bar(kQReady + qb), (MULTI ? k : k >> 1) & 1);
-                    if (!ok) break;
-                    if (busy) c = fmaxf(*down * p.scale_log2, FLT_MIN);
+                    if (lane == 0) mbar_arrive(bar(kQReady + buf));
                 }
             }
             const int tail = first_tail(S);
             float mrow = neg_inf();
             float2 lsum = make_float2(0.f, 0.f);
             for (int j = 0; j < nk; ++j) {
-                const int jt = slot(k)->j0 + (lone ? 2 * j + t : j);  // key tile
+                const int jt = slot(k)->j0 + 2 * j + t;  // key tile
                 uint32_t see[4];
                 if (busy && jt >= tail) {  // this row's bits of the tile, while S is on its way
                     const int x = jt * BN - first;
@@ -766,50 +799,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ok = warp_wait(bar(kSFull + t), (sc + j) & 1);
                 if (!ok || aborted(abort_flag)) break;
+                if constexpr (Q4) {
+                    if (j == 0) {  // (S is there, so this use of the buffer was announced, and none after it)
+                        const int buf = q_buf(k);
+                        ok = warp_wait(bar(kQReady + buf), q_use(k) & 1);
+                        if (!ok) break;
+                        if (busy)
+                            c = fmaxf(reinterpret_cast<const float*>(smem_raw + M.q_scale)[buf * BM + r] * p.scale_log2, FLT_MIN);
+                    }
+                }
                 if (busy) {
                     tc::fence_after_sync();
-                    float x[4][32];
-#pragma unroll
-                    for (int cc = 0; cc < 4; ++cc) tc::ld32(trow + 128u * t + cc * 32, x[cc]);
-                    tc::wait_ld();
-                    if (jt >= tail) {
-#pragma unroll
-                        for (int cc = 0; cc < 4; ++cc)
+                    const uint32_t st = trow + 128u * t;
+                    float2 ts = make_float2(0.f, 0.f);
+                    float mx = neg_inf(), alpha = 1.f;
+                    // 32 scores: masked, and the largest of them and mx
+                    auto largest = [&](float (&x)[32], int cc) {
+                        if (jt >= tail) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!(see[cc] >> e & 1u)) x[cc][e] = neg_inf();
-                    }
-                    float mq[4];
+                                if (!(see[cc] >> e & 1u)) x[e] = neg_inf();
+                        }
+                        float a = fmax3(x[0], x[1], mx), b = x[2];
 #pragma unroll
-                    for (int cc = 0; cc < 4; ++cc) {
-                        mq[cc] = x[cc][0];
+                        for (int e = 3; e < 31; e += 4) {
+                            a = fmax3(a, x[e], x[e + 1]);
+                            b = fmax3(b, x[e + 2], x[e + 3]);
+                        }
+                        mx = fmax3(a, b, x[31]);
+                    };
+                    // their weights against the maximum mu
+                    auto weights = [&](float (&x)[32], uint32_t* w, float mu) {
+                        const float2 c2 = make_float2(c, c), nm2 = make_float2(-mu, -mu);
 #pragma unroll
-                        for (int e = 1; e < 31; e += 2) mq[cc] = fmax3(mq[cc], x[cc][e], x[cc][e + 1]);
-                        mq[cc] = fmaxf(mq[cc], x[cc][31]);
-                    }
-                    const float mt = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * c;
-                    const bool grow = mt > mrow + kLazyRescaleLog2;
-                    const bool any_grow = __any_sync(0xffffffffu, grow);
-                    const float alpha = grow ? fast_exp2(mrow - mt) : 1.f;  // 2^-inf = 0 at the start
-                    if (grow) mrow = mt;
-                    const float mu = mrow == neg_inf() ? 0.f : mrow;
-                    const float2 c2 = make_float2(c, c), nm2 = make_float2(-mu, -mu);
-                    float2 ts = make_float2(0.f, 0.f);
-                    uint32_t pw[64];
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), c2, nm2);
+                            const float2 ex = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                            w[i] = Q4 ? pack_f16x2(ex.x, ex.y) : pack_bf16x2(ex.x, ex.y);
+                            ts = __fadd2_rn(ts, Q4 ? ex : bf16x2_to_float2(w[i]));
+                        }
+                    };
+                    // the tile's maximum from all of S; true where the row's moved
+                    auto maximum = [&](float slack) {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        const int cc = i >> 4, e = (i & 15) * 2;
-                        const float2 y = __ffma2_rn(make_float2(x[cc][e], x[cc][e + 1]), c2, nm2);
-                        const float2 ex = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                        pw[i] = Q4 ? pack_f16x2(ex.x, ex.y) : pack_bf16x2(ex.x, ex.y);
-                        ts = __fadd2_rn(ts, Q4 ? ex : bf16x2_to_float2(pw[i]));
-                    }
-                    lsum.x = lsum.x * alpha + ts.x;
-                    lsum.y = lsum.y * alpha + ts.y;
+                        for (int cc = 0; cc < 4; ++cc) {
+                            float x[32];
+                            tc::ld32(st + cc * 32, x);
+                            tc::wait_ld();
+                            largest(x, cc);
+                        }
+                        const float mt = mx * c;
+                        const bool grow = valid && mt > mrow + slack;  // (other rows hold anything)
+                        if (grow) {
+                            alpha = fast_exp2(mrow - mt);  // 2^-inf = 0 at the start
+                            mrow = mt;
+                        }
+                        return __any_sync(0xffffffffu, grow);
+                    };
                     // O is rescaled once this slot's previous P V is done
-                    if (any_grow && j > 0) {
-                        ok = warp_wait(bar(kODone + t), (sc + j - 1) & 1);
-                        if (!ok || aborted(abort_flag)) break;
+                    auto rescale = [&]() {
+                        if (!warp_wait(bar(kODone + t), (sc + j - 1) & 1)) return false;
                         tc::fence_after_sync();
 #pragma unroll 1
                         for (int cc = 0; cc < 4; ++cc) {
@@ -821,10 +870,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::st32(trow + 256u + 128u * t + cc * 32, o);
                         }
                         tc::wait_st();
+                        return true;
+                    };
+                    // P goes over the first 64 columns of this slot's S
+                    if constexpr (Q4) {
+                        // S is read twice, so that few registers do (the producers need them);
+                        // 32 keys' P lies over scores that are used up
+                        if (maximum(kSlack) && j > 0) {
+                            ok = rescale();
+                            if (!ok) break;
+                        }
+                        const float mu = mrow == neg_inf() ? 0.f : mrow;
+#pragma unroll
+                        for (int cc = 0; cc < 4; ++cc) {
+                            float x[32];
+                            tc::ld32(st + cc * 32, x);
+                            tc::wait_ld();
+                            if (jt >= tail) largest(x, cc);
+                            uint32_t w[16];
+                            weights(x, w, mu);
+                            tc::st16(st + cc * 16, w);
+                        }
+                    } else {
+                        // Against the maximum so far: no weight waits for the scores behind it.
+                        // Only where that was too low by 2^kSlack (or there was none) is the
+                        // tile done again, with its own maximum.
+                        uint32_t pw[64];
+                        bool again = true;
+                        if (j > 0) {
+                            const float mu = mrow == neg_inf() ? 0.f : mrow;
+                            float x[2][32];
+                            tc::ld32(st, x[0]);
+#pragma unroll
+                            for (int cc = 0; cc < 4; ++cc) {
+                                tc::wait_ld();
+                                if (cc < 3) tc::ld32(st + cc * 32 + 32, x[(cc + 1) & 1]);
+                                largest(x[cc & 1], cc);
+                                weights(x[cc & 1], pw + 16 * cc, mu);
+                            }
+                            again = __any_sync(0xffffffffu, valid && mx * c > mrow + kSlack);
+                        }
+                        if (again) {
+                            mx = neg_inf();
+                            if (maximum(0.f) && j > 0) {
+                                ok = rescale();
+                                if (!ok) break;
+                            }
+                            ts = make_float2(0.f, 0.f);
+                            const float mu = mrow == neg_inf() ? 0.f : mrow;
+#pragma unroll
+                            for (int cc = 0; cc < 4; ++cc) {
+                                float x[32];
+                                tc::ld32(st + cc * 32, x);
+                                tc::wait_ld();
+                                if (jt >= tail) largest(x, cc);
+                                weights(x, pw + 16 * cc, mu);
+                            }
+                        }
+                        tc::st32(st, *reinterpret_cast<const uint32_t(*)[32]>(pw));
+                        tc::st32(st + 32, *reinterpret_cast<const uint32_t(*)[32]>(pw + 32));
                     }
-                    // P over the first 64 columns of this slot's S (read above)
-                    tc::st32(trow + 128u * t, *reinterpret_cast<const uint32_t(*)[32]>(pw));
-                    tc::st32(trow + 128u * t + 32, *reinterpret_cast<const uint32_t(*)[32]>(pw + 32));
+                    lsum.x = lsum.x * alpha + ts.x;
+                    lsum.y = lsum.y * alpha + ts.y;
                     tc::wait_st();
                     tc::fence_before_sync();
                 }
@@ -833,58 +940,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok || aborted(abort_flag)) break;
             const volatile Item* const it = slot(k);
+            // The two slots' states of a row are joined by both warpgroups, 64 dims each (one
+            // tile: A has them all).
             float l1 = lsum.x + lsum.y;
-            if (lone && t == 1) {  // A joins this half with its own
-                if (nk > 0) {
-                    float2* const x = reinterpret_cast<float2*>(sbase + kOffX) + (xc & 1) * BM + r;
-                    *x = make_float2(mrow, l1);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kXFull + (xc & 1)));
-                    ++xc;
-                }
-                release(k);
-                continue;
+            const bool both = n > 1;
+            float w0 = 1.f, w1 = 0.f;  // weights of O 0 and O 1
+            if (both) {
+                float2* const x = reinterpret_cast<float2*>(smem_raw + M.x) + r;
+                ok = xc == 0 || warp_wait(bar(kXFree), (xc - 1) & 1);  // (the last joined piece's are read)
+                if (!ok) break;
+                x[t * BM] = make_float2(mrow, l1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kXFull));
+                ok = warp_wait(bar(kXFull), xc & 1);
+                if (!ok) break;
+                ++xc;
+                const float2 a = x[0], e = x[BM];
+                const float mm = fmaxf(a.y == 0.f ? neg_inf() : a.x, e.y == 0.f ? neg_inf() : e.x);
+                w0 = a.y == 0.f ? 0.f : fast_exp2(a.x - mm);
+                w1 = e.y == 0.f ? 0.f : fast_exp2(e.x - mm);
+                l1 = (a.y == 0.f ? 0.f : a.y * w0) + (e.y == 0.f ? 0.f : e.y * w1);
+                mrow = mm;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kXFree));
+                ok = warp_wait(bar(kODone), (it->before[0] + ((n + 1) >> 1) - 1) & 1) &&
+                     warp_wait(bar(kODone + 1), (it->before[1] + (n >> 1) - 1) & 1);
+                if (!ok) break;
+            } else if (t == 0) {
+                ok = warp_wait(bar(kODone), sc & 1);
+                if (!ok) break;
             }
             const bool full = it->n == it->ng;
             // (a full piece has tail tiles)
             const bool drafted = it->live[l >> 5] >> (l & 31) & 1u;
             const long long row = (static_cast<long long>(it->b) * p.H_kv + it->kvh) * p.R + m * BM + r;
-            const long long part = ((2ll * blockIdx.x + (it->j0 > 0 ? 0 : 1)) * 2 + (lone ? 0 : t)) * BM + r;
-            const int nb = lone ? it->jobs[1] : 0;  // jobs of the other half
-            float own = 1.f, other = 0.f;
-            if (nb > 0) {
-                ok = warp_wait(bar(kXFull + (xc & 1)), (xc >> 1) & 1);
-                if (!ok) break;
-                const float2 x = reinterpret_cast<const float2*>(sbase + kOffX)[(xc & 1) * BM + r];
-                ++xc;
-                if (x.y != 0.f) {
-                    const float M = fmaxf(mrow, x.x);
-                    own = fast_exp2(mrow - M);
-                    other = fast_exp2(x.x - M);
-                    l1 = l1 * own + x.y * other;
-                    mrow = M;
-                }
-                ok = warp_wait(bar(kODone + 1), (it->before[1] + nb - 1) & 1);
-                if (!ok) break;
-            }
-            if (!full && valid) p.part_ml[part] = make_float2(mrow, l1);
-            ok = warp_wait(bar(kODone + t), (sc + nk - 1) & 1);
-            if (!ok) break;
-            if (busy) {
+            const long long part = (2ll * blockIdx.x + (it->j0 > 0 ? 0 : 1)) * BM + r;
+            if (!full && valid && t == 0) p.part_ml[part] = make_float2(mrow, l1);
+            if (busy && (both || t == 0)) {
                 tc::fence_after_sync();
                 const float inv = l1 == 0.f ? 0.f : 1.f / l1;
+                // 32 dims a step
 #pragma unroll 1
-                for (int cc = 0; cc < 4; ++cc) {
+                for (int cc = both ? 2 * t : 0; cc < (both ? 2 * t + 2 : 4); ++cc) {
                     float o[32];
                     __syncwarp();
-                    tc::ld32(trow + 256u + 128u * t + cc * 32, o);
-                    tc::wait_ld();
-                    if (nb > 0) {  // (uniform)
+                    tc::ld32(trow + 256u + cc * 32, o);
+                    if (both) {
                         float o2[32];
-                        tc::ld32(trow + 256u + 128u + cc * 32, o2);
+                        tc::ld32(trow + 384u + cc * 32, o2);
                         tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = o[e] * own + o2[e] * other;
+                        for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + o2[e] * w1;
+                    } else {
+                        tc::wait_ld();
                     }
                     if (!valid) continue;
                     if (full) {
@@ -912,8 +1020,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O is read: the next piece's first P V may overwrite it
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(bar(kOFree + t));
-                if (nb > 0) mbar_arrive(bar(kOFree + 1));
+                if (both || t == 0) mbar_arrive(bar(kOFree));
+                if (!both && t == 0) mbar_arrive(bar(kOFree));  // (for B's warp, which has nothing to read)
+                if (both) mbar_arrive(bar(kOFree + 1));
             }
             release(k);
         }
@@ -923,55 +1032,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- tear-down: free TMEM once every role is done ---------------------------
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == kProd) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmemCols);
     }
+    if constexpr (C > 1) cluster_sync();  // peers' copies and commits come here until they are done
 }
 
 // Merges the partial states of the segments that cross shares: CTA y + ny c takes rows
-// 8 y .. of the segment that starts in share c, one a warp, four partial states in flight.
-constexpr int kMergeRows = 8;
-__global__ void __launch_bounds__(256) tree_merge_kernel(const TileParams p, int ny) {
+// 32 y .. of the segment that starts in share c, four a warp, two partial states of each in
+// flight.  C: CTAs of a share, one query tile each.
+constexpr int kMergeRows = 4;
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TileParams p, int ny, int C) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = static_cast<int>(blockIdx.x) / ny, rr = kMergeRows * (static_cast<int>(blockIdx.x) - c * ny) + warp;
+    const int c = static_cast<int>(blockIdx.x) / ny;
+    const int r0 = kMergeRows * (8 * (static_cast<int>(blockIdx.x) - c * ny) + warp);
     pdl_wait_primary();
     const int4 sp = p.split[c];
-    const int in_head = sp.z * 2 * BM + rr;
+    const int in_head = sp.z * C * BM + r0;
     if (sp.x < 0 || in_head >= p.R) return;
-    const int t = rr >> 7, r = rr & 127, l = in_head % p.L;
-    const uint32_t* const m = p.mask + (static_cast<long long>(sp.x) * p.L + l) * p.W;
-    const bool drafted = __any_sync(0xffffffffu, lane < p.W && __ldg(m + lane) != 0u);
-    float M = neg_inf(), sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int U = 4;
-    for (int k = c; k <= sp.w && drafted; k += U) {
-        float2 v[U];
-        float4 x[U];
+    uint32_t drafted[kMergeRows];  // a word of the row's mask
+    float M[kMergeRows], sum[kMergeRows];
+    float4 acc[kMergeRows];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            v[u] = make_float2(neg_inf(), 0.f);
-            if (k + u > sp.w) continue;
-            const long long slot = ((2ll * (k + u) + (k + u == c ? 1 : 0)) * 2 + t) * BM + r;
-            v[u] = p.part_ml[slot];
-            x[u] = *reinterpret_cast<const float4*>(p.part_o + slot * kD + 4 * lane);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (v[u].y == 0.f) continue;  // no key (x was not written)
-            const float mx = fmaxf(M, v[u].x), a = fast_exp2(M - mx), b = fast_exp2(v[u].x - mx);
-            M = mx;
-            sum = sum * a + v[u].y * b;
-            acc.x = acc.x * a + x[u].x * b;
-            acc.y = acc.y * a + x[u].y * b;
-            acc.z = acc.z * a + x[u].z * b;
-            acc.w = acc.w * a + x[u].w * b;
-        }
+    for (int i = 0; i < kMergeRows; ++i) {
+        const uint32_t* const m = p.mask + (static_cast<long long>(sp.x) * p.L + (in_head + i) % p.L) * p.W;
+        drafted[i] = lane < p.W ? __ldg(m + lane) : 0u;
+        M[i] = neg_inf();
+        sum[i] = 0.f;
+        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (0: a row without keys; NaN stays)
-    const long long row = (static_cast<long long>(sp.x) * p.H_kv + sp.y) * p.R + in_head;
-    *reinterpret_cast<uint2*>(p.out + row * kD + 4 * lane) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    constexpr int U = 2;
+    for (int k = c; k <= sp.w; k += U) {
+        float2 v[U][kMergeRows];
+        float4 x[U][kMergeRows];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < kMergeRows; ++i) {
+                v[u][i] = make_float2(neg_inf(), 0.f);
+                if (k + u > sp.w || in_head + i >= p.R) continue;
+                const int cta = (k + u) * C + (r0 + i) / BM;
+                const long long slot = (2ll * cta + (k + u == c ? 1 : 0)) * BM + (r0 + i) % BM;
+                v[u][i] = p.part_ml[slot];
+                x[u][i] = *reinterpret_cast<const float4*>(p.part_o + slot * kD + 4 * lane);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < kMergeRows; ++i) {
+                if (v[u][i].y == 0.f) continue;  // no key (x was not written)
+                const float mx = fmaxf(M[i], v[u][i].x), a = fast_exp2(M[i] - mx), b = fast_exp2(v[u][i].x - mx);
+                M[i] = mx;
+                sum[i] = sum[i] * a + v[u][i].y * b;
+                acc[i].x = acc[i].x * a + x[u][i].x * b;
+                acc[i].y = acc[i].y * a + x[u][i].y * b;
+                acc[i].z = acc[i].z * a + x[u][i].z * b;
+                acc[i].w = acc[i].w * a + x[u][i].w * b;
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+        const bool live = __any_sync(0xffffffffu, drafted[i] != 0u);
+        if (in_head + i >= p.R) continue;
+        const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];  // (0: a row without keys; NaN stays)
+        const long long row = (static_cast<long long>(sp.x) * p.H_kv + sp.y) * p.R + in_head + i;
+        uint2 w = make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+        if (!live) w = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2*>(p.out + row * kD + 4 * lane) = w;
+    }
 }
 
 struct TilePlan {
@@ -981,26 +1110,70 @@ struct TilePlan {
 // (the same for every shape)
 TilePlan plan(int sm_count) {
     TilePlan t;
-    const size_t slots = 2ull * sm_count * 2 * BM;
+    const size_t states = 2ull * sm_count * BM;
     t.split_off = kFlagBytes;
     t.ml_off = align_up(t.split_off + 16ull * sm_count, 256);
-    t.o_off = align_up(t.ml_off + slots * 8, 256);
-    t.total = t.o_off + slots * kD * 4;
+    t.o_off = align_up(t.ml_off + states * 8, 256);
+    t.total = t.o_off + states * kD * 4;
     return t;
 }
 
-template <Source SRC, bool MULTI>
-pa_status launch_tiles(const TileParams& p, const CUtensorMap* maps, const TreeCall& c) {
-    static int attr_done[64] = {0};
-    if (!attr_done[c.dev.device]) {
-        if (cudaFuncSetAttribute(tree_tile_kernel<SRC, MULTI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 smem_bytes(SRC)) != cudaSuccess)
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        else
+            cudaGetLastError();
+    });
+    return fn;
+}
+
+// 4-D map of a pool: 64 dims, 8 rows, 2 halves of the dims, groups of 8 rows; boxes of
+// box_rows rows land as [8 rows][half][row][64 dims], 128-byte swizzle.
+bool make_pool_map(CUtensorMap* map, const void* ptr, long long rows, int box_rows) {
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {64, 8, 2, static_cast<cuuint64_t>(rows / 8)};
+    const cuuint64_t strides[3] = {kD * 2, kD, 8 * kD * 2};
+    const cuuint32_t box[4] = {64, 8, 2, static_cast<cuuint32_t>(box_rows / 8)};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, steps,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Source SRC, int C>
+pa_status launch_tiles(const TileParams& p, const CUtensorMap* maps, const TreeCall& c, int* shares) {
+    constexpr int bytes = smem(SRC).total;
+    static int clusters[64] = {0};  // resident together, per device
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(threads(SRC));
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    cfg.gridDim = dim3(static_cast<unsigned>(c.dev.sm_count / C * C));
+    if (!clusters[c.dev.device]) {
+        if (cudaFuncSetAttribute(tree_tile_kernel<SRC, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
             return PA_ERR_CUDA;
-        attr_done[c.dev.device] = 1;
+        int n = c.dev.sm_count;
+        if (C > 1 && cudaOccupancyMaxActiveClusters(&n, tree_tile_kernel<SRC, C>, &cfg) != cudaSuccess) return PA_ERR_CUDA;
+        clusters[c.dev.device] = std::min(n, c.dev.sm_count / C);
+        if (clusters[c.dev.device] < 1) return PA_ERR_UNSUPPORTED;
     }
-    tree_tile_kernel<SRC, MULTI><<<static_cast<unsigned>(c.dev.sm_count), kThreads, smem_bytes(SRC), c.stream>>>(
-        p, maps[0], maps[1], maps[2]);
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    *shares = clusters[c.dev.device];
+    cfg.gridDim = dim3(static_cast<unsigned>(*shares * C));
+    return cudaLaunchKernelEx(&cfg, tree_tile_kernel<SRC, C>, p, maps[0], maps[1], maps[2]) == cudaSuccess ? PA_OK
+                                                                                                         : PA_ERR_CUDA;
 }
 
 int gcd_int(int a, int b) {
@@ -1017,16 +1190,16 @@ int gcd_int(int a, int b) {
 bool tree_tiles_supported(const pa_shape& sh) {
     const long long R = static_cast<long long>(sh.H_q / sh.H_kv) * sh.L;
     const long long cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
-    const long long pairs = (R + 2 * BM - 1) / (2 * BM);
     // costs are counted in an int
-    return sh.dtype == PA_BF16 && static_cast<long long>(sh.B) * sh.H_kv * pairs * (cap / BN + 1 + kSegCost) < INT_MAX / 2;
+    return sh.dtype == PA_BF16 &&
+           static_cast<long long>(sh.B) * sh.H_kv * ((R + BM - 1) / BM) * (cap / BN + 1 + kSegCost) < INT_MAX / 2;
 }
 
 size_t tree_tiles_workspace_bytes(int sm_count) { return plan(sm_count).total; }
 
 pa_status tree_tiles_launch(const TreeCall& c) {
     const pa_shape& sh = c.sh;
-    if (c.dev.smem_optin < smem_bytes(kQ4)) return PA_ERR_UNSUPPORTED;
+    if (c.dev.smem_optin < smem(kTma).total || c.dev.smem_optin < smem(kQ4).total) return PA_ERR_UNSUPPORTED;
     const TilePlan t = plan(c.dev.sm_count);
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
     TileParams p;
@@ -1047,35 +1220,33 @@ pa_status tree_tiles_launch(const TreeCall& c) {
     p.R = sh.H_q / sh.H_kv * sh.L;
     p.L = sh.L;
     p.W = tree_words(sh.L);
-    p.nM = (p.R + BM - 1) / BM;
-    p.nPairs = (p.nM + 1) / 2;
     p.num_pages = sh.num_pages;
     p.ps = sh.page_size;
     p.max_npg = sh.max_pages_per_seq;
     p.pool_rows = sh.num_pages * sh.H_kv * sh.page_size;
-    p.box = gcd_int(sh.page_size, BN);
     p.q_box = std::min(BM, (p.R + 7) / 8 * 8);
+    p.q_bufs = p.q_box <= BM / 2 ? 2 : 1;
+    p.q_half = kTile / 2 / p.q_bufs;
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     p.scale_log2 = c.scale * 1.4426950408889634f;
     p.out32 = reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
     const bool tma = !c.ks && sh.page_size % 8 == 0;
+    const int nM = (p.R + BM - 1) / BM, C = tma && nM > 1 ? 2 : 1;
+    p.nG = (nM + C - 1) / C;
+    p.box = std::min(gcd_int(sh.page_size, BN), BN / C);
     CUtensorMap maps[3];
     if (!make_map(&maps[0], c.q, static_cast<long long>(sh.B) * sh.H_q * sh.L, p.q_box)) return PA_ERR_CUDA;
     maps[1] = maps[2] = maps[0];
-    if (tma && (!make_map(&maps[1], c.kc, p.pool_rows, p.box) || !make_map(&maps[2], c.vc, p.pool_rows, p.box)))
+    if (tma && (!make_pool_map(&maps[1], c.kc, p.pool_rows, p.box) || !make_pool_map(&maps[2], c.vc, p.pool_rows, p.box)))
         return PA_ERR_CUDA;
-    pa_status st;
-    if (p.nM > 1)
-        st = c.ks  ? launch_tiles<kQ4, true>(p, maps, c)
-             : tma ? launch_tiles<kTma, true>(p, maps, c)
-                   : launch_tiles<kCopy, true>(p, maps, c);
-    else
-        st = c.ks  ? launch_tiles<kQ4, false>(p, maps, c)
-             : tma ? launch_tiles<kTma, false>(p, maps, c)
-                   : launch_tiles<kCopy, false>(p, maps, c);
+    int shares = 0;
+    const pa_status st = c.ks    ? launch_tiles<kQ4, 1>(p, maps, c, &shares)
+                         : !tma  ? launch_tiles<kCopy, 1>(p, maps, c, &shares)
+                         : C > 1 ? launch_tiles<kTma, 2>(p, maps, c, &shares)
+                                 : launch_tiles<kTma, 1>(p, maps, c, &shares);
     if (st != PA_OK) return st;
-    const int ny = (std::min(p.R, 2 * BM) + kMergeRows - 1) / kMergeRows;
-    return launch_dependent(tree_merge_kernel, dim3(static_cast<unsigned>(c.dev.sm_count * ny)), 256, 0, c.stream, p, ny)
+    const int ny = (std::min(p.R, C * BM) + 8 * kMergeRows - 1) / (8 * kMergeRows);
+    return launch_dependent(tree_merge_kernel, dim3(static_cast<unsigned>(shares * ny)), 256, 0, c.stream, p, ny, C)
                ? PA_OK
                : PA_ERR_CUDA;
 }
