@@ -20,8 +20,8 @@
 //     states that tree_merge_kernel joins.
 //   * The key tiles of a piece go in turn to two slots t = 0, 1, each with its own S and P
 //     (P over S), O, m and l in Tensor Memory and one softmax warpgroup, one row per thread;
-//     both join them at the piece's end.  The MMA warp issues P V of tile i, then
-//     Q K^T of tile i + 2, so one slot's softmax overlaps the other's products.
+//     both join them at the piece's end.  The MMA warp issues P V of tile i, then Q K^T of
+//     tile i + 2, so one slot's softmax overlaps the other's products.
 //   * The producer warps bring K and V into rings in the 128-byte swizzle that the MMA reads:
 //     one lane per page box by TMA (bf16, pages of a multiple of 8 slots), 16-byte
 //     asynchronous copies (other page sizes), or 4-bit rows dequantised on the way.
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         mbar_init(bar(kMmaDone), 1);
         for (int s = 0; s < I; ++s) {
             mbar_init(bar(kItemFull + s), 1);
-            // K/V warps, the MMA thread, the query warp, softmax warps
+            // K/V warps, the MMA warp, the query warp, softmax warps
             mbar_init(bar(kItemEmpty + s), (SRC == kTma ? 2 : kProd) + 2 + 8);
         }
         *abort_flag = 0;
@@ -305,6 +305,21 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const int total = share[0], per = share[1], first_b = share[2], first_unit = share[3];
+    // which slots of the share's first sequence hold a draft, where one warp would take long
+    uint32_t first_live = 0u;
+    if (p.W > 4 && my_share * per < total) {
+        uint32_t* const words = reinterpret_cast<uint32_t*>(share) + 64;
+        if (tid < 32) words[tid] = 0u;
+        __syncthreads();
+        const uint32_t* const mask = p.mask + static_cast<long long>(first_b) * p.L * p.W;
+#pragma unroll 4
+        for (int i = warp; i < p.L; i += kThreads / 32) {
+            const uint32_t word = lane < p.W ? __ldg(mask + static_cast<long long>(i) * p.W + lane) : 0u;
+            if (__any_sync(0xffffffffu, word != 0u) && lane == 0) atomicOr(words + (i >> 5), 1u << (i & 31));
+        }
+        __syncthreads();
+        first_live = words[lane];
+    }
     __syncthreads();  // (the states lie there)
     auto slot = [&](int k) { return reinterpret_cast<volatile Item*>(smem_raw + M.items + kItemBytes * (k % I)); };
     auto take = [&](int k) { return warp_wait(bar(kItemFull + k % I), (k / I) & 1); };  // a whole warp
@@ -320,7 +335,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
 
     if (warp < kProd) {
         // ========================= K/V producers ==================================
-        reg_dec<72>();
+        reg_dec<Q4 ? 64 : 72>();
         bool ok = true;
         if constexpr (SRC == kTma) {
             if (warp == 0) {
@@ -531,7 +546,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         }
         if (!ok && lane == 0) give_up(p, abort_flag);
     } else if (warp < kProd + 4) {
-        reg_dec<Q4 ? 72 : 104>();
+        reg_dec<Q4 ? 64 : 104>();
         if (warp == kProd) {
             // =========================== MMA issuer ===============================
             // The whole warp runs the loop and one elected lane issues.
@@ -647,6 +662,10 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             }
             int4 crossing = make_int4(-1, 0, 0, 0);
             int before0 = 0, before1 = 0;
+            // lane w: word w of the slots of sequence live_b that hold a draft
+            int live_b = start < end ? first_b : -1;
+            uint32_t live = first_live;
+            if (p.W <= 4) live_b = -1;
             bool ok = true;
             for (int k = 0;; ++k) {
                 // this share's key tiles of the segment (none: the share ends before them)
@@ -661,29 +680,29 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 }
                 volatile Item* const o = slot(k);
                 if (n > 0 && (j0 + n) * BN > S - p.L) {
-                    const uint32_t* const m = p.mask + static_cast<long long>(b) * p.L * p.W;
-                    if (p.W <= 4) {  // a lane per draft
-                        for (int w = 0; w < p.W; ++w) {
-                            const int i = 32 * w + lane;
-                            uint32_t any = 0u;
-                            for (int x = 0; x < p.W; ++x)
-                                if (i < p.L) any |= __ldg(m + static_cast<long long>(i) * p.W + x);
-                            any = __ballot_sync(0xffffffffu, any != 0u);
-                            if (lane == 0) o->live[w] = any;
-                        }
-                    } else {  // a lane per word
-                        for (int w = 0; w < p.W; ++w) {
-                            uint32_t bits = 0u;
-#pragma unroll 8
-                            for (int i = 0; i < 32; ++i) {
-                                const int row = 32 * w + i;
-                                const uint32_t word =
-                                    row < p.L && lane < p.W ? __ldg(m + static_cast<long long>(row) * p.W + lane) : 0u;
-                                bits |= (__any_sync(0xffffffffu, word != 0u) ? 1u : 0u) << i;
+                    if (b != live_b) {
+                        live_b = b;
+                        live = 0u;
+                        const uint32_t* const mask = p.mask + static_cast<long long>(b) * p.L * p.W;
+                        if (p.W <= 4) {  // a lane per draft
+                            for (int w = 0; w < p.W; ++w) {
+                                const int i = 32 * w + lane;
+                                uint32_t any = 0u;
+                                for (int x = 0; x < p.W; ++x)
+                                    if (i < p.L) any |= __ldg(mask + static_cast<long long>(i) * p.W + x);
+                                any = __ballot_sync(0xffffffffu, any != 0u);
+                                if (lane == w) live = any;
                             }
-                            if (lane == 0) o->live[w] = bits;
+                        } else {
+#pragma unroll 16
+                            for (int i = 0; i < p.L; ++i) {
+                                const uint32_t word = lane < p.W ? __ldg(mask + static_cast<long long>(i) * p.W + lane) : 0u;
+                                const bool any = __any_sync(0xffffffffu, word != 0u);
+                                if (any && lane == (i >> 5)) live |= 1u << (i & 31);
+                            }
                         }
                     }
+                    o->live[lane] = live;
                 }
                 if (lane == 0) {
                     o->b = b;
@@ -722,7 +741,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         __syncwarp();
     } else {
         // ============================== softmax =======================================
-        reg_inc<Q4 ? 128 : 168>();
+        reg_inc<Q4 ? 144 : 168>();
         const int t = (warp - kProd - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;  // slot, lane quarter, row
         const uint32_t trow = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         // How far (log2) a row's scores may rise above its maximum before O is rescaled:
@@ -730,16 +749,108 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         constexpr float kSlack = Q4 ? 8.f : 64.f;
         int xc = 0;  // pieces whose states were joined
         bool ok = true;
+        // The end of piece k, with this slot's maximum and sum.  The two slots' states of a row are joined by both warpgroups,
+        // 64 dims each (one tile: A has them all).
+        auto finish = [&](int k, float m1, float l1) {
+            const volatile Item* const it = slot(k);
+            const bool both = it->n > 1;
+            const int m = it->mp * C + rank, rows = p.R - m * BM;
+            const bool busy = q4 * 32 < rows, valid = r < rows;
+            const int l = static_cast<unsigned>(m * BM + r) % static_cast<unsigned>(p.L);  // draft
+            float w0 = 1.f, w1 = 0.f;  // weights of O 0 and O 1
+            if (both) {
+                float2* const x = reinterpret_cast<float2*>(smem_raw + M.x) + r;
+                ok = xc == 0 || warp_wait(bar(kXFree), (xc - 1) & 1);  // (the last joined piece's are read)
+                if (!ok) return false;
+                x[t * BM] = make_float2(m1, l1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kXFull));
+                ok = warp_wait(bar(kXFull), xc & 1);
+                if (!ok) return false;
+                ++xc;
+                const float2 a = x[0], e = x[BM];
+                const float mm = fmaxf(a.y == 0.f ? neg_inf() : a.x, e.y == 0.f ? neg_inf() : e.x);
+                w0 = a.y == 0.f ? 0.f : fast_exp2(a.x - mm);
+                w1 = e.y == 0.f ? 0.f : fast_exp2(e.x - mm);
+                l1 = (a.y == 0.f ? 0.f : a.y * w0) + (e.y == 0.f ? 0.f : e.y * w1);
+                m1 = mm;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kXFree));
+                ok = warp_wait(bar(kODone), (it->before[0] + ((it->n + 1) >> 1) - 1) & 1) &&
+                     warp_wait(bar(kODone + 1), (it->before[1] + (it->n >> 1) - 1) & 1);
+                if (!ok) return false;
+            } else if (t == 0) {
+                ok = warp_wait(bar(kODone), it->before[0] & 1);
+                if (!ok) return false;
+            }
+            const bool full = it->n == it->ng;
+            // (a full piece has tail tiles)
+            const bool drafted = it->live[l >> 5] >> (l & 31) & 1u;
+            const long long row = (static_cast<long long>(it->b) * p.H_kv + it->kvh) * p.R + m * BM + r;
+            const long long part = (2ll * blockIdx.x + (it->j0 > 0 ? 0 : 1)) * BM + r;
+            if (!full && valid && t == 0) p.part_ml[part] = make_float2(m1, l1);
+            if (busy && (both || t == 0)) {
+                tc::fence_after_sync();
+                const float inv = l1 == 0.f ? 0.f : 1.f / l1;
+                // 32 dims a step
+#pragma unroll 1
+                for (int cc = both ? 2 * t : 0; cc < (both ? 2 * t + 2 : 4); ++cc) {
+                    float o[32];
+                    __syncwarp();
+                    tc::ld32(trow + 256u + cc * 32, o);
+                    if (both) {
+                        float o1[32];
+                        tc::ld32(trow + 384u + cc * 32, o1);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + o1[e] * w1;
+                    } else {
+                        tc::wait_ld();
+                    }
+                    if (!valid) continue;
+                    if (full) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = drafted ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+                        uint16_t* const dst = p.out + row * kD + cc * 32;
+                        if (p.out32) {  // whole sectors
+                            st_global_v8(dst, *reinterpret_cast<const uint32_t(*)[8]>(w));
+                            st_global_v8(dst + 16, *reinterpret_cast<const uint32_t(*)[8]>(w + 8));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                reinterpret_cast<uint4*>(dst)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                        }
+                    } else if (l1 != 0.f) {
+                        float* const dst = p.part_o + part * kD + cc * 32;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            st_global_v8(dst + 8 * e, *reinterpret_cast<const uint32_t(*)[8]>(o + 8 * e));
+                    }
+                }
+                tc::fence_before_sync();
+            }
+            // O is read: the next piece's first P V may overwrite it
+            __syncwarp();
+            if (lane == 0) {
+                if (both || t == 0) mbar_arrive(bar(kOFree));
+                if (!both && t == 0) mbar_arrive(bar(kOFree));  // (for B's warp, which has nothing to read)
+                if (both) mbar_arrive(bar(kOFree + 1));
+            }
+            release(k);
+            return true;
+        };
         for (int k = 0;; ++k) {
             ok = take(k);
-            if (!ok || slot(k)->n == 0) break;
+            if (!ok) break;
             const int n = slot(k)->n, nk = (n + 1 - t) >> 1;  // this slot's tiles
+            if (n == 0) break;
             const int sc = slot(k)->before[t], S = slot(k)->S, first = S - p.L;
             const int m = slot(k)->mp * C + rank;  // query tile
             const int rows = p.R - m * BM;         // of which a tile has at most BM
             const bool busy = q4 * 32 < rows, valid = r < rows;
-            const int l = (m * BM + r) % p.L;  // draft
-            const uint32_t* const mask = p.mask + (static_cast<long long>(slot(k)->b) * p.L + l) * p.W;
+            const uint32_t* const mask =
+                p.mask + (static_cast<long long>(slot(k)->b) * p.L + static_cast<unsigned>(m * BM + r) % static_cast<unsigned>(p.L)) * p.W;
             float c = fmaxf(p.scale_log2, FLT_MIN);  // (scale 0: -inf stays -inf)
             if constexpr (Q4) {
                 // A takes the rows in place to f16, the largest value in [2^14, 2^15)
@@ -840,7 +951,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         }
                     };
                     // the tile's maximum from all of S; true where the row's moved
-                    auto maximum = [&](float slack) {
+                    auto maximum = [&]() {
 #pragma unroll
                         for (int cc = 0; cc < 4; ++cc) {
                             float x[32];
@@ -849,7 +960,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             largest(x, cc);
                         }
                         const float mt = mx * c;
-                        const bool grow = valid && mt > mrow + slack;  // (other rows hold anything)
+                        const bool grow = valid && mt > mrow;  // (other rows hold anything)
                         if (grow) {
                             alpha = fast_exp2(mrow - mt);  // 2^-inf = 0 at the start
                             mrow = mt;
@@ -873,13 +984,33 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         return true;
                     };
                     // P goes over the first 64 columns of this slot's S
-                    if constexpr (Q4) {
-                        // S is read twice, so that few registers do (the producers need them);
-                        // 32 keys' P lies over scores that are used up
-                        if (maximum(kSlack) && j > 0) {
+                    // Against the maximum so far: no weight waits for the scores behind it.  Only
+                    // where that was too low by 2^kSlack (or there was none) is the tile done
+                    // again, with its own maximum.
+                    uint32_t pw[64];
+                    bool again = true;
+                    if (j > 0) {
+                        const float mu = mrow == neg_inf() ? 0.f : mrow;
+                        constexpr int kLoads = Q4 ? 1 : 2;  // 32 columns each in flight (registers)
+                        float x[kLoads][32];
+                        if constexpr (kLoads > 1) tc::ld32(st, x[0]);
+#pragma unroll
+                        for (int cc = 0; cc < 4; ++cc) {
+                            if constexpr (kLoads == 1) tc::ld32(st + cc * 32, x[0]);
+                            tc::wait_ld();
+                            if (kLoads > 1 && cc < 3) tc::ld32(st + cc * 32 + 32, x[(cc + 1) & (kLoads - 1)]);
+                            largest(x[cc & (kLoads - 1)], cc);
+                            weights(x[cc & (kLoads - 1)], pw + 16 * cc, mu);
+                        }
+                        again = __any_sync(0xffffffffu, valid && mx * c > mrow + kSlack);
+                    }
+                    if (again) {
+                        mx = neg_inf();
+                        if (maximum() && j > 0) {
                             ok = rescale();
                             if (!ok) break;
                         }
+                        ts = make_float2(0.f, 0.f);
                         const float mu = mrow == neg_inf() ? 0.f : mrow;
 #pragma unroll
                         for (int cc = 0; cc < 4; ++cc) {
@@ -887,49 +1018,11 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             tc::ld32(st + cc * 32, x);
                             tc::wait_ld();
                             if (jt >= tail) largest(x, cc);
-                            uint32_t w[16];
-                            weights(x, w, mu);
-                            tc::st16(st + cc * 16, w);
+                            weights(x, pw + 16 * cc, mu);
                         }
-                    } else {
-                        // Against the maximum so far: no weight waits for the scores behind it.
-                        // Only where that was too low by 2^kSlack (or there was none) is the
-                        // tile done again, with its own maximum.
-                        uint32_t pw[64];
-                        bool again = true;
-                        if (j > 0) {
-                            const float mu = mrow == neg_inf() ? 0.f : mrow;
-                            float x[2][32];
-                            tc::ld32(st, x[0]);
-#pragma unroll
-                            for (int cc = 0; cc < 4; ++cc) {
-                                tc::wait_ld();
-                                if (cc < 3) tc::ld32(st + cc * 32 + 32, x[(cc + 1) & 1]);
-                                largest(x[cc & 1], cc);
-                                weights(x[cc & 1], pw + 16 * cc, mu);
-                            }
-                            again = __any_sync(0xffffffffu, valid && mx * c > mrow + kSlack);
-                        }
-                        if (again) {
-                            mx = neg_inf();
-                            if (maximum(0.f) && j > 0) {
-                                ok = rescale();
-                                if (!ok) break;
-                            }
-                            ts = make_float2(0.f, 0.f);
-                            const float mu = mrow == neg_inf() ? 0.f : mrow;
-#pragma unroll
-                            for (int cc = 0; cc < 4; ++cc) {
-                                float x[32];
-                                tc::ld32(st + cc * 32, x);
-                                tc::wait_ld();
-                                if (jt >= tail) largest(x, cc);
-                                weights(x, pw + 16 * cc, mu);
-                            }
-                        }
-                        tc::st32(st, *reinterpret_cast<const uint32_t(*)[32]>(pw));
-                        tc::st32(st + 32, *reinterpret_cast<const uint32_t(*)[32]>(pw + 32));
                     }
+                    tc::st32(st, *reinterpret_cast<const uint32_t(*)[32]>(pw));
+                    tc::st32(st + 32, *reinterpret_cast<const uint32_t(*)[32]>(pw + 32));
                     lsum.x = lsum.x * alpha + ts.x;
                     lsum.y = lsum.y * alpha + ts.y;
                     tc::wait_st();
@@ -939,92 +1032,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 if (lane == 0) mbar_arrive(bar(kPFull + t));
             }
             if (!ok || aborted(abort_flag)) break;
-            const volatile Item* const it = slot(k);
-            // The two slots' states of a row are joined by both warpgroups, 64 dims each (one
-            // tile: A has them all).
-            float l1 = lsum.x + lsum.y;
-            const bool both = n > 1;
-            float w0 = 1.f, w1 = 0.f;  // weights of O 0 and O 1
-            if (both) {
-                float2* const x = reinterpret_cast<float2*>(smem_raw + M.x) + r;
-                ok = xc == 0 || warp_wait(bar(kXFree), (xc - 1) & 1);  // (the last joined piece's are read)
-                if (!ok) break;
-                x[t * BM] = make_float2(mrow, l1);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kXFull));
-                ok = warp_wait(bar(kXFull), xc & 1);
-                if (!ok) break;
-                ++xc;
-                const float2 a = x[0], e = x[BM];
-                const float mm = fmaxf(a.y == 0.f ? neg_inf() : a.x, e.y == 0.f ? neg_inf() : e.x);
-                w0 = a.y == 0.f ? 0.f : fast_exp2(a.x - mm);
-                w1 = e.y == 0.f ? 0.f : fast_exp2(e.x - mm);
-                l1 = (a.y == 0.f ? 0.f : a.y * w0) + (e.y == 0.f ? 0.f : e.y * w1);
-                mrow = mm;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kXFree));
-                ok = warp_wait(bar(kODone), (it->before[0] + ((n + 1) >> 1) - 1) & 1) &&
-                     warp_wait(bar(kODone + 1), (it->before[1] + (n >> 1) - 1) & 1);
-                if (!ok) break;
-            } else if (t == 0) {
-                ok = warp_wait(bar(kODone), sc & 1);
-                if (!ok) break;
-            }
-            const bool full = it->n == it->ng;
-            // (a full piece has tail tiles)
-            const bool drafted = it->live[l >> 5] >> (l & 31) & 1u;
-            const long long row = (static_cast<long long>(it->b) * p.H_kv + it->kvh) * p.R + m * BM + r;
-            const long long part = (2ll * blockIdx.x + (it->j0 > 0 ? 0 : 1)) * BM + r;
-            if (!full && valid && t == 0) p.part_ml[part] = make_float2(mrow, l1);
-            if (busy && (both || t == 0)) {
-                tc::fence_after_sync();
-                const float inv = l1 == 0.f ? 0.f : 1.f / l1;
-                // 32 dims a step
-#pragma unroll 1
-                for (int cc = both ? 2 * t : 0; cc < (both ? 2 * t + 2 : 4); ++cc) {
-                    float o[32];
-                    __syncwarp();
-                    tc::ld32(trow + 256u + cc * 32, o);
-                    if (both) {
-                        float o2[32];
-                        tc::ld32(trow + 384u + cc * 32, o2);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + o2[e] * w1;
-                    } else {
-                        tc::wait_ld();
-                    }
-                    if (!valid) continue;
-                    if (full) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = drafted ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
-                        uint16_t* const dst = p.out + row * kD + cc * 32;
-                        if (p.out32) {  // whole sectors
-                            st_global_v8(dst, *reinterpret_cast<const uint32_t(*)[8]>(w));
-                            st_global_v8(dst + 16, *reinterpret_cast<const uint32_t(*)[8]>(w + 8));
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                reinterpret_cast<uint4*>(dst)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-                        }
-                    } else if (l1 != 0.f) {
-                        float* const dst = p.part_o + part * kD + cc * 32;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            st_global_v8(dst + 8 * e, *reinterpret_cast<const uint32_t(*)[8]>(o + 8 * e));
-                    }
-                }
-                tc::fence_before_sync();
-            }
-            // O is read: the next piece's first P V may overwrite it
-            __syncwarp();
-            if (lane == 0) {
-                if (both || t == 0) mbar_arrive(bar(kOFree));
-                if (!both && t == 0) mbar_arrive(bar(kOFree));  // (for B's warp, which has nothing to read)
-                if (both) mbar_arrive(bar(kOFree + 1));
-            }
-            release(k);
+            ok = finish(k, mrow, lsum.x + lsum.y);
+            if (!ok) break;
         }
         if (!ok && lane == 0) give_up(p, abort_flag);
     }
