@@ -28,12 +28,9 @@ struct TreeCall {
     cudaStream_t stream;
     DeviceInfo dev;
 };
-// On the tensor cores (bf16 queries), or on the CUDA cores.
-bool tree_tiles_supported(const pa_shape& sh);
-size_t tree_tiles_workspace_bytes(int sm_count);
-pa_status tree_tiles_launch(const TreeCall& c);
-size_t tree_rows_workspace_bytes(const pa_shape& sh, int sm_count);
-pa_status tree_rows_launch(const TreeCall& c);
+bool tree_supported(const pa_shape& sh);
+size_t tree_workspace_bytes(int sm_count);
+pa_status tree_launch(const TreeCall& c);
 
 pa_status tree_mask_launch(int B, int L, const int32_t* parents, uint32_t* mask, int32_t* depths, uint32_t* flag,
                            cudaStream_t stream);

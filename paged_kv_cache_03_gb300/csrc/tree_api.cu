@@ -21,16 +21,6 @@ pa_status device_ok(DeviceInfo* dev) {
 
 PoolBufs bufs(const pa_q4_pool& p) { return {{p.key_codes, p.value_codes, p.key_scales, p.value_scales}}; }
 
-// (a CTA per 8 rows or fewer; the tiles count key tiles in an int)
-bool tree_supported(const pa_shape& sh) {
-    return sh.L <= kTreeMax && static_cast<long long>(sh.B) * sh.H_q * sh.L < INT_MAX &&
-           (sh.dtype != PA_BF16 || tree_tiles_supported(sh));
-}
-
-size_t workspace_bytes(const pa_shape& sh, int sm_count) {
-    return sh.dtype == PA_BF16 ? tree_tiles_workspace_bytes(sm_count) : tree_rows_workspace_bytes(sh, sm_count);
-}
-
 pa_status attend(const pa_shape* shape, const void* query, const void* kc, const void* vc, const void* ks,
                  const void* vs, const int32_t* bt, const int32_t* ctx, const uint32_t* mask, float scale, void* out,
                  void* ws, size_t ws_bytes, void* stream) {
@@ -42,7 +32,7 @@ pa_status attend(const pa_shape* shape, const void* query, const void* kc, const
     TreeCall c;
     st = device_ok(&c.dev);
     if (st != PA_OK) return st;
-    if (ws_bytes < workspace_bytes(*shape, c.dev.sm_count)) return PA_ERR_WORKSPACE;
+    if (ws_bytes < tree_workspace_bytes(c.dev.sm_count)) return PA_ERR_WORKSPACE;
     c.sh = *shape;
     c.q = query;
     c.kc = kc;
@@ -57,7 +47,7 @@ pa_status attend(const pa_shape* shape, const void* query, const void* kc, const
     c.ws = ws;
     c.ws_bytes = ws_bytes;
     c.stream = static_cast<cudaStream_t>(stream);
-    return shape->dtype == PA_BF16 ? tree_tiles_launch(c) : tree_rows_launch(c);
+    return tree_launch(c);
 }
 
 pa_status compact(const pa_shape* shape, const PoolBufs& pool, const int32_t* bt, const int32_t* ctx, const int32_t* path,
@@ -105,7 +95,7 @@ pa_status pa_tree_mask(int B, int L, const int32_t* parents, uint32_t* mask, int
 size_t pa_tree_workspace_bytes(const pa_shape* shape) {
     DeviceInfo dev;
     if (check_shape(shape) != PA_OK || !tree_supported(*shape) || current_device_info(&dev) != PA_OK) return 0;
-    return workspace_bytes(*shape, dev.sm_count);
+    return tree_workspace_bytes(dev.sm_count);
 }
 
 pa_status pa_paged_attention_tree(const pa_shape* shape, const void* query, const void* key_pages,

@@ -62,7 +62,8 @@ enum Bar {
     kKEmpty = 9,    // + slot: in every CTA of the cluster
     kVFull = 12,    // + slot
     kVEmpty = 15,   // + slot
-    kVTail = 18,    // + slot: a tail tile's values are there, not yet cleaned
+    kVTail = 18,    // + slot: a tail tile's values are there, not yet cleaned (by TMA)
+    kVScale = 18,   // + t: the scales of V's rows are there (fp32 pages)
     kSFull = 21,    // + t
     kPFull = 23,    // + t
     kODone = 25,    // + t
@@ -72,34 +73,49 @@ enum Bar {
     kMmaDone = 31,
     kItemFull = 32    // + place, then kItemEmpty + place
 };
-enum Source { kTma, kCopy, kQ4 };
-// Warps: K/V producers (4 bit: four for K, four for V), then four of MMA and pieces, then
-// eight of softmax.
-constexpr int producers(Source s) { return s == kQ4 ? 8 : 4; }
+// bf16 queries: bf16 pages by TMA or by copies, 4-bit pages.  fp32 queries: fp32 pages,
+// 4-bit pages.
+enum Source { kTma, kCopy, kQ4, kF32, kQ4F };
+constexpr bool fp32(Source s) { return s >= kF32; }
+constexpr bool four_bit(Source s) { return s == kQ4 || s == kQ4F; }
+constexpr bool is_f16(Source s) { return s >= kQ4; }  // the products' operands
+// f16 parts of an operand: of Q (and P), of K and V.
+constexpr int q_parts(Source s) { return fp32(s) ? 2 : 1; }
+constexpr int kv_parts(Source s) { return s == kF32 ? 2 : 1; }
+// Warps: K/V producers (rows that are converted: four for K, four for V), then four of MMA
+// and pieces, then eight of softmax.
+constexpr int producers(Source s) { return is_f16(s) ? 8 : 4; }
 constexpr int threads(Source s) { return 32 * (producers(s) + 4 + 8); }
 // K and V tiles in the rings.  Three: with C = 2 a tile's time is below the latency of HBM.
-// 4-bit rows wait as they are, kRawStages tiles of them, and need the space for that.
-constexpr int slots(Source s) { return s == kQ4 ? 2 : 3; }
-constexpr int kRawStages = 3;
+// 4-bit rows wait as they are, raw_stages tiles of them, and need the space for that.
+constexpr int slots(Source s) { return s == kF32 ? 1 : is_f16(s) ? 2 : 3; }
+constexpr int raw_stages(Source s) { return s == kQ4 ? 3 : s == kQ4F ? 1 : 0; }
 // Published pieces: enough for producers that are that many tiles ahead, were each tile a
 // piece.
-constexpr int items(Source s) { return s == kQ4 ? 8 : 4; }
+constexpr int items(Source s) { return is_f16(s) ? 8 : 4; }
+// Registers of a thread by role: what setmaxnreg can share out, 512 x 128 or 640 x 96.
+struct Regs {
+    int producer, misc, softmax;
+};
+constexpr Regs regs(Source s) {
+    return !is_f16(s) ? Regs{72, 104, 168} : s == kF32 ? Regs{80, 64, 128} : Regs{64, 64, 144};
+}
 
 // Shared memory from a 1024-byte boundary (the attribute of smem_raw) on.  Q: one tile, or
 // two of at most 64 rows that the pieces take in turn.
 struct Smem {
-    int k, v, raw, bar, items, tmem, abort, x, q_scale, total;
+    int k, v, raw, bar, items, tmem, abort, x, q_scale, kv_scale, total;
 };
 constexpr int kItemBytes = 168;
 constexpr Smem smem(Source s) {
     Smem m{};
-    int at = kTile;
-    m.k = at;
-    at += slots(s) * kTile;
+    int at = q_parts(s) * kTile;
+    m.k = at;  // [slot][part]
+    at += slots(s) * kv_parts(s) * kTile;
     m.v = at;
-    at += slots(s) * kTile;
+    at += slots(s) * kv_parts(s) * kTile;
     m.raw = at;  // [producer warp][stage]
-    if (s == kQ4) at += 8 * kRawStages * kRawStage;
+    at += 8 * raw_stages(s) * kRawStage;
     m.bar = at;
     at += (kItemFull + 2 * items(s)) * 8;
     m.items = at;
@@ -109,27 +125,33 @@ constexpr Smem smem(Source s) {
     at += 16;
     m.x = at;  // [2][128] maximum and sum; before that the share and the scan's sums
     at += 2 * BM * 8;
-    m.q_scale = at;  // 4 bit: [2][128] the inverse of a row's scale
-    if (s == kQ4) at += 2 * BM * 4;
+    m.q_scale = at;  // f16: [2][128] the inverse of a row's scale
+    if (is_f16(s)) at += 2 * BM * 4;
+    m.kv_scale = at;  // fp32 pages, of 8 keys each: [4][16] K's inverse scale, [2][16] V's scale
+    if (s == kF32) at += (4 + 2) * 16 * 4;
     m.total = at;
     return m;
 }
-static_assert(smem(kTma).total <= 232448 && smem(kQ4).total <= 232448, "227 KB");
-static_assert(smem(kQ4).raw % 16 == 0 && smem(kTma).bar % 8 == 0 && smem(kTma).x % 8 == 0, "alignment");
+static_assert(smem(kTma).total <= 232448 && smem(kQ4).total <= 232448 && smem(kF32).total <= 232448 &&
+                  smem(kQ4F).total <= 232448,
+              "227 KB");
+static_assert(smem(kQ4).raw % 16 == 0 && smem(kQ4F).raw % 16 == 0 && smem(kTma).x % 8 == 0 && smem(kF32).kv_scale % 16 == 0,
+              "alignment");
 
 struct TileParams {
-    const uint8_t *kc, *ks, *vc, *vs;  // codes or bf16 rows, scales
+    const uint8_t *kc, *ks, *vc, *vs;  // codes or rows, scales
+    const float* q;                    // fp32 queries
     const int32_t* bt;
     const int32_t* ctx;
     const uint32_t* mask;
-    uint16_t* out;
+    void* out;
     uint32_t* flag;
     float2* part_ml;  // [2 per CTA][128]: max, sum
     float* part_o;    // [2 per CTA][128][D]
     int4* split;      // per share: the segment that starts in it and ends in a later one
     int B, H_kv, R, L, W, nG, num_pages, ps, max_npg;  // nG: groups of C query tiles
     int pool_rows, box;          // rows of the pool, of a K/V box
-    int q_box, q_half, q_bufs;   // rows of a query box, bytes of 64 dims of them, buffers
+    int q_box, q_half, q_bufs;   // rows of a query box, bytes of 64 dims of a buffer, buffers
     long long max_S;
     float scale_log2;
     int out32;  // the output is 32-byte aligned
@@ -182,6 +204,12 @@ constexpr uint32_t idesc(bool f16, int a_mn, int b_mn) {
     return tc::idesc_bf16(BM, BN, a_mn, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+// k of 2^k (a normal number).
+__device__ __forceinline__ float exponent_of(float x) { return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127); }
+
 template <int N>
 __device__ __forceinline__ void reg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -196,8 +224,9 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     tree_tile_kernel(const TileParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
     static_assert(C == 1 || SRC == kTma, "only TMA multicasts");
-    constexpr bool Q4 = SRC == kQ4;
+    constexpr bool F16 = is_f16(SRC), F32 = fp32(SRC);
     constexpr int kThreads = threads(SRC), kProd = producers(SRC), N = slots(SRC), I = items(SRC);
+    constexpr int QP = q_parts(SRC), VP = kv_parts(SRC), kRing = VP * kTile;
     constexpr int kItemEmpty = kItemFull + I;
     constexpr Smem M = smem(SRC);
     // Tiles behind TMA: [8 rows][64-dim half][row][128 bytes], as boxes of rows come; else
@@ -234,7 +263,11 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             mbar_init(bar(kKEmpty + s), C);
             mbar_init(bar(kVFull + s), SRC == kTma ? 1 : 4);
             mbar_init(bar(kVEmpty + s), C);
-            mbar_init(bar(kVTail + s), 1);
+            if (SRC == kTma) mbar_init(bar(kVTail + s), 1);
+        }
+        if (SRC == kF32) {
+            mbar_init(bar(kVScale), 4);
+            mbar_init(bar(kVScale + 1), 4);
         }
         mbar_init(bar(kMmaDone), 1);
         for (int s = 0; s < I; ++s) {
@@ -295,8 +328,9 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             if (seq_len(p, b) > 0) continue;
             if (tid == 0) atomicOr(p.flag, PA_FLAG_BAD_CONTEXT);
             const long long rows = static_cast<long long>(p.H_kv) * p.R;
-            uint4* const o = reinterpret_cast<uint4*>(p.out + b * rows * kD);
-            for (long long i = tid; i < rows * (kD / 8); i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            constexpr int kVecs = F32 ? kD / 4 : kD / 8;  // 16 bytes each
+            uint4* const o = static_cast<uint4*>(p.out) + b * rows * kVecs;
+            for (long long i = tid; i < rows * kVecs; i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
     tc::fence_before_sync();
@@ -335,7 +369,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
 
     if (warp < kProd) {
         // ========================= K/V producers ==================================
-        reg_dec<Q4 ? 64 : 72>();
+        reg_dec<regs(SRC).producer>();
         bool ok = true;
         if constexpr (SRC == kTma) {
             if (warp == 0) {
@@ -476,7 +510,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 if (more) lookup(k, j);
             };
             Ring<N> g;
-            if constexpr (Q4) {
+            if constexpr (four_bit(SRC)) {
+                constexpr int kRawStages = raw_stages(SRC);
                 // Warps 0-3 dequantise K, 4-7 V.  A tile's 4-bit rows are copied to the warp's
                 // staging kRawStages tiles ahead.
                 const bool is_v = warp >= 4;
@@ -511,6 +546,80 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     r.next();
                 }
                 cp_async_wait<0>();
+            } else if constexpr (SRC == kF32) {
+                // Warps 0-3 bring K, 4-7 V: warp w rows 32 i + 8 w .., the next 8 on their way.
+                // Each 8 rows are taken by a power of two so that their largest value lies in
+                // [2^14, 2^15), and stored in two f16 parts: all but 2^-22 of a value, or 2^-40 of
+                // the 8 rows' largest.  Scores are scaled back by key, V's scale goes into P.
+                const bool is_v = warp >= 4;
+                const int w = warp & 3;
+                const float* const pool = reinterpret_cast<const float*>(is_v ? p.vc : p.kc);
+                const uint32_t ring = base + (is_v ? M.v : M.k);
+                const int full = is_v ? kVFull : kKFull, empty = is_v ? kVEmpty : kKEmpty;
+                float* const scales = reinterpret_cast<float*>(smem_raw + M.kv_scale) + (is_v ? 64 : 0);
+                const int r8 = lane >> 2, l4 = lane & 3;  // row of 8, dims 16 q + 4 l4 ..
+                auto load = [&](float4 (&v)[8], int rows, int i) {
+                    const int row = __shfl_sync(0xffffffffu, rows, 8 * i + r8);
+                    const float4* const src = reinterpret_cast<const float4*>(pool + (row < 0 ? 0 : static_cast<long long>(row) * kD)) + l4;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] = row < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcs(src + 4 * q);
+                };
+                float last_up = 1.f;
+                auto store = [&](const float4 (&v)[8], int i, int at16) {
+                    float mx = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) mx = fmax3(fmax3(mx, fabsf(v[q].x), fabsf(v[q].y)), fabsf(v[q].z), fabsf(v[q].w));
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    float up, down;
+                    f16_scale(mx, up, down);
+                    if (is_v) {
+                        up = fminf(up, 1.2676506e30f);  // 2^100: what P 2^v adds up to stays a number
+                        if (mx == 0.f) up = last_up;    // (any will do; one like the others' keeps P in range)
+                        last_up = up;
+                    }
+                    if (lane == 0) scales[at16 * 16 + 4 * i + w] = is_v ? up : down;
+                    const uint32_t at = ring + (32 * i + 8 * w + r8) * 128 + (l4 & 1) * 8;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float x[4] = {v[q].x * up, v[q].y * up, v[q].z * up, v[q].w * up};
+                        float hi[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) hi[e] = __uint_as_float(__float_as_uint(x[e]) & 0xffffe000u);
+                        const int c = (4 * q + l4) >> 1;  // chunk of 8 dims
+                        const uint32_t to = at + (c >> 3) * kHalf + (((c & 7) ^ r8) << 4);
+                        sts64(to, pack_f16x2(hi[0], hi[1]), pack_f16x2(hi[2], hi[3]));
+                        sts64(to + kTile, pack_f16x2(x[0] - hi[0], x[1] - hi[1]), pack_f16x2(x[2] - hi[2], x[3] - hi[3]));
+                    }
+                };
+                float4 a[8], b[8];
+                int rows = -1, tile = 0;
+                if (more) {
+                    rows = rows_of();
+                    load(a, rows, 0);
+                }
+                while (more) {
+                    const int t = (j - slot(k)->j0) & 1, at16 = is_v ? t : tile & 3;  // where its scales go
+                    next();  // (the tile after: its page ids are on their way)
+                    if (!ok) break;
+                    load(b, rows, 1);
+                    ok = warp_wait(bar(empty + g.s), g.phase ^ 1u);
+                    if (!ok || aborted(abort_flag)) break;
+                    store(a, 0, at16);
+                    load(a, rows, 2);
+                    store(b, 1, at16);
+                    load(b, rows, 3);
+                    store(a, 2, at16);
+                    if (more) {
+                        rows = rows_of();
+                        load(a, rows, 0);
+                    }
+                    store(b, 3, at16);
+                    announce(full + g.s);
+                    if (is_v && lane == 0) mbar_arrive(bar(kVScale + t));
+                    ++tile;
+                    g.next();
+                }
             } else {
                 // K and V of a tile are one group of copies; a tile is announced when the next
                 // one is requested.
@@ -546,12 +655,12 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         }
         if (!ok && lane == 0) give_up(p, abort_flag);
     } else if (warp < kProd + 4) {
-        reg_dec<Q4 ? 64 : 104>();
+        reg_dec<regs(SRC).misc>();
         if (warp == kProd) {
             // =========================== MMA issuer ===============================
             // The whole warp runs the loop and one elected lane issues.
-            constexpr uint32_t idS = idesc(Q4, 0, 0);  // Q, K both K-major
-            constexpr uint32_t idO = idesc(Q4, 0, 1);  // P K-major, V MN-major
+            constexpr uint32_t idS = idesc(F16, 0, 0);  // Q, K both K-major
+            constexpr uint32_t idO = idesc(F16, 0, 1);  // P K-major, V MN-major
             const uint64_t dQ0 = tc::smem_desc_sw128(base, 16, 1024);
             const uint64_t dK0 = tc::smem_desc_sw128(base + M.k, 16, kGroup);
             const uint64_t dV0 = tc::smem_desc_sw128(base + M.v, kHalf, kGroup);
@@ -566,18 +675,27 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 release(k);
                 if (n == 0) break;
                 const int buf = q_buf(k);
-                const uint64_t dq0 = tc::desc_advance(dQ0, buf * (kTile / 2)), dq1 = tc::desc_advance(dq0, p.q_half);
+                const uint64_t dq0 = tc::desc_advance(dQ0, buf * (QP * kTile / 2)), dq1 = tc::desc_advance(dq0, p.q_half);
                 auto qk = [&](int i) {  // Q K^T of the piece's tile i
                     if (!warp_wait(bar(kKFull + kr.s), kr.phase)) return false;
                     tc::fence_after_sync();
-                    const uint64_t dk = tc::desc_advance(dK0, kr.s * kTile);
+                    const uint64_t dk = tc::desc_advance(dK0, kr.s * kRing);
                     const uint32_t d = tmem + 128u * (i & 1);
                     if (leader) {
-                        tc::mma_bf16_c<0>(d, dq0, dk, idS);
+                        // the products of the parts, the smallest first (low x low is left out)
 #pragma unroll
-                        for (int kk = 1; kk < kD / 16; ++kk)
-                            tc::mma_bf16_c<1>(d, tc::desc_advance(kk < 4 ? dq0 : dq1, (kk & 3) * 32),
-                                              tc::desc_advance(dk, (kk >> 2) * kHalf + (kk & 3) * 32), idS);
+                        for (int part = QP + VP - 2; part >= 0; --part) {
+                            const uint64_t qa = part == 1 ? tc::desc_advance(dq0, 2 * p.q_half) : dq0;
+                            const uint64_t qb = part == 1 ? tc::desc_advance(dq1, 2 * p.q_half) : dq1;
+                            const uint64_t ka = part == 2 ? tc::desc_advance(dk, kTile) : dk;
+#pragma unroll
+                            for (int kk = 0; kk < kD / 16; ++kk) {
+                                const uint64_t x = tc::desc_advance(kk < 4 ? qa : qb, (kk & 3) * 32);
+                                const uint64_t y = tc::desc_advance(ka, (kk >> 2) * kHalf + (kk & 3) * 32);
+                                if (kk == 0 && part == QP + VP - 2) tc::mma_bf16_c<0>(d, x, y, idS);
+                                else tc::mma_bf16_c<1>(d, x, y, idS);
+                            }
+                        }
                         tc::commit(bar(kSFull + (i & 1)));
                         if constexpr (C == 1) tc::commit(bar(kKEmpty + kr.s));
                         else tc::commit_multicast(bar(kKEmpty + kr.s), kAll);
@@ -587,7 +705,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     kr.next();
                     return true;
                 };
-                ok = warp_wait(bar((Q4 ? kQReady : kQFull) + buf), q_use(k) & 1);
+                ok = warp_wait(bar((F16 ? kQReady : kQFull) + buf), q_use(k) & 1);
                 if (!ok) break;
                 ok = qk(0) && (n < 2 || qk(1));
                 for (int i = 0; ok && i < n; ++i) {
@@ -597,13 +715,22 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     if (ok && i < 2 && oe > 0) ok = warp_wait(bar(kOFree + t), (oe - 1) & 1);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const uint64_t dv = tc::desc_advance(dV0, vr.s * kTile);
+                    const uint64_t dv = tc::desc_advance(dV0, vr.s * kRing);
                     const uint32_t d = tmem + 256u + 128u * t, a = tmem + 128u * t;
                     if (leader) {
-                        tc::mma_bf16_ts(d, a, dv, idO, i >= 2);
 #pragma unroll
-                        for (int kk = 1; kk < BN / 16; ++kk)
-                            tc::mma_bf16_ts_c<1>(d, a + kk * 8, tc::desc_advance(dv, kk * 2 * kGroup), idO);
+                        for (int part = QP + VP - 2; part >= 0; --part) {
+                            // two parts of P: 16 columns of each for 32 keys
+                            const uint32_t pa = a + (part == 1 ? 16u : 0u);
+                            const uint64_t va = part == 2 ? tc::desc_advance(dv, kTile) : dv;
+#pragma unroll
+                            for (int kk = 0; kk < BN / 16; ++kk) {
+                                const uint32_t x = pa + (QP == 1 ? kk * 8 : (kk >> 1) * 32 + (kk & 1) * 8);
+                                const uint64_t y = tc::desc_advance(va, kk * 2 * kGroup);
+                                if (kk == 0 && part == QP + VP - 2) tc::mma_bf16_ts(d, x, y, idO, i >= 2);
+                                else tc::mma_bf16_ts_c<1>(d, x, y, idO);
+                            }
+                        }
                         tc::commit(bar(kODone + t));
                         if constexpr (C == 1) tc::commit(bar(kVEmpty + vr.s));
                         else tc::commit_multicast(bar(kVEmpty + vr.s), kAll);
@@ -632,6 +759,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 const int buf = q_buf(k), use = q_use(k), m = slot(k)->mp * C + rank;
                 const int row = (slot(k)->b * p.H_kv + slot(k)->kvh) * p.R + m * BM;
                 release(k);
+                if constexpr (F32) continue;  // (the softmax warps load them)
                 ok = use == 0 || warp_wait(bar(kQEmpty + buf), (use - 1) & 1);
                 if (!ok || aborted(abort_flag)) break;
                 if (lane == 0) {
@@ -741,12 +869,12 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         __syncwarp();
     } else {
         // ============================== softmax =======================================
-        reg_inc<Q4 ? 144 : 168>();
+        reg_inc<regs(SRC).softmax>();
         const int t = (warp - kProd - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;  // slot, lane quarter, row
         const uint32_t trow = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         // How far (log2) a row's scores may rise above its maximum before O is rescaled:
         // bf16 weights and fp32 sums have the exponents for it, f16 ends at 2^16.
-        constexpr float kSlack = Q4 ? 8.f : 64.f;
+        constexpr float kSlack = F16 ? 8.f : 64.f;
         int xc = 0;  // pieces whose states were joined
         bool ok = true;
         // The end of piece k, with this slot's maximum and sum.  The two slots' states of a row are joined by both warpgroups,
@@ -808,11 +936,18 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         tc::wait_ld();
                     }
                     if (!valid) continue;
-                    if (full) {
+                    if (F32 && full) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = drafted ? o[e] * inv : 0.f;
+                        float* const dst = static_cast<float*>(p.out) + row * kD + cc * 32;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            reinterpret_cast<float4*>(dst)[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else if (full) {
                         uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) w[e] = drafted ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
-                        uint16_t* const dst = p.out + row * kD + cc * 32;
+                        uint16_t* const dst = static_cast<uint16_t*>(p.out) + row * kD + cc * 32;
                         if (p.out32) {  // whole sectors
                             st_global_v8(dst, *reinterpret_cast<const uint32_t(*)[8]>(w));
                             st_global_v8(dst + 16, *reinterpret_cast<const uint32_t(*)[8]>(w + 8));
@@ -852,38 +987,73 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             const uint32_t* const mask =
                 p.mask + (static_cast<long long>(slot(k)->b) * p.L + static_cast<unsigned>(m * BM + r) % static_cast<unsigned>(p.L)) * p.W;
             float c = fmaxf(p.scale_log2, FLT_MIN);  // (scale 0: -inf stays -inf)
-            if constexpr (Q4) {
-                // A takes the rows in place to f16, the largest value in [2^14, 2^15)
+            if constexpr (F16) {
+                // A takes the rows to f16 (fp32: two parts), the largest value in [2^14, 2^15):
+                // 16-bit rows in place, fp32 rows from global memory, read twice
                 const int buf = q_buf(k);
                 float* const down = reinterpret_cast<float*>(smem_raw + M.q_scale) + buf * BM + r;
                 if (t == 0) {
-                    ok = warp_wait(bar(kQFull + buf), q_use(k) & 1);
-                    if (!ok) break;
-                    const uint32_t qrow = base + buf * (kTile / 2);
-                    if (busy) {
-                        uint4 v[16];
-                        float mx = 0.f;
+                    const uint32_t qrow = base + buf * (QP * kTile / 2);
+                    if constexpr (F32) {
+                        // (the products of the last piece in the buffer are done)
+                        ok = q_use(k) == 0 || warp_wait(bar(kQEmpty + buf), (q_use(k) - 1) & 1);
+                        if (!ok) break;
+                        if (busy) {
+                            const long long row = (static_cast<long long>(slot(k)->b) * p.H_kv + slot(k)->kvh) * p.R + m * BM + r;
+                            const float4* const src = reinterpret_cast<const float4*>(p.q + (valid ? row : 0) * kD);
+                            float mx = 0.f;
+#pragma unroll 8
+                            for (int i = 0; i < kD / 4; ++i) {
+                                const float4 v = __ldg(src + i);
+                                mx = fmax3(fmax3(mx, fabsf(v.x), fabsf(v.y)), fabsf(v.z), fabsf(v.w));
+                            }
+                            float up, dn;
+                            f16_scale(mx, up, dn);
+#pragma unroll 4
+                            for (int c = 0; c < 16; ++c) {
+                                const float4 v[2] = {__ldg(src + 2 * c), __ldg(src + 2 * c + 1)};
+                                const float x[8] = {v[0].x * up, v[0].y * up, v[0].z * up, v[0].w * up,
+                                                    v[1].x * up, v[1].y * up, v[1].z * up, v[1].w * up};
+                                float hi[8];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
-                                         : "r"(qrow + (c >> 3) * p.q_half + sw128(r, c & 7)));
-                            const float2 f[4] = {bf16x2_to_float2(v[c].x), bf16x2_to_float2(v[c].y),
-                                                 bf16x2_to_float2(v[c].z), bf16x2_to_float2(v[c].w)};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) mx = fmax3(mx, fabsf(f[e].x), fabsf(f[e].y));
+                                for (int e = 0; e < 8; ++e) hi[e] = __uint_as_float(__float_as_uint(x[e]) & 0xffffe000u);
+                                const uint32_t at = qrow + (c >> 3) * p.q_half + sw128(r, c & 7);
+                                sts128(at, pack_f16x2(hi[0], hi[1]), pack_f16x2(hi[2], hi[3]), pack_f16x2(hi[4], hi[5]),
+                                       pack_f16x2(hi[6], hi[7]));
+                                sts128(at + 2 * p.q_half, pack_f16x2(x[0] - hi[0], x[1] - hi[1]),
+                                       pack_f16x2(x[2] - hi[2], x[3] - hi[3]), pack_f16x2(x[4] - hi[4], x[5] - hi[5]),
+                                       pack_f16x2(x[6] - hi[6], x[7] - hi[7]));
+                            }
+                            *down = dn;
                         }
-                        float up, dn;
-                        f16_scale(mx, up, dn);
+                    } else {
+                        ok = warp_wait(bar(kQFull + buf), q_use(k) & 1);
+                        if (!ok) break;
+                        if (busy) {
+                            uint4 v[16];
+                            float mx = 0.f;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const float2 f[4] = {bf16x2_to_float2(v[c].x), bf16x2_to_float2(v[c].y),
-                                                 bf16x2_to_float2(v[c].z), bf16x2_to_float2(v[c].w)};
-                            sts128(qrow + (c >> 3) * p.q_half + sw128(r, c & 7), pack_f16x2(f[0].x * up, f[0].y * up),
-                                   pack_f16x2(f[1].x * up, f[1].y * up), pack_f16x2(f[2].x * up, f[2].y * up),
-                                   pack_f16x2(f[3].x * up, f[3].y * up));
+                            for (int c = 0; c < 16; ++c) {
+                                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
+                                             : "r"(qrow + (c >> 3) * p.q_half + sw128(r, c & 7)));
+                                const float2 f[4] = {bf16x2_to_float2(v[c].x), bf16x2_to_float2(v[c].y),
+                                                     bf16x2_to_float2(v[c].z), bf16x2_to_float2(v[c].w)};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) mx = fmax3(mx, fabsf(f[e].x), fabsf(f[e].y));
+                            }
+                            float up, dn;
+                            f16_scale(mx, up, dn);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                const float2 f[4] = {bf16x2_to_float2(v[c].x), bf16x2_to_float2(v[c].y),
+                                                     bf16x2_to_float2(v[c].z), bf16x2_to_float2(v[c].w)};
+                                sts128(qrow + (c >> 3) * p.q_half + sw128(r, c & 7), pack_f16x2(f[0].x * up, f[0].y * up),
+                                       pack_f16x2(f[1].x * up, f[1].y * up), pack_f16x2(f[2].x * up, f[2].y * up),
+                                       pack_f16x2(f[3].x * up, f[3].y * up));
+                            }
+                            *down = dn;
                         }
-                        *down = dn;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -910,7 +1080,11 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 }
                 ok = warp_wait(bar(kSFull + t), (sc + j) & 1);
                 if (!ok || aborted(abort_flag)) break;
-                if constexpr (Q4) {
+                if constexpr (SRC == kF32) {  // the scales of this tile's V
+                    ok = warp_wait(bar(kVScale + t), (sc + j) & 1);
+                    if (!ok) break;
+                }
+                if constexpr (F16) {
                     if (j == 0) {  // (S is there, so this use of the buffer was announced, and none after it)
                         const int buf = q_buf(k);
                         ok = warp_wait(bar(kQReady + buf), q_use(k) & 1);
@@ -946,8 +1120,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         for (int i = 0; i < 16; ++i) {
                             const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), c2, nm2);
                             const float2 ex = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                            w[i] = Q4 ? pack_f16x2(ex.x, ex.y) : pack_bf16x2(ex.x, ex.y);
-                            ts = __fadd2_rn(ts, Q4 ? ex : bf16x2_to_float2(w[i]));
+                            w[i] = F16 ? pack_f16x2(ex.x, ex.y) : pack_bf16x2(ex.x, ex.y);
+                            ts = __fadd2_rn(ts, F16 ? ex : bf16x2_to_float2(w[i]));
                         }
                     };
                     // the tile's maximum from all of S; true where the row's moved
@@ -984,45 +1158,114 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         return true;
                     };
                     // P goes over the first 64 columns of this slot's S
-                    // Against the maximum so far: no weight waits for the scores behind it.  Only
-                    // where that was too low by 2^kSlack (or there was none) is the tile done
-                    // again, with its own maximum.
-                    uint32_t pw[64];
-                    bool again = true;
-                    if (j > 0) {
-                        const float mu = mrow == neg_inf() ? 0.f : mrow;
-                        constexpr int kLoads = Q4 ? 1 : 2;  // 32 columns each in flight (registers)
-                        float x[kLoads][32];
-                        if constexpr (kLoads > 1) tc::ld32(st, x[0]);
+                    if constexpr (F32) {
+                        // Two parts of P do not fit the registers beside S: S is read twice, and 32
+                        // keys' P lies over their own scores.  fp32 pages: V's rows were scaled by
+                        // 2^v (by eights), so P is 2^(score - v - maximum), the maximum that of score
+                        // - v, and the sum adds P 2^v: the weights relative to that maximum.
+                        const float4* const scales = reinterpret_cast<const float4*>(smem_raw + M.kv_scale);
+                        const int tile = slot(k)->before[0] + slot(k)->before[1] + 2 * j + t;
+                        auto scores = [&](float (&x)[32], int cc, float4& vs) {
+                            tc::ld32(st + cc * 32, x);
+                            float kf[4] = {c, c, c, c}, off[4] = {0.f, 0.f, 0.f, 0.f};
+                            if constexpr (SRC == kF32) {
+                                const float4 ks = scales[(tile & 3) * 4 + cc];
+                                vs = scales[16 + t * 4 + cc];
+                                kf[0] = c * ks.x, kf[1] = c * ks.y, kf[2] = c * ks.z, kf[3] = c * ks.w;
+                                // (a power of two: its exponent)
+                                off[0] = exponent_of(vs.x), off[1] = exponent_of(vs.y), off[2] = exponent_of(vs.z),
+                                off[3] = exponent_of(vs.w);
+                            }
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], kf[e >> 3], -off[e >> 3]);
+                            if (jt >= tail) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(see[cc] >> e & 1u)) x[e] = neg_inf();
+                            }
+                        };
+                        float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
 #pragma unroll
                         for (int cc = 0; cc < 4; ++cc) {
-                            if constexpr (kLoads == 1) tc::ld32(st + cc * 32, x[0]);
-                            tc::wait_ld();
-                            if (kLoads > 1 && cc < 3) tc::ld32(st + cc * 32 + 32, x[(cc + 1) & (kLoads - 1)]);
-                            largest(x[cc & (kLoads - 1)], cc);
-                            weights(x[cc & (kLoads - 1)], pw + 16 * cc, mu);
+                            float x[32];
+                            scores(x, cc, vs);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
                         }
-                        again = __any_sync(0xffffffffu, valid && mx * c > mrow + kSlack);
-                    }
-                    if (again) {
-                        mx = neg_inf();
-                        if (maximum() && j > 0) {
+                        const bool grow = valid && mx > mrow + kSlack;
+                        if (grow) {
+                            alpha = fast_exp2(mrow - mx);  // 2^-inf = 0 at the start
+                            mrow = mx;
+                        }
+                        if (__any_sync(0xffffffffu, grow) && j > 0) {
                             ok = rescale();
                             if (!ok) break;
                         }
-                        ts = make_float2(0.f, 0.f);
                         const float mu = mrow == neg_inf() ? 0.f : mrow;
 #pragma unroll
                         for (int cc = 0; cc < 4; ++cc) {
                             float x[32];
-                            tc::ld32(st + cc * 32, x);
-                            tc::wait_ld();
-                            if (jt >= tail) largest(x, cc);
-                            weights(x, pw + 16 * cc, mu);
+                            scores(x, cc, vs);
+                            const float back[4] = {vs.x, vs.y, vs.z, vs.w};
+                            uint32_t w[32];  // 16 of the high parts, 16 of the low ones
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 ex = make_float2(fast_exp2(x[2 * i] - mu), fast_exp2(x[2 * i + 1] - mu));
+                                const float2 hi = make_float2(__uint_as_float(__float_as_uint(ex.x) & 0xffffe000u),
+                                                              __uint_as_float(__float_as_uint(ex.y) & 0xffffe000u));
+                                w[i] = pack_f16x2(hi.x, hi.y);
+                                w[16 + i] = pack_f16x2(ex.x - hi.x, ex.y - hi.y);
+                                if constexpr (SRC == kF32) {
+                                    ts.x = fmaf(ex.x, back[i >> 2], ts.x);
+                                    ts.y = fmaf(ex.y, back[i >> 2], ts.y);
+                                } else {
+                                    ts = __fadd2_rn(ts, ex);
+                                }
+                            }
+                            tc::st32(st + cc * 32, w);
                         }
+                    } else {
+                        // Against the maximum so far: no weight waits for the scores behind it.  Only
+                        // where that was too low by 2^kSlack (or there was none) is the tile done
+                        // again, with its own maximum.
+                        uint32_t pw[64];
+                        bool again = true;
+                        if (j > 0) {
+                            const float mu = mrow == neg_inf() ? 0.f : mrow;
+                            constexpr int kLoads = F16 ? 1 : 2;  // 32 columns each in flight (registers)
+                            float x[kLoads][32];
+                            if constexpr (kLoads > 1) tc::ld32(st, x[0]);
+#pragma unroll
+                            for (int cc = 0; cc < 4; ++cc) {
+                                if constexpr (kLoads == 1) tc::ld32(st + cc * 32, x[0]);
+                                tc::wait_ld();
+                                if (kLoads > 1 && cc < 3) tc::ld32(st + cc * 32 + 32, x[(cc + 1) & (kLoads - 1)]);
+                                largest(x[cc & (kLoads - 1)], cc);
+                                weights(x[cc & (kLoads - 1)], pw + 16 * cc, mu);
+                            }
+                            again = __any_sync(0xffffffffu, valid && mx * c > mrow + kSlack);
+                        }
+                        if (again) {
+                            mx = neg_inf();
+                            if (maximum() && j > 0) {
+                                ok = rescale();
+                                if (!ok) break;
+                            }
+                            ts = make_float2(0.f, 0.f);
+                            const float mu = mrow == neg_inf() ? 0.f : mrow;
+#pragma unroll
+                            for (int cc = 0; cc < 4; ++cc) {
+                                float x[32];
+                                tc::ld32(st + cc * 32, x);
+                                tc::wait_ld();
+                                if (jt >= tail) largest(x, cc);
+                                weights(x, pw + 16 * cc, mu);
+                            }
+                        }
+                        tc::st32(st, *reinterpret_cast<const uint32_t(*)[32]>(pw));
+                        tc::st32(st + 32, *reinterpret_cast<const uint32_t(*)[32]>(pw + 32));
                     }
-                    tc::st32(st, *reinterpret_cast<const uint32_t(*)[32]>(pw));
-                    tc::st32(st + 32, *reinterpret_cast<const uint32_t(*)[32]>(pw + 32));
                     lsum.x = lsum.x * alpha + ts.x;
                     lsum.y = lsum.y * alpha + ts.y;
                     tc::wait_st();
@@ -1052,6 +1295,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
 // 32 y .. of the segment that starts in share c, four a warp, two partial states of each in
 // flight.  C: CTAs of a share, one query tile each.
 constexpr int kMergeRows = 4;
+template <bool F32>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TileParams p, int ny, int C) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = static_cast<int>(blockIdx.x) / ny;
@@ -1106,9 +1350,13 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TileParams p, int
         if (in_head + i >= p.R) continue;
         const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];  // (0: a row without keys; NaN stays)
         const long long row = (static_cast<long long>(sp.x) * p.H_kv + sp.y) * p.R + in_head + i;
-        uint2 w = make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
-        if (!live) w = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2*>(p.out + row * kD + 4 * lane) = w;
+        float4 o = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+        if (!live) o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (F32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kD + 4 * lane) = o;
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kD + 4 * lane) =
+                make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     }
 }
 
@@ -1196,19 +1444,19 @@ int gcd_int(int a, int b) {
 
 }  // namespace
 
-bool tree_tiles_supported(const pa_shape& sh) {
+bool tree_supported(const pa_shape& sh) {
+    if (sh.L > kTreeMax || static_cast<long long>(sh.B) * sh.H_q * sh.L >= INT_MAX) return false;
     const long long R = static_cast<long long>(sh.H_q / sh.H_kv) * sh.L;
     const long long cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     // costs are counted in an int
-    return sh.dtype == PA_BF16 &&
-           static_cast<long long>(sh.B) * sh.H_kv * ((R + BM - 1) / BM) * (cap / BN + 1 + kSegCost) < INT_MAX / 2;
+    return static_cast<long long>(sh.B) * sh.H_kv * ((R + BM - 1) / BM) * (cap / BN + 1 + kSegCost) < INT_MAX / 2;
 }
 
-size_t tree_tiles_workspace_bytes(int sm_count) { return plan(sm_count).total; }
+size_t tree_workspace_bytes(int sm_count) { return plan(sm_count).total; }
 
-pa_status tree_tiles_launch(const TreeCall& c) {
+pa_status tree_launch(const TreeCall& c) {
     const pa_shape& sh = c.sh;
-    if (c.dev.smem_optin < smem(kTma).total || c.dev.smem_optin < smem(kQ4).total) return PA_ERR_UNSUPPORTED;
+    if (c.dev.smem_optin < 232448) return PA_ERR_UNSUPPORTED;
     const TilePlan t = plan(c.dev.sm_count);
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
     TileParams p;
@@ -1219,7 +1467,8 @@ pa_status tree_tiles_launch(const TreeCall& c) {
     p.bt = c.bt;
     p.ctx = c.ctx;
     p.mask = c.mask;
-    p.out = static_cast<uint16_t*>(c.out);
+    p.q = static_cast<const float*>(c.q);
+    p.out = c.out;
     p.flag = reinterpret_cast<uint32_t*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + t.ml_off);
     p.part_o = reinterpret_cast<float*>(ws + t.o_off);
@@ -1236,26 +1485,29 @@ pa_status tree_tiles_launch(const TreeCall& c) {
     p.q_box = std::min(BM, (p.R + 7) / 8 * 8);
     p.q_bufs = p.q_box <= BM / 2 ? 2 : 1;
     p.q_half = kTile / 2 / p.q_bufs;
+    const bool f32 = sh.dtype == PA_F32;
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     p.scale_log2 = c.scale * 1.4426950408889634f;
     p.out32 = reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
-    const bool tma = !c.ks && sh.page_size % 8 == 0;
+    const bool tma = !f32 && !c.ks && sh.page_size % 8 == 0;
     const int nM = (p.R + BM - 1) / BM, C = tma && nM > 1 ? 2 : 1;
     p.nG = (nM + C - 1) / C;
     p.box = std::min(gcd_int(sh.page_size, BN), BN / C);
-    CUtensorMap maps[3];
-    if (!make_map(&maps[0], c.q, static_cast<long long>(sh.B) * sh.H_q * sh.L, p.q_box)) return PA_ERR_CUDA;
+    CUtensorMap maps[3] = {};
+    if (!f32 && !make_map(&maps[0], c.q, static_cast<long long>(sh.B) * sh.H_q * sh.L, p.q_box)) return PA_ERR_CUDA;
     maps[1] = maps[2] = maps[0];
     if (tma && (!make_pool_map(&maps[1], c.kc, p.pool_rows, p.box) || !make_pool_map(&maps[2], c.vc, p.pool_rows, p.box)))
         return PA_ERR_CUDA;
     int shares = 0;
-    const pa_status st = c.ks    ? launch_tiles<kQ4, 1>(p, maps, c, &shares)
+    const pa_status st = f32     ? c.ks ? launch_tiles<kQ4F, 1>(p, maps, c, &shares) : launch_tiles<kF32, 1>(p, maps, c, &shares)
+                         : c.ks  ? launch_tiles<kQ4, 1>(p, maps, c, &shares)
                          : !tma  ? launch_tiles<kCopy, 1>(p, maps, c, &shares)
                          : C > 1 ? launch_tiles<kTma, 2>(p, maps, c, &shares)
                                  : launch_tiles<kTma, 1>(p, maps, c, &shares);
     if (st != PA_OK) return st;
     const int ny = (std::min(p.R, C * BM) + 8 * kMergeRows - 1) / (8 * kMergeRows);
-    return launch_dependent(tree_merge_kernel, dim3(static_cast<unsigned>(shares * ny)), 256, 0, c.stream, p, ny, C)
+    return launch_dependent(f32 ? tree_merge_kernel<true> : tree_merge_kernel<false>,
+                            dim3(static_cast<unsigned>(shares * ny)), 256, 0, c.stream, p, ny, C)
                ? PA_OK
                : PA_ERR_CUDA;
 }
