@@ -47,13 +47,13 @@ namespace pa {
 namespace {
 
 constexpr int kD = kHeadDim;
-constexpr int BM = 128, BN = 128;  // query rows and keys of a tile
+constexpr int BM = 128;  // query rows of a tile
 constexpr uint32_t kTmemCols = 512;  // S of slot t at 128 t, O at 256 + 128 t
 // What a segment's query load, first softmax and epilogue cost, in key tiles: the
 // shares count it, or CTAs with many short segments would finish last.
 constexpr int kSegCost = 3;
 constexpr int kMinPer = 8;  // least cost of a share
-constexpr int kTile = BN * kD * 2;
+constexpr int kQTile = BM * kD * 2;
 enum Bar {
     kQFull = 0,     // + buffer: the query tile is there (4 bit: as it is)
     kQReady = 2,    // + buffer: ... in f16 (4 bit)
@@ -63,7 +63,6 @@ enum Bar {
     kVFull = 12,    // + slot
     kVEmpty = 15,   // + slot
     kVTail = 18,    // + slot: a tail tile's values are there, not yet cleaned (by TMA)
-    kVScale = 18,   // + t: the scales of V's rows are there (fp32 pages)
     kSFull = 21,    // + t
     kPFull = 23,    // + t
     kODone = 25,    // + t
@@ -71,7 +70,7 @@ enum Bar {
     kXFull = 29,    // both slots' maxima and sums are there
     kXFree = 30,    // ... and read
     kMmaDone = 31,
-    kItemFull = 32    // + place, then kItemEmpty + place
+    kVScale = 32    // + tile & 3: the scales of V's rows are there (fp32 pages)
 };
 // bf16 queries: bf16 pages by TMA or by copies, 4-bit pages.  fp32 queries: fp32 pages,
 // 4-bit pages.
@@ -88,18 +87,30 @@ constexpr int producers(Source s) { return is_f16(s) ? 8 : 4; }
 constexpr int threads(Source s) { return 32 * (producers(s) + 4 + 8); }
 // K and V tiles in the rings.  Three: with C = 2 a tile's time is below the latency of HBM.
 // 4-bit rows wait as they are, raw_stages tiles of them, and need the space for that.
-constexpr int slots(Source s) { return s == kF32 ? 1 : is_f16(s) ? 2 : 3; }
+constexpr int slots(Source s) { return is_f16(s) ? 2 : 3; }
+// Keys of a tile: two parts of 128 would leave no room for a second tile.
+constexpr int keys(Source s) { return s == kF32 ? 64 : 128; }
 constexpr int raw_stages(Source s) { return s == kQ4 ? 3 : s == kQ4F ? 1 : 0; }
 // Published pieces: enough for producers that are that many tiles ahead, were each tile a
 // piece.
 constexpr int items(Source s) { return is_f16(s) ? 8 : 4; }
+// The pieces' barriers: full + place, then empty + place.
+constexpr int item_bars(Source s) { return s == kF32 ? kVScale + 4 : kVScale; }
 // Registers of a thread by role: what setmaxnreg can share out, 512 x 128 or 640 x 96.
 struct Regs {
     int producer, misc, softmax;
 };
 constexpr Regs regs(Source s) {
-    return !is_f16(s) ? Regs{72, 104, 168} : s == kF32 ? Regs{80, 64, 128} : Regs{64, 64, 144};
+    return !is_f16(s) ? Regs{72, 104, 168} : s == kF32 ? Regs{104, 48, 112} : Regs{64, 64, 144};
 }
+
+constexpr int launch_regs(Source s) { return is_f16(s) ? 96 : 128; }  // what __launch_bounds__ leaves a thread
+constexpr bool regs_fit(Source s) {
+    const Regs r = regs(s);
+    return 32 * (producers(s) * r.producer + 4 * r.misc + 8 * r.softmax) <= threads(s) * launch_regs(s);
+}
+static_assert(regs_fit(kTma) && regs_fit(kCopy) && regs_fit(kQ4) && regs_fit(kF32) && regs_fit(kQ4F),
+              "an increase beyond what the others gave up would wait forever");
 
 // Shared memory from a 1024-byte boundary (the attribute of smem_raw) on.  Q: one tile, or
 // two of at most 64 rows that the pieces take in turn.
@@ -109,15 +120,15 @@ struct Smem {
 constexpr int kItemBytes = 168;
 constexpr Smem smem(Source s) {
     Smem m{};
-    int at = q_parts(s) * kTile;
+    int at = q_parts(s) * kQTile;
     m.k = at;  // [slot][part]
-    at += slots(s) * kv_parts(s) * kTile;
+    at += slots(s) * kv_parts(s) * keys(s) * kD * 2;
     m.v = at;
-    at += slots(s) * kv_parts(s) * kTile;
+    at += slots(s) * kv_parts(s) * keys(s) * kD * 2;
     m.raw = at;  // [producer warp][stage]
     at += 8 * raw_stages(s) * kRawStage;
     m.bar = at;
-    at += (kItemFull + 2 * items(s)) * 8;
+    at += (item_bars(s) + 2 * items(s)) * 8;
     m.items = at;
     at += items(s) * kItemBytes;
     m.tmem = at;
@@ -127,8 +138,8 @@ constexpr Smem smem(Source s) {
     at += 2 * BM * 8;
     m.q_scale = at;  // f16: [2][128] the inverse of a row's scale
     if (is_f16(s)) at += 2 * BM * 4;
-    m.kv_scale = at;  // fp32 pages, of 8 keys each: [4][16] K's inverse scale, [2][16] V's scale
-    if (s == kF32) at += (4 + 2) * 16 * 4;
+    m.kv_scale = at;  // fp32 pages, of 8 keys each: [8 tiles] K's inverse scale, [4 tiles] V's scale
+    if (s == kF32) at += (8 + 4) * (keys(s) / 8) * 4;
     m.total = at;
     return m;
 }
@@ -164,9 +175,13 @@ __device__ __forceinline__ int seq_len(const TileParams& p, int b) {
     const int S = __ldg(p.ctx + b);
     return S < p.L || static_cast<long long>(S) > p.max_S ? 0 : S;
 }
-__device__ __forceinline__ int key_tiles(int S) { return (S + BN - 1) / BN; }
+template <int BN>
+__device__ __forceinline__ int key_tiles(int S) {
+    return (S + BN - 1) / BN;
+}
+template <int BN>
 __device__ __forceinline__ int seq_cost(const TileParams& p, int S) {
-    return S == 0 ? 0 : p.H_kv * p.nG * (kSegCost + key_tiles(S));
+    return S == 0 ? 0 : p.H_kv * p.nG * (kSegCost + key_tiles<BN>(S));
 }
 
 // A published piece: key tiles j0 .. j0 + n - 1 of its ng.  Place k % items holds piece k
@@ -200,23 +215,29 @@ __device__ __forceinline__ void give_up(const TileParams& p, volatile int* f) {
     atomicOr(p.flag, PA_FLAG_TIMEOUT);
 }
 
-constexpr uint32_t idesc(bool f16, int a_mn, int b_mn) {
-    return tc::idesc_bf16(BM, BN, a_mn, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
+constexpr uint32_t idesc(bool f16, int n, int b_mn) {
+    return tc::idesc_bf16(BM, n, 0, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
 __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
+// A pair of numbers in f16's range in two f16 parts.
+__device__ __forceinline__ void split_f16(float2 x, uint32_t& hi, uint32_t& lo) {
+    const float2 h = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffffe000u),
+                                 __uint_as_float(__float_as_uint(x.y) & 0xffffe000u));
+    hi = pack_f16x2(h.x, h.y);
+    lo = pack_f16x2(x.x - h.x, x.y - h.y);
+}
 // k of 2^k (a normal number).
 __device__ __forceinline__ float exponent_of(float x) { return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127); }
 
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+// A warp's registers from here on (a warpgroup together): fewer than at the launch, or more.
+template <int N, int LAUNCH>
+__device__ __forceinline__ void reg_set() {
+    static_assert(N % 8 == 0 && N >= 24 && N <= 256, "setmaxnreg");
+    if constexpr (N <= LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <Source SRC, int C>
@@ -226,12 +247,13 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     static_assert(C == 1 || SRC == kTma, "only TMA multicasts");
     constexpr bool F16 = is_f16(SRC), F32 = fp32(SRC);
     constexpr int kThreads = threads(SRC), kProd = producers(SRC), N = slots(SRC), I = items(SRC);
+    constexpr int BN = keys(SRC), kTile = BN * kD * 2;
     constexpr int QP = q_parts(SRC), VP = kv_parts(SRC), kRing = VP * kTile;
-    constexpr int kItemEmpty = kItemFull + I;
+    constexpr int kItemFull = item_bars(SRC), kItemEmpty = kItemFull + I;
     constexpr Smem M = smem(SRC);
     // Tiles behind TMA: [8 rows][64-dim half][row][128 bytes], as boxes of rows come; else
-    // [half][128 rows][128 bytes].
-    constexpr uint32_t kHalf = SRC == kTma ? 1024u : kStageHalf, kGroup = SRC == kTma ? 2048u : 1024u;
+    // [half][BN rows][128 bytes].
+    constexpr uint32_t kHalf = SRC == kTma ? 1024u : BN * 128u, kGroup = SRC == kTma ? 2048u : 1024u;
     constexpr uint16_t kAll = (1u << C) - 1u;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
@@ -265,10 +287,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             mbar_init(bar(kVEmpty + s), C);
             if (SRC == kTma) mbar_init(bar(kVTail + s), 1);
         }
-        if (SRC == kF32) {
-            mbar_init(bar(kVScale), 4);
-            mbar_init(bar(kVScale + 1), 4);
-        }
+        if (SRC == kF32)
+            for (int s = 0; s < 4; ++s) mbar_init(bar(kVScale + s), 4);
         mbar_init(bar(kMmaDone), 1);
         for (int s = 0; s < I; ++s) {
             mbar_init(bar(kItemFull + s), 1);
@@ -286,7 +306,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     {
         int mine = 0, v = 0;
         for (int b = tid; b < p.B; b += kThreads) {
-            const int n = seq_cost(p, seq_len(p, b));
+            const int n = seq_cost<BN>(p, seq_len(p, b));
             if (b == tid) mine = n;
             v += n;
         }
@@ -305,7 +325,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         for (int b0 = 0; b0 < p.B; b0 += kThreads) {
             const int b = b0 + tid;
             int x = mine;
-            if (b0 > 0) x = b < p.B ? seq_cost(p, seq_len(p, b)) : 0;
+            if (b0 > 0) x = b < p.B ? seq_cost<BN>(p, seq_len(p, b)) : 0;
             int incl = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -369,7 +389,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
 
     if (warp < kProd) {
         // ========================= K/V producers ==================================
-        reg_dec<regs(SRC).producer>();
+        reg_set<regs(SRC).producer, launch_regs(SRC)>();
         bool ok = true;
         if constexpr (SRC == kTma) {
             if (warp == 0) {
@@ -468,7 +488,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 const volatile Item* const it = slot(k);
                 const int key = j * BN + 32 * (lane >> 3) + 8 * (warp & 3) + (lane & 7), lp = key / p.ps;
                 const int S = it->S, x = key - (S - p.L);
-                const bool seen = key < S && (x < 0 || (it->live[x >> 5] >> (x & 31) & 1u));
+                const bool seen = key < S && (lane >> 3) < BN / 32 && (x < 0 || (it->live[x >> 5] >> (x & 31) & 1u));
                 in_page = seen ? key - lp * p.ps : -1;
                 page = seen ? __ldg(p.bt + static_cast<long long>(it->b) * p.max_npg + lp) : 0;
                 row_base = it->kvh;
@@ -547,76 +567,98 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 }
                 cp_async_wait<0>();
             } else if constexpr (SRC == kF32) {
-                // Warps 0-3 bring K, 4-7 V: warp w rows 32 i + 8 w .., the next 8 on their way.
-                // Each 8 rows are taken by a power of two so that their largest value lies in
-                // [2^14, 2^15), and stored in two f16 parts: all but 2^-22 of a value, or 2^-40 of
-                // the 8 rows' largest.  Scores are scaled back by key, V's scale goes into P.
+                // Warps 0-3 bring K, 4-7 V: warp w rows 32 i + 8 w .., i = 0, 1, which are loaded a
+                // tile ahead.  Each 8 rows are taken by a power of two so that their largest value
+                // lies in [2^14, 2^15), and stored in two f16 parts: all but 2^-22 of a value, or
+                // 2^-40 of the 8 rows' largest.  Scores are scaled back by key; V's scale goes into
+                // P, so it is announced before V's place in the ring is free.
                 const bool is_v = warp >= 4;
                 const int w = warp & 3;
                 const float* const pool = reinterpret_cast<const float*>(is_v ? p.vc : p.kc);
                 const uint32_t ring = base + (is_v ? M.v : M.k);
                 const int full = is_v ? kVFull : kKFull, empty = is_v ? kVEmpty : kKEmpty;
-                float* const scales = reinterpret_cast<float*>(smem_raw + M.kv_scale) + (is_v ? 64 : 0);
-                const int r8 = lane >> 2, l4 = lane & 3;  // row of 8, dims 16 q + 4 l4 ..
+                float* const scales = reinterpret_cast<float*>(smem_raw + M.kv_scale) + (is_v ? 8 * (BN / 8) : 0);
+                // Row of 8 and dims 16 q + 4 l4 ..: 16 lanes take every other row, so that their 8-byte
+                // stores hit all banks once.
+                const int r8 = (lane >> 2 & 3) * 2 + (lane >> 4), l4 = lane & 3;
+                auto prefetch = [&](int rows) {
+                    if (rows >= 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) prefetch_l2(pool + static_cast<long long>(rows) * kD + 32 * i);
+                    }
+                };
                 auto load = [&](float4 (&v)[8], int rows, int i) {
                     const int row = __shfl_sync(0xffffffffu, rows, 8 * i + r8);
                     const float4* const src = reinterpret_cast<const float4*>(pool + (row < 0 ? 0 : static_cast<long long>(row) * kD)) + l4;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) v[q] = row < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcs(src + 4 * q);
                 };
-                float last_up = 1.f;
-                auto store = [&](const float4 (&v)[8], int i, int at16) {
+                auto largest_of = [&](const float4 (&v)[8]) {
                     float mx = 0.f;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) mx = fmax3(fmax3(mx, fabsf(v[q].x), fabsf(v[q].y)), fabsf(v[q].z), fabsf(v[q].w));
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    float up, down;
-                    f16_scale(mx, up, down);
-                    if (is_v) {
-                        up = fminf(up, 1.2676506e30f);  // 2^100: what P 2^v adds up to stays a number
-                        if (mx == 0.f) up = last_up;    // (any will do; one like the others' keeps P in range)
-                        last_up = up;
-                    }
-                    if (lane == 0) scales[at16 * 16 + 4 * i + w] = is_v ? up : down;
-                    const uint32_t at = ring + (32 * i + 8 * w + r8) * 128 + (l4 & 1) * 8;
+                    return mx;
+                };
+                auto store = [&](const float4 (&v)[8], int i, float up) {
+                    const uint32_t at = ring + g.s * kRing + (32 * i + 8 * w + r8) * 128 + (l4 & 1) * 8;
+                    const float2 up2 = make_float2(up, up);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        const float x[4] = {v[q].x * up, v[q].y * up, v[q].z * up, v[q].w * up};
-                        float hi[4];
+                        const float2 x[2] = {__fmul2_rn(make_float2(v[q].x, v[q].y), up2),
+                                             __fmul2_rn(make_float2(v[q].z, v[q].w), up2)};
+                        uint32_t hi[2], lo[2];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) hi[e] = __uint_as_float(__float_as_uint(x[e]) & 0xffffe000u);
+                        for (int e = 0; e < 2; ++e) split_f16(x[e], hi[e], lo[e]);
                         const int c = (4 * q + l4) >> 1;  // chunk of 8 dims
                         const uint32_t to = at + (c >> 3) * kHalf + (((c & 7) ^ r8) << 4);
-                        sts64(to, pack_f16x2(hi[0], hi[1]), pack_f16x2(hi[2], hi[3]));
-                        sts64(to + kTile, pack_f16x2(x[0] - hi[0], x[1] - hi[1]), pack_f16x2(x[2] - hi[2], x[3] - hi[3]));
+                        sts64(to, hi[0], hi[1]);
+                        sts64(to + kTile, lo[0], lo[1]);
                     }
                 };
                 float4 a[8], b[8];
-                int rows = -1, tile = 0;
+                float last_up = 1.f;
+                // of 8 rows: the factor, kept for V's softmax as it is, for K's inverted
+                auto scale_of = [&](float mx, float* out) {
+                    float up, down;
+                    f16_scale(mx, up, down);
+                    if (is_v) {
+                        // 2^100: what P 2^v adds up to stays a number.  Zeros: any will do; one like
+                        // the others' keeps P in range.
+                        up = last_up = mx == 0.f ? last_up : fminf(up, 1.2676506e30f);
+                    }
+                    if (lane == 0) *out = is_v ? up : down;
+                    return up;
+                };
+                // rows of this tile; page ids of the next one are always on their way
+                int tile = 0;
+                bool there = more;
                 if (more) {
-                    rows = rows_of();
+                    const int rows = rows_of();
                     load(a, rows, 0);
-                }
-                while (more) {
-                    const int t = (j - slot(k)->j0) & 1, at16 = is_v ? t : tile & 3;  // where its scales go
-                    next();  // (the tile after: its page ids are on their way)
-                    if (!ok) break;
                     load(b, rows, 1);
+                    next();
+                }
+                while (ok && there) {
+                    there = more;
+                    const int rows = more ? rows_of() : -1;  // of the tile after
+                    prefetch(rows);
+                    if (more) next();
+                    if (!ok) break;
+                    // (K's may be written while the softmax of four tiles before is under way, V's
+                    // of three)
+                    float* const mine = scales + (tile & (is_v ? 3 : 7)) * (BN / 8) + w;
+                    const float up0 = scale_of(largest_of(a), mine), up1 = scale_of(largest_of(b), mine + 4);
+                    __syncwarp();
+                    if (is_v && lane == 0) mbar_arrive(bar(kVScale + (tile & 3)));
                     ok = warp_wait(bar(empty + g.s), g.phase ^ 1u);
                     if (!ok || aborted(abort_flag)) break;
-                    store(a, 0, at16);
-                    load(a, rows, 2);
-                    store(b, 1, at16);
-                    load(b, rows, 3);
-                    store(a, 2, at16);
-                    if (more) {
-                        rows = rows_of();
-                        load(a, rows, 0);
-                    }
-                    store(b, 3, at16);
+                    store(a, 0, up0);
+                    load(a, rows, 0);
+                    store(b, 1, up1);
+                    load(b, rows, 1);
                     announce(full + g.s);
-                    if (is_v && lane == 0) mbar_arrive(bar(kVScale + t));
                     ++tile;
                     g.next();
                 }
@@ -655,12 +697,12 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         }
         if (!ok && lane == 0) give_up(p, abort_flag);
     } else if (warp < kProd + 4) {
-        reg_dec<regs(SRC).misc>();
+        reg_set<regs(SRC).misc, launch_regs(SRC)>();
         if (warp == kProd) {
             // =========================== MMA issuer ===============================
             // The whole warp runs the loop and one elected lane issues.
-            constexpr uint32_t idS = idesc(F16, 0, 0);  // Q, K both K-major
-            constexpr uint32_t idO = idesc(F16, 0, 1);  // P K-major, V MN-major
+            constexpr uint32_t idS = idesc(F16, BN, 0);  // Q, K both K-major
+            constexpr uint32_t idO = idesc(F16, kD, 1);  // P K-major, V MN-major
             const uint64_t dQ0 = tc::smem_desc_sw128(base, 16, 1024);
             const uint64_t dK0 = tc::smem_desc_sw128(base + M.k, 16, kGroup);
             const uint64_t dV0 = tc::smem_desc_sw128(base + M.v, kHalf, kGroup);
@@ -675,7 +717,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 release(k);
                 if (n == 0) break;
                 const int buf = q_buf(k);
-                const uint64_t dq0 = tc::desc_advance(dQ0, buf * (QP * kTile / 2)), dq1 = tc::desc_advance(dq0, p.q_half);
+                const uint64_t dq0 = tc::desc_advance(dQ0, buf * (QP * kQTile / 2)), dq1 = tc::desc_advance(dq0, p.q_half);
                 auto qk = [&](int i) {  // Q K^T of the piece's tile i
                     if (!warp_wait(bar(kKFull + kr.s), kr.phase)) return false;
                     tc::fence_after_sync();
@@ -764,7 +806,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 if (!ok || aborted(abort_flag)) break;
                 if (lane == 0) {
                     if (m * BM < p.R) {
-                        const uint32_t dst = base + buf * (kTile / 2);
+                        const uint32_t dst = base + buf * (kQTile / 2);
                         mbar_arrive_expect_tx(bar(kQFull + buf), static_cast<uint32_t>(p.q_box) * 256u);
                         tc::tma_load_2d(dst, &qmap, 0, row, bar(kQFull + buf), policy);
                         tc::tma_load_2d(dst + p.q_half, &qmap, 64, row, bar(kQFull + buf), policy);
@@ -782,7 +824,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             if (start < end) {
                 b = first_b;
                 S = seq_len(p, b);
-                ng = key_tiles(S);
+                ng = key_tiles<BN>(S);
                 const int i = (start - first_unit) / (kSegCost + ng);
                 kvh = i / p.nG;
                 mp = i - kvh * p.nG;
@@ -859,7 +901,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         kvh = 0;
                         do S = seq_len(p, ++b);
                         while (S == 0);
-                        ng = key_tiles(S);
+                        ng = key_tiles<BN>(S);
                     }
                 }
             }
@@ -869,7 +911,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         __syncwarp();
     } else {
         // ============================== softmax =======================================
-        reg_inc<regs(SRC).softmax>();
+        reg_set<regs(SRC).softmax, launch_regs(SRC)>();
         const int t = (warp - kProd - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;  // slot, lane quarter, row
         const uint32_t trow = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         // How far (log2) a row's scores may rise above its maximum before O is rescaled:
@@ -993,7 +1035,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 const int buf = q_buf(k);
                 float* const down = reinterpret_cast<float*>(smem_raw + M.q_scale) + buf * BM + r;
                 if (t == 0) {
-                    const uint32_t qrow = base + buf * (QP * kTile / 2);
+                    const uint32_t qrow = base + buf * (QP * kQTile / 2);
                     if constexpr (F32) {
                         // (the products of the last piece in the buffer are done)
                         ok = q_use(k) == 0 || warp_wait(bar(kQEmpty + buf), (q_use(k) - 1) & 1);
@@ -1014,15 +1056,12 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                                 const float4 v[2] = {__ldg(src + 2 * c), __ldg(src + 2 * c + 1)};
                                 const float x[8] = {v[0].x * up, v[0].y * up, v[0].z * up, v[0].w * up,
                                                     v[1].x * up, v[1].y * up, v[1].z * up, v[1].w * up};
-                                float hi[8];
+                                uint32_t hi[4], lo[4];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) hi[e] = __uint_as_float(__float_as_uint(x[e]) & 0xffffe000u);
+                                for (int e = 0; e < 4; ++e) split_f16(make_float2(x[2 * e], x[2 * e + 1]), hi[e], lo[e]);
                                 const uint32_t at = qrow + (c >> 3) * p.q_half + sw128(r, c & 7);
-                                sts128(at, pack_f16x2(hi[0], hi[1]), pack_f16x2(hi[2], hi[3]), pack_f16x2(hi[4], hi[5]),
-                                       pack_f16x2(hi[6], hi[7]));
-                                sts128(at + 2 * p.q_half, pack_f16x2(x[0] - hi[0], x[1] - hi[1]),
-                                       pack_f16x2(x[2] - hi[2], x[3] - hi[3]), pack_f16x2(x[4] - hi[4], x[5] - hi[5]),
-                                       pack_f16x2(x[6] - hi[6], x[7] - hi[7]));
+                                sts128(at, hi[0], hi[1], hi[2], hi[3]);
+                                sts128(at + 2 * p.q_half, lo[0], lo[1], lo[2], lo[3]);
                             }
                             *down = dn;
                         }
@@ -1065,23 +1104,24 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             float2 lsum = make_float2(0.f, 0.f);
             for (int j = 0; j < nk; ++j) {
                 const int jt = slot(k)->j0 + 2 * j + t;  // key tile
-                uint32_t see[4];
+                uint32_t see[BN / 32];
                 if (busy && jt >= tail) {  // this row's bits of the tile, while S is on its way
                     const int x = jt * BN - first;
                     const int w0 = x >> 5, sh = x & 31;  // (floor: words before the drafts are all ones)
-                    uint32_t w[5];
+                    uint32_t w[BN / 32 + 1];
 #pragma unroll
-                    for (int i = 0; i < 5; ++i) {
+                    for (int i = 0; i < BN / 32 + 1; ++i) {
                         const int wi = w0 + i;
                         w[i] = wi < 0 ? 0xffffffffu : wi < p.W ? __ldg(mask + wi) & slot(k)->live[wi] : 0u;
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) see[i] = __funnelshift_r(w[i], w[i + 1], sh);
+                    for (int i = 0; i < BN / 32; ++i) see[i] = __funnelshift_r(w[i], w[i + 1], sh);
                 }
                 ok = warp_wait(bar(kSFull + t), (sc + j) & 1);
                 if (!ok || aborted(abort_flag)) break;
                 if constexpr (SRC == kF32) {  // the scales of this tile's V
-                    ok = warp_wait(bar(kVScale + t), (sc + j) & 1);
+                    const int tile = slot(k)->before[0] + slot(k)->before[1] + 2 * j + t;
+                    ok = warp_wait(bar(kVScale + (tile & 3)), (tile >> 2) & 1);
                     if (!ok) break;
                 }
                 if constexpr (F16) {
@@ -1169,8 +1209,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             tc::ld32(st + cc * 32, x);
                             float kf[4] = {c, c, c, c}, off[4] = {0.f, 0.f, 0.f, 0.f};
                             if constexpr (SRC == kF32) {
-                                const float4 ks = scales[(tile & 3) * 4 + cc];
-                                vs = scales[16 + t * 4 + cc];
+                                const float4 ks = scales[(tile & 7) * (BN / 32) + cc];
+                                vs = scales[(8 + (tile & 3)) * (BN / 32) + cc];
                                 kf[0] = c * ks.x, kf[1] = c * ks.y, kf[2] = c * ks.z, kf[3] = c * ks.w;
                                 // (a power of two: its exponent)
                                 off[0] = exponent_of(vs.x), off[1] = exponent_of(vs.y), off[2] = exponent_of(vs.z),
@@ -1187,7 +1227,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         };
                         float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
 #pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) {
+                        for (int cc = 0; cc < BN / 32; ++cc) {
                             float x[32];
                             scores(x, cc, vs);
 #pragma unroll
@@ -1204,7 +1244,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         }
                         const float mu = mrow == neg_inf() ? 0.f : mrow;
 #pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) {
+                        for (int cc = 0; cc < BN / 32; ++cc) {
                             float x[32];
                             scores(x, cc, vs);
                             const float back[4] = {vs.x, vs.y, vs.z, vs.w};
@@ -1212,10 +1252,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const float2 ex = make_float2(fast_exp2(x[2 * i] - mu), fast_exp2(x[2 * i + 1] - mu));
-                                const float2 hi = make_float2(__uint_as_float(__float_as_uint(ex.x) & 0xffffe000u),
-                                                              __uint_as_float(__float_as_uint(ex.y) & 0xffffe000u));
-                                w[i] = pack_f16x2(hi.x, hi.y);
-                                w[16 + i] = pack_f16x2(ex.x - hi.x, ex.y - hi.y);
+                                split_f16(ex, w[i], w[16 + i]);
                                 if constexpr (SRC == kF32) {
                                     ts.x = fmaf(ex.x, back[i >> 2], ts.x);
                                     ts.y = fmaf(ex.y, back[i >> 2], ts.y);
@@ -1422,6 +1459,10 @@ pa_status launch_tiles(const TileParams& p, const CUtensorMap* maps, const TreeC
     if (!clusters[c.dev.device]) {
         if (cudaFuncSetAttribute(tree_tile_kernel<SRC, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
             return PA_ERR_CUDA;
+        // the roles' registers come out of what the launch has
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, tree_tile_kernel<SRC, C>) != cudaSuccess) return PA_ERR_CUDA;
+        if (at.numRegs != launch_regs(SRC)) return PA_ERR_UNSUPPORTED;
         int n = c.dev.sm_count;
         if (C > 1 && cudaOccupancyMaxActiveClusters(&n, tree_tile_kernel<SRC, C>, &cfg) != cudaSuccess) return PA_ERR_CUDA;
         clusters[c.dev.device] = std::min(n, c.dev.sm_count / C);
@@ -1449,7 +1490,7 @@ bool tree_supported(const pa_shape& sh) {
     const long long R = static_cast<long long>(sh.H_q / sh.H_kv) * sh.L;
     const long long cap = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     // costs are counted in an int
-    return static_cast<long long>(sh.B) * sh.H_kv * ((R + BM - 1) / BM) * (cap / BN + 1 + kSegCost) < INT_MAX / 2;
+    return static_cast<long long>(sh.B) * sh.H_kv * ((R + BM - 1) / BM) * (cap / keys(kF32) + 1 + kSegCost) < INT_MAX / 2;
 }
 
 size_t tree_workspace_bytes(int sm_count) { return plan(sm_count).total; }
@@ -1484,7 +1525,7 @@ pa_status tree_launch(const TreeCall& c) {
     p.pool_rows = sh.num_pages * sh.H_kv * sh.page_size;
     p.q_box = std::min(BM, (p.R + 7) / 8 * 8);
     p.q_bufs = p.q_box <= BM / 2 ? 2 : 1;
-    p.q_half = kTile / 2 / p.q_bufs;
+    p.q_half = kQTile / 2 / p.q_bufs;
     const bool f32 = sh.dtype == PA_F32;
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     p.scale_log2 = c.scale * 1.4426950408889634f;
@@ -1492,7 +1533,7 @@ pa_status tree_launch(const TreeCall& c) {
     const bool tma = !f32 && !c.ks && sh.page_size % 8 == 0;
     const int nM = (p.R + BM - 1) / BM, C = tma && nM > 1 ? 2 : 1;
     p.nG = (nM + C - 1) / C;
-    p.box = std::min(gcd_int(sh.page_size, BN), BN / C);
+    p.box = std::min(gcd_int(sh.page_size, keys(kTma)), keys(kTma) / C);
     CUtensorMap maps[3] = {};
     if (!f32 && !make_map(&maps[0], c.q, static_cast<long long>(sh.B) * sh.H_q * sh.L, p.q_box)) return PA_ERR_CUDA;
     maps[1] = maps[2] = maps[0];
