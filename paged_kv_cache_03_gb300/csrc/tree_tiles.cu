@@ -51,8 +51,12 @@ constexpr int BM = 128;  // query rows of a tile
 constexpr uint32_t kTmemCols = 512;  // S of slot t at 128 t, O at 256 + 128 t
 // What a segment's query load, first softmax and epilogue cost, in key tiles: the
 // shares count it, or CTAs with many short segments would finish last.
-constexpr int kSegCost = 3;
+constexpr int kSegCost = 4;
 constexpr int kMinPer = 8;  // least cost of a share
+// Where there is a CTA for each segment and tables hold at most so many key tiles, segments
+// stay whole and there is no merge: alone with 1000 / 2000 keys of bf16, 17 / 27 us whole
+// and 19 / 21 cut; of fp32 with 500 / 1000 keys, 26 / 44 whole and 29 / 30 cut.
+constexpr int kWholeTiles = 8;
 constexpr int kQTile = BM * kD * 2;
 enum Bar {
     kQFull = 0,     // + buffer: the query tile is there (4 bit: as it is)
@@ -166,6 +170,7 @@ struct TileParams {
     long long max_S;
     float scale_log2;
     int out32;  // the output is 32-byte aligned
+    int whole;  // a CTA (cluster) per segment
 };
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -303,7 +308,15 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         tc::tmem_relinquish();
     }
     // ---- this share ----------------------------------------------------------------
-    {
+    if (p.whole) {
+        // segment i: a share that holds it and no other
+        if (tid == 0) {
+            const int b = my_share / (p.H_kv * p.nG), cost = kSegCost + key_tiles<BN>(seq_len(p, b));
+            share[0] = INT_MAX;
+            share[1] = cost;
+            share[2] = b;
+        }
+    } else {
         int mine = 0, v = 0;
         for (int b = tid; b < p.B; b += kThreads) {
             const int n = seq_cost<BN>(p, seq_len(p, b));
@@ -343,6 +356,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             }
             for (int w = 0; w < kThreads / 32; ++w) carry += sums[w];
         }
+    }
+    {
         // sequences that break the contract: zero rows
         for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
             if (seq_len(p, b) > 0) continue;
@@ -358,10 +373,10 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     if constexpr (C > 1) cluster_sync();  // no peer's copy or commit before the barriers stand
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const int total = share[0], per = share[1], first_b = share[2], first_unit = share[3];
+    const int total = share[0], per = share[1], first_b = share[2], first_unit = p.whole ? 0 : share[3];
     // which slots of the share's first sequence hold a draft, where one warp would take long
     uint32_t first_live = 0u;
-    if (p.W > 4 && my_share * per < total) {
+    if (p.W > 4 && (p.whole || my_share * per < total)) {
         uint32_t* const words = reinterpret_cast<uint32_t*>(share) + 64;
         if (tid < 32) words[tid] = 0u;
         __syncthreads();
@@ -819,16 +834,16 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             if (!ok && lane == 0) give_up(p, abort_flag);
         } else if (warp == kProd + 3) {
             // ============================ pieces =====================================
-            const int start = my_share * per, end = min(start + per, total);
+            const int start = p.whole ? 0 : my_share * per, end = p.whole ? per : min(start + per, total);
             int b = 0, S = 0, kvh = 0, mp = 0, ng = 0, seg = end;  // seg: first position of the segment
             if (start < end) {
                 b = first_b;
                 S = seq_len(p, b);
                 ng = key_tiles<BN>(S);
-                const int i = (start - first_unit) / (kSegCost + ng);
+                const int i = p.whole ? my_share % (p.H_kv * p.nG) : (start - first_unit) / (kSegCost + ng);
                 kvh = i / p.nG;
                 mp = i - kvh * p.nG;
-                seg = first_unit + i * (kSegCost + ng);
+                seg = p.whole ? 0 : first_unit + i * (kSegCost + ng);
             }
             int4 crossing = make_int4(-1, 0, 0, 0);
             int before0 = 0, before1 = 0;
@@ -905,7 +920,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     }
                 }
             }
-            if (lane == 0 && rank == 0) p.split[my_share] = crossing;
+            if (lane == 0 && rank == 0 && !p.whole) p.split[my_share] = crossing;
             if (!ok && lane == 0) give_up(p, abort_flag);
         }
         __syncwarp();
@@ -1442,7 +1457,7 @@ bool make_pool_map(CUtensorMap* map, const void* ptr, long long rows, int box_ro
 }
 
 template <Source SRC, int C>
-pa_status launch_tiles(const TileParams& p, const CUtensorMap* maps, const TreeCall& c, int* shares) {
+pa_status launch_tiles(TileParams p, const CUtensorMap* maps, const TreeCall& c, int* shares) {
     constexpr int bytes = smem(SRC).total;
     static int clusters[64] = {0};  // resident together, per device
     cudaLaunchConfig_t cfg = {};
@@ -1469,9 +1484,13 @@ pa_status launch_tiles(const TileParams& p, const CUtensorMap* maps, const TreeC
         if (clusters[c.dev.device] < 1) return PA_ERR_UNSUPPORTED;
     }
     *shares = clusters[c.dev.device];
+    const long long segs = static_cast<long long>(p.B) * p.H_kv * p.nG;
+    p.whole = segs <= *shares && p.max_S <= kWholeTiles * keys(SRC);
+    if (p.whole) *shares = static_cast<int>(segs);
     cfg.gridDim = dim3(static_cast<unsigned>(*shares * C));
-    return cudaLaunchKernelEx(&cfg, tree_tile_kernel<SRC, C>, p, maps[0], maps[1], maps[2]) == cudaSuccess ? PA_OK
-                                                                                                         : PA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, tree_tile_kernel<SRC, C>, p, maps[0], maps[1], maps[2]) != cudaSuccess) return PA_ERR_CUDA;
+    if (p.whole) *shares = 0;
+    return PA_OK;
 }
 
 int gcd_int(int a, int b) {
@@ -1545,7 +1564,7 @@ pa_status tree_launch(const TreeCall& c) {
                          : !tma  ? launch_tiles<kCopy, 1>(p, maps, c, &shares)
                          : C > 1 ? launch_tiles<kTma, 2>(p, maps, c, &shares)
                                  : launch_tiles<kTma, 1>(p, maps, c, &shares);
-    if (st != PA_OK) return st;
+    if (st != PA_OK || shares == 0) return st;  // (0: nothing to merge)
     const int ny = (std::min(p.R, C * BM) + 8 * kMergeRows - 1) / (8 * kMergeRows);
     return launch_dependent(f32 ? tree_merge_kernel<true> : tree_merge_kernel<false>,
                             dim3(static_cast<unsigned>(shares * ny)), 256, 0, c.stream, p, ny, C)
