@@ -43,14 +43,16 @@ __global__ void __launch_bounds__(1024) tree_mask_kernel(const int32_t* parents,
             anc = a;
         }
     }
-    uint32_t* const mine = rows + tid * stride;
-    for (int w = 0; w < W; ++w) mine[w] = 0u;
-    mine[warp] = lost ? 0u : bits;
-    ups[tid] = lost ? -1 : up;
+    if (warp < W) {
+        uint32_t* const mine = rows + tid * stride;
+        for (int w = 0; w < W; ++w) mine[w] = w == warp && !lost ? bits : 0u;
+        ups[tid] = lost ? -1 : up;
+    }
     // the words of the ancestors before the 32, a warp per row and a lane per word
+    const int warps = static_cast<int>(blockDim.x) >> 5;
     for (int k = 1; k < W; ++k) {
         __syncthreads();
-        for (int i = warp; i < 32; i += W) {
+        for (int i = warp; i < 32; i += warps) {
             const int u = ups[32 * k + i];
             if (u < 0) continue;
             const uint32_t own = rows[u * stride + (u >> 5)];  // its own bit: it is a draft
@@ -62,11 +64,14 @@ __global__ void __launch_bounds__(1024) tree_mask_kernel(const int32_t* parents,
         }
     }
     __syncthreads();
-    for (int i = warp; i < L; i += W) {
-        const uint32_t word = lane < W ? rows[i * stride + lane] : 0u;
-        if (lane < W) mask[(first + i) * W + lane] = word;
-        const int n = __reduce_add_sync(0xffffffffu, __popc(word));
-        if (lane == 0) depths[first + i] = n - 1;
+    for (int i = tid; i < L * W; i += blockDim.x) {
+        const int r = i / W;
+        mask[first * W + i] = rows[r * stride + i - r * W];
+    }
+    for (int i = tid; i < L; i += blockDim.x) {
+        int n = -1;
+        for (int w = 0; w < W; ++w) n += __popc(rows[i * stride + w]);
+        depths[first + i] = n;
     }
 }
 
@@ -127,6 +132,9 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
     const int b = static_cast<int>(blockIdx.x) / p.H_kv, kvh = static_cast<int>(blockIdx.x) - b * p.H_kv;
     const bool writes = threadIdx.x == 0 && kvh == 0 && blockIdx.y == 0;  // lengths and flags
     const int S = __ldg(p.ctx + b), n = __ldg(p.path_lens + b);
+    const int32_t* const path = p.path + static_cast<long long>(b) * p.path_n;
+    // (the first entries are requested beside their number)
+    const int early = threadIdx.x < p.path_n ? __ldg(path + threadIdx.x) : 0;
     if (S < p.L || static_cast<long long>(S) > p.max_S) {
         if (writes) {
             p.ctx_out[b] = S;
@@ -137,8 +145,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
     bool bad = n < 0 || n > p.L || n > p.path_n;
     if (!bad)
         for (int j = threadIdx.x; j < n; j += blockDim.x) {
-            const int32_t* const path = p.path + static_cast<long long>(b) * p.path_n;
-            const int i = __ldg(path + j), before = j > 0 ? __ldg(path + j - 1) : -1;
+            const int i = j == threadIdx.x ? early : __ldg(path + j), before = j > 0 ? __ldg(path + j - 1) : -1;
             bad |= i <= before || i >= p.L;
         }
     bad = __syncthreads_or(bad);
@@ -173,7 +180,7 @@ pa_status tree_mask_launch(int B, int L, const int32_t* parents, uint32_t* mask,
             return PA_ERR_CUDA;
         attr_done[dev.device] = 1;
     }
-    tree_mask_kernel<<<static_cast<unsigned>(B), static_cast<unsigned>(32 * W), smem, stream>>>(parents, mask, depths, flag,
+    tree_mask_kernel<<<static_cast<unsigned>(B), static_cast<unsigned>(W > 8 ? 32 * W : 256), smem, stream>>>(parents, mask, depths, flag,
                                                                                                 L, W);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
