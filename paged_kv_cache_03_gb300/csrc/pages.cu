@@ -82,24 +82,33 @@ struct ResizeParams {
     int* list;        // free pages, ascending
     int2* share;      // per page: sequences that grow from it, the last of them
     int2* need;       // per sequence: pages taken before it, what it takes
-    int chunks;       // of 1024 table entries per sequence
+    int chunks;       // of 32 table entries per sequence
 };
 
 constexpr int kKeeps = 1 << 30, kCopies = 1 << 29, kTakes = kCopies - 1;  // bits of need.y
 
+// A sequence that grows: its lengths, and the partly filled last page where others hold it
+// too (-1: none), with its holders.
+struct Growth {
+    int S, n, page, refs;
+    bool grows;
+};
+
 // All CTAs give back the pages past new ends; the last one to finish then finds the free
 // pages and hands them out, so growing sequences can have what shrinking ones gave up.
 // Releasing is bound by the rate of atomics and spreads over the SMs; handing out is a
-// chain of short steps on one SM (two scans, the lists in L2).
+// chain of short steps on one SM, each a round trip to L2: what a sequence is about to do is
+// read once where a thread has one sequence, and the first counts are read ahead.
 __global__ void __launch_bounds__(1024) resize_kernel(const ResizeParams p) {
     const PagesParams& t = p.t;
     __shared__ int sums[32];
     __shared__ int last_cta, found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t flags = 0u;
-    for (long long item = blockIdx.x; item < static_cast<long long>(t.B) * p.chunks; item += gridDim.x) {
+    const long long items = static_cast<long long>(t.B) * p.chunks;
+    for (long long item = 32ll * blockIdx.x + warp; item < items; item += 32ll * gridDim.x) {
         const int b = static_cast<int>(item / p.chunks);
-        const int e = static_cast<int>(item - static_cast<long long>(b) * p.chunks) * 1024 + tid;
+        const int e = static_cast<int>(item - static_cast<long long>(b) * p.chunks) * 32 + lane;
         const int S = t.ctx[b], n = __ldg(p.new_lens + b);
         if (n < 0 || n >= S || !t.len_ok(S) || e < t.pages(n) || e >= t.pages(S)) continue;
         const int page = t.row(b)[e];
@@ -124,49 +133,67 @@ __global__ void __launch_bounds__(1024) resize_kernel(const ResizeParams p) {
         found = 0;
     }
 
-    // the partly filled last page of a sequence that grows, where others hold it too
-    auto grows = [&](int b, int& S, int& n) {
-        S = t.ctx[b];
-        n = __ldg(p.new_lens + b);
-        return n > S && t.len_ok(S) && t.len_ok(n);
+    // the first free pages, and this thread's first sequence
+    uint32_t is_free[8];
+    auto look = [&](int p0) {  // a warp takes 256 counts
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int page = p0 + 256 * warp + 32 * k + lane;
+            is_free[k] = page < t.num_pages && __ldcg(t.refs + page) == 0 ? 1u : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) is_free[k] = __ballot_sync(0xffffffffu, is_free[k] != 0u);
     };
-    auto shared_page = [&](int b, int S) {
-        if (S % t.ps == 0) return -1;
-        const int page = t.row(b)[S / t.ps];
-        return t.page_ok(page) && __ldcg(t.refs + page) > 1 ? page : -1;
+    auto growth = [&](int b) {
+        Growth g;
+        g.S = t.ctx[b];
+        g.n = __ldg(p.new_lens + b);
+        g.grows = g.n > g.S && t.len_ok(g.S) && t.len_ok(g.n);
+        g.page = -1;
+        g.refs = 0;
+        if (g.grows && g.S % t.ps != 0) {
+            const int page = t.row(b)[g.S / t.ps];
+            if (t.page_ok(page)) {
+                g.refs = __ldcg(t.refs + page);
+                if (g.refs > 1) g.page = page;
+            }
+        }
+        return g;
     };
+    Growth mine = {};
+    if (tid < t.B) mine = growth(tid);
+    look(0);
+    auto growth_of = [&](int b) { return b == tid ? mine : growth(b); };
     for (int b = tid; b < t.B; b += 1024) {
-        int S, n;
-        if (!grows(b, S, n)) continue;
-        const int page = shared_page(b, S);
-        if (page >= 0) p.share[page] = make_int2(0, -1);
+        const Growth g = growth_of(b);
+        if (g.page >= 0) p.share[g.page] = make_int2(0, -1);
     }
     __syncthreads();
     for (int b = tid; b < t.B; b += 1024) {
-        int S, n;
-        if (!grows(b, S, n)) continue;
-        const int page = shared_page(b, S);
-        if (page < 0) continue;
-        atomicAdd(&p.share[page].x, 1);
-        atomicMax(&p.share[page].y, b);
+        const Growth g = growth_of(b);
+        if (g.page < 0) continue;
+        atomicAdd(&p.share[g.page].x, 1);
+        atomicMax(&p.share[g.page].y, b);
     }
     __syncthreads();
     // what every sequence takes, and what those before it take
     int total = 0;
     for (int b0 = 0; b0 < t.B; b0 += 1024) {
         const int b = b0 + tid;
-        int take = 0, bits = 0, S, n;
-        if (b < t.B && grows(b, S, n)) {
-            const int page = shared_page(b, S);
-            take = t.pages(n) - t.pages(S);
-            if (page >= 0) {
-                // where all its holders grow, the last of them keeps it
-                const int2 s = __ldcg(&p.share[page]);
-                if (s.x == __ldcg(t.refs + page) && s.y == b) {
-                    bits = kKeeps;
-                } else {
-                    bits = kCopies;
-                    ++take;
+        int take = 0, bits = 0;
+        if (b < t.B) {
+            const Growth g = growth_of(b);
+            if (g.grows) {
+                take = t.pages(g.n) - t.pages(g.S);
+                if (g.page >= 0) {
+                    // where all its holders grow, the last of them keeps it
+                    const int2 s = __ldcg(&p.share[g.page]);
+                    if (s.x == g.refs && s.y == b) {
+                        bits = kKeeps;
+                    } else {
+                        bits = kCopies;
+                        ++take;
+                    }
                 }
             }
         }
@@ -184,17 +211,13 @@ __global__ void __launch_bounds__(1024) resize_kernel(const ResizeParams p) {
         total += all;
         __syncthreads();
     }
-    // the lowest free pages: a warp takes 256 counts at a time
+    // the lowest free pages
     for (int p0 = 0; p0 < t.num_pages && total > 0; p0 += 8192) {
-        uint32_t is_free[8];
-        int mine = 0;
+        if (p0 > 0) look(p0);
+        int free_here = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int page = p0 + 256 * warp + 32 * k + lane;
-            is_free[k] = __ballot_sync(0xffffffffu, page < t.num_pages && __ldcg(t.refs + page) == 0);
-            mine += __popc(is_free[k]);
-        }
-        if (lane == 0) sums[warp] = mine;
+        for (int k = 0; k < 8; ++k) free_here += __popc(is_free[k]);
+        if (lane == 0) sums[warp] = free_here;
         __syncthreads();
         int at = found + __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0);
         const int all = __reduce_add_sync(0xffffffffu, sums[lane]);
@@ -212,10 +235,10 @@ __global__ void __launch_bounds__(1024) resize_kernel(const ResizeParams p) {
     const int have = min(found, total);
     // hand them out, a warp per sequence
     for (int b = warp; b < t.B; b += 32) {
-        int S, n;
+        const int S = t.ctx[b], n = __ldg(p.new_lens + b);
+        const int2 need = p.need[b];
         int32_t copy[3] = {-1, -1, 0};
-        if (grows(b, S, n)) {
-            const int2 need = p.need[b];
+        if (n > S && t.len_ok(S) && t.len_ok(n)) {
             const int take = need.y & kTakes;
             // (a page is kept only where every other holder had one for its copy)
             if ((take > 0 || (need.y & kKeeps)) && static_cast<long long>(need.x) + take > have) {
@@ -339,9 +362,9 @@ pa_status resize_launch(const pa_shape& sh, int32_t* bt, int32_t* ctx, int32_t* 
     p.share = reinterpret_cast<int2*>(w + off);
     off += align_up(8 * static_cast<size_t>(sh.num_pages), 256);
     p.need = reinterpret_cast<int2*>(w + off);
-    p.chunks = (sh.max_pages_per_seq + 1023) / 1024;
-    const long long items = static_cast<long long>(sh.B) * p.chunks, most = 2ll * sm_count;
-    resize_kernel<<<static_cast<unsigned>(items < most ? items : most), 1024, 0, stream>>>(p);
+    p.chunks = (sh.max_pages_per_seq + 31) / 32;
+    const long long ctas = (static_cast<long long>(sh.B) * p.chunks + 31) / 32, most = 2ll * sm_count;
+    resize_kernel<<<static_cast<unsigned>(ctas < most ? ctas : most), 1024, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
