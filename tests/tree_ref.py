@@ -145,6 +145,10 @@ def attend(inp: Inputs, skip=()):
       additions each off by at most 2^-23 T (the tensor cores cut) make 2^-16 T;
       with the scaling and the exponential's own 2^-21 at most 2^-15 T + 2^-20
       relative in every p (T of the row's largest score, both in p and the sum);
+    * fp32 operands enter the products as two f16 parts, which hold all but 2^-22 of
+      a value (and 2^-40 of the largest of its 8 rows): q and k 2^-21 T together,
+      inside the 2^-16 T that the line above leaves; p and v 2^-21 relative, inside
+      the S 2^-24 below, whose worst case no sum of rounded terms comes near;
     * p of bf16 queries is rounded to bf16 over bf16 pages: 2^-8, and as much again
       as the row sum adds the rounded ones; over 4-bit pages to f16: 2^-11 from
       2^-14 on, below that its steps are 2^-24, so up to 2^-25 is lost of a p whose
