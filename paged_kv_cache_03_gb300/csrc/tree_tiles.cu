@@ -18,10 +18,11 @@
 //   * The key tiles of all segments are cut into equal shares, one per CTA (cluster), so
 //     ragged contexts leave no SM idle; a segment that crosses shares leaves fp32 partial
 //     states that tree_merge_kernel joins.
-//   * The key tiles of a piece go in turn to two slots t = 0, 1, each with its own S and P
-//     (P over S), O, m and l in Tensor Memory and one softmax warpgroup, one row per thread;
-//     both join them at the piece's end.  The MMA warp issues P V of tile i, then Q K^T of
-//     tile i + 2, so one slot's softmax overlaps the other's products.
+//   * Two slots t = 0, 1, one softmax warpgroup each with one row per thread, have their own
+//     P (over S), O, m and l in Tensor Memory and join them at the piece's end.  bf16 queries:
+//     each takes half of every tile's keys and S has two places; fp32 queries: the tiles go to
+//     the slots in turn.  One warp issues Q K^T and one P V, so products run beside both
+//     softmaxes.
 //   * The producer warps bring K and V into rings in the 128-byte swizzle that the MMA reads:
 //     one lane per page box by TMA (bf16, pages of a multiple of 8 slots), 16-byte
 //     asynchronous copies (other page sizes), or 4-bit rows dequantised on the way.
@@ -60,21 +61,21 @@ constexpr int kWholeTiles = 8;
 constexpr int kQTile = BM * kD * 2;
 enum Bar {
     kQFull = 0,     // + buffer: the query tile is there (4 bit: as it is)
-    kQReady = 2,    // + buffer: ... in f16 (4 bit)
-    kQEmpty = 4,    // + buffer: every Q K^T of its piece is done
-    kKFull = 6,     // + slot
-    kKEmpty = 9,    // + slot: in every CTA of the cluster
-    kVFull = 12,    // + slot
-    kVEmpty = 15,   // + slot
-    kVTail = 18,    // + slot: a tail tile's values are there, not yet cleaned (by TMA)
-    kSFull = 21,    // + t
-    kPFull = 23,    // + t
-    kODone = 25,    // + t
-    kOFree = 27,    // + t: the epilogue has read O
-    kXFull = 29,    // both slots' maxima and sums are there
-    kXFree = 30,    // ... and read
-    kMmaDone = 31,
-    kVScale = 32    // + tile & 3: the scales of V's rows are there (fp32 pages)
+    kQEmpty = 2,    // + buffer: every Q K^T of its piece is done
+    kKFull = 4,     // + slot
+    kKEmpty = 7,    // + slot: in every CTA of the cluster
+    kVFull = 10,    // + slot
+    kVEmpty = 13,   // + slot
+    kVTail = 16,    // + slot: a tail tile's values are there, not yet cleaned (by TMA)
+    kQReady = 16,   // + buffer: the query tile is there in f16 (f16 products)
+    kSFull = 19,    // + place of S
+    kPFull = 21,    // + place of P
+    kODone = 25,    // + place of the P that O has taken in
+    kOFree = 29,    // + t: the epilogue has read O
+    kXFull = 31,    // both slots' maxima and sums are there
+    kXFree = 32,    // ... and read
+    kMmaDone = 33,
+    kVScale = 34    // + tile & 3: the scales of V's rows are there (fp32 pages)
 };
 // bf16 queries: bf16 pages by TMA or by copies, 4-bit pages.  fp32 queries: fp32 pages,
 // 4-bit pages.
@@ -94,6 +95,10 @@ constexpr int threads(Source s) { return 32 * (producers(s) + 4 + 8); }
 constexpr int slots(Source s) { return is_f16(s) ? 2 : 3; }
 // Keys of a tile: two parts of 128 would leave no room for a second tile.
 constexpr int keys(Source s) { return s == kF32 ? 64 : 128; }
+// bf16 queries: each slot takes half of every tile's keys, and S has two places, so a slot's
+// softmax finds the next S there.  fp32 queries (products of three or two parts, which bound
+// them): the slots take the tiles in turn.
+constexpr bool halves(Source s) { return !fp32(s); }
 constexpr int raw_stages(Source s) { return s == kQ4 ? 3 : s == kQ4F ? 1 : 0; }
 // Published pieces: enough for producers that are that many tiles ahead, were each tile a
 // piece.
@@ -253,6 +258,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     constexpr bool F16 = is_f16(SRC), F32 = fp32(SRC);
     constexpr int kThreads = threads(SRC), kProd = producers(SRC), N = slots(SRC), I = items(SRC);
     constexpr int BN = keys(SRC), kTile = BN * kD * 2;
+    constexpr bool HALF = halves(SRC);
+    constexpr int UK = HALF ? BN / 2 : BN;  // keys of a slot's P
     constexpr int QP = q_parts(SRC), VP = kv_parts(SRC), kRing = VP * kTile;
     constexpr int kItemFull = item_bars(SRC), kItemEmpty = kItemFull + I;
     constexpr Smem M = smem(SRC);
@@ -277,11 +284,13 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar(kQFull + s), 1);
-            mbar_init(bar(kQReady + s), 4);
+            if (F16) mbar_init(bar(kQReady + s), 4);
             mbar_init(bar(kQEmpty + s), 1);
             mbar_init(bar(kSFull + s), 1);
-            mbar_init(bar(kPFull + s), 4);
-            mbar_init(bar(kODone + s), 1);
+            for (int b = 0; b < 4; b += 2) {
+                mbar_init(bar(kPFull + s + b), 4);
+                mbar_init(bar(kODone + s + b), 1);
+            }
             mbar_init(bar(kOFree + s), 8);
             mbar_init(bar(kXFull + s), 8);  // (and kXFree)
         }
@@ -294,11 +303,11 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         }
         if (SRC == kF32)
             for (int s = 0; s < 4; ++s) mbar_init(bar(kVScale + s), 4);
-        mbar_init(bar(kMmaDone), 1);
+        mbar_init(bar(kMmaDone), 2);
         for (int s = 0; s < I; ++s) {
             mbar_init(bar(kItemFull + s), 1);
-            // K/V warps, the MMA warp, the query warp, softmax warps
-            mbar_init(bar(kItemEmpty + s), (SRC == kTma ? 2 : kProd) + 2 + 8);
+            // K/V warps, the MMA warps, the query warp, softmax warps
+            mbar_init(bar(kItemEmpty + s), (SRC == kTma ? 2 : kProd) + 3 + 8);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -713,17 +722,19 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         if (!ok && lane == 0) give_up(p, abort_flag);
     } else if (warp < kProd + 4) {
         reg_set<regs(SRC).misc, launch_regs(SRC)>();
-        if (warp == kProd) {
-            // =========================== MMA issuer ===============================
+        if (warp < kProd + 2) {
+            // ========================== MMA issuers ==============================
+            // One warp for Q K^T, one for P V: what one spends on waits and issues, the other
+            // fills (one warp for both: 2000 cycles a tile of which the products are 1024).
             // The whole warp runs the loop and one elected lane issues.
             constexpr uint32_t idS = idesc(F16, BN, 0);  // Q, K both K-major
             constexpr uint32_t idO = idesc(F16, kD, 1);  // P K-major, V MN-major
             const uint64_t dQ0 = tc::smem_desc_sw128(base, 16, 1024);
             const uint64_t dK0 = tc::smem_desc_sw128(base + M.k, 16, kGroup);
             const uint64_t dV0 = tc::smem_desc_sw128(base + M.v, kHalf, kGroup);
-            const bool leader = elect_one();
-            Ring<N> kr, vr;
-            int pc0 = 0, pc1 = 0, oe0 = 0, oe1 = 0;
+            const bool leader = elect_one(), values = warp != kProd;
+            Ring<N> ring;
+            int g0 = 0, u0 = 0, u1 = 0, oe0 = 0, oe1 = 0;  // of earlier pieces: tiles, of each slot, epilogues
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 ok = take(k);
@@ -731,74 +742,87 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 const int n = slot(k)->n;
                 release(k);
                 if (n == 0) break;
-                const int buf = q_buf(k);
-                const uint64_t dq0 = tc::desc_advance(dQ0, buf * (QP * kQTile / 2)), dq1 = tc::desc_advance(dq0, p.q_half);
-                auto qk = [&](int i) {  // Q K^T of the piece's tile i
-                    if (!warp_wait(bar(kKFull + kr.s), kr.phase)) return false;
-                    tc::fence_after_sync();
-                    const uint64_t dk = tc::desc_advance(dK0, kr.s * kRing);
-                    const uint32_t d = tmem + 128u * (i & 1);
-                    if (leader) {
-                        // the products of the parts, the smallest first (low x low is left out)
+                if (!values) {
+                    const int buf = q_buf(k);
+                    const uint64_t dq0 = tc::desc_advance(dQ0, buf * (QP * kQTile / 2)), dq1 = tc::desc_advance(dq0, p.q_half);
+                    ok = warp_wait(bar((F16 ? kQReady : kQFull) + buf), q_use(k) & 1);
+                    for (int i = 0; ok && i < n; ++i, ring.next()) {
+                        // the place of S, and how often it was used
+                        const int place = (HALF ? g0 + i : i) & 1, use = HALF ? (g0 + i) >> 1 : (i & 1 ? u1 : u0) + (i >> 1);
+                        ok = warp_wait(bar(kKFull + ring.s), ring.phase);
+                        // (its P V, and with halves that of the other slot before it, has read P)
+                        if (ok && use > 0) ok = warp_wait(bar(kODone + (HALF ? 1 + 2 * place : place)), (use - 1) & 1);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        const uint64_t dk = tc::desc_advance(dK0, ring.s * kRing);
+                        const uint32_t d = tmem + 128u * place;
+                        if (leader) {
+                            // the products of the parts, the smallest first (low x low is left out)
 #pragma unroll
-                        for (int part = QP + VP - 2; part >= 0; --part) {
-                            const uint64_t qa = part == 1 ? tc::desc_advance(dq0, 2 * p.q_half) : dq0;
-                            const uint64_t qb = part == 1 ? tc::desc_advance(dq1, 2 * p.q_half) : dq1;
-                            const uint64_t ka = part == 2 ? tc::desc_advance(dk, kTile) : dk;
+                            for (int part = QP + VP - 2; part >= 0; --part) {
+                                const uint64_t qa = part == 1 ? tc::desc_advance(dq0, 2 * p.q_half) : dq0;
+                                const uint64_t qb = part == 1 ? tc::desc_advance(dq1, 2 * p.q_half) : dq1;
+                                const uint64_t ka = part == 2 ? tc::desc_advance(dk, kTile) : dk;
 #pragma unroll
-                            for (int kk = 0; kk < kD / 16; ++kk) {
-                                const uint64_t x = tc::desc_advance(kk < 4 ? qa : qb, (kk & 3) * 32);
-                                const uint64_t y = tc::desc_advance(ka, (kk >> 2) * kHalf + (kk & 3) * 32);
-                                if (kk == 0 && part == QP + VP - 2) tc::mma_bf16_c<0>(d, x, y, idS);
-                                else tc::mma_bf16_c<1>(d, x, y, idS);
+                                for (int kk = 0; kk < kD / 16; ++kk) {
+                                    const uint64_t x = tc::desc_advance(kk < 4 ? qa : qb, (kk & 3) * 32);
+                                    const uint64_t y = tc::desc_advance(ka, (kk >> 2) * kHalf + (kk & 3) * 32);
+                                    if (kk == 0 && part == QP + VP - 2) tc::mma_bf16_c<0>(d, x, y, idS);
+                                    else tc::mma_bf16_c<1>(d, x, y, idS);
+                                }
                             }
+                            tc::commit(bar(kSFull + place));
+                            if constexpr (C == 1) tc::commit(bar(kKEmpty + ring.s));
+                            else tc::commit_multicast(bar(kKEmpty + ring.s), kAll);
+                            if (i == n - 1) tc::commit(bar(kQEmpty + buf));
                         }
-                        tc::commit(bar(kSFull + (i & 1)));
-                        if constexpr (C == 1) tc::commit(bar(kKEmpty + kr.s));
-                        else tc::commit_multicast(bar(kKEmpty + kr.s), kAll);
-                        if (i == n - 1) tc::commit(bar(kQEmpty + buf));
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    kr.next();
-                    return true;
-                };
-                ok = warp_wait(bar((F16 ? kQReady : kQFull) + buf), q_use(k) & 1);
-                if (!ok) break;
-                ok = qk(0) && (n < 2 || qk(1));
-                for (int i = 0; ok && i < n; ++i) {
-                    const int t = i & 1, pc = t ? pc1++ : pc0++, oe = t ? oe1 : oe0;
-                    ok = warp_wait(bar(kVFull + vr.s), vr.phase) && warp_wait(bar(kPFull + t), pc & 1);
-                    // the previous piece's epilogue has read O
-                    if (ok && i < 2 && oe > 0) ok = warp_wait(bar(kOFree + t), (oe - 1) & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    const uint64_t dv = tc::desc_advance(dV0, vr.s * kRing);
-                    const uint32_t d = tmem + 256u + 128u * t, a = tmem + 128u * t;
-                    if (leader) {
+                } else {
+                    for (int i = 0; ok && i < n; ++i, ring.next()) {
+                        ok = warp_wait(bar(kVFull + ring.s), ring.phase);
+                        const uint64_t dv = tc::desc_advance(dV0, ring.s * kRing);
 #pragma unroll
-                        for (int part = QP + VP - 2; part >= 0; --part) {
-                            // two parts of P: 16 columns of each for 32 keys
-                            const uint32_t pa = a + (part == 1 ? 16u : 0u);
-                            const uint64_t va = part == 2 ? tc::desc_advance(dv, kTile) : dv;
+                        for (int h = 0; h < (HALF ? 2 : 1); ++h) {
+                            const int t = HALF ? h : i & 1, oe = t ? oe1 : oe0;  // the slot
+                            const int b = HALF ? (g0 + i) & 1 : 0, use = HALF ? (g0 + i) >> 1 : (t ? u1 : u0) + (i >> 1);
+                            ok = ok && warp_wait(bar(kPFull + t + 2 * b), use & 1);
+                            // the previous piece's epilogue has read O
+                            if (ok && i < (HALF ? 1 : 2) && oe > 0) ok = warp_wait(bar(kOFree + t), (oe - 1) & 1);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            const uint32_t d = tmem + 256u + 128u * t, a = tmem + (HALF ? 128u * b + UK * t : 128u * t);
+                            if (leader) {
 #pragma unroll
-                            for (int kk = 0; kk < BN / 16; ++kk) {
-                                const uint32_t x = pa + (QP == 1 ? kk * 8 : (kk >> 1) * 32 + (kk & 1) * 8);
-                                const uint64_t y = tc::desc_advance(va, kk * 2 * kGroup);
-                                if (kk == 0 && part == QP + VP - 2) tc::mma_bf16_ts(d, x, y, idO, i >= 2);
-                                else tc::mma_bf16_ts_c<1>(d, x, y, idO);
+                                for (int part = QP + VP - 2; part >= 0; --part) {
+                                    // two parts of P: 16 columns of each for 32 keys
+                                    const uint32_t pa = a + (part == 1 ? 16u : 0u);
+                                    const uint64_t va = part == 2 ? tc::desc_advance(dv, kTile) : dv;
+#pragma unroll
+                                    for (int kk = 0; kk < UK / 16; ++kk) {
+                                        const uint32_t x = pa + (QP == 1 ? kk * 8 : (kk >> 1) * 32 + (kk & 1) * 8);
+                                        const uint64_t y = tc::desc_advance(va, (h * (UK / 16) + kk) * 2 * kGroup);
+                                        if (kk == 0 && part == QP + VP - 2) tc::mma_bf16_ts(d, x, y, idO, i >= (HALF ? 1 : 2));
+                                        else tc::mma_bf16_ts_c<1>(d, x, y, idO);
+                                    }
+                                }
+                                tc::commit(bar(kODone + t + 2 * b));
+                                if (!HALF || h == 1) {
+                                    if constexpr (C == 1) tc::commit(bar(kVEmpty + ring.s));
+                                    else tc::commit_multicast(bar(kVEmpty + ring.s), kAll);
+                                }
                             }
+                            __syncwarp();
                         }
-                        tc::commit(bar(kODone + t));
-                        if constexpr (C == 1) tc::commit(bar(kVEmpty + vr.s));
-                        else tc::commit_multicast(bar(kVEmpty + vr.s), kAll);
+                        if (!ok) break;
                     }
-                    __syncwarp();
-                    vr.next();
-                    if (i + 2 < n) ok = qk(i + 2);
                 }
                 if (!ok) break;
+                g0 += n;
+                u0 += (n + 1) >> 1;
+                u1 += n >> 1;
                 ++oe0;
-                if (n > 1) ++oe1;
+                if (HALF || n > 1) ++oe1;
             }
             if (!ok && lane == 0) give_up(p, abort_flag);
             // nothing of ours may still be running when TMEM is freed
@@ -938,7 +962,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         // 64 dims each (one tile: A has them all).
         auto finish = [&](int k, float m1, float l1) {
             const volatile Item* const it = slot(k);
-            const bool both = it->n > 1;
+            const bool both = HALF || it->n > 1;
             const int m = it->mp * C + rank, rows = p.R - m * BM;
             const bool busy = q4 * 32 < rows, valid = r < rows;
             const int l = static_cast<unsigned>(m * BM + r) % static_cast<unsigned>(p.L);  // draft
@@ -961,8 +985,13 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 m1 = mm;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kXFree));
-                ok = warp_wait(bar(kODone), (it->before[0] + ((it->n + 1) >> 1) - 1) & 1) &&
-                     warp_wait(bar(kODone + 1), (it->before[1] + (it->n >> 1) - 1) & 1);
+                if constexpr (HALF) {
+                    const int g = it->before[0] + it->before[1] + it->n - 1, b = 2 * (g & 1);
+                    ok = warp_wait(bar(kODone + b), (g >> 1) & 1) && warp_wait(bar(kODone + 1 + b), (g >> 1) & 1);
+                } else {
+                    ok = warp_wait(bar(kODone), (it->before[0] + ((it->n + 1) >> 1) - 1) & 1) &&
+                         warp_wait(bar(kODone + 1), (it->before[1] + (it->n >> 1) - 1) & 1);
+                }
                 if (!ok) return false;
             } else if (t == 0) {
                 ok = warp_wait(bar(kODone), it->before[0] & 1);
@@ -1035,9 +1064,10 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         for (int k = 0;; ++k) {
             ok = take(k);
             if (!ok) break;
-            const int n = slot(k)->n, nk = (n + 1 - t) >> 1;  // this slot's tiles
+            const int n = slot(k)->n, nk = HALF ? n : (n + 1 - t) >> 1;  // this slot's tiles
             if (n == 0) break;
-            const int sc = slot(k)->before[t], S = slot(k)->S, first = S - p.L;
+            const int sc = slot(k)->before[t], g0 = slot(k)->before[0] + slot(k)->before[1];
+            const int S = slot(k)->S, first = S - p.L;
             const int m = slot(k)->mp * C + rank;  // query tile
             const int rows = p.R - m * BM;         // of which a tile has at most BM
             const bool busy = q4 * 32 < rows, valid = r < rows;
@@ -1118,24 +1148,26 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             float mrow = neg_inf();
             float2 lsum = make_float2(0.f, 0.f);
             for (int j = 0; j < nk; ++j) {
-                const int jt = slot(k)->j0 + 2 * j + t;  // key tile
-                uint32_t see[BN / 32];
+                const int i = HALF ? j : 2 * j + t, jt = slot(k)->j0 + i;  // key tile
+                // the places of S, P and their uses before
+                const int b = HALF ? (g0 + j) & 1 : 0, use = HALF ? (g0 + j) >> 1 : sc + j;
+                uint32_t see[UK / 32];
                 if (busy && jt >= tail) {  // this row's bits of the tile, while S is on its way
-                    const int x = jt * BN - first;
+                    const int x = jt * BN + (HALF ? UK * t : 0) - first;
                     const int w0 = x >> 5, sh = x & 31;  // (floor: words before the drafts are all ones)
-                    uint32_t w[BN / 32 + 1];
+                    uint32_t w[UK / 32 + 1];
 #pragma unroll
-                    for (int i = 0; i < BN / 32 + 1; ++i) {
-                        const int wi = w0 + i;
-                        w[i] = wi < 0 ? 0xffffffffu : wi < p.W ? __ldg(mask + wi) & slot(k)->live[wi] : 0u;
+                    for (int e = 0; e < UK / 32 + 1; ++e) {
+                        const int wi = w0 + e;
+                        w[e] = wi < 0 ? 0xffffffffu : wi < p.W ? __ldg(mask + wi) & slot(k)->live[wi] : 0u;
                     }
 #pragma unroll
-                    for (int i = 0; i < BN / 32; ++i) see[i] = __funnelshift_r(w[i], w[i + 1], sh);
+                    for (int e = 0; e < UK / 32; ++e) see[e] = __funnelshift_r(w[e], w[e + 1], sh);
                 }
-                ok = warp_wait(bar(kSFull + t), (sc + j) & 1);
+                ok = warp_wait(bar(kSFull + (HALF ? b : t)), use & 1);
                 if (!ok || aborted(abort_flag)) break;
                 if constexpr (SRC == kF32) {  // the scales of this tile's V
-                    const int tile = slot(k)->before[0] + slot(k)->before[1] + 2 * j + t;
+                    const int tile = g0 + i;
                     ok = warp_wait(bar(kVScale + (tile & 3)), (tile >> 2) & 1);
                     if (!ok) break;
                 }
@@ -1150,7 +1182,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 }
                 if (busy) {
                     tc::fence_after_sync();
-                    const uint32_t st = trow + 128u * t;
+                    const uint32_t st = trow + (HALF ? 128u * b + UK * t : 128u * t);
                     float2 ts = make_float2(0.f, 0.f);
                     float mx = neg_inf(), alpha = 1.f;
                     // 32 scores: masked, and the largest of them and mx
@@ -1182,7 +1214,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     // the tile's maximum from all of S; true where the row's moved
                     auto maximum = [&]() {
 #pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) {
+                        for (int cc = 0; cc < UK / 32; ++cc) {
                             float x[32];
                             tc::ld32(st + cc * 32, x);
                             tc::wait_ld();
@@ -1198,7 +1230,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     };
                     // O is rescaled once this slot's previous P V is done
                     auto rescale = [&]() {
-                        if (!warp_wait(bar(kODone + t), (sc + j - 1) & 1)) return false;
+                        const int g = g0 + j - 1;
+                        if (!warp_wait(bar(kODone + t + (HALF ? 2 * (g & 1) : 0)), (HALF ? g >> 1 : sc + j - 1) & 1)) return false;
                         tc::fence_after_sync();
 #pragma unroll 1
                         for (int cc = 0; cc < 4; ++cc) {
@@ -1212,14 +1245,14 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         tc::wait_st();
                         return true;
                     };
-                    // P goes over the first 64 columns of this slot's S
+                    // P goes over the first columns of its S
                     if constexpr (F32) {
                         // Two parts of P do not fit the registers beside S: S is read twice, and 32
                         // keys' P lies over their own scores.  fp32 pages: V's rows were scaled by
                         // 2^v (by eights), so P is 2^(score - v - maximum), the maximum that of score
                         // - v, and the sum adds P 2^v: the weights relative to that maximum.
                         const float4* const scales = reinterpret_cast<const float4*>(smem_raw + M.kv_scale);
-                        const int tile = slot(k)->before[0] + slot(k)->before[1] + 2 * j + t;
+                        const int tile = g0 + i;
                         auto scores = [&](float (&x)[32], int cc, float4& vs) {
                             tc::ld32(st + cc * 32, x);
                             float kf[4] = {c, c, c, c}, off[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1281,20 +1314,18 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         // Against the maximum so far: no weight waits for the scores behind it.  Only
                         // where that was too low by 2^kSlack (or there was none) is the tile done
                         // again, with its own maximum.
-                        uint32_t pw[64];
+                        uint32_t pw[UK / 2];
                         bool again = true;
                         if (j > 0) {
                             const float mu = mrow == neg_inf() ? 0.f : mrow;
-                            constexpr int kLoads = F16 ? 1 : 2;  // 32 columns each in flight (registers)
-                            float x[kLoads][32];
-                            if constexpr (kLoads > 1) tc::ld32(st, x[0]);
+                            float x[2][32];
+                            tc::ld32(st, x[0]);
 #pragma unroll
-                            for (int cc = 0; cc < 4; ++cc) {
-                                if constexpr (kLoads == 1) tc::ld32(st + cc * 32, x[0]);
+                            for (int cc = 0; cc < UK / 32; ++cc) {
                                 tc::wait_ld();
-                                if (kLoads > 1 && cc < 3) tc::ld32(st + cc * 32 + 32, x[(cc + 1) & (kLoads - 1)]);
-                                largest(x[cc & (kLoads - 1)], cc);
-                                weights(x[cc & (kLoads - 1)], pw + 16 * cc, mu);
+                                if (cc + 1 < UK / 32) tc::ld32(st + cc * 32 + 32, x[(cc + 1) & 1]);
+                                largest(x[cc & 1], cc);
+                                weights(x[cc & 1], pw + 16 * cc, mu);
                             }
                             again = __any_sync(0xffffffffu, valid && mx * c > mrow + kSlack);
                         }
@@ -1307,7 +1338,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             ts = make_float2(0.f, 0.f);
                             const float mu = mrow == neg_inf() ? 0.f : mrow;
 #pragma unroll
-                            for (int cc = 0; cc < 4; ++cc) {
+                            for (int cc = 0; cc < UK / 32; ++cc) {
                                 float x[32];
                                 tc::ld32(st + cc * 32, x);
                                 tc::wait_ld();
@@ -1315,8 +1346,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                                 weights(x, pw + 16 * cc, mu);
                             }
                         }
-                        tc::st32(st, *reinterpret_cast<const uint32_t(*)[32]>(pw));
-                        tc::st32(st + 32, *reinterpret_cast<const uint32_t(*)[32]>(pw + 32));
+                        tc::st32(st, pw);
                     }
                     lsum.x = lsum.x * alpha + ts.x;
                     lsum.y = lsum.y * alpha + ts.y;
@@ -1324,7 +1354,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     tc::fence_before_sync();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kPFull + t));
+                if (lane == 0) mbar_arrive(bar(kPFull + t + 2 * b));
             }
             if (!ok || aborted(abort_flag)) break;
             ok = finish(k, mrow, lsum.x + lsum.y);
