@@ -7,7 +7,7 @@
 // the end ("tail"); there a row's 128 bits come out of its words of the tree's mask.
 //   S = Q K^T,  P = 2^(scale S - m),  O += P V,  with a maximum m and the sum l per row;
 //   O / l at the end.
-// bf16 pages: P rounded to bf16, l adds the rounded ones.  4-bit pages: K and V dequantised
+// bf16 pages: P rounded to bf16.  4-bit pages: K and V dequantised
 // to f16 on chip (exact), Q scaled by a power of two into f16's range (exact), P rounded to
 // f16 (2^-11).
 //
@@ -267,6 +267,9 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     // [half][BN rows][128 bytes].
     constexpr uint32_t kHalf = SRC == kTma ? 1024u : BN * 128u, kGroup = SRC == kTma ? 2048u : 1024u;
     constexpr uint16_t kAll = (1u << C) - 1u;
+    // By TMA, K and V come from a warp each in clusters, where K is read ahead of V (256 rows:
+    // 145 us from one warp, 139 from two), else from one (at the rate of HBM: 320 and 327).
+    constexpr bool kApart = C > 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     auto bar = [&](int i) { return base + M.bar + 8u * static_cast<uint32_t>(i); };
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         for (int s = 0; s < I; ++s) {
             mbar_init(bar(kItemFull + s), 1);
             // K/V warps, the MMA warps, the query warp, softmax warps
-            mbar_init(bar(kItemEmpty + s), (SRC == kTma ? 2 : kProd) + 3 + 8);
+            mbar_init(bar(kItemEmpty + s), (SRC != kTma ? kProd : kApart ? 3 : 2) + 3 + 8);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -416,7 +419,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         reg_set<regs(SRC).producer, launch_regs(SRC)>();
         bool ok = true;
         if constexpr (SRC == kTma) {
-            if (warp == 0) {
+            if (warp == 0 || (kApart && warp == 2)) {
+                const bool keys = warp == 0, values = !kApart || warp == 2;
                 const uint64_t policy = p.nG == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
                 const int nbox = BN / p.box;
                 bool bad_page = false;
@@ -459,7 +463,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             }
                             return true;
                         };
-                        ok = load(kKEmpty, kKFull, M.k, &kmap) && load(kVEmpty, j >= tail ? kVTail : kVFull, M.v, &vmap);
+                        ok = (!keys || load(kKEmpty, kKFull, M.k, &kmap)) &&
+                             (!values || load(kVEmpty, j >= tail ? kVTail : kVFull, M.v, &vmap));
                         if (!ok) break;
                     }
                 }
@@ -467,8 +472,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 // give those in flight time to land before the shared memory goes.
                 if (!ok)
                     for (int s = 0; s < N; ++s) {
-                        mbar_wait_for(bar(kKFull + s), g.phase ^ (s >= g.s), 50000000ull);
-                        mbar_wait_for(bar(kVFull + s), g.phase ^ (s >= g.s), 50000000ull);
+                        if (keys) mbar_wait_for(bar(kKFull + s), g.phase ^ (s >= g.s), 50000000ull);
+                        if (values) mbar_wait_for(bar(kVFull + s), g.phase ^ (s >= g.s), 50000000ull);
                     }
                 if (__any_sync(0xffffffffu, bad_page) && lane == 0) atomicOr(p.flag, PA_FLAG_BAD_PAGE);
             } else if (warp == 1) {
@@ -1185,13 +1190,14 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     const uint32_t st = trow + (HALF ? 128u * b + UK * t : 128u * t);
                     float2 ts = make_float2(0.f, 0.f);
                     float mx = neg_inf(), alpha = 1.f;
-                    // 32 scores: masked, and the largest of them and mx
-                    auto largest = [&](float (&x)[32], int cc) {
-                        if (jt >= tail) {
+                    // 32 scores of a tail tile, those that this row does not see masked
+                    auto hide = [&](float (&x)[32], int cc) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(see[cc] >> e & 1u)) x[e] = neg_inf();
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see[cc] >> e & 1u)) x[e] = neg_inf();
+                    };
+                    // the largest of 32 scores and mx
+                    auto largest = [&](const float (&x)[32]) {
                         float a = fmax3(x[0], x[1], mx), b = x[2];
 #pragma unroll
                         for (int e = 3; e < 31; e += 4) {
@@ -1208,7 +1214,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), c2, nm2);
                             const float2 ex = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                             w[i] = F16 ? pack_f16x2(ex.x, ex.y) : pack_bf16x2(ex.x, ex.y);
-                            ts = __fadd2_rn(ts, F16 ? ex : bf16x2_to_float2(w[i]));
+                            ts = __fadd2_rn(ts, ex);
                         }
                     };
                     // the tile's maximum from all of S; true where the row's moved
@@ -1218,7 +1224,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             float x[32];
                             tc::ld32(st + cc * 32, x);
                             tc::wait_ld();
-                            largest(x, cc);
+                            if (jt >= tail) hide(x, cc);
+                            largest(x);
                         }
                         const float mt = mx * c;
                         const bool grow = valid && mt > mrow;  // (other rows hold anything)
@@ -1318,14 +1325,18 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         bool again = true;
                         if (j > 0) {
                             const float mu = mrow == neg_inf() ? 0.f : mrow;
-                            float x[2][32];
-                            tc::ld32(st, x[0]);
+                            float x[UK / 32][32];
+#pragma unroll
+                            for (int cc = 0; cc < UK / 32; ++cc) tc::ld32(st + cc * 32, x[cc]);
+                            tc::wait_ld();
+                            if (jt >= tail) {
+#pragma unroll
+                                for (int cc = 0; cc < UK / 32; ++cc) hide(x[cc], cc);
+                            }
 #pragma unroll
                             for (int cc = 0; cc < UK / 32; ++cc) {
-                                tc::wait_ld();
-                                if (cc + 1 < UK / 32) tc::ld32(st + cc * 32 + 32, x[(cc + 1) & 1]);
-                                largest(x[cc & 1], cc);
-                                weights(x[cc & 1], pw + 16 * cc, mu);
+                                largest(x[cc]);
+                                weights(x[cc], pw + 16 * cc, mu);
                             }
                             again = __any_sync(0xffffffffu, valid && mx * c > mrow + kSlack);
                         }
@@ -1342,7 +1353,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                                 float x[32];
                                 tc::ld32(st + cc * 32, x);
                                 tc::wait_ld();
-                                if (jt >= tail) largest(x, cc);
+                                if (jt >= tail) hide(x, cc);
                                 weights(x, pw + 16 * cc, mu);
                             }
                         }
