@@ -1152,8 +1152,9 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             const int tail = first_tail(S);
             float mrow = neg_inf();
             float2 lsum = make_float2(0.f, 0.f);
+            const int j0 = slot(k)->j0;
             for (int j = 0; j < nk; ++j) {
-                const int i = HALF ? j : 2 * j + t, jt = slot(k)->j0 + i;  // key tile
+                const int i = HALF ? j : 2 * j + t, jt = j0 + i;  // key tile
                 // the places of S, P and their uses before
                 const int b = HALF ? (g0 + j) & 1 : 0, use = HALF ? (g0 + j) >> 1 : sc + j;
                 uint32_t see[UK / 32];
