@@ -168,7 +168,8 @@ struct TileParams {
     uint32_t* flag;
     float2* part_ml;  // [2 per CTA][128]: max, sum
     float* part_o;    // [2 per CTA][128][D]
-    int4* split;      // per share: the segment that starts in it and ends in a later one
+    int4* split;      // per share: the segment that starts in it and ends in a later one,
+    int* join;        // and the share in which the segment that comes into it starts (-1: none)
     int B, H_kv, R, L, W, nG, num_pages, ps, max_npg;  // nG: groups of C query tiles
     int pool_rows, box;          // rows of the pool, of a K/V box
     int q_box, q_half, q_bufs;   // rows of a query box, bytes of 64 dims of a buffer, buffers
@@ -875,6 +876,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 seg = p.whole ? 0 : first_unit + i * (kSegCost + ng);
             }
             int4 crossing = make_int4(-1, 0, 0, 0);
+            int from = -1;  // the share in which the segment that comes into this one starts
             int before0 = 0, before1 = 0;
             // lane w: word w of the slots of sequence live_b that hold a draft
             int live_b = start < end ? first_b : -1;
@@ -930,6 +932,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     o->before[1] = before1;
                     before0 += (n + 1) / 2;
                     before1 += n / 2;
+                    if (n > 0 && j0 > 0) from = (seg + kSegCost) / per;
                     if (n > 0 && j0 == 0 && n < ng)  // it ends in a later share
                         crossing = make_int4(b, kvh, mp, (seg + kSegCost + ng - 1) / per);
                     mbar_arrive(bar(kItemFull + k % I));
@@ -949,7 +952,10 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     }
                 }
             }
-            if (lane == 0 && rank == 0 && !p.whole) p.split[my_share] = crossing;
+            if (lane == 0 && rank == 0 && !p.whole) {
+                p.split[my_share] = crossing;
+                p.join[my_share] = from;
+            }
             if (!ok && lane == 0) give_up(p, abort_flag);
         }
         __syncwarp();
@@ -1385,49 +1391,42 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     if constexpr (C > 1) cluster_sync();  // peers' copies and commits come here until they are done
 }
 
-// Merges the partial states of the segments that cross shares: CTA y + ny c takes rows
-// 32 y .. of the segment that starts in share c, four a warp, two partial states of each in
-// flight.  C: CTAs of a share, one query tile each.
-constexpr int kMergeRows = 4;
-template <bool F32>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const TileParams p, int ny, int C) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = static_cast<int>(blockIdx.x) / ny;
-    const int r0 = kMergeRows * (8 * (static_cast<int>(blockIdx.x) - c * ny) + warp);
-    pdl_wait_primary();
-    const int4 sp = p.split[c];
-    const int in_head = sp.z * C * BM + r0;
-    if (sp.x < 0 || in_head >= p.R) return;
-    uint32_t drafted[kMergeRows];  // a word of the row's mask
-    float M[kMergeRows], sum[kMergeRows];
-    float4 acc[kMergeRows];
+// Rows r .. r + ROWS - 1 of the segment that starts in share c and ends in share sp.w, its
+// partial states U at a time: four loads in flight.
+template <bool F32, int ROWS, int U>
+__device__ __forceinline__ void merge_rows(const TileParams& p, int C, const int4 sp, int c, int r) {
+    const int lane = threadIdx.x & 31;
+    const int in_head = sp.z * C * BM + r;
+    if (r >= C * BM || in_head >= p.R) return;
+    uint32_t drafted[ROWS];  // a word of the row's mask
+    float M[ROWS], sum[ROWS];
+    float4 acc[ROWS];
 #pragma unroll
-    for (int i = 0; i < kMergeRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         const uint32_t* const m = p.mask + (static_cast<long long>(sp.x) * p.L + (in_head + i) % p.L) * p.W;
         drafted[i] = lane < p.W ? __ldg(m + lane) : 0u;
         M[i] = neg_inf();
         sum[i] = 0.f;
         acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    constexpr int U = 2;
     for (int k = c; k <= sp.w; k += U) {
-        float2 v[U][kMergeRows];
-        float4 x[U][kMergeRows];
+        float2 v[U][ROWS];
+        float4 x[U][ROWS];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < kMergeRows; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 v[u][i] = make_float2(neg_inf(), 0.f);
                 if (k + u > sp.w || in_head + i >= p.R) continue;
-                const int cta = (k + u) * C + (r0 + i) / BM;
-                const long long slot = (2ll * cta + (k + u == c ? 1 : 0)) * BM + (r0 + i) % BM;
+                const int cta = (k + u) * C + (r + i) / BM;
+                const long long slot = (2ll * cta + (k + u == c ? 1 : 0)) * BM + (r + i) % BM;
                 v[u][i] = p.part_ml[slot];
                 x[u][i] = *reinterpret_cast<const float4*>(p.part_o + slot * kD + 4 * lane);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < kMergeRows; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 if (v[u][i].y == 0.f) continue;  // no key (x was not written)
                 const float mx = fmaxf(M[i], v[u][i].x), a = fast_exp2(M[i] - mx), b = fast_exp2(v[u][i].x - mx);
                 M[i] = mx;
@@ -1439,7 +1438,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TileParams p, int
             }
     }
 #pragma unroll
-    for (int i = 0; i < kMergeRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         const bool live = __any_sync(0xffffffffu, drafted[i] != 0u);
         if (in_head + i >= p.R) continue;
         const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];  // (0: a row without keys; NaN stays)
@@ -1454,8 +1453,26 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TileParams p, int
     }
 }
 
+// Merges the partial states of the segments that cross shares.  The ny CTAs of a share take
+// part in the segment that comes into it, so one cut into many pieces has as many CTAs, a
+// warp a row of it (one sequence of 16000 keys: 33 us in all with the CTAs of its first share
+// alone, 27 with all).  What it takes is its launch and L2's latency: 4 to 7 us of a call.
+constexpr int kMergeRows = 2;
+template <bool F32>
+__global__ void __launch_bounds__(256, 3) tree_merge_kernel(const TileParams p, int ny, int C) {
+    const int k = static_cast<int>(blockIdx.x) / ny, y = static_cast<int>(blockIdx.x) - k * ny;
+    pdl_wait_primary();
+    const int c = p.join[k];
+    if (c < 0) return;
+    const int4 sp = p.split[c];
+    if (sp.x < 0) return;  // (a share that gave up)
+    const int groups = sp.w - c, at = ((k - c - 1) * ny + y) * 8 + static_cast<int>(threadIdx.x >> 5);
+    if (groups == 1) merge_rows<F32, kMergeRows, 2>(p, C, sp, c, at * kMergeRows);
+    else merge_rows<F32, 1, 4>(p, C, sp, c, at);
+}
+
 struct TilePlan {
-    size_t split_off, ml_off, o_off, total;
+    size_t split_off, join_off, ml_off, o_off, total;
 };
 
 // (the same for every shape)
@@ -1463,7 +1480,8 @@ TilePlan plan(int sm_count) {
     TilePlan t;
     const size_t states = 2ull * sm_count * BM;
     t.split_off = kFlagBytes;
-    t.ml_off = align_up(t.split_off + 16ull * sm_count, 256);
+    t.join_off = t.split_off + 16ull * sm_count;
+    t.ml_off = align_up(t.join_off + 4ull * sm_count, 256);
     t.o_off = align_up(t.ml_off + states * 8, 256);
     t.total = t.o_off + states * kD * 4;
     return t;
@@ -1575,6 +1593,7 @@ pa_status tree_launch(const TreeCall& c) {
     p.part_ml = reinterpret_cast<float2*>(ws + t.ml_off);
     p.part_o = reinterpret_cast<float*>(ws + t.o_off);
     p.split = reinterpret_cast<int4*>(ws + t.split_off);
+    p.join = reinterpret_cast<int*>(ws + t.join_off);
     p.B = sh.B;
     p.H_kv = sh.H_kv;
     p.R = sh.H_q / sh.H_kv * sh.L;
