@@ -34,7 +34,8 @@ struct PagesParams {
 
 // ---- fork -------------------------------------------------------------------------
 // One CTA per fork.  What a CTA reads of the table and the lengths no other writes:
-// a target appears once (later ones are refused) and no source is a target.
+// a target appears once (later ones are refused) and no source is a target.  Bound by the
+// atomics of shared pages: 64 forks of up to 32 pages 4 us, 48 of up to 2000 pages 7.
 __global__ void __launch_bounds__(256) fork_kernel(const PagesParams p, const int32_t* sources, const int32_t* targets,
                                                    const int32_t* lens, int n) {
     const int f = blockIdx.x, tid = threadIdx.x;
@@ -98,7 +99,8 @@ struct Growth {
 // pages and hands them out, so growing sequences can have what shrinking ones gave up.
 // Releasing is bound by the rate of atomics and spreads over the SMs; handing out is a
 // chain of short steps on one SM, each a round trip to L2: what a sequence is about to do is
-// read once where a thread has one sequence, and the first counts are read ahead.
+// read once where a thread has one sequence, and the first counts are read ahead.  80
+// rows 9 to 11 us, where 64 end and where 64 grow.
 __global__ void __launch_bounds__(1024) resize_kernel(const ResizeParams p) {
     const PagesParams& t = p.t;
     __shared__ int sums[32];
@@ -294,7 +296,8 @@ __device__ __forceinline__ void copy_units(U* dst, const U* src, long long n) {
 }
 
 // A CTA per (copy, kv head) and buffer: the first rows of one page to another, one
-// contiguous run of bytes.  Bound by HBM.
+// contiguous run of bytes.  Bound by HBM, few by latency: 64 copies of up to 128 rows of 8
+// heads in bf16 9 us.
 __global__ void __launch_bounds__(256) copy_pages_kernel(const CopyParams p) {
     const int i = static_cast<int>(blockIdx.x) / p.H_kv, h = static_cast<int>(blockIdx.x) - i * p.H_kv;
     const int src = p.copies[3ll * i], dst = p.copies[3ll * i + 1], rows = p.copies[3ll * i + 2];

@@ -1,15 +1,19 @@
-// tree_tiles.cu -- attention of drafted trees for bf16 queries on tcgen05 tensor cores,
-// over bf16 and 4-bit pages.
+// tree_tiles.cu -- attention of drafted trees on tcgen05 tensor cores: bf16 queries over
+// bf16 and 4-bit pages, fp32 queries over fp32 and 4-bit pages.
 //
 // The rows of a (sequence, kv head), r = (query head of the group, draft l), are R = G L
 // consecutive rows of the query, cut into tiles of 128.  All of them see every position
-// before the drafts, so a key tile of 128 needs no mask unless it holds drafts or lies at
-// the end ("tail"); there a row's 128 bits come out of its words of the tree's mask.
+// before the drafts, so a key tile needs no mask unless it holds drafts or lies at the end
+// ("tail"); there a row's bits come out of its words of the tree's mask.
 //   S = Q K^T,  P = 2^(scale S - m),  O += P V,  with a maximum m and the sum l per row;
 //   O / l at the end.
-// bf16 pages: P rounded to bf16.  4-bit pages: K and V dequantised
-// to f16 on chip (exact), Q scaled by a power of two into f16's range (exact), P rounded to
-// f16 (2^-11).
+// m is the largest score when it was last too low by 2^kSlack (or there was none): a weight
+// does not wait for the scores behind it, and O is rescaled only then.
+// bf16 pages: P rounded to bf16 (2^-8).  4-bit pages: K and V dequantised to f16 on chip
+// (exact), Q scaled by a power of two into f16's range (exact), P rounded to f16 (2^-11).
+// fp32: Q, K, V and P in two f16 parts each, x = h + l up to 2^-22 x, and products h h + h l
+// + l h (l l is below 2^-22); rows are scaled into f16's range by powers of two, K and V by
+// eights of rows, and K's scale is undone in the scores, V's in the weights.
 //
 // Layout on GB300: one CTA per SM.
 //   * A segment is one query tile of one (sequence, kv head) over all its key tiles, or, over
@@ -25,7 +29,7 @@
 //     softmaxes.
 //   * The producer warps bring K and V into rings in the 128-byte swizzle that the MMA reads:
 //     one lane per page box by TMA (bf16, pages of a multiple of 8 slots), 16-byte
-//     asynchronous copies (other page sizes), or 4-bit rows dequantised on the way.
+//     asynchronous copies (other page sizes), or rows converted on the way (4 bits, fp32).
 //   * One warp publishes the pieces of segments in a ring, with the bits of the slots that
 //     hold drafts, and another loads the query tiles by TMA.
 //   * Value rows that nobody sees (behind the context, slots without a draft) may hold
@@ -33,6 +37,17 @@
 //     before the tile is announced.
 //   * All waits are bounded; on a timeout the CTA records PA_FLAG_TIMEOUT, frees its TMEM
 //     and exits.
+//
+// Measured (G = 4, H_kv = 8, a call among others, with the merge):
+//   64 sequences of 128 .. 4096 keys, 64 rows    89 us, 6.4 TB/s of rows: bound by HBM
+//   16 of 32768, 128 rows, pages of 16          320 us, 6.7 TB/s
+//   16 of 1000 .. 8000, 252 rows                 78 us, 940 TFLOP/s: a tile takes
+//     1750 cycles, of them 1024 products at the peak rate; Q, K, V and TMA's stores pass
+//     through shared memory in 1280.  Without exponentials it is no faster, without maxima
+//     and sums 9%
+//   32 of 500 .. 8000 in 4 bits, 96 rows         81 us: a tile takes 2170 cycles, the softmax
+//     beside eight converting warps
+//   8 of 1000 .. 8000 in fp32, 64 / 256 rows     97 / 183 us: conversion / three products
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -51,9 +66,10 @@ constexpr int kD = kHeadDim;
 constexpr int BM = 128;  // query rows of a tile
 constexpr uint32_t kTmemCols = 512;  // S of slot t at 128 t, O at 256 + 128 t
 // What a segment's query load, first softmax and epilogue cost, in key tiles: the
-// shares count it, or CTAs with many short segments would finish last.
+// shares count it, or CTAs with many short segments would finish last.  (Of 64 sequences,
+// 256 rows take 158, 154 and 151 us with 3, 4 and 5, 64 rows 91, 91 and 94.)
 constexpr int kSegCost = 4;
-constexpr int kMinPer = 8;  // least cost of a share
+constexpr int kMinPer = 8;  // least cost of a share (6 and 12: the same within noise)
 // Where there is a CTA for each segment and tables hold at most so many key tiles, segments
 // stay whole and there is no merge: alone with 1000 / 2000 keys of bf16, 17 / 27 us whole
 // and 19 / 21 cut; of fp32 with 500 / 1000 keys, 26 / 44 whole and 29 / 30 cut.
@@ -96,8 +112,9 @@ constexpr int slots(Source s) { return is_f16(s) ? 2 : 3; }
 // Keys of a tile: two parts of 128 would leave no room for a second tile.
 constexpr int keys(Source s) { return s == kF32 ? 64 : 128; }
 // bf16 queries: each slot takes half of every tile's keys, and S has two places, so a slot's
-// softmax finds the next S there.  fp32 queries (products of three or two parts, which bound
-// them): the slots take the tiles in turn.
+// softmax finds the next S there (with whole tiles in turn and one place each 256 rows of 64
+// sequences took 154 us, not 139, and contexts of 100 .. 500 keys 43, not 34).  fp32 queries
+// (products of three or two parts, which bound them): the slots take the tiles in turn.
 constexpr bool halves(Source s) { return !fp32(s); }
 constexpr int raw_stages(Source s) { return s == kQ4 ? 3 : s == kQ4F ? 1 : 0; }
 // Published pieces: enough for producers that are that many tiles ahead, were each tile a
@@ -969,8 +986,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         constexpr float kSlack = F16 ? 8.f : 64.f;
         int xc = 0;  // pieces whose states were joined
         bool ok = true;
-        // The end of piece k, with this slot's maximum and sum.  The two slots' states of a row are joined by both warpgroups,
-        // 64 dims each (one tile: A has them all).
+        // The end of piece k, with this slot's maximum and sum.  The two slots' states of a row
+        // are joined by both warpgroups, 64 dims each (one tile: A has them all).
         auto finish = [&](int k, float m1, float l1) {
             const volatile Item* const it = slot(k);
             const bool both = HALF || it->n > 1;
