@@ -15,15 +15,15 @@ namespace {
 //
 // One CTA per sequence, warp k drafts 32 k .. 32 k + 31.  A parent comes before its
 // children, so within a warp five rounds of pointer doubling by shuffles give every draft
-// its ancestors in the warp and the one before them (`up`); then 32 drafts after 32 take
-// over the finished words of `up`, all warps together.  Bound by that chain of steps: 64
-// trees of 64 drafts 4 us, 8 of 1001 drafts 14 us (32 rounds of a barrier and two trips to
-// shared memory).
+// its ancestors in the warp, one word, and the one before them (`up`); then every draft
+// follows the `up`s, at most one a warp before its own, and takes their words.  A chain of
+// latencies: 64 trees of 64 drafts 2.2 us, 8 of 1001 drafts 7 us (14 when all warps took 32
+// drafts after 32 with a barrier for each).
 __global__ void __launch_bounds__(1024) tree_mask_kernel(const int32_t* parents, uint32_t* mask, int32_t* depths,
                                                          uint32_t* flag, int L, int W) {
-    extern __shared__ uint32_t rows[];  // [32 W][W | 1], then [32 W] of `up`
+    extern __shared__ uint32_t rows[];  // [32 W][W | 1], then [32 W] of word and `up`
     const int stride = W | 1;           // odd: a word of 32 rows lies in 32 banks
-    int* const ups = reinterpret_cast<int*>(rows + 32 * W * stride);
+    int2* const drafts = reinterpret_cast<int2*>(rows + 32 * W * stride);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long first = static_cast<long long>(blockIdx.x) * L;
     const int parent = tid < L ? __ldg(parents + first + tid) : -2;
@@ -45,36 +45,36 @@ __global__ void __launch_bounds__(1024) tree_mask_kernel(const int32_t* parents,
             anc = a;
         }
     }
+    uint32_t* const mine = rows + tid * stride;
     if (warp < W) {
-        uint32_t* const mine = rows + tid * stride;
+        drafts[tid] = lost ? make_int2(0, -1) : make_int2(static_cast<int>(bits), up);
         for (int w = 0; w < W; ++w) mine[w] = w == warp && !lost ? bits : 0u;
-        ups[tid] = lost ? -1 : up;
-    }
-    // the words of the ancestors before the 32, a warp per row and a lane per word
-    const int warps = static_cast<int>(blockDim.x) >> 5;
-    for (int k = 1; k < W; ++k) {
-        __syncthreads();
-        for (int i = warp; i < 32; i += warps) {
-            const int u = ups[32 * k + i];
-            if (u < 0) continue;
-            const uint32_t own = rows[u * stride + (u >> 5)];  // its own bit: it is a draft
-            if (!(own >> (u & 31) & 1u)) {
-                if (lane == k) rows[(32 * k + i) * stride + k] = 0u;
-            } else if (lane < k) {
-                rows[(32 * k + i) * stride + lane] = rows[u * stride + lane];
-            }
-        }
     }
     __syncthreads();
-    for (int i = tid; i < L * W; i += blockDim.x) {
-        const int r = i / W;
-        mask[first * W + i] = rows[r * stride + i - r * W];
+    if (tid < L) {
+        int depth = __popc(bits) - 1;
+        if (!lost)
+            for (int u = up; u >= 0;) {
+                const int2 d = drafts[u];
+                if (d.x == 0) {  // no draft, so this one is none
+                    lost = true;
+                    break;
+                }
+                mine[u >> 5] = static_cast<uint32_t>(d.x);
+                depth += __popc(d.x);
+                u = d.y;
+            }
+        if (lost)
+            for (int w = 0; w < W; ++w) mine[w] = 0u;
+        depths[first + tid] = lost ? -1 : depth;
     }
-    for (int i = tid; i < L; i += blockDim.x) {
-        int n = -1;
-        for (int w = 0; w < W; ++w) n += __popc(rows[i * stride + w]);
-        depths[first + i] = n;
-    }
+    __syncthreads();
+    const int warps = static_cast<int>(blockDim.x) >> 5;
+    // 2^shift lanes a row
+    const int shift = W > 1 ? 32 - __clz(W - 1) : 0, per = 32 >> shift, w = lane & ((1 << shift) - 1);
+#pragma unroll 4
+    for (int r = warp * per + (lane >> shift); r < L; r += warps * per)
+        if (w < W) mask[(first + r) * W + w] = rows[r * stride + w];
 }
 
 // ---- compaction -------------------------------------------------------------------
@@ -171,18 +171,18 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
 pa_status tree_mask_launch(int B, int L, const int32_t* parents, uint32_t* mask, int32_t* depths, uint32_t* flag,
                            cudaStream_t stream) {
     const int W = tree_words(L);
-    const size_t smem = (32ull * W * (W | 1) + 32ull * W) * 4;
+    const size_t smem = (32ull * W * (W | 1) + 64ull * W) * 4;
     static int attr_done[64] = {0};
     DeviceInfo dev;
     const pa_status st = current_device_info(&dev);
     if (st != PA_OK) return st;
     if (!attr_done[dev.device]) {
-        constexpr int most = (kTreeMax * (kTreeMax / 32 + 1) + kTreeMax) * 4;
+        constexpr int most = (kTreeMax * (kTreeMax / 32 + 1) + 2 * kTreeMax) * 4;
         if (cudaFuncSetAttribute(tree_mask_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
             return PA_ERR_CUDA;
         attr_done[dev.device] = 1;
     }
-    const int threads = W > 8 ? 32 * W : 256;  // (small trees: more warps for the chain and the writes, 8 -> 4 us)
+    const int threads = W > 8 ? 32 * W : 256;  // (small trees: more warps for the writes)
     tree_mask_kernel<<<static_cast<unsigned>(B), static_cast<unsigned>(threads), smem, stream>>>(parents, mask, depths,
                                                                                                  flag, L, W);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
