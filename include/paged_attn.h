@@ -489,8 +489,8 @@ pa_status pa_tree_mask(int B, int L, const int32_t* parents, uint32_t* mask, int
  * Rounded on the way: with bf16 queries each probability to bf16 (2^-8).  fp32
  * numbers and their probabilities enter the products as two f16 parts, rows scaled by
  * powers of two (keys and values 8 rows together): all but 2^-22 of a number, or
- * 2^-40 of the largest of its rows, is kept, and the products of two low parts (2^-22)
- * are left out.  Maxima, sums and the output before its own rounding are fp32.  NaN as
+ * 2^-40 of the largest of its rows (values: or 2^-105; probabilities: or 2^-32 of the
+ * row's largest), is kept, and the products of two low parts (2^-22) are left out.  Maxima, sums and the output before its own rounding are fp32.  NaN as
  * in pa_paged_attention_q4.
  * A sequence with context_lens[b] < L or above the table's capacity sets
  * PA_FLAG_BAD_CONTEXT and gets zero rows; keys behind a bad page id read as zeros
@@ -507,8 +507,8 @@ pa_status pa_paged_attention_tree(const pa_shape* shape, const void* query, cons
 size_t pa_tree_workspace_bytes(const pa_shape* shape);
 
 /* pa_paged_attention_tree over a 4-bit pool, bf16 or fp32 query and output.  Rounded
- * on the way: with bf16 queries each probability to f16 (2^-11, below 2^-14 by up to
- * 2^-25), with fp32 queries they and their probabilities as above. */
+ * on the way: with bf16 queries each probability to f16 (2^-11, and 2^-32 of the
+ * row's largest), with fp32 queries they and their probabilities as above. */
 pa_status pa_paged_attention_tree_q4(const pa_shape* shape, const void* query,
                                      const pa_q4_pool* pool, const int32_t* block_table,
                                      const int32_t* context_lens, const uint32_t* tree_mask,

@@ -10,7 +10,8 @@
 // m is the largest score when it was last too low by 2^kSlack (or there was none): a weight
 // does not wait for the scores behind it, and O is rescaled only then.
 // bf16 pages: P rounded to bf16 (2^-8).  4-bit pages: K and V dequantised to f16 on chip
-// (exact), Q scaled by a power of two into f16's range (exact), P rounded to f16 (2^-11).
+// (exact), Q scaled by a power of two into f16's range (exact), P rounded to f16 (2^-11, and
+// 2^-32 of the row's largest).
 // fp32: Q, K, V and P in two f16 parts each, x = h + l up to 2^-22 x, and products h h + h l
 // + l h (l l is below 2^-22); rows are scaled into f16's range by powers of two, K and V by
 // eights of rows, and K's scale is undone in the scores, V's in the weights.
@@ -665,16 +666,13 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     }
                 };
                 float4 a[8], b[8];
-                float last_up = 1.f;
                 // of 8 rows: the factor, kept for V's softmax as it is, for K's inverted
                 auto scale_of = [&](float mx, float* out) {
                     float up, down;
                     f16_scale(mx, up, down);
-                    if (is_v) {
-                        // 2^100: what P 2^v adds up to stays a number.  Zeros: any will do; one like
-                        // the others' keeps P in range.
-                        up = last_up = mx == 0.f ? last_up : fminf(up, 1.2676506e30f);
-                    }
+                    // At most 2^80, so that the sum of P 2^v (P below 2^16) stays a number; for zeros
+                    // just that: they leave the maximum to keys that the output is made of.
+                    if (is_v) up = mx == 0.f ? 1.2089258e24f : fminf(up, 1.2089258e24f);
                     if (lane == 0) *out = is_v ? up : down;
                     return up;
                 };
@@ -984,6 +982,9 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         // How far (log2) a row's scores may rise above its maximum before O is rescaled:
         // bf16 weights and fp32 sums have the exponents for it, f16 ends at 2^16.
         constexpr float kSlack = F16 ? 8.f : 64.f;
+        // f16 weights are taken 2^kLift times as large (O and l are, too): below 2^-14 f16 has
+        // steps of 2^-24, so a light key loses 2^-32 of the heaviest one's weight at most.
+        constexpr float kLift = F16 ? 7.f : 0.f;
         int xc = 0;  // pieces whose states were joined
         bool ok = true;
         // The end of piece k, with this slot's maximum and sum.  The two slots' states of a row
@@ -1321,7 +1322,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             ok = rescale();
                             if (!ok) break;
                         }
-                        const float mu = mrow == neg_inf() ? 0.f : mrow;
+                        const float mu = mrow == neg_inf() ? 0.f : mrow - kLift;
 #pragma unroll
                         for (int cc = 0; cc < BN / 32; ++cc) {
                             float x[32];
@@ -1348,7 +1349,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         uint32_t pw[UK / 2];
                         bool again = true;
                         if (j > 0) {
-                            const float mu = mrow == neg_inf() ? 0.f : mrow;
+                            const float mu = mrow == neg_inf() ? 0.f : mrow - kLift;
                             float x[UK / 32][32];
 #pragma unroll
                             for (int cc = 0; cc < UK / 32; ++cc) tc::ld32(st + cc * 32, x[cc]);
@@ -1371,7 +1372,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                                 if (!ok) break;
                             }
                             ts = make_float2(0.f, 0.f);
-                            const float mu = mrow == neg_inf() ? 0.f : mrow;
+                            const float mu = mrow == neg_inf() ? 0.f : mrow - kLift;
 #pragma unroll
                             for (int cc = 0; cc < UK / 32; ++cc) {
                                 float x[32];

@@ -174,6 +174,29 @@ def test_large_scores_and_scales():
             assert ref.worst(got, want, tol) <= 1.0
 
 
+@pytest.mark.parametrize("pool,dtype", [("bf16", "bf16"), ("f32", "f32"), ("q4", "bf16"),
+                                        ("q4", "f32")])
+def test_light_keys(pool, dtype):
+    """Where the heaviest key's values are 0 the output is the light keys', to the
+    precision of their own weights."""
+    inp = tr.Inputs(tr.Case(4, 2, 24, 16, [300, 24], pool, dtype, seed=2))
+    inp.scale *= 8  # other keys weigh 2^-10 and less
+    for b, S in enumerate(inp.ctx):
+        K = ref.rows_of(inp.dense[0], inp.table, b, S, 16)
+        for h in range(2):
+            q = inp.q[b, 4 * h:4 * h + 4][:, inp.drafted[b]].astype(np.float64)
+            see = inp.see[b][inp.drafted[b]]
+            x = np.einsum("gld,sd->gls", q, np.nan_to_num(K[h]))
+            hide = np.concatenate([np.zeros((len(see), S - 24), bool), ~see], 1)
+            heavy = np.unique(np.where(hide, -np.inf, x).argmax(-1))
+            page, slot = inp.table[b, heavy // 16], heavy % 16
+            inp.raw[-1 if pool != "q4" else 2][page, h, slot] = 0
+            inp.dense[1][page, h, slot] = 0
+    want, tol = tr.attend(inp)
+    got = tr.call(inp, inp.device()).double().cpu().numpy()
+    assert ref.worst(got, want, tol) <= 1.0
+
+
 # ---- compaction ------------------------------------------------------------------
 def paths_of(rng, drafted, L):
     out = []

@@ -150,9 +150,11 @@ def attend(inp: Inputs, skip=()):
       inside the 2^-16 T that the line above leaves; p and v 2^-21 relative, inside
       the S 2^-24 below, whose worst case no sum of rounded terms comes near;
     * p of bf16 queries is rounded to bf16 over bf16 pages: 2^-8; over 4-bit pages to
-      f16: 2^-11 from 2^-14 on, below that its steps are 2^-24, so up to 2^-25 is lost
-      of a p whose row's largest is 1 or more (the maximum that p is taken against is
-      one that some key of the row has reached); the sums add them unrounded;
+      f16: 2^-11; the sums add them unrounded.  Weights in f16, one part or two, are 2^7
+      times p / (the row's largest p, or one up to 2^8 times smaller that the maximum so
+      far stands for): from 2^-14 on they are rounded relatively (two parts: 2^-22, the
+      low one being cut at 2^-25), below that to steps of 2^-24, so at most 2^-25 2^-7 of
+      the row's largest p is lost of each;
     * sums of S terms in fp32: 2^-24 S at worst;
     * a p below 2^-126 of the row's largest is 0 in fp32 (the smallest normal
       number): at most 2^-126 of every value is lost (times the row's largest p).
@@ -162,7 +164,7 @@ def attend(inp: Inputs, skip=()):
     tol = np.full(inp.q.shape, 1e-300)
     eps = 2.0 ** -8 if c.dtype == "bf16" else 2.0 ** -24
     pop = 0.0 if c.dtype == "f32" else 2.0 ** -11 if c.pool == "q4" else 2.0 ** -8
-    lost = 2.0 ** -25 if c.dtype == "bf16" and c.pool == "q4" else 2.0 ** -126
+    lost = 2.0 ** -126 if c.pool == c.dtype == "bf16" else 2.0 ** -32
     for b, S in enumerate(inp.ctx):
         if b in skip:
             continue
