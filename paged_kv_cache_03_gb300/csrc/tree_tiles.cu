@@ -70,11 +70,14 @@ constexpr uint32_t kTmemCols = 512;  // S of slot t at 128 t, O at 256 + 128 t
 // shares count it, or CTAs with many short segments would finish last.  (Of 64 sequences,
 // 256 rows take 158, 154 and 151 us with 3, 4 and 5, 64 rows 91, 91 and 94.)
 constexpr int kSegCost = 4;
-constexpr int kMinPer = 8;  // least cost of a share (6 and 12: the same within noise)
+// Least cost of a share.  Two tiles: one sequence of 2000 keys, 4 kv heads, 13 us of bf16 and
+// 19 of fp32, with 8 of them 20 and 29.
+constexpr int kMinPer = 2;
 // Where there is a CTA for each segment and tables hold at most so many key tiles, segments
-// stay whole and there is no merge: alone with 1000 / 2000 keys of bf16, 17 / 27 us whole
-// and 19 / 21 cut; of fp32 with 500 / 1000 keys, 26 / 44 whole and 29 / 30 cut.
-constexpr int kWholeTiles = 8;
+// stay whole and there is no merge: 4, or 8 where segments are for at least a quarter of the
+// CTAs (whole and cut, bf16: 4 segments of 4 tiles 11.2 and 13, of 8 tiles 16.5 and 11.8; 120
+// segments of 8 tiles 18 and 22; fp32: 32 of 8 tiles 31 and 25, 120 of them 28 and 35 us).
+constexpr int kWholeFew = 4, kWholeMany = 8;
 constexpr int kQTile = BM * kD * 2;
 enum Bar {
     kQFull = 0,     // + buffer: the query tile is there (4 bit: as it is)
@@ -1563,7 +1566,7 @@ pa_status launch_tiles(TileParams p, const CUtensorMap* maps, const TreeCall& c,
     }
     *shares = clusters[c.dev.device];
     const long long segs = static_cast<long long>(p.B) * p.H_kv * p.nG;
-    p.whole = segs <= *shares && p.max_S <= kWholeTiles * keys(SRC);
+    p.whole = segs <= *shares && p.max_S <= (4 * segs < *shares ? kWholeFew : kWholeMany) * keys(SRC);
     if (p.whole) *shares = static_cast<int>(segs);
     cfg.gridDim = dim3(static_cast<unsigned>(*shares * C));
     if (cudaLaunchKernelEx(&cfg, tree_tile_kernel<SRC, C>, p, maps[0], maps[1], maps[2]) != cudaSuccess) return PA_ERR_CUDA;
