@@ -202,3 +202,68 @@ def test_pages_past_32_bit_offsets(pool):
             b[int(inp.table[seq, dst // 16]), :, dst % 16] = \
                 b[int(inp.table[seq, src // 16]), :, src % 16]
         assert t[base:].view(torch.uint8).equal(b.view(torch.uint8))
+
+
+def test_calls_at_once():
+    """Two streams and two host threads, a workspace each: neither disturbs the other."""
+    import threading
+    import torch
+    jobs = []
+    for c in (tr.Case(4, 2, 64, 16, [1500, 700, 64]), tr.Case(4, 2, 24, 16, [900, 400], "q4"),
+              tr.Case(2, 2, 12, 16, [800, 31], "f32", "f32")):
+        inp = tr.Inputs(c)
+        d = inp.device()
+        ws = B.new_tree_workspace(d["q"], d["pool"] if c.pool == "q4" else d["pool"][0], d["table"])
+        jobs.append((inp, d, ws, torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+
+    def work(inp, d, ws, stream, outs):
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                outs.append(tr.call(inp, d, workspace=ws))
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for inp, d, ws, _, outs in jobs:
+        want, tol = tr.attend(inp)
+        assert len(outs) == 20 and all(o.equal(outs[0]) for o in outs)
+        assert ref.worst(outs[0].double().cpu().numpy(), want, tol) <= 1.0
+        assert B.pa_check_device_flag(ws)[1] == 0
+
+
+def test_captured_first_calls():
+    """A call may be captured before any other of its kind was made (in a process of its own)."""
+    import os
+    import subprocess
+    import sys
+    program = """
+import torch, tree_ref as tr, cache_ref as ref
+from paged_kv_cache_03_gb300 import binding as B
+for pool, dtype in (("bf16", "bf16"), ("q4", "bf16"), ("f32", "f32"), ("q4", "f32")):
+    for L in (8, 64):
+        inp = tr.Inputs(tr.Case(4, 1, L, 16, [2000, 64], pool, dtype))
+        d = inp.device()
+        ws = B.new_tree_workspace(d["q"], d["pool"] if pool == "q4" else d["pool"][0], d["table"])
+        out = torch.empty_like(d["q"])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tr.call(inp, d, out=out, workspace=ws)
+        g.replay()
+        want, tol = tr.attend(inp)
+        assert ref.worst(out.double().cpu().numpy(), want, tol) <= 1.0
+parents = torch.tensor([[-1, 0, 0]], dtype=torch.int32, device="cuda")
+ws = B.new_cache_workspace()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    mask, depths = B.tree_mask(parents, workspace=ws)
+g.replay()
+assert mask[0, :, 0].tolist() == [1, 3, 5] and depths[0].tolist() == [0, 1, 1]
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
+    r = subprocess.run([sys.executable, "-c", program], env=env, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
