@@ -87,10 +87,10 @@ enum Bar {
     kVFull = 10,    // + slot
     kVEmpty = 13,   // + slot
     kVTail = 16,    // + slot: a tail tile's values are there, not yet cleaned (by TMA)
-    kQReady = 16,   // + buffer: the query tile is there in f16 (f16 products)
-    kSFull = 19,    // + place of S
-    kPFull = 21,    // + place of P
-    kODone = 25,    // + place of the P that O has taken in
+    kQReady = 16,   // + buffer: the query tile is there in f16 (f16 products; never with kVTail)
+    kSFull = 19,    // + place of S (halves) or slot
+    kPFull = 21,    // + t + 2 x place
+    kODone = 25,    // + t + 2 x place: O has taken in that P
     kOFree = 29,    // + t: the epilogue has read O
     kXFull = 31,    // both slots' maxima and sums are there
     kXFree = 32,    // ... and read
@@ -220,7 +220,7 @@ __device__ __forceinline__ int seq_cost(const TileParams& p, int S) {
 // from kItemFull to kItemEmpty.
 struct Item {
     int b, S, kvh, mp, ng, j0, n;  // n = 0: no more
-    int before[2];      // tiles of slot t in earlier pieces
+    int before[2];      // the even and the odd tiles of earlier pieces (in turn: of slot t)
     uint32_t live[32];  // slots that hold a draft (pieces with tail tiles)
 };
 static_assert(sizeof(Item) <= kItemBytes && kItemBytes % 8 == 0, "item slot");
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         if (!ok) break;
                     }
                 }
-                // Without an error every copy has been waited for by the MMA thread.  With one,
+                // Without an error every copy has been waited for by the MMA warps.  With one,
                 // give those in flight time to land before the shared memory goes.
                 if (!ok)
                     for (int s = 0; s < N; ++s) {
@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         int xc = 0;  // pieces whose states were joined
         bool ok = true;
         // The end of piece k, with this slot's maximum and sum.  The two slots' states of a row
-        // are joined by both warpgroups, 64 dims each (one tile: A has them all).
+        // are joined by both warpgroups, 64 dims each (one tile and no halves: A has them all).
         auto finish = [&](int k, float m1, float l1) {
             const volatile Item* const it = slot(k);
             const bool both = HALF || it->n > 1;
