@@ -1108,7 +1108,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             float c = fmaxf(p.scale_log2, FLT_MIN);  // (scale 0: -inf stays -inf)
             if constexpr (F16) {
                 // A takes the rows to f16 (fp32: two parts), the largest value in [2^14, 2^15):
-                // 16-bit rows in place, fp32 rows from global memory, read twice
+                // 16-bit rows in place, fp32 rows from global memory
                 const int buf = q_buf(k);
                 float* const down = reinterpret_cast<float*>(smem_raw + M.q_scale) + buf * BM + r;
                 if (t == 0) {
@@ -1118,29 +1118,33 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         ok = q_use(k) == 0 || warp_wait(bar(kQEmpty + buf), (q_use(k) - 1) & 1);
                         if (!ok) break;
                         if (busy) {
-                            const long long row = (static_cast<long long>(slot(k)->b) * p.H_kv + slot(k)->kvh) * p.R + m * BM + r;
-                            const float4* const src = reinterpret_cast<const float4*>(p.q + (valid ? row : 0) * kD);
-                            float mx = 0.f;
-#pragma unroll 8
-                            for (int i = 0; i < kD / 4; ++i) {
-                                const float4 v = __ldg(src + i);
-                                mx = fmax3(fmax3(mx, fabsf(v.x), fabsf(v.y)), fabsf(v.z), fabsf(v.w));
-                            }
-                            float up, dn;
-                            f16_scale(mx, up, dn);
-#pragma unroll 4
-                            for (int c = 0; c < 16; ++c) {
-                                const float4 v[2] = {__ldg(src + 2 * c), __ldg(src + 2 * c + 1)};
-                                const float x[8] = {v[0].x * up, v[0].y * up, v[0].z * up, v[0].w * up,
-                                                    v[1].x * up, v[1].y * up, v[1].z * up, v[1].w * up};
-                                uint32_t hi[4], lo[4];
+                            // a row at once, four dims a lane, eight rows on their way (sixteen: registers run out)
+                            const long long first_row =
+                                (static_cast<long long>(slot(k)->b) * p.H_kv + slot(k)->kvh) * p.R + m * BM + q4 * 32;
+                            const float4* const src = reinterpret_cast<const float4*>(p.q + first_row * kD) + lane;
+                            const uint32_t at = qrow + (lane >> 4) * p.q_half + (lane & 1) * 8;
+#pragma unroll 1
+                            for (int r0 = 0; r0 < 32 && q4 * 32 + r0 < rows; r0 += 8) {
+                                float4 v[8];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) split_f16(make_float2(x[2 * e], x[2 * e + 1]), hi[e], lo[e]);
-                                const uint32_t at = qrow + (c >> 3) * p.q_half + sw128(r, c & 7);
-                                sts128(at, hi[0], hi[1], hi[2], hi[3]);
-                                sts128(at + 2 * p.q_half, lo[0], lo[1], lo[2], lo[3]);
+                                for (int i = 0; i < 8; ++i)
+                                    v[i] = q4 * 32 + r0 + i < rows ? __ldg(src + (r0 + i) * (kD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    // (as bits: the order of numbers above 0)
+                                    const float mx = fmax3(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fabsf(v[i].z), fabsf(v[i].w));
+                                    float up, dn;
+                                    f16_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx))), up, dn);
+                                    uint32_t hi[2], lo[2];
+                                    split_f16(make_float2(v[i].x * up, v[i].y * up), hi[0], lo[0]);
+                                    split_f16(make_float2(v[i].z * up, v[i].w * up), hi[1], lo[1]);
+                                    const int x = q4 * 32 + r0 + i;
+                                    const uint32_t to = at + sw128(x, lane >> 1 & 7);
+                                    sts64(to, hi[0], hi[1]);
+                                    sts64(to + 2 * p.q_half, lo[0], lo[1]);
+                                    if (lane == 0) down[x - r] = dn;
+                                }
                             }
-                            *down = dn;
                         }
                     } else {
                         ok = warp_wait(bar(kQFull + buf), q_use(k) & 1);
