@@ -18,9 +18,10 @@
 //
 // Layout on GB300: one CTA per SM.
 //   * A segment is one query tile of one (sequence, kv head) over all its key tiles, or, over
-//     bf16 pages by TMA, C query tiles on the C CTAs of a cluster: each CTA loads 1 / C of
-//     every key tile and multicasts it to all, so K and V cross from HBM once for C tiles.
-//   * The key tiles of all segments are cut into equal shares, one per CTA (cluster), so
+//     bf16 pages by TMA, C query tiles on C neighbouring CTAs, which walk the same key tiles
+//     at about the same time: K and V cross from HBM about once and the others of the C find
+//     them in L2.  Nothing waits for a neighbour.
+//   * The key tiles of all segments are cut into equal shares, one per CTA (C CTAs), so
 //     ragged contexts leave no SM idle; a segment that crosses shares leaves fp32 partial
 //     states that tree_merge_kernel joins.
 //   * Two slots t = 0, 1, one softmax warpgroup each with one row per thread, have their own
@@ -42,7 +43,7 @@
 // Measured (G = 4, H_kv = 8, a call among others, with the merge):
 //   64 sequences of 128 .. 4096 keys, 64 rows    89 us, 6.4 TB/s of rows: bound by HBM
 //   16 of 32768, 128 rows, pages of 16          320 us, 6.7 TB/s
-//   16 of 1000 .. 8000, 252 rows                 78 us, 940 TFLOP/s: a tile takes
+//   16 of 1000 .. 8000, 252 rows                 76 us, 970 TFLOP/s: a tile takes
 //     1750 cycles, of them 1024 products at the peak rate; Q, K, V and TMA's stores pass
 //     through shared memory in 1280.  Without exponentials it is no faster, without maxima
 //     and sums 9%
@@ -57,8 +58,8 @@
 
 #include <cudaTypedefs.h>
 
-#include "cluster.cuh"
 #include "stage.cuh"
+#include "tc.cuh"
 #include "tree.h"
 
 namespace pa {
@@ -84,7 +85,7 @@ enum Bar {
     kQFull = 0,     // + buffer: the query tile is there (4 bit: as it is)
     kQEmpty = 2,    // + buffer: every Q K^T of its piece is done
     kKFull = 4,     // + slot
-    kKEmpty = 7,    // + slot: in every CTA of the cluster
+    kKEmpty = 7,    // + slot
     kVFull = 10,    // + slot
     kVEmpty = 13,   // + slot
     kVTail = 16,    // + slot: a tail tile's values are there, not yet cleaned (by TMA)
@@ -198,7 +199,7 @@ struct TileParams {
     long long max_S;
     float scale_log2;
     int out32;  // the output is 32-byte aligned
-    int whole;  // a CTA (cluster) per segment
+    int whole;  // a CTA (C CTAs) per segment
 };
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -277,7 +278,6 @@ template <Source SRC, int C>
 __global__ void __launch_bounds__(threads(SRC), 1)
     tree_tile_kernel(const TileParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
-    static_assert(C == 1 || SRC == kTma, "only TMA multicasts");
     constexpr bool F16 = is_f16(SRC), F32 = fp32(SRC);
     constexpr int kThreads = threads(SRC), kProd = producers(SRC), N = slots(SRC), I = items(SRC);
     constexpr int BN = keys(SRC), kTile = BN * kD * 2;
@@ -289,9 +289,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     // Tiles behind TMA: [8 rows][64-dim half][row][128 bytes], as boxes of rows come; else
     // [half][BN rows][128 bytes].
     constexpr uint32_t kHalf = SRC == kTma ? 1024u : BN * 128u, kGroup = SRC == kTma ? 2048u : 1024u;
-    constexpr uint16_t kAll = (1u << C) - 1u;
-    // By TMA, K and V come from a warp each in clusters, where K is read ahead of V (256 rows:
-    // 145 us from one warp, 139 from two), else from one (at the rate of HBM: 320 and 327).
+    // By TMA, K and V of C > 1 tiles come from a warp each, so that K is read ahead of V (256
+    // rows: 142 us from one warp, 136 from two), else from one (at the rate of HBM: 320 and 327).
     constexpr bool kApart = C > 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     int* const share = reinterpret_cast<int*>(smem_raw + M.x);
     int* const sums = share + 4;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = C == 1 ? 0 : static_cast<int>(cluster_rank());
+    const int rank = static_cast<int>(blockIdx.x) % C;  // which of the C query tiles
     const int my_share = static_cast<int>(blockIdx.x) / C, shares = static_cast<int>(gridDim.x) / C;
     pdl_launch_dependents();
 
@@ -322,9 +321,9 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         }
         for (int s = 0; s < N; ++s) {
             mbar_init(bar(kKFull + s), SRC == kTma ? 1 : 4);
-            mbar_init(bar(kKEmpty + s), C);
+            mbar_init(bar(kKEmpty + s), 1);
             mbar_init(bar(kVFull + s), SRC == kTma ? 1 : 4);
-            mbar_init(bar(kVEmpty + s), C);
+            mbar_init(bar(kVEmpty + s), 1);
             if (SRC == kTma) mbar_init(bar(kVTail + s), 1);
         }
         if (SRC == kF32)
@@ -405,7 +404,6 @@ __global__ void __launch_bounds__(threads(SRC), 1)
     }
     tc::fence_before_sync();
     __syncthreads();
-    if constexpr (C > 1) cluster_sync();  // no peer's copy or commit before the barriers stand
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const int total = share[0], per = share[1], first_b = share[2], first_unit = p.whole ? 0 : share[3];
@@ -444,6 +442,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         if constexpr (SRC == kTma) {
             if (warp == 0 || (kApart && warp == 2)) {
                 const bool keys = warp == 0, values = !kApart || warp == 2;
+                // (read once, or by C CTAs close together: 256 rows of a head 136 us, kept to the last 141)
                 const uint64_t policy = p.nG == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
                 const int nbox = BN / p.box;
                 bool bad_page = false;
@@ -457,8 +456,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     if (n == 0) break;
                     const int32_t* const table = p.bt + static_cast<long long>(b) * p.max_npg;
                     const int tail = first_tail(S);
-                    // lane i brings box i of a tile (every C-th from its rank on); its page id
-                    // is requested a tile ahead
+                    // lane i brings box i of a tile; its page id is requested a tile ahead
                     auto page_of = [&](int j) {
                         const int key = j * BN + lane * p.box;
                         return lane < nbox && key < S ? __ldg(table + key / p.ps) : 0;
@@ -466,7 +464,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     int page = page_of(j0);
                     for (int j = j0; j < j0 + n; ++j, g.next(), ++tiles) {
                         const int key = j * BN + lane * p.box;
-                        const bool there = lane < nbox && key < S, mine = there && lane % C == rank;
+                        const bool there = lane < nbox && key < S;
                         const bool good = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
                         bad_page |= there && !good;
                         // (groups of 8 rows; those behind the pool read as zeros)
@@ -477,13 +475,9 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             if (!warp_wait(bar(empty + g.s), g.phase ^ 1u) || aborted(abort_flag)) return false;
                             if (lane == 0) mbar_arrive_expect_tx(bar(full + g.s), bytes);
                             __syncwarp();
-                            if (mine) {
-                                const uint32_t dst = base + ring + g.s * kTile + lane * p.box * 256;
-                                if constexpr (C == 1)
-                                    tc::tma_load_4d(dst, map, 0, 0, 0, row, bar(full + g.s), policy);
-                                else
-                                    tc::tma_load_4d_multicast(dst, map, 0, 0, 0, row, bar(full + g.s), kAll, policy);
-                            }
+                            if (there)
+                                tc::tma_load_4d(base + ring + g.s * kTile + lane * p.box * 256, map, 0, 0, 0, row, bar(full + g.s),
+                                                policy);
                             return true;
                         };
                         ok = (!keys || load(kKEmpty, kKFull, M.k, &kmap)) &&
@@ -797,8 +791,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                                 }
                             }
                             tc::commit(bar(kSFull + place));
-                            if constexpr (C == 1) tc::commit(bar(kKEmpty + ring.s));
-                            else tc::commit_multicast(bar(kKEmpty + ring.s), kAll);
+                            tc::commit(bar(kKEmpty + ring.s));
                             if (i == n - 1) tc::commit(bar(kQEmpty + buf));
                         }
                         __syncwarp();
@@ -832,10 +825,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                                     }
                                 }
                                 tc::commit(bar(kODone + t + 2 * b));
-                                if (!HALF || h == 1) {
-                                    if constexpr (C == 1) tc::commit(bar(kVEmpty + ring.s));
-                                    else tc::commit_multicast(bar(kVEmpty + ring.s), kAll);
-                                }
+                                if (!HALF || h == 1) tc::commit(bar(kVEmpty + ring.s));
                             }
                             __syncwarp();
                         }
@@ -1414,7 +1404,6 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmemCols);
     }
-    if constexpr (C > 1) cluster_sync();  // peers' copies and commits come here until they are done
 }
 
 // Rows r .. r + ROWS - 1 of the segment that starts in share c and ends in share sp.w, its
@@ -1545,36 +1534,23 @@ bool make_pool_map(CUtensorMap* map, const void* ptr, long long rows, int box_ro
 template <Source SRC, int C>
 pa_status launch_tiles(TileParams p, const CUtensorMap* maps, const TreeCall& c, int* shares) {
     constexpr int bytes = smem(SRC).total;
-    static int clusters[64] = {0};  // resident together, per device
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(threads(SRC));
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = c.stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = C;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = C > 1 ? 1 : 0;
-    cfg.gridDim = dim3(static_cast<unsigned>(c.dev.sm_count / C * C));
-    if (!clusters[c.dev.device]) {
+    static int ready[64] = {0};  // per device
+    if (!ready[c.dev.device]) {
         if (cudaFuncSetAttribute(tree_tile_kernel<SRC, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
             return PA_ERR_CUDA;
         // the roles' registers come out of what the launch has
         cudaFuncAttributes at;
         if (cudaFuncGetAttributes(&at, tree_tile_kernel<SRC, C>) != cudaSuccess) return PA_ERR_CUDA;
         if (at.numRegs != launch_regs(SRC)) return PA_ERR_UNSUPPORTED;
-        int n = c.dev.sm_count;
-        if (C > 1 && cudaOccupancyMaxActiveClusters(&n, tree_tile_kernel<SRC, C>, &cfg) != cudaSuccess) return PA_ERR_CUDA;
-        clusters[c.dev.device] = std::min(n, c.dev.sm_count / C);
-        if (clusters[c.dev.device] < 1) return PA_ERR_UNSUPPORTED;
+        ready[c.dev.device] = 1;
     }
-    *shares = clusters[c.dev.device];
+    *shares = c.dev.sm_count / C;
+    if (*shares < 1) return PA_ERR_UNSUPPORTED;
     const long long segs = static_cast<long long>(p.B) * p.H_kv * p.nG;
     p.whole = segs <= *shares && p.max_S <= (4 * segs < *shares ? kWholeFew : kWholeMany) * keys(SRC);
     if (p.whole) *shares = static_cast<int>(segs);
-    cfg.gridDim = dim3(static_cast<unsigned>(*shares * C));
-    if (cudaLaunchKernelEx(&cfg, tree_tile_kernel<SRC, C>, p, maps[0], maps[1], maps[2]) != cudaSuccess) return PA_ERR_CUDA;
+    tree_tile_kernel<SRC, C><<<static_cast<unsigned>(*shares * C), threads(SRC), bytes, c.stream>>>(p, maps[0], maps[1], maps[2]);
+    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     if (p.whole) *shares = 0;
     return PA_OK;
 }
@@ -1637,9 +1613,12 @@ pa_status tree_launch(const TreeCall& c) {
     p.scale_log2 = c.scale * 1.4426950408889634f;
     p.out32 = reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
     const bool tma = !f32 && !c.ks && sh.page_size % 8 == 0;
+    // Two query tiles side by side read K and V from HBM once (a tile alone at a time, in turn:
+    // 252 rows 98 us, in pairs 76; 256 rows 178 and 136; 1020 rows 180 and 162; an odd number
+    // leaves a CTA of the last pair without rows: 260 rows 72 and 79).
     const int nM = (p.R + BM - 1) / BM, C = tma && nM > 1 ? 2 : 1;
     p.nG = (nM + C - 1) / C;
-    p.box = std::min(gcd_int(sh.page_size, keys(kTma)), keys(kTma) / C);
+    p.box = gcd_int(sh.page_size, keys(kTma));
     CUtensorMap maps[3] = {};
     if (!f32 && !make_map(&maps[0], c.q, static_cast<long long>(sh.B) * sh.H_q * sh.L, p.q_box)) return PA_ERR_CUDA;
     maps[1] = maps[2] = maps[0];
