@@ -486,7 +486,9 @@ pa_status pa_tree_mask(int B, int L, const int32_t* parents, uint32_t* mask, int
  * draft: its output is 0, no draft sees it whatever its bits say, and its key and
  * value rows may hold anything.  bf16 or fp32 pages of the query's type, any page
  * size and group size.
- * Rounded on the way: with bf16 queries each probability to bf16 (2^-8).  fp32
+ * Rounded on the way: with bf16 queries each probability to bf16 (2^-8); their sums with
+ * values are fp32, of weights up to 2^8 beside the row's first keys, so that values of
+ * 2^120 / context_lens[b] and more may come out as infinities.  fp32
  * numbers and their probabilities enter the products as two f16 parts, rows scaled by
  * powers of two (keys and values 8 rows together): all but 2^-22 of a number, or
  * 2^-40 of the largest of its rows (values: or 2^-105; probabilities: or 2^-32 of the

@@ -973,9 +973,10 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         reg_set<regs(SRC).softmax, launch_regs(SRC)>();
         const int t = (warp - kProd - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;  // slot, lane quarter, row
         const uint32_t trow = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-        // How far (log2) a row's scores may rise above its maximum before O is rescaled:
-        // bf16 weights and fp32 sums have the exponents for it, f16 ends at 2^16.
-        constexpr float kSlack = F16 ? 8.f : 64.f;
+        // How far (log2) a row's scores may rise above its maximum before O is rescaled: f16
+        // weights end at 2^16, and a sum of bf16 weights times values at 2^128, which leaves
+        // N values 2^120 / N.
+        constexpr float kSlack = 8.f;
         // f16 weights are taken 2^kLift times as large (O and l are, too): below 2^-14 f16 has
         // steps of 2^-24, so a light key loses 2^-32 of the heaviest one's weight at most.
         constexpr float kLift = F16 ? 7.f : 0.f;
