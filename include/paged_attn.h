@@ -490,10 +490,13 @@ pa_status pa_tree_mask(int B, int L, const int32_t* parents, uint32_t* mask, int
  * values are fp32, of weights up to 2^8 beside the row's first keys, so that values of
  * 2^120 / context_lens[b] and more may come out as infinities.  fp32
  * numbers and their probabilities enter the products as two f16 parts, rows scaled by
- * powers of two (keys and values 8 rows together): all but 2^-22 of a number, or
- * 2^-40 of the largest of its rows (values: or 2^-105; probabilities: or 2^-32 of the
- * row's largest), is kept, and the products of two low parts (2^-22) are left out.  Maxima, sums and the output before its own rounding are fp32.  NaN as
- * in pa_paged_attention_q4.
+ * powers of two: all but 2^-22 of a number, or 2^-40 of the largest of its row (values: or
+ * 2^-105; probabilities: or 2^-32 of the row's largest, over fp32 pages each taken times
+ * the largest value of its key), is kept, and the products of two low parts (2^-22) are
+ * left out.  A probability below
+ * 2^(k - 133) of another whose key's fp32 values are 2^k times larger (zeros count as 2^-66)
+ * is 0.  Maxima, sums and the output before its own rounding are fp32.  NaN as in
+ * pa_paged_attention_q4.
  * A sequence with context_lens[b] < L or above the table's capacity sets
  * PA_FLAG_BAD_CONTEXT and gets zero rows; keys behind a bad page id read as zeros
  * (PA_FLAG_BAD_PAGE).

@@ -13,8 +13,8 @@
 // (exact), Q scaled by a power of two into f16's range (exact), P rounded to f16 (2^-11, and
 // 2^-32 of the row's largest).
 // fp32: Q, K, V and P in two f16 parts each, x = h + l up to 2^-22 x, and products h h + h l
-// + l h (l l is below 2^-22); rows are scaled into f16's range by powers of two, K and V by
-// eights of rows, and K's scale is undone in the scores, V's in the weights.
+// + l h (l l is below 2^-22); every row is scaled into f16's range by a power of two, and K's
+// scale is undone in the scores, V's in the weights.
 //
 // Layout on GB300: one CTA per SM.
 //   * A segment is one query tile of one (sequence, kv head) over all its key tiles, or, over
@@ -170,8 +170,10 @@ constexpr Smem smem(Source s) {
     at += 2 * BM * 8;
     m.q_scale = at;  // f16: [2][128] the inverse of a row's scale
     if (is_f16(s)) at += 2 * BM * 4;
-    m.kv_scale = at;  // fp32 pages, of 8 keys each: [8 tiles] K's inverse scale, [4 tiles] V's scale
-    if (s == kF32) at += (8 + 4) * (keys(s) / 8) * 4;
+    // fp32 pages, a number per key: [8 tiles] K's inverse scale, [4 tiles] the exponent of V's
+    // scale, [4 tiles] that scale
+    m.kv_scale = at;
+    if (s == kF32) at += (8 + 4 + 4) * keys(s) * 4;
     m.total = at;
     return m;
 }
@@ -614,16 +616,16 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 cp_async_wait<0>();
             } else if constexpr (SRC == kF32) {
                 // Warps 0-3 bring K, 4-7 V: warp w rows 32 i + 8 w .., i = 0, 1, which are loaded a
-                // tile ahead.  Each 8 rows are taken by a power of two so that their largest value
-                // lies in [2^14, 2^15), and stored in two f16 parts: all but 2^-22 of a value, or
-                // 2^-40 of the 8 rows' largest.  Scores are scaled back by key; V's scale goes into
-                // P, so it is announced before V's place in the ring is free.
+                // tile ahead.  A row is taken by a power of two so that its largest value lies in
+                // [2^14, 2^15), and stored in two f16 parts: all but 2^-22 of a value, or 2^-40 of
+                // the row's largest.  Scores are scaled back by key; V's scale goes into P, so it is
+                // announced before V's place in the ring is free.
                 const bool is_v = warp >= 4;
                 const int w = warp & 3;
                 const float* const pool = reinterpret_cast<const float*>(is_v ? p.vc : p.kc);
                 const uint32_t ring = base + (is_v ? M.v : M.k);
                 const int full = is_v ? kVFull : kKFull, empty = is_v ? kVEmpty : kKEmpty;
-                float* const scales = reinterpret_cast<float*>(smem_raw + M.kv_scale) + (is_v ? 8 * (BN / 8) : 0);
+                float* const scales = reinterpret_cast<float*>(smem_raw + M.kv_scale) + (is_v ? 8 * BN : 0);
                 // Row of 8 and dims 16 q + 4 l4 ..: 16 lanes take every other row, so that their 8-byte
                 // stores hit all banks once.
                 const int r8 = (lane >> 2 & 3) * 2 + (lane >> 4), l4 = lane & 3;
@@ -639,12 +641,12 @@ __global__ void __launch_bounds__(threads(SRC), 1)
 #pragma unroll
                     for (int q = 0; q < 8; ++q) v[q] = row < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcs(src + 4 * q);
                 };
-                auto largest_of = [&](const float4 (&v)[8]) {
+                auto largest_of = [&](const float4 (&v)[8]) {  // of the row: its four lanes
                     float mx = 0.f;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) mx = fmax3(fmax3(mx, fabsf(v[q].x), fabsf(v[q].y)), fabsf(v[q].z), fabsf(v[q].w));
 #pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    for (int d = 1; d < 4; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                     return mx;
                 };
                 auto store = [&](const float4 (&v)[8], int i, float up) {
@@ -664,14 +666,19 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     }
                 };
                 float4 a[8], b[8];
-                // of 8 rows: the factor, kept for V's softmax as it is, for K's inverted
+                // of a row: the factor, kept for the softmax, of K inverted, of V with its exponent
                 auto scale_of = [&](float mx, float* out) {
                     float up, down;
                     f16_scale(mx, up, down);
                     // At most 2^80, so that the sum of P 2^v (P below 2^16) stays a number; for zeros
-                    // just that: they leave the maximum to keys that the output is made of.
+                    // just that: they leave the maximum to keys that the output is made of.  (P is 0
+                    // below 2^-126: a key whose values are 2^k times smaller than another's is lost to
+                    // the sum where it weighs less than 2^(k - 133) of that one.)
                     if (is_v) up = mx == 0.f ? 1.2089258e24f : fminf(up, 1.2089258e24f);
-                    if (lane == 0) *out = is_v ? up : down;
+                    if (l4 == 0) {
+                        *out = is_v ? exponent_of(up) : down;
+                        if (is_v) out[4 * BN] = up;
+                    }
                     return up;
                 };
                 // rows of this tile; page ids of the next one are always on their way
@@ -691,8 +698,8 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     if (!ok) break;
                     // (K's may be written while the softmax of four tiles before is under way, V's
                     // of three)
-                    float* const mine = scales + (tile & (is_v ? 3 : 7)) * (BN / 8) + w;
-                    const float up0 = scale_of(largest_of(a), mine), up1 = scale_of(largest_of(b), mine + 4);
+                    float* const mine = scales + (tile & (is_v ? 3 : 7)) * BN + 8 * w + r8;
+                    const float up0 = scale_of(largest_of(a), mine), up1 = scale_of(largest_of(b), mine + 32);
                     __syncwarp();
                     if (is_v && lane == 0) mbar_arrive(bar(kVScale + (tile & 3)));
                     ok = warp_wait(bar(empty + g.s), g.phase ^ 1u);
@@ -1278,40 +1285,42 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                     };
                     // P goes over the first columns of its S
                     if constexpr (F32) {
-                        // Two parts of P do not fit the registers beside S: S is read twice, and 32
-                        // keys' P lies over their own scores.  fp32 pages: V's rows were scaled by
-                        // 2^v (by eights), so P is 2^(score - v - maximum), the maximum that of score
-                        // - v, and the sum adds P 2^v: the weights relative to that maximum.
-                        const float4* const scales = reinterpret_cast<const float4*>(smem_raw + M.kv_scale);
-                        const int tile = g0 + i;
-                        auto scores = [&](float (&x)[32], int cc, float4& vs) {
+                        // Two parts of P do not fit the registers beside S: the masked scores, scaled
+                        // to powers of two, go back over S, and then 32 keys' P over their own (all
+                        // done twice, from S as it was, the second 32 keys unrolled: fp32 pages, 256
+                        // rows, 192 us for 172, fp32 queries over 4 bits 57 for 51).  fp32 pages: V's rows were scaled by
+                        // 2^v, so P is 2^(score - v - maximum), the maximum that of score - v, and
+                        // the sum adds P 2^v: the weights relative to that maximum.
+                        const float4* const k_scale = reinterpret_cast<const float4*>(smem_raw + M.kv_scale) + ((g0 + i) & 7) * (BN / 4);
+                        const float4* const v_scale = reinterpret_cast<const float4*>(smem_raw + M.kv_scale) + (8 + ((g0 + i) & 3)) * (BN / 4);
+#pragma unroll
+                        for (int cc = 0; cc < BN / 32; ++cc) {
+                            float x[32];
                             tc::ld32(st + cc * 32, x);
-                            float kf[4] = {c, c, c, c}, off[4] = {0.f, 0.f, 0.f, 0.f};
-                            if constexpr (SRC == kF32) {
-                                const float4 ks = scales[(tile & 7) * (BN / 32) + cc];
-                                vs = scales[(8 + (tile & 3)) * (BN / 32) + cc];
-                                kf[0] = c * ks.x, kf[1] = c * ks.y, kf[2] = c * ks.z, kf[3] = c * ks.w;
-                                // (a power of two: its exponent)
-                                off[0] = exponent_of(vs.x), off[1] = exponent_of(vs.y), off[2] = exponent_of(vs.z),
-                                off[3] = exponent_of(vs.w);
-                            }
                             tc::wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], kf[e >> 3], -off[e >> 3]);
+                            for (int e = 0; e < 32; e += 4) {
+                                float4 kf = make_float4(c, c, c, c), off = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if constexpr (SRC == kF32) {
+                                    const float4 ks = k_scale[cc * 8 + e / 4];
+                                    kf = make_float4(c * ks.x, c * ks.y, c * ks.z, c * ks.w);
+                                    off = v_scale[cc * 8 + e / 4];
+                                }
+                                x[e] = fmaf(x[e], kf.x, -off.x);
+                                x[e + 1] = fmaf(x[e + 1], kf.y, -off.y);
+                                x[e + 2] = fmaf(x[e + 2], kf.z, -off.z);
+                                x[e + 3] = fmaf(x[e + 3], kf.w, -off.w);
+                            }
                             if (jt >= tail) {
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
                                     if (!(see[cc] >> e & 1u)) x[e] = neg_inf();
                             }
-                        };
-                        float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
-#pragma unroll
-                        for (int cc = 0; cc < BN / 32; ++cc) {
-                            float x[32];
-                            scores(x, cc, vs);
+                            tc::st32(st + cc * 32, x);
 #pragma unroll
                             for (int e = 0; e < 32; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
                         }
+                        tc::wait_st();
                         const bool grow = valid && mx > mrow + kSlack;
                         if (grow) {
                             alpha = fast_exp2(mrow - mx);  // 2^-inf = 0 at the start
@@ -1322,19 +1331,19 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             if (!ok) break;
                         }
                         const float mu = mrow == neg_inf() ? 0.f : mrow - kLift;
-#pragma unroll
+#pragma unroll 1  // (registers)
                         for (int cc = 0; cc < BN / 32; ++cc) {
                             float x[32];
-                            scores(x, cc, vs);
-                            const float back[4] = {vs.x, vs.y, vs.z, vs.w};
+                            tc::ld32(st + cc * 32, x);
+                            tc::wait_ld();
                             uint32_t w[32];  // 16 of the high parts, 16 of the low ones
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const float2 ex = make_float2(fast_exp2(x[2 * i] - mu), fast_exp2(x[2 * i + 1] - mu));
                                 split_f16(ex, w[i], w[16 + i]);
                                 if constexpr (SRC == kF32) {
-                                    ts.x = fmaf(ex.x, back[i >> 2], ts.x);
-                                    ts.y = fmaf(ex.y, back[i >> 2], ts.y);
+                                    const float2 back = reinterpret_cast<const float2*>(v_scale + BN)[cc * 16 + i];
+                                    ts = __ffma2_rn(ex, back, ts);
                                 } else {
                                     ts = __fadd2_rn(ts, ex);
                                 }
