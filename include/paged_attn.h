@@ -564,12 +564,14 @@ pa_status pa_compact_kv_q4(const pa_shape* shape, const pa_q4_pool* pool,
  * positions have (lens null: all of them), whose counts go up by one, -1 behind
  * them, and context_lens[targets[i]] = that length.  No row of K or V is copied:
  * a shared page is read by all, and pa_resize_pages gives a sequence that is about
- * to write into one a page of its own.  Sources are taken as they were before the
- * call.  PA_FLAG_BAD_CONTEXT, and that fork is not made, for a row outside [0, B),
- * a target that is not empty (length 0), that is also a source of the same fork or
- * of another of this call, or that an earlier fork of this call has, and a length
- * outside [0, context_lens[sources[i]]].  A page id out of range is copied but not
- * counted (PA_FLAG_BAD_PAGE).  n = 0 is PA_OK.  workspace: >= 256 bytes, zeroed
+ * to write into one a page of its own.  PA_FLAG_BAD_CONTEXT, and that fork is not
+ * made, for a row outside [0, B), a source that any fork of this call names as its
+ * target (its own, a later or an earlier one, made or not: what is read of a source is
+ * what it was before the call), a target that is not empty (length 0) or that an
+ * earlier fork of this call names (made or not), a source whose length is outside [0,
+ * capacity], and a length outside [0, context_lens[sources[i]]].  So of 0 -> 2 and 2 ->
+ * 3 the first is made and the second is not.  A page id out of range is copied but
+ * not counted (PA_FLAG_BAD_PAGE).  n = 0 is PA_OK.  workspace: >= 256 bytes, zeroed
  * once. */
 pa_status pa_fork_pages(const pa_shape* shape, int32_t* block_table, int32_t* context_lens,
                         int32_t* page_refs, const int32_t* sources, const int32_t* targets,

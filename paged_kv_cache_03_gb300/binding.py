@@ -1147,7 +1147,8 @@ def fork_pages(block_table, context_lens, page_refs, sources, targets, page_size
     """Row targets[i] of block_table becomes a fork of row sources[i] (int32
     [n]): the pages of its first lens[i] positions (None: all) are named twice
     and counted in page_refs (int32 [num_pages], 0: free); nothing is copied.
-    Targets must be empty (length 0).  Table, lengths and counts change in
+    Targets must be empty (length 0); no fork of a call may read a row that
+    one of them names as its target.  Table, lengths and counts change in
     place."""
     index = _page_state(block_table, context_lens, page_refs)
     _int32("sources", sources, (sources.shape[0],))

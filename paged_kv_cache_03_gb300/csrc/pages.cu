@@ -33,9 +33,11 @@ struct PagesParams {
 };
 
 // ---- fork -------------------------------------------------------------------------
-// One CTA per fork.  What a CTA reads of the table and the lengths no other writes:
-// a target appears once (later ones are refused) and no source is a target.  Bound by the
-// atomics of shared pages: 64 forks of up to 32 pages 4 us, 48 of up to 2000 pages 7.
+// One CTA per fork.  What a CTA reads of the table and the lengths no other writes: of the
+// forks that name a target the first alone may have it, and a fork whose source any fork names
+// as its target is refused, whether or not that one is made (which another CTA decides).
+// Bound by the atomics of shared pages: 64 forks of up to 32 pages 4 us, 48 of up to 2000
+// pages 7.
 __global__ void __launch_bounds__(256) fork_kernel(const PagesParams p, const int32_t* sources, const int32_t* targets,
                                                    const int32_t* lens, int n) {
     const int f = blockIdx.x, tid = threadIdx.x;
