@@ -971,6 +971,11 @@ def pa_copy_pages_q4(shape, pool, copies, n, workspace, workspace_bytes, stream=
         int(workspace_bytes), _stream(stream))
 
 
+def _c_int(name, x):
+    if not 0 < x < 1 << 31:  # (ctypes keeps the low 32 bits of any number)
+        raise ValueError(f"{name} must be positive and fit 32 bits")
+
+
 def _int32(name, t, shape):
     if t.dtype is not (_torch or _load_torch()).int32 or t.shape != shape:
         raise ValueError(f"{name} must be int32 {list(shape)}")
@@ -1075,6 +1080,7 @@ def _compact(name, fn, pools, dims, dtype_id, device, block_table, context_lens,
     torch = _torch or _load_torch()
     P, H_kv, ps = dims
     B_ = block_table.shape[0]
+    _c_int("L", L)
     _table(block_table, context_lens, B_)
     if path.dim() != 2 or path.shape[1] < 1:
         raise ValueError("path must be int32 [B, n]")
@@ -1122,8 +1128,10 @@ def _pages_shape(block_table, page_refs, page_size):
                     block_table.shape[1], PA_BF16)
 
 
-def _page_state(block_table, context_lens, page_refs):
-    """The CUDA device index of a checked table, lengths and page counts."""
+def _page_state(block_table, context_lens, page_refs, page_size):
+    """The CUDA device index of a checked table, lengths, page counts and page
+    size."""
+    _c_int("page_size", page_size)
     _table(block_table, context_lens, block_table.shape[0])
     _int32("page_refs", page_refs, (page_refs.shape[0],))
     index = block_table.get_device()
@@ -1150,7 +1158,7 @@ def fork_pages(block_table, context_lens, page_refs, sources, targets, page_size
     Targets must be empty (length 0); no fork of a call may read a row that
     one of them names as its target.  Table, lengths and counts change in
     place."""
-    index = _page_state(block_table, context_lens, page_refs)
+    index = _page_state(block_table, context_lens, page_refs, page_size)
     _int32("sources", sources, (sources.shape[0],))
     _int32("targets", targets, (sources.shape[0],))
     at = 0
@@ -1179,7 +1187,7 @@ def resize_pages(block_table, context_lens, page_refs, new_lens, page_size, *, c
     page, rows) for copy_pages, which every layer's pool needs before it is
     written to, or (-1, -1, 0)."""
     torch = _torch or _load_torch()
-    index = _page_state(block_table, context_lens, page_refs)
+    index = _page_state(block_table, context_lens, page_refs, page_size)
     B_ = block_table.shape[0]
     _int32("new_lens", new_lens, (B_,))
     if copies is None:
