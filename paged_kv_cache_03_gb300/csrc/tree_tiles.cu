@@ -449,7 +449,6 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 const int nbox = BN / p.box;
                 bool bad_page = false;
                 Ring<N> g;
-                int tiles = 0;
                 for (int k = 0; ok; ++k) {
                     ok = take(k);
                     if (!ok) break;
@@ -464,7 +463,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         return lane < nbox && key < S ? __ldg(table + key / p.ps) : 0;
                     };
                     int page = page_of(j0);
-                    for (int j = j0; j < j0 + n; ++j, g.next(), ++tiles) {
+                    for (int j = j0; j < j0 + n; ++j, g.next()) {
                         const int key = j * BN + lane * p.box;
                         const bool there = lane < nbox && key < S;
                         const bool good = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
@@ -855,6 +854,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             // ========================= query tiles ===================================
             const uint64_t policy = l2_policy_evict_first();
             bool ok = true;
+            int last = -1;  // piece whose query tile was asked for
             for (int k = 0;; ++k) {
                 ok = take(k);
                 if (!ok || slot(k)->n == 0) break;
@@ -875,8 +875,12 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         mbar_arrive(bar(kQFull + buf));
                     }
                 }
+                last = k;
                 __syncwarp();
             }
+            // What an error elsewhere left in flight lands before the shared memory goes: the last
+            // tile of each buffer.
+            for (int k = max(0, last - p.q_bufs + 1); k <= last; ++k) mbar_wait_for(bar(kQFull + q_buf(k)), q_use(k) & 1, 50000000ull);
             if (!ok && lane == 0) give_up(p, abort_flag);
         } else if (warp == kProd + 3) {
             // ============================ pieces =====================================
