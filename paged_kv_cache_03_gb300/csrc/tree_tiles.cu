@@ -13,7 +13,7 @@
 // (exact), Q scaled by a power of two into f16's range (exact), P rounded to f16 (2^-11, and
 // 2^-32 of the row's largest).
 // fp32: Q, K, V and P in two f16 parts each, x = h + l up to 2^-22 x, and products h h + h l
-// + l h (l l is below 2^-22); every row is scaled into f16's range by a power of two, and K's
+// + l h (l l is below 2^-22), O in stretches (kFold); every row is scaled into f16's range by a power of two, and K's
 // scale is undone in the scores, V's in the weights.
 //
 // Layout on GB300: one CTA per SM.
@@ -122,6 +122,13 @@ constexpr int keys(Source s) { return s == kF32 ? 64 : 128; }
 // sequences took 154 us, not 139, and contexts of 100 .. 500 keys 43, not 34).  fp32 queries
 // (products of three or two parts, which bound them): the slots take the tiles in turn.
 constexpr bool halves(Source s) { return !fp32(s); }
+// fp32 queries: so many tiles of a slot add their products to O, which is then added to the sum
+// of earlier ones in global memory and begun anew.  The tensor cores cut every sum towards 0,
+// so O falls behind by 2^-25 of itself at each of a tile's 12 (fp32 pages) or 16 steps, while
+// these additions are rounded.  Without them fp32 pages come 7e-6 short over 4000 keys of one
+// CTA and 8e-5 over 64000; with 8 tiles 2.3e-6 at any length, with 4 1.5e-6, with 16 3.9e-6.
+// 20 sequences of 16000 .. 32000, 128 rows: 876 us without, 922 with 8, 974 with 4, 929 with 16.
+constexpr int kFold = 8;
 constexpr int raw_stages(Source s) { return s == kQ4 ? 3 : s == kQ4F ? 1 : 0; }
 // Published pieces: enough for producers that are that many tiles ahead, were each tile a
 // piece.
@@ -193,6 +200,7 @@ struct TileParams {
     uint32_t* flag;
     float2* part_ml;  // [2 per CTA][128]: max, sum
     float* part_o;    // [2 per CTA][128][D]
+    float4* fold_o;   // [CTA][slot][D / 4][128], fp32 queries
     int4* split;      // per share: the segment that starts in it and ends in a later one,
     int* join;        // and the share in which the segment that comes into it starts (-1: none)
     int B, H_kv, R, L, W, nG, num_pages, ps, max_npg;  // nG: groups of C query tiles
@@ -826,7 +834,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                                     for (int kk = 0; kk < UK / 16; ++kk) {
                                         const uint32_t x = pa + (QP == 1 ? kk * 8 : (kk >> 1) * 32 + (kk & 1) * 8);
                                         const uint64_t y = tc::desc_advance(va, (h * (UK / 16) + kk) * 2 * kGroup);
-                                        if (kk == 0 && part == QP + VP - 2) tc::mma_bf16_ts(d, x, y, idO, i >= (HALF ? 1 : 2));
+                                        if (kk == 0 && part == QP + VP - 2) tc::mma_bf16_ts(d, x, y, idO, HALF ? i > 0 : (i >> 1) % kFold != 0);
                                         else tc::mma_bf16_ts_c<1>(d, x, y, idO);
                                     }
                                 }
@@ -993,6 +1001,17 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         constexpr float kLift = F16 ? 7.f : 0.f;
         int xc = 0;  // pieces whose states were joined
         bool ok = true;
+        float4* const fold_row = p.fold_o + (2ll * blockIdx.x + t) * (BM * kD / 4) + r;
+        auto add_folded = [](float (&o)[32], const float4* sum, float w) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float4 x = __ldcg(sum + e * BM);
+                o[4 * e] = fmaf(x.x, w, o[4 * e]);
+                o[4 * e + 1] = fmaf(x.y, w, o[4 * e + 1]);
+                o[4 * e + 2] = fmaf(x.z, w, o[4 * e + 2]);
+                o[4 * e + 3] = fmaf(x.w, w, o[4 * e + 3]);
+            }
+        };
         // The end of piece k, with this slot's maximum and sum.  The two slots' states of a row
         // are joined by both warpgroups, 64 dims each (one tile and no halves: A has them all).
         auto finish = [&](int k, float m1, float l1) {
@@ -1184,7 +1203,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 }
             }
             const int tail = first_tail(S);
-            float mrow = neg_inf();
+            float mrow = neg_inf(), folded = neg_inf();  // maxima: of O, of the sum of earlier ones
             float2 lsum = make_float2(0.f, 0.f);
             const int j0 = slot(k)->j0;
             for (int j = 0; j < nk; ++j) {
@@ -1287,6 +1306,28 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         tc::wait_st();
                         return true;
                     };
+                    // fp32: O, relative to the maximum so far, into the sum of those before it; the next
+                    // P V starts another one.
+                    auto fold = [&]() {
+                        if (!warp_wait(bar(kODone + t), (sc + j - 1) & 1)) return false;
+                        tc::fence_after_sync();
+                        const float before = folded == mrow ? 1.f : fast_exp2(folded - mrow);
+#pragma unroll 1
+                        for (int cc = 0; cc < 4; ++cc) {
+                            float o[32];
+                            __syncwarp();
+                            tc::ld32(trow + 256u + 128u * t + cc * 32, o);
+                            tc::wait_ld();
+                            if (!valid) continue;
+                            float4* const sum = fold_row + cc * 8 * BM;
+                            if (j > kFold) add_folded(o, sum, before);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) sum[e * BM] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                        __syncwarp();
+                        folded = mrow;
+                        return true;
+                    };
                     // P goes over the first columns of its S
                     if constexpr (F32) {
                         // Two parts of P do not fit the registers beside S: the masked scores, scaled
@@ -1325,12 +1366,16 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             for (int e = 0; e < 32; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
                         }
                         tc::wait_st();
+                        if (j > 0 && j % kFold == 0) {
+                            ok = fold();
+                            if (!ok) break;
+                        }
                         const bool grow = valid && mx > mrow + kSlack;
                         if (grow) {
                             alpha = fast_exp2(mrow - mx);  // 2^-inf = 0 at the start
                             mrow = mx;
                         }
-                        if (__any_sync(0xffffffffu, grow) && j > 0) {
+                        if (__any_sync(0xffffffffu, grow) && j % kFold != 0) {
                             ok = rescale();
                             if (!ok) break;
                         }
@@ -1405,6 +1450,24 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 if (lane == 0) mbar_arrive(bar(kPFull + t + 2 * b));
             }
             if (!ok || aborted(abort_flag)) break;
+            if (F32 && nk > kFold && busy) {  // the earlier ones' sum goes into O
+                ok = warp_wait(bar(kODone + t), (sc + nk - 1) & 1);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const float before = folded == mrow ? 1.f : fast_exp2(folded - mrow);
+#pragma unroll 1
+                for (int cc = 0; cc < 4; ++cc) {
+                    float o[32];
+                    __syncwarp();
+                    tc::ld32(trow + 256u + 128u * t + cc * 32, o);
+                    tc::wait_ld();
+                    if (valid) add_folded(o, fold_row + cc * 8 * BM, before);
+                    __syncwarp();
+                    tc::st32(trow + 256u + 128u * t + cc * 32, o);
+                }
+                tc::wait_st();
+                tc::fence_before_sync();
+            }
             ok = finish(k, mrow, lsum.x + lsum.y);
             if (!ok) break;
         }
@@ -1501,18 +1564,19 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const TileParams p, 
 }
 
 struct TilePlan {
-    size_t split_off, join_off, ml_off, o_off, total;
+    size_t split_off, join_off, ml_off, o_off, fold_off, total;
 };
 
-// (the same for every shape)
-TilePlan plan(int sm_count) {
+// (the same for every shape of a type)
+TilePlan plan(int sm_count, bool f32) {
     TilePlan t;
     const size_t states = 2ull * sm_count * BM;
     t.split_off = kFlagBytes;
     t.join_off = t.split_off + 16ull * sm_count;
     t.ml_off = align_up(t.join_off + 4ull * sm_count, 256);
     t.o_off = align_up(t.ml_off + states * 8, 256);
-    t.total = t.o_off + states * kD * 4;
+    t.fold_off = t.o_off + states * kD * 4;
+    t.total = t.fold_off + (f32 ? states * kD * 4 : 0);
     return t;
 }
 
@@ -1588,12 +1652,13 @@ bool tree_supported(const pa_shape& sh) {
     return static_cast<long long>(sh.B) * sh.H_kv * ((R + BM - 1) / BM) * (cap / keys(kF32) + 1 + kSegCost) < INT_MAX / 2;
 }
 
-size_t tree_workspace_bytes(int sm_count) { return plan(sm_count).total; }
+size_t tree_workspace_bytes(const pa_shape& sh, int sm_count) { return plan(sm_count, sh.dtype == PA_F32).total; }
 
 pa_status tree_launch(const TreeCall& c) {
     const pa_shape& sh = c.sh;
     if (c.dev.smem_optin < 232448) return PA_ERR_UNSUPPORTED;
-    const TilePlan t = plan(c.dev.sm_count);
+    const bool f32 = sh.dtype == PA_F32;
+    const TilePlan t = plan(c.dev.sm_count, f32);
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
     TileParams p;
     p.kc = static_cast<const uint8_t*>(c.kc);
@@ -1608,6 +1673,7 @@ pa_status tree_launch(const TreeCall& c) {
     p.flag = reinterpret_cast<uint32_t*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + t.ml_off);
     p.part_o = reinterpret_cast<float*>(ws + t.o_off);
+    p.fold_o = reinterpret_cast<float4*>(ws + t.fold_off);
     p.split = reinterpret_cast<int4*>(ws + t.split_off);
     p.join = reinterpret_cast<int*>(ws + t.join_off);
     p.B = sh.B;
@@ -1622,7 +1688,6 @@ pa_status tree_launch(const TreeCall& c) {
     p.q_box = std::min(BM, (p.R + 7) / 8 * 8);
     p.q_bufs = p.q_box <= BM / 2 ? 2 : 1;
     p.q_half = kQTile / 2 / p.q_bufs;
-    const bool f32 = sh.dtype == PA_F32;
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     p.scale_log2 = c.scale * 1.4426950408889634f;
     p.out32 = reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
