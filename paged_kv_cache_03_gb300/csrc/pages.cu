@@ -215,8 +215,9 @@ __global__ void __launch_bounds__(1024) resize_kernel(const ResizeParams p) {
         total += all;
         __syncthreads();
     }
-    // the lowest free pages
-    for (int p0 = 0; p0 < t.num_pages && total > 0; p0 += 8192) {
+    // the lowest free pages (unsigned: the step behind the last pages may pass 2^31)
+    for (uint32_t next = 0; next < static_cast<uint32_t>(t.num_pages) && total > 0; next += 8192) {
+        const int p0 = static_cast<int>(next);
         if (p0 > 0) look(p0);
         int free_here = 0;
 #pragma unroll
@@ -298,8 +299,9 @@ __device__ __forceinline__ void copy_units(U* dst, const U* src, long long n) {
 }
 
 // A CTA per (copy, kv head) and buffer: the first rows of one page to another, one
-// contiguous run of bytes.  Bound by HBM, few by latency: 64 copies of up to 128 rows of 8
-// heads in bf16 9 us.
+// contiguous run of bytes.  Bound by latency, a launch, the copy's entry and two rounds of
+// loads a thread: 64 copies of up to 128 rows of 8 heads in bf16 9 us, of whose 16 MB HBM would
+// take 3.
 __global__ void __launch_bounds__(256) copy_pages_kernel(const CopyParams p) {
     const int i = static_cast<int>(blockIdx.x) / p.H_kv, h = static_cast<int>(blockIdx.x) - i * p.H_kv;
     const int src = p.copies[3ll * i], dst = p.copies[3ll * i + 1], rows = p.copies[3ll * i + 2];
