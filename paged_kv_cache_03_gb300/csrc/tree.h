@@ -29,7 +29,7 @@ struct TreeCall {
     DeviceInfo dev;
 };
 bool tree_supported(const pa_shape& sh);
-size_t tree_workspace_bytes(const pa_shape& sh, int sm_count);
+size_t tree_workspace_bytes(int sm_count);
 pa_status tree_launch(const TreeCall& c);
 
 pa_status tree_mask_launch(int B, int L, const int32_t* parents, uint32_t* mask, int32_t* depths, uint32_t* flag,

@@ -32,7 +32,7 @@ pa_status attend(const pa_shape* shape, const void* query, const void* kc, const
     TreeCall c;
     st = device_ok(&c.dev);
     if (st != PA_OK) return st;
-    if (ws_bytes < tree_workspace_bytes(*shape, c.dev.sm_count)) return PA_ERR_WORKSPACE;
+    if (ws_bytes < tree_workspace_bytes(c.dev.sm_count)) return PA_ERR_WORKSPACE;
     c.sh = *shape;
     c.q = query;
     c.kc = kc;
@@ -95,7 +95,7 @@ pa_status pa_tree_mask(int B, int L, const int32_t* parents, uint32_t* mask, int
 size_t pa_tree_workspace_bytes(const pa_shape* shape) {
     DeviceInfo dev;
     if (check_shape(shape) != PA_OK || !tree_supported(*shape) || current_device_info(&dev) != PA_OK) return 0;
-    return tree_workspace_bytes(*shape, dev.sm_count);
+    return tree_workspace_bytes(dev.sm_count);
 }
 
 pa_status pa_paged_attention_tree(const pa_shape* shape, const void* query, const void* key_pages,

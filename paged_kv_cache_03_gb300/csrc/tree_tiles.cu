@@ -13,7 +13,7 @@
 // (exact), Q scaled by a power of two into f16's range (exact), P rounded to f16 (2^-11, and
 // 2^-32 of the row's largest).
 // fp32: Q, K, V and P in two f16 parts each, x = h + l up to 2^-22 x, and products h h + h l
-// + l h (l l is below 2^-22), O in stretches (kFold); every row is scaled into f16's range by a power of two, and K's
+// + l h (l l is below 2^-22); every row is scaled into f16's range by a power of two, and K's
 // scale is undone in the scores, V's in the weights.
 //
 // Layout on GB300: one CTA per SM.
@@ -25,10 +25,13 @@
 //     ragged contexts leave no SM idle; a segment that crosses shares leaves fp32 partial
 //     states that tree_merge_kernel joins.
 //   * Two slots t = 0, 1, one softmax warpgroup each with one row per thread, have their own
-//     P (over S), O, m and l in Tensor Memory and join them at the piece's end.  bf16 queries:
-//     each takes half of every tile's keys and S has two places; fp32 queries: the tiles go to
-//     the slots in turn.  One warp issues Q K^T and one P V, so products run beside both
-//     softmaxes.
+//     P (over S), m and l, which are joined at the piece's end.  bf16 queries: each takes half
+//     of every tile's keys into an O of its own, and S has two places.  fp32 queries: the tiles
+//     go to the slots in turn, and there is one O.  Tensor cores cut what they add to towards
+//     0, so products of all of a CTA's keys in one sum came 7e-6 short over 4000 fp32 keys and
+//     8e-5 over 64000; a tile's products are a sum of their own, which its slot's warps add to
+//     O, in fp32 rounding: 0.9e-6 at any length (256 rows 182 us, 172 in one sum; over 4 bits
+//     49 and 51).  One warp issues Q K^T and one P V, so products run beside both softmaxes.
 //   * The producer warps bring K and V into rings in the 128-byte swizzle that the MMA reads:
 //     one lane per page box by TMA (bf16, pages of a multiple of 8 slots), 16-byte
 //     asynchronous copies (other page sizes), or rows converted on the way (4 bits, fp32).
@@ -67,7 +70,8 @@ namespace {
 
 constexpr int kD = kHeadDim;
 constexpr int BM = 128;  // query rows of a tile
-constexpr uint32_t kTmemCols = 512;  // S of slot t at 128 t, O at 256 + 128 t
+// S of slot t at 128 t, O at 256 + 128 t; fp32 queries: O at 256, a tile's products at 384.
+constexpr uint32_t kTmemCols = 512;
 // What a segment's query load, first softmax and epilogue cost, in key tiles: the
 // shares count it, or CTAs with many short segments would finish last.  (Of 64 sequences,
 // 256 rows take 158, 154 and 151 us with 3, 4 and 5, 64 rows 91, 91 and 94.)
@@ -90,6 +94,7 @@ enum Bar {
     kVEmpty = 13,   // + slot
     kVTail = 16,    // + slot: a tail tile's values are there, not yet cleaned (by TMA)
     kQReady = 16,   // + buffer: the query tile is there in f16 (f16 products; never with kVTail)
+    kTFree = 18,    // a tile's products are in O (fp32 queries; never with kVTail)
     kSFull = 19,    // + place of S (halves) or slot
     kPFull = 21,    // + t + 2 x place
     kODone = 25,    // + t + 2 x place: O has taken in that P
@@ -122,13 +127,6 @@ constexpr int keys(Source s) { return s == kF32 ? 64 : 128; }
 // sequences took 154 us, not 139, and contexts of 100 .. 500 keys 43, not 34).  fp32 queries
 // (products of three or two parts, which bound them): the slots take the tiles in turn.
 constexpr bool halves(Source s) { return !fp32(s); }
-// fp32 queries: so many tiles of a slot add their products to O, which is then added to the sum
-// of earlier ones in global memory and begun anew.  The tensor cores cut every sum towards 0,
-// so O falls behind by 2^-25 of itself at each of a tile's 12 (fp32 pages) or 16 steps, while
-// these additions are rounded.  Without them fp32 pages come 7e-6 short over 4000 keys of one
-// CTA and 8e-5 over 64000; with 8 tiles 2.3e-6 at any length, with 4 1.5e-6, with 16 3.9e-6.
-// 20 sequences of 16000 .. 32000, 128 rows: 876 us without, 922 with 8, 974 with 4, 929 with 16.
-constexpr int kFold = 8;
 constexpr int raw_stages(Source s) { return s == kQ4 ? 3 : s == kQ4F ? 1 : 0; }
 // Published pieces: enough for producers that are that many tiles ahead, were each tile a
 // piece.
@@ -154,7 +152,7 @@ static_assert(regs_fit(kTma) && regs_fit(kCopy) && regs_fit(kQ4) && regs_fit(kF3
 // Shared memory from a 1024-byte boundary (the attribute of smem_raw) on.  Q: one tile, or
 // two of at most 64 rows that the pieces take in turn.
 struct Smem {
-    int k, v, raw, bar, items, tmem, abort, x, q_scale, kv_scale, total;
+    int k, v, raw, bar, items, tmem, abort, x, q_scale, o_max, kv_scale, total;
 };
 constexpr int kItemBytes = 168;
 constexpr Smem smem(Source s) {
@@ -177,6 +175,8 @@ constexpr Smem smem(Source s) {
     at += 2 * BM * 8;
     m.q_scale = at;  // f16: [2][128] the inverse of a row's scale
     if (is_f16(s)) at += 2 * BM * 4;
+    m.o_max = at;  // fp32 queries: [2 pieces][128] the maximum that O is relative to
+    if (fp32(s)) at += 2 * BM * 4;
     // fp32 pages, a number per key: [8 tiles] K's inverse scale, [4 tiles] the exponent of V's
     // scale, [4 tiles] that scale
     m.kv_scale = at;
@@ -200,7 +200,6 @@ struct TileParams {
     uint32_t* flag;
     float2* part_ml;  // [2 per CTA][128]: max, sum
     float* part_o;    // [2 per CTA][128][D]
-    float4* fold_o;   // [CTA][slot][D / 4][128], fp32 queries
     int4* split;      // per share: the segment that starts in it and ends in a later one,
     int* join;        // and the share in which the segment that comes into it starts (-1: none)
     int B, H_kv, R, L, W, nG, num_pages, ps, max_npg;  // nG: groups of C query tiles
@@ -329,6 +328,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             mbar_init(bar(kOFree + s), 8);
             mbar_init(bar(kXFull + s), 8);  // (and kXFree)
         }
+        if (F32) mbar_init(bar(kTFree), 4);
         for (int s = 0; s < N; ++s) {
             mbar_init(bar(kKFull + s), SRC == kTma ? 1 : 4);
             mbar_init(bar(kKEmpty + s), 1);
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             const uint64_t dV0 = tc::smem_desc_sw128(base + M.v, kHalf, kGroup);
             const bool leader = elect_one(), values = warp != kProd;
             Ring<N> ring;
-            int g0 = 0, u0 = 0, u1 = 0, oe0 = 0, oe1 = 0;  // of earlier pieces: tiles, of each slot, epilogues
+            int g0 = 0, u0 = 0, u1 = 0, oe = 0;  // of earlier pieces: tiles, of each slot, epilogues
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 ok = take(k);
@@ -816,14 +816,16 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         const uint64_t dv = tc::desc_advance(dV0, ring.s * kRing);
 #pragma unroll
                         for (int h = 0; h < (HALF ? 2 : 1); ++h) {
-                            const int t = HALF ? h : i & 1, oe = t ? oe1 : oe0;  // the slot
+                            const int t = HALF ? h : i & 1;  // the slot
                             const int b = HALF ? (g0 + i) & 1 : 0, use = HALF ? (g0 + i) >> 1 : (t ? u1 : u0) + (i >> 1);
                             ok = ok && warp_wait(bar(kPFull + t + 2 * b), use & 1);
                             // the previous piece's epilogue has read O
-                            if (ok && i < (HALF ? 1 : 2) && oe > 0) ok = warp_wait(bar(kOFree + t), (oe - 1) & 1);
+                            if (ok && i == 0 && oe > 0) ok = warp_wait(bar(kOFree + t), (oe - 1) & 1);
+                            // the tile before has been added to O
+                            if (!HALF && ok && i > 0) ok = warp_wait(bar(kTFree), (g0 + i - 1) & 1);
                             if (!ok) break;
                             tc::fence_after_sync();
-                            const uint32_t d = tmem + 256u + 128u * t, a = tmem + (HALF ? 128u * b + UK * t : 128u * t);
+                            const uint32_t d = tmem + 256u + 128u * (HALF ? t : i > 0), a = tmem + (HALF ? 128u * b + UK * t : 128u * t);
                             if (leader) {
 #pragma unroll
                                 for (int part = QP + VP - 2; part >= 0; --part) {
@@ -834,7 +836,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                                     for (int kk = 0; kk < UK / 16; ++kk) {
                                         const uint32_t x = pa + (QP == 1 ? kk * 8 : (kk >> 1) * 32 + (kk & 1) * 8);
                                         const uint64_t y = tc::desc_advance(va, (h * (UK / 16) + kk) * 2 * kGroup);
-                                        if (kk == 0 && part == QP + VP - 2) tc::mma_bf16_ts(d, x, y, idO, HALF ? i > 0 : (i >> 1) % kFold != 0);
+                                        if (kk == 0 && part == QP + VP - 2) tc::mma_bf16_ts(d, x, y, idO, HALF && i > 0);
                                         else tc::mma_bf16_ts_c<1>(d, x, y, idO);
                                     }
                                 }
@@ -850,8 +852,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 g0 += n;
                 u0 += (n + 1) >> 1;
                 u1 += n >> 1;
-                ++oe0;
-                if (HALF || n > 1) ++oe1;
+                ++oe;
             }
             if (!ok && lane == 0) give_up(p, abort_flag);
             // nothing of ours may still be running when TMEM is freed
@@ -1001,17 +1002,6 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         constexpr float kLift = F16 ? 7.f : 0.f;
         int xc = 0;  // pieces whose states were joined
         bool ok = true;
-        float4* const fold_row = p.fold_o + (2ll * blockIdx.x + t) * (BM * kD / 4) + r;
-        auto add_folded = [](float (&o)[32], const float4* sum, float w) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float4 x = __ldcg(sum + e * BM);
-                o[4 * e] = fmaf(x.x, w, o[4 * e]);
-                o[4 * e + 1] = fmaf(x.y, w, o[4 * e + 1]);
-                o[4 * e + 2] = fmaf(x.z, w, o[4 * e + 2]);
-                o[4 * e + 3] = fmaf(x.w, w, o[4 * e + 3]);
-            }
-        };
         // The end of piece k, with this slot's maximum and sum.  The two slots' states of a row
         // are joined by both warpgroups, 64 dims each (one tile and no halves: A has them all).
         auto finish = [&](int k, float m1, float l1) {
@@ -1020,7 +1010,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             const int m = it->mp * C + rank, rows = p.R - m * BM;
             const bool busy = q4 * 32 < rows, valid = r < rows;
             const int l = static_cast<unsigned>(m * BM + r) % static_cast<unsigned>(p.L);  // draft
-            float w0 = 1.f, w1 = 0.f;  // weights of O 0 and O 1
+            float w0 = 1.f, w1 = 0.f;  // weights of O 0 and O 1 (fp32: of O and the last tile's products)
             if (both) {
                 float2* const x = reinterpret_cast<float2*>(smem_raw + M.x) + r;
                 ok = xc == 0 || warp_wait(bar(kXFree), (xc - 1) & 1);  // (the last joined piece's are read)
@@ -1042,11 +1032,17 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 if constexpr (HALF) {
                     const int g = it->before[0] + it->before[1] + it->n - 1, b = 2 * (g & 1);
                     ok = warp_wait(bar(kODone + b), (g >> 1) & 1) && warp_wait(bar(kODone + 1 + b), (g >> 1) & 1);
+                    if (!ok) return false;
                 } else {
-                    ok = warp_wait(bar(kODone), (it->before[0] + ((it->n + 1) >> 1) - 1) & 1) &&
-                         warp_wait(bar(kODone + 1), (it->before[1] + (it->n >> 1) - 1) & 1);
+                    const int last = it->n - 1, s = last & 1;
+                    const float m0 = reinterpret_cast<const float*>(smem_raw + M.o_max)[(k & 1) * BM + r], mx = s ? e.x : a.x;
+                    w0 = m0 == mm ? 1.f : fast_exp2(m0 - mm);
+                    w1 = mx == mm ? 1.f : fast_exp2(mx - mm);
+                    ok = warp_wait(bar(kODone + s), (it->before[s] + (last >> 1)) & 1);
+                    if (!ok) return false;
+                    // (behind the arrivals for the tile before, and not before the products that wait for those)
+                    if (t == s && lane == 0) mbar_arrive(bar(kTFree));
                 }
-                if (!ok) return false;
             } else if (t == 0) {
                 ok = warp_wait(bar(kODone), it->before[0] & 1);
                 if (!ok) return false;
@@ -1110,7 +1106,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
             if (lane == 0) {
                 if (both || t == 0) mbar_arrive(bar(kOFree));
                 if (!both && t == 0) mbar_arrive(bar(kOFree));  // (for B's warp, which has nothing to read)
-                if (both) mbar_arrive(bar(kOFree + 1));
+                if (HALF) mbar_arrive(bar(kOFree + 1));
             }
             release(k);
             return true;
@@ -1203,7 +1199,7 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 }
             }
             const int tail = first_tail(S);
-            float mrow = neg_inf(), folded = neg_inf();  // maxima: of O, of the sum of earlier ones
+            float mrow = neg_inf();
             float2 lsum = make_float2(0.f, 0.f);
             const int j0 = slot(k)->j0;
             for (int j = 0; j < nk; ++j) {
@@ -1306,28 +1302,6 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         tc::wait_st();
                         return true;
                     };
-                    // fp32: O, relative to the maximum so far, into the sum of those before it; the next
-                    // P V starts another one.
-                    auto fold = [&]() {
-                        if (!warp_wait(bar(kODone + t), (sc + j - 1) & 1)) return false;
-                        tc::fence_after_sync();
-                        const float before = folded == mrow ? 1.f : fast_exp2(folded - mrow);
-#pragma unroll 1
-                        for (int cc = 0; cc < 4; ++cc) {
-                            float o[32];
-                            __syncwarp();
-                            tc::ld32(trow + 256u + 128u * t + cc * 32, o);
-                            tc::wait_ld();
-                            if (!valid) continue;
-                            float4* const sum = fold_row + cc * 8 * BM;
-                            if (j > kFold) add_folded(o, sum, before);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) sum[e * BM] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        }
-                        __syncwarp();
-                        folded = mrow;
-                        return true;
-                    };
                     // P goes over the first columns of its S
                     if constexpr (F32) {
                         // Two parts of P do not fit the registers beside S: the masked scores, scaled
@@ -1366,18 +1340,10 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                             for (int e = 0; e < 32; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
                         }
                         tc::wait_st();
-                        if (j > 0 && j % kFold == 0) {
-                            ok = fold();
-                            if (!ok) break;
-                        }
                         const bool grow = valid && mx > mrow + kSlack;
                         if (grow) {
                             alpha = fast_exp2(mrow - mx);  // 2^-inf = 0 at the start
                             mrow = mx;
-                        }
-                        if (__any_sync(0xffffffffu, grow) && j % kFold != 0) {
-                            ok = rescale();
-                            if (!ok) break;
                         }
                         const float mu = mrow == neg_inf() ? 0.f : mrow - kLift;
 #pragma unroll 1  // (registers)
@@ -1448,26 +1414,37 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kPFull + t + 2 * b));
+                if constexpr (!HALF) {
+                    // The first tile's products are O.  The others' are added to it here, one tile after
+                    // the other, but for the last tile's, which are where the piece ends.
+                    float* const o_max = reinterpret_cast<float*>(smem_raw + M.o_max) + (k & 1) * BM + r;
+                    const bool here = i > 0 && i < n - 1;
+                    if (here) ok = warp_wait(bar(kODone + t), use & 1) && warp_wait(bar(kTFree), (g0 + i - 1) & 1);
+                    if (!ok) break;
+                    if (busy && i == 0) *o_max = mrow;
+                    if (busy && here) {
+                        tc::fence_after_sync();
+                        const float m0 = *o_max, mm = fmaxf(m0, mrow);
+                        const float w0 = m0 == mm ? 1.f : fast_exp2(m0 - mm), w1 = mrow == mm ? 1.f : fast_exp2(mrow - mm);
+#pragma unroll 1
+                        for (int cc = 0; cc < 4; ++cc) {
+                            float o[32], x[32];
+                            tc::ld32(trow + 256u + cc * 32, o);
+                            tc::ld32(trow + 384u + cc * 32, x);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = fmaf(x[e], w1, o[e] * w0);
+                            tc::st32(trow + 256u + cc * 32, o);
+                        }
+                        *o_max = mm;
+                        tc::wait_st();
+                        tc::fence_before_sync();
+                    }
+                    __syncwarp();
+                    if (lane == 0 && (i == 0 || here)) mbar_arrive(bar(kTFree));
+                }
             }
             if (!ok || aborted(abort_flag)) break;
-            if (F32 && nk > kFold && busy) {  // the earlier ones' sum goes into O
-                ok = warp_wait(bar(kODone + t), (sc + nk - 1) & 1);
-                if (!ok) break;
-                tc::fence_after_sync();
-                const float before = folded == mrow ? 1.f : fast_exp2(folded - mrow);
-#pragma unroll 1
-                for (int cc = 0; cc < 4; ++cc) {
-                    float o[32];
-                    __syncwarp();
-                    tc::ld32(trow + 256u + 128u * t + cc * 32, o);
-                    tc::wait_ld();
-                    if (valid) add_folded(o, fold_row + cc * 8 * BM, before);
-                    __syncwarp();
-                    tc::st32(trow + 256u + 128u * t + cc * 32, o);
-                }
-                tc::wait_st();
-                tc::fence_before_sync();
-            }
             ok = finish(k, mrow, lsum.x + lsum.y);
             if (!ok) break;
         }
@@ -1564,19 +1541,18 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const TileParams p, 
 }
 
 struct TilePlan {
-    size_t split_off, join_off, ml_off, o_off, fold_off, total;
+    size_t split_off, join_off, ml_off, o_off, total;
 };
 
-// (the same for every shape of a type)
-TilePlan plan(int sm_count, bool f32) {
+// (the same for every shape)
+TilePlan plan(int sm_count) {
     TilePlan t;
     const size_t states = 2ull * sm_count * BM;
     t.split_off = kFlagBytes;
     t.join_off = t.split_off + 16ull * sm_count;
     t.ml_off = align_up(t.join_off + 4ull * sm_count, 256);
     t.o_off = align_up(t.ml_off + states * 8, 256);
-    t.fold_off = t.o_off + states * kD * 4;
-    t.total = t.fold_off + (f32 ? states * kD * 4 : 0);
+    t.total = t.o_off + states * kD * 4;
     return t;
 }
 
@@ -1652,13 +1628,12 @@ bool tree_supported(const pa_shape& sh) {
     return static_cast<long long>(sh.B) * sh.H_kv * ((R + BM - 1) / BM) * (cap / keys(kF32) + 1 + kSegCost) < INT_MAX / 2;
 }
 
-size_t tree_workspace_bytes(const pa_shape& sh, int sm_count) { return plan(sm_count, sh.dtype == PA_F32).total; }
+size_t tree_workspace_bytes(int sm_count) { return plan(sm_count).total; }
 
 pa_status tree_launch(const TreeCall& c) {
     const pa_shape& sh = c.sh;
     if (c.dev.smem_optin < 232448) return PA_ERR_UNSUPPORTED;
-    const bool f32 = sh.dtype == PA_F32;
-    const TilePlan t = plan(c.dev.sm_count, f32);
+    const TilePlan t = plan(c.dev.sm_count);
     uint8_t* const ws = static_cast<uint8_t*>(c.ws);
     TileParams p;
     p.kc = static_cast<const uint8_t*>(c.kc);
@@ -1673,7 +1648,6 @@ pa_status tree_launch(const TreeCall& c) {
     p.flag = reinterpret_cast<uint32_t*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + t.ml_off);
     p.part_o = reinterpret_cast<float*>(ws + t.o_off);
-    p.fold_o = reinterpret_cast<float4*>(ws + t.fold_off);
     p.split = reinterpret_cast<int4*>(ws + t.split_off);
     p.join = reinterpret_cast<int*>(ws + t.join_off);
     p.B = sh.B;
@@ -1688,6 +1662,7 @@ pa_status tree_launch(const TreeCall& c) {
     p.q_box = std::min(BM, (p.R + 7) / 8 * 8);
     p.q_bufs = p.q_box <= BM / 2 ? 2 : 1;
     p.q_half = kQTile / 2 / p.q_bufs;
+    const bool f32 = sh.dtype == PA_F32;
     p.max_S = static_cast<long long>(sh.max_pages_per_seq) * sh.page_size;
     p.scale_log2 = c.scale * 1.4426950408889634f;
     p.out32 = reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
