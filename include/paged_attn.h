@@ -487,8 +487,8 @@ pa_status pa_tree_mask(int B, int L, const int32_t* parents, uint32_t* mask, int
  * value rows may hold anything.  bf16 or fp32 pages of the query's type, any page
  * size and group size.
  * Rounded on the way: with bf16 queries each probability to bf16 (2^-8); their sums with
- * values are fp32, of weights up to 2^8 beside the row's first keys, so that values of
- * 2^120 / context_lens[b] and more may come out as infinities.  fp32
+ * values are fp32, of weights up to 2^8 relative to the row's maximum so far, so that over
+ * bf16 pages values of 2^120 / context_lens[b] and more may come out as infinities.  fp32
  * numbers and their probabilities enter the products as two f16 parts, rows scaled by
  * powers of two: all but 2^-22 of a number, or 2^-40 of the largest of its row (values: or
  * 2^-105; probabilities: or 2^-32 of the row's largest, over fp32 pages each taken times

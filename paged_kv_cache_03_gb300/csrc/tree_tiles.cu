@@ -44,16 +44,18 @@
 //     and exits.
 //
 // Measured (G = 4, H_kv = 8, a call among others, with the merge):
-//   64 sequences of 128 .. 4096 keys, 64 rows    89 us, 6.4 TB/s of rows: bound by HBM
-//   16 of 32768, 128 rows, pages of 16          320 us, 6.7 TB/s
-//   16 of 1000 .. 8000, 252 rows                 76 us, 970 TFLOP/s: a tile takes
+//   64 sequences of 128 .. 4096 keys, 64 rows    89 us for 506 MB, 5.7 TB/s: HBM is 70% busy
+//   16 of 32768, 128 rows, pages of 16          320 us, 6.7 TB/s: bound by HBM
+//   16 of 1000 .. 8000, 252 rows                 76 us for 69 GFLOP, 900 TFLOP/s: a tile takes
 //     1750 cycles, of them 1024 products at the peak rate; Q, K, V and TMA's stores pass
 //     through shared memory in 1280.  Without exponentials it is no faster, without maxima
 //     and sums 9%
 //   32 of 500 .. 8000 in 4 bits, 96 rows         81 us: a tile takes 2170 cycles, the softmax
 //     beside eight converting warps
-//   8 of 1000 .. 8000 in fp32, 64 / 256 rows     94 / 177 us: conversion, 4500 cycles a tile of
+//   8 of 1000 .. 8000 in fp32, 64 / 256 rows     94 / 182 us: conversion, 4500 cycles a tile of
 //     64 keys, and three products, 3200
+//   8 of 1000 .. 8000 in 4 bits, fp32, 64 rows   49 us: changes of segment, and 3500 cycles a
+//     tile, of them 2048 products
 #include <algorithm>
 #include <cfloat>
 #include <climits>
