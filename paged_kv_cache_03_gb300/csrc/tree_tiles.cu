@@ -995,9 +995,9 @@ __global__ void __launch_bounds__(threads(SRC), 1)
         reg_set<regs(SRC).softmax, launch_regs(SRC)>();
         const int t = (warp - kProd - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;  // slot, lane quarter, row
         const uint32_t trow = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-        // How far (log2) a row's scores may rise above its maximum before O is rescaled: f16
-        // weights end at 2^16, and a sum of bf16 weights times values at 2^128, which leaves
-        // N values 2^120 / N.
+        // How far (log2) a row's scores may rise above its maximum before that moves (and an O
+        // relative to it is rescaled): f16 weights end at 2^16, and a sum of bf16 weights times
+        // values at 2^128, which leaves N values 2^120 / N.
         constexpr float kSlack = 8.f;
         // f16 weights are taken 2^kLift times as large (O and l are, too): below 2^-14 f16 has
         // steps of 2^-24, so a light key loses 2^-32 of the heaviest one's weight at most.
@@ -1309,9 +1309,9 @@ __global__ void __launch_bounds__(threads(SRC), 1)
                         // Two parts of P do not fit the registers beside S: the masked scores, scaled
                         // to powers of two, go back over S, and then 32 keys' P over their own (all
                         // done twice, from S as it was, the second 32 keys unrolled: fp32 pages, 256
-                        // rows, 192 us for 172, fp32 queries over 4 bits 57 for 51).  fp32 pages: V's rows were scaled by
-                        // 2^v, so P is 2^(score - v - maximum), the maximum that of score - v, and
-                        // the sum adds P 2^v: the weights relative to that maximum.
+                        // rows, 192 us for 172, fp32 queries over 4 bits 57 for 51).  fp32 pages: V's
+                        // rows were scaled by 2^v, so P is 2^(score - v - maximum), the maximum that
+                        // of score - v, and the sum adds P 2^v: the weights relative to that maximum.
                         const float4* const k_scale = reinterpret_cast<const float4*>(smem_raw + M.kv_scale) + ((g0 + i) & 7) * (BN / 4);
                         const float4* const v_scale = reinterpret_cast<const float4*>(smem_raw + M.kv_scale) + (8 + ((g0 + i) & 3)) * (BN / 4);
 #pragma unroll
@@ -1605,8 +1605,12 @@ pa_status launch_tiles(TileParams p, const CUtensorMap* maps, const TreeCall& c,
     const long long segs = static_cast<long long>(p.B) * p.H_kv * p.nG;
     p.whole = segs <= *shares && p.max_S <= (4 * segs < *shares ? kWholeFew : kWholeMany) * keys(SRC);
     if (p.whole) *shares = static_cast<int>(segs);
-    tree_tile_kernel<SRC, C><<<static_cast<unsigned>(*shares * C), threads(SRC), bytes, c.stream>>>(p, maps[0], maps[1], maps[2]);
-    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(*shares * C));
+    cfg.blockDim = dim3(threads(SRC));
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = c.stream;
+    if (cudaLaunchKernelEx(&cfg, tree_tile_kernel<SRC, C>, p, maps[0], maps[1], maps[2]) != cudaSuccess) return PA_ERR_CUDA;
     if (p.whole) *shares = 0;
     return PA_OK;
 }
